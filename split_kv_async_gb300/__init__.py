@@ -28,15 +28,20 @@ FDPP_TC_MMA_AUTO, FDPP_TC_MMA_SYNC, FDPP_TC_MMA_TCGEN05 = 0, 1, 2
 FDPP_FLAG_OUT, FDPP_FLAG_ABOVE, FDPP_FLAG_BELOW, FDPP_FLAG_NAN, FDPP_FLAG_RECOMPUTED = 1, 2, 4, 8, 16
 FDPP_FLAG_SLOT = 32
 FDPP_ERRBIT_SEQ_LEN, FDPP_ERRBIT_BLOCK_TABLE, FDPP_ERRBIT_TIMEOUT = 1, 2, 4
+FDPP_ERRBIT_POOL, FDPP_ERRBIT_ROOM, FDPP_ERRBIT_SLOT, FDPP_ERRBIT_TOKENS, FDPP_ERRBIT_PREFIX = 8, 16, 32, 64, 128
+FDPP_ROPE_PLAIN, FDPP_ROPE_LINEAR, FDPP_ROPE_NTK, FDPP_ROPE_PARTS = 0, 1, 2, 3
+FDPP_ROWS_MAX_GROUP = 128
 FDPP_AUTO_UNITS_PER_SM, FDPP_AUTO_GRANULE, FDPP_AUTO_MIN_SPLIT = 4, 64, 256
 
-# Names every build of the library exports (the C ABI of include/fdpp.h and include/fdpp_gemm.h).
+# Names every build of the library exports (the C ABI of the headers in include/).
 EXPORTED = ("fdpp_max_splits", "fdpp_workspace_size", "fdpp_workspace_init", "fdpp_decode_attn",
             "fdpp_decode_attn_timed", "fdpp_decode_attn_noalloc", "fdpp_score_ranges",
             "fdpp_pick_phi", "fdpp_read_diag", "fdpp_read_diag_noalloc", "fdpp_status_str",
             "fdpp_last_error", "fdpp_attn_set_lut", "fdpp_attn_auto_choice",
             "fdpp_flat_gemm_split_k", "fdpp_flat_gemm_workspace_size", "fdpp_flat_gemm",
-            "fdpp_flat_gemm_set_lut", "fdpp_flat_gemm_read_error")
+            "fdpp_flat_gemm_set_lut", "fdpp_flat_gemm_read_error",
+            "fdpp_block_map_workspace_size", "fdpp_block_map", "fdpp_rope_table", "fdpp_rope_append",
+            "fdpp_read_error", "fdpp_rows_workspace_size", "fdpp_rows_attn", "fdpp_prefix_attn")
 FDPP_GEMM_MAX_M = 128
 FDPP_NOALLOC_WORKSPACE_BYTES = 16 << 20
 FDPP_TC_MAX_PARTS = 512
@@ -84,6 +89,31 @@ class fdpp_diag(ctypes.Structure):
 class fdpp_attn_lut_row(ctypes.Structure):
     _fields_ = [(name, ctypes.c_int) for name in ("max_batch", "max_seq_len", "max_rows", "kernel",
                                                   "units_per_sm", "min_split")]
+
+
+class fdpp_block_params(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int) for name in ("batch", "block_size", "max_blocks_per_seq", "num_kv_blocks",
+                                                  "max_tokens")]
+
+
+class fdpp_rope_params(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int), ("num_q_heads", ctypes.c_int), ("num_kv_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int), ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+        ("dtype", ctypes.c_int), ("q_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong),
+        ("v_stride", ctypes.c_longlong), ("num_slots", ctypes.c_longlong), ("magnitude", ctypes.c_float),
+    ]
+
+
+class fdpp_rows_params(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int), ("num_q_heads", ctypes.c_int), ("num_kv_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("num_tokens", ctypes.c_int),
+        ("max_seq_len", ctypes.c_int), ("block_size", ctypes.c_int), ("max_blocks_per_seq", ctypes.c_int),
+        ("num_kv_blocks", ctypes.c_int), ("max_prefix_len", ctypes.c_int), ("scale", ctypes.c_float),
+        ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("key_begin", ctypes.c_void_p),
+        ("key_end", ctypes.c_void_p), ("kernel", ctypes.c_int),
+    ]
 
 
 def _load() -> ctypes.CDLL:
@@ -135,6 +165,24 @@ def _load() -> ctypes.CDLL:
     lib.fdpp_flat_gemm_set_lut.restype = ci
     lib.fdpp_flat_gemm_read_error.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
     lib.fdpp_flat_gemm_read_error.restype = ci
+    cz, cd = ctypes.c_size_t, ctypes.c_double
+    PB, PR, PA = (ctypes.POINTER(t) for t in (fdpp_block_params, fdpp_rope_params, fdpp_rows_params))
+    lib.fdpp_block_map_workspace_size.argtypes = [PB]
+    lib.fdpp_block_map_workspace_size.restype = cz
+    lib.fdpp_block_map.argtypes = [vp, vp, vp, PB] + [vp] * 9 + [cz, vp]
+    lib.fdpp_block_map.restype = ci
+    lib.fdpp_rope_table.argtypes = [ci, cd, ci, cd, ci, cd, cd, vp]
+    lib.fdpp_rope_table.restype = ci
+    lib.fdpp_rope_append.argtypes = [vp] * 6 + [PR] + [vp] * 4 + [cz, vp]
+    lib.fdpp_rope_append.restype = ci
+    lib.fdpp_read_error.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
+    lib.fdpp_read_error.restype = ci
+    lib.fdpp_rows_workspace_size.argtypes = [PA, ctypes.POINTER(cz)]
+    lib.fdpp_rows_workspace_size.restype = ci
+    lib.fdpp_rows_attn.argtypes = [vp] * 6 + [PA, vp, cz, vp, vp]
+    lib.fdpp_rows_attn.restype = ci
+    lib.fdpp_prefix_attn.argtypes = [vp] * 10 + [PA, vp, cz, vp, vp]
+    lib.fdpp_prefix_attn.restype = ci
     return lib
 
 
@@ -354,3 +402,124 @@ def fdpp_flat_gemm_read_error(workspace) -> int:
     _check(lib.fdpp_flat_gemm_read_error(_ptr(workspace), ctypes.byref(bits)),
            "fdpp_flat_gemm_read_error")
     return int(bits.value)
+
+
+# ---- cache upkeep (include/fdpp_cache.h) ----------------------------------------------------
+
+def _bytes(t) -> int:
+    return t.numel() * t.element_size()
+
+
+def make_block_params(*, batch, block_size, max_blocks_per_seq, num_kv_blocks, max_tokens) -> fdpp_block_params:
+    return fdpp_block_params(batch, block_size, max_blocks_per_seq, num_kv_blocks, max_tokens)
+
+
+def fdpp_block_map_workspace_size(p: fdpp_block_params) -> int:
+    return int(lib.fdpp_block_map_workspace_size(ctypes.byref(p)))
+
+
+def alloc_block_workspace(p: fdpp_block_params, device="cuda"):
+    """A zeroed uint8 device tensor large enough for fdpp_block_map with `p`."""
+    import torch
+    n = fdpp_block_map_workspace_size(p)
+    if n == 0:
+        raise FdppError(FDPP_ERR_INVALID_ARG, "fdpp_block_map_workspace_size", "invalid parameters")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def fdpp_block_map(held_lens, want_lens, pool_in, p: fdpp_block_params, block_table, pool_queue, seq_lens, pool_out,
+                   cu_tokens, token_seq, positions, slots, workspace, stream=None) -> None:
+    """Block tables from held_lens to want_lens tokens per sequence, and the new tokens' rows
+    (contiguous int32 device tensors; slots int64)."""
+    _check(lib.fdpp_block_map(held_lens.data_ptr(), want_lens.data_ptr(), pool_in.data_ptr(), p,
+                              block_table.data_ptr(), pool_queue.data_ptr(), seq_lens.data_ptr(),
+                              pool_out.data_ptr(), cu_tokens.data_ptr(), token_seq.data_ptr(), positions.data_ptr(),
+                              slots.data_ptr(), workspace.data_ptr(), _bytes(workspace), _stream_handle(stream)),
+           "fdpp_block_map")
+
+
+def fdpp_rope_table(rot_dim: int, base: float, *, scaling=FDPP_ROPE_PLAIN, factor=1.0, context=0, low_turns=1.0,
+                    high_turns=32.0):
+    """Angles of the rotation as float32 numpy [rot_dim / 2][2] (host only; copy it to the device)."""
+    import numpy as np
+    table = np.zeros((max(0, rot_dim) // 2, 2), np.float32)
+    _check(lib.fdpp_rope_table(rot_dim, base, scaling, factor, context, low_turns, high_turns, table.ctypes.data),
+           "fdpp_rope_table")
+    return table
+
+
+def make_rope_params(*, num_tokens, num_q_heads, num_kv_heads, head_dim, rot_dim, dtype, num_slots, q_stride=None,
+                     k_stride=None, v_stride=None, interleaved=False, magnitude=1.0) -> fdpp_rope_params:
+    """Strides in elements from one token's row to the next; None: contiguous rows."""
+    kv = num_kv_heads * head_dim
+    return fdpp_rope_params(num_tokens, num_q_heads, num_kv_heads, head_dim, rot_dim, int(interleaved), dtype,
+                            num_q_heads * head_dim if q_stride is None else q_stride,
+                            kv if k_stride is None else k_stride, kv if v_stride is None else v_stride, num_slots,
+                            magnitude)
+
+
+def alloc_rope_workspace(device="cuda"):
+    import torch
+    return torch.zeros(256, dtype=torch.uint8, device=device)
+
+
+def fdpp_rope_append(q, k, v, positions, slots, table, p: fdpp_rope_params, q_out, k_cache, v_cache, workspace,
+                     stream=None) -> None:
+    """Rotated q into q_out, rotated k and v into the caches' slots (q, k and v may be views of one
+    projection's output with the strides of `p`)."""
+    _check(lib.fdpp_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), positions.data_ptr(), slots.data_ptr(),
+                                table.data_ptr(), p, q_out.data_ptr(), k_cache.data_ptr(),
+                                v_cache.data_ptr(), workspace.data_ptr(), _bytes(workspace),
+                                _stream_handle(stream)), "fdpp_rope_append")
+
+
+def fdpp_read_error(workspace) -> int:
+    """Sticky error bits of the calls on this workspace (synchronises)."""
+    bits = ctypes.c_uint32(0)
+    _check(lib.fdpp_read_error(_ptr(workspace), ctypes.byref(bits)), "fdpp_read_error")
+    return int(bits.value)
+
+
+# ---- rows attention (include/fdpp_rows.h) ---------------------------------------------------
+
+def make_rows_params(*, batch, num_q_heads, num_kv_heads, head_dim, dtype, num_tokens, max_seq_len, scale, softcap=0.0,
+                     slopes=None, key_begin=None, key_end=None, block_size=0, max_blocks_per_seq=0, num_kv_blocks=0,
+                     max_prefix_len=0, kernel=FDPP_KERNEL_AUTO) -> fdpp_rows_params:
+    """slopes: float32 device tensor [num_q_heads] or None; key_begin, key_end: int32 device tensors
+    [num_tokens] or None (the caller keeps them alive as long as `p` is used)."""
+    return fdpp_rows_params(batch, num_q_heads, num_kv_heads, head_dim, dtype, num_tokens, max_seq_len, block_size,
+                            max_blocks_per_seq, num_kv_blocks, max_prefix_len, scale, softcap, _ptr(slopes),
+                            _ptr(key_begin), _ptr(key_end), kernel)
+
+
+def fdpp_rows_workspace_size(p: fdpp_rows_params) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib.fdpp_rows_workspace_size(ctypes.byref(p), ctypes.byref(n)), "fdpp_rows_workspace_size")
+    return n.value
+
+
+def alloc_rows_workspace(p: fdpp_rows_params, device="cuda", stream=None):
+    """Allocates (torch) and zeroes a workspace for `p`. The library itself allocates nothing."""
+    import torch
+    ws = torch.empty(fdpp_rows_workspace_size(p), dtype=torch.uint8, device=device)
+    fdpp_workspace_init(ws, stream)
+    return ws
+
+
+def fdpp_rows_attn(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, p: fdpp_rows_params, workspace, out,
+                   stream=None) -> None:
+    """Attention of the ragged token rows q [T][Hq][d] to their sequences' caches (contiguous device
+    tensors; block_table and cu_tokens may be None)."""
+    _check(lib.fdpp_rows_attn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(block_table),
+                              seq_lens.data_ptr(), _ptr(cu_tokens), p, workspace.data_ptr(),
+                              _bytes(workspace), out.data_ptr(), _stream_handle(stream)), "fdpp_rows_attn")
+
+
+def fdpp_prefix_attn(q, prefix_k, prefix_v, prefix_blocks, prefix_len, k_cache, v_cache, block_table, seq_lens, cu_tokens,
+                     p: fdpp_rows_params, workspace, out, stream=None) -> None:
+    """fdpp_rows_attn for a batch whose sequences share a prefix (prefix_k and prefix_v with contiguous
+    caches, prefix_blocks with paged ones; prefix_len: int32 device tensor of one element)."""
+    _check(lib.fdpp_prefix_attn(q.data_ptr(), _ptr(prefix_k), _ptr(prefix_v), _ptr(prefix_blocks),
+                                prefix_len.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(block_table),
+                                seq_lens.data_ptr(), _ptr(cu_tokens), p, workspace.data_ptr(),
+                                _bytes(workspace), out.data_ptr(), _stream_handle(stream)), "fdpp_prefix_attn")
