@@ -111,9 +111,9 @@ fdpp_status encode_cache(CUtensorMap* map, const void* base, const fdpp_rows_par
     return FDPP_OK;
 }
 
-// q as {d, Hq, T}, box {64, G, floor(128 / G)}: one load lands a row tile's rows (token i, head h of
-// the kv head in row i G + h) as rows of 128 bytes, 128-byte swizzled.
-fdpp_status encode_q(CUtensorMap* map, const void* q, const fdpp_rows_params& p)
+// q as {d, Hq, T}, box {64, G, tokens}: one load lands a row tile's rows (token i, head h of the kv
+// head in row i G + h) as rows of 128 bytes, 128-byte swizzled.
+fdpp_status encode_q(CUtensorMap* map, const void* q, const fdpp_rows_params& p, int tokens)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
     const fdpp_status st = get_tensor_map_encoder(&enc);
@@ -122,7 +122,7 @@ fdpp_status encode_q(CUtensorMap* map, const void* q, const fdpp_rows_params& p)
     const int G = p.num_q_heads / p.num_kv_heads;
     cuuint64_t dims[3] = {D, Hq, (cuuint64_t)p.num_tokens};
     cuuint64_t strides[2] = {D * 2, Hq * D * 2};
-    cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(ROWS_TILE / G)};
+    cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tokens};
     cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
@@ -207,6 +207,7 @@ fdpp_status attend(const void* q, const void* prefix_k, const void* prefix_v, co
     a.num_blocks = paged ? p->num_kv_blocks : 0;
     a.max_prefix = prefix ? p->max_prefix_len : 0;
     a.tpt = ROWS_TILE / a.G;
+    a.tpn = ROWS_NARROW / a.G;
     a.max_rt = w.max_rt;
     a.slot_rows = w.slot_rows;
     a.scale = p->scale;
@@ -224,17 +225,18 @@ fdpp_status attend(const void* q, const void* prefix_k, const void* prefix_v, co
     if (a.stages < 3) return rfail(FDPP_ERR_UNSUPPORTED, "too little shared memory for the tensor kernel");
     const int box = paged ? std::min(p->block_size, ROWS_KEYS) : ROWS_KEYS;
     const long long rows = paged ? p->block_size : p->max_seq_len, outer = paged ? p->num_kv_blocks : p->batch;
-    CUtensorMap tq, tk, tv, tpk, tpv;
-    if ((st = encode_q(&tq, q, *p)) != FDPP_OK) return st;
-    if ((st = encode_cache(&tk, k_cache, *p, rows, outer, box)) != FDPP_OK) return st;
-    if ((st = encode_cache(&tv, v_cache, *p, rows, outer, box)) != FDPP_OK) return st;
-    tpk = tk;
-    tpv = tv;
+    RowsMaps m;
+    if ((st = encode_q(&m.q, q, *p, a.tpt)) != FDPP_OK) return st;
+    if ((st = encode_q(&m.qn, q, *p, std::max(1, a.tpn))) != FDPP_OK) return st;
+    if ((st = encode_cache(&m.k, k_cache, *p, rows, outer, box)) != FDPP_OK) return st;
+    if ((st = encode_cache(&m.v, v_cache, *p, rows, outer, box)) != FDPP_OK) return st;
+    m.pk = m.k;
+    m.pv = m.v;
     if (prefix && !paged) {
-        if ((st = encode_cache(&tpk, prefix_k, *p, p->max_prefix_len, 1, ROWS_KEYS)) != FDPP_OK) return st;
-        if ((st = encode_cache(&tpv, prefix_v, *p, p->max_prefix_len, 1, ROWS_KEYS)) != FDPP_OK) return st;
+        if ((st = encode_cache(&m.pk, prefix_k, *p, p->max_prefix_len, 1, ROWS_KEYS)) != FDPP_OK) return st;
+        if ((st = encode_cache(&m.pv, prefix_v, *p, p->max_prefix_len, 1, ROWS_KEYS)) != FDPP_OK) return st;
     }
-    const cudaError_t e = launch_rows_tc(a, tq, tk, tv, tpk, tpv, s);
+    const cudaError_t e = launch_rows_tc(a, m, s);
     if (e != cudaSuccess) return rfail(FDPP_ERR_CUDA, "rows kernel launch: %s", cudaGetErrorString(e));
     return FDPP_OK;
 }

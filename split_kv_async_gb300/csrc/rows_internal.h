@@ -14,6 +14,8 @@ namespace fdpp {
 constexpr int ROWS_TILE = 128;
 constexpr int ROWS_PAIR = 2 * ROWS_TILE;
 constexpr int ROWS_KEYS = 128;
+// Most rows of a key-major run (scores with the keys on the tensor-memory lanes).
+constexpr int ROWS_NARROW = 32;
 // Parts that the key tiles of all units are cut into, at most (one per CTA, one CTA per SM).
 constexpr int ROWS_MAX_PARTS = 160;
 // Counters of the CUDA-core kernel's splits (zero between calls): it splits only calls with fewer
@@ -78,7 +80,7 @@ struct RowsArgs {
     float2* row_ml;                 // [2][T][Hq]
     int B, Hq, Hkv, G, D, T, per_seq;
     int max_seq_len, block_size, max_blocks, num_blocks, max_prefix, prefix_width;
-    int tpt;                        // tokens per 128-row tile: floor(128 / G)
+    int tpt, tpn;                   // tokens per 128-row tile and per key-major run: floor(128 / G), floor(32 / G)
     int max_rt, slot_rows, parts, splits, stages;
     float scale, cap;
 };
@@ -86,10 +88,13 @@ struct RowsArgs {
 RowsLayout rows_layout(const fdpp_rows_params& p);
 
 cudaError_t launch_rows_simt(const RowsArgs& a, int dtype, cudaStream_t s);
-// Plan, tile kernel and join. tq: q as {d, Hq, T}; tk, tv: the caches; tpk, tpv: the prefix (the pools
-// again for paged caches).
-cudaError_t launch_rows_tc(const RowsArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                           const CUtensorMap& tpk, const CUtensorMap& tpv, cudaStream_t s);
+// Plan, tile kernel and join.
+struct RowsMaps {
+    CUtensorMap q, qn;     // q as {d, Hq, T}: boxes of a 128-row tile, and of a key-major run's 32 rows
+    CUtensorMap k, v;      // the caches
+    CUtensorMap pk, pv;    // the prefix (the pools again for paged caches)
+};
+cudaError_t launch_rows_tc(const RowsArgs& a, const RowsMaps& m, cudaStream_t s);
 // K/V stages that fit the device's shared memory per block.
 int rows_tc_stages(int head_dim, int smem_per_block);
 

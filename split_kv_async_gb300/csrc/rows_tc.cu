@@ -47,7 +47,9 @@ namespace {
 
 constexpr int RW_MMA_WARP = 8;
 constexpr int RW_LOAD_WARP = 9;
-constexpr int RW_THREADS = 10 * 32;
+constexpr int RW_THREADS = 12 * 32;      // the last two warps idle: register shares go by warpgroup
+constexpr int RW_SOFT_REGS = 200;        // 2 x 128 x 200 + 128 x 104 = 64512 = 384 x 168, the launch's share
+constexpr int RW_HELP_REGS = 104;
 constexpr int RW_HDRS = 4;               // run headers in flight
 constexpr int RW_HDR_BYTES = 64;
 constexpr float RW_LAG = 8.f;            // log2 of the growth of a row's max that moves its frame
@@ -55,20 +57,37 @@ constexpr float RW_LAG = 8.f;            // log2 of the growth of a row's max th
 enum { RH_KIND = 0, RH_G, RH_B, RH_TOK0, RH_NTOK, RH_LEN, RH_A0, RH_A1, RH_B0, RH_B1, RH_T0, RH_T1, RH_DEST,
        RH_FLAGS, RH_BASE, RH_WORDS };
 enum { RUN_ROWS = 0, RUN_END = 1 };
-enum { RF_PAIR = 1, RF_START = 2 };      // two row tiles; the first key tile goes to stream 1
+// two row tiles; few rows (key-major); the first key tile goes to stream 1
+enum { RF_PAIR = 1, RF_NARROW = 2, RF_START = 4 };
 enum { DEST_OUT = -1, DEST_ROWS = -2 };  // else a slot
 static_assert(RH_WORDS * 4 <= RW_HDR_BYTES, "header fits its slot");
 
+// What the key-major runs share between warps (in the second Q buffer, which they leave free).
+struct NarrowShared {
+    float wmax[2][4][ROWS_NARROW];       // per stream and warp: rows' maxima of a tile
+    float lsum[2][4][ROWS_NARROW];       // sums of a run
+    float frame[2][ROWS_NARROW];
+    int flag[2][2][4];                   // per stream, tile parity and warp: a score beyond its row's frame
+};
+
+// Shared memory. A key-major run keeps to the Q buffers: two slots of 32 query rows and the weights of
+// both streams ([32 rows][128 keys] bf16) in the first, NarrowShared in the second; the load warp lets
+// all runs of one kind end before it starts one of the other.
 template <int D>
 struct RowsSmem {
     static constexpr int QB = ROWS_TILE * D * 2;           // a row tile's Q
     static constexpr int SB = ROWS_KEYS * D * 2;           // a K or V tile
     static constexpr int HALF = ROWS_KEYS * 128;           // one 64-wide half of either
+    static constexpr int NQ = ROWS_NARROW * D * 2;         // a key-major run's Q
+    static constexpr int NQ_HALF = ROWS_NARROW * 128;
+    static constexpr int NP = ROWS_NARROW * ROWS_KEYS * 2; // its weights, per stream
+    static constexpr int NP_OFF = 2 * NQ, NSH_OFF = 2 * NQ + 2 * NP;
     int q, stages, hdr, ml, bars, misc, tslot, total;
     __host__ __device__ explicit RowsSmem(int nst)
         : q(0), stages(2 * QB), hdr(stages + nst * SB), ml(hdr + RW_HDRS * RW_HDR_BYTES), bars(ml + 2 * ROWS_TILE * 8),
-          misc(bars + (2 * nst + 2 * 2 + 2 * RW_HDRS + 6 * 2 + 1) * 8), tslot(misc + 16), total(tslot + 16)
+          misc(bars + (2 * nst + 2 * 2 + 2 * RW_HDRS + 7 * 2 + 1) * 8), tslot(misc + 16), total(tslot + 16)
     {
+        static_assert(NSH_OFF + (int)sizeof(NarrowShared) <= 2 * QB, "a key-major run fits the Q buffers");
     }
 };
 
@@ -76,9 +95,10 @@ struct RowsBars {
     uint32_t kvfull, kvempty;     // [stages]
     uint32_t qfull, qempty;       // [2]
     uint32_t hfull, hempty;       // [RW_HDRS] run headers: read by the MMA warp and the eight softmax warps
-    uint32_t sfull, pready;       // [2] scores written; weights written over them
+    uint32_t sfull, pready;       // [2] scores written; weights written
     uint32_t ofull, ofree;        // [2] accumulator complete; read out
-    uint32_t mlready, mlfree;     // [2] the second stream's maxima and sums for the joined epilogue
+    uint32_t mlready, mlfree;     // [2] a stream's maxima and sums for the joined epilogue
+    uint32_t vote;                // [2] the warps of a stream meet (key-major runs)
     uint32_t drain;
     __device__ __forceinline__ RowsBars(uint32_t base, int nst)
     {
@@ -94,7 +114,8 @@ struct RowsBars {
         ofree = ofull + 16;
         mlready = ofree + 16;
         mlfree = mlready + 16;
-        drain = mlfree + 16;
+        vote = mlfree + 16;
+        drain = vote + 16;
     }
 };
 
@@ -108,6 +129,20 @@ __device__ __forceinline__ bool rwait(uint32_t bar, uint32_t parity, volatile in
         rows_error(a, FDPP_ERRBIT_TIMEOUT);
     }
     return ok;
+}
+
+// Whether the phase of `parity` has completed (no waiting).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // First tile of part c of the `total` tiles.
@@ -358,17 +393,30 @@ struct RowsLoader {
             : "memory");
     }
 
-    __device__ __forceinline__ bool query(const CUtensorMap* map, int g, int tok0)
+    // Query rows into the next Q buffer (or the next slot of the key-major runs).
+    __device__ __forceinline__ bool query(const CUtensorMap* map, int g, int tok0, bool narrow)
     {
         const int lane = threadIdx.x & 31;
         const uint32_t qb = nq & 1u, bar = bars.qfull + 8 * qb;
         if (!rwait(bars.qempty + 8 * qb, ((nq >> 1) & 1u) ^ 1u, misc, a)) return false;
-        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(a.tpt * a.G * 128 * (D / 64)));
+        const int rows = (narrow ? a.tpn : a.tpt) * a.G;
+        const uint32_t dst = sbase + lay.q + qb * (narrow ? RowsSmem<D>::NQ : RowsSmem<D>::QB);
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(rows * 128 * (D / 64)));
         __syncwarp();
         if (lane < D / 64)
-            tma_load(sbase + lay.q + qb * RowsSmem<D>::QB + lane * RowsSmem<D>::HALF, map, lane * 64, g * a.G, tok0, bar);
+            tma_load(dst + lane * (narrow ? RowsSmem<D>::NQ_HALF : RowsSmem<D>::HALF), map, lane * 64, g * a.G, tok0, bar);
         __syncwarp();
         ++nq;
+        return true;
+    }
+
+    // Both Q buffers are back: the runs so far have left everything that the two kinds share.
+    __device__ __forceinline__ bool settle_queries()
+    {
+        for (uint32_t k = 0; k < 2 && k < nq; ++k) {
+            const uint32_t i = nq - 1 - k;
+            if (!rwait(bars.qempty + 8 * (i & 1u), (i >> 1) & 1u, misc, a)) return false;
+        }
         return true;
     }
 
@@ -385,8 +433,8 @@ struct RowsLoader {
         ++nh;
     }
 
-    __device__ __forceinline__ bool run(const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv,
-                                        const CUtensorMap* tpk, const CUtensorMap* tpv)
+    __device__ __forceinline__ bool run(const CUtensorMap* tq, const CUtensorMap* tqn, const CUtensorMap* tk,
+                                        const CUtensorMap* tv, const CUtensorMap* tpk, const CUtensorMap* tpv)
     {
         const int lane = threadIdx.x & 31;
         const int total = a.plan[RP_TILES], nrt = a.plan[RP_NRT], P = a.plan[RP_PREFIX];
@@ -395,8 +443,12 @@ struct RowsLoader {
         const int end = part_begin(c + 1, total, parts);
         int rt = pos < end ? find_rt(a.rec, nrt, pos) : 0;
         uint32_t toggle = 0;
+        bool was_narrow = false;
         while (pos < end) {
             const RowTileRec r = a.rec[rt];
+            const bool narrow = r.ntok <= a.tpn;
+            if (narrow != was_narrow && !settle_queries()) return false;
+            was_narrow = narrow;
             const int past = r.start + r.nt * a.Hkv;
             while (pos < end && pos < past) {
                 const int g = (pos - r.start) / r.nt, ta = (pos - r.start) - g * r.nt, tb = min(r.nt, ta + end - pos);
@@ -418,14 +470,14 @@ struct RowsLoader {
                     h[RH_T0] = t0;
                     h[RH_T1] = t1;
                     h[RH_DEST] = whole ? (a.prefix_len ? DEST_ROWS : DEST_OUT) : 2 * c + (ta == 0 ? 1 : 0);
-                    h[RH_FLAGS] = pair ? RF_PAIR : (toggle ? RF_START : 0);
+                    h[RH_FLAGS] = (pair ? RF_PAIR : (toggle ? RF_START : 0)) | (narrow ? RF_NARROW : 0);
                     h[RH_BASE] = r.b < 0 ? 0 : P;
                 }
                 publish();
                 if (!pair) toggle = (toggle + (uint32_t)(t1 - t0)) & 1u;
                 int ent = a.block_table ? entry(r, t0) : 0;
-                if (!query(tq, g, r.tok0)) return false;
-                if (pair && !query(tq, g, r.tok0 + a.tpt)) return false;
+                if (!query(narrow ? tqn : tq, g, r.tok0, narrow)) return false;
+                if (pair && !query(tq, g, r.tok0 + a.tpt, false)) return false;
                 for (int t = t0; t < t1; ++t) {
                     const int next = a.block_table && t + 1 < t1 ? entry(r, t + 1) : 0;
                     if (!tile(r.b < 0 ? tpk : tk, r, g, t, ent)) return false;
@@ -467,104 +519,158 @@ struct RowsLoader {
 // ------------------------------------------------------------------------------------------
 // MMA warp
 // ------------------------------------------------------------------------------------------
-// Tensor memory: the scores of streams 0 and 1 (128 columns each; P takes the first 64 of them), then
-// their accumulators (D columns each).
+// Tensor memory: the scores of streams 0 and 1 (128 columns each; P takes the first 64 of them, or the
+// first 16 or 32 hold S^T of a key-major run), then their accumulators (D columns each; O^T of a key-major
+// run takes 16 or 32).
 constexpr uint32_t TM_S = ROWS_KEYS;
+
+// Keeps a value in one place: its uses are computed from it where they are, not ahead of the loop.
+__device__ __forceinline__ void keep(uint64_t& x) { asm volatile("" : "+l"(x)); }
+
+__device__ __forceinline__ uint32_t narrow_cols(int rows) { return rows <= 16 ? 16u : 32u; }
 
 template <int D>
 struct RowsMma {
     const RowsArgs& a;
     const RowsSmem<D>& lay;
     const RowsBars& bars;
-    uint8_t* sm;
     uint32_t sbase, tmem;
     volatile int* misc;
     // a stream's tile whose P V is still to be issued
     struct Pending {
-        bool on;
-        uint32_t tile, stage, phase;
-        bool first, last, release;
-    } pend[2];
-    uint32_t np[2], nacc[2];       // P V issued, runs begun, per stream
+        bool on = false, first = false, last = false, release = false;
+        uint32_t tile = 0, stage = 0, phase = 0, ncols = 0;     // ncols: of a key-major run, else 0
+    } p0, p1;
+    uint32_t np0 = 0, np1 = 0, nacc0 = 0, nacc1 = 0;            // P V issued, runs begun, per stream
 
-    // Issues the P V that stream s owes, after one that the other stream owes from before it (of the
+    // Issues the P V that stream S owes, after one that the other stream owes from before it (of the
     // same tile: stream 0's first): the joined epilogue waits for both accumulators, and a tile's last
     // P V gives its stage back.
-    __device__ __forceinline__ bool flush(int s)
+    template <int S>
+    __device__ __forceinline__ bool flush()
     {
-        const Pending& o = pend[s ^ 1];
-        if (!pend[s].on) return true;
-        if (o.on && (o.tile < pend[s].tile || (o.tile == pend[s].tile && s == 1)) && !issue(s ^ 1)) return false;
-        return issue(s);
+        const Pending& o = S ? p0 : p1;
+        const Pending& p = S ? p1 : p0;
+        if (!p.on) return true;
+        if (o.on && (o.tile < p.tile || (o.tile == p.tile && S == 1)) && !issue<S ^ 1>()) return false;
+        return issue<S>();
     }
 
-    __device__ __forceinline__ bool issue(int s)
+    template <int S>
+    __device__ __forceinline__ bool issue()
     {
-        constexpr uint32_t IDESC = umma_idesc_bf16(128, D, false) | (1u << 16);     // V: MN-major
-        Pending& p = pend[s];
-        if (!rwait(bars.pready + 8 * s, np[s] & 1u, misc, a)) return false;
+        constexpr uint32_t IDESC = umma_idesc_bf16(128, D, false) | (1u << 16);     // V: MN-major B
+        Pending& p = S ? p1 : p0;
+        uint32_t& np = S ? np1 : np0;
+        uint32_t& nacc = S ? nacc1 : nacc0;
+        if (!rwait(bars.pready + 8 * S, np & 1u, misc, a)) return false;
         if (!rwait(bars.kvfull + 8 * p.stage, p.phase, misc, a)) return false;
-        if (p.first && !rwait(bars.ofree + 8 * s, (nacc[s] & 1u) ^ 1u, misc, a)) return false;
+        if (p.first && !rwait(bars.ofree + 8 * S, (nacc & 1u) ^ 1u, misc, a)) return false;
         tc_fence_after();
         if ((threadIdx.x & 31) == 0) {
-            const uint64_t vd =
-                sw128_mnmajor_desc(sbase + lay.stages + p.stage * RowsSmem<D>::SB, RowsSmem<D>::HALF, 1024);
-            const uint32_t pd = tmem + s * TM_S, od = tmem + 2 * TM_S + s * D;
+            const uint32_t od = tmem + 2 * TM_S + S * D;
+            uint64_t vd = sw128_mnmajor_desc(sbase + lay.stages + p.stage * RowsSmem<D>::SB, RowsSmem<D>::HALF, 1024);
+            keep(vd);
+            if (p.ncols == 0) {
+                const uint32_t pd = tmem + S * TM_S;
 #pragma unroll
-            for (int k = 0; k < ROWS_KEYS / 16; ++k)
-                umma_bf16_ta(od, pd + 8 * k, vd + k * (2048 >> 4), IDESC, (p.first && k == 0) ? 0u : 1u);
+                for (int k = 0; k < ROWS_KEYS / 16; ++k)
+                    umma_bf16_ta(od, pd + 8 * k, vd + k * (2048 >> 4), IDESC, (p.first && k == 0) ? 0u : 1u);
+            } else {
+                // O^T += V^T P^T: d on M, the rows on N, 64 keys per half of P^T
+                const uint32_t idesc = umma_idesc_bf16(D, 16, true) + ((p.ncols - 16) >> 3 << 17);
+                uint64_t pd = sw128_kmajor_desc(sbase + lay.q + RowsSmem<D>::NP_OFF + S * RowsSmem<D>::NP);
+                keep(pd);
+#pragma unroll
+                for (int k = 0; k < ROWS_KEYS / 16; ++k)
+                    umma_bf16(od, vd + k * (2048 >> 4), pd + (k >> 2) * (RowsSmem<D>::NQ_HALF >> 4) + (k & 3) * 2, idesc,
+                              (p.first && k == 0) ? 0u : 1u);
+            }
             if (p.release) umma_commit(bars.kvempty + 8 * p.stage);
-            if (p.last) umma_commit(bars.ofull + 8 * s);
+            if (p.last) umma_commit(bars.ofull + 8 * S);
         }
         __syncwarp();
-        ++np[s];
-        if (p.first) ++nacc[s];
+        ++np;
+        if (p.first) ++nacc;
         p.on = false;
         return true;
     }
 
-    __device__ __forceinline__ bool run()
+    // Waits for something the load warp brings. What the streams still owe goes first where it is not
+    // there yet: the load warp may itself be waiting for a run to end (its query slot, its stages).
+    __device__ __forceinline__ bool await(uint32_t bar, uint32_t parity)
+    {
+        if ((p0.on || p1.on) && !__all_sync(0xffffffffu, mbar_test(bar, parity)) && !(flush<0>() && flush<1>()))
+            return false;
+        return rwait(bar, parity, misc, a);
+    }
+
+    // Q K^T of one tile for stream S.
+    template <int S>
+    __device__ __forceinline__ void scores(uint32_t qb, uint32_t stage, uint32_t ncols, bool release, bool free_q)
     {
         constexpr uint32_t IDESC = umma_idesc_bf16(128, ROWS_KEYS, false);
+        if ((threadIdx.x & 31) == 0) {
+            uint64_t kd = sw128_kmajor_desc(sbase + lay.stages + stage * RowsSmem<D>::SB);
+            keep(kd);
+            if (ncols == 0) {
+                uint64_t qd = sw128_kmajor_desc(sbase + lay.q + qb * RowsSmem<D>::QB);
+                keep(qd);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (uint32_t)(k >> 2) * (RowsSmem<D>::HALF >> 4) + (uint32_t)(k & 3) * 2u;
+                    umma_bf16(tmem + S * TM_S, qd + off, kd + off, IDESC, k > 0 ? 1u : 0u);
+                }
+            } else {
+                // S^T = K Q^T: the keys on M, the rows on N
+                const uint32_t idesc = umma_idesc_bf16(128, 16, false) + ((ncols - 16) >> 3 << 17);
+                uint64_t qd = sw128_kmajor_desc(sbase + lay.q + qb * RowsSmem<D>::NQ);
+                keep(qd);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    umma_bf16(tmem + S * TM_S, kd + (uint32_t)(k >> 2) * (RowsSmem<D>::HALF >> 4) + (uint32_t)(k & 3) * 2u,
+                              qd + (uint32_t)(k >> 2) * (RowsSmem<D>::NQ_HALF >> 4) + (uint32_t)(k & 3) * 2u, idesc,
+                              k > 0 ? 1u : 0u);
+            }
+            umma_commit(bars.sfull + 8 * S);
+            if (release) umma_commit(bars.kvempty + 8 * stage);
+            if (free_q) umma_commit(bars.qempty + 8 * qb);
+        }
+        __syncwarp();
+    }
+
+    __device__ __forceinline__ bool run(uint8_t* sm)
+    {
         const int lane = threadIdx.x & 31;
         uint32_t stage = 0, phase = 0, nq = 0, nh = 0, tile = 0;
-        pend[0].on = pend[1].on = false;
-        np[0] = np[1] = nacc[0] = nacc[1] = 0;
         for (;; ++nh) {
             const uint32_t hs = nh % RW_HDRS;
-            if (!rwait(bars.hfull + 8 * hs, (nh / RW_HDRS) & 1u, misc, a)) return false;
+            if (!await(bars.hfull + 8 * hs, (nh / RW_HDRS) & 1u)) return false;
             const int* h = reinterpret_cast<const int*>(sm + lay.hdr + hs * RW_HDR_BYTES);
             const int kind = h[RH_KIND], len = h[RH_LEN], t0 = h[RH_T0], t1 = h[RH_T1], flags = h[RH_FLAGS];
             const int a0 = h[RH_A0], a1 = h[RH_A1], b0 = h[RH_B0], b1 = h[RH_B1];
+            const uint32_t ncols = (flags & RF_NARROW) ? narrow_cols(h[RH_NTOK] * a.G) : 0u;
             __syncwarp();
             if (lane == 0) mbar_arrive(bars.hempty + 8 * hs);
             if (kind == RUN_END) break;
             const bool pair = flags & RF_PAIR;
+            const int start = (flags & RF_START) ? 1 : 0;
             const uint32_t qb0 = nq & 1u;
             for (uint32_t k = 0; k < (pair ? 2u : 1u); ++k, ++nq)
-                if (!rwait(bars.qfull + 8 * (nq & 1u), (nq >> 1) & 1u, misc, a)) return false;
-            bool begun[2] = {false, false};
+                if (!await(bars.qfull + 8 * (nq & 1u), (nq >> 1) & 1u)) return false;
+            bool begun0 = false, begun1 = false;
             for (int t = t0; t < t1; ++t, ++tile) {
                 // a P V left behind by a stream that is not in turn holds a stage: issue it first
-                for (int s = 0; s < 2; ++s)
-                    if (pend[s].on && pend[s].tile + 1 < tile && !flush(s)) return false;
+                if (p0.on && p0.tile + 1 < tile && !flush<0>()) return false;
+                if (p1.on && p1.tile + 1 < tile && !flush<1>()) return false;
                 uint32_t vstage = stage + 1, vphase = phase;
                 if (vstage == (uint32_t)a.stages) { vstage = 0; vphase ^= 1u; }
-                bool act[2], lst[2];
-                if (pair) {
-                    act[0] = t >= a0 && t < a1;
-                    act[1] = t >= b0 && t < b1;
-                    lst[0] = t + 1 == a1;
-                    lst[1] = t + 1 == b1;
-                } else {
-                    const int s = ((t - t0) + ((flags & RF_START) ? 1 : 0)) & 1;
-                    act[s] = true;
-                    act[s ^ 1] = false;
-                    lst[0] = lst[1] = t + 2 >= t1;
-                }
-                if (!rwait(bars.kvfull + 8 * stage, phase, misc, a)) return false;
+                const int turn = ((t - t0) + start) & 1;
+                const bool act0 = pair ? t >= a0 && t < a1 : turn == 0, act1 = pair ? t >= b0 && t < b1 : turn == 1;
+                const bool last0 = pair ? t + 1 == a1 : t + 2 >= t1, last1 = pair ? t + 1 == b1 : t + 2 >= t1;
+                if (!await(bars.kvfull + 8 * stage, phase)) return false;
                 const int nv = len - t * ROWS_KEYS;
-                if (nv < ROWS_KEYS || !(act[0] || act[1])) {
+                if (nv < ROWS_KEYS || !(act0 || act1)) {
                     if (!rwait(bars.kvfull + 8 * vstage, vphase, misc, a)) return false;
                 }
                 if (nv < ROWS_KEYS) {              // V past the source's end: zeros
@@ -577,34 +683,29 @@ struct RowsMma {
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                for (int s = 0; s < 2; ++s) {
-                    if (!act[s]) continue;
-                    if (!flush(s)) return false;
-                    const uint32_t qb = pair ? (qb0 + (uint32_t)s) & 1u : qb0;
-                    const bool release = s == 1 || !act[1];
+                if (act0) {
+                    if (!flush<0>()) return false;
                     tc_fence_after();
-                    if (lane == 0) {
-                        const uint64_t qd = sw128_kmajor_desc(sbase + lay.q + qb * RowsSmem<D>::QB);
-                        const uint64_t kd = sw128_kmajor_desc(sbase + lay.stages + stage * RowsSmem<D>::SB);
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t off = (uint32_t)(k >> 2) * (RowsSmem<D>::HALF >> 4) + (uint32_t)(k & 3) * 2u;
-                            umma_bf16(tmem + s * TM_S, qd + off, kd + off, IDESC, k > 0 ? 1u : 0u);
-                        }
-                        umma_commit(bars.sfull + 8 * s);
-                        if (release) umma_commit(bars.kvempty + 8 * stage);
-                        // a row tile's Q is free after its last tile of the run
-                        if (pair ? lst[s] : t + 1 == t1) umma_commit(bars.qempty + 8 * qb);
-                    }
-                    __syncwarp();
-                    pend[s] = Pending{true, tile, vstage, vphase, !begun[s], lst[s], release};
-                    begun[s] = true;
+                    // a row tile's Q is free after its last tile of the run
+                    scores<0>(qb0, stage, ncols, !act1, ncols == 0 && (pair ? last0 : t + 1 == t1));
+                    p0.on = true; p0.first = !begun0; p0.last = last0; p0.release = !act1;
+                    p0.tile = tile; p0.stage = vstage; p0.phase = vphase; p0.ncols = ncols;
+                    begun0 = true;
                 }
-                if (!(act[0] || act[1]) && lane == 0) {     // a tile that neither half sees
+                if (act1) {
+                    if (!flush<1>()) return false;
+                    tc_fence_after();
+                    scores<1>(pair ? qb0 ^ 1u : qb0, stage, ncols, true, ncols == 0 && (pair ? last1 : t + 1 == t1));
+                    p1.on = true; p1.first = !begun1; p1.last = last1; p1.release = true;
+                    p1.tile = tile; p1.stage = vstage; p1.phase = vphase; p1.ncols = ncols;
+                    begun1 = true;
+                }
+                if (!(act0 || act1) && lane == 0) {         // a tile that neither half sees
                     mbar_arrive(bars.kvempty + 8 * stage);
                     mbar_arrive(bars.kvempty + 8 * vstage);
                 }
                 __syncwarp();
+#pragma unroll
                 for (int k = 0; k < 2; ++k)
                     if (++stage == (uint32_t)a.stages) { stage = 0; phase ^= 1u; }
             }
@@ -615,7 +716,7 @@ struct RowsMma {
             }
             __syncwarp();
         }
-        return flush(0) && flush(1);
+        return flush<0>() && flush<1>();
     }
 };
 
@@ -623,25 +724,24 @@ struct RowsMma {
 // softmax warps
 // ------------------------------------------------------------------------------------------
 // The keys [k0, k1) of a row again, for columns of its sums that are not finite: sums over the keys it
-// sees alone, in the frame M. By one warp; o: this lane's D / 32 columns (lane + 32 i).
-template <int D>
+// sees alone, in the frame M. By one warp; o: its columns col + 32 i of each lane.
+template <int D, int NC>
 __device__ __noinline__ void redo_row(const RowsArgs& a, int b, int g, int h, int row, int pos, int k0, int k1, int base,
-                                      float M, float cap_rate, float (&o)[D / 32], unsigned& bad)
+                                      float M, int col, float (&o)[NC])
 {
     const int lane = threadIdx.x & 31;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + ((long long)row * a.Hq + h) * D;
     const __nv_bfloat16* kc = static_cast<const __nv_bfloat16*>(b < 0 && a.pk ? a.pk : a.k);
     const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(b < 0 && a.pv ? a.pv : a.v);
-    const float slope = a.slopes ? a.slopes[h] * LOG2E : 0.f;
+    const float slope = a.slopes ? a.slopes[h] * LOG2E : 0.f, cap_rate = a.cap > 0.f ? 2.f * LOG2E / a.cap : 0.f;
     float qr[D / 32];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-        qr[i] = __bfloat162float(q[lane + 32 * i]);
-        o[i] = 0.f;
-    }
+    for (int i = 0; i < D / 32; ++i) qr[i] = __bfloat162float(q[lane + 32 * i]);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) o[i] = 0.f;
     for (int t = k0; t < k1; ++t) {
         const long long off = key_offset(a, b, t, g);
-        if (off < 0) { bad |= FDPP_ERRBIT_BLOCK_TABLE; continue; }
+        if (off < 0) continue;                           // (reported by the load warp)
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) s = fmaf(qr[i], __bfloat162float(kc[off + lane + 32 * i]), s);
@@ -649,8 +749,8 @@ __device__ __noinline__ void redo_row(const RowsArgs& a, int b, int g, int h, in
         const float p = ex2(mod_score(s, a.scale, a.cap, cap_rate, slope, (float)(base + t - pos)) - M);
         bool done = true;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            o[i] = fmaf(p, __bfloat162float(vc[off + lane + 32 * i]), o[i]);
+        for (int i = 0; i < NC; ++i) {
+            o[i] = fmaf(p, __bfloat162float(vc[off + col + 32 * i]), o[i]);
             done = done && o[i] != o[i];
         }
         if (__all_sync(0xffffffffu, done)) break;       // NaN stays NaN
@@ -664,51 +764,148 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
-template <int D, bool MOD>
-__device__ __forceinline__ bool softmax_stream(const RowsArgs& a, const RowsSmem<D>& lay, const RowsBars& bars,
-                                               uint8_t* sm, uint32_t tmem, int s, volatile int* misc)
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair2(float x, float y)
 {
-    const int lane = threadIdx.x & 31, r = threadIdx.x & (ROWS_TILE - 1);
-    const uint32_t lane_base = (uint32_t)(r & ~31) << 16;
-    const uint32_t ts = tmem + lane_base + s * TM_S, to = tmem + lane_base + 2 * TM_S;
-    float2* ml = reinterpret_cast<float2*>(sm + lay.ml);
-    const float rate = MOD ? 1.f : a.scale * LOG2E;      // log2 units per unit of v
-    const float cap_rate = a.cap > 0.f ? 2.f * LOG2E / a.cap : 0.f;
-    const int live_rows = a.tpt * a.G;
-    uint32_t nh = 0, ntile = 0, nacc[2] = {0, 0}, nml[2] = {0, 0};
-    unsigned bad = 0;
-    for (;; ++nh) {
-        const uint32_t hs = nh % RW_HDRS;
-        if (!rwait(bars.hfull + 8 * hs, (nh / RW_HDRS) & 1u, misc, a)) return false;
-        const int* h = reinterpret_cast<const int*>(sm + lay.hdr + hs * RW_HDR_BYTES);
-        const int kind = h[RH_KIND], g = h[RH_G], b = h[RH_B], tok0 = h[RH_TOK0], ntok = h[RH_NTOK], len = h[RH_LEN];
-        const int t0 = h[RH_T0], t1 = h[RH_T1], dest = h[RH_DEST], flags = h[RH_FLAGS], base = h[RH_BASE];
-        const int s0 = s ? h[RH_B0] : h[RH_A0], s1 = s ? h[RH_B1] : h[RH_A1];
-        const bool other_tiles = s ? h[RH_A1] > h[RH_A0] : h[RH_B1] > h[RH_B0];      // (pairs)
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars.hempty + 8 * hs);
-        if (kind == RUN_END) break;
-        const bool pair = flags & RF_PAIR;
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+    return d;
+}
+__device__ __forceinline__ void unpair2(uint64_t d, float& x, float& y)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(d));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+template <int NR>
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[NR])
+{
+    if constexpr (NR == 32) {
+        tmem_ld32_async(taddr, r);
+    } else if constexpr (NR == 16) {
+        tmem_ld16_async(taddr, r);
+    } else {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+    }
+}
+
+template <int NR>
+__device__ __forceinline__ void tmem_st_rows(uint32_t taddr, const uint32_t (&r)[NR])
+{
+#pragma unroll
+    for (int i = 0; i < NR; i += 8)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[i]),
+                     "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]),
+                     "r"(r[i + 7]), "r"(taddr + i)
+                     : "memory");
+}
+
+// Ties the registers to the tcgen05.wait::ld before it.
+template <int NR>
+__device__ __forceinline__ void reg_fence(uint32_t (&r)[NR])
+{
+#pragma unroll
+    for (int i = 0; i < NR; ++i) asm volatile("" : "+r"(r[i]) : : "memory");
+}
+
+// How scores become v, in units of log2: scale alone; scale and bias; cap, scale and bias.
+enum { MODE_PLAIN = 0, MODE_BIAS = 1, MODE_CAP = 2 };
+
+template <int D, int MODE>
+struct Softmax {
+    const RowsArgs& a;
+    const RowsSmem<D>& lay;
+    const RowsBars& bars;
+    uint8_t* sm;
+    uint32_t sbase, tmem;
+    volatile int* misc;
+    // phases passed: headers, this stream's tiles, runs of either stream's accumulator, hand-overs of
+    // either, meetings of this stream's warps, Q buffers
+    uint32_t nh = 0, ntile = 0, nacc = 0, nacc_o = 0, nml = 0, nml_o = 0, nvote = 0, nq = 0;
+
+    struct Run {
+        int g, b, tok0, ntok, len, t0, t1, dest, flags, base, s0, s1;
+        bool other_tiles;
+    };
+
+    template <int S>
+    __device__ __forceinline__ bool run()
+    {
+        const int lane = threadIdx.x & 31;
+        bool ok = true;
+        for (;; ++nh) {
+            const uint32_t hs = nh % RW_HDRS;
+            if (!rwait(bars.hfull + 8 * hs, (nh / RW_HDRS) & 1u, misc, a)) { ok = false; break; }
+            const int* h = reinterpret_cast<const int*>(sm + lay.hdr + hs * RW_HDR_BYTES);
+            const int kind = h[RH_KIND];
+            Run r;
+            r.g = h[RH_G]; r.b = h[RH_B]; r.tok0 = h[RH_TOK0]; r.ntok = h[RH_NTOK]; r.len = h[RH_LEN];
+            r.t0 = h[RH_T0]; r.t1 = h[RH_T1]; r.dest = h[RH_DEST]; r.flags = h[RH_FLAGS]; r.base = h[RH_BASE];
+            r.s0 = S ? h[RH_B0] : h[RH_A0];
+            r.s1 = S ? h[RH_B1] : h[RH_A1];
+            r.other_tiles = S ? h[RH_A1] > h[RH_A0] : h[RH_B1] > h[RH_B0];      // (pairs)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.hempty + 8 * hs);
+            if (kind == RUN_END) break;
+            if (r.flags & RF_NARROW) {
+                const int rows = r.ntok * a.G;
+                ok = rows <= 8 ? narrow<S, 8>(r) : rows <= 16 ? narrow<S, 16>(r) : narrow<S, 32>(r);
+            } else {
+                ok = wide<S>(r);
+            }
+            nq += (r.flags & RF_PAIR) ? 2u : 1u;
+            if (!ok) break;
+        }
+        return ok;
+    }
+
+    // ---- 128 rows on the lanes ----
+    template <int S>
+    __device__ __forceinline__ bool wide(const Run& run)
+    {
+        const int lane = threadIdx.x & 31, r = threadIdx.x & (ROWS_TILE - 1);
+        const uint32_t lane_base = (uint32_t)(r & ~31) << 16;
+        const uint32_t ts = tmem + lane_base + S * TM_S, to = tmem + lane_base + 2 * TM_S;
+        float2* ml = reinterpret_cast<float2*>(sm + lay.ml);
+        const bool pair = run.flags & RF_PAIR;
+        const int start = (run.flags & RF_START) ? 1 : 0, t0 = run.t0, t1 = run.t1, base = run.base;
         // this stream's tiles: first, first + step, .. below past
-        const int start = (flags & RF_START) ? 1 : 0;
-        const int first = pair ? s0 : t0 + (s ^ start), past = pair ? s1 : t1, step = pair ? 1 : 2;
+        const int first = pair ? run.s0 : t0 + (S ^ start), past = pair ? run.s1 : t1, step = pair ? 1 : 2;
         const int ti = r / a.G, hh = r - ti * a.G;
-        const int tok = tok0 + (pair ? s * a.tpt : 0) + ti;
-        const bool live = r < live_rows && tok < tok0 + ntok;
+        const int tok = run.tok0 + (pair ? S * a.tpt : 0) + ti;
+        const bool live = ti < a.tpt && tok < run.tok0 + run.ntok;
         const bool warp_live = __any_sync(0xffffffffu, live);
         RowToken tk{0, 0, 0, -1};
         if (live) tk = a.tok[tok];
         const bool mine = live && tk.rt >= 0;
         // keys of this source that the row sees; a row that is not one masks nothing and is not written
-        int lo = mine ? max(tk.lo - base, 0) : 0, hi = mine ? min(tk.hi - base, len) : INT32_MAX;
+        int lo = mine ? max(tk.lo - base, 0) : 0, hi = mine ? min(tk.hi - base, run.len) : INT32_MAX;
         if (mine && hi <= lo) lo = hi = 0;
+        const bool empty = hi <= lo;
         float slope = 0.f;
-        if (MOD && a.slopes && live) slope = a.slopes[g * a.G + hh] * LOG2E;
-        const float fpos = (float)(tk.pos - base);       // the position in this source's indexes
+        if (MODE != MODE_PLAIN && a.slopes && live) slope = a.slopes[run.g * a.G + hh] * LOG2E;
+        const int spos = tk.pos - base;                  // the position in this source's indexes
+        const float rate = a.scale * LOG2E;
+        const float cap_rate = MODE == MODE_CAP ? 2.f * LOG2E / a.cap : 0.f;
+        // every visible key is at or before the position: the bias is linear in the key
+        const bool linear = __all_sync(0xffffffffu, !mine || hi <= spos + 1);
         float m = -INFINITY, l = 0.f;                    // frame (log2 units) and sum
         int count = 0;
         for (int t = first; t < past; t += step, ++ntile, ++count) {
-            if (!rwait(bars.sfull + 8 * s, ntile & 1u, misc, a)) return false;
+            if (!rwait(bars.sfull + 8 * S, ntile & 1u, misc, a)) return false;
             tc_fence_after();
             if (warp_live) {
                 uint32_t x[ROWS_KEYS];
@@ -718,11 +915,23 @@ __device__ __forceinline__ bool softmax_stream(const RowsArgs& a, const RowsSmem
 #pragma unroll
                 for (int i = 0; i < 4; ++i) reg_fence32(x + 32 * i);
                 const int k0 = t * ROWS_KEYS;
-                if (MOD) {
-                    const float d0 = (float)k0 - fpos;
+                if (MODE == MODE_BIAS && linear) {
+                    const float b0 = slope * (float)(k0 - spos);
+                    const uint64_t rate2 = pair2(rate, rate);
+#pragma unroll
+                    for (int i = 0; i < ROWS_KEYS; i += 2) {
+                        float v0, v1;
+                        unpair2(fma2(pair2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), rate2,
+                                     pair2(fmaf(slope, (float)i, b0), fmaf(slope, (float)(i + 1), b0))), v0, v1);
+                        x[i] = __float_as_uint(v0);
+                        x[i + 1] = __float_as_uint(v1);
+                    }
+                } else if (MODE != MODE_PLAIN) {
+                    const float d0 = (float)(k0 - spos);
 #pragma unroll
                     for (int i = 0; i < ROWS_KEYS; ++i)
-                        x[i] = __float_as_uint(mod_score(__uint_as_float(x[i]), a.scale, a.cap, cap_rate, slope, d0 + (float)i));
+                        x[i] = __float_as_uint(mod_score(__uint_as_float(x[i]), a.scale, MODE == MODE_CAP ? a.cap : 0.f,
+                                                         cap_rate, slope, d0 + (float)i));
                 }
                 if (!__all_sync(0xffffffffu, lo <= k0 && hi >= k0 + ROWS_KEYS)) {
                     const int c0 = lo - k0, c1 = hi - k0;
@@ -738,7 +947,8 @@ __device__ __forceinline__ bool softmax_stream(const RowsArgs& a, const RowsSmem
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         mx[k] = max3(mx[k], __uint_as_float(x[i + k]), __uint_as_float(x[i + 4 + k]));
-                const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * rate;
+                float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                if (MODE == MODE_PLAIN) top *= rate;
                 if (count == 0) {
                     m = top;
                 } else if (__any_sync(0xffffffffu, top > m + RW_LAG)) {
@@ -747,85 +957,90 @@ __device__ __forceinline__ bool softmax_stream(const RowsArgs& a, const RowsSmem
                     const float f = fmaxf(m, top), w = m == f ? 1.f : ex2(m - f);
                     m = f;
                     l *= w;
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        uint32_t o[32];
-                        tmem_ld32_async(to + s * D + 32 * i, o);
+#pragma unroll 1
+                    for (int i = 0; i < D; i += 16) {
+                        uint32_t o[16];
+                        tmem_ld16_async(to + S * D + i, o);
                         tmem_wait_ld();
-                        reg_fence32(o);
+                        reg_fence16(o);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * w);
-                        tmem_st32(to + s * D + 32 * i, o);
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * w);
+                        tmem_st_rows<16>(to + S * D + i, o);
                     }
                 }
                 const float mu = m == -INFINITY ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t nmu = pair2(-mu, -mu), rate2 = pair2(rate, rate);
+                uint64_t s0 = pair2(0.f, 0.f), s1 = s0;
 #pragma unroll
                 for (int i = 0; i < ROWS_KEYS; i += 4) {
-                    float p[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        p[k] = ex2(fmaf(__uint_as_float(x[i + k]), rate, -mu));
-                        sum[k] += p[k];
-                    }
-                    x[i / 2] = pack_bf16x2(p[0], p[1]);
-                    x[i / 2 + 1] = pack_bf16x2(p[2], p[3]);
+                    uint64_t v0 = pair2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                    uint64_t v1 = pair2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+                    if (MODE == MODE_PLAIN) { v0 = fma2(v0, rate2, nmu); v1 = fma2(v1, rate2, nmu); }
+                    else { v0 = add2(v0, nmu); v1 = add2(v1, nmu); }
+                    float p0, p1, p2, p3;
+                    unpair2(v0, p0, p1);
+                    unpair2(v1, p2, p3);
+                    p0 = ex2(p0); p1 = ex2(p1); p2 = ex2(p2); p3 = ex2(p3);
+                    s0 = add2(s0, pair2(p0, p1));
+                    s1 = add2(s1, pair2(p2, p3));
+                    x[i / 2] = pack_bf16x2(p0, p1);
+                    x[i / 2 + 1] = pack_bf16x2(p2, p3);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tmem_st32(ts, x);
                 tmem_st32(ts + 32, x + 32);
+                float p0, p1;
+                unpair2(add2(s0, s1), p0, p1);
+                l += p0 + p1;
                 tmem_wait_st();
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bars.pready + 8 * s);
+            if (lane == 0) mbar_arrive(bars.pready + 8 * S);
         }
 
         // ---- the run's end ----
-        const int other = s ^ 1;
-        const int n_other = pair ? 0 : max(0, (t1 - t0 + (other == start ? 1 : 0)) / 2);
-        if (!pair && s != start) {                       // hand over to the other stream
+        constexpr int O = S ^ 1;
+        if (!pair && S != start) {                       // hand over to the other stream
             if (count > 0) {
-                if (!rwait(bars.mlfree + 8 * s, (nml[s] & 1u) ^ 1u, misc, a)) return false;
-                ml[s * ROWS_TILE + r] = make_float2(m, l);
+                if (!rwait(bars.mlfree + 8 * S, (nml & 1u) ^ 1u, misc, a)) return false;
+                ml[S * ROWS_TILE + r] = make_float2(m, l);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bars.mlready + 8 * s);
-                ++nml[s];
-                ++nacc[s];
+                if (lane == 0) mbar_arrive(bars.mlready + 8 * S);
+                ++nml;
+                ++nacc;
             }
-            ++nacc[other];
-            continue;
+            ++nacc_o;
+            return true;
         }
-        float mo = -INFINITY, wo = 0.f, ws = 1.f;        // the other stream's frame and weights
-        if (count > 0 && !rwait(bars.ofull + 8 * s, nacc[s] & 1u, misc, a)) return false;
-        if (n_other > 0) {
-            if (!rwait(bars.mlready + 8 * other, nml[other] & 1u, misc, a)) return false;
-            const float2 x = ml[other * ROWS_TILE + r];
+        const bool other = !pair && t1 - t0 > 1;         // the other stream had tiles of these rows
+        float wo = 0.f, ws = 1.f;                        // the streams' weights
+        if (count > 0 && !rwait(bars.ofull + 8 * S, nacc & 1u, misc, a)) return false;
+        if (other) {
+            if (!rwait(bars.mlready + 8 * O, nml_o & 1u, misc, a)) return false;
+            const float2 x = ml[O * ROWS_TILE + r];
             __syncwarp();
-            if (lane == 0) mbar_arrive(bars.mlfree + 8 * other);
-            if (!rwait(bars.ofull + 8 * other, nacc[other] & 1u, misc, a)) return false;
-            mo = x.x;
-            const float f = fmaxf(m, mo);
+            if (lane == 0) mbar_arrive(bars.mlfree + 8 * O);
+            if (!rwait(bars.ofull + 8 * O, nacc_o & 1u, misc, a)) return false;
+            const float f = fmaxf(m, x.x);
             ws = m == f ? 1.f : ex2(m - f);
-            wo = mo == f ? 1.f : ex2(mo - f);
+            wo = x.x == f ? 1.f : ex2(x.x - f);
             l = l * ws + x.y * wo;
             m = f;
         }
         tc_fence_after();
-        const int head = g * a.G + hh;
-        const bool direct = dest == DEST_OUT;
-        const bool empty = hi <= lo;
+        const int head = run.g * a.G + hh;
+        const bool direct = run.dest == DEST_OUT;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((long long)tok * a.Hq + head) * D;
         float* po = nullptr;
         if (!direct && mine) {
             long long at;
             float2* pml;
-            if (dest == DEST_ROWS) {
-                at = ((b < 0 ? 0ll : (long long)a.T) + tok) * a.Hq + head;
+            if (run.dest == DEST_ROWS) {
+                at = ((run.b < 0 ? 0ll : (long long)a.T) + tok) * a.Hq + head;
                 po = a.row_o + at * D;
                 pml = a.row_ml + at;
             } else {
-                at = (long long)dest * a.slot_rows + (tok - tok0) * a.G + hh;
+                at = (long long)run.dest * a.slot_rows + (tok - run.tok0) * a.G + hh;
                 po = a.slot_o + at * D;
                 pml = a.slot_ml + at;
             }
@@ -835,13 +1050,15 @@ __device__ __forceinline__ bool softmax_stream(const RowsArgs& a, const RowsSmem
         if (warp_live && (count > 0 || direct)) {
             const float inv = direct ? 1.f / l : 1.f;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
+            for (int i = 0; i < D; i += 32) {
                 uint32_t x[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[k] = 0u;
                 if (count > 0) {
-                    tmem_ld32_async(to + s * D + 32 * i, x);
-                    if (n_other > 0) {
+                    tmem_ld32_async(to + S * D + i, x);
+                    if (other) {
                         uint32_t y[32];
-                        tmem_ld32_async(to + other * D + 32 * i, y);
+                        tmem_ld32_async(to + O * D + i, y);
                         tmem_wait_ld();
                         reg_fence32(x);
                         reg_fence32(y);
@@ -855,8 +1072,7 @@ __device__ __forceinline__ bool softmax_stream(const RowsArgs& a, const RowsSmem
                 }
 #pragma unroll
                 for (int k = 0; k < 32; ++k) fine = fine && fabsf(__uint_as_float(x[k])) < INFINITY;
-                if (!mine) continue;
-                if (direct) {
+                if (mine && direct) {
 #pragma unroll
                     for (int k = 0; k < 32; k += 8) {
                         uint4 v = make_uint4(0, 0, 0, 0);
@@ -865,23 +1081,23 @@ __device__ __forceinline__ bool softmax_stream(const RowsArgs& a, const RowsSmem
                                            pack_bf16x2(__uint_as_float(x[k + 2]) * inv, __uint_as_float(x[k + 3]) * inv),
                                            pack_bf16x2(__uint_as_float(x[k + 4]) * inv, __uint_as_float(x[k + 5]) * inv),
                                            pack_bf16x2(__uint_as_float(x[k + 6]) * inv, __uint_as_float(x[k + 7]) * inv));
-                        *reinterpret_cast<uint4*>(out + 32 * i + k) = v;
+                        *reinterpret_cast<uint4*>(out + i + k) = v;
                     }
-                } else {
+                } else if (mine) {
 #pragma unroll
                     for (int k = 0; k < 32; k += 4)
-                        *reinterpret_cast<uint4*>(po + 32 * i + k) = make_uint4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+                        *reinterpret_cast<uint4*>(po + i + k) = make_uint4(x[k], x[k + 1], x[k + 2], x[k + 3]);
                 }
             }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-            if (count > 0) mbar_arrive(bars.ofree + 8 * s);
-            if (n_other > 0) mbar_arrive(bars.ofree + 8 * other);
+            if (count > 0) mbar_arrive(bars.ofree + 8 * S);
+            if (other) mbar_arrive(bars.ofree + 8 * O);
         }
         // Rows that may have met a non-finite V of a key they do not see
-        const int seen0 = (pair ? s0 : t0) * ROWS_KEYS, seen1 = min((pair ? s1 : t1) * ROWS_KEYS, len);
+        const int seen0 = (pair ? run.s0 : t0) * ROWS_KEYS, seen1 = min((pair ? run.s1 : t1) * ROWS_KEYS, run.len);
         const bool again = mine && count > 0 && !fine && !empty && fabsf(l) < INFINITY && (lo > seen0 || hi < seen1);
         unsigned todo = __ballot_sync(0xffffffffu, again);
         while (todo) {
@@ -893,7 +1109,7 @@ __device__ __forceinline__ bool softmax_stream(const RowsArgs& a, const RowsSmem
             const float jm = __shfl_sync(0xffffffffu, m, j), jl = __shfl_sync(0xffffffffu, l, j);
             float* jpo = reinterpret_cast<float*>(__shfl_sync(0xffffffffu, (unsigned long long)po, j));
             float o[D / 32];
-            redo_row<D>(a, b, g, jhead, jtok, jpos, jlo, jhi, base, jm == -INFINITY ? 0.f : jm, cap_rate, o, bad);
+            redo_row<D, D / 32>(a, run.b, run.g, jhead, jtok, jpos, jlo, jhi, base, jm == -INFINITY ? 0.f : jm, lane, o);
             __nv_bfloat16* jout = static_cast<__nv_bfloat16*>(a.out) + ((long long)jtok * a.Hq + jhead) * D;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
@@ -901,22 +1117,270 @@ __device__ __forceinline__ bool softmax_stream(const RowsArgs& a, const RowsSmem
                 else jpo[lane + 32 * i] = o[i];
             }
         }
-        if (count > 0) ++nacc[s];
-        if (n_other > 0) { ++nacc[other]; ++nml[other]; }
-        if (pair && other_tiles) ++nacc[other];
+        if (count > 0) ++nacc;
+        if (other) ++nml_o;
+        if (pair ? run.other_tiles : other) ++nacc_o;
+        return true;
     }
-    rows_error(a, bad);
-    return true;
-}
+
+    // The four warps of this stream meet (bounded).
+    template <int S>
+    __device__ __forceinline__ bool meet()
+    {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bars.vote + 8 * S);
+        const bool ok = rwait(bars.vote + 8 * S, nvote & 1u, misc, a);
+        ++nvote;
+        return ok;
+    }
+
+    // ---- up to 32 rows, the keys on the lanes ----
+    // A thread holds one key of each tile for all NR rows: S^T comes from tensor memory as NR columns,
+    // the weights go to shared memory as the K-major operand P^T, and O^T has d on its lanes. The rows'
+    // frames are the same in all threads: the warps meet once a tile to see whether a score is beyond its
+    // row's frame by more than the lag, and exchange maxima only then.
+    template <int S, int NR>
+    __device__ __forceinline__ bool narrow(const Run& run)
+    {
+        constexpr int O = S ^ 1;
+        const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
+        const uint32_t lane_base = (uint32_t)(32 * w) << 16;
+        const uint32_t ts = tmem + lane_base + S * TM_S, to = tmem + lane_base + 2 * TM_S;
+        volatile NarrowShared& sh = *reinterpret_cast<volatile NarrowShared*>(sm + lay.q + RowsSmem<D>::NSH_OFF);
+        uint8_t* prow = sm + lay.q + RowsSmem<D>::NP_OFF + S * RowsSmem<D>::NP + (w >> 1) * RowsSmem<D>::NQ_HALF;
+        const int pcol = ((w & 1) * 32 + lane) * 2;
+        const int start = (run.flags & RF_START) ? 1 : 0, base = run.base, R = run.ntok * a.G;
+        // row `lane` (of the rows < R): token, head, keys
+        const int ti = lane / a.G, hh = lane - ti * a.G, tok = run.tok0 + ti, head = run.g * a.G + hh;
+        RowToken tk{0, 0, 0, -1};
+        if (lane < R) tk = a.tok[tok];
+        const bool mine = lane < R && tk.rt >= 0;
+        int lo = 0, hi = 0;
+        if (mine) {
+            lo = max(tk.lo - base, 0);
+            hi = min(tk.hi - base, run.len);
+            if (hi <= lo) lo = hi = 0;
+        }
+        const int all_lo = warp_max(mine ? lo : 0), all_hi = warp_min(mine ? hi : INT32_MAX);
+        float slope_l = 0.f;
+        if (MODE != MODE_PLAIN && a.slopes && lane < R) slope_l = a.slopes[head] * LOG2E;
+        const int spos_l = tk.pos - base;
+        float fr[NR], l[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            fr[r] = -INFINITY;
+            l[r] = 0.f;
+        }
+        const float rate = a.scale * LOG2E;
+        const float cap_rate = MODE == MODE_CAP ? 2.f * LOG2E / a.cap : 0.f;
+        int count = 0;
+        for (int t = run.t0 + (S ^ start); t < run.t1; t += 2, ++ntile, ++count) {
+            if (!rwait(bars.sfull + 8 * S, ntile & 1u, misc, a)) return false;
+            tc_fence_after();
+            uint32_t x[NR];
+            tmem_ld_rows<NR>(ts, x);
+            tmem_wait_ld();
+            reg_fence<NR>(x);
+            const int k0 = t * ROWS_KEYS, key = k0 + 32 * w + lane;
+            float v[NR];
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                if (MODE == MODE_PLAIN) {
+                    v[r] = __uint_as_float(x[r]) * rate;
+                } else {
+                    const float slope = __shfl_sync(0xffffffffu, slope_l, r);
+                    const int spos = __shfl_sync(0xffffffffu, spos_l, r);
+                    v[r] = mod_score(__uint_as_float(x[r]), a.scale, MODE == MODE_CAP ? a.cap : 0.f, cap_rate, slope,
+                                     (float)(key - spos));
+                }
+                if (r >= R) v[r] = -INFINITY;
+            }
+            if (!(all_lo <= k0 && all_hi >= k0 + ROWS_KEYS)) {
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const int rlo = __shfl_sync(0xffffffffu, lo, r), rhi = __shfl_sync(0xffffffffu, hi, r);
+                    if (key < rlo || key >= rhi) v[r] = -INFINITY;
+                }
+            }
+            bool beyond = false;
+#pragma unroll
+            for (int r = 0; r < NR; ++r) beyond = beyond || v[r] > fr[r] + RW_LAG;
+            beyond = __any_sync(0xffffffffu, beyond);
+            const uint32_t par = nvote & 1u;
+            if (lane == 0) sh.flag[S][par][w] = beyond;
+            if (!meet<S>()) return false;
+            if (sh.flag[S][par][0] | sh.flag[S][par][1] | sh.flag[S][par][2] | sh.flag[S][par][3]) {
+                float mine_max = -INFINITY;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    float x = v[r];
+#pragma unroll
+                    for (int k = 16; k > 0; k >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
+                    if (lane == r) mine_max = x;
+                }
+                if (lane < NR) sh.wmax[S][w][lane] = mine_max;
+                if (!meet<S>()) return false;
+#pragma unroll
+                for (int c = 0; c < NR; c += 8) {
+                    uint32_t o[8];
+                    if (count > 0) {
+                        tmem_ld_rows<8>(to + S * D + c, o);
+                        tmem_wait_ld();
+                        reg_fence<8>(o);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = c + i;
+                        const float f = fmaxf(fmaxf(fr[r], fmaxf(sh.wmax[S][0][r], sh.wmax[S][1][r])),
+                                              fmaxf(sh.wmax[S][2][r], sh.wmax[S][3][r]));
+                        const float wt = fr[r] == f ? 1.f : ex2(fr[r] - f);
+                        fr[r] = f;
+                        l[r] *= wt;
+                        if (count > 0) o[i] = __float_as_uint(__uint_as_float(o[i]) * wt);
+                    }
+                    if (count > 0) tmem_st_rows<8>(to + S * D + c, o);
+                }
+                tmem_wait_st();
+            }
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                const float p = ex2(v[r] - (fr[r] == -INFINITY ? 0.f : fr[r]));
+                l[r] += p;
+                *reinterpret_cast<__nv_bfloat16*>(prow + r * 128 + (pcol ^ ((r & 7) << 4))) = __float2bfloat16_rn(p);
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.pready + 8 * S);
+        }
+
+        // ---- the run's end ----
+        if (count > 0) {
+            if (!rwait(bars.mlfree + 8 * S, (nml & 1u) ^ 1u, misc, a)) return false;
+            float mine_l = 0.f, mine_f = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                const float x = warp_sum(l[r]);
+                if (lane == r) { mine_l = x; mine_f = fr[r]; }
+            }
+            if (lane < NR) {
+                sh.lsum[S][w][lane] = mine_l;
+                if (w == 0) sh.frame[S][lane] = mine_f;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.mlready + 8 * S);
+            ++nml;
+        }
+        const bool other = run.t1 - run.t0 > 1;          // both streams had tiles
+        if (S != start) {
+            if (count > 0) ++nacc;
+            ++nacc_o;
+            ++nml_o;
+            return true;
+        }
+        if (!rwait(bars.mlready + 8 * S, (nml - 1) & 1u, misc, a)) return false;
+        if (!rwait(bars.ofull + 8 * S, nacc & 1u, misc, a)) return false;
+        if (other) {
+            if (!rwait(bars.mlready + 8 * O, nml_o & 1u, misc, a)) return false;
+            if (!rwait(bars.ofull + 8 * O, nacc_o & 1u, misc, a)) return false;
+        }
+        tc_fence_after();
+        // row `lane`: both streams' frames and sums joined
+        float m = -INFINITY, lt = 0.f, ws = 1.f, wo = 0.f;
+        if (lane < NR) {
+            m = sh.frame[S][lane];
+            lt = (sh.lsum[S][0][lane] + sh.lsum[S][1][lane]) + (sh.lsum[S][2][lane] + sh.lsum[S][3][lane]);
+            if (other) {
+                const float mo = sh.frame[O][lane], f = fmaxf(m, mo);
+                const float lo_ = (sh.lsum[O][0][lane] + sh.lsum[O][1][lane]) + (sh.lsum[O][2][lane] + sh.lsum[O][3][lane]);
+                ws = m == f ? 1.f : ex2(m - f);
+                wo = mo == f ? 1.f : ex2(mo - f);
+                lt = lt * ws + lo_ * wo;
+                m = f;
+            }
+        }
+        const bool direct = run.dest == DEST_OUT;
+        const bool has = D == 128 || lane < 16;           // a 64-row accumulator leaves lanes 16-31 out
+        const int d = D == 128 ? 32 * w + lane : 16 * w + (lane & 15);
+        long long at = 0;                                 // the row's place: out, a slot or the whole-unit arrays
+        if (direct) at = (long long)tok * a.Hq + head;
+        else if (run.dest == DEST_ROWS) at = ((run.b < 0 ? 0ll : (long long)a.T) + tok) * a.Hq + head;
+        else at = (long long)run.dest * a.slot_rows + lane;
+        float* pbase = run.dest == DEST_ROWS ? a.row_o : a.slot_o;
+        if (!direct && mine && w == 0) (run.dest == DEST_ROWS ? a.row_ml : a.slot_ml)[at] = make_float2(m, lt);
+        const float inv_l = 1.f / lt;
+        const bool empty_l = hi <= lo;
+        unsigned todo = 0;
+#pragma unroll 1
+        for (int c = 0; c < NR; c += 8) {
+            uint32_t x[8], y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            tmem_ld_rows<8>(to + S * D + c, x);
+            if (other) tmem_ld_rows<8>(to + O * D + c, y);
+            tmem_wait_ld();
+            reg_fence<8>(x);
+            reg_fence<8>(y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = c + i;
+                const float rws = __shfl_sync(0xffffffffu, ws, r), rwo = __shfl_sync(0xffffffffu, wo, r);
+                const float inv = __shfl_sync(0xffffffffu, inv_l, r);
+                const long long rat = __shfl_sync(0xffffffffu, at, r);
+                const bool rmine = __shfl_sync(0xffffffffu, (int)mine, r), rempty = __shfl_sync(0xffffffffu, (int)empty_l, r);
+                float val = __uint_as_float(x[i]);
+                if (other) val = val * rws + __uint_as_float(y[i]) * rwo;
+                if (__any_sync(0xffffffffu, has && !(fabsf(val) < INFINITY))) todo |= 1u << r;
+                if (!rmine || !has) continue;
+                if (direct) static_cast<__nv_bfloat16*>(a.out)[rat * D + d] = __float2bfloat16_rn(rempty ? 0.f : val * inv);
+                else pbase[rat * D + d] = val;
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(bars.ofree + 8 * S);
+            mbar_arrive(bars.mlfree + 8 * S);
+            if (other) {
+                mbar_arrive(bars.ofree + 8 * O);
+                mbar_arrive(bars.mlfree + 8 * O);
+            }
+        }
+        // Rows that may have met a non-finite V of a key they do not see: this warp's columns again
+        const int seen0 = run.t0 * ROWS_KEYS, seen1 = min(run.t1 * ROWS_KEYS, run.len);
+        todo &= __ballot_sync(0xffffffffu, mine && !empty_l && fabsf(lt) < INFINITY && (lo > seen0 || hi < seen1));
+        __syncwarp();
+        while (todo) {
+            const int j = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const int jtok = __shfl_sync(0xffffffffu, tok, j), jhead = __shfl_sync(0xffffffffu, head, j);
+            const int jpos = __shfl_sync(0xffffffffu, tk.pos, j);
+            const int jlo = max(__shfl_sync(0xffffffffu, lo, j), seen0), jhi = min(__shfl_sync(0xffffffffu, hi, j), seen1);
+            const float jm = __shfl_sync(0xffffffffu, m, j), inv = __shfl_sync(0xffffffffu, inv_l, j);
+            const long long jat = __shfl_sync(0xffffffffu, at, j);
+            float o[1];
+            redo_row<D, 1>(a, run.b, run.g, jhead, jtok, jpos, jlo, jhi, base, jm == -INFINITY ? 0.f : jm, d, o);
+            if (has) {
+                if (direct) static_cast<__nv_bfloat16*>(a.out)[jat * D + d] = __float2bfloat16_rn(o[0] * inv);
+                else pbase[jat * D + d] = o[0];
+            }
+        }
+        ++nacc;
+        if (other) { ++nacc_o; ++nml_o; }
+        // the run's Q slot, weights and shared words are free
+        if (!meet<S>()) return false;
+        if (w == 0 && lane == 0) mbar_arrive(bars.qempty + 8 * (nq & 1u));
+        return true;
+    }
+};
 
 // ------------------------------------------------------------------------------------------
 // tile kernel
 // ------------------------------------------------------------------------------------------
-template <int D, bool MOD>
+template <int D, int MODE>
 __global__ void __launch_bounds__(RW_THREADS, 1)
-    rows_tile_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tpk,
-                     const __grid_constant__ CUtensorMap tpv, const RowsArgs a)
+    rows_tile_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tqn,
+                     const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                     const __grid_constant__ CUtensorMap tpk, const __grid_constant__ CUtensorMap tpv,
+                     const __grid_constant__ RowsArgs a)
 {
     extern __shared__ __align__(1024) uint8_t sm[];
     constexpr uint32_t NCOLS = 512;              // 2 x 128 of scores, 2 x D of sums
@@ -948,6 +1412,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
             mbar_init(bars.ofree + 8 * i, 4);
             mbar_init(bars.mlready + 8 * i, 4);
             mbar_init(bars.mlfree + 8 * i, 4);
+            mbar_init(bars.vote + 8 * i, 4);
         }
         mbar_init(bars.drain, 1);
         misc[0] = 0;
@@ -956,6 +1421,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
     if (warp == RW_MMA_WARP) tmem_alloc(smem_u32(tslot), NCOLS);
     if (warp == RW_LOAD_WARP && lane == 0) {
         prefetch_tensormap(&tq);
+        prefetch_tensormap(&tqn);
         prefetch_tensormap(&tk);
         prefetch_tensormap(&tv);
         prefetch_tensormap(&tpk);
@@ -967,20 +1433,25 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
     const uint32_t tmem = *tslot;
     grid_dependency_wait();
     grid_launch_dependents();
-    if (warp == RW_LOAD_WARP) {
-        RowsLoader<D> ld{a, lay, bars, sm, sbase, misc};
-        if (!ld.run(&tq, &tk, &tv, &tpk, &tpv)) ld.settle();
-        if (ld.bad) rows_error(a, ld.bad);
-    } else if (warp == RW_MMA_WARP) {
-        RowsMma<D> mma{a, lay, bars, sm, sbase, tmem, misc};
-        mma.run();
-        // every MMA issued has landed before the tensor memory and the stages go
-        if (lane == 0) umma_commit(bars.drain);
-        __syncwarp();
-        if (!mbar_wait(bars.drain, 0u) && lane == 0) rows_error(a, FDPP_ERRBIT_TIMEOUT);
-        __syncwarp();
+    if (warp >= RW_MMA_WARP) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RW_HELP_REGS));
+        if (warp == RW_LOAD_WARP) {
+            RowsLoader<D> ld{a, lay, bars, sm, sbase, misc};
+            if (!ld.run(&tq, &tqn, &tk, &tv, &tpk, &tpv)) ld.settle();
+            if (ld.bad) rows_error(a, ld.bad);
+        } else if (warp == RW_MMA_WARP) {
+            RowsMma<D> mma{a, lay, bars, sbase, tmem, misc};
+            mma.run(sm);
+            // every MMA issued has landed before the tensor memory and the stages go
+            if (lane == 0) umma_commit(bars.drain);
+            __syncwarp();
+            if (!mbar_wait(bars.drain, 0u) && lane == 0) rows_error(a, FDPP_ERRBIT_TIMEOUT);
+            __syncwarp();
+        }
     } else {
-        softmax_stream<D, MOD>(a, lay, bars, sm, tmem, warp >> 2, misc);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(RW_SOFT_REGS));
+        Softmax<D, MODE> sx{a, lay, bars, sm, sbase, tmem, misc};
+        if (warp < 4) sx.template run<0>(); else sx.template run<1>();
         tc_fence_before();
     }
     __syncthreads();
@@ -1116,18 +1587,17 @@ struct PdlConfig {
     }
 };
 
-template <int D, bool MOD>
-cudaError_t launch_d(const RowsArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                     const CUtensorMap& tpk, const CUtensorMap& tpv, cudaStream_t s)
+template <int D, int MODE>
+cudaError_t launch_d(const RowsArgs& a, const RowsMaps& m, cudaStream_t s)
 {
     PdlConfig plan(dim3(1), PLAN_THREADS, 0, s);
     cudaError_t e = cudaLaunchKernelEx(&plan.cfg, rows_plan_kernel, a);
     if (e != cudaSuccess) return e;
-    auto kern = rows_tile_kernel<D, MOD>;
+    auto kern = rows_tile_kernel<D, MODE>;
     const int smem = RowsSmem<D>(a.stages).total;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
     PdlConfig tile(dim3((unsigned)a.parts), RW_THREADS, (size_t)smem, s);
-    if ((e = cudaLaunchKernelEx(&tile.cfg, kern, tq, tk, tv, tpk, tpv, a)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&tile.cfg, kern, m.q, m.qn, m.k, m.v, m.pk, m.pv, a)) != cudaSuccess) return e;
     if (a.prefix_len) {
         const long long rows = (long long)a.T * a.Hq;
         PdlConfig join(dim3((unsigned)((rows + JOIN_WARPS - 1) / JOIN_WARPS)), JOIN_WARPS * 32, 0, s);
@@ -1148,13 +1618,16 @@ int rows_tc_stages(int head_dim, int smem_per_block)
     return n;
 }
 
-cudaError_t launch_rows_tc(const RowsArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                           const CUtensorMap& tpk, const CUtensorMap& tpv, cudaStream_t s)
+cudaError_t launch_rows_tc(const RowsArgs& a, const RowsMaps& m, cudaStream_t s)
 {
-    const bool mod = a.cap > 0.f || a.slopes;
+    const int mode = a.cap > 0.f ? MODE_CAP : (a.slopes ? MODE_BIAS : MODE_PLAIN);
     if (a.D == 128)
-        return mod ? launch_d<128, true>(a, tq, tk, tv, tpk, tpv, s) : launch_d<128, false>(a, tq, tk, tv, tpk, tpv, s);
-    return mod ? launch_d<64, true>(a, tq, tk, tv, tpk, tpv, s) : launch_d<64, false>(a, tq, tk, tv, tpk, tpv, s);
+        return mode == MODE_CAP    ? launch_d<128, MODE_CAP>(a, m, s)
+               : mode == MODE_BIAS ? launch_d<128, MODE_BIAS>(a, m, s)
+                                   : launch_d<128, MODE_PLAIN>(a, m, s);
+    return mode == MODE_CAP    ? launch_d<64, MODE_CAP>(a, m, s)
+           : mode == MODE_BIAS ? launch_d<64, MODE_BIAS>(a, m, s)
+                               : launch_d<64, MODE_PLAIN>(a, m, s);
 }
 
 }  // namespace fdpp
