@@ -47,9 +47,7 @@ namespace {
 
 constexpr int RW_MMA_WARP = 8;
 constexpr int RW_LOAD_WARP = 9;
-constexpr int RW_THREADS = 12 * 32;      // the last two warps idle: register shares go by warpgroup
-constexpr int RW_SOFT_REGS = 200;        // 2 x 128 x 200 + 128 x 104 = 64512 = 384 x 168, the launch's share
-constexpr int RW_HELP_REGS = 104;
+constexpr int RW_THREADS = 10 * 32;
 constexpr int RW_HDRS = 4;               // run headers in flight
 constexpr int RW_HDR_BYTES = 64;
 constexpr float RW_LAG = 8.f;            // log2 of the growth of a row's max that moves its frame
@@ -764,6 +762,18 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
+__device__ __forceinline__ float max32(const uint32_t (&y)[32])
+{
+    float m[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = fmaxf(__uint_as_float(y[k]), __uint_as_float(y[k + 4]));
+#pragma unroll
+    for (int i = 8; i < 32; i += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = max3(m[k], __uint_as_float(y[i + k]), __uint_as_float(y[i + 4 + k]));
+    return max3(fmaxf(m[0], m[1]), m[2], m[3]);
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t pair2(float x, float y)
 {
@@ -805,6 +815,14 @@ __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[NR])
 template <int NR>
 __device__ __forceinline__ void tmem_st_rows(uint32_t taddr, const uint32_t (&r)[NR])
 {
+    if constexpr (NR == 16) {
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+            "%13, %14, %15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+            "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+            : "memory");
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < NR; i += 8)
         asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[i]),
@@ -830,8 +848,9 @@ struct Softmax {
     const RowsSmem<D>& lay;
     const RowsBars& bars;
     uint8_t* sm;
-    uint32_t sbase, tmem;
+    uint32_t tmem;
     volatile int* misc;
+    int S;                   // the stream
     // phases passed: headers, this stream's tiles, runs of either stream's accumulator, hand-overs of
     // either, meetings of this stream's warps, Q buffers
     uint32_t nh = 0, ntile = 0, nacc = 0, nacc_o = 0, nml = 0, nml_o = 0, nvote = 0, nq = 0;
@@ -841,7 +860,6 @@ struct Softmax {
         bool other_tiles;
     };
 
-    template <int S>
     __device__ __forceinline__ bool run()
     {
         const int lane = threadIdx.x & 31;
@@ -862,9 +880,9 @@ struct Softmax {
             if (kind == RUN_END) break;
             if (r.flags & RF_NARROW) {
                 const int rows = r.ntok * a.G;
-                ok = rows <= 8 ? narrow<S, 8>(r) : rows <= 16 ? narrow<S, 16>(r) : narrow<S, 32>(r);
+                ok = rows <= 8 ? narrow<8>(r) : rows <= 16 ? narrow<16>(r) : narrow<32>(r);
             } else {
-                ok = wide<S>(r);
+                ok = wide(r);
             }
             nq += (r.flags & RF_PAIR) ? 2u : 1u;
             if (!ok) break;
@@ -873,7 +891,6 @@ struct Softmax {
     }
 
     // ---- 128 rows on the lanes ----
-    template <int S>
     __device__ __forceinline__ bool wide(const Run& run)
     {
         const int lane = threadIdx.x & 31, r = threadIdx.x & (ROWS_TILE - 1);
@@ -908,47 +925,62 @@ struct Softmax {
             if (!rwait(bars.sfull + 8 * S, ntile & 1u, misc, a)) return false;
             tc_fence_after();
             if (warp_live) {
-                uint32_t x[ROWS_KEYS];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tmem_ld32_async(ts + 32 * i, x + 32 * i);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) reg_fence32(x + 32 * i);
                 const int k0 = t * ROWS_KEYS;
-                if (MODE == MODE_BIAS && linear) {
-                    const float b0 = slope * (float)(k0 - spos);
-                    const uint64_t rate2 = pair2(rate, rate);
+                // first pass: the tile's maximum. Scores that need more than the scale go back to tensor
+                // memory as v, masked ones as -inf.
+                const bool open = __all_sync(0xffffffffu, lo <= k0 && hi >= k0 + ROWS_KEYS);
+                float top = -INFINITY;
+                uint32_t x[2][32];
+                tmem_ld32_async(ts, x[0]);
+                if (MODE == MODE_PLAIN && open) {
 #pragma unroll
-                    for (int i = 0; i < ROWS_KEYS; i += 2) {
-                        float v0, v1;
-                        unpair2(fma2(pair2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), rate2,
-                                     pair2(fmaf(slope, (float)i, b0), fmaf(slope, (float)(i + 1), b0))), v0, v1);
-                        x[i] = __float_as_uint(v0);
-                        x[i + 1] = __float_as_uint(v1);
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t(&y)[32] = x[c & 1];
+                        tmem_wait_ld();
+                        reg_fence32(y);
+                        if (c < 3) tmem_ld32_async(ts + 32 * (c + 1), x[(c + 1) & 1]);
+                        top = fmaxf(top, max32(y));
                     }
-                } else if (MODE != MODE_PLAIN) {
-                    const float d0 = (float)(k0 - spos);
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_wait_ld();
+                        reg_fence32(x[0]);
+                        uint32_t(&y)[32] = x[0];
+                        const int kc = k0 + 32 * c;
+                        if (MODE == MODE_BIAS && linear) {
+                            const float b0 = slope * (float)(kc - spos);
+                            const uint64_t rate2 = pair2(rate, rate);
 #pragma unroll
-                    for (int i = 0; i < ROWS_KEYS; ++i)
-                        x[i] = __float_as_uint(mod_score(__uint_as_float(x[i]), a.scale, MODE == MODE_CAP ? a.cap : 0.f,
-                                                         cap_rate, slope, d0 + (float)i));
+                            for (int i = 0; i < 32; i += 2) {
+                                float v0, v1;
+                                unpair2(fma2(pair2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), rate2,
+                                             pair2(fmaf(slope, (float)i, b0), fmaf(slope, (float)(i + 1), b0))), v0, v1);
+                                y[i] = __float_as_uint(v0);
+                                y[i + 1] = __float_as_uint(v1);
+                            }
+                        } else if (MODE != MODE_PLAIN) {
+                            const float d0 = (float)(kc - spos);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                y[i] = __float_as_uint(mod_score(__uint_as_float(y[i]), a.scale,
+                                                                 MODE == MODE_CAP ? a.cap : 0.f, cap_rate, slope,
+                                                                 d0 + (float)i));
+                        }
+                        if (!open) {
+                            const int c0 = lo - kc, c1 = hi - kc;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i < c0 || i >= c1) y[i] = __float_as_uint(-INFINITY);
+                        }
+                        tmem_st32(ts + 32 * c, y);
+                        top = fmaxf(top, max32(y));
+                        tmem_wait_st();
+                        if (c < 3) tmem_ld32_async(ts + 32 * (c + 1), x[0]);
+                    }
                 }
-                if (!__all_sync(0xffffffffu, lo <= k0 && hi >= k0 + ROWS_KEYS)) {
-                    const int c0 = lo - k0, c1 = hi - k0;
-#pragma unroll
-                    for (int i = 0; i < ROWS_KEYS; ++i)
-                        if (i < c0 || i >= c1) x[i] = __float_as_uint(-INFINITY);
-                }
-                float mx[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) mx[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 4]));
-#pragma unroll
-                for (int i = 8; i < ROWS_KEYS; i += 8)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mx[k] = max3(mx[k], __uint_as_float(x[i + k]), __uint_as_float(x[i + 4 + k]));
-                float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
                 if (MODE == MODE_PLAIN) top *= rate;
+                tmem_ld32_async(ts, x[0]);
                 if (count == 0) {
                     m = top;
                 } else if (__any_sync(0xffffffffu, top > m + RW_LAG)) {
@@ -968,26 +1000,34 @@ struct Softmax {
                         tmem_st_rows<16>(to + S * D + i, o);
                     }
                 }
+                // second pass: the weights, over the first half of the scores' columns
                 const float mu = m == -INFINITY ? 0.f : m;
                 const uint64_t nmu = pair2(-mu, -mu), rate2 = pair2(rate, rate);
                 uint64_t s0 = pair2(0.f, 0.f), s1 = s0;
 #pragma unroll
-                for (int i = 0; i < ROWS_KEYS; i += 4) {
-                    uint64_t v0 = pair2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-                    uint64_t v1 = pair2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
-                    if (MODE == MODE_PLAIN) { v0 = fma2(v0, rate2, nmu); v1 = fma2(v1, rate2, nmu); }
-                    else { v0 = add2(v0, nmu); v1 = add2(v1, nmu); }
-                    float p0, p1, p2, p3;
-                    unpair2(v0, p0, p1);
-                    unpair2(v1, p2, p3);
-                    p0 = ex2(p0); p1 = ex2(p1); p2 = ex2(p2); p3 = ex2(p3);
-                    s0 = add2(s0, pair2(p0, p1));
-                    s1 = add2(s1, pair2(p2, p3));
-                    x[i / 2] = pack_bf16x2(p0, p1);
-                    x[i / 2 + 1] = pack_bf16x2(p2, p3);
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t(&y)[32] = x[c & 1];
+                    tmem_wait_ld();
+                    reg_fence32(y);
+                    if (c < 3) tmem_ld32_async(ts + 32 * (c + 1), x[(c + 1) & 1]);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        uint64_t v0 = pair2(__uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+                        uint64_t v1 = pair2(__uint_as_float(y[i + 2]), __uint_as_float(y[i + 3]));
+                        if (MODE == MODE_PLAIN) { v0 = fma2(v0, rate2, nmu); v1 = fma2(v1, rate2, nmu); }
+                        else { v0 = add2(v0, nmu); v1 = add2(v1, nmu); }
+                        float p0, p1, p2, p3;
+                        unpair2(v0, p0, p1);
+                        unpair2(v1, p2, p3);
+                        p0 = ex2(p0); p1 = ex2(p1); p2 = ex2(p2); p3 = ex2(p3);
+                        s0 = add2(s0, pair2(p0, p1));
+                        s1 = add2(s1, pair2(p2, p3));
+                        w[i / 2] = pack_bf16x2(p0, p1);
+                        w[i / 2 + 1] = pack_bf16x2(p2, p3);
+                    }
+                    tmem_st_rows<16>(ts + 16 * c, w);
                 }
-                tmem_st32(ts, x);
-                tmem_st32(ts + 32, x + 32);
                 float p0, p1;
                 unpair2(add2(s0, s1), p0, p1);
                 l += p0 + p1;
@@ -999,7 +1039,7 @@ struct Softmax {
         }
 
         // ---- the run's end ----
-        constexpr int O = S ^ 1;
+        const int O = S ^ 1;
         if (!pair && S != start) {                       // hand over to the other stream
             if (count > 0) {
                 if (!rwait(bars.mlfree + 8 * S, (nml & 1u) ^ 1u, misc, a)) return false;
@@ -1124,7 +1164,6 @@ struct Softmax {
     }
 
     // The four warps of this stream meet (bounded).
-    template <int S>
     __device__ __forceinline__ bool meet()
     {
         __syncwarp();
@@ -1139,10 +1178,11 @@ struct Softmax {
     // the weights go to shared memory as the K-major operand P^T, and O^T has d on its lanes. The rows'
     // frames are the same in all threads: the warps meet once a tile to see whether a score is beyond its
     // row's frame by more than the lag, and exchange maxima only then.
-    template <int S, int NR>
+    template <int NR>
     __device__ __forceinline__ bool narrow(const Run& run)
     {
-        constexpr int O = S ^ 1;
+        constexpr int CH = NR < 16 ? NR : 16;
+        const int O = S ^ 1;
         const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
         const uint32_t lane_base = (uint32_t)(32 * w) << 16;
         const uint32_t ts = tmem + lane_base + S * TM_S, to = tmem + lane_base + 2 * TM_S;
@@ -1177,49 +1217,62 @@ struct Softmax {
         for (int t = run.t0 + (S ^ start); t < run.t1; t += 2, ++ntile, ++count) {
             if (!rwait(bars.sfull + 8 * S, ntile & 1u, misc, a)) return false;
             tc_fence_after();
-            uint32_t x[NR];
-            tmem_ld_rows<NR>(ts, x);
-            tmem_wait_ld();
-            reg_fence<NR>(x);
             const int k0 = t * ROWS_KEYS, key = k0 + 32 * w + lane;
-            float v[NR];
+            const bool open = all_lo <= k0 && all_hi >= k0 + ROWS_KEYS;
+            // v of CH rows from row c on. Sixteen rows at most are held at a time: with 32 their scores are
+            // read from tensor memory again for each step.
+            auto load = [&](int c, float (&v)[CH]) {
+                uint32_t x[CH];
+                tmem_ld_rows<CH>(ts + c, x);
+                tmem_wait_ld();
+                reg_fence<CH>(x);
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                if (MODE == MODE_PLAIN) {
-                    v[r] = __uint_as_float(x[r]) * rate;
-                } else {
-                    const float slope = __shfl_sync(0xffffffffu, slope_l, r);
-                    const int spos = __shfl_sync(0xffffffffu, spos_l, r);
-                    v[r] = mod_score(__uint_as_float(x[r]), a.scale, MODE == MODE_CAP ? a.cap : 0.f, cap_rate, slope,
-                                     (float)(key - spos));
+                for (int i = 0; i < CH; ++i) {
+                    if (MODE == MODE_PLAIN) {
+                        v[i] = __uint_as_float(x[i]) * rate;
+                    } else {
+                        const float slope = __shfl_sync(0xffffffffu, slope_l, c + i);
+                        const int spos = __shfl_sync(0xffffffffu, spos_l, c + i);
+                        v[i] = mod_score(__uint_as_float(x[i]), a.scale, MODE == MODE_CAP ? a.cap : 0.f, cap_rate, slope,
+                                         (float)(key - spos));
+                    }
+                    if (c + i >= R) v[i] = -INFINITY;
                 }
-                if (r >= R) v[r] = -INFINITY;
-            }
-            if (!(all_lo <= k0 && all_hi >= k0 + ROWS_KEYS)) {
+                if (!open) {
 #pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    const int rlo = __shfl_sync(0xffffffffu, lo, r), rhi = __shfl_sync(0xffffffffu, hi, r);
-                    if (key < rlo || key >= rhi) v[r] = -INFINITY;
+                    for (int i = 0; i < CH; ++i) {
+                        const int rlo = __shfl_sync(0xffffffffu, lo, c + i), rhi = __shfl_sync(0xffffffffu, hi, c + i);
+                        if (key < rlo || key >= rhi) v[i] = -INFINITY;
+                    }
                 }
-            }
+            };
+            float v[CH];
             bool beyond = false;
 #pragma unroll
-            for (int r = 0; r < NR; ++r) beyond = beyond || v[r] > fr[r] + RW_LAG;
+            for (int c = 0; c < NR; c += CH) {
+                load(c, v);
+#pragma unroll
+                for (int i = 0; i < CH; ++i) beyond = beyond || v[i] > fr[c + i] + RW_LAG;
+            }
             beyond = __any_sync(0xffffffffu, beyond);
             const uint32_t par = nvote & 1u;
             if (lane == 0) sh.flag[S][par][w] = beyond;
-            if (!meet<S>()) return false;
+            if (!meet()) return false;
             if (sh.flag[S][par][0] | sh.flag[S][par][1] | sh.flag[S][par][2] | sh.flag[S][par][3]) {
                 float mine_max = -INFINITY;
 #pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    float x = v[r];
+                for (int c = 0; c < NR; c += CH) {
+                    if (CH < NR) load(c, v);
 #pragma unroll
-                    for (int k = 16; k > 0; k >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
-                    if (lane == r) mine_max = x;
+                    for (int i = 0; i < CH; ++i) {
+                        float x = v[i];
+#pragma unroll
+                        for (int k = 16; k > 0; k >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
+                        if (lane == c + i) mine_max = x;
+                    }
                 }
                 if (lane < NR) sh.wmax[S][w][lane] = mine_max;
-                if (!meet<S>()) return false;
+                if (!meet()) return false;
 #pragma unroll
                 for (int c = 0; c < NR; c += 8) {
                     uint32_t o[8];
@@ -1243,10 +1296,15 @@ struct Softmax {
                 tmem_wait_st();
             }
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                const float p = ex2(v[r] - (fr[r] == -INFINITY ? 0.f : fr[r]));
-                l[r] += p;
-                *reinterpret_cast<__nv_bfloat16*>(prow + r * 128 + (pcol ^ ((r & 7) << 4))) = __float2bfloat16_rn(p);
+            for (int c = 0; c < NR; c += CH) {
+                if (CH < NR) load(c, v);
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                    const int r = c + i;
+                    const float p = ex2(v[i] - (fr[r] == -INFINITY ? 0.f : fr[r]));
+                    l[r] += p;
+                    *reinterpret_cast<__nv_bfloat16*>(prow + r * 128 + (pcol ^ ((r & 7) << 4))) = __float2bfloat16_rn(p);
+                }
             }
             fence_proxy_async_smem();
             tc_fence_before();
@@ -1366,7 +1424,7 @@ struct Softmax {
         ++nacc;
         if (other) { ++nacc_o; ++nml_o; }
         // the run's Q slot, weights and shared words are free
-        if (!meet<S>()) return false;
+        if (!meet()) return false;
         if (w == 0 && lane == 0) mbar_arrive(bars.qempty + 8 * (nq & 1u));
         return true;
     }
@@ -1433,25 +1491,21 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
     const uint32_t tmem = *tslot;
     grid_dependency_wait();
     grid_launch_dependents();
-    if (warp >= RW_MMA_WARP) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RW_HELP_REGS));
-        if (warp == RW_LOAD_WARP) {
-            RowsLoader<D> ld{a, lay, bars, sm, sbase, misc};
-            if (!ld.run(&tq, &tqn, &tk, &tv, &tpk, &tpv)) ld.settle();
-            if (ld.bad) rows_error(a, ld.bad);
-        } else if (warp == RW_MMA_WARP) {
-            RowsMma<D> mma{a, lay, bars, sbase, tmem, misc};
-            mma.run(sm);
-            // every MMA issued has landed before the tensor memory and the stages go
-            if (lane == 0) umma_commit(bars.drain);
-            __syncwarp();
-            if (!mbar_wait(bars.drain, 0u) && lane == 0) rows_error(a, FDPP_ERRBIT_TIMEOUT);
-            __syncwarp();
-        }
+    if (warp == RW_LOAD_WARP) {
+        RowsLoader<D> ld{a, lay, bars, sm, sbase, misc};
+        if (!ld.run(&tq, &tqn, &tk, &tv, &tpk, &tpv)) ld.settle();
+        if (ld.bad) rows_error(a, ld.bad);
+    } else if (warp == RW_MMA_WARP) {
+        RowsMma<D> mma{a, lay, bars, sbase, tmem, misc};
+        mma.run(sm);
+        // every MMA issued has landed before the tensor memory and the stages go
+        if (lane == 0) umma_commit(bars.drain);
+        __syncwarp();
+        if (!mbar_wait(bars.drain, 0u) && lane == 0) rows_error(a, FDPP_ERRBIT_TIMEOUT);
+        __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(RW_SOFT_REGS));
-        Softmax<D, MODE> sx{a, lay, bars, sm, sbase, tmem, misc};
-        if (warp < 4) sx.template run<0>(); else sx.template run<1>();
+        Softmax<D, MODE> sx{a, lay, bars, sm, tmem, misc, warp >> 2};
+        sx.run();
         tc_fence_before();
     }
     __syncthreads();
