@@ -75,7 +75,7 @@ fdpp_status check_params(const fdpp_rows_params* p)
     const long long keys = (long long)p->max_seq_len + p->max_prefix_len;
     const int G = p->num_q_heads / p->num_kv_heads, tpt = ROWS_TILE / G;
     const long long rt = p->batch + 2ll * ((p->num_tokens + 2ll * tpt - 1) / (2 * tpt)) + 1;
-    if (keys > (1ll << 30) || rt * p->num_kv_heads > (1ll << 31) / (keys / ROWS_KEYS + 2) ||
+    if (keys > (1ll << 30) || rt * p->num_kv_heads > (1ll << 31) / (keys / ROWS_KEYS + 8) ||
         (long long)p->num_tokens * p->num_q_heads >= (1ll << 31) / 2 || simt_units(*p) >= (1ll << 31) - 1)
         return rfail(FDPP_ERR_INVALID_ARG, "problem too large for one call");
     return FDPP_OK;
@@ -222,7 +222,7 @@ fdpp_status attend(const void* q, const void* prefix_k, const void* prefix_v, co
     }
     a.parts = std::min(sms, ROWS_MAX_PARTS);
     a.stages = rows_tc_stages(a.D, std::min(smem_blk, smem_sm - 1024));
-    if (a.stages < 3) return rfail(FDPP_ERR_UNSUPPORTED, "too little shared memory for the tensor kernel");
+    if (a.stages < 4) return rfail(FDPP_ERR_UNSUPPORTED, "too little shared memory for the tensor kernel");
     const int box = paged ? std::min(p->block_size, ROWS_KEYS) : ROWS_KEYS;
     const long long rows = paged ? p->block_size : p->max_seq_len, outer = paged ? p->num_kv_blocks : p->batch;
     RowsMaps m;
@@ -252,7 +252,7 @@ RowsLayout rows_layout(const fdpp_rows_params& p)
     const int G = p.num_q_heads / p.num_kv_heads, pair = 2 * (ROWS_TILE / G);
     w.counters = ROWS_OFF_COUNTERS;
     w.plan = ROWS_OFF_PLAN;
-    size_t off = align256(w.plan + RP_WORDS * 4);
+    size_t off = align256(w.plan + (RP_WORDS + ROWS_MAX_PARTS) * 4);
     if (!tensor_kernel(p)) {
         const size_t splits = (size_t)simt_splits(p), rows = splits > 1 ? T * Hq * splits : 0;
         w.tok = w.seq_rt = w.rec = w.slot_o = w.slot_ml = off;

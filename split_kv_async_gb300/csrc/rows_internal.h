@@ -50,7 +50,7 @@ struct RowsLayout {
 constexpr size_t ROWS_OFF_COUNTERS = 256;
 constexpr size_t ROWS_OFF_PLAN = ROWS_OFF_COUNTERS + ROWS_COUNTERS * 4;
 
-// Plan header words.
+// Plan header words, then the first row tile of each part.
 enum { RP_NRT = 0, RP_NPRE = 1, RP_TILES = 2, RP_PREFIX = 3, RP_ROWS = 4, RP_WORDS = 16 };
 
 struct RowsArgs {

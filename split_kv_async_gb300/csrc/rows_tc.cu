@@ -6,19 +6,24 @@
 // more than 2^8 since it was set (until then the weights stay below 2^8, and the sums are exact in
 // the same frame), so that the accumulator is hardly ever rescaled.
 //
-// How. One CTA per SM, ten warps, two streams:
-//   warp 9   loads: walks this CTA's part of the key tiles (128 keys each), writes a header for each run
+// How. One CTA per SM, eleven warps, two streams:
+//   warp 10  loads: walks this CTA's part of the key tiles (128 keys each), writes a header for each run
 //            (the part's share of one unit = (row tile, kv head)), brings Q by one 3-D TMA load per 64
 //            of d and the K and V tiles into a ring of stages (128-byte swizzle).
-//   warp 8   issues the MMAs of both streams (one thread): S = Q K^T (M = 128 rows, N = 128 keys), and
-//            O += P V with P from tensor memory and V MN-major from the TMA-landed tile. A stream's P V
-//            of one tile is issued right before its next Q K^T, so while one stream's softmax runs the
-//            tensor cores work on the other's tile.
+//   warps 8, 9  issue the MMAs of streams 0 and 1 (one thread each): S = Q K^T (M = 128 rows, N = 128
+//            keys), and O += P V with P from tensor memory and V MN-major from the TMA-landed tile. A
+//            stream's P V of one tile is issued right before its next Q K^T, and while one stream's
+//            softmax runs the tensor cores work on the other's tile.
 //   warps 0-3, 4-7   the softmax of streams 0 and 1: a thread owns a row (tensor-memory lane), reads its
 //            128 scores, and writes P as bf16 over them. P's rounding (2^-9 of each weight, independent)
-//            leaves an error of the order of the output's own rounding; l sums the unrounded weights.
+//            leaves an error of the order of the output's own rounding; l sums the unrounded weights. A
+//            tile is computed in the frame that the row had before it; only when a score is beyond the
+//            frame by more than the lag is the frame moved and the tile computed again.
 // With more than 128 rows a unit is a pair: two row tiles, one per stream, share every K/V tile. With
 // fewer, both streams take the same rows, alternate key tiles and are joined at the run's end.
+//
+// Few rows (32 at most): the same with the operands exchanged, the keys on the tensor-memory lanes. A
+// row per lane would leave one warp of four with all the work; a key per lane shares it evenly.
 //
 // What bounds it. Many rows: the tensor pipe (4 x 128 keys x 128 rows x d FLOP per row tile and key tile)
 // with the softmax's 128 x 128 exponentials on the MUFU units beside it. Few rows: HBM (K and V of a kv
@@ -39,15 +44,17 @@
 // MMAs land, frees its tensor memory and exits.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "rows_common.cuh"
 #include "tcgen05.cuh"
 
 namespace fdpp {
 namespace {
 
-constexpr int RW_MMA_WARP = 8;
-constexpr int RW_LOAD_WARP = 9;
-constexpr int RW_THREADS = 10 * 32;
+constexpr int RW_MMA_WARP = 8;           // and the next: one per stream
+constexpr int RW_LOAD_WARP = 10;
+constexpr int RW_THREADS = 11 * 32;
 constexpr int RW_HDRS = 4;               // run headers in flight
 constexpr int RW_HDR_BYTES = 64;
 constexpr float RW_LAG = 8.f;            // log2 of the growth of a row's max that moves its frame
@@ -68,34 +75,45 @@ struct NarrowShared {
     int flag[2][2][4];                   // per stream, tile parity and warp: a score beyond its row's frame
 };
 
-// Shared memory. A key-major run keeps to the Q buffers: two slots of 32 query rows and the weights of
-// both streams ([32 rows][128 keys] bf16) in the first, NarrowShared in the second; the load warp lets
-// all runs of one kind end before it starts one of the other.
+// Shared memory. Each softmax warp has 4 kB through which it turns its accumulator rows into whole
+// 128-byte lines on their way out. A key-major run keeps to the Q buffers: two slots of 32 query rows and
+// the weights of both streams ([32 rows][128 keys] bf16) in the first, two slots more and NarrowShared in
+// the second; the load warp lets all runs of one kind end before it starts one of the other.
 template <int D>
 struct RowsSmem {
     static constexpr int QB = ROWS_TILE * D * 2;           // a row tile's Q
     static constexpr int SB = ROWS_KEYS * D * 2;           // a K or V tile
     static constexpr int HALF = ROWS_KEYS * 128;           // one 64-wide half of either
+    static constexpr int TURN = 32 * 128;                  // a warp's rows, 128 bytes of each
+    static constexpr int NSLOTS = 4;
     static constexpr int NQ = ROWS_NARROW * D * 2;         // a key-major run's Q
     static constexpr int NQ_HALF = ROWS_NARROW * 128;
     static constexpr int NP = ROWS_NARROW * ROWS_KEYS * 2; // its weights, per stream
-    static constexpr int NP_OFF = 2 * NQ, NSH_OFF = 2 * NQ + 2 * NP;
-    int q, stages, hdr, ml, bars, misc, tslot, total;
+    // d = 64: the weights fill the first buffer, the slots the second, and NarrowShared lies at the end
+    static constexpr int FIRST_SLOTS = (QB - 2 * NP) / NQ;
+    static constexpr int NP_OFF = QB - 2 * NP;
+    __host__ __device__ static constexpr int slot(int i) { return i < FIRST_SLOTS ? i * NQ : QB + (i - FIRST_SLOTS) * NQ; }
+    static constexpr int SLOTS_END = QB + (NSLOTS - FIRST_SLOTS) * NQ;
+    static constexpr bool NSH_IN_Q = SLOTS_END + (int)sizeof(NarrowShared) <= 2 * QB;
+    int q, stages, turn, hdr, ml, bars, misc, tslot, nsh, total;
     __host__ __device__ explicit RowsSmem(int nst)
-        : q(0), stages(2 * QB), hdr(stages + nst * SB), ml(hdr + RW_HDRS * RW_HDR_BYTES), bars(ml + 2 * ROWS_TILE * 8),
-          misc(bars + (2 * nst + 2 * 2 + 2 * RW_HDRS + 7 * 2 + 1) * 8), tslot(misc + 16), total(tslot + 16)
+        : q(0), stages(2 * QB), turn(stages + nst * SB), hdr(turn + 8 * TURN), ml(hdr + RW_HDRS * RW_HDR_BYTES),
+          bars(ml + 2 * ROWS_TILE * 8), misc(bars + (2 * nst + 2 * (2 + NSLOTS) + 2 * RW_HDRS + 6 * 2 + 1) * 8),
+          tslot(misc + 64), nsh(NSH_IN_Q ? SLOTS_END : tslot + 16),
+          total(tslot + 16 + (NSH_IN_Q ? 0 : (int)sizeof(NarrowShared)))
     {
-        static_assert(NSH_OFF + (int)sizeof(NarrowShared) <= 2 * QB, "a key-major run fits the Q buffers");
+        static_assert(QB >= 2 * NP && SLOTS_END <= 2 * QB, "a key-major run fits the Q buffers");
     }
 };
 
 struct RowsBars {
     uint32_t kvfull, kvempty;     // [stages]
     uint32_t qfull, qempty;       // [2]
-    uint32_t hfull, hempty;       // [RW_HDRS] run headers: read by the MMA warp and the eight softmax warps
+    uint32_t nqfull, nqempty;     // [4] the key-major runs' slots
+    uint32_t hfull, hempty;       // [RW_HDRS] run headers: read by the MMA warps and the eight softmax warps
     uint32_t sfull, pready;       // [2] scores written; weights written
     uint32_t ofull, ofree;        // [2] accumulator complete; read out
-    uint32_t mlready, mlfree;     // [2] a stream's maxima and sums for the joined epilogue
+    uint32_t mlfree;              // [2] a stream's maxima and sums have been read
     uint32_t vote;                // [2] the warps of a stream meet (key-major runs)
     uint32_t drain;
     __device__ __forceinline__ RowsBars(uint32_t base, int nst)
@@ -104,29 +122,37 @@ struct RowsBars {
         kvempty = kvfull + 8 * nst;
         qfull = kvempty + 8 * nst;
         qempty = qfull + 16;
-        hfull = qempty + 16;
+        nqfull = qempty + 16;
+        nqempty = nqfull + 32;
+        hfull = nqempty + 32;
         hempty = hfull + 8 * RW_HDRS;
         sfull = hempty + 8 * RW_HDRS;
         pready = sfull + 16;
         ofull = pready + 16;
         ofree = ofull + 16;
-        mlready = ofree + 16;
-        mlfree = mlready + 16;
+        mlfree = ofree + 16;
         vote = mlfree + 16;
         drain = vote + 16;
     }
 };
 
-// All lanes wait; a wait that runs out aborts the CTA (warp-uniform result).
-__device__ __forceinline__ bool rwait(uint32_t bar, uint32_t parity, volatile int* misc, const RowsArgs& a)
+// All lanes wait. A wait that is over when asked for costs two instructions; otherwise it is bounded, and
+// one that runs out aborts the CTA (warp-uniform result).
+__device__ __noinline__ bool rwait_slow(uint32_t bar, uint32_t parity, volatile int* misc, unsigned* err)
 {
-    bool ok = (misc[0] == 0) && mbar_wait(bar, parity & 1u);
+    bool ok = (misc[0] == 0) && mbar_wait(bar, parity);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok && (threadIdx.x & 31) == 0) {
         misc[0] = 1;
-        rows_error(a, FDPP_ERRBIT_TIMEOUT);
+        atomicOr(err, FDPP_ERRBIT_TIMEOUT);
     }
     return ok;
+}
+
+__device__ __forceinline__ bool rwait(uint32_t bar, uint32_t parity, volatile int* misc, const RowsArgs& a)
+{
+    if (__builtin_expect(__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u)), 1)) return true;
+    return rwait_slow(bar, parity & 1u, misc, a.err);
 }
 
 // Whether the phase of `parity` has completed (no waiting).
@@ -151,6 +177,11 @@ __device__ __forceinline__ int part_of(int x, int total, int parts)
 {
     return (int)((((long long)x + 1) * parts - 1) / total);
 }
+
+// A unit takes its key tiles and RW_GAP more in the order that is cut: the time of a run's beginning and
+// end, in key tiles, so that a part with many short runs holds fewer tiles.
+constexpr int RW_GAP = 2;
+__device__ __forceinline__ int unit_span(int nt) { return nt > 0 ? nt + RW_GAP : 0; }
 
 // The row tile whose units hold tile x (x < total): the last that starts at or before it.
 __device__ __forceinline__ int find_rt(const RowTileRec* rec, int n, int x)
@@ -218,25 +249,30 @@ __device__ __forceinline__ void set_tiles(RowTileRec& r, int loA, int hiA, int l
 __global__ void __launch_bounds__(PLAN_THREADS) rows_plan_kernel(RowsArgs a)
 {
     __shared__ long long red[32];
-    __shared__ int srt[PLAN_SMEM_SEQS + 1];
+    __shared__ int srt[PLAN_SMEM_SEQS + 1];              // first row tile of each sequence
+    __shared__ int sc0[PLAN_SMEM_SEQS], sn[PLAN_SMEM_SEQS], sl[PLAN_SMEM_SEQS];
+    __shared__ int sstart[PLAN_SMEM_SEQS];               // first tile of each row tile
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     grid_dependency_wait();
     grid_launch_dependents();
     unsigned bad = 0;
-    const int P = prefix_keys(a, bad);
+    const bool in_smem = a.B <= PLAN_SMEM_SEQS;
+    int* first_rt = in_smem ? srt : a.seq_rt;
     const int pair = 2 * a.tpt;
     int last = a.T;
     if (a.cu) last = clamp_len(a.cu[a.B], a.T);
+    const int P = prefix_keys(a, bad);
     // prefix row tiles first, over all rows up to the last sequence's end
     const int npre = P > 0 ? ceil_div_i(last, pair) : 0;
-    for (int t = threadIdx.x; t < a.T; t += blockDim.x) a.tok[t] = RowToken{0, 0, 0, -1};
-    const bool in_smem = a.B <= PLAN_SMEM_SEQS;
-    int* first_rt = in_smem ? srt : a.seq_rt;
     long long run = npre;
     for (int base = 0; base < a.B; base += blockDim.x) {
         const int b = base + threadIdx.x;
-        int c0 = 0, n = 0;
-        if (b < a.B) n = seq_rows(a, b, c0, bad);
+        int c0 = 0, n = 0, L = 0;
+        if (b < a.B) {
+            n = seq_rows(a, b, c0, bad);
+            L = own_len(a, b, bad);
+            if (in_smem) { sc0[b] = c0; sn[b] = n; sl[b] = L; }
+        }
         const long long mine = ceil_div_i(n, pair);
         long long total;
         const long long incl = plan_scan(mine, total, red);
@@ -247,43 +283,73 @@ __global__ void __launch_bounds__(PLAN_THREADS) rows_plan_kernel(RowsArgs a)
     if (run > a.max_rt) bad |= FDPP_ERRBIT_TOKENS;      // sequences whose rows overlap
     if (threadIdx.x == 0) first_rt[a.B] = nrt;
     __syncthreads();
-
-    // own row tiles: the tokens' positions and key ranges, and the tiles' key tiles
-    for (int rt = npre + warp; rt < nrt; rt += nw) {
-        int lo = 0, hi = a.B;                           // first_rt[lo] <= rt < first_rt[hi]
+    auto sequence = [&](int b, int& c0, int& n, int& L) {
+        if (in_smem) {
+            c0 = sc0[b]; n = sn[b]; L = sl[b];
+        } else {
+            unsigned again = 0;
+            n = seq_rows(a, b, c0, again);
+            L = own_len(a, b, again);
+        }
+    };
+    auto of_rt = [&](int rt) {                          // first_rt[b] <= rt < first_rt[b + 1]
+        int lo = 0, hi = a.B;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (first_rt[mid] <= rt) lo = mid; else hi = mid;
         }
-        const int b = lo;
-        int c0;
-        const int n = seq_rows(a, b, c0, bad), L = own_len(a, b, bad);
-        const int i0 = (rt - first_rt[b]) * pair, nt = min(pair, n - i0);
-        int loA = INT32_MAX, hiA = 0, loB = INT32_MAX, hiB = 0;
-        for (int i = lane; i < nt; i += 32) {
-            RowToken k;
-            const int row = c0 + i0 + i;
-            k.pos = P + L - n + i0 + i;
-            k.rt = rt;
-            row_keys(a, row, k.pos, P + L, k.lo, k.hi);
-            a.tok[row] = k;
-            const int x = max(k.lo - P, 0), y = k.hi - P;
-            if (y > x) {
-                if (i < a.tpt) { loA = min(loA, x); hiA = max(hiA, y); }
-                else { loB = min(loB, x); hiB = max(hiB, y); }
+        return lo;
+    };
+    // rows of no sequence
+    const int first_row = a.cu ? clamp_len(a.cu[0], a.T) : 0;
+    for (int t = threadIdx.x; t < a.T; t += blockDim.x)
+        if (t < first_row || t >= last) a.tok[t] = RowToken{0, 0, 0, -1};
+
+    // own row tiles: the tokens' positions and key ranges, and the tiles' key tiles
+    const bool arrays = a.key_begin || a.key_end;
+    const int per = !arrays && pair <= 8 ? 1 : (arrays || pair > 32 ? 32 : 8);      // lanes of a row tile
+    const int sub = threadIdx.x % per;
+    for (int rt0 = npre + (int)threadIdx.x / per; rt0 - (int)threadIdx.x / per < nrt; rt0 += blockDim.x / per) {
+        const bool on = rt0 < nrt;
+        const int rt = on ? rt0 : nrt - 1;
+        int loA = INT32_MAX, hiA = 0, loB = INT32_MAX, hiB = 0, c0 = 0, n = 0, L = 0, i0 = 0, nt = 0, b = 0;
+        if (on) {
+            b = of_rt(rt);
+            sequence(b, c0, n, L);
+            i0 = (rt - first_rt[b]) * pair;
+            nt = max(0, min(pair, n - i0));
+            for (int i = sub; i < nt; i += per) {
+                RowToken k;
+                const int row = c0 + i0 + i;
+                k.pos = P + L - n + i0 + i;
+                k.rt = rt;
+                row_keys(a, row, k.pos, P + L, k.lo, k.hi);
+                a.tok[row] = k;
+                const int x = max(k.lo - P, 0), y = k.hi - P;
+                if (y > x) {
+                    if (i < a.tpt) { loA = min(loA, x); hiA = max(hiA, y); }
+                    else { loB = min(loB, x); hiB = max(hiB, y); }
+                }
             }
         }
+        for (int o = per >> 1; o > 0; o >>= 1) {
+            loA = min(loA, __shfl_xor_sync(0xffffffffu, loA, o));
+            hiA = max(hiA, __shfl_xor_sync(0xffffffffu, hiA, o));
+            loB = min(loB, __shfl_xor_sync(0xffffffffu, loB, o));
+            hiB = max(hiB, __shfl_xor_sync(0xffffffffu, hiB, o));
+        }
+        if (!on) continue;
         RowTileRec r{};
         r.b = b;
         r.tok0 = c0 + i0;
         r.ntok = nt;
         r.len = L;
-        set_tiles(r, warp_min(loA), warp_max(hiA), warp_min(loB), warp_max(hiB));
-        if (lane == 0) a.rec[rt] = r;
+        set_tiles(r, loA, hiA, loB, hiB);
+        if (sub == 0) a.rec[rt] = r;
         if (r.nt == 0 && !a.prefix_len) {               // rows that see nothing, and no unit writes
             uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + (long long)r.tok0 * a.Hq * a.D);
             const long long words = (long long)nt * a.Hq * a.D / 2;
-            for (long long i = lane; i < words; i += 32) o[i] = 0u;
+            for (long long i = sub; i < words; i += per) o[i] = 0u;
         }
     }
     __syncthreads();
@@ -306,15 +372,31 @@ __global__ void __launch_bounds__(PLAN_THREADS) rows_plan_kernel(RowsArgs a)
         set_tiles(r, warp_min(loA), warp_max(hiA), warp_min(loB), warp_max(hiB));
         if (lane == 0) a.rec[rt] = r;
     }
-    __syncthreads();
+    if (npre) __syncthreads();
+    const bool starts_in_smem = nrt <= PLAN_SMEM_SEQS;
     long long tiles = 0;
     for (int base = 0; base < nrt; base += blockDim.x) {
         const int rt = base + threadIdx.x;
-        const long long mine = rt < nrt ? (long long)a.rec[rt].nt * a.Hkv : 0;
+        const long long mine = rt < nrt ? (long long)unit_span(a.rec[rt].nt) * a.Hkv : 0;
         long long total;
         const long long incl = plan_scan(mine, total, red);
-        if (rt < nrt) a.rec[rt].start = (int)(tiles + incl - mine);
+        if (rt < nrt) {
+            const int start = (int)(tiles + incl - mine);
+            a.rec[rt].start = start;
+            if (starts_in_smem) sstart[rt] = start;
+        }
         tiles += total;
+    }
+    __syncthreads();
+    // the row tile that each part begins in
+    for (int c = threadIdx.x; c < a.parts; c += blockDim.x) {
+        const int x = part_begin(c, (int)tiles, a.parts);
+        int lo = 0, hi = nrt;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if ((starts_in_smem ? sstart[mid] : a.rec[mid].start) <= x) lo = mid; else hi = mid;
+        }
+        a.plan[RP_WORDS + c] = lo;
     }
     if (threadIdx.x == 0) {
         a.plan[RP_NRT] = nrt;
@@ -336,7 +418,7 @@ struct RowsLoader {
     uint8_t* sm;
     uint32_t sbase;
     volatile int* misc;
-    uint32_t stage = 0, phase = 0, nq = 0, nh = 0;
+    uint32_t stage = 0, phase = 0, nq = 0, nqn = 0, nh = 0;      // Q buffers and key-major slots filled, headers
     unsigned bad = 0;
 
     // Block of key tile t that this lane answers for (-1: none): entry t's first block + lane.
@@ -391,29 +473,44 @@ struct RowsLoader {
             : "memory");
     }
 
-    // Query rows into the next Q buffer (or the next slot of the key-major runs).
-    __device__ __forceinline__ bool query(const CUtensorMap* map, int g, int tok0, bool narrow)
+    // Query rows into the next Q buffer, or the next slot of the key-major runs.
+    __device__ __forceinline__ bool query(const CUtensorMap* map, int g, int tok0)
     {
         const int lane = threadIdx.x & 31;
         const uint32_t qb = nq & 1u, bar = bars.qfull + 8 * qb;
         if (!rwait(bars.qempty + 8 * qb, ((nq >> 1) & 1u) ^ 1u, misc, a)) return false;
-        const int rows = (narrow ? a.tpn : a.tpt) * a.G;
-        const uint32_t dst = sbase + lay.q + qb * (narrow ? RowsSmem<D>::NQ : RowsSmem<D>::QB);
-        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(rows * 128 * (D / 64)));
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(a.tpt * a.G * 128 * (D / 64)));
         __syncwarp();
         if (lane < D / 64)
-            tma_load(dst + lane * (narrow ? RowsSmem<D>::NQ_HALF : RowsSmem<D>::HALF), map, lane * 64, g * a.G, tok0, bar);
+            tma_load(sbase + lay.q + qb * RowsSmem<D>::QB + lane * RowsSmem<D>::HALF, map, lane * 64, g * a.G, tok0, bar);
         __syncwarp();
         ++nq;
         return true;
     }
+    __device__ __forceinline__ bool query_narrow(const CUtensorMap* map, int g, int tok0)
+    {
+        const int lane = threadIdx.x & 31;
+        const uint32_t i = nqn & 3u, bar = bars.nqfull + 8 * i;
+        if (!rwait(bars.nqempty + 8 * i, ((nqn >> 2) & 1u) ^ 1u, misc, a)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(a.tpn * a.G * 128 * (D / 64)));
+        __syncwarp();
+        if (lane < D / 64)
+            tma_load(sbase + lay.q + RowsSmem<D>::slot(i) + lane * RowsSmem<D>::NQ_HALF, map, lane * 64, g * a.G, tok0, bar);
+        __syncwarp();
+        ++nqn;
+        return true;
+    }
 
-    // Both Q buffers are back: the runs so far have left everything that the two kinds share.
+    // The runs so far have left everything that the two kinds of runs share.
     __device__ __forceinline__ bool settle_queries()
     {
         for (uint32_t k = 0; k < 2 && k < nq; ++k) {
             const uint32_t i = nq - 1 - k;
             if (!rwait(bars.qempty + 8 * (i & 1u), (i >> 1) & 1u, misc, a)) return false;
+        }
+        for (uint32_t k = 0; k < 4 && k < nqn; ++k) {
+            const uint32_t i = nqn - 1 - k;
+            if (!rwait(bars.nqempty + 8 * (i & 3u), (i >> 2) & 1u, misc, a)) return false;
         }
         return true;
     }
@@ -435,21 +532,26 @@ struct RowsLoader {
                                         const CUtensorMap* tv, const CUtensorMap* tpk, const CUtensorMap* tpv)
     {
         const int lane = threadIdx.x & 31;
-        const int total = a.plan[RP_TILES], nrt = a.plan[RP_NRT], P = a.plan[RP_PREFIX];
         const int c = blockIdx.x, parts = gridDim.x;
+        const int total = a.plan[RP_TILES], P = a.plan[RP_PREFIX];
+        int rt = a.plan[RP_WORDS + c];                   // the row tile that the part begins in
         int pos = part_begin(c, total, parts);
         const int end = part_begin(c + 1, total, parts);
-        int rt = pos < end ? find_rt(a.rec, nrt, pos) : 0;
         uint32_t toggle = 0;
         bool was_narrow = false;
-        while (pos < end) {
+        while (pos < end && rt < a.max_rt) {
             const RowTileRec r = a.rec[rt];
             const bool narrow = r.ntok <= a.tpn;
             if (narrow != was_narrow && !settle_queries()) return false;
             was_narrow = narrow;
-            const int past = r.start + r.nt * a.Hkv;
+            const int span = unit_span(r.nt), past = r.start + span * a.Hkv;
             while (pos < end && pos < past) {
-                const int g = (pos - r.start) / r.nt, ta = (pos - r.start) - g * r.nt, tb = min(r.nt, ta + end - pos);
+                const int g = (pos - r.start) / span, ta = (pos - r.start) - g * span, tb = min(r.nt, ta + end - pos);
+                const int next_pos = r.start + (g + 1) * span;
+                if (ta >= r.nt) {                        // between two units
+                    pos = next_pos;
+                    continue;
+                }
                 const int t0 = r.k0 + ta, t1 = r.k0 + tb;
                 const bool pair = r.ntok > a.tpt, whole = ta == 0 && tb == r.nt;
                 int* h = header();
@@ -474,15 +576,15 @@ struct RowsLoader {
                 publish();
                 if (!pair) toggle = (toggle + (uint32_t)(t1 - t0)) & 1u;
                 int ent = a.block_table ? entry(r, t0) : 0;
-                if (!query(narrow ? tqn : tq, g, r.tok0, narrow)) return false;
-                if (pair && !query(tq, g, r.tok0 + a.tpt, false)) return false;
+                if (narrow ? !query_narrow(tqn, g, r.tok0) : !query(tq, g, r.tok0)) return false;
+                if (pair && !query(tq, g, r.tok0 + a.tpt)) return false;
                 for (int t = t0; t < t1; ++t) {
                     const int next = a.block_table && t + 1 < t1 ? entry(r, t + 1) : 0;
                     if (!tile(r.b < 0 ? tpk : tk, r, g, t, ent)) return false;
                     if (!tile(r.b < 0 ? tpv : tv, r, g, t, ent)) return false;
                     ent = next;
                 }
-                pos += tb - ta;
+                pos = tb < r.nt ? end : next_pos;
             }
             ++rt;
         }
@@ -509,6 +611,12 @@ struct RowsLoader {
                 while (!mbar_try_wait(bars.qfull + 8 * (i & 1u), (i >> 1) & 1u) && global_ns() - t0 < 100000000ull) {
                 }
             }
+            for (uint32_t k = 0; k < 4 && k < nqn; ++k) {
+                const uint32_t i = nqn - 1 - k;
+                const uint64_t t0 = global_ns();
+                while (!mbar_try_wait(bars.nqfull + 8 * (i & 3u), (i >> 2) & 1u) && global_ns() - t0 < 100000000ull) {
+                }
+            }
         }
         __syncwarp();
     }
@@ -522,8 +630,8 @@ struct RowsLoader {
 // run takes 16 or 32).
 constexpr uint32_t TM_S = ROWS_KEYS;
 
-// Keeps a value in one place: its uses are computed from it where they are, not ahead of the loop.
-__device__ __forceinline__ void keep(uint64_t& x) { asm volatile("" : "+l"(x)); }
+// A value that is the same in all lanes, told to the compiler.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 __device__ __forceinline__ uint32_t narrow_cols(int rows) { return rows <= 16 ? 16u : 32u; }
 
@@ -534,187 +642,161 @@ struct RowsMma {
     const RowsBars& bars;
     uint32_t sbase, tmem;
     volatile int* misc;
-    // a stream's tile whose P V is still to be issued
-    struct Pending {
-        bool on = false, first = false, last = false, release = false;
-        uint32_t tile = 0, stage = 0, phase = 0, ncols = 0;     // ncols: of a key-major run, else 0
-    } p0, p1;
-    uint32_t np0 = 0, np1 = 0, nacc0 = 0, nacc1 = 0;            // P V issued, runs begun, per stream
+    uint32_t S;                                  // the stream
+    // the tile whose P V is still to be issued (ncols: of a key-major run, else 0)
+    bool owes = false, pfirst = false, plast = false;
+    uint32_t pstage = 0, pphase = 0, pcols = 0;
+    uint32_t np = 0, nacc = 0;                   // P V issued, runs begun
 
-    // Issues the P V that stream S owes, after one that the other stream owes from before it (of the
-    // same tile: stream 0's first): the joined epilogue waits for both accumulators, and a tile's last
-    // P V gives its stage back.
-    template <int S>
+    // Issues the P V that is owed.
     __device__ __forceinline__ bool flush()
     {
-        const Pending& o = S ? p0 : p1;
-        const Pending& p = S ? p1 : p0;
-        if (!p.on) return true;
-        if (o.on && (o.tile < p.tile || (o.tile == p.tile && S == 1)) && !issue<S ^ 1>()) return false;
-        return issue<S>();
-    }
-
-    template <int S>
-    __device__ __forceinline__ bool issue()
-    {
         constexpr uint32_t IDESC = umma_idesc_bf16(128, D, false) | (1u << 16);     // V: MN-major B
-        Pending& p = S ? p1 : p0;
-        uint32_t& np = S ? np1 : np0;
-        uint32_t& nacc = S ? nacc1 : nacc0;
-        if (!rwait(bars.pready + 8 * S, np & 1u, misc, a)) return false;
-        if (!rwait(bars.kvfull + 8 * p.stage, p.phase, misc, a)) return false;
-        if (p.first && !rwait(bars.ofree + 8 * S, (nacc & 1u) ^ 1u, misc, a)) return false;
-        tc_fence_after();
-        if ((threadIdx.x & 31) == 0) {
-            const uint32_t od = tmem + 2 * TM_S + S * D;
-            uint64_t vd = sw128_mnmajor_desc(sbase + lay.stages + p.stage * RowsSmem<D>::SB, RowsSmem<D>::HALF, 1024);
-            keep(vd);
-            if (p.ncols == 0) {
-                const uint32_t pd = tmem + S * TM_S;
-#pragma unroll
-                for (int k = 0; k < ROWS_KEYS / 16; ++k)
-                    umma_bf16_ta(od, pd + 8 * k, vd + k * (2048 >> 4), IDESC, (p.first && k == 0) ? 0u : 1u);
-            } else {
-                // O^T += V^T P^T: d on M, the rows on N, 64 keys per half of P^T
-                const uint32_t idesc = umma_idesc_bf16(D, 16, true) + ((p.ncols - 16) >> 3 << 17);
-                uint64_t pd = sw128_kmajor_desc(sbase + lay.q + RowsSmem<D>::NP_OFF + S * RowsSmem<D>::NP);
-                keep(pd);
-#pragma unroll
-                for (int k = 0; k < ROWS_KEYS / 16; ++k)
-                    umma_bf16(od, vd + k * (2048 >> 4), pd + (k >> 2) * (RowsSmem<D>::NQ_HALF >> 4) + (k & 3) * 2, idesc,
-                              (p.first && k == 0) ? 0u : 1u);
-            }
-            if (p.release) umma_commit(bars.kvempty + 8 * p.stage);
-            if (p.last) umma_commit(bars.ofull + 8 * S);
+        if (!owes) return true;
+        owes = false;
+        if (!rwait(bars.kvfull + 8 * pstage, pphase, misc, a)) return false;
+        if (pfirst) {
+            if (!rwait(bars.ofree + 8 * S, (nacc & 1u) ^ 1u, misc, a)) return false;
+            ++nacc;
         }
-        __syncwarp();
+        if (!rwait(bars.pready + 8 * S, np & 1u, misc, a)) return false;
         ++np;
-        if (p.first) ++nacc;
-        p.on = false;
+        tc_fence_after();
+        const bool lead = elect_one();
+        const uint32_t od = tmem + 2 * TM_S + S * D, more = pfirst ? 0u : 1u;
+        const uint32_t vd = sw128_mnmajor_lo(sbase + lay.stages + pstage * RowsSmem<D>::SB, RowsSmem<D>::HALF);
+        if (pcols == 0) {
+            const uint32_t pd = tmem + S * TM_S;
+#pragma unroll
+            for (int k = 0; k < ROWS_KEYS / 16; ++k)
+                umma_bf16_ta_lo(lead, od, pd + 8 * k, vd + k * (2048 >> 4), IDESC, k == 0 ? more : 1u);
+        } else {
+            // O^T += V^T P^T: d on M, the rows on N, 64 keys per half of P^T
+            const uint32_t idesc = umma_idesc_bf16(D, 16, true) + ((pcols - 16) >> 3 << 17);
+            const uint32_t pd = sw128_kmajor_lo(sbase + lay.q + RowsSmem<D>::NP_OFF + S * RowsSmem<D>::NP);
+#pragma unroll
+            for (int k = 0; k < ROWS_KEYS / 16; ++k)
+                umma_bf16_lo(lead, od, vd + k * (2048 >> 4), pd + (k >> 2) * (RowsSmem<D>::NQ_HALF >> 4) + (k & 3) * 2,
+                             idesc, k == 0 ? more : 1u);
+        }
+        umma_commit(lead, bars.kvempty + 8 * pstage);
+        if (plast) umma_commit(lead, bars.ofull + 8 * S);
+        __syncwarp();
         return true;
     }
 
-    // Waits for something the load warp brings. What the streams still owe goes first where it is not
-    // there yet: the load warp may itself be waiting for a run to end (its query slot, its stages).
+    // Waits for something the load warp brings. The P V that is owed goes first where it is not there yet:
+    // the load warp may itself be waiting for a run to end (its query slot, its stages).
     __device__ __forceinline__ bool await(uint32_t bar, uint32_t parity)
     {
-        if ((p0.on || p1.on) && !__all_sync(0xffffffffu, mbar_test(bar, parity)) && !(flush<0>() && flush<1>()))
-            return false;
+        if (owes && !__all_sync(0xffffffffu, mbar_test(bar, parity)) && !flush()) return false;
         return rwait(bar, parity, misc, a);
-    }
-
-    // Q K^T of one tile for stream S.
-    template <int S>
-    __device__ __forceinline__ void scores(uint32_t qb, uint32_t stage, uint32_t ncols, bool release, bool free_q)
-    {
-        constexpr uint32_t IDESC = umma_idesc_bf16(128, ROWS_KEYS, false);
-        if ((threadIdx.x & 31) == 0) {
-            uint64_t kd = sw128_kmajor_desc(sbase + lay.stages + stage * RowsSmem<D>::SB);
-            keep(kd);
-            if (ncols == 0) {
-                uint64_t qd = sw128_kmajor_desc(sbase + lay.q + qb * RowsSmem<D>::QB);
-                keep(qd);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (uint32_t)(k >> 2) * (RowsSmem<D>::HALF >> 4) + (uint32_t)(k & 3) * 2u;
-                    umma_bf16(tmem + S * TM_S, qd + off, kd + off, IDESC, k > 0 ? 1u : 0u);
-                }
-            } else {
-                // S^T = K Q^T: the keys on M, the rows on N
-                const uint32_t idesc = umma_idesc_bf16(128, 16, false) + ((ncols - 16) >> 3 << 17);
-                uint64_t qd = sw128_kmajor_desc(sbase + lay.q + qb * RowsSmem<D>::NQ);
-                keep(qd);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    umma_bf16(tmem + S * TM_S, kd + (uint32_t)(k >> 2) * (RowsSmem<D>::HALF >> 4) + (uint32_t)(k & 3) * 2u,
-                              qd + (uint32_t)(k >> 2) * (RowsSmem<D>::NQ_HALF >> 4) + (uint32_t)(k & 3) * 2u, idesc,
-                              k > 0 ? 1u : 0u);
-            }
-            umma_commit(bars.sfull + 8 * S);
-            if (release) umma_commit(bars.kvempty + 8 * stage);
-            if (free_q) umma_commit(bars.qempty + 8 * qb);
-        }
-        __syncwarp();
     }
 
     __device__ __forceinline__ bool run(uint8_t* sm)
     {
+        constexpr uint32_t IDESC = umma_idesc_bf16(128, ROWS_KEYS, false);
         const int lane = threadIdx.x & 31;
-        uint32_t stage = 0, phase = 0, nq = 0, nh = 0, tile = 0;
+        const uint32_t sd = tmem + S * TM_S;
+        uint32_t stage = 0, phase = 0, nq = 0, nqn = 0, nh = 0;
         for (;; ++nh) {
             const uint32_t hs = nh % RW_HDRS;
             if (!await(bars.hfull + 8 * hs, (nh / RW_HDRS) & 1u)) return false;
             const int* h = reinterpret_cast<const int*>(sm + lay.hdr + hs * RW_HDR_BYTES);
-            const int kind = h[RH_KIND], len = h[RH_LEN], t0 = h[RH_T0], t1 = h[RH_T1], flags = h[RH_FLAGS];
-            const int a0 = h[RH_A0], a1 = h[RH_A1], b0 = h[RH_B0], b1 = h[RH_B1];
-            const uint32_t ncols = (flags & RF_NARROW) ? narrow_cols(h[RH_NTOK] * a.G) : 0u;
+            const int kind = uniform(h[RH_KIND]), len = uniform(h[RH_LEN]), flags = uniform(h[RH_FLAGS]);
+            const int t0 = uniform(h[RH_T0]), t1 = uniform(h[RH_T1]);
+            const int s0 = uniform(S ? h[RH_B0] : h[RH_A0]), s1 = uniform(S ? h[RH_B1] : h[RH_A1]);
+            const uint32_t ncols = (flags & RF_NARROW) ? narrow_cols(uniform(h[RH_NTOK]) * a.G) : 0u;
             __syncwarp();
             if (lane == 0) mbar_arrive(bars.hempty + 8 * hs);
             if (kind == RUN_END) break;
             const bool pair = flags & RF_PAIR;
-            const int start = (flags & RF_START) ? 1 : 0;
-            const uint32_t qb0 = nq & 1u;
-            for (uint32_t k = 0; k < (pair ? 2u : 1u); ++k, ++nq)
-                if (!await(bars.qfull + 8 * (nq & 1u), (nq >> 1) & 1u)) return false;
-            bool begun0 = false, begun1 = false;
-            for (int t = t0; t < t1; ++t, ++tile) {
-                // a P V left behind by a stream that is not in turn holds a stage: issue it first
-                if (p0.on && p0.tile + 1 < tile && !flush<0>()) return false;
-                if (p1.on && p1.tile + 1 < tile && !flush<1>()) return false;
+            const uint32_t start = (flags & RF_START) ? 1u : 0u;
+            // this stream's tiles: all of a pair's from first to past, else every second one
+            const int first = pair ? s0 : t0 + (int)(S ^ start), past = pair ? s1 : t1;
+            const bool any = first < past;
+            const int last = any ? (pair ? past - 1 : past - 1 - ((past - 1 - first) & 1)) : -1;
+            // Q: of a pair, the buffer that is not this stream's goes back at once, as one without tiles does
+            uint32_t qd = 0, qbar = 0;
+            if (ncols) {
+                const uint32_t i = nqn & 3u;
+                if (!await(bars.nqfull + 8 * i, (nqn >> 2) & 1u)) return false;
+                qd = sw128_kmajor_lo(sbase + lay.q + RowsSmem<D>::slot(i));
+                ++nqn;
+            } else {
+                for (uint32_t k = 0; k < (pair ? 2u : 1u); ++k, ++nq) {
+                    const uint32_t qb = nq & 1u;
+                    if (!await(bars.qfull + 8 * qb, (nq >> 1) & 1u)) return false;
+                    if (any && (!pair || k == S)) {
+                        qd = sw128_kmajor_lo(sbase + lay.q + qb * RowsSmem<D>::QB);
+                        qbar = bars.qempty + 8 * qb;
+                    } else if (lane == 0) {
+                        mbar_arrive(bars.qempty + 8 * qb);
+                    }
+                }
+            }
+            for (int t = t0; t < t1; ++t) {
                 uint32_t vstage = stage + 1, vphase = phase;
                 if (vstage == (uint32_t)a.stages) { vstage = 0; vphase ^= 1u; }
-                const int turn = ((t - t0) + start) & 1;
-                const bool act0 = pair ? t >= a0 && t < a1 : turn == 0, act1 = pair ? t >= b0 && t < b1 : turn == 1;
-                const bool last0 = pair ? t + 1 == a1 : t + 2 >= t1, last1 = pair ? t + 1 == b1 : t + 2 >= t1;
-                if (!await(bars.kvfull + 8 * stage, phase)) return false;
-                const int nv = len - t * ROWS_KEYS;
-                if (nv < ROWS_KEYS || !(act0 || act1)) {
-                    if (!rwait(bars.kvfull + 8 * vstage, vphase, misc, a)) return false;
-                }
-                if (nv < ROWS_KEYS) {              // V past the source's end: zeros
-                    uint8_t* v = sm + lay.stages + vstage * RowsSmem<D>::SB;
-                    const int chunks = (ROWS_KEYS - nv) * 8;
-                    for (int i = lane; i < chunks * (D / 64); i += 32) {
-                        const int half = i / chunks, x = i - half * chunks;
-                        *reinterpret_cast<uint4*>(v + half * RowsSmem<D>::HALF + nv * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+                const bool mine = t >= first && t < past && (pair || (((uint32_t)(t - t0) ^ start ^ S) & 1u) == 0u);
+                if (mine) {
+                    if (!await(bars.kvfull + 8 * stage, phase)) return false;
+                    const int nv = len - t * ROWS_KEYS;
+                    if (nv < ROWS_KEYS) {          // V past the source's end: zeros
+                        if (!rwait(bars.kvfull + 8 * vstage, vphase, misc, a)) return false;
+                        uint8_t* v = sm + lay.stages + vstage * RowsSmem<D>::SB;
+                        const int chunks = (ROWS_KEYS - nv) * 8;
+                        for (int i = lane; i < chunks * (D / 64); i += 32) {
+                            const int half = i / chunks, x = i - half * chunks;
+                            *reinterpret_cast<uint4*>(v + half * RowsSmem<D>::HALF + nv * 128 + x * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
                     }
-                    fence_proxy_async_smem();
+                    if (!flush()) return false;
+                    tc_fence_after();
+                    const bool lead = elect_one();
+                    const uint32_t kd = sw128_kmajor_lo(sbase + lay.stages + stage * RowsSmem<D>::SB);
+                    if (ncols == 0) {
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t off = (uint32_t)(k >> 2) * (RowsSmem<D>::HALF >> 4) + (uint32_t)(k & 3) * 2u;
+                            umma_bf16_lo(lead, sd, qd + off, kd + off, IDESC, k > 0 ? 1u : 0u);
+                        }
+                    } else {
+                        // S^T = K Q^T: the keys on M, the rows on N
+                        const uint32_t idesc = umma_idesc_bf16(128, 16, false) + ((ncols - 16) >> 3 << 17);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            umma_bf16_lo(lead, sd, kd + (uint32_t)(k >> 2) * (RowsSmem<D>::HALF >> 4) + (uint32_t)(k & 3) * 2u,
+                                         qd + (uint32_t)(k >> 2) * (RowsSmem<D>::NQ_HALF >> 4) + (uint32_t)(k & 3) * 2u, idesc,
+                                         k > 0 ? 1u : 0u);
+                    }
+                    umma_commit(lead, bars.sfull + 8 * S);
+                    umma_commit(lead, bars.kvempty + 8 * stage);
+                    if (qbar && t == last) umma_commit(lead, qbar);
                     __syncwarp();
+                    owes = true;
+                    pfirst = t == first;
+                    plast = t == last;
+                    pstage = vstage;
+                    pphase = vphase;
+                    pcols = ncols;
+                } else {
+                    // a tile of the other stream (or of neither): given back as far as this one goes
+                    if (!flush()) return false;
+                    if (!rwait(bars.kvfull + 8 * stage, phase, misc, a)) return false;
+                    if (lane == 0) mbar_arrive(bars.kvempty + 8 * stage);
+                    if (!rwait(bars.kvfull + 8 * vstage, vphase, misc, a)) return false;
+                    if (lane == 0) mbar_arrive(bars.kvempty + 8 * vstage);
                 }
-                if (act0) {
-                    if (!flush<0>()) return false;
-                    tc_fence_after();
-                    // a row tile's Q is free after its last tile of the run
-                    scores<0>(qb0, stage, ncols, !act1, ncols == 0 && (pair ? last0 : t + 1 == t1));
-                    p0.on = true; p0.first = !begun0; p0.last = last0; p0.release = !act1;
-                    p0.tile = tile; p0.stage = vstage; p0.phase = vphase; p0.ncols = ncols;
-                    begun0 = true;
-                }
-                if (act1) {
-                    if (!flush<1>()) return false;
-                    tc_fence_after();
-                    scores<1>(pair ? qb0 ^ 1u : qb0, stage, ncols, true, ncols == 0 && (pair ? last1 : t + 1 == t1));
-                    p1.on = true; p1.first = !begun1; p1.last = last1; p1.release = true;
-                    p1.tile = tile; p1.stage = vstage; p1.phase = vphase; p1.ncols = ncols;
-                    begun1 = true;
-                }
-                if (!(act0 || act1) && lane == 0) {         // a tile that neither half sees
-                    mbar_arrive(bars.kvempty + 8 * stage);
-                    mbar_arrive(bars.kvempty + 8 * vstage);
-                }
-                __syncwarp();
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
                     if (++stage == (uint32_t)a.stages) { stage = 0; phase ^= 1u; }
             }
-            // a half without tiles in this run gives its Q back here
-            if (pair && lane == 0) {
-                if (a1 <= a0) mbar_arrive(bars.qempty + 8 * qb0);
-                if (b1 <= b0) mbar_arrive(bars.qempty + 8 * (qb0 ^ 1u));
-            }
-            __syncwarp();
         }
-        return flush<0>() && flush<1>();
+        return flush();
     }
 };
 
@@ -791,6 +873,12 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 {
     uint64_t d;
@@ -851,9 +939,9 @@ struct Softmax {
     uint32_t tmem;
     volatile int* misc;
     int S;                   // the stream
-    // phases passed: headers, this stream's tiles, runs of either stream's accumulator, hand-overs of
-    // either, meetings of this stream's warps, Q buffers
-    uint32_t nh = 0, ntile = 0, nacc = 0, nacc_o = 0, nml = 0, nml_o = 0, nvote = 0, nq = 0;
+    // phases passed: headers, this stream's tiles, runs of either stream's accumulator, its own
+    // hand-overs, meetings of this stream's warps, Q buffers
+    uint32_t nh = 0, ntile = 0, nacc = 0, nacc_o = 0, nml = 0, nvote = 0, nqn = 0;
 
     struct Run {
         int g, b, tok0, ntok, len, t0, t1, dest, flags, base, s0, s1;
@@ -884,7 +972,6 @@ struct Softmax {
             } else {
                 ok = wide(r);
             }
-            nq += (r.flags & RF_PAIR) ? 2u : 1u;
             if (!ok) break;
         }
         return ok;
@@ -926,111 +1013,120 @@ struct Softmax {
             tc_fence_after();
             if (warp_live) {
                 const int k0 = t * ROWS_KEYS;
-                // first pass: the tile's maximum. Scores that need more than the scale go back to tensor
-                // memory as v, masked ones as -inf.
                 const bool open = __all_sync(0xffffffffu, lo <= k0 && hi >= k0 + ROWS_KEYS);
-                float top = -INFINITY;
-                uint32_t x[2][32];
-                tmem_ld32_async(ts, x[0]);
-                if (MODE == MODE_PLAIN && open) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t(&y)[32] = x[c & 1];
-                        tmem_wait_ld();
-                        reg_fence32(y);
-                        if (c < 3) tmem_ld32_async(ts + 32 * (c + 1), x[(c + 1) & 1]);
-                        top = fmaxf(top, max32(y));
-                    }
-                } else {
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_wait_ld();
-                        reg_fence32(x[0]);
-                        uint32_t(&y)[32] = x[0];
-                        const int kc = k0 + 32 * c;
-                        if (MODE == MODE_BIAS && linear) {
-                            const float b0 = slope * (float)(kc - spos);
-                            const uint64_t rate2 = pair2(rate, rate);
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                float v0, v1;
-                                unpair2(fma2(pair2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), rate2,
-                                             pair2(fmaf(slope, (float)i, b0), fmaf(slope, (float)(i + 1), b0))), v0, v1);
-                                y[i] = __float_as_uint(v0);
-                                y[i + 1] = __float_as_uint(v1);
-                            }
-                        } else if (MODE != MODE_PLAIN) {
-                            const float d0 = (float)(kc - spos);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                y[i] = __float_as_uint(mod_score(__uint_as_float(y[i]), a.scale,
-                                                                 MODE == MODE_CAP ? a.cap : 0.f, cap_rate, slope,
-                                                                 d0 + (float)i));
-                        }
-                        if (!open) {
-                            const int c0 = lo - kc, c1 = hi - kc;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (i < c0 || i >= c1) y[i] = __float_as_uint(-INFINITY);
-                        }
-                        tmem_st32(ts + 32 * c, y);
-                        top = fmaxf(top, max32(y));
-                        tmem_wait_st();
-                        if (c < 3) tmem_ld32_async(ts + 32 * (c + 1), x[0]);
-                    }
-                }
-                if (MODE == MODE_PLAIN) top *= rate;
-                tmem_ld32_async(ts, x[0]);
-                if (count == 0) {
-                    m = top;
-                } else if (__any_sync(0xffffffffu, top > m + RW_LAG)) {
-                    // move the frame: the accumulator's P V of the tile before has completed (the
-                    // scores' barrier counts every MMA issued before them)
-                    const float f = fmaxf(m, top), w = m == f ? 1.f : ex2(m - f);
-                    m = f;
-                    l *= w;
-#pragma unroll 1
-                    for (int i = 0; i < D; i += 16) {
-                        uint32_t o[16];
-                        tmem_ld16_async(to + S * D + i, o);
-                        tmem_wait_ld();
-                        reg_fence16(o);
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * w);
-                        tmem_st_rows<16>(to + S * D + i, o);
-                    }
-                }
-                // second pass: the weights, over the first half of the scores' columns
-                const float mu = m == -INFINITY ? 0.f : m;
-                const uint64_t nmu = pair2(-mu, -mu), rate2 = pair2(rate, rate);
-                uint64_t s0 = pair2(0.f, 0.f), s1 = s0;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t(&y)[32] = x[c & 1];
+                // 32 scores as v
+                auto load = [&](int c, uint32_t (&y)[32]) {
+                    tmem_ld32_async(ts + 32 * c, y);
                     tmem_wait_ld();
                     reg_fence32(y);
-                    if (c < 3) tmem_ld32_async(ts + 32 * (c + 1), x[(c + 1) & 1]);
-                    uint32_t w[16];
+                    const int kc = k0 + 32 * c;
+                    if (MODE == MODE_BIAS && linear) {
+                        const float b0 = slope * (float)(kc - spos);
+                        const uint64_t rate2 = pair2(rate, rate);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        uint64_t v0 = pair2(__uint_as_float(y[i]), __uint_as_float(y[i + 1]));
-                        uint64_t v1 = pair2(__uint_as_float(y[i + 2]), __uint_as_float(y[i + 3]));
-                        if (MODE == MODE_PLAIN) { v0 = fma2(v0, rate2, nmu); v1 = fma2(v1, rate2, nmu); }
-                        else { v0 = add2(v0, nmu); v1 = add2(v1, nmu); }
-                        float p0, p1, p2, p3;
-                        unpair2(v0, p0, p1);
-                        unpair2(v1, p2, p3);
-                        p0 = ex2(p0); p1 = ex2(p1); p2 = ex2(p2); p3 = ex2(p3);
-                        s0 = add2(s0, pair2(p0, p1));
-                        s1 = add2(s1, pair2(p2, p3));
-                        w[i / 2] = pack_bf16x2(p0, p1);
-                        w[i / 2 + 1] = pack_bf16x2(p2, p3);
+                        for (int i = 0; i < 32; i += 2) {
+                            float v0, v1;
+                            unpair2(fma2(pair2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), rate2,
+                                         pair2(fmaf(slope, (float)i, b0), fmaf(slope, (float)(i + 1), b0))), v0, v1);
+                            y[i] = __float_as_uint(v0);
+                            y[i + 1] = __float_as_uint(v1);
+                        }
+                    } else if (MODE != MODE_PLAIN) {
+                        const float d0 = (float)(kc - spos);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            y[i] = __float_as_uint(mod_score(__uint_as_float(y[i]), a.scale, MODE == MODE_CAP ? a.cap : 0.f,
+                                                             cap_rate, slope, d0 + (float)i));
                     }
-                    tmem_st_rows<16>(ts + 16 * c, w);
+                    if (!open) {
+                        const int c0 = lo - kc, c1 = hi - kc;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i < c0 || i >= c1) y[i] = __float_as_uint(-INFINITY);
+                    }
+                };
+                auto tile_max = [&]() {
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t y[32];
+                        load(c, y);
+                        top = fmaxf(top, max32(y));
+                    }
+                    return MODE == MODE_PLAIN ? top * rate : top;
+                };
+                // The tile's weights in the frame m, their sum, and the largest v - m. EXACT: v is rounded
+                // before the frame is taken off, so that no v - m is above 0 in the frame of the largest v.
+                uint32_t w[64];
+                float sum;
+                auto weigh = [&](auto exact) {
+                    constexpr bool EXACT = decltype(exact)::value;
+                    const float mu = m == -INFINITY ? 0.f : m;
+                    const uint64_t nmu = pair2(-mu, -mu), rate2 = pair2(rate, rate);
+                    uint64_t s0 = pair2(0.f, 0.f), s1 = s0;
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t y[32];
+                        load(c, y);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            uint64_t v0 = pair2(__uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+                            uint64_t v1 = pair2(__uint_as_float(y[i + 2]), __uint_as_float(y[i + 3]));
+                            if (MODE != MODE_PLAIN) {
+                                v0 = add2(v0, nmu);
+                                v1 = add2(v1, nmu);
+                            } else if (EXACT) {
+                                v0 = add2(mul2(v0, rate2), nmu);
+                                v1 = add2(mul2(v1, rate2), nmu);
+                            } else {
+                                v0 = fma2(v0, rate2, nmu);
+                                v1 = fma2(v1, rate2, nmu);
+                            }
+                            float p0, p1, p2, p3;
+                            unpair2(v0, p0, p1);
+                            unpair2(v1, p2, p3);
+                            if (!EXACT) {
+                                top = max3(top, p0, p1);
+                                top = max3(top, p2, p3);
+                            }
+                            p0 = ex2(p0); p1 = ex2(p1); p2 = ex2(p2); p3 = ex2(p3);
+                            s0 = add2(s0, pair2(p0, p1));
+                            s1 = add2(s1, pair2(p2, p3));
+                            w[16 * c + i / 2] = pack_bf16x2(p0, p1);
+                            w[16 * c + i / 2 + 1] = pack_bf16x2(p2, p3);
+                        }
+                    }
+                    float p0, p1;
+                    unpair2(add2(s0, s1), p0, p1);
+                    sum = p0 + p1;
+                    return top;
+                };
+                if (count == 0) m = tile_max();          // a frame to begin with
+                const float top = weigh(std::false_type());
+                if (__any_sync(0xffffffffu, top > (m == -INFINITY ? -INFINITY : RW_LAG))) {
+                    // move the frame: the accumulator's P V of the tile before has completed (the scores'
+                    // barrier counts every MMA issued before them)
+                    const float f = fmaxf(m, tile_max()), wt = m == f ? 1.f : ex2(m - f);
+                    m = f;
+                    l *= wt;
+                    if (count > 0) {
+#pragma unroll 1
+                        for (int i = 0; i < D; i += 16) {
+                            uint32_t o[16];
+                            tmem_ld16_async(to + S * D + i, o);
+                            tmem_wait_ld();
+                            reg_fence16(o);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * wt);
+                            tmem_st_rows<16>(to + S * D + i, o);
+                        }
+                    }
+                    weigh(std::true_type());
                 }
-                float p0, p1;
-                unpair2(add2(s0, s1), p0, p1);
-                l += p0 + p1;
+                tmem_st32(ts, w);
+                tmem_st32(ts + 32, w + 32);
+                l += sum;
                 tmem_wait_st();
             }
             tc_fence_before();
@@ -1044,8 +1140,7 @@ struct Softmax {
             if (count > 0) {
                 if (!rwait(bars.mlfree + 8 * S, (nml & 1u) ^ 1u, misc, a)) return false;
                 ml[S * ROWS_TILE + r] = make_float2(m, l);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars.mlready + 8 * S);
+                tell();
                 ++nml;
                 ++nacc;
             }
@@ -1056,7 +1151,7 @@ struct Softmax {
         float wo = 0.f, ws = 1.f;                        // the streams' weights
         if (count > 0 && !rwait(bars.ofull + 8 * S, nacc & 1u, misc, a)) return false;
         if (other) {
-            if (!rwait(bars.mlready + 8 * O, nml_o & 1u, misc, a)) return false;
+            if (!told(O)) return false;
             const float2 x = ml[O * ROWS_TILE + r];
             __syncwarp();
             if (lane == 0) mbar_arrive(bars.mlfree + 8 * O);
@@ -1070,64 +1165,77 @@ struct Softmax {
         tc_fence_after();
         const int head = run.g * a.G + hh;
         const bool direct = run.dest == DEST_OUT;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((long long)tok * a.Hq + head) * D;
-        float* po = nullptr;
-        if (!direct && mine) {
-            long long at;
-            float2* pml;
-            if (run.dest == DEST_ROWS) {
-                at = ((run.b < 0 ? 0ll : (long long)a.T) + tok) * a.Hq + head;
-                po = a.row_o + at * D;
-                pml = a.row_ml + at;
-            } else {
-                at = (long long)run.dest * a.slot_rows + (tok - run.tok0) * a.G + hh;
-                po = a.slot_o + at * D;
-                pml = a.slot_ml + at;
-            }
-            *pml = make_float2(count > 0 ? m : -INFINITY, l);
+        // the row's place in out, in a slot or in the whole-unit arrays
+        long long at = -1;
+        if (mine) {
+            if (direct) at = (long long)tok * a.Hq + head;
+            else if (run.dest == DEST_ROWS) at = ((run.b < 0 ? 0ll : (long long)a.T) + tok) * a.Hq + head;
+            else at = (long long)run.dest * a.slot_rows + (tok - run.tok0) * a.G + hh;
+            if (!direct) (run.dest == DEST_ROWS ? a.row_ml : a.slot_ml)[at] = make_float2(count > 0 ? m : -INFINITY, l);
         }
+        float* pbase = run.dest == DEST_ROWS ? a.row_o : a.slot_o;
         bool fine = true;
         if (warp_live && (count > 0 || direct)) {
             const float inv = direct ? 1.f / l : 1.f;
+            // 128 bytes of every row at a time: turned through shared memory (16-byte pieces of row r at
+            // piece ^ (r & 7)), so that a store instruction writes four whole lines
+            uint8_t* turn = sm + lay.turn + (threadIdx.x >> 5) * RowsSmem<D>::TURN;
+            const int cols = direct ? 64 : 32;
+#pragma unroll 1
+            for (int i = 0; i < D; i += cols) {
+#pragma unroll 1
+                for (int c = 0; c < cols; c += 32) {
+                    uint32_t x[32];
 #pragma unroll
-            for (int i = 0; i < D; i += 32) {
-                uint32_t x[32];
+                    for (int k = 0; k < 32; ++k) x[k] = 0u;
+                    if (count > 0) {
+                        tmem_ld32_async(to + S * D + i + c, x);
+                        if (other) {
+                            uint32_t y[32];
+                            tmem_ld32_async(to + O * D + i + c, y);
+                            tmem_wait_ld();
+                            reg_fence32(x);
+                            reg_fence32(y);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) x[k] = 0u;
-                if (count > 0) {
-                    tmem_ld32_async(to + S * D + i, x);
-                    if (other) {
-                        uint32_t y[32];
-                        tmem_ld32_async(to + O * D + i, y);
-                        tmem_wait_ld();
-                        reg_fence32(x);
-                        reg_fence32(y);
+                            for (int k = 0; k < 32; ++k)
+                                x[k] = __float_as_uint(__uint_as_float(x[k]) * ws + __uint_as_float(y[k]) * wo);
+                        } else {
+                            tmem_wait_ld();
+                            reg_fence32(x);
+                        }
+                    }
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            x[k] = __float_as_uint(__uint_as_float(x[k]) * ws + __uint_as_float(y[k]) * wo);
+                    for (int k = 0; k < 32; ++k) fine = fine && fabsf(__uint_as_float(x[k])) < INFINITY;
+                    if (direct) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) {
+                            uint4 v = make_uint4(0, 0, 0, 0);
+                            if (!empty)
+                                v = make_uint4(pack_bf16x2(__uint_as_float(x[k]) * inv, __uint_as_float(x[k + 1]) * inv),
+                                               pack_bf16x2(__uint_as_float(x[k + 2]) * inv, __uint_as_float(x[k + 3]) * inv),
+                                               pack_bf16x2(__uint_as_float(x[k + 4]) * inv, __uint_as_float(x[k + 5]) * inv),
+                                               pack_bf16x2(__uint_as_float(x[k + 6]) * inv, __uint_as_float(x[k + 7]) * inv));
+                            *reinterpret_cast<uint4*>(turn + lane * 128 + ((((c + k) >> 3) ^ (lane & 7)) << 4)) = v;
+                        }
                     } else {
-                        tmem_wait_ld();
-                        reg_fence32(x);
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<uint4*>(turn + lane * 128 + (((k >> 2) ^ (lane & 7)) << 4)) =
+                                make_uint4(x[k], x[k + 1], x[k + 2], x[k + 3]);
                     }
                 }
+                __syncwarp();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) fine = fine && fabsf(__uint_as_float(x[k])) < INFINITY;
-                if (mine && direct) {
-#pragma unroll
-                    for (int k = 0; k < 32; k += 8) {
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (!empty)
-                            v = make_uint4(pack_bf16x2(__uint_as_float(x[k]) * inv, __uint_as_float(x[k + 1]) * inv),
-                                           pack_bf16x2(__uint_as_float(x[k + 2]) * inv, __uint_as_float(x[k + 3]) * inv),
-                                           pack_bf16x2(__uint_as_float(x[k + 4]) * inv, __uint_as_float(x[k + 5]) * inv),
-                                           pack_bf16x2(__uint_as_float(x[k + 6]) * inv, __uint_as_float(x[k + 7]) * inv));
-                        *reinterpret_cast<uint4*>(out + i + k) = v;
+                for (int k = 0; k < 32; k += 4) {
+                    const int row = k + (lane >> 3), piece = lane & 7;
+                    const long long rat = __shfl_sync(0xffffffffu, at, row);
+                    const uint4 v = *reinterpret_cast<const uint4*>(turn + row * 128 + ((piece ^ (row & 7)) << 4));
+                    if (rat >= 0) {
+                        if (direct) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + rat * D + i + 8 * piece) = v;
+                        else *reinterpret_cast<uint4*>(pbase + rat * D + i + 4 * piece) = v;
                     }
-                } else if (mine) {
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4)
-                        *reinterpret_cast<uint4*>(po + i + k) = make_uint4(x[k], x[k + 1], x[k + 2], x[k + 3]);
                 }
+                __syncwarp();
             }
         }
         tc_fence_before();
@@ -1147,19 +1255,51 @@ struct Softmax {
             const int jpos = __shfl_sync(0xffffffffu, tk.pos, j);
             const int jlo = max(__shfl_sync(0xffffffffu, lo, j), seen0), jhi = min(__shfl_sync(0xffffffffu, hi, j), seen1);
             const float jm = __shfl_sync(0xffffffffu, m, j), jl = __shfl_sync(0xffffffffu, l, j);
-            float* jpo = reinterpret_cast<float*>(__shfl_sync(0xffffffffu, (unsigned long long)po, j));
+            const long long jat = __shfl_sync(0xffffffffu, at, j);
             float o[D / 32];
             redo_row<D, D / 32>(a, run.b, run.g, jhead, jtok, jpos, jlo, jhi, base, jm == -INFINITY ? 0.f : jm, lane, o);
-            __nv_bfloat16* jout = static_cast<__nv_bfloat16*>(a.out) + ((long long)jtok * a.Hq + jhead) * D;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
-                if (direct) jout[lane + 32 * i] = __float2bfloat16_rn(o[i] / jl);
-                else jpo[lane + 32 * i] = o[i];
+                if (direct) static_cast<__nv_bfloat16*>(a.out)[jat * D + lane + 32 * i] = __float2bfloat16_rn(o[i] / jl);
+                else pbase[jat * D + lane + 32 * i] = o[i];
             }
         }
         if (count > 0) ++nacc;
-        if (other) ++nml_o;
         if (pair ? run.other_tiles : other) ++nacc_o;
+        return true;
+    }
+
+    // A stream's maxima and sums of run nh, for whichever stream joins the two. Neither stream waits for
+    // the other's runs in general, so either may be some runs ahead: a run number per warp, which a
+    // barrier's one bit of phase could not tell apart.
+    __device__ __forceinline__ void tell() const
+    {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) {
+            __threadfence_block();
+            misc[4 + (threadIdx.x >> 5)] = (int)nh + 1;
+        }
+        __syncwarp();
+    }
+    __device__ __forceinline__ bool told(int s) const
+    {
+        const int lane = threadIdx.x & 31;
+        const uint64_t t0 = global_ns();
+        for (uint32_t it = 1;; ++it) {
+            const int v = lane < 4 ? misc[4 + 4 * s + lane] : INT32_MAX;
+            if (__all_sync(0xffffffffu, v > (int)nh)) break;
+            if ((it & 63u) == 0) {
+                const bool late = misc[0] != 0 || global_ns() - t0 > FDPP_WAIT_NS;
+                if (__any_sync(0xffffffffu, late)) {
+                    if (lane == 0) {
+                        misc[0] = 1;
+                        rows_error(a, FDPP_ERRBIT_TIMEOUT);
+                    }
+                    return false;
+                }
+            }
+        }
+        __threadfence_block();
         return true;
     }
 
@@ -1186,7 +1326,7 @@ struct Softmax {
         const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
         const uint32_t lane_base = (uint32_t)(32 * w) << 16;
         const uint32_t ts = tmem + lane_base + S * TM_S, to = tmem + lane_base + 2 * TM_S;
-        volatile NarrowShared& sh = *reinterpret_cast<volatile NarrowShared*>(sm + lay.q + RowsSmem<D>::NSH_OFF);
+        volatile NarrowShared& sh = *reinterpret_cast<volatile NarrowShared*>(sm + lay.nsh);
         uint8_t* prow = sm + lay.q + RowsSmem<D>::NP_OFF + S * RowsSmem<D>::NP + (w >> 1) * RowsSmem<D>::NQ_HALF;
         const int pcol = ((w & 1) * 32 + lane) * 2;
         const int start = (run.flags & RF_START) ? 1 : 0, base = run.base, R = run.ntok * a.G;
@@ -1325,21 +1465,20 @@ struct Softmax {
                 sh.lsum[S][w][lane] = mine_l;
                 if (w == 0) sh.frame[S][lane] = mine_f;
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bars.mlready + 8 * S);
+            tell();
             ++nml;
         }
         const bool other = run.t1 - run.t0 > 1;          // both streams had tiles
         if (S != start) {
             if (count > 0) ++nacc;
             ++nacc_o;
-            ++nml_o;
+            ++nqn;
             return true;
         }
-        if (!rwait(bars.mlready + 8 * S, (nml - 1) & 1u, misc, a)) return false;
+        if (!told(S)) return false;
         if (!rwait(bars.ofull + 8 * S, nacc & 1u, misc, a)) return false;
         if (other) {
-            if (!rwait(bars.mlready + 8 * O, nml_o & 1u, misc, a)) return false;
+            if (!told(O)) return false;                  // (and so the accumulator's phase is this run's)
             if (!rwait(bars.ofull + 8 * O, nacc_o & 1u, misc, a)) return false;
         }
         tc_fence_after();
@@ -1422,10 +1561,11 @@ struct Softmax {
             }
         }
         ++nacc;
-        if (other) { ++nacc_o; ++nml_o; }
+        if (other) ++nacc_o;
         // the run's Q slot, weights and shared words are free
         if (!meet()) return false;
-        if (w == 0 && lane == 0) mbar_arrive(bars.qempty + 8 * (nq & 1u));
+        if (w == 0 && lane == 0) mbar_arrive(bars.nqempty + 8 * (nqn & 3u));
+        ++nqn;
         return true;
     }
 };
@@ -1444,7 +1584,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
     constexpr uint32_t NCOLS = 512;              // 2 x 128 of scores, 2 x D of sums
     const RowsSmem<D> lay(a.stages);
     const uint32_t sbase = smem_u32(sm);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     volatile int* misc = reinterpret_cast<volatile int*>(sm + lay.misc);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + lay.tslot);
     const RowsBars bars(sbase + lay.bars, a.stages);
@@ -1455,25 +1595,28 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; ++i) {
             mbar_init(bars.kvfull + 8 * i, 1);
-            mbar_init(bars.kvempty + 8 * i, 1);
+            mbar_init(bars.kvempty + 8 * i, 2);      // both streams
         }
         for (int i = 0; i < RW_HDRS; ++i) {
             mbar_init(bars.hfull + 8 * i, 1);
-            mbar_init(bars.hempty + 8 * i, 9);
+            mbar_init(bars.hempty + 8 * i, 10);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bars.qfull + 8 * i, 1);
-            mbar_init(bars.qempty + 8 * i, 1);
+            mbar_init(bars.qempty + 8 * i, 2);       // both streams
             mbar_init(bars.sfull + 8 * i, 1);
             mbar_init(bars.pready + 8 * i, 4);
             mbar_init(bars.ofull + 8 * i, 1);
             mbar_init(bars.ofree + 8 * i, 4);
-            mbar_init(bars.mlready + 8 * i, 4);
             mbar_init(bars.mlfree + 8 * i, 4);
             mbar_init(bars.vote + 8 * i, 4);
         }
-        mbar_init(bars.drain, 1);
-        misc[0] = 0;
+        for (int i = 0; i < RowsSmem<D>::NSLOTS; ++i) {
+            mbar_init(bars.nqfull + 8 * i, 1);
+            mbar_init(bars.nqempty + 8 * i, 1);
+        }
+        mbar_init(bars.drain, 2);
+        for (int i = 0; i < 16; ++i) misc[i] = 0;
         fence_mbar_init();
     }
     if (warp == RW_MMA_WARP) tmem_alloc(smem_u32(tslot), NCOLS);
@@ -1488,18 +1631,18 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tslot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
     grid_dependency_wait();
     grid_launch_dependents();
     if (warp == RW_LOAD_WARP) {
         RowsLoader<D> ld{a, lay, bars, sm, sbase, misc};
         if (!ld.run(&tq, &tqn, &tk, &tv, &tpk, &tpv)) ld.settle();
         if (ld.bad) rows_error(a, ld.bad);
-    } else if (warp == RW_MMA_WARP) {
-        RowsMma<D> mma{a, lay, bars, sbase, tmem, misc};
+    } else if (warp >= RW_MMA_WARP) {
+        RowsMma<D> mma{a, lay, bars, sbase, tmem, misc, (uint32_t)(warp - RW_MMA_WARP)};
         mma.run(sm);
         // every MMA issued has landed before the tensor memory and the stages go
-        if (lane == 0) umma_commit(bars.drain);
+        umma_commit(elect_one(), bars.drain);
         __syncwarp();
         if (!mbar_wait(bars.drain, 0u) && lane == 0) rows_error(a, FDPP_ERRBIT_TIMEOUT);
         __syncwarp();
@@ -1584,8 +1727,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) rows_join_cut_kernel(RowsArgs
     const int x = part_begin(c, total, a.parts);
     if (x <= 0 || x >= total) return;
     const RowTileRec r = a.rec[find_rt(a.rec, a.plan[RP_NRT], x)];
-    const int g = (x - r.start) / r.nt, start = r.start + g * r.nt;
-    if (x == start || part_begin(c - 1, total, a.parts) > start) return;
+    const int span = unit_span(r.nt), g = (x - r.start) / span, start = r.start + g * span;
+    if (x == start || x >= start + r.nt || part_begin(c - 1, total, a.parts) > start) return;
     const int rows = r.ntok * a.G, y0 = blockIdx.y * JOIN_ROWS;
     for (int row = y0 + (threadIdx.x >> 5); row < min(rows, y0 + JOIN_ROWS); row += JOIN_WARPS) {
         const int i = row / a.G, tok = r.tok0 + i;
@@ -1614,7 +1757,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) rows_join_prefix_kernel(RowsA
         if (src == 0 && npre == 0) continue;
         const RowTileRec r = a.rec[src ? tk.rt : tok / (2 * a.tpt)];
         if (r.nt == 0) continue;
-        const int start = r.start + g * r.nt, first = part_of(start, total, a.parts);
+        const int start = r.start + g * unit_span(r.nt), first = part_of(start, total, a.parts);
         if (part_of(start + r.nt - 1, total, a.parts) == first) {
             const long long at = ((long long)src * a.T + tok) * a.Hq + head;
             s.add(__ldcg(a.row_ml + at), a.row_o + at * D);

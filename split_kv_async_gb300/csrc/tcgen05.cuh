@@ -220,15 +220,67 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r)
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// As umma_bf16 with A in tensor memory: lane = row of A, two consecutive bf16 of k per 32-bit column.
-__device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+// True in one lane of the (converged) warp, the same one every time. A branch on it leaves the warp's
+// values uniform for the compiler, which a branch on a lane number does not: the issue of an MMA, whose
+// operands are uniform registers, then needs no moves from per-lane registers.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+// Descriptors in halves: the low word holds the address (and the leading byte offset), the high word the
+// stride byte offset of 1024, version 1 and the 128-byte swizzle. An operand's k-step adds to the low word.
+constexpr uint32_t SW128_DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t sw128_kmajor_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t sw128_mnmajor_lo(uint32_t saddr, uint32_t lbo)
+{
+    return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+
+// umma_bf16 with descriptors given by their low words, issued by the lane where `lead` is set: the whole
+// warp runs the code around it, so that no branch makes the operands look different from lane to lane.
+__device__ __forceinline__ void umma_bf16_lo(bool lead, uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc,
                                              uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "mov.b64 da, {%1, %5};\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(alo), "r"(blo), "r"(idesc), "r"(accumulate), "n"(SW128_DESC_HI), "r"((uint32_t)lead)
+        : "memory");
+}
+
+// The same with A in tensor memory: lane = row of A, two consecutive bf16 of k per 32-bit column.
+__device__ __forceinline__ void umma_bf16_ta_lo(bool lead, uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t idesc,
+                                                uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(blo), "r"(idesc), "r"(accumulate), "n"(SW128_DESC_HI), "r"((uint32_t)lead)
+        : "memory");
+}
+
+// umma_commit by the lane where `lead` is set.
+__device__ __forceinline__ void umma_commit(bool lead, uint32_t bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"((uint32_t)lead)
         : "memory");
 }
 
