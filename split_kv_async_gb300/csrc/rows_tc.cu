@@ -6,10 +6,13 @@
 // more than 2^8 since it was set (until then the weights stay below 2^8, and the sums are exact in
 // the same frame), so that the accumulator is hardly ever rescaled.
 //
-// How. One CTA per SM, eleven warps, two streams:
-//   warp 10  loads: walks this CTA's part of the key tiles (128 keys each), writes a header for each run
-//            (the part's share of one unit = (row tile, kv head)), brings Q by one 3-D TMA load per 64
-//            of d and the K and V tiles into a ring of stages (128-byte swizzle).
+// How. One CTA per SM, twelve warps, two streams:
+//   warps 10, 11  load: the first walks this CTA's part of the key tiles (128 keys each), writes a header
+//            for each run (the part's share of one unit = (row tile, kv head)) and brings Q, by one 3-D
+//            TMA load per 64 of d, and the K tiles; the second brings the V tiles, into the other stages
+//            of one ring (128-byte swizzle). Blocks of 16 tokens take 16 loads per tile and operand: with
+//            one warp for both, issuing them took longer than HBM takes for the tile (438 us against 344
+//            for the contiguous cache, 64 sequences of 512 to 16384 keys, 8 kv heads, d = 128).
 //   warps 8, 9  issue the MMAs of streams 0 and 1 (one thread each): S = Q K^T (M = 128 rows, N = 128
 //            keys), and O += P V with P from tensor memory and V MN-major from the TMA-landed tile. A
 //            stream's P V of one tile is issued right before its next Q K^T, and while one stream's
@@ -53,8 +56,8 @@ namespace fdpp {
 namespace {
 
 constexpr int RW_MMA_WARP = 8;           // and the next: one per stream
-constexpr int RW_LOAD_WARP = 10;
-constexpr int RW_THREADS = 11 * 32;
+constexpr int RW_LOAD_WARP = 10;         // and the next: K (with the headers and Q), and V
+constexpr int RW_THREADS = 12 * 32;
 constexpr int RW_HDRS = 4;               // run headers in flight
 constexpr int RW_HDR_BYTES = 64;
 constexpr float RW_LAG = 8.f;            // log2 of the growth of a row's max that moves its frame
@@ -110,7 +113,7 @@ struct RowsBars {
     uint32_t kvfull, kvempty;     // [stages]
     uint32_t qfull, qempty;       // [2]
     uint32_t nqfull, nqempty;     // [4] the key-major runs' slots
-    uint32_t hfull, hempty;       // [RW_HDRS] run headers: read by the MMA warps and the eight softmax warps
+    uint32_t hfull, hempty;       // [RW_HDRS] run headers: read by the V loader, the MMA and softmax warps
     uint32_t sfull, pready;       // [2] scores written; weights written
     uint32_t ofull, ofree;        // [2] accumulator complete; read out
     uint32_t mlfree;              // [2] a stream's maxima and sums have been read
@@ -422,17 +425,17 @@ struct RowsLoader {
     unsigned bad = 0;
 
     // Block of key tile t that this lane answers for (-1: none): entry t's first block + lane.
-    __device__ __forceinline__ int entry(const RowTileRec& r, int t)
+    __device__ __forceinline__ int entry(int b, int len, int t)
     {
         const int lane = threadIdx.x & 31;
-        const int bs = a.block_size, first = t * ROWS_KEYS / bs, nv = min(ROWS_KEYS, r.len - t * ROWS_KEYS);
+        const int bs = a.block_size, first = t * ROWS_KEYS / bs, nv = min(ROWS_KEYS, len - t * ROWS_KEYS);
         const int nb = bs >= ROWS_KEYS ? 1 : ceil_div_i(nv, bs);
         if (nv <= 0 || lane >= nb) return -1;
-        return r.b < 0 ? a.prefix_blocks[first + lane] : a.block_table[(long long)r.b * a.max_blocks + first + lane];
+        return b < 0 ? a.prefix_blocks[first + lane] : a.block_table[(long long)b * a.max_blocks + first + lane];
     }
 
     // One K or V tile into the next stage.
-    __device__ __forceinline__ bool tile(const CUtensorMap* map, const RowTileRec& r, int g, int t, int ent)
+    __device__ __forceinline__ bool tile(const CUtensorMap* map, int b, int len, int g, int t, int ent)
     {
         constexpr int HALVES = D / 64;
         const int lane = threadIdx.x & 31;
@@ -442,9 +445,9 @@ struct RowsLoader {
             if (lane == 0) mbar_arrive_expect_tx(bar, RowsSmem<D>::SB);
             __syncwarp();
             if (lane < HALVES)
-                tma_load(dst + lane * RowsSmem<D>::HALF, map, g * D + lane * 64, t * ROWS_KEYS, r.b < 0 ? 0 : r.b, bar);
+                tma_load(dst + lane * RowsSmem<D>::HALF, map, g * D + lane * 64, t * ROWS_KEYS, max(b, 0), bar);
         } else {
-            const int bs = a.block_size, box = min(bs, ROWS_KEYS), nv = min(ROWS_KEYS, r.len - t * ROWS_KEYS);
+            const int bs = a.block_size, box = min(bs, ROWS_KEYS), nv = min(ROWS_KEYS, len - t * ROWS_KEYS);
             const int nb = ceil_div_i(nv, box);
             const int blk = lane / HALVES, half = lane % HALVES;
             const int e = __shfl_sync(0xffffffffu, ent, blk);
@@ -460,7 +463,8 @@ struct RowsLoader {
                          bs > ROWS_KEYS ? (t * ROWS_KEYS) % bs : 0, e, bar);
         }
         __syncwarp();
-        if (++stage == (uint32_t)a.stages) { stage = 0; phase ^= 1u; }
+        stage += 2;                                      // the stage between is the other loader's
+        if (stage >= (uint32_t)a.stages) { stage -= (uint32_t)a.stages; phase ^= 1u; }
         return true;
     }
 
@@ -528,8 +532,8 @@ struct RowsLoader {
         ++nh;
     }
 
-    __device__ __forceinline__ bool run(const CUtensorMap* tq, const CUtensorMap* tqn, const CUtensorMap* tk,
-                                        const CUtensorMap* tv, const CUtensorMap* tpk, const CUtensorMap* tpv)
+    __device__ __forceinline__ bool run_k(const CUtensorMap* tq, const CUtensorMap* tqn, const CUtensorMap* tk,
+                                          const CUtensorMap* tpk)
     {
         const int lane = threadIdx.x & 31;
         const int c = blockIdx.x, parts = gridDim.x;
@@ -575,13 +579,12 @@ struct RowsLoader {
                 }
                 publish();
                 if (!pair) toggle = (toggle + (uint32_t)(t1 - t0)) & 1u;
-                int ent = a.block_table ? entry(r, t0) : 0;
+                int ent = a.block_table ? entry(r.b, r.len, t1 - 1) : 0;
                 if (narrow ? !query_narrow(tqn, g, r.tok0) : !query(tq, g, r.tok0)) return false;
                 if (pair && !query(tq, g, r.tok0 + a.tpt)) return false;
-                for (int t = t0; t < t1; ++t) {
-                    const int next = a.block_table && t + 1 < t1 ? entry(r, t + 1) : 0;
-                    if (!tile(r.b < 0 ? tpk : tk, r, g, t, ent)) return false;
-                    if (!tile(r.b < 0 ? tpv : tv, r, g, t, ent)) return false;
+                for (int t = t1 - 1; t >= t0; --t) {
+                    const int next = a.block_table && t > t0 ? entry(r.b, r.len, t - 1) : 0;
+                    if (!tile(r.b < 0 ? tpk : tk, r.b, r.len, g, t, ent)) return false;
                     ent = next;
                 }
                 pos = tb < r.nt ? end : next_pos;
@@ -595,11 +598,33 @@ struct RowsLoader {
         return true;
     }
 
-    // After an abort: every copy issued lands before the CTA exits (bounded waits).
-    __device__ __forceinline__ void settle()
+    __device__ __forceinline__ bool run_v(const CUtensorMap* tv, const CUtensorMap* tpv)
+    {
+        const int lane = threadIdx.x & 31;
+        stage = 1;
+        for (;; ++nh) {
+            const uint32_t hs = nh % RW_HDRS;
+            if (!rwait(bars.hfull + 8 * hs, (nh / RW_HDRS) & 1u, misc, a)) return false;
+            const int* h = reinterpret_cast<const int*>(sm + lay.hdr + hs * RW_HDR_BYTES);
+            const int kind = h[RH_KIND], g = h[RH_G], b = h[RH_B], len = h[RH_LEN], t0 = h[RH_T0], t1 = h[RH_T1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.hempty + 8 * hs);
+            if (kind == RUN_END) return true;
+            int ent = a.block_table ? entry(b, len, t1 - 1) : 0;
+            for (int t = t1 - 1; t >= t0; --t) {
+                const int next = a.block_table && t > t0 ? entry(b, len, t - 1) : 0;
+                if (!tile(b < 0 ? tpv : tv, b, len, g, t, ent)) return false;
+                ent = next;
+            }
+        }
+    }
+
+    // After an abort: every copy issued lands before the CTA exits (bounded waits). `first`: this loader's
+    // first stage.
+    __device__ __forceinline__ void settle(int first)
     {
         if ((threadIdx.x & 31) == 0) {
-            for (int s = 0; s < a.stages; ++s) {
+            for (int s = first; s < a.stages; s += 2) {
                 const uint32_t par = (uint32_t)s < stage ? phase : (phase ^ 1u);
                 const uint64_t t0 = global_ns();
                 while (!mbar_try_wait(bars.kvfull + 8 * s, par) && global_ns() - t0 < 100000000ull) {
@@ -712,10 +737,10 @@ struct RowsMma {
             if (kind == RUN_END) break;
             const bool pair = flags & RF_PAIR;
             const uint32_t start = (flags & RF_START) ? 1u : 0u;
-            // this stream's tiles: all of a pair's from first to past, else every second one
-            const int first = pair ? s0 : t0 + (int)(S ^ start), past = pair ? s1 : t1;
-            const bool any = first < past;
-            const int last = any ? (pair ? past - 1 : past - 1 - ((past - 1 - first) & 1)) : -1;
+            // this stream's tiles, counted from the run's last: a pair's from j0 to j1, else every second one
+            const int n = t1 - t0, j0 = pair ? t1 - s1 : (int)(S ^ start), j1 = pair ? t1 - s0 : n;
+            const bool any = j0 < j1;
+            const int last = pair ? j1 - 1 : j1 - 1 - ((j1 - 1 - j0) & 1);
             // Q: of a pair, the buffer that is not this stream's goes back at once, as one without tiles does
             uint32_t qd = 0, qbar = 0;
             if (ncols) {
@@ -735,10 +760,11 @@ struct RowsMma {
                     }
                 }
             }
-            for (int t = t0; t < t1; ++t) {
+            for (int j = 0; j < n; ++j) {
+                const int t = t1 - 1 - j;
                 uint32_t vstage = stage + 1, vphase = phase;
                 if (vstage == (uint32_t)a.stages) { vstage = 0; vphase ^= 1u; }
-                const bool mine = t >= first && t < past && (pair || (((uint32_t)(t - t0) ^ start ^ S) & 1u) == 0u);
+                const bool mine = j >= j0 && j < j1 && (pair || ((uint32_t)(j - j0) & 1u) == 0u);
                 if (mine) {
                     if (!await(bars.kvfull + 8 * stage, phase)) return false;
                     const int nv = len - t * ROWS_KEYS;
@@ -775,11 +801,11 @@ struct RowsMma {
                     }
                     umma_commit(lead, bars.sfull + 8 * S);
                     umma_commit(lead, bars.kvempty + 8 * stage);
-                    if (qbar && t == last) umma_commit(lead, qbar);
+                    if (qbar && j == last) umma_commit(lead, qbar);
                     __syncwarp();
                     owes = true;
-                    pfirst = t == first;
-                    plast = t == last;
+                    pfirst = j == j0;
+                    plast = j == last;
                     pstage = vstage;
                     pphase = vphase;
                     pcols = ncols;
@@ -986,8 +1012,9 @@ struct Softmax {
         float2* ml = reinterpret_cast<float2*>(sm + lay.ml);
         const bool pair = run.flags & RF_PAIR;
         const int start = (run.flags & RF_START) ? 1 : 0, t0 = run.t0, t1 = run.t1, base = run.base;
-        // this stream's tiles: first, first + step, .. below past
-        const int first = pair ? run.s0 : t0 + (S ^ start), past = pair ? run.s1 : t1, step = pair ? 1 : 2;
+        // this stream's tiles, from the last key on (the bias grows towards the row's own position, so a
+        // row's largest scores tend to come first): first, first - step, .. down to `least`
+        const int first = pair ? run.s1 - 1 : t1 - 1 - (S ^ start), least = pair ? run.s0 : t0, step = pair ? 1 : 2;
         const int ti = r / a.G, hh = r - ti * a.G;
         const int tok = run.tok0 + (pair ? S * a.tpt : 0) + ti;
         const bool live = ti < a.tpt && tok < run.tok0 + run.ntok;
@@ -1008,7 +1035,7 @@ struct Softmax {
         const bool linear = __all_sync(0xffffffffu, !mine || hi <= spos + 1);
         float m = -INFINITY, l = 0.f;                    // frame (log2 units) and sum
         int count = 0;
-        for (int t = first; t < past; t += step, ++ntile, ++count) {
+        for (int t = first; t >= least; t -= step, ++ntile, ++count) {
             if (!rwait(bars.sfull + 8 * S, ntile & 1u, misc, a)) return false;
             tc_fence_after();
             if (warp_live) {
@@ -1354,7 +1381,7 @@ struct Softmax {
         const float rate = a.scale * LOG2E;
         const float cap_rate = MODE == MODE_CAP ? 2.f * LOG2E / a.cap : 0.f;
         int count = 0;
-        for (int t = run.t0 + (S ^ start); t < run.t1; t += 2, ++ntile, ++count) {
+        for (int t = run.t1 - 1 - (S ^ start); t >= run.t0; t -= 2, ++ntile, ++count) {
             if (!rwait(bars.sfull + 8 * S, ntile & 1u, misc, a)) return false;
             tc_fence_after();
             const int k0 = t * ROWS_KEYS, key = k0 + 32 * w + lane;
@@ -1599,7 +1626,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
         }
         for (int i = 0; i < RW_HDRS; ++i) {
             mbar_init(bars.hfull + 8 * i, 1);
-            mbar_init(bars.hempty + 8 * i, 10);
+            mbar_init(bars.hempty + 8 * i, 11);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bars.qfull + 8 * i, 1);
@@ -1634,9 +1661,13 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
     grid_dependency_wait();
     grid_launch_dependents();
-    if (warp == RW_LOAD_WARP) {
+    if (warp >= RW_LOAD_WARP) {
         RowsLoader<D> ld{a, lay, bars, sm, sbase, misc};
-        if (!ld.run(&tq, &tqn, &tk, &tv, &tpk, &tpv)) ld.settle();
+        if (warp == RW_LOAD_WARP) {
+            if (!ld.run_k(&tq, &tqn, &tk, &tpk)) ld.settle(0);
+        } else {
+            if (!ld.run_v(&tv, &tpv)) ld.settle(1);
+        }
         if (ld.bad) rows_error(a, ld.bad);
     } else if (warp >= RW_MMA_WARP) {
         RowsMma<D> mma{a, lay, bars, sbase, tmem, misc, (uint32_t)(warp - RW_MMA_WARP)};
@@ -1811,8 +1842,8 @@ cudaError_t launch_d(const RowsArgs& a, const RowsMaps& m, cudaStream_t s)
 int rows_tc_stages(int head_dim, int smem_per_block)
 {
     int n = 0;
-    while (n < 16 && (head_dim == 128 ? RowsSmem<128>(n + 1).total : RowsSmem<64>(n + 1).total) <= smem_per_block) ++n;
-    return n;
+    while (n < 16 && (head_dim == 128 ? RowsSmem<128>(n + 2).total : RowsSmem<64>(n + 2).total) <= smem_per_block) n += 2;
+    return n;                                            // even: K and V tiles take turns
 }
 
 cudaError_t launch_rows_tc(const RowsArgs& a, const RowsMaps& m, cudaStream_t s)
