@@ -19,9 +19,7 @@
 //            softmax runs the tensor cores work on the other's tile.
 //   warps 0-3, 4-7   the softmax of streams 0 and 1: a thread owns a row (tensor-memory lane), reads its
 //            128 scores, and writes P as bf16 over them. P's rounding (2^-9 of each weight, independent)
-//            leaves an error of the order of the output's own rounding; l sums the unrounded weights. A
-//            tile is computed in the frame that the row had before it; only when a score is beyond the
-//            frame by more than the lag is the frame moved and the tile computed again.
+//            leaves an error of the order of the output's own rounding; l sums the unrounded weights.
 // With more than 128 rows a unit is a pair: two row tiles, one per stream, share every K/V tile. With
 // fewer, both streams take the same rows, alternate key tiles and are joined at the run's end.
 //
@@ -47,8 +45,6 @@
 // MMAs land, frees its tensor memory and exits.
 #include <cuda_bf16.h>
 
-#include <type_traits>
-
 #include "rows_common.cuh"
 #include "tcgen05.cuh"
 
@@ -58,6 +54,9 @@ namespace {
 constexpr int RW_MMA_WARP = 8;           // and the next: one per stream
 constexpr int RW_LOAD_WARP = 10;         // and the next: K (with the headers and Q), and V
 constexpr int RW_THREADS = 12 * 32;
+// Registers of a softmax warp and of the others: (2 x 200 + 104) x 128 = 64512, the 384 x 168 of the launch.
+constexpr int RW_SOFT_REGS = 200;
+constexpr int RW_HELP_REGS = 104;
 constexpr int RW_HDRS = 4;               // run headers in flight
 constexpr int RW_HDR_BYTES = 64;
 constexpr float RW_LAG = 8.f;            // log2 of the growth of a row's max that moves its frame
@@ -101,7 +100,7 @@ struct RowsSmem {
     int q, stages, turn, hdr, ml, bars, misc, tslot, nsh, total;
     __host__ __device__ explicit RowsSmem(int nst)
         : q(0), stages(2 * QB), turn(stages + nst * SB), hdr(turn + 8 * TURN), ml(hdr + RW_HDRS * RW_HDR_BYTES),
-          bars(ml + 2 * ROWS_TILE * 8), misc(bars + (2 * nst + 2 * (2 + NSLOTS) + 2 * RW_HDRS + 6 * 2 + 1) * 8),
+          bars(ml + 2 * ROWS_TILE * 8), misc(bars + (2 * nst + 2 * (2 + NSLOTS) + 2 * RW_HDRS + 7 * 2 + 1) * 8),
           tslot(misc + 64), nsh(NSH_IN_Q ? SLOTS_END : tslot + 16),
           total(tslot + 16 + (NSH_IN_Q ? 0 : (int)sizeof(NarrowShared)))
     {
@@ -114,7 +113,8 @@ struct RowsBars {
     uint32_t qfull, qempty;       // [2]
     uint32_t nqfull, nqempty;     // [4] the key-major runs' slots
     uint32_t hfull, hempty;       // [RW_HDRS] run headers: read by the V loader, the MMA and softmax warps
-    uint32_t sfull, pready;       // [2] scores written; weights written
+    uint32_t sfull, pready;       // [2] scores written; weights written (128-row runs: of the first 64 keys,
+    uint32_t prest;               //     and the rest)
     uint32_t ofull, ofree;        // [2] accumulator complete; read out
     uint32_t mlfree;              // [2] a stream's maxima and sums have been read
     uint32_t vote;                // [2] the warps of a stream meet (key-major runs)
@@ -131,7 +131,8 @@ struct RowsBars {
         hempty = hfull + 8 * RW_HDRS;
         sfull = hempty + 8 * RW_HDRS;
         pready = sfull + 16;
-        ofull = pready + 16;
+        prest = pready + 16;
+        ofull = prest + 16;
         ofree = ofull + 16;
         mlfree = ofree + 16;
         vote = mlfree + 16;
@@ -141,7 +142,7 @@ struct RowsBars {
 
 // All lanes wait. A wait that is over when asked for costs two instructions; otherwise it is bounded, and
 // one that runs out aborts the CTA (warp-uniform result).
-__device__ __noinline__ bool rwait_slow(uint32_t bar, uint32_t parity, volatile int* misc, unsigned* err)
+__device__ __forceinline__ bool rwait_slow(uint32_t bar, uint32_t parity, volatile int* misc, unsigned* err)
 {
     bool ok = (misc[0] == 0) && mbar_wait(bar, parity);
     ok = __all_sync(0xffffffffu, ok);
@@ -671,14 +672,11 @@ struct RowsMma {
     // the tile whose P V is still to be issued (ncols: of a key-major run, else 0)
     bool owes = false, pfirst = false, plast = false;
     uint32_t pstage = 0, pphase = 0, pcols = 0;
-    uint32_t np = 0, nacc = 0;                   // P V issued, runs begun
+    uint32_t np = 0, nrest = 0, nacc = 0;        // P V issued (and those in two halves), runs begun
 
-    // Issues the P V that is owed.
-    __device__ __forceinline__ bool flush()
+    // Waits until the P V that is owed can be issued.
+    __device__ __forceinline__ bool ready()
     {
-        constexpr uint32_t IDESC = umma_idesc_bf16(128, D, false) | (1u << 16);     // V: MN-major B
-        if (!owes) return true;
-        owes = false;
         if (!rwait(bars.kvfull + 8 * pstage, pphase, misc, a)) return false;
         if (pfirst) {
             if (!rwait(bars.ofree + 8 * S, (nacc & 1u) ^ 1u, misc, a)) return false;
@@ -686,15 +684,27 @@ struct RowsMma {
         }
         if (!rwait(bars.pready + 8 * S, np & 1u, misc, a)) return false;
         ++np;
+        return true;
+    }
+
+    __device__ __forceinline__ bool issue_pv()
+    {
+        constexpr uint32_t IDESC = umma_idesc_bf16(128, D, false) | (1u << 16);     // V: MN-major B
         tc_fence_after();
         const bool lead = elect_one();
         const uint32_t od = tmem + 2 * TM_S + S * D, more = pfirst ? 0u : 1u;
         const uint32_t vd = sw128_mnmajor_lo(sbase + lay.stages + pstage * RowsSmem<D>::SB, RowsSmem<D>::HALF);
         if (pcols == 0) {
+            // the first 64 keys' weights come before the others
             const uint32_t pd = tmem + S * TM_S;
 #pragma unroll
-            for (int k = 0; k < ROWS_KEYS / 16; ++k)
+            for (int k = 0; k < 4; ++k)
                 umma_bf16_ta_lo(lead, od, pd + 8 * k, vd + k * (2048 >> 4), IDESC, k == 0 ? more : 1u);
+            if (!rwait(bars.prest + 8 * S, nrest & 1u, misc, a)) return false;
+            ++nrest;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 4; k < 8; ++k) umma_bf16_ta_lo(lead, od, pd + 8 * k, vd + k * (2048 >> 4), IDESC, 1u);
         } else {
             // O^T += V^T P^T: d on M, the rows on N, 64 keys per half of P^T
             const uint32_t idesc = umma_idesc_bf16(D, 16, true) + ((pcols - 16) >> 3 << 17);
@@ -707,7 +717,15 @@ struct RowsMma {
         umma_commit(lead, bars.kvempty + 8 * pstage);
         if (plast) umma_commit(lead, bars.ofull + 8 * S);
         __syncwarp();
+        owes = false;
         return true;
+    }
+
+    // Issues the P V that is owed.
+    __device__ __forceinline__ bool flush()
+    {
+        if (!owes) return true;
+        return ready() && issue_pv();
     }
 
     // Waits for something the load warp brings. The P V that is owed goes first where it is not there yet:
@@ -870,7 +888,7 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
-__device__ __forceinline__ float max32(const uint32_t (&y)[32])
+__device__ __forceinline__ float max32(const uint32_t* y)
 {
     float m[4];
 #pragma unroll
@@ -899,12 +917,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 {
     uint64_t d;
@@ -926,17 +938,18 @@ __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[NR])
     }
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+        "%13, %14, %15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+        : "memory");
+}
+
 template <int NR>
 __device__ __forceinline__ void tmem_st_rows(uint32_t taddr, const uint32_t (&r)[NR])
 {
-    if constexpr (NR == 16) {
-        asm volatile(
-            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-            "%13, %14, %15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-            "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
-            : "memory");
-        return;
-    }
 #pragma unroll
     for (int i = 0; i < NR; i += 8)
         asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[i]),
@@ -1040,125 +1053,101 @@ struct Softmax {
             tc_fence_after();
             if (warp_live) {
                 const int k0 = t * ROWS_KEYS;
-                const bool open = __all_sync(0xffffffffu, lo <= k0 && hi >= k0 + ROWS_KEYS);
-                // 32 scores as v
-                auto load = [&](int c, uint32_t (&y)[32]) {
-                    tmem_ld32_async(ts + 32 * c, y);
-                    tmem_wait_ld();
-                    reg_fence32(y);
-                    const int kc = k0 + 32 * c;
-                    if (MODE == MODE_BIAS && linear) {
-                        const float b0 = slope * (float)(kc - spos);
-                        const uint64_t rate2 = pair2(rate, rate);
+                // all 128 scores at once: a load's latency is long while the other stream's MMAs use the
+                // tensor memory
+                uint32_t x[ROWS_KEYS];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            float v0, v1;
-                            unpair2(fma2(pair2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), rate2,
-                                         pair2(fmaf(slope, (float)i, b0), fmaf(slope, (float)(i + 1), b0))), v0, v1);
-                            y[i] = __float_as_uint(v0);
-                            y[i + 1] = __float_as_uint(v1);
-                        }
-                    } else if (MODE != MODE_PLAIN) {
-                        const float d0 = (float)(kc - spos);
+                for (int c = 0; c < 4; ++c) tmem_ld32_async(ts + 32 * c, x + 32 * c);
+                tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            y[i] = __float_as_uint(mod_score(__uint_as_float(y[i]), a.scale, MODE == MODE_CAP ? a.cap : 0.f,
-                                                             cap_rate, slope, d0 + (float)i));
+                for (int c = 0; c < 4; ++c) reg_fence32(x + 32 * c);
+                // v, where it is more than the scale
+                if (MODE == MODE_BIAS && linear) {
+                    const float b0 = slope * (float)(k0 - spos);
+                    const uint64_t rate2 = pair2(rate, rate);
+#pragma unroll
+                    for (int i = 0; i < ROWS_KEYS; i += 2) {
+                        float v0, v1;
+                        unpair2(fma2(pair2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), rate2,
+                                     pair2(fmaf(slope, (float)i, b0), fmaf(slope, (float)(i + 1), b0))), v0, v1);
+                        x[i] = __float_as_uint(v0);
+                        x[i + 1] = __float_as_uint(v1);
                     }
-                    if (!open) {
-                        const int c0 = lo - kc, c1 = hi - kc;
+                } else if (MODE != MODE_PLAIN) {
+                    const float d0 = (float)(k0 - spos);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (i < c0 || i >= c1) y[i] = __float_as_uint(-INFINITY);
-                    }
-                };
-                auto tile_max = [&]() {
-                    float top = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t y[32];
-                        load(c, y);
-                        top = fmaxf(top, max32(y));
-                    }
-                    return MODE == MODE_PLAIN ? top * rate : top;
-                };
-                // The tile's weights in the frame m, their sum, and the largest v - m. EXACT: v is rounded
-                // before the frame is taken off, so that no v - m is above 0 in the frame of the largest v.
-                uint32_t w[64];
-                float sum;
-                auto weigh = [&](auto exact) {
-                    constexpr bool EXACT = decltype(exact)::value;
-                    const float mu = m == -INFINITY ? 0.f : m;
-                    const uint64_t nmu = pair2(-mu, -mu), rate2 = pair2(rate, rate);
-                    uint64_t s0 = pair2(0.f, 0.f), s1 = s0;
-                    float top = -INFINITY;
+                    for (int i = 0; i < ROWS_KEYS; ++i)
+                        x[i] = __float_as_uint(mod_score(__uint_as_float(x[i]), a.scale, MODE == MODE_CAP ? a.cap : 0.f,
+                                                         cap_rate, slope, d0 + (float)i));
+                }
+                if (!__all_sync(0xffffffffu, lo <= k0 && hi >= k0 + ROWS_KEYS)) {
+                    const int c0 = lo - k0, c1 = hi - k0;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t y[32];
-                        load(c, y);
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            uint64_t v0 = pair2(__uint_as_float(y[i]), __uint_as_float(y[i + 1]));
-                            uint64_t v1 = pair2(__uint_as_float(y[i + 2]), __uint_as_float(y[i + 3]));
-                            if (MODE != MODE_PLAIN) {
-                                v0 = add2(v0, nmu);
-                                v1 = add2(v1, nmu);
-                            } else if (EXACT) {
-                                v0 = add2(mul2(v0, rate2), nmu);
-                                v1 = add2(mul2(v1, rate2), nmu);
-                            } else {
-                                v0 = fma2(v0, rate2, nmu);
-                                v1 = fma2(v1, rate2, nmu);
-                            }
-                            float p0, p1, p2, p3;
-                            unpair2(v0, p0, p1);
-                            unpair2(v1, p2, p3);
-                            if (!EXACT) {
-                                top = max3(top, p0, p1);
-                                top = max3(top, p2, p3);
-                            }
-                            p0 = ex2(p0); p1 = ex2(p1); p2 = ex2(p2); p3 = ex2(p3);
-                            s0 = add2(s0, pair2(p0, p1));
-                            s1 = add2(s1, pair2(p2, p3));
-                            w[16 * c + i / 2] = pack_bf16x2(p0, p1);
-                            w[16 * c + i / 2 + 1] = pack_bf16x2(p2, p3);
-                        }
-                    }
-                    float p0, p1;
-                    unpair2(add2(s0, s1), p0, p1);
-                    sum = p0 + p1;
-                    return top;
-                };
-                if (count == 0) m = tile_max();          // a frame to begin with
-                const float top = weigh(std::false_type());
-                if (__any_sync(0xffffffffu, top > (m == -INFINITY ? -INFINITY : RW_LAG))) {
+                    for (int i = 0; i < ROWS_KEYS; ++i)
+                        if (i < c0 || i >= c1) x[i] = __float_as_uint(-INFINITY);
+                }
+                float top = max3(fmaxf(max32(x), max32(x + 32)), max32(x + 64), max32(x + 96));
+                if (MODE == MODE_PLAIN) top *= rate;
+                if (count == 0) {
+                    m = top;
+                } else if (__any_sync(0xffffffffu, top > (m == -INFINITY ? -INFINITY : m + RW_LAG))) {
                     // move the frame: the accumulator's P V of the tile before has completed (the scores'
                     // barrier counts every MMA issued before them)
-                    const float f = fmaxf(m, tile_max()), wt = m == f ? 1.f : ex2(m - f);
+                    const float f = fmaxf(m, top), wt = m == f ? 1.f : ex2(m - f);
                     m = f;
                     l *= wt;
-                    if (count > 0) {
 #pragma unroll 1
-                        for (int i = 0; i < D; i += 16) {
-                            uint32_t o[16];
-                            tmem_ld16_async(to + S * D + i, o);
-                            tmem_wait_ld();
-                            reg_fence16(o);
+                    for (int i = 0; i < D; i += 16) {
+                        uint32_t o[16];
+                        tmem_ld16_async(to + S * D + i, o);
+                        tmem_wait_ld();
+                        reg_fence16(o);
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * wt);
-                            tmem_st_rows<16>(to + S * D + i, o);
-                        }
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * wt);
+                        tmem_st16(to + S * D + i, o);
                     }
-                    weigh(std::true_type());
                 }
-                tmem_st32(ts, w);
-                tmem_st32(ts + 32, w + 32);
-                l += sum;
+                // The weights, two to a register. The first 64 keys' go to the MMA warp while the last ones
+                // are still computed; the wait for their stores comes after the third quarter's arithmetic.
+                const float mu = m == -INFINITY ? 0.f : m;
+                const uint64_t nmu = pair2(-mu, -mu), rate2 = pair2(rate, rate);
+                uint64_t s0 = pair2(0.f, 0.f), s1 = s0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t* y = x + 32 * c;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        uint64_t v0 = pair2(__uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+                        uint64_t v1 = pair2(__uint_as_float(y[i + 2]), __uint_as_float(y[i + 3]));
+                        if (MODE == MODE_PLAIN) { v0 = fma2(v0, rate2, nmu); v1 = fma2(v1, rate2, nmu); }
+                        else { v0 = add2(v0, nmu); v1 = add2(v1, nmu); }
+                        float p0, p1, p2, p3;
+                        unpair2(v0, p0, p1);
+                        unpair2(v1, p2, p3);
+                        p0 = ex2(p0); p1 = ex2(p1); p2 = ex2(p2); p3 = ex2(p3);
+                        s0 = add2(s0, pair2(p0, p1));
+                        s1 = add2(s1, pair2(p2, p3));
+                        y[i / 2] = pack_bf16x2(p0, p1);
+                        y[i / 2 + 1] = pack_bf16x2(p2, p3);
+                    }
+                    if (c == 2) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bars.pready + 8 * S);
+                    }
+                    tmem_st16(ts + 16 * c, y);
+                }
+                float p0, p1;
+                unpair2(add2(s0, s1), p0, p1);
+                l += p0 + p1;
                 tmem_wait_st();
+            } else if (lane == 0) {
+                mbar_arrive(bars.pready + 8 * S);
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bars.pready + 8 * S);
+            if (lane == 0) mbar_arrive(bars.prest + 8 * S);
         }
 
         // ---- the run's end ----
@@ -1633,6 +1622,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
             mbar_init(bars.qempty + 8 * i, 2);       // both streams
             mbar_init(bars.sfull + 8 * i, 1);
             mbar_init(bars.pready + 8 * i, 4);
+            mbar_init(bars.prest + 8 * i, 4);
             mbar_init(bars.ofull + 8 * i, 1);
             mbar_init(bars.ofree + 8 * i, 4);
             mbar_init(bars.mlfree + 8 * i, 4);
@@ -1661,23 +1651,27 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
     grid_dependency_wait();
     grid_launch_dependents();
-    if (warp >= RW_LOAD_WARP) {
-        RowsLoader<D> ld{a, lay, bars, sm, sbase, misc};
-        if (warp == RW_LOAD_WARP) {
-            if (!ld.run_k(&tq, &tqn, &tk, &tpk)) ld.settle(0);
+    if (warp >= RW_MMA_WARP) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RW_HELP_REGS));
+        if (warp >= RW_LOAD_WARP) {
+            RowsLoader<D> ld{a, lay, bars, sm, sbase, misc};
+            if (warp == RW_LOAD_WARP) {
+                if (!ld.run_k(&tq, &tqn, &tk, &tpk)) ld.settle(0);
+            } else {
+                if (!ld.run_v(&tv, &tpv)) ld.settle(1);
+            }
+            if (ld.bad) rows_error(a, ld.bad);
         } else {
-            if (!ld.run_v(&tv, &tpv)) ld.settle(1);
+            RowsMma<D> mma{a, lay, bars, sbase, tmem, misc, (uint32_t)(warp - RW_MMA_WARP)};
+            mma.run(sm);
+            // every MMA issued has landed before the tensor memory and the stages go
+            umma_commit(elect_one(), bars.drain);
+            __syncwarp();
+            if (!mbar_wait(bars.drain, 0u) && lane == 0) rows_error(a, FDPP_ERRBIT_TIMEOUT);
+            __syncwarp();
         }
-        if (ld.bad) rows_error(a, ld.bad);
-    } else if (warp >= RW_MMA_WARP) {
-        RowsMma<D> mma{a, lay, bars, sbase, tmem, misc, (uint32_t)(warp - RW_MMA_WARP)};
-        mma.run(sm);
-        // every MMA issued has landed before the tensor memory and the stages go
-        umma_commit(elect_one(), bars.drain);
-        __syncwarp();
-        if (!mbar_wait(bars.drain, 0u) && lane == 0) rows_error(a, FDPP_ERRBIT_TIMEOUT);
-        __syncwarp();
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(RW_SOFT_REGS));
         Softmax<D, MODE> sx{a, lay, bars, sm, tmem, misc, warp >> 2};
         sx.run();
         tc_fence_before();
