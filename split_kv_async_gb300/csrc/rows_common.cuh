@@ -82,15 +82,13 @@ __device__ __forceinline__ long long key_offset(const RowsArgs& a, int b, int t,
 }
 
 // The score in units of log2: cap, then the bias -slope |pos - t|. tanh(x) = 1 - 2 / (e^2x + 1): two
-// MUFU operations, absolute error a few 2^-23 of the cap (tanh.approx would be 2^-11 off).
+// MUFU operations, absolute error a few 2^-23 of the cap (tanh.approx would be 2^-11 off). cap_rate: 2
+// scale log2(e) / cap.
 __device__ __forceinline__ float mod_score(float qk, float scale, float cap, float cap_rate, float slope2, float dist)
 {
-    float s = qk * scale;
-    if (cap > 0.f) {
-        const float e = ex2(s * cap_rate);                  // e^(2 s / cap)
-        s = cap - 2.f * cap * rcp(e + 1.f);
-    }
-    return fmaf(s, LOG2E, -slope2 * fabsf(dist));
+    float s = qk * (scale * LOG2E);
+    if (cap > 0.f) s = fmaf(-2.f * LOG2E * cap, rcp(ex2(qk * cap_rate) + 1.f), LOG2E * cap);
+    return fmaf(-slope2, fabsf(dist), s);
 }
 
 }  // namespace

@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
             for (int e = 0; e < 4; ++e) { qr[h][4 * i + e] = x[e]; o[h][4 * i + e] = 0.f; }
         }
     }
-    const float cap_rate = a.cap > 0.f ? 2.f * LOG2E / a.cap : 0.f;
+    const float cap_rate = a.cap > 0.f ? 2.f * LOG2E * a.scale / a.cap : 0.f;
     const unsigned gmask = 0xffu << (lane & ~(LANES - 1));
 
 #pragma unroll 2
