@@ -227,6 +227,8 @@ __device__ __forceinline__ long long plan_scan(long long x, long long& total, lo
 __device__ __forceinline__ void set_tiles(RowTileRec& r, int loA, int hiA, int loB, int hiB)
 {
     r.a0 = r.a1 = r.b0 = r.b1 = 0;
+    hiA = min(hiA, r.len);
+    hiB = min(hiB, r.len);
     if (hiA > loA) { r.a0 = loA / ROWS_KEYS; r.a1 = ceil_div_i(hiA, ROWS_KEYS); }
     if (hiB > loB) { r.b0 = loB / ROWS_KEYS; r.b1 = ceil_div_i(hiB, ROWS_KEYS); }
     int k0 = r.a0, k1 = r.a1;
@@ -238,6 +240,140 @@ __device__ __forceinline__ void set_tiles(RowTileRec& r, int loA, int hiA, int l
     r.nt = k1 - k0;
 }
 
+// The plan of calls with at most PLAN_SMALL sequences and row tiles: everything in shared memory, each
+// token looked at once. It is on every call's critical path, so it has few steps and little code (a kernel
+// starts with cold instruction caches): one row of loads per sequence, a scan, one pass over the tokens
+// that leaves the row tiles' key ranges in shared memory, a scan.
+constexpr int PLAN_SMALL = 1024;
+
+// Inclusive scan of x over the CTA's 1024 threads, and the total.
+__device__ __forceinline__ int scan_1024(int x, int& total, int* red)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) red[warp] = x;
+    __syncthreads();
+    int y = red[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
+    }
+    total = __shfl_sync(0xffffffffu, y, 31);
+    const int before = __shfl_sync(0xffffffffu, y, (warp + 31) & 31);
+    __syncthreads();
+    return x + (warp ? before : 0);
+}
+
+// The last i in [0, n) with v[i] <= x (v[0] <= x).
+__device__ __forceinline__ int last_at_most(const int* v, int n, int x)
+{
+    int lo = 0, hi = n;
+#pragma unroll 1
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (v[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(PLAN_SMALL) rows_plan_small_kernel(RowsArgs a)
+{
+    __shared__ int red[32];
+    __shared__ int rt0[PLAN_SMALL + 1], c0[PLAN_SMALL], cnt[PLAN_SMALL], len[PLAN_SMALL];
+    __shared__ int low[2][PLAN_SMALL], high[2][PLAN_SMALL];      // key ranges of the row tiles' halves; later: starts
+    const int t = threadIdx.x;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    unsigned bad = 0;
+    int first = 0, n = 0, L = 0;
+    if (t < a.B) {
+        n = seq_rows(a, t, first, bad);
+        L = own_len(a, t, bad);
+    }
+    const int P = prefix_keys(a, bad);
+    const int last = a.cu ? clamp_len(a.cu[a.B], a.T) : a.T;
+    const int pair = 2 * a.tpt, npre = P > 0 ? ceil_div_i(last, pair) : 0;
+    low[0][t] = low[1][t] = INT32_MAX;
+    high[0][t] = high[1][t] = 0;
+    int total;
+    const int mine = min(ceil_div_i(n, pair), PLAN_SMALL), incl = scan_1024(mine, total, red);
+    const int nrt = min(npre + total, a.max_rt);
+    if (npre + total > a.max_rt) bad |= FDPP_ERRBIT_TOKENS;      // sequences whose rows overlap
+    if (t < a.B) {
+        rt0[t] = min(npre + incl - mine, a.max_rt);
+        c0[t] = first;
+        cnt[t] = n;
+        len[t] = L;
+    }
+    __syncthreads();
+    for (int base = 0; base < a.T; base += PLAN_SMALL) {
+        const int row = base + t;
+        // (rows of an earlier sequence that the next one's overlap go to the later one)
+        const int b = last_at_most(c0, a.B, row), i = row - c0[b], rt = rt0[b] + i / pair;
+        if (row >= a.T) continue;
+        RowToken k{0, 0, 0, -1};
+        if (i >= 0 && i < cnt[b] && rt < nrt) {
+            k.pos = P + len[b] - cnt[b] + i;
+            k.rt = rt;
+            row_keys(a, row, k.pos, P + len[b], k.lo, k.hi);
+            if (k.hi > max(k.lo, P)) {
+                const int half = i % pair >= a.tpt;
+                atomicMin(&low[half][rt], max(k.lo - P, 0));
+                atomicMax(&high[half][rt], k.hi - P);
+            }
+            if (row < last && k.lo < min(k.hi, P)) {
+                const int half = row % pair >= a.tpt;
+                atomicMin(&low[half][row / pair], k.lo);
+                atomicMax(&high[half][row / pair], min(k.hi, P));
+            }
+            if (k.lo >= k.hi && !a.prefix_len) {                 // no unit may come by this row
+                uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (long long)row * a.Hq * a.D);
+                for (int x = 0; x < a.Hq * a.D / 8; ++x) o[x] = make_uint4(0, 0, 0, 0);
+            }
+        }
+        a.tok[row] = k;
+    }
+    __syncthreads();
+    RowTileRec r{};
+    if (t < nrt) {
+        if (t < npre) {
+            r.b = -1;
+            r.tok0 = t * pair;
+            r.ntok = min(pair, last - r.tok0);
+            r.len = P;
+        } else {
+            r.b = last_at_most(rt0, a.B, t);
+            const int i0 = (t - rt0[r.b]) * pair;
+            r.tok0 = c0[r.b] + i0;
+            r.ntok = max(0, min(pair, cnt[r.b] - i0));
+            r.len = len[r.b];
+        }
+        set_tiles(r, low[0][t], high[0][t], low[1][t], high[1][t]);
+    }
+    const int span = t < nrt ? unit_span(a, r) * a.Hkv : 0;
+    int tiles;
+    r.start = scan_1024(span, tiles, red) - span;
+    if (t < nrt) {
+        a.rec[t] = r;
+        low[0][t] = r.start;
+    }
+    __syncthreads();
+    if (t < a.parts) a.plan[RP_WORDS + t] = nrt ? last_at_most(low[0], nrt, part_begin(t, tiles, a.parts)) : 0;
+    if (t == 0) {
+        a.plan[RP_NRT] = nrt;
+        a.plan[RP_NPRE] = npre;
+        a.plan[RP_TILES] = tiles;
+        a.plan[RP_PREFIX] = P;
+    }
+    rows_error(a, bad);
+}
+
+// The plan of larger calls.
 __global__ void __launch_bounds__(PLAN_THREADS) rows_plan_kernel(RowsArgs a)
 {
     __shared__ long long red[32];
@@ -1723,8 +1859,7 @@ struct RowSum {
 };
 
 // The partials of a unit cut in two or more, tiles [start, start + nt): the part of its first tile left
-// its own in slot 2 c + 1, every later one in slot 2 c. Four are read at a time; an entry that is not the
-// unit's is read all the same (its slot exists) and counts as empty.
+// its own in slot 2 c + 1, every later one in slot 2 c. Four are read at a time.
 template <int E>
 __device__ __forceinline__ void add_cut(const RowsArgs& a, const int* begins, RowSum<E>& x, int start, int nt, int first,
                                         long long row)
@@ -1736,10 +1871,11 @@ __device__ __forceinline__ void add_cut(const RowsArgs& a, const int* begins, Ro
         for (int k = 0; k < 4; ++k) {
             const int c = min(c0 + k, a.parts - 1);
             const long long at = (long long)(2 * c + (c == first ? 1 : 0)) * a.slot_rows + row;
-            ml[k] = __ldcg(a.slot_ml + at);
-            RowSum<E>::fetch(a.slot_o + at * (E * 32), v[k]);
-            const bool has = c0 + k < a.parts && begins[c] < start + nt && (c == first || begins[c] < begins[c + 1]);
-            if (!has) ml[k] = make_float2(-INFINITY, 0.f);
+            ml[k] = make_float2(-INFINITY, 0.f);
+            if (c0 + k < a.parts && begins[c] < start + nt && (c == first || begins[c] < begins[c + 1])) {
+                ml[k] = __ldcg(a.slot_ml + at);
+                RowSum<E>::fetch(a.slot_o + at * (E * 32), v[k]);
+            }
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) x.add(ml[k], v[k]);
@@ -1838,8 +1974,9 @@ struct PdlConfig {
 template <int D, int MODE>
 cudaError_t launch_d(const RowsArgs& a, const RowsMaps& m, cudaStream_t s)
 {
-    PdlConfig plan(dim3(1), PLAN_THREADS, 0, s);
-    cudaError_t e = cudaLaunchKernelEx(&plan.cfg, rows_plan_kernel, a);
+    const bool small = a.B <= PLAN_SMALL && a.max_rt <= PLAN_SMALL;
+    PdlConfig plan(dim3(1), small ? PLAN_SMALL : PLAN_THREADS, 0, s);
+    cudaError_t e = cudaLaunchKernelEx(&plan.cfg, small ? rows_plan_small_kernel : rows_plan_kernel, a);
     if (e != cudaSuccess) return e;
     auto kern = rows_tile_kernel<D, MODE>;
     const int smem = RowsSmem<D>(a.stages).total;
