@@ -311,32 +311,43 @@ __global__ void __launch_bounds__(PLAN_SMALL) rows_plan_small_kernel(RowsArgs a)
         len[t] = L;
     }
     __syncthreads();
+    // the least and greatest key of each half of a row tile, one shared-memory operation for all the lanes
+    // of a warp that belong to it
+    auto widen = [&](int key, int from, int to) {
+        const unsigned m = __match_any_sync(0xffffffffu, key);
+        const int lo = __reduce_min_sync(m, from), hi = __reduce_max_sync(m, to);
+        if (key >= 0 && (t & 31) == __ffs(m) - 1) {
+            atomicMin(&low[key & 1][key >> 1], lo);
+            atomicMax(&high[key & 1][key >> 1], hi);
+        }
+    };
+    // key ranges are read a round ahead
+    int kb = a.key_begin && t < a.T ? a.key_begin[t] : 0, ke = a.key_end && t < a.T ? a.key_end[t] : 0;
     for (int base = 0; base < a.T; base += PLAN_SMALL) {
-        const int row = base + t;
-        // (rows of an earlier sequence that the next one's overlap go to the later one)
+        const int row = base + t, after = row + PLAN_SMALL;
+        const int nb = a.key_begin && after < a.T ? a.key_begin[after] : 0;
+        const int ne = a.key_end && after < a.T ? a.key_end[after] : 0;
         const int b = last_at_most(c0, a.B, row), i = row - c0[b], rt = rt0[b] + i / pair;
-        if (row >= a.T) continue;
         RowToken k{0, 0, 0, -1};
-        if (i >= 0 && i < cnt[b] && rt < nrt) {
+        int own = -1, pre = -1;
+        if (row < a.T && i >= 0 && i < cnt[b] && rt < nrt) {
             k.pos = P + len[b] - cnt[b] + i;
             k.rt = rt;
-            row_keys(a, row, k.pos, P + len[b], k.lo, k.hi);
-            if (k.hi > max(k.lo, P)) {
-                const int half = i % pair >= a.tpt;
-                atomicMin(&low[half][rt], max(k.lo - P, 0));
-                atomicMax(&high[half][rt], k.hi - P);
-            }
-            if (row < last && k.lo < min(k.hi, P)) {
-                const int half = row % pair >= a.tpt;
-                atomicMin(&low[half][row / pair], k.lo);
-                atomicMax(&high[half][row / pair], min(k.hi, P));
-            }
+            k.lo = max(kb, 0);
+            k.hi = min(a.key_end ? ke : k.pos + 1, P + len[b]);
+            if (k.hi <= k.lo) k.lo = k.hi = 0;
+            if (k.hi > max(k.lo, P)) own = rt * 2 + (i % pair >= a.tpt);
+            if (row < last && k.lo < min(k.hi, P)) pre = row / pair * 2 + (row % pair >= a.tpt);
             if (k.lo >= k.hi && !a.prefix_len) {                 // no unit may come by this row
                 uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (long long)row * a.Hq * a.D);
                 for (int x = 0; x < a.Hq * a.D / 8; ++x) o[x] = make_uint4(0, 0, 0, 0);
             }
         }
-        a.tok[row] = k;
+        widen(own, max(k.lo - P, 0), k.hi - P);
+        if (P > 0) widen(pre, k.lo, min(k.hi, P));
+        if (row < a.T) a.tok[row] = k;
+        kb = nb;
+        ke = ne;
     }
     __syncthreads();
     RowTileRec r{};
