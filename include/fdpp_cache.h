@@ -46,7 +46,7 @@ typedef struct fdpp_block_params {
     int max_tokens;          /* rows of token_seq, positions and slots */
 } fdpp_block_params;
 
-/* Bytes of workspace fdpp_block_map needs for `p` (an error word and a plan of 24 bytes per
+/* Bytes of workspace fdpp_block_map needs for `p` (an error word and a plan of 20 bytes per
  * sequence). 0 if the parameters are invalid. */
 size_t fdpp_block_map_workspace_size(const fdpp_block_params* p);
 

@@ -225,11 +225,22 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+_raw_stream = None     # torch's current stream as a handle, without building a Stream object (2 us a call)
+
+
 def _stream_handle(stream) -> Optional[int]:
-    if stream is None:
+    if stream is not None:
+        return stream.cuda_stream
+    global _raw_stream
+    if _raw_stream is None:
         import torch
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream
+        torch.cuda.init()
+        c = torch._C
+        if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
+            _raw_stream = lambda: c._cuda_getCurrentRawStream(c._cuda_getDevice())  # noqa: E731
+        else:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _raw_stream()
 
 
 def fdpp_workspace_init(workspace, stream=None) -> None:
@@ -407,7 +418,7 @@ def fdpp_flat_gemm_read_error(workspace) -> int:
 # ---- cache upkeep (include/fdpp_cache.h) ----------------------------------------------------
 
 def _bytes(t) -> int:
-    return t.numel() * t.element_size()
+    return t.nbytes
 
 
 def make_block_params(*, batch, block_size, max_blocks_per_seq, num_kv_blocks, max_tokens) -> fdpp_block_params:

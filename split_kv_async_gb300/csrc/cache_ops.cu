@@ -39,8 +39,13 @@ __device__ __forceinline__ void raise(unsigned* err, unsigned bits)
 //
 // Every new block holds a new token at its first position, so the row of that token writes the
 // table entry, and a row whose block is new takes it from the queue itself: nothing waits for the
-// table. What bounds this is latency, not bytes (a tick of 64 sequences moves 2 kB): one CTA that
-// does all in one launch up to MAP_ONE_CTA_ROWS rows, a second launch over the rows beyond.
+// table. What bounds this is latency, not bytes (a tick of 64 sequences moves 2 kB). So it is one
+// launch wherever it can be: up to MAP_SMEM_SEQS sequences every CTA makes the whole plan for itself in
+// shared memory (a few microseconds less than a launch that waits for another: 512 sequences with 81920
+// rows 8.5 us in two launches) and takes its share of the rows; with one CTA that also serves calls in
+// place and, with the plan in the workspace, any number of sequences. Only what needs more than one CTA
+// and cannot plan apart (in place, where a CTA would read lengths that another has already replaced, or
+// more sequences) takes a second launch over the rows.
 struct MapArgs {
     const int32_t* held;
     const int32_t* want;
@@ -54,8 +59,9 @@ struct MapArgs {
     int32_t* pos;
     int64_t* slots;
     unsigned* err;
-    // plan (workspace), for the rows: tokens held before, first queue entry of the new blocks,
-    // freed blocks of the sequences up to each one, blocks kept
+    // plan (workspace or shared memory), for the rows: first row of each sequence, tokens held before,
+    // first queue entry of the new blocks, freed blocks of the sequences up to each one, blocks kept
+    int32_t* p_cu;     // [B + 1]
     int32_t* p_held;   // [B]
     int32_t* p_first;  // [B]
     int32_t* p_back;   // [B + 1]
@@ -81,41 +87,42 @@ __device__ __forceinline__ void block_scan2(long long& x, long long& y, long lon
         const long long a = __shfl_up_sync(0xffffffffu, x, o), b = __shfl_up_sync(0xffffffffu, y, o);
         if (lane >= o) { x += a; y += b; }
     }
-    __syncthreads();
     if (lane == 31) { red[warp] = x; red[32 + warp] = y; }
     __syncthreads();
-    long long ax = 0, ay = 0;
-    tx = ty = 0;
-    for (int w = 0; w < nw; ++w) {
-        const long long a = red[w], b = red[32 + w];
-        if (w < warp) { ax += a; ay += b; }
-        tx += a;
-        ty += b;
+    long long sx = lane < nw ? red[lane] : 0, sy = lane < nw ? red[32 + lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long a = __shfl_up_sync(0xffffffffu, sx, o), b = __shfl_up_sync(0xffffffffu, sy, o);
+        if (lane >= o) { sx += a; sy += b; }
     }
-    x += ax;
-    y += ay;
+    tx = __shfl_sync(0xffffffffu, sx, 31);
+    ty = __shfl_sync(0xffffffffu, sy, 31);
+    const long long bx = __shfl_sync(0xffffffffu, sx, (warp + 31) & 31), by = __shfl_sync(0xffffffffu, sy, (warp + 31) & 31);
+    if (warp) { x += bx; y += by; }
+    __syncthreads();
 }
 
-__device__ __forceinline__ int wrap(long long i, int cap) { return (int)(i % cap); }
+// Queue entry i past the first (both below 2^31, so that the sum fits 32 bits unsigned).
+__device__ __forceinline__ int wrap(long long i, int cap) { return (int)((unsigned)i % (unsigned)cap); }
 
 // Rows r = first, first + step, ..: the sequence of a row is the last one that starts at or before
 // it among those with rows (cu is non-decreasing).
 __device__ __forceinline__ unsigned map_rows(const MapArgs& a, int first, int step)
 {
     unsigned bad = 0;
-    const int total = a.cu[a.B], bs = 1 << a.shift;
+    const int total = a.p_cu[a.B], bs = 1 << a.shift;
     const int head = a.p_pool[0];
     for (int r = first; r < a.room; r += step) {
         int b = -1, pos = 0;
         long long slot = -1;
         if (r < total) {
-            int lo = 0, hi = a.B;          // cu[lo] <= r < cu[hi]
+            int lo = 0, hi = a.B;          // p_cu[lo] <= r < p_cu[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (a.cu[mid] <= r) lo = mid; else hi = mid;
+                if (a.p_cu[mid] <= r) lo = mid; else hi = mid;
             }
             b = lo;
-            pos = a.p_held[b] + (r - a.cu[b]);
+            pos = a.p_held[b] + (r - a.p_cu[b]);
             const int j = pos >> a.shift, had = (a.p_held[b] + bs - 1) >> a.shift;
             int block;
             if (j < had) {
@@ -146,13 +153,27 @@ __device__ __forceinline__ unsigned map_rows(const MapArgs& a, int first, int st
     return bad;
 }
 
-template <bool ALL>      // ALL: the rows as well, in the same launch
+constexpr int MAP_SMEM_SEQS = 1024;
+
+// ROWS: the rows as well, in the same launch. SMEM: the plan in shared memory, so that any number of CTAs
+// may make it; the first one writes what the caller gets of it.
+template <bool ROWS, bool SMEM>
 __global__ void __launch_bounds__(MAP_THREADS) block_map_kernel(MapArgs a)
 {
     __shared__ long long red[64];
+    __shared__ int32_t plan[SMEM ? 5 * MAP_SMEM_SEQS + 4 : 4];
     unsigned bad = 0;
     const int bs = 1 << a.shift;
     const int most = (int)min((long long)a.width << a.shift, (long long)INT32_MAX);
+    const bool publish = blockIdx.x == 0;
+    if (SMEM) {
+        a.p_pool = plan;
+        a.p_held = plan + 2;
+        a.p_first = a.p_held + MAP_SMEM_SEQS;
+        a.p_kept = a.p_first + MAP_SMEM_SEQS;
+        a.p_back = a.p_kept + MAP_SMEM_SEQS;
+        a.p_cu = a.p_back + MAP_SMEM_SEQS + 1;
+    }
     grid_dependency_wait();
     int head = a.pool_in[0], count = a.pool_in[1];
     if (head < 0 || head >= a.cap || count < 0 || count > a.cap) {
@@ -181,38 +202,45 @@ __global__ void __launch_bounds__(MAP_THREADS) block_map_kernel(MapArgs a)
         const bool served = !short_blocks && !short_rows;
         if (short_blocks) bad |= FDPP_ERRBIT_POOL;
         if (short_rows) bad |= FDPP_ERRBIT_ROOM;
+        // rows and blocks of the served, both below 2^31, in one word
         const int rows = served ? ask : 0, back = max(0, old_blocks - new_blocks);
-        long long rows_i = rows, back_i = back, rows_t, back_t;
-        block_scan2(rows_i, back_i, rows_t, back_t, red);
-        long long got = served ? need : 0, zero = 0, got_t, zero_t;
-        block_scan2(got, zero, got_t, zero_t, red);
+        long long both_i = (long long)rows | ((long long)(served ? need : 0) << 32), back_i = back, both_t, back_t;
+        block_scan2(both_i, back_i, both_t, back_t, red);
+        const long long rows_i = both_i & 0xffffffffll, rows_t = both_t & 0xffffffffll;
         if (b < a.B) {
-            a.lens[b] = served ? want : held;
-            a.cu[b] = (int)(run.rows + rows_i - rows);
+            const int cu = (int)(run.rows + rows_i - rows);
+            a.p_cu[b] = cu;
             a.p_held[b] = held;
             a.p_first[b] = (int)min(run.need + need_i - need, (long long)INT32_MAX);
             a.p_back[b] = (int)(run.back + back_i - back);
             a.p_kept[b] = new_blocks;
+            if (publish) {
+                a.lens[b] = served ? want : held;
+                a.cu[b] = cu;
+            }
         }
         run.need += need_t;
         run.ask += ask_t;
         run.rows += rows_t;
         run.back += back_t;
-        taken += got_t;
+        taken += both_t >> 32;
     }
     if (threadIdx.x == 0) {
-        a.cu[a.B] = (int)run.rows;
+        a.p_cu[a.B] = (int)run.rows;
         a.p_back[a.B] = (int)run.back;
         a.p_pool[0] = head;
         a.p_pool[1] = count;
         const long long now = (long long)count - taken + run.back;
         if (now > a.cap) bad |= FDPP_ERRBIT_POOL;      // more freed than the pool has
-        a.pool_out[0] = wrap((long long)head + taken, a.cap);
-        a.pool_out[1] = (int)min(now, (long long)a.cap);
+        if (publish) {
+            a.cu[a.B] = (int)run.rows;
+            a.pool_out[0] = wrap((long long)head + taken, a.cap);
+            a.pool_out[1] = (int)min(now, (long long)a.cap);
+        }
     }
-    if (ALL) {
+    if (ROWS) {
         __syncthreads();
-        bad |= map_rows(a, threadIdx.x, blockDim.x);
+        bad |= map_rows(a, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
     }
     raise(a.err, bad);
 }
@@ -233,7 +261,7 @@ bool block_params_ok(const fdpp_block_params* p)
            p->max_tokens >= 0 && (long long)p->batch * p->max_blocks_per_seq < (1ll << 31);
 }
 
-size_t block_ws_bytes(const fdpp_block_params& p) { return 256 + ((size_t)p.batch * 4 + 4) * 4; }
+size_t block_ws_bytes(const fdpp_block_params& p) { return 256 + ((size_t)p.batch * 5 + 4) * 4; }
 
 // ------------------------------------------------------------------------------------------
 // rotary positions and append
@@ -501,14 +529,25 @@ fdpp_status fdpp_block_map(const int32_t* held_lens, const int32_t* want_lens, c
     a.p_first = a.p_held + a.B;
     a.p_kept = a.p_first + a.B;
     a.p_back = a.p_kept + a.B;
-    const bool one = a.room <= MAP_ONE_CTA_ROWS;
-    const int work = std::max(a.B, one ? a.room : 0);
-    const int threads = std::min(MAP_THREADS, std::max(64, (work + 31) / 32 * 32));
+    a.p_cu = a.p_back + a.B + 1;
     cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t e = launch_pdl(one ? block_map_kernel<true> : block_map_kernel<false>, dim3(1), threads, s, a);
-    if (e == cudaSuccess && !one) {
-        const int grid = std::min((a.room + 255) / 256, sms * 8);
-        e = launch_pdl(block_map_rows_kernel, dim3((unsigned)grid), 256, s, a);
+    cudaError_t e;
+    const bool in_place = held_lens == seq_lens || pool_in == pool_out;
+    if (a.B <= MAP_SMEM_SEQS && (a.room <= MAP_ONE_CTA_ROWS || !in_place)) {
+        // several CTAs: just threads for the sequences, since each makes the plan, and a row a thread
+        const bool one = a.room <= MAP_ONE_CTA_ROWS;
+        const int work = one ? std::max(a.B, a.room) : std::max(a.B, 256);
+        const int threads = std::min(MAP_THREADS, std::max(64, (work + 31) / 32 * 32));
+        const int grid = one ? 1 : std::min(2 * sms, (a.room + threads - 1) / threads);
+        e = launch_pdl(block_map_kernel<true, true>, dim3((unsigned)grid), threads, s, a);
+    } else if (a.room <= MAP_ONE_CTA_ROWS) {
+        e = launch_pdl(block_map_kernel<true, false>, dim3(1), MAP_THREADS, s, a);
+    } else {
+        e = launch_pdl(block_map_kernel<false, false>, dim3(1), MAP_THREADS, s, a);
+        if (e == cudaSuccess) {
+            const int grid = std::min((a.room + 255) / 256, sms * 8);
+            e = launch_pdl(block_map_rows_kernel, dim3((unsigned)grid), 256, s, a);
+        }
     }
     if (e != cudaSuccess) return cfail(FDPP_ERR_CUDA, "block map launch: %s", cudaGetErrorString(e));
     return FDPP_OK;

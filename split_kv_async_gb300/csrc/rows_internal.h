@@ -23,7 +23,7 @@ constexpr int ROWS_MAX_PARTS = 160;
 constexpr int ROWS_COUNTERS = 1024;
 // Heads of one kv head that a CTA of the CUDA-core kernel takes, and its splits at most.
 constexpr int ROWS_SIMT_HEADS = 4;
-constexpr int ROWS_SIMT_MAX_SPLITS = 32;
+constexpr int ROWS_SIMT_MAX_SPLITS = 64;
 
 // A token row: its position and the keys [lo, hi) it sees, prefix keys first; lo >= hi: none. rt: its
 // own row tile, -1: a row of no sequence.

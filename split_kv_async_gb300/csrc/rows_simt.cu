@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
     constexpr int E = NV * 4;
     __shared__ float sm_m[GROUPS][SH], sm_l[GROUPS][SH];
     __shared__ float sm_o[SW][SH][D];
+    __shared__ float sm_w[SH][ROWS_SIMT_MAX_SPLITS];
     __shared__ int last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = threadIdx.x / LANES, j = lane % LANES;
     const int chunks = (a.G + SH - 1) / SH;
@@ -209,17 +210,37 @@ __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
     __syncthreads();
     if (!last) return;
     __threadfence();
-    for (int h = 0; h < nh; ++h) {
-        const float2* ml = a.row_ml + slot0 + h * a.splits;
-        const float* po = a.row_o + (slot0 + h * a.splits) * D;
+    // a warp per head: the splits' maxima and sums over its lanes, their weights into shared memory
+    if (warp < nh) {
+        const float2* ml = a.row_ml + slot0 + warp * a.splits;
+        float2 x[ROWS_SIMT_MAX_SPLITS / 32];
         float M = -INFINITY, lt = 0.f;
-        for (int s = 0; s < a.splits; ++s) M = fmaxf(M, __ldcg(&ml[s].x));
-        for (int s = 0; s < a.splits; ++s) lt += __ldcg(&ml[s].y) * join_weight(__ldcg(&ml[s].x), M);
-        for (int d = threadIdx.x; d < D; d += SW * 32) {
-            float x = 0.f;
-            for (int s = 0; s < a.splits; ++s) x += __ldcg(po + (long long)s * D + d) * join_weight(__ldcg(&ml[s].x), M);
-            store_one(out + h * D + d, len == 0 ? 0.f : x / lt);
+#pragma unroll
+        for (int i = 0; i < ROWS_SIMT_MAX_SPLITS / 32; ++i) {
+            x[i] = lane + 32 * i < a.splits ? __ldcg(ml + lane + 32 * i) : make_float2(-INFINITY, 0.f);
+            M = fmaxf(M, x[i].x);
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll
+        for (int i = 0; i < ROWS_SIMT_MAX_SPLITS / 32; ++i) {
+            const float w = join_weight(x[i].x, M);
+            if (lane + 32 * i < a.splits) {
+                sm_w[warp][lane + 32 * i] = w;
+                lt += x[i].y * w;
+            }
+        }
+        lt = warp_sum(lt);
+        if (lane == 0) sm_l[0][warp] = lt;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < nh * D; i += SW * 32) {
+        const int h = i / D, d = i - h * D;
+        const float* po = a.row_o + (slot0 + h * a.splits) * D + d;
+        float x = 0.f;
+#pragma unroll 8
+        for (int s = 0; s < a.splits; ++s) x += __ldcg(po + (long long)s * D) * sm_w[h][s];
+        store_one(out + i, len == 0 ? 0.f : x / sm_l[0][h]);
     }
 }
 
