@@ -91,5 +91,18 @@ __device__ __forceinline__ float mod_score(float qk, float scale, float cap, flo
     return fmaf(-slope2, fabsf(dist), s);
 }
 
+// Two scores capped at once (top: log2(e) cap), with one reciprocal of the product of their denominators:
+// a reciprocal takes the MUFU twice as long as an exponential. The exponents are cut at 60, where the tanh
+// is 1 in fp32, so that the product stays finite; NaN stays NaN.
+__device__ __forceinline__ void cap_pair(float& x0, float& x1, float cap_rate, float top)
+{
+    float t0, t1;
+    asm("min.NaN.f32 %0, %1, 0f42700000;" : "=f"(t0) : "f"(x0 * cap_rate));
+    asm("min.NaN.f32 %0, %1, 0f42700000;" : "=f"(t1) : "f"(x1 * cap_rate));
+    const float e0 = ex2(t0) + 1.f, e1 = ex2(t1) + 1.f, r = rcp(e0 * e1);
+    x0 = fmaf(-2.f * top, r * e1, top);
+    x1 = fmaf(-2.f * top, r * e0, top);
+}
+
 }  // namespace
 }  // namespace fdpp

@@ -1188,6 +1188,40 @@ struct Softmax {
             tc_fence_after();
             if (warp_live) {
                 const int k0 = t * ROWS_KEYS;
+                // Scores that need more than the scale (and a bias that is linear in the key) become v first,
+                // masked ones -inf, back in tensor memory: a rolled loop, since code that few tiles need
+                // costs more to fetch than it saves.
+                const bool open = __all_sync(0xffffffffu, lo <= k0 && hi >= k0 + ROWS_KEYS);
+                const bool ready_v = MODE == MODE_PLAIN || (MODE == MODE_BIAS && linear && open);
+                if (!open || !ready_v) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t y[32];
+                        tmem_ld32_async(ts + 32 * c, y);
+                        tmem_wait_ld();
+                        reg_fence32(y);
+                        const int kc = k0 + 32 * c, c0 = lo - kc, c1 = hi - kc;
+                        const float d0 = (float)(kc - spos);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            // a masked score may be anything, and one that is NaN would take its neighbour along
+                            const bool in0 = i >= c0 && i < c1, in1 = i + 1 >= c0 && i + 1 < c1;
+                            float v0 = in0 ? __uint_as_float(y[i]) : 0.f, v1 = in1 ? __uint_as_float(y[i + 1]) : 0.f;
+                            if (MODE == MODE_CAP) {
+                                cap_pair(v0, v1, cap_rate, LOG2E * a.cap);
+                                v0 = fmaf(-slope, fabsf(d0 + (float)i), v0);
+                                v1 = fmaf(-slope, fabsf(d0 + (float)(i + 1)), v1);
+                            } else if (MODE == MODE_BIAS) {
+                                v0 = mod_score(v0, a.scale, 0.f, 0.f, slope, d0 + (float)i);
+                                v1 = mod_score(v1, a.scale, 0.f, 0.f, slope, d0 + (float)(i + 1));
+                            }
+                            y[i] = __float_as_uint(in0 ? v0 : -INFINITY);
+                            y[i + 1] = __float_as_uint(in1 ? v1 : -INFINITY);
+                        }
+                        tmem_st32(ts + 32 * c, y);
+                    }
+                    tmem_wait_st();
+                }
                 // all 128 scores at once: a load's latency is long while the other stream's MMAs use the
                 // tensor memory
                 uint32_t x[ROWS_KEYS];
@@ -1196,8 +1230,7 @@ struct Softmax {
                 tmem_wait_ld();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) reg_fence32(x + 32 * c);
-                // v, where it is more than the scale
-                if (MODE == MODE_BIAS && linear) {
+                if (MODE == MODE_BIAS && ready_v) {
                     const float b0 = slope * (float)(k0 - spos);
                     const uint64_t rate2 = pair2(rate, rate);
 #pragma unroll
@@ -1208,18 +1241,6 @@ struct Softmax {
                         x[i] = __float_as_uint(v0);
                         x[i + 1] = __float_as_uint(v1);
                     }
-                } else if (MODE != MODE_PLAIN) {
-                    const float d0 = (float)(k0 - spos);
-#pragma unroll
-                    for (int i = 0; i < ROWS_KEYS; ++i)
-                        x[i] = __float_as_uint(mod_score(__uint_as_float(x[i]), a.scale, MODE == MODE_CAP ? a.cap : 0.f,
-                                                         cap_rate, slope, d0 + (float)i));
-                }
-                if (!__all_sync(0xffffffffu, lo <= k0 && hi >= k0 + ROWS_KEYS)) {
-                    const int c0 = lo - k0, c1 = hi - k0;
-#pragma unroll
-                    for (int i = 0; i < ROWS_KEYS; ++i)
-                        if (i < c0 || i >= c1) x[i] = __float_as_uint(-INFINITY);
                 }
                 float top = max3(fmaxf(max32(x), max32(x + 32)), max32(x + 64), max32(x + 96));
                 if (MODE == MODE_PLAIN) top *= rate;
