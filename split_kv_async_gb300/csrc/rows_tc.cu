@@ -243,8 +243,25 @@ __device__ __forceinline__ void set_tiles(RowTileRec& r, int loA, int hiA, int l
 // The plan of calls with at most PLAN_SMALL sequences and row tiles: everything in shared memory, each
 // token looked at once. It is on every call's critical path, so it has few steps and little code (a kernel
 // starts with cold instruction caches): one row of loads per sequence, a scan, one pass over the tokens
-// that leaves the row tiles' key ranges in shared memory, a scan.
+// that leaves the row tiles' key ranges in shared memory, a scan. With more than 1024 tokens it is a
+// cluster of up to PLAN_CLUSTER CTAs that share out the tokens; the ranges gather in the first one's
+// shared memory (5 rounds of 1024 tokens took 16 us in one CTA).
 constexpr int PLAN_SMALL = 1024;
+constexpr int PLAN_CLUSTER = 8;
+
+__device__ __forceinline__ void cluster_meet()
+{
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// The first CTA's copy of a shared variable.
+template <typename T>
+__device__ __forceinline__ T* in_first(T* p)
+{
+    uint64_t q;
+    asm("mapa.u64 %0, %1, 0;" : "=l"(q) : "l"(p));
+    return reinterpret_cast<T*>(q);
+}
 
 // Inclusive scan of x over the CTA's 1024 threads, and the total.
 __device__ __forceinline__ int scan_1024(int x, int& total, int* red)
@@ -286,7 +303,7 @@ __global__ void __launch_bounds__(PLAN_SMALL) rows_plan_small_kernel(RowsArgs a)
     __shared__ int red[32];
     __shared__ int rt0[PLAN_SMALL + 1], c0[PLAN_SMALL], cnt[PLAN_SMALL], len[PLAN_SMALL];
     __shared__ int low[2][PLAN_SMALL], high[2][PLAN_SMALL];      // key ranges of the row tiles' halves; later: starts
-    const int t = threadIdx.x;
+    const int t = threadIdx.x, rank = blockIdx.x, ranks = gridDim.x;      // (the grid is one cluster)
     grid_dependency_wait();
     grid_launch_dependents();
     unsigned bad = 0;
@@ -310,21 +327,24 @@ __global__ void __launch_bounds__(PLAN_SMALL) rows_plan_small_kernel(RowsArgs a)
         cnt[t] = n;
         len[t] = L;
     }
-    __syncthreads();
+    if (ranks > 1) cluster_meet(); else __syncthreads();
+    int* const low0 = ranks > 1 ? in_first(&low[0][0]) : &low[0][0];
+    int* const high0 = ranks > 1 ? in_first(&high[0][0]) : &high[0][0];
     // the least and greatest key of each half of a row tile, one shared-memory operation for all the lanes
     // of a warp that belong to it
     auto widen = [&](int key, int from, int to) {
         const unsigned m = __match_any_sync(0xffffffffu, key);
         const int lo = __reduce_min_sync(m, from), hi = __reduce_max_sync(m, to);
         if (key >= 0 && (t & 31) == __ffs(m) - 1) {
-            atomicMin(&low[key & 1][key >> 1], lo);
-            atomicMax(&high[key & 1][key >> 1], hi);
+            atomicMin(low0 + (key & 1) * PLAN_SMALL + (key >> 1), lo);
+            atomicMax(high0 + (key & 1) * PLAN_SMALL + (key >> 1), hi);
         }
     };
     // key ranges are read a round ahead
-    int kb = a.key_begin && t < a.T ? a.key_begin[t] : 0, ke = a.key_end && t < a.T ? a.key_end[t] : 0;
-    for (int base = 0; base < a.T; base += PLAN_SMALL) {
-        const int row = base + t, after = row + PLAN_SMALL;
+    const int row0 = rank * PLAN_SMALL + t, step = ranks * PLAN_SMALL;
+    int kb = a.key_begin && row0 < a.T ? a.key_begin[row0] : 0, ke = a.key_end && row0 < a.T ? a.key_end[row0] : 0;
+    for (int base = rank * PLAN_SMALL; base < a.T; base += step) {
+        const int row = base + t, after = row + step;
         const int nb = a.key_begin && after < a.T ? a.key_begin[after] : 0;
         const int ne = a.key_end && after < a.T ? a.key_end[after] : 0;
         const int b = last_at_most(c0, a.B, row), i = row - c0[b], rt = rt0[b] + i / pair;
@@ -349,7 +369,9 @@ __global__ void __launch_bounds__(PLAN_SMALL) rows_plan_small_kernel(RowsArgs a)
         kb = nb;
         ke = ne;
     }
-    __syncthreads();
+    rows_error(a, bad);
+    if (ranks > 1) cluster_meet(); else __syncthreads();
+    if (rank) return;
     RowTileRec r{};
     if (t < nrt) {
         if (t < npre) {
@@ -381,7 +403,6 @@ __global__ void __launch_bounds__(PLAN_SMALL) rows_plan_small_kernel(RowsArgs a)
         a.plan[RP_TILES] = tiles;
         a.plan[RP_PREFIX] = P;
     }
-    rows_error(a, bad);
 }
 
 // The plan of larger calls.
@@ -1989,8 +2010,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) rows_join_prefix_kernel(RowsA
 
 struct PdlConfig {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    PdlConfig(dim3 grid, int threads, size_t smem, cudaStream_t s)
+    cudaLaunchAttribute attr[2];
+    PdlConfig(dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster = 1)
     {
         cfg.gridDim = grid;
         cfg.blockDim = dim3((unsigned)threads);
@@ -1998,8 +2019,11 @@ struct PdlConfig {
         cfg.stream = s;
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)cluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = cluster > 1 ? 2 : 1;
     }
 };
 
@@ -2007,7 +2031,8 @@ template <int D, int MODE>
 cudaError_t launch_d(const RowsArgs& a, const RowsMaps& m, cudaStream_t s)
 {
     const bool small = a.B <= PLAN_SMALL && a.max_rt <= PLAN_SMALL;
-    PdlConfig plan(dim3(1), small ? PLAN_SMALL : PLAN_THREADS, 0, s);
+    const int rounds = (a.T + PLAN_SMALL - 1) / PLAN_SMALL, ranks = !small || rounds == 1 ? 1 : (rounds < PLAN_CLUSTER ? rounds : PLAN_CLUSTER);
+    PdlConfig plan(dim3((unsigned)ranks), small ? PLAN_SMALL : PLAN_THREADS, 0, s, ranks);
     cudaError_t e = cudaLaunchKernelEx(&plan.cfg, small ? rows_plan_small_kernel : rows_plan_kernel, a);
     if (e != cudaSuccess) return e;
     auto kern = rows_tile_kernel<D, MODE>;
