@@ -13,12 +13,14 @@
 //            of one ring (128-byte swizzle). Blocks of 16 tokens take 16 loads per tile and operand: with
 //            one warp for both, issuing them took longer than HBM takes for the tile (438 us against 344
 //            for the contiguous cache, 64 sequences of 512 to 16384 keys, 8 kv heads, d = 128).
-//   warps 8, 9  issue the MMAs of streams 0 and 1 (one thread each): S = Q K^T (M = 128 rows, N = 128
-//            keys), and O += P V with P from tensor memory and V MN-major from the TMA-landed tile. A
-//            stream's P V of one tile is issued right before its next Q K^T, and while one stream's
-//            softmax runs the tensor cores work on the other's tile.
+//   warps 8, 9  issue the MMAs of streams 0 and 1 (one thread each): S = Q K^T (M = 128 rows, N = 64
+//            keys, half a tile), and O += P V with P from tensor memory and V MN-major from the
+//            TMA-landed tile. A stream has two score buffers: while the softmax works on one half, the
+//            tensor cores finish the other (its P V, then the next Q K^T into its place). With whole
+//            tiles P lay over the only scores, and a stream's softmax and MMAs took turns: 523 us for a
+//            prompt of 8192 tokens, although N = 64 runs at three quarters of the rate of N = 128.
 //   warps 0-3, 4-7   the softmax of streams 0 and 1: a thread owns a row (tensor-memory lane), reads its
-//            128 scores, and writes P as bf16 over them. P's rounding (2^-9 of each weight, independent)
+//            64 scores, and writes P as bf16 over them. P's rounding (2^-9 of each weight, independent)
 //            leaves an error of the order of the output's own rounding; l sums the unrounded weights.
 // With more than 128 rows a unit is a pair: two row tiles, one per stream, share every K/V tile. With
 // fewer, both streams take the same rows, alternate key tiles and are joined at the run's end.
@@ -54,9 +56,6 @@ namespace {
 constexpr int RW_MMA_WARP = 8;           // and the next: one per stream
 constexpr int RW_LOAD_WARP = 10;         // and the next: K (with the headers and Q), and V
 constexpr int RW_THREADS = 12 * 32;
-// Registers of a softmax warp and of the others: (2 x 200 + 104) x 128 = 64512, the 384 x 168 of the launch.
-constexpr int RW_SOFT_REGS = 200;
-constexpr int RW_HELP_REGS = 104;
 constexpr int RW_HDRS = 4;               // run headers in flight
 constexpr int RW_HDR_BYTES = 64;
 constexpr float RW_LAG = 8.f;            // log2 of the growth of a row's max that moves its frame
@@ -100,7 +99,7 @@ struct RowsSmem {
     int q, stages, turn, hdr, ml, bars, misc, tslot, nsh, total;
     __host__ __device__ explicit RowsSmem(int nst)
         : q(0), stages(2 * QB), turn(stages + nst * SB), hdr(turn + 8 * TURN), ml(hdr + RW_HDRS * RW_HDR_BYTES),
-          bars(ml + 2 * ROWS_TILE * 8), misc(bars + (2 * nst + 2 * (2 + NSLOTS) + 2 * RW_HDRS + 7 * 2 + 1) * 8),
+          bars(ml + 2 * ROWS_TILE * 8), misc(bars + (2 * nst + 2 * (2 + NSLOTS) + 2 * RW_HDRS + 2 * 4 + 5 * 2 + 1) * 8),
           tslot(misc + 64), nsh(NSH_IN_Q ? SLOTS_END : tslot + 16),
           total(tslot + 16 + (NSH_IN_Q ? 0 : (int)sizeof(NarrowShared)))
     {
@@ -113,8 +112,9 @@ struct RowsBars {
     uint32_t qfull, qempty;       // [2]
     uint32_t nqfull, nqempty;     // [4] the key-major runs' slots
     uint32_t hfull, hempty;       // [RW_HDRS] run headers: read by the V loader, the MMA and softmax warps
-    uint32_t sfull, pready;       // [2] scores written; weights written (128-row runs: of the first 64 keys,
-    uint32_t prest;               //     and the rest)
+    uint32_t sfull, pready;       // [2][2] scores written; weights written (per stream and score buffer: either
+                                  //     side may be one buffer ahead)
+    uint32_t pvdone;              // [2] the P V of 64 keys complete (128-row runs)
     uint32_t ofull, ofree;        // [2] accumulator complete; read out
     uint32_t mlfree;              // [2] a stream's maxima and sums have been read
     uint32_t vote;                // [2] the warps of a stream meet (key-major runs)
@@ -130,9 +130,9 @@ struct RowsBars {
         hfull = nqempty + 32;
         hempty = hfull + 8 * RW_HDRS;
         sfull = hempty + 8 * RW_HDRS;
-        pready = sfull + 16;
-        prest = pready + 16;
-        ofull = prest + 16;
+        pready = sfull + 32;
+        pvdone = pready + 32;
+        ofull = pvdone + 16;
         ofree = ofull + 16;
         mlfree = ofree + 16;
         vote = mlfree + 16;
@@ -825,76 +825,82 @@ struct RowsMma {
     uint32_t sbase, tmem;
     volatile int* misc;
     uint32_t S;                                  // the stream
-    // the tile whose P V is still to be issued (ncols: of a key-major run, else 0)
-    bool owes = false, pfirst = false, plast = false;
-    uint32_t pstage = 0, pphase = 0, pcols = 0;
-    uint32_t np = 0, nrest = 0, nacc = 0;        // P V issued (and those in two halves), runs begun
+    // P V still to be issued, the older first: of 64 keys each (cols = 0), or of a key-major run's tile
+    struct Owed {
+        uint32_t stage, phase, cols, half;       // half: of the tile's keys, 1 the upper
+        bool first, last, release;               // of its run's; the tile's last (its V goes back)
+    } o0, o1;
+    int owed = 0;
+    uint32_t np0 = 0, np1 = 0, nacc = 0;         // P V issued from either buffer, runs begun
 
-    // Waits until the P V that is owed can be issued.
-    __device__ __forceinline__ bool ready()
+    __device__ __forceinline__ void owe(uint32_t stage, uint32_t phase, uint32_t cols, uint32_t half, bool first, bool last,
+                                        bool release)
     {
-        if (!rwait(bars.kvfull + 8 * pstage, pphase, misc, a)) return false;
-        if (pfirst) {
+        const Owed o{stage, phase, cols, half, first, last, release};
+        if (owed == 0) o0 = o; else o1 = o;
+        ++owed;
+    }
+
+    // Issues the oldest P V that is owed.
+    __device__ __forceinline__ bool pay()
+    {
+        constexpr uint32_t IDESC = umma_idesc_bf16(128, D, false) | (1u << 16);     // V: MN-major B
+        if (!rwait(bars.kvfull + 8 * o0.stage, o0.phase, misc, a)) return false;
+        if (o0.first) {
             if (!rwait(bars.ofree + 8 * S, (nacc & 1u) ^ 1u, misc, a)) return false;
             ++nacc;
         }
-        if (!rwait(bars.pready + 8 * S, np & 1u, misc, a)) return false;
-        ++np;
-        return true;
-    }
-
-    __device__ __forceinline__ bool issue_pv()
-    {
-        constexpr uint32_t IDESC = umma_idesc_bf16(128, D, false) | (1u << 16);     // V: MN-major B
+        // the upper half's scores and weights lie in the first buffer, as a key-major run's do
+        const uint32_t buf = o0.cols == 0 && o0.half == 0 ? 1u : 0u;
+        if (!rwait(bars.pready + 16 * S + 8 * buf, buf ? np1 : np0, misc, a)) return false;
+        if (buf) ++np1; else ++np0;
         tc_fence_after();
         const bool lead = elect_one();
-        const uint32_t od = tmem + 2 * TM_S + S * D, more = pfirst ? 0u : 1u;
-        const uint32_t vd = sw128_mnmajor_lo(sbase + lay.stages + pstage * RowsSmem<D>::SB, RowsSmem<D>::HALF);
-        if (pcols == 0) {
-            // the first 64 keys' weights come before the others
-            const uint32_t pd = tmem + S * TM_S;
+        const uint32_t od = tmem + 2 * TM_S + S * D, more = o0.first ? 0u : 1u;
+        const uint32_t vd = sw128_mnmajor_lo(sbase + lay.stages + o0.stage * RowsSmem<D>::SB, RowsSmem<D>::HALF);
+        if (o0.cols == 0) {
+            const uint32_t pd = tmem + S * TM_S + 64 * buf, vh = vd + o0.half * (64 * 128 >> 4);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                umma_bf16_ta_lo(lead, od, pd + 8 * k, vd + k * (2048 >> 4), IDESC, k == 0 ? more : 1u);
-            if (!rwait(bars.prest + 8 * S, nrest & 1u, misc, a)) return false;
-            ++nrest;
-            tc_fence_after();
-#pragma unroll
-            for (int k = 4; k < 8; ++k) umma_bf16_ta_lo(lead, od, pd + 8 * k, vd + k * (2048 >> 4), IDESC, 1u);
+                umma_bf16_ta_lo(lead, od, pd + 8 * k, vh + k * (2048 >> 4), IDESC, k == 0 ? more : 1u);
+            umma_commit(lead, bars.pvdone + 8 * S);
         } else {
             // O^T += V^T P^T: d on M, the rows on N, 64 keys per half of P^T
-            const uint32_t idesc = umma_idesc_bf16(D, 16, true) + ((pcols - 16) >> 3 << 17);
+            const uint32_t idesc = umma_idesc_bf16(D, 16, true) + ((o0.cols - 16) >> 3 << 17);
             const uint32_t pd = sw128_kmajor_lo(sbase + lay.q + RowsSmem<D>::NP_OFF + S * RowsSmem<D>::NP);
 #pragma unroll
             for (int k = 0; k < ROWS_KEYS / 16; ++k)
                 umma_bf16_lo(lead, od, vd + k * (2048 >> 4), pd + (k >> 2) * (RowsSmem<D>::NQ_HALF >> 4) + (k & 3) * 2,
                              idesc, k == 0 ? more : 1u);
         }
-        umma_commit(lead, bars.kvempty + 8 * pstage);
-        if (plast) umma_commit(lead, bars.ofull + 8 * S);
+        if (o0.release) umma_commit(lead, bars.kvempty + 8 * o0.stage);
+        if (o0.last) umma_commit(lead, bars.ofull + 8 * S);
         __syncwarp();
-        owes = false;
+        o0 = o1;
+        --owed;
         return true;
     }
 
-    // Issues the P V that is owed.
+    // Issues all P V that are owed.
     __device__ __forceinline__ bool flush()
     {
-        if (!owes) return true;
-        return ready() && issue_pv();
+#pragma unroll 1
+        while (owed > 0)
+            if (!pay()) return false;
+        return true;
     }
 
-    // Waits for something the load warp brings. The P V that is owed goes first where it is not there yet:
-    // the load warp may itself be waiting for a run to end (its query slot, its stages).
+    // Waits for something the load warps bring. What is owed goes first where it is not there yet: the
+    // load warps may themselves be waiting for a run to end (its query slot, its stages).
     __device__ __forceinline__ bool await(uint32_t bar, uint32_t parity)
     {
-        if (owes && !__all_sync(0xffffffffu, mbar_test(bar, parity)) && !flush()) return false;
+        if (owed > 0 && !__all_sync(0xffffffffu, mbar_test(bar, parity)) && !flush()) return false;
         return rwait(bar, parity, misc, a);
     }
 
     __device__ __forceinline__ bool run(uint8_t* sm)
     {
-        constexpr uint32_t IDESC = umma_idesc_bf16(128, ROWS_KEYS, false);
+        constexpr uint32_t IDESC = umma_idesc_bf16(128, 64, false);
         const int lane = threadIdx.x & 31;
         const uint32_t sd = tmem + S * TM_S;
         uint32_t stage = 0, phase = 0, nq = 0, nqn = 0, nh = 0;
@@ -954,17 +960,31 @@ struct RowsMma {
                         fence_proxy_async_smem();
                         __syncwarp();
                     }
-                    if (!flush()) return false;
-                    tc_fence_after();
-                    const bool lead = elect_one();
                     const uint32_t kd = sw128_kmajor_lo(sbase + lay.stages + stage * RowsSmem<D>::SB);
                     if (ncols == 0) {
+#pragma unroll 1
+                        for (uint32_t o = 0; o < 2; ++o) {       // the upper 64 keys, then the lower
+                            if (owed == 2 && !pay()) return false;
+                            tc_fence_after();
+                            const bool lead = elect_one();
+                            const uint32_t kh = kd + (o ^ 1u) * (64 * 128 >> 4);
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t off = (uint32_t)(k >> 2) * (RowsSmem<D>::HALF >> 4) + (uint32_t)(k & 3) * 2u;
-                            umma_bf16_lo(lead, sd, qd + off, kd + off, IDESC, k > 0 ? 1u : 0u);
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t off = (uint32_t)(k >> 2) * (RowsSmem<D>::HALF >> 4) + (uint32_t)(k & 3) * 2u;
+                                umma_bf16_lo(lead, sd + 64 * o, qd + off, kh + off, IDESC, k > 0 ? 1u : 0u);
+                            }
+                            umma_commit(lead, bars.sfull + 16 * S + 8 * o);
+                            if (o == 1) {
+                                umma_commit(lead, bars.kvempty + 8 * stage);
+                                if (j == last) umma_commit(lead, qbar);
+                            }
+                            __syncwarp();
+                            owe(vstage, vphase, 0, o ^ 1u, j == j0 && o == 0, j == last && o == 1, o == 1);
                         }
                     } else {
+                        if (!flush()) return false;
+                        tc_fence_after();
+                        const bool lead = elect_one();
                         // S^T = K Q^T: the keys on M, the rows on N
                         const uint32_t idesc = umma_idesc_bf16(128, 16, false) + ((ncols - 16) >> 3 << 17);
 #pragma unroll
@@ -972,17 +992,11 @@ struct RowsMma {
                             umma_bf16_lo(lead, sd, kd + (uint32_t)(k >> 2) * (RowsSmem<D>::HALF >> 4) + (uint32_t)(k & 3) * 2u,
                                          qd + (uint32_t)(k >> 2) * (RowsSmem<D>::NQ_HALF >> 4) + (uint32_t)(k & 3) * 2u, idesc,
                                          k > 0 ? 1u : 0u);
+                        umma_commit(lead, bars.sfull + 16 * S);
+                        umma_commit(lead, bars.kvempty + 8 * stage);
+                        __syncwarp();
+                        owe(vstage, vphase, ncols, 0, j == j0, j == last, true);
                     }
-                    umma_commit(lead, bars.sfull + 8 * S);
-                    umma_commit(lead, bars.kvempty + 8 * stage);
-                    if (qbar && j == last) umma_commit(lead, qbar);
-                    __syncwarp();
-                    owes = true;
-                    pfirst = j == j0;
-                    plast = j == last;
-                    pstage = vstage;
-                    pphase = vphase;
-                    pcols = ncols;
                 } else {
                     // a tile of the other stream (or of neither): given back as far as this one goes
                     if (!flush()) return false;
@@ -1134,9 +1148,9 @@ struct Softmax {
     uint32_t tmem;
     volatile int* misc;
     int S;                   // the stream
-    // phases passed: headers, this stream's tiles, runs of either stream's accumulator, its own
+    // phases passed: headers, this stream's tiles, and the lower halves of those in 128-row runs, runs of either stream's accumulator, its own
     // hand-overs, meetings of this stream's warps, Q buffers
-    uint32_t nh = 0, ntile = 0, nacc = 0, nacc_o = 0, nml = 0, nvote = 0, nqn = 0;
+    uint32_t nh = 0, ntile = 0, nlow = 0, nacc = 0, nacc_o = 0, nml = 0, nvote = 0, nqn = 0;
 
     struct Run {
         int g, b, tok0, ntok, len, t0, t1, dest, flags, base, s0, s1;
@@ -1204,21 +1218,25 @@ struct Softmax {
         const bool linear = __all_sync(0xffffffffu, !mine || hi <= spos + 1);
         float m = -INFINITY, l = 0.f;                    // frame (log2 units) and sum
         int count = 0;
-        for (int t = first; t >= least; t -= step, ++ntile, ++count) {
-            if (!rwait(bars.sfull + 8 * S, ntile & 1u, misc, a)) return false;
+        for (int t = first; t >= least; t -= step) {
+#pragma unroll 1
+          for (int half = 1; half >= 0; --half, ++count) {
+            const uint32_t buf = half ? 0u : 1u;
+            if (!rwait(bars.sfull + 16 * S + 8 * buf, half ? ntile : nlow, misc, a)) return false;
             tc_fence_after();
             if (warp_live) {
-                const int k0 = t * ROWS_KEYS;
+                const int k0 = t * ROWS_KEYS + 64 * half;
+                const uint32_t tb = ts + 64 * buf;
                 // Scores that need more than the scale (and a bias that is linear in the key) become v first,
                 // masked ones -inf, back in tensor memory: a rolled loop, since code that few tiles need
                 // costs more to fetch than it saves.
-                const bool open = __all_sync(0xffffffffu, lo <= k0 && hi >= k0 + ROWS_KEYS);
+                const bool open = __all_sync(0xffffffffu, lo <= k0 && hi >= k0 + 64);
                 const bool ready_v = MODE == MODE_PLAIN || (MODE == MODE_BIAS && linear && open);
                 if (!open || !ready_v) {
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 2; ++c) {
                         uint32_t y[32];
-                        tmem_ld32_async(ts + 32 * c, y);
+                        tmem_ld32_async(tb + 32 * c, y);
                         tmem_wait_ld();
                         reg_fence32(y);
                         const int kc = k0 + 32 * c, c0 = lo - kc, c1 = hi - kc;
@@ -1239,23 +1257,21 @@ struct Softmax {
                             y[i] = __float_as_uint(in0 ? v0 : -INFINITY);
                             y[i + 1] = __float_as_uint(in1 ? v1 : -INFINITY);
                         }
-                        tmem_st32(ts + 32 * c, y);
+                        tmem_st32(tb + 32 * c, y);
                     }
                     tmem_wait_st();
                 }
-                // all 128 scores at once: a load's latency is long while the other stream's MMAs use the
-                // tensor memory
-                uint32_t x[ROWS_KEYS];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32_async(ts + 32 * c, x + 32 * c);
+                uint32_t x[64];
+                tmem_ld32_async(tb, x);
+                tmem_ld32_async(tb + 32, x + 32);
                 tmem_wait_ld();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) reg_fence32(x + 32 * c);
+                reg_fence32(x);
+                reg_fence32(x + 32);
                 if (MODE == MODE_BIAS && ready_v) {
                     const float b0 = slope * (float)(k0 - spos);
                     const uint64_t rate2 = pair2(rate, rate);
 #pragma unroll
-                    for (int i = 0; i < ROWS_KEYS; i += 2) {
+                    for (int i = 0; i < 64; i += 2) {
                         float v0, v1;
                         unpair2(fma2(pair2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), rate2,
                                      pair2(fmaf(slope, (float)i, b0), fmaf(slope, (float)(i + 1), b0))), v0, v1);
@@ -1263,13 +1279,15 @@ struct Softmax {
                         x[i + 1] = __float_as_uint(v1);
                     }
                 }
-                float top = max3(fmaxf(max32(x), max32(x + 32)), max32(x + 64), max32(x + 96));
+                float top = fmaxf(max32(x), max32(x + 32));
                 if (MODE == MODE_PLAIN) top *= rate;
                 if (count == 0) {
                     m = top;
                 } else if (__any_sync(0xffffffffu, top > (m == -INFINITY ? -INFINITY : m + RW_LAG))) {
-                    // move the frame: the accumulator's P V of the tile before has completed (the scores'
-                    // barrier counts every MMA issued before them)
+                    // move the frame, once the P V of the half before is complete (those before it are: the
+                    // scores' barrier counts every MMA issued before them)
+                    if (!rwait(bars.pvdone + 8 * S, half ? 1u : 0u, misc, a)) return false;
+                    tc_fence_after();
                     const float f = fmaxf(m, top), wt = m == f ? 1.f : ex2(m - f);
                     m = f;
                     l *= wt;
@@ -1284,13 +1302,12 @@ struct Softmax {
                         tmem_st16(to + S * D + i, o);
                     }
                 }
-                // The weights, two to a register. The first 64 keys' go to the MMA warp while the last ones
-                // are still computed; the wait for their stores comes after the third quarter's arithmetic.
+                // the weights, two to a register
                 const float mu = m == -INFINITY ? 0.f : m;
                 const uint64_t nmu = pair2(-mu, -mu), rate2 = pair2(rate, rate);
                 uint64_t s0 = pair2(0.f, 0.f), s1 = s0;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
                     uint32_t* y = x + 32 * c;
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
@@ -1307,24 +1324,18 @@ struct Softmax {
                         y[i / 2] = pack_bf16x2(p0, p1);
                         y[i / 2 + 1] = pack_bf16x2(p2, p3);
                     }
-                    if (c == 2) {
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bars.pready + 8 * S);
-                    }
-                    tmem_st16(ts + 16 * c, y);
+                    tmem_st16(tb + 16 * c, y);
                 }
                 float p0, p1;
                 unpair2(add2(s0, s1), p0, p1);
                 l += p0 + p1;
                 tmem_wait_st();
-            } else if (lane == 0) {
-                mbar_arrive(bars.pready + 8 * S);
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bars.prest + 8 * S);
+            if (lane == 0) mbar_arrive(bars.pready + 16 * S + 8 * buf);
+            if (half) ++ntile; else ++nlow;
+          }
         }
 
         // ---- the run's end ----
@@ -1548,7 +1559,7 @@ struct Softmax {
         const float cap_rate = MODE == MODE_CAP ? 2.f * LOG2E * a.scale / a.cap : 0.f;
         int count = 0;
         for (int t = run.t1 - 1 - (S ^ start); t >= run.t0; t -= 2, ++ntile, ++count) {
-            if (!rwait(bars.sfull + 8 * S, ntile & 1u, misc, a)) return false;
+            if (!rwait(bars.sfull + 16 * S, ntile, misc, a)) return false;
             tc_fence_after();
             const int k0 = t * ROWS_KEYS, key = k0 + 32 * w + lane;
             const bool open = all_lo <= k0 && all_hi >= k0 + ROWS_KEYS;
@@ -1650,7 +1661,7 @@ struct Softmax {
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bars.pready + 8 * S);
+            if (lane == 0) mbar_arrive(bars.pready + 16 * S);
         }
 
         // ---- the run's end ----
@@ -1805,9 +1816,11 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(bars.qfull + 8 * i, 1);
             mbar_init(bars.qempty + 8 * i, 2);       // both streams
-            mbar_init(bars.sfull + 8 * i, 1);
-            mbar_init(bars.pready + 8 * i, 4);
-            mbar_init(bars.prest + 8 * i, 4);
+            for (int k = 0; k < 2; ++k) {
+                mbar_init(bars.sfull + 16 * i + 8 * k, 1);
+                mbar_init(bars.pready + 16 * i + 8 * k, 4);
+            }
+            mbar_init(bars.pvdone + 8 * i, 1);
             mbar_init(bars.ofull + 8 * i, 1);
             mbar_init(bars.ofree + 8 * i, 4);
             mbar_init(bars.mlfree + 8 * i, 4);
@@ -1837,7 +1850,6 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
     grid_dependency_wait();
     grid_launch_dependents();
     if (warp >= RW_MMA_WARP) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RW_HELP_REGS));
         if (warp >= RW_LOAD_WARP) {
             RowsLoader<D> ld{a, lay, bars, sm, sbase, misc};
             if (warp == RW_LOAD_WARP) {
@@ -1856,7 +1868,6 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(RW_SOFT_REGS));
         Softmax<D, MODE> sx{a, lay, bars, sm, tmem, misc, warp >> 2};
         sx.run();
         tc_fence_before();
