@@ -6,19 +6,19 @@
 // more than 2^8 since it was set (until then the weights stay below 2^8, and the sums are exact in
 // the same frame), so that the accumulator is hardly ever rescaled.
 //
-// How. One CTA per SM, twelve warps, two streams:
-//   warps 10, 11  load: the first walks this CTA's part of the key tiles (128 keys each), writes a header
+// How. One CTA per SM, fourteen warps, two streams:
+//   warps 12, 13  load: the first walks this CTA's part of the key tiles (128 keys each), writes a header
 //            for each run (the part's share of one unit = (row tile, kv head)) and brings Q, by one 3-D
 //            TMA load per 64 of d, and the K tiles; the second brings the V tiles, into the other stages
 //            of one ring (128-byte swizzle). Blocks of 16 tokens take 16 loads per tile and operand: with
 //            one warp for both, issuing them took longer than HBM takes for the tile (438 us against 344
 //            for the contiguous cache, 64 sequences of 512 to 16384 keys, 8 kv heads, d = 128).
-//   warps 8, 9  issue the MMAs of streams 0 and 1 (one thread each): S = Q K^T (M = 128 rows, N = 64
-//            keys, half a tile), and O += P V with P from tensor memory and V MN-major from the
-//            TMA-landed tile. A stream has two score buffers: while the softmax works on one half, the
-//            tensor cores finish the other (its P V, then the next Q K^T into its place). With whole
-//            tiles P lay over the only scores, and a stream's softmax and MMAs took turns: 523 us for a
-//            prompt of 8192 tokens, although N = 64 runs at three quarters of the rate of N = 128.
+//   warps 8, 9   issue Q K^T of streams 0 and 1 (one thread each): S, M = 128 rows, N = 64 keys, half a tile;
+//   warps 10, 11 issue P V: O += P V with P from tensor memory and V MN-major from the TMA-landed tile. A
+//            stream has two score buffers: while the softmax works on one half, the tensor cores finish
+//            the other (its P V, then the next Q K^T into its place). With whole tiles P lay over the only
+//            scores, and a stream's softmax and MMAs took turns; and with one warp for both products its
+//            own instructions, between those of two busy softmax warps, set the pace.
 //   warps 0-3, 4-7   the softmax of streams 0 and 1: a thread owns a row (tensor-memory lane), reads its
 //            64 scores, and writes P as bf16 over them. P's rounding (2^-9 of each weight, independent)
 //            leaves an error of the order of the output's own rounding; l sums the unrounded weights.
@@ -53,9 +53,12 @@
 namespace fdpp {
 namespace {
 
-constexpr int RW_MMA_WARP = 8;           // and the next: one per stream
-constexpr int RW_LOAD_WARP = 10;         // and the next: K (with the headers and Q), and V
-constexpr int RW_THREADS = 12 * 32;
+constexpr int RW_MMA_WARP = 8;           // Q K^T of either stream, then P V of either
+constexpr int RW_LOAD_WARP = 12;         // K (with the headers and Q), and V
+constexpr int RW_THREADS = 16 * 32;      // the last two warps idle: register shares go by four warps
+// Registers of a softmax warp and of the others: 2 x (176 + 80) x 128 = 65536 = 512 x 128, the launch's.
+constexpr int RW_SOFT_REGS = 176;
+constexpr int RW_HELP_REGS = 80;
 constexpr int RW_HDRS = 4;               // run headers in flight
 constexpr int RW_HDR_BYTES = 64;
 constexpr float RW_LAG = 8.f;            // log2 of the growth of a row's max that moves its frame
@@ -99,7 +102,7 @@ struct RowsSmem {
     int q, stages, turn, hdr, ml, bars, misc, tslot, nsh, total;
     __host__ __device__ explicit RowsSmem(int nst)
         : q(0), stages(2 * QB), turn(stages + nst * SB), hdr(turn + 8 * TURN), ml(hdr + RW_HDRS * RW_HDR_BYTES),
-          bars(ml + 2 * ROWS_TILE * 8), misc(bars + (2 * nst + 2 * (2 + NSLOTS) + 2 * RW_HDRS + 2 * 4 + 5 * 2 + 1) * 8),
+          bars(ml + 2 * ROWS_TILE * 8), misc(bars + (2 * nst + 2 * (2 + NSLOTS) + 2 * RW_HDRS + 3 * 4 + 4 * 2 + 1) * 8),
           tslot(misc + 64), nsh(NSH_IN_Q ? SLOTS_END : tslot + 16),
           total(tslot + 16 + (NSH_IN_Q ? 0 : (int)sizeof(NarrowShared)))
     {
@@ -111,10 +114,10 @@ struct RowsBars {
     uint32_t kvfull, kvempty;     // [stages]
     uint32_t qfull, qempty;       // [2]
     uint32_t nqfull, nqempty;     // [4] the key-major runs' slots
-    uint32_t hfull, hempty;       // [RW_HDRS] run headers: read by the V loader, the MMA and softmax warps
+    uint32_t hfull, hempty;       // [RW_HDRS] run headers: read by the V loader, the MMA and the softmax warps
     uint32_t sfull, pready;       // [2][2] scores written; weights written (per stream and score buffer: either
                                   //     side may be one buffer ahead)
-    uint32_t pvdone;              // [2] the P V of 64 keys complete (128-row runs)
+    uint32_t pvdone;              // [2][2] the P V complete: the buffer is free
     uint32_t ofull, ofree;        // [2] accumulator complete; read out
     uint32_t mlfree;              // [2] a stream's maxima and sums have been read
     uint32_t vote;                // [2] the warps of a stream meet (key-major runs)
@@ -132,7 +135,7 @@ struct RowsBars {
         sfull = hempty + 8 * RW_HDRS;
         pready = sfull + 32;
         pvdone = pready + 32;
-        ofull = pvdone + 16;
+        ofull = pvdone + 32;
         ofree = ofull + 16;
         mlfree = ofree + 16;
         vote = mlfree + 16;
@@ -157,20 +160,6 @@ __device__ __forceinline__ bool rwait(uint32_t bar, uint32_t parity, volatile in
 {
     if (__builtin_expect(__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u)), 1)) return true;
     return rwait_slow(bar, parity & 1u, misc, a.err);
-}
-
-// Whether the phase of `parity` has completed (no waiting).
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
 }
 
 // First tile of part c of the `total` tiles.
@@ -817,122 +806,67 @@ __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, 
 
 __device__ __forceinline__ uint32_t narrow_cols(int rows) { return rows <= 16 ? 16u : 32u; }
 
+// What the MMA warps take from a run's header: whose tiles are theirs, counted from the run's last.
+struct MmaRun {
+    int kind, len, t1, n, j0, j1, last;
+    bool pair;
+    uint32_t ncols;                              // of a key-major run, else 0
+
+    __device__ __forceinline__ void read(const int* h, uint32_t S, int G)
+    {
+        kind = uniform(h[RH_KIND]);
+        len = uniform(h[RH_LEN]);
+        const int flags = uniform(h[RH_FLAGS]), t0 = uniform(h[RH_T0]);
+        t1 = uniform(h[RH_T1]);
+        const int s0 = uniform(S ? h[RH_B0] : h[RH_A0]), s1 = uniform(S ? h[RH_B1] : h[RH_A1]);
+        ncols = (flags & RF_NARROW) ? narrow_cols(uniform(h[RH_NTOK]) * G) : 0u;
+        pair = flags & RF_PAIR;
+        const uint32_t start = (flags & RF_START) ? 1u : 0u;
+        n = t1 - t0;
+        j0 = pair ? t1 - s1 : (int)(S ^ start);
+        j1 = pair ? t1 - s0 : n;
+        last = j0 >= j1 ? -1 : (pair ? j1 - 1 : j1 - 1 - ((j1 - 1 - j0) & 1));
+    }
+    __device__ __forceinline__ bool mine(int j) const { return j >= j0 && j < j1 && (pair || ((uint32_t)(j - j0) & 1u) == 0u); }
+};
+
+// Q K^T of stream S: every half tile (a key-major run: tile) as soon as its keys are there and its score
+// buffer is free.
 template <int D>
-struct RowsMma {
+struct RowsQk {
     const RowsArgs& a;
     const RowsSmem<D>& lay;
     const RowsBars& bars;
     uint32_t sbase, tmem;
     volatile int* misc;
-    uint32_t S;                                  // the stream
-    // P V still to be issued, the older first: of 64 keys each (cols = 0), or of a key-major run's tile
-    struct Owed {
-        uint32_t stage, phase, cols, half;       // half: of the tile's keys, 1 the upper
-        bool first, last, release;               // of its run's; the tile's last (its V goes back)
-    } o0, o1;
-    int owed = 0;
-    uint32_t np0 = 0, np1 = 0, nacc = 0;         // P V issued from either buffer, runs begun
-
-    __device__ __forceinline__ void owe(uint32_t stage, uint32_t phase, uint32_t cols, uint32_t half, bool first, bool last,
-                                        bool release)
-    {
-        const Owed o{stage, phase, cols, half, first, last, release};
-        if (owed == 0) o0 = o; else o1 = o;
-        ++owed;
-    }
-
-    // Issues the oldest P V that is owed.
-    __device__ __forceinline__ bool pay()
-    {
-        constexpr uint32_t IDESC = umma_idesc_bf16(128, D, false) | (1u << 16);     // V: MN-major B
-        if (!rwait(bars.kvfull + 8 * o0.stage, o0.phase, misc, a)) return false;
-        if (o0.first) {
-            if (!rwait(bars.ofree + 8 * S, (nacc & 1u) ^ 1u, misc, a)) return false;
-            ++nacc;
-        }
-        // the upper half's scores and weights lie in the first buffer, as a key-major run's do
-        const uint32_t buf = o0.cols == 0 && o0.half == 0 ? 1u : 0u;
-        if (!rwait(bars.pready + 16 * S + 8 * buf, buf ? np1 : np0, misc, a)) return false;
-        if (buf) ++np1; else ++np0;
-        tc_fence_after();
-        const bool lead = elect_one();
-        const uint32_t od = tmem + 2 * TM_S + S * D, more = o0.first ? 0u : 1u;
-        const uint32_t vd = sw128_mnmajor_lo(sbase + lay.stages + o0.stage * RowsSmem<D>::SB, RowsSmem<D>::HALF);
-        if (o0.cols == 0) {
-            const uint32_t pd = tmem + S * TM_S + 64 * buf, vh = vd + o0.half * (64 * 128 >> 4);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                umma_bf16_ta_lo(lead, od, pd + 8 * k, vh + k * (2048 >> 4), IDESC, k == 0 ? more : 1u);
-            umma_commit(lead, bars.pvdone + 8 * S);
-        } else {
-            // O^T += V^T P^T: d on M, the rows on N, 64 keys per half of P^T
-            const uint32_t idesc = umma_idesc_bf16(D, 16, true) + ((o0.cols - 16) >> 3 << 17);
-            const uint32_t pd = sw128_kmajor_lo(sbase + lay.q + RowsSmem<D>::NP_OFF + S * RowsSmem<D>::NP);
-#pragma unroll
-            for (int k = 0; k < ROWS_KEYS / 16; ++k)
-                umma_bf16_lo(lead, od, vd + k * (2048 >> 4), pd + (k >> 2) * (RowsSmem<D>::NQ_HALF >> 4) + (k & 3) * 2,
-                             idesc, k == 0 ? more : 1u);
-        }
-        if (o0.release) umma_commit(lead, bars.kvempty + 8 * o0.stage);
-        if (o0.last) umma_commit(lead, bars.ofull + 8 * S);
-        __syncwarp();
-        o0 = o1;
-        --owed;
-        return true;
-    }
-
-    // Issues all P V that are owed.
-    __device__ __forceinline__ bool flush()
-    {
-#pragma unroll 1
-        while (owed > 0)
-            if (!pay()) return false;
-        return true;
-    }
-
-    // Waits for something the load warps bring. What is owed goes first where it is not there yet: the
-    // load warps may themselves be waiting for a run to end (its query slot, its stages).
-    __device__ __forceinline__ bool await(uint32_t bar, uint32_t parity)
-    {
-        if (owed > 0 && !__all_sync(0xffffffffu, mbar_test(bar, parity)) && !flush()) return false;
-        return rwait(bar, parity, misc, a);
-    }
+    uint32_t S;
 
     __device__ __forceinline__ bool run(uint8_t* sm)
     {
         constexpr uint32_t IDESC = umma_idesc_bf16(128, 64, false);
         const int lane = threadIdx.x & 31;
         const uint32_t sd = tmem + S * TM_S;
-        uint32_t stage = 0, phase = 0, nq = 0, nqn = 0, nh = 0;
-        for (;; ++nh) {
+        uint32_t stage = 0, phase = 0, nq = 0, nqn = 0, use0 = 0, use1 = 0;
+        for (uint32_t nh = 0;; ++nh) {
             const uint32_t hs = nh % RW_HDRS;
-            if (!await(bars.hfull + 8 * hs, (nh / RW_HDRS) & 1u)) return false;
-            const int* h = reinterpret_cast<const int*>(sm + lay.hdr + hs * RW_HDR_BYTES);
-            const int kind = uniform(h[RH_KIND]), len = uniform(h[RH_LEN]), flags = uniform(h[RH_FLAGS]);
-            const int t0 = uniform(h[RH_T0]), t1 = uniform(h[RH_T1]);
-            const int s0 = uniform(S ? h[RH_B0] : h[RH_A0]), s1 = uniform(S ? h[RH_B1] : h[RH_A1]);
-            const uint32_t ncols = (flags & RF_NARROW) ? narrow_cols(uniform(h[RH_NTOK]) * a.G) : 0u;
+            if (!rwait(bars.hfull + 8 * hs, (nh / RW_HDRS) & 1u, misc, a)) return false;
+            MmaRun r;
+            r.read(reinterpret_cast<const int*>(sm + lay.hdr + hs * RW_HDR_BYTES), S, a.G);
             __syncwarp();
             if (lane == 0) mbar_arrive(bars.hempty + 8 * hs);
-            if (kind == RUN_END) break;
-            const bool pair = flags & RF_PAIR;
-            const uint32_t start = (flags & RF_START) ? 1u : 0u;
-            // this stream's tiles, counted from the run's last: a pair's from j0 to j1, else every second one
-            const int n = t1 - t0, j0 = pair ? t1 - s1 : (int)(S ^ start), j1 = pair ? t1 - s0 : n;
-            const bool any = j0 < j1;
-            const int last = pair ? j1 - 1 : j1 - 1 - ((j1 - 1 - j0) & 1);
+            if (r.kind == RUN_END) return true;
             // Q: of a pair, the buffer that is not this stream's goes back at once, as one without tiles does
             uint32_t qd = 0, qbar = 0;
-            if (ncols) {
+            if (r.ncols) {
                 const uint32_t i = nqn & 3u;
-                if (!await(bars.nqfull + 8 * i, (nqn >> 2) & 1u)) return false;
+                if (!rwait(bars.nqfull + 8 * i, (nqn >> 2) & 1u, misc, a)) return false;
                 qd = sw128_kmajor_lo(sbase + lay.q + RowsSmem<D>::slot(i));
                 ++nqn;
             } else {
-                for (uint32_t k = 0; k < (pair ? 2u : 1u); ++k, ++nq) {
+                for (uint32_t k = 0; k < (r.pair ? 2u : 1u); ++k, ++nq) {
                     const uint32_t qb = nq & 1u;
-                    if (!await(bars.qfull + 8 * qb, (nq >> 1) & 1u)) return false;
-                    if (any && (!pair || k == S)) {
+                    if (!rwait(bars.qfull + 8 * qb, (nq >> 1) & 1u, misc, a)) return false;
+                    if (r.last >= 0 && (!r.pair || k == S)) {
                         qd = sw128_kmajor_lo(sbase + lay.q + qb * RowsSmem<D>::QB);
                         qbar = bars.qempty + 8 * qb;
                     } else if (lane == 0) {
@@ -940,31 +874,16 @@ struct RowsMma {
                     }
                 }
             }
-            for (int j = 0; j < n; ++j) {
-                const int t = t1 - 1 - j;
-                uint32_t vstage = stage + 1, vphase = phase;
-                if (vstage == (uint32_t)a.stages) { vstage = 0; vphase ^= 1u; }
-                const bool mine = j >= j0 && j < j1 && (pair || ((uint32_t)(j - j0) & 1u) == 0u);
-                if (mine) {
-                    if (!await(bars.kvfull + 8 * stage, phase)) return false;
-                    const int nv = len - t * ROWS_KEYS;
-                    if (nv < ROWS_KEYS) {          // V past the source's end: zeros
-                        if (!rwait(bars.kvfull + 8 * vstage, vphase, misc, a)) return false;
-                        uint8_t* v = sm + lay.stages + vstage * RowsSmem<D>::SB;
-                        const int chunks = (ROWS_KEYS - nv) * 8;
-                        for (int i = lane; i < chunks * (D / 64); i += 32) {
-                            const int half = i / chunks, x = i - half * chunks;
-                            *reinterpret_cast<uint4*>(v + half * RowsSmem<D>::HALF + nv * 128 + x * 16) =
-                                make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
+            for (int j = 0; j < r.n; ++j) {
+                if (!rwait(bars.kvfull + 8 * stage, phase, misc, a)) return false;
+                if (!r.mine(j)) {                  // a tile of the other stream, or of neither
+                    if (lane == 0) mbar_arrive(bars.kvempty + 8 * stage);
+                } else {
                     const uint32_t kd = sw128_kmajor_lo(sbase + lay.stages + stage * RowsSmem<D>::SB);
-                    if (ncols == 0) {
+                    if (r.ncols == 0) {
 #pragma unroll 1
                         for (uint32_t o = 0; o < 2; ++o) {       // the upper 64 keys, then the lower
-                            if (owed == 2 && !pay()) return false;
+                            if (!rwait(bars.pvdone + 16 * S + 8 * o, (o ? use1 : use0) ^ 1u, misc, a)) return false;
                             tc_fence_after();
                             const bool lead = elect_one();
                             const uint32_t kh = kd + (o ^ 1u) * (64 * 128 >> 4);
@@ -976,17 +895,17 @@ struct RowsMma {
                             umma_commit(lead, bars.sfull + 16 * S + 8 * o);
                             if (o == 1) {
                                 umma_commit(lead, bars.kvempty + 8 * stage);
-                                if (j == last) umma_commit(lead, qbar);
+                                if (j == r.last) umma_commit(lead, qbar);
                             }
                             __syncwarp();
-                            owe(vstage, vphase, 0, o ^ 1u, j == j0 && o == 0, j == last && o == 1, o == 1);
                         }
+                        ++use1;
                     } else {
-                        if (!flush()) return false;
+                        if (!rwait(bars.pvdone + 16 * S, use0 ^ 1u, misc, a)) return false;
                         tc_fence_after();
                         const bool lead = elect_one();
                         // S^T = K Q^T: the keys on M, the rows on N
-                        const uint32_t idesc = umma_idesc_bf16(128, 16, false) + ((ncols - 16) >> 3 << 17);
+                        const uint32_t idesc = umma_idesc_bf16(128, 16, false) + ((r.ncols - 16) >> 3 << 17);
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
                             umma_bf16_lo(lead, sd, kd + (uint32_t)(k >> 2) * (RowsSmem<D>::HALF >> 4) + (uint32_t)(k & 3) * 2u,
@@ -995,22 +914,104 @@ struct RowsMma {
                         umma_commit(lead, bars.sfull + 16 * S);
                         umma_commit(lead, bars.kvempty + 8 * stage);
                         __syncwarp();
-                        owe(vstage, vphase, ncols, 0, j == j0, j == last, true);
                     }
-                } else {
-                    // a tile of the other stream (or of neither): given back as far as this one goes
-                    if (!flush()) return false;
-                    if (!rwait(bars.kvfull + 8 * stage, phase, misc, a)) return false;
-                    if (lane == 0) mbar_arrive(bars.kvempty + 8 * stage);
-                    if (!rwait(bars.kvfull + 8 * vstage, vphase, misc, a)) return false;
-                    if (lane == 0) mbar_arrive(bars.kvempty + 8 * vstage);
+                    ++use0;
                 }
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    if (++stage == (uint32_t)a.stages) { stage = 0; phase ^= 1u; }
+                stage += 2;
+                if (stage == (uint32_t)a.stages) { stage = 0; phase ^= 1u; }
             }
         }
-        return flush();
+    }
+};
+
+// P V of stream S: as soon as the weights are there.
+template <int D>
+struct RowsPv {
+    const RowsArgs& a;
+    const RowsSmem<D>& lay;
+    const RowsBars& bars;
+    uint32_t sbase, tmem;
+    volatile int* misc;
+    uint32_t S;
+
+    __device__ __forceinline__ bool run(uint8_t* sm)
+    {
+        constexpr uint32_t IDESC = umma_idesc_bf16(128, D, false) | (1u << 16);     // V: MN-major B
+        const int lane = threadIdx.x & 31;
+        const uint32_t od = tmem + 2 * TM_S + S * D;
+        uint32_t stage = 1, phase = 0, use0 = 0, use1 = 0, nacc = 0;
+        for (uint32_t nh = 0;; ++nh) {
+            const uint32_t hs = nh % RW_HDRS;
+            if (!rwait(bars.hfull + 8 * hs, (nh / RW_HDRS) & 1u, misc, a)) return false;
+            MmaRun r;
+            r.read(reinterpret_cast<const int*>(sm + lay.hdr + hs * RW_HDR_BYTES), S, a.G);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.hempty + 8 * hs);
+            if (r.kind == RUN_END) return true;
+            for (int j = 0; j < r.n; ++j) {
+                if (!rwait(bars.kvfull + 8 * stage, phase, misc, a)) return false;
+                if (!r.mine(j)) {
+                    if (lane == 0) mbar_arrive(bars.kvempty + 8 * stage);
+                } else {
+                    const int nv = r.len - (r.t1 - 1 - j) * ROWS_KEYS;
+                    if (nv < ROWS_KEYS) {          // V past the source's end: zeros
+                        uint8_t* v = sm + lay.stages + stage * RowsSmem<D>::SB;
+                        const int chunks = (ROWS_KEYS - nv) * 8;
+                        for (int i = lane; i < chunks * (D / 64); i += 32) {
+                            const int half = i / chunks, x = i - half * chunks;
+                            *reinterpret_cast<uint4*>(v + half * RowsSmem<D>::HALF + nv * 128 + x * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (j == r.j0) {               // the run's first: the accumulator has been read out
+                        if (!rwait(bars.ofree + 8 * S, (nacc & 1u) ^ 1u, misc, a)) return false;
+                        ++nacc;
+                    }
+                    const uint32_t vd = sw128_mnmajor_lo(sbase + lay.stages + stage * RowsSmem<D>::SB, RowsSmem<D>::HALF);
+                    uint32_t more = j == r.j0 ? 0u : 1u;
+                    if (r.ncols == 0) {
+#pragma unroll 1
+                        for (uint32_t o = 0; o < 2; ++o) {       // the upper 64 keys, then the lower
+                            if (!rwait(bars.pready + 16 * S + 8 * o, o ? use1 : use0, misc, a)) return false;
+                            tc_fence_after();
+                            const bool lead = elect_one();
+                            const uint32_t pd = tmem + S * TM_S + 64 * o, vh = vd + (o ^ 1u) * (64 * 128 >> 4);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                umma_bf16_ta_lo(lead, od, pd + 8 * k, vh + k * (2048 >> 4), IDESC, k == 0 ? more : 1u);
+                            umma_commit(lead, bars.pvdone + 16 * S + 8 * o);
+                            if (o == 1) {
+                                umma_commit(lead, bars.kvempty + 8 * stage);
+                                if (j == r.last) umma_commit(lead, bars.ofull + 8 * S);
+                            }
+                            more = 1u;
+                            __syncwarp();
+                        }
+                        ++use1;
+                    } else {
+                        if (!rwait(bars.pready + 16 * S, use0, misc, a)) return false;
+                        tc_fence_after();
+                        const bool lead = elect_one();
+                        // O^T += V^T P^T: d on M, the rows on N, 64 keys per half of P^T
+                        const uint32_t idesc = umma_idesc_bf16(D, 16, true) + ((r.ncols - 16) >> 3 << 17);
+                        const uint32_t pd = sw128_kmajor_lo(sbase + lay.q + RowsSmem<D>::NP_OFF + S * RowsSmem<D>::NP);
+#pragma unroll
+                        for (int k = 0; k < ROWS_KEYS / 16; ++k)
+                            umma_bf16_lo(lead, od, vd + k * (2048 >> 4),
+                                         pd + (k >> 2) * (RowsSmem<D>::NQ_HALF >> 4) + (k & 3) * 2, idesc, k == 0 ? more : 1u);
+                        umma_commit(lead, bars.pvdone + 16 * S);
+                        umma_commit(lead, bars.kvempty + 8 * stage);
+                        if (j == r.last) umma_commit(lead, bars.ofull + 8 * S);
+                        __syncwarp();
+                    }
+                    ++use0;
+                }
+                stage += 2;
+                if (stage >= (uint32_t)a.stages) { stage -= (uint32_t)a.stages; phase ^= 1u; }
+            }
+        }
     }
 };
 
@@ -1284,9 +1285,9 @@ struct Softmax {
                 if (count == 0) {
                     m = top;
                 } else if (__any_sync(0xffffffffu, top > (m == -INFINITY ? -INFINITY : m + RW_LAG))) {
-                    // move the frame, once the P V of the half before is complete (those before it are: the
-                    // scores' barrier counts every MMA issued before them)
-                    if (!rwait(bars.pvdone + 8 * S, half ? 1u : 0u, misc, a)) return false;
+                    // move the frame, once the P V of the half before is complete (the one before that is: its
+                    // buffer has held these scores since)
+                    if (!rwait(bars.pvdone + 16 * S + 8 * (buf ^ 1u), (half ? nlow : ntile) - 1u, misc, a)) return false;
                     tc_fence_after();
                     const float f = fmaxf(m, top), wt = m == f ? 1.f : ex2(m - f);
                     m = f;
@@ -1811,7 +1812,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
         }
         for (int i = 0; i < RW_HDRS; ++i) {
             mbar_init(bars.hfull + 8 * i, 1);
-            mbar_init(bars.hempty + 8 * i, 11);
+            mbar_init(bars.hempty + 8 * i, 13);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bars.qfull + 8 * i, 1);
@@ -1819,8 +1820,8 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
             for (int k = 0; k < 2; ++k) {
                 mbar_init(bars.sfull + 16 * i + 8 * k, 1);
                 mbar_init(bars.pready + 16 * i + 8 * k, 4);
+                mbar_init(bars.pvdone + 16 * i + 8 * k, 1);
             }
-            mbar_init(bars.pvdone + 8 * i, 1);
             mbar_init(bars.ofull + 8 * i, 1);
             mbar_init(bars.ofree + 8 * i, 4);
             mbar_init(bars.mlfree + 8 * i, 4);
@@ -1830,7 +1831,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
             mbar_init(bars.nqfull + 8 * i, 1);
             mbar_init(bars.nqempty + 8 * i, 1);
         }
-        mbar_init(bars.drain, 2);
+        mbar_init(bars.drain, 4);
         for (int i = 0; i < 16; ++i) misc[i] = 0;
         fence_mbar_init();
     }
@@ -1850,17 +1851,24 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
     grid_dependency_wait();
     grid_launch_dependents();
     if (warp >= RW_MMA_WARP) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RW_HELP_REGS));
         if (warp >= RW_LOAD_WARP) {
             RowsLoader<D> ld{a, lay, bars, sm, sbase, misc};
             if (warp == RW_LOAD_WARP) {
                 if (!ld.run_k(&tq, &tqn, &tk, &tpk)) ld.settle(0);
-            } else {
+            } else if (warp == RW_LOAD_WARP + 1) {
                 if (!ld.run_v(&tv, &tpv)) ld.settle(1);
             }
             if (ld.bad) rows_error(a, ld.bad);
         } else {
-            RowsMma<D> mma{a, lay, bars, sbase, tmem, misc, (uint32_t)(warp - RW_MMA_WARP)};
-            mma.run(sm);
+            const uint32_t stream = (uint32_t)warp & 1u;
+            if (warp < RW_MMA_WARP + 2) {
+                RowsQk<D> qk{a, lay, bars, sbase, tmem, misc, stream};
+                qk.run(sm);
+            } else {
+                RowsPv<D> pv{a, lay, bars, sbase, tmem, misc, stream};
+                pv.run(sm);
+            }
             // every MMA issued has landed before the tensor memory and the stages go
             umma_commit(elect_one(), bars.drain);
             __syncwarp();
@@ -1868,6 +1876,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
             __syncwarp();
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(RW_SOFT_REGS));
         Softmax<D, MODE> sx{a, lay, bars, sm, tmem, misc, warp >> 2};
         sx.run();
         tc_fence_before();
