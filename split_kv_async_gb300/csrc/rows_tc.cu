@@ -1228,11 +1228,11 @@ struct Softmax {
             if (warp_live) {
                 const int k0 = t * ROWS_KEYS + 64 * half;
                 const uint32_t tb = ts + 64 * buf;
-                // Scores that need more than the scale (and a bias that is linear in the key) become v first,
-                // masked ones -inf, back in tensor memory: a rolled loop, since code that few tiles need
-                // costs more to fetch than it saves.
+                // Half tiles with masked scores, or a bias that is not linear in the key: v (masked: -inf) back
+                // to tensor memory first, by a rolled loop, since code that few tiles need costs more to fetch
+                // than it saves.
                 const bool open = __all_sync(0xffffffffu, lo <= k0 && hi >= k0 + 64);
-                const bool ready_v = MODE == MODE_PLAIN || (MODE == MODE_BIAS && linear && open);
+                const bool ready_v = MODE == MODE_PLAIN || (open && (MODE == MODE_CAP || linear));
                 if (!open || !ready_v) {
 #pragma unroll 1
                     for (int c = 0; c < 2; ++c) {
@@ -1268,6 +1268,16 @@ struct Softmax {
                 tmem_wait_ld();
                 reg_fence32(x);
                 reg_fence32(x + 32);
+                if (MODE == MODE_CAP && ready_v) {
+                    const float d0 = (float)(k0 - spos);
+#pragma unroll
+                    for (int i = 0; i < 64; i += 2) {
+                        float v0 = __uint_as_float(x[i]), v1 = __uint_as_float(x[i + 1]);
+                        cap_pair(v0, v1, cap_rate, LOG2E * a.cap);
+                        x[i] = __float_as_uint(fmaf(-slope, fabsf(d0 + (float)i), v0));
+                        x[i + 1] = __float_as_uint(fmaf(-slope, fabsf(d0 + (float)(i + 1)), v1));
+                    }
+                }
                 if (MODE == MODE_BIAS && ready_v) {
                     const float b0 = slope * (float)(k0 - spos);
                     const uint64_t rate2 = pair2(rate, rate);
