@@ -41,6 +41,9 @@ extern "C" {
 
 /* Most query heads of one kv head (G) that these calls take. */
 #define FDPP_ROWS_MAX_GROUP 128
+/* Largest softcap: the cap is formed in fp32 to within a few 2^-23 of softcap, here 2^-11 of a score
+ * unit, which is the accuracy of the weights. */
+#define FDPP_ROWS_MAX_SOFTCAP 4096.0f
 
 typedef struct fdpp_rows_params {
     int batch;               /* B >= 1 sequences */
@@ -59,7 +62,8 @@ typedef struct fdpp_rows_params {
                                 count of prefix_k and prefix_v (contiguous) or
                                 ceil(max_prefix_len / block_size) the length of prefix_blocks */
     float scale;             /* positive and finite */
-    float softcap;           /* > 0: scores are capped at +-softcap; 0: not */
+    float softcap;           /* > 0: scores are capped at +-softcap (at most FDPP_ROWS_MAX_SOFTCAP);
+                                0: not */
     const float* slopes;     /* DEVICE float [Hq], 4-byte aligned, or NULL */
     const int32_t* key_begin;  /* DEVICE int32 [T], 4-byte aligned: first key each token row sees,
                                 or NULL (0) */

@@ -31,6 +31,7 @@ FDPP_ERRBIT_SEQ_LEN, FDPP_ERRBIT_BLOCK_TABLE, FDPP_ERRBIT_TIMEOUT = 1, 2, 4
 FDPP_ERRBIT_POOL, FDPP_ERRBIT_ROOM, FDPP_ERRBIT_SLOT, FDPP_ERRBIT_TOKENS, FDPP_ERRBIT_PREFIX = 8, 16, 32, 64, 128
 FDPP_ROPE_PLAIN, FDPP_ROPE_LINEAR, FDPP_ROPE_NTK, FDPP_ROPE_PARTS = 0, 1, 2, 3
 FDPP_ROWS_MAX_GROUP = 128
+FDPP_ROWS_MAX_SOFTCAP = 4096.0
 FDPP_AUTO_UNITS_PER_SM, FDPP_AUTO_GRANULE, FDPP_AUTO_MIN_SPLIT = 4, 64, 256
 
 # Names every build of the library exports (the C ABI of the headers in include/).

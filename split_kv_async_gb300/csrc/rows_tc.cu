@@ -167,8 +167,9 @@ __device__ __forceinline__ int part_begin(int c, int total, int parts) { return 
 
 // A unit takes its key tiles and some more in the order that is cut: the time of a run's beginning and
 // end, in key tiles, so that a part with many short runs holds fewer tiles. With one tile for every run a
-// prompt of 8192 tokens takes 709 us, with two 580, with three 557, with four 561 (32 heads, 8 kv heads,
-// d = 128); 64 short key-major units behind a shared prefix 104, 99, 103 and 116 us.
+// prompt of 8192 tokens takes 637 us, with two 532, with three 443, with four 443, with five 445 (32 heads,
+// 8 kv heads, d = 128), ragged prompts of 333 to 1500 tokens 57, 55, 57, 61 and 62; 64 single-token rows
+// behind a shared prefix, whose own units are key-major, take 89 us with one, 81 with two and 86 with three.
 constexpr int RW_GAP = 3, RW_NARROW_GAP = 2;
 __device__ __forceinline__ int unit_span(const RowsArgs& a, const RowTileRec& r)
 {
@@ -449,10 +450,12 @@ __global__ void __launch_bounds__(PLAN_THREADS) rows_plan_kernel(RowsArgs a)
         }
         return lo;
     };
-    // rows of no sequence
+    // rows of no sequence: outside [cu_tokens[0], cu_tokens[B]), and anywhere if cu_tokens is not in order
     const int first_row = a.cu ? clamp_len(a.cu[0], a.T) : 0;
+    const bool disorder = __syncthreads_or((int)(bad & FDPP_ERRBIT_TOKENS));
     for (int t = threadIdx.x; t < a.T; t += blockDim.x)
-        if (t < first_row || t >= last) a.tok[t] = RowToken{0, 0, 0, -1};
+        if (disorder || t < first_row || t >= last) a.tok[t] = RowToken{0, 0, 0, -1};
+    if (disorder) __syncthreads();
 
     // own row tiles: the tokens' positions and key ranges, and the tiles' key tiles
     const bool arrays = a.key_begin || a.key_end;
@@ -1018,8 +1021,29 @@ struct RowsPv {
 // ------------------------------------------------------------------------------------------
 // softmax warps
 // ------------------------------------------------------------------------------------------
+// Whether V of a key that a row does not see, in [k0, lo) or [hi, k1), is not finite in this warp's columns
+// col + 32 i, or is not known (its block lies outside the pool). If not, a row that is not finite got there
+// by the keys that it sees.
+template <int D, int NC>
+__device__ __noinline__ bool unseen_values(const RowsArgs& a, int b, int g, int k0, int lo, int hi, int k1, int col)
+{
+    const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(b < 0 && a.pv ? a.pv : a.v);
+    bool found = false;
+    for (int t = k0; t < k1; ++t) {
+        if (t == lo) t = hi;
+        if (t >= k1) break;
+        const long long off = key_offset(a, b, t, g);
+        found = found || off < 0;
+        if (off >= 0)
+#pragma unroll
+            for (int i = 0; i < NC; ++i) found = found || !(fabsf(__bfloat162float(vc[off + col + 32 * i])) < INFINITY);
+    }
+    return __any_sync(0xffffffffu, found);
+}
+
 // The keys [k0, k1) of a row again, for columns of its sums that are not finite: sums over the keys it
-// sees alone, in the frame M. By one warp; o: its columns col + 32 i of each lane.
+// sees alone, in the frame M. By one warp, four keys at a time (their loads and sums over the lanes overlap);
+// o: its columns col + 32 i of each lane.
 template <int D, int NC>
 __device__ __noinline__ void redo_row(const RowsArgs& a, int b, int g, int h, int row, int pos, int k0, int k1, int base,
                                       float M, int col, float (&o)[NC])
@@ -1034,20 +1058,33 @@ __device__ __noinline__ void redo_row(const RowsArgs& a, int b, int g, int h, in
     for (int i = 0; i < D / 32; ++i) qr[i] = __bfloat162float(q[lane + 32 * i]);
 #pragma unroll
     for (int i = 0; i < NC; ++i) o[i] = 0.f;
-    for (int t = k0; t < k1; ++t) {
-        const long long off = key_offset(a, b, t, g);
-        if (off < 0) continue;                           // (reported by the load warp)
-        float s = 0.f;
+    for (int t = k0; t < k1; t += 4) {
+        long long off[4];
+        float s[4], v[4][NC];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) s = fmaf(qr[i], __bfloat162float(kc[off + lane + 32 * i]), s);
-        s = warp_sum(s);
-        const float p = ex2(mod_score(s, a.scale, a.cap, cap_rate, slope, (float)(base + t - pos)) - M);
+        for (int k = 0; k < 4; ++k) {
+            off[k] = t + k < k1 ? key_offset(a, b, t + k, g) : -1;      // (a block outside the pool: reported)
+            s[k] = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+                s[k] = fmaf(qr[i], off[k] < 0 ? 0.f : __bfloat162float(kc[off[k] + lane + 32 * i]), s[k]);
+#pragma unroll
+            for (int i = 0; i < NC; ++i) v[k][i] = off[k] < 0 ? 0.f : __bfloat162float(vc[off[k] + col + 32 * i]);
+        }
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (off[k] < 0) continue;
+            const float p = ex2(mod_score(s[k], a.scale, a.cap, cap_rate, slope, (float)(base + t + k - pos)) - M);
+#pragma unroll
+            for (int i = 0; i < NC; ++i) o[i] = fmaf(p, v[k][i], o[i]);
+        }
         bool done = true;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            o[i] = fmaf(p, __bfloat162float(vc[off + col + 32 * i]), o[i]);
-            done = done && o[i] != o[i];
-        }
+        for (int i = 0; i < NC; ++i) done = done && o[i] != o[i];
         if (__all_sync(0xffffffffu, done)) break;       // NaN stays NaN
     }
 }
@@ -1471,6 +1508,7 @@ struct Softmax {
             const int jlo = max(__shfl_sync(0xffffffffu, lo, j), seen0), jhi = min(__shfl_sync(0xffffffffu, hi, j), seen1);
             const float jm = __shfl_sync(0xffffffffu, m, j), jl = __shfl_sync(0xffffffffu, l, j);
             const long long jat = __shfl_sync(0xffffffffu, at, j);
+            if (!unseen_values<D, D / 32>(a, run.b, run.g, seen0, jlo, jhi, seen1, lane)) continue;
             float o[D / 32];
             redo_row<D, D / 32>(a, run.b, run.g, jhead, jtok, jpos, jlo, jhi, base, jm == -INFINITY ? 0.f : jm, lane, o);
 #pragma unroll
@@ -1776,6 +1814,7 @@ struct Softmax {
             const int jlo = max(__shfl_sync(0xffffffffu, lo, j), seen0), jhi = min(__shfl_sync(0xffffffffu, hi, j), seen1);
             const float jm = __shfl_sync(0xffffffffu, m, j), inv = __shfl_sync(0xffffffffu, inv_l, j);
             const long long jat = __shfl_sync(0xffffffffu, at, j);
+            if (!unseen_values<D, 1>(a, run.b, run.g, seen0, jlo, jhi, seen1, d)) continue;
             float o[1];
             redo_row<D, 1>(a, run.b, run.g, jhead, jtok, jpos, jlo, jhi, base, jm == -INFINITY ? 0.f : jm, d, o);
             if (has) {
@@ -2019,7 +2058,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) rows_join_prefix_kernel(RowsA
     for (int src = 0; src < 2; ++src) {
         if (src == 0 && npre == 0) continue;
         const RowTileRec r = a.rec[src ? tk.rt : tok / (2 * a.tpt)];
-        if (r.nt == 0) continue;
+        // (the row is not one of the tile's where sequences overlap)
+        if (r.nt == 0 || tok < r.tok0 || tok >= r.tok0 + r.ntok) continue;
         const int start = r.start + g * unit_span(a, r);
         int first = 0, past = a.parts;                    // the part of the unit's first tile
         while (past - first > 1) {

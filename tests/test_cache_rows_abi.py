@@ -31,6 +31,7 @@ def test_constants_match_the_headers():
     for name, value in re.findall(r"\b(FDPP_(?:ERRBIT|ROPE)_\w+) = (\d+)", text):
         assert getattr(F, name) == int(value), name
     assert F.FDPP_ROWS_MAX_GROUP == int(re.search(r"#define FDPP_ROWS_MAX_GROUP (\d+)", text).group(1))
+    assert F.FDPP_ROWS_MAX_SOFTCAP == float(re.search(r"#define FDPP_ROWS_MAX_SOFTCAP ([\d.]+)f", text).group(1))
 
 
 # ---- block map ---------------------------------------------------------------------------------
@@ -172,7 +173,7 @@ def _attend(p, ws=1 << 32, ws_bytes=1 << 32, prefix=False, **kw):
     ("num_q_heads", 2 * 129, 2), ("num_tokens", 0, 1), ("max_seq_len", 0, 1), ("max_seq_len", (1 << 30) + 1, 1),
     ("max_prefix_len", -1, 1), ("scale", 0.0, 1), ("scale", float("inf"), 1), ("softcap", -1.0, 1),
     ("softcap", float("nan"), 1), ("kernel", 7, 1), ("slopes", 2, 1), ("key_begin", 1, 1), ("key_end", 3, 1),
-    ("num_tokens", 1 << 28, 1),
+    ("num_tokens", 1 << 28, 1), ("softcap", 4097.0, 2), ("softcap", 1e-40, 1),
 ])
 def test_rows_reject_bad_parameters(field, value, status):
     p = _rows()
