@@ -102,6 +102,20 @@ def test_block_map_large(batch, block, room):
     m.check(want)
 
 
+@pytest.mark.parametrize("batch,block,room,in_place", [(1500, 16, 9000, False), (1024, 16, 4097, True),
+                                                       (40, 64, 20000, True), (1025, 16, 5000, True),
+                                                       (3, 16, 100000, False), (1024, 128, 70000, False)])
+def test_block_map_in_two_launches_or_many_ctas(batch, block, room, in_place):
+    # sequences that end, grow and stay; with and without refusals; blocks given back while others are taken
+    rng = np.random.default_rng(batch + room)
+    held = rng.integers(0, 300, batch).tolist()
+    want = [0 if rng.random() < 0.3 else h + int(rng.integers(0, 2 * room // batch + 2)) for h in held]
+    need = sum(max(0, -(-w // block) - -(-h // block)) for h, w in zip(held, want))
+    for share in (1.0, 0.5):
+        m = Map(held, block, free=max(1, int(need * share)), width=-(-max(held + want) // block) + 1, room=room, seed=7)
+        m.check(want, in_place)
+
+
 def test_block_map_many_steps_give_and_take():
     # forty steps of one pool, its state carried on the device; the queue wraps around several times
     rng = np.random.default_rng(4)

@@ -263,3 +263,23 @@ def test_captured_and_on_another_stream():
         torch.cuda.synchronize()
         x.check(got=x.out)
         y.check(got=y.out)
+
+
+@pytest.mark.parametrize("rows", [1025, 2100, 9000])
+@pytest.mark.parametrize("kw", [dict(), dict(prefix=90), dict(cap=20.0, prefix=200),
+                                dict(mask=lambda row, pos, total: (pos // 64 * 64 if row % 5 else pos, pos + 1 + (row % 3 == 0)))],
+                         ids=["plain", "prefix", "cap", "mask"])
+def test_plans_of_many_tokens(rows, kw):
+    # one to nine rounds of 1024 tokens: a plan made by several CTAs, the last one with few tokens or none
+    rng = np.random.default_rng(rows)
+    seqs, left = [], rows
+    while left:
+        n = min(left, int(rng.choice([1, 1, 7, 200, 700])))
+        seqs.append((n, n + int(rng.integers(0, 60))))
+        left -= n
+    Problem(seqs, hq=4, hkv=1, d=64, block=16, seed=rows, lead=3, tail=5, **kw).check()
+
+
+def test_uniform_tokens_of_many_sequences():
+    Problem([(3, 40)] * 1000, hq=2, hkv=2, d=64, seed=2, uniform=True).check()
+    Problem([(9, 9)] * 1100, hq=2, hkv=1, d=64, seed=2, uniform=True).check()
