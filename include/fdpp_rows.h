@@ -41,8 +41,8 @@ extern "C" {
 
 /* Most query heads of one kv head (G) that these calls take. */
 #define FDPP_ROWS_MAX_GROUP 128
-/* Largest softcap: the cap is formed in fp32 to within a few 2^-23 of softcap, here 2^-11 of a score
- * unit, which is the accuracy of the weights. */
+/* Largest softcap of the tensor kernel, which forms the cap to within a few 2^-23 of softcap: here 2^-11,
+ * the accuracy of its weights. (The CUDA-core kernel's tanh is fp32's.) */
 #define FDPP_ROWS_MAX_SOFTCAP 4096.0f
 
 typedef struct fdpp_rows_params {
@@ -62,8 +62,8 @@ typedef struct fdpp_rows_params {
                                 count of prefix_k and prefix_v (contiguous) or
                                 ceil(max_prefix_len / block_size) the length of prefix_blocks */
     float scale;             /* positive and finite */
-    float softcap;           /* > 0: scores are capped at +-softcap (at most FDPP_ROWS_MAX_SOFTCAP);
-                                0: not */
+    float softcap;           /* > 0: scores are capped at +-softcap (tensor kernel:
+                                at most FDPP_ROWS_MAX_SOFTCAP); 0: not */
     const float* slopes;     /* DEVICE float [Hq], 4-byte aligned, or NULL */
     const int32_t* key_begin;  /* DEVICE int32 [T], 4-byte aligned: first key each token row sees,
                                 or NULL (0) */

@@ -65,8 +65,8 @@ fdpp_status check_params(const fdpp_rows_params* p)
         return rfail(FDPP_ERR_INVALID_ARG, "scale must be positive and finite (got %g)", (double)p->scale);
     if (!std::isfinite(p->softcap) || p->softcap < 0.f)
         return rfail(FDPP_ERR_INVALID_ARG, "softcap must be 0 or positive and finite (got %g)", (double)p->softcap);
-    // the cap's tanh is off by a few 2^-23 softcap: above this limit by more than bf16 weights are
-    if (p->softcap > FDPP_ROWS_MAX_SOFTCAP)
+    // the tensor kernel's tanh is off by a few 2^-23 softcap: above this limit by more than its weights are
+    if (tensor_kernel(*p) && p->softcap > FDPP_ROWS_MAX_SOFTCAP)
         return rfail(FDPP_ERR_UNSUPPORTED, "softcap %g > %g", (double)p->softcap, (double)FDPP_ROWS_MAX_SOFTCAP);
     if (p->softcap > 0.f && !std::isfinite(2.f * p->scale * 1.4426950f / p->softcap))
         return rfail(FDPP_ERR_INVALID_ARG, "scale / softcap overflows");

@@ -81,7 +81,7 @@ __device__ __forceinline__ long long key_offset(const RowsArgs& a, int b, int t,
     return (slot * a.Hkv + g) * a.D;
 }
 
-// The score in units of log2: cap, then the bias -slope |pos - t|. tanh(x) = 1 - 2 / (e^2x + 1): two
+// The score in units of log2, to the accuracy of bf16 weights: cap, then the bias -slope |pos - t|. tanh(x) = 1 - 2 / (e^2x + 1): two
 // MUFU operations, absolute error a few 2^-23 of the cap (tanh.approx would be 2^-11 off). cap_rate: 2
 // scale log2(e) / cap.
 __device__ __forceinline__ float mod_score(float qk, float scale, float cap, float cap_rate, float slope2, float dist)

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
             for (int e = 0; e < 4; ++e) { qr[h][4 * i + e] = x[e]; o[h][4 * i + e] = 0.f; }
         }
     }
-    const float cap_rate = a.cap > 0.f ? 2.f * LOG2E * a.scale / a.cap : 0.f;
+    const float cap_rate = a.cap > 0.f ? a.scale / a.cap : 0.f;
     const unsigned gmask = 0xffu << (lane & ~(LANES - 1));
 
 #pragma unroll 2
@@ -131,8 +131,22 @@ __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
             for (int e = 0; e < E; ++e) acc = fmaf(qr[h][e], kx[e], acc);
 #pragma unroll
             for (int x = LANES / 2; x > 0; x >>= 1) acc += __shfl_xor_sync(gmask, acc, x);
-            s[h] = mod_score(acc, a.scale, a.cap, cap_rate, slope[h], (float)(t - pos));
+            s[h] = acc;
         }
+        // fp32 results need tanh to fp32's accuracy (1 - 2 / (e^2x + 1) is a few 2^-23 of the cap off: with a
+        // cap of 50 ten times the error of the rest). All eight lanes hold all scores: each takes one head's.
+        if (a.cap > 0.f) {
+            float x = s[0];
+#pragma unroll
+            for (int h = 1; h < SH; ++h)
+                if (j % SH == h) x = s[h];
+            x = a.cap * tanhf(x * cap_rate);
+#pragma unroll
+            for (int h = 0; h < SH; ++h) s[h] = __shfl_sync(gmask, x, h, LANES);
+        }
+#pragma unroll
+        for (int h = 0; h < SH; ++h)
+            s[h] = fmaf(-slope[h], fabsf((float)(t - pos)), s[h] * (a.cap > 0.f ? LOG2E : a.scale * LOG2E));
 #pragma unroll
         for (int h = 0; h < SH; ++h) {
             if (s[h] > m[h]) {

@@ -3,6 +3,8 @@ rows_harness). Caches hold NaN wherever no sequence has a key."""
 import numpy as np
 import pytest
 
+import rows_reference as R
+
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
@@ -283,3 +285,17 @@ def test_plans_of_many_tokens(rows, kw):
 def test_uniform_tokens_of_many_sequences():
     Problem([(3, 40)] * 1000, hq=2, hkv=2, d=64, seed=2, uniform=True).check()
     Problem([(9, 9)] * 1100, hq=2, hkv=1, d=64, seed=2, uniform=True).check()
+
+
+@pytest.mark.parametrize("cap", [2.0, 50.0, 1000.0])
+def test_capped_scores_in_fp32_keep_its_accuracy(cap):
+    # a score: each of eight lanes adds 16 products and three additions join them, 19 x 2^-24 scale sum |q k|,
+    # below 2^-16 (scale 0.09, sum |q k| about 82, up to 115); the cap: two units in the last place of a value
+    # below 5, 2^-20; the exponent's product with log2(e), 2^-21. A weight is off by as much of itself, the
+    # sums by 2^-22
+    x = Problem([(2, 130), (1, 700)], hq=8, hkv=2, dtype="f32", cap=cap, seed=8)
+    got = x.call()
+    torch.cuda.synchronize()
+    ref, spread = R.attention(x.host)
+    err = np.abs(got.double().cpu().numpy() - ref)
+    assert (err <= 2.0 ** -24 * np.abs(ref) + (2.0 ** -16 + 2.0 ** -19) * spread).all(), (err / spread).max()
