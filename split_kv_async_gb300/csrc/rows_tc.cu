@@ -320,14 +320,21 @@ __global__ void __launch_bounds__(PLAN_SMALL) rows_plan_small_kernel(RowsArgs a)
     if (ranks > 1) cluster_meet(); else __syncthreads();
     int* const low0 = ranks > 1 ? in_first(&low[0][0]) : &low[0][0];
     int* const high0 = ranks > 1 ? in_first(&high[0][0]) : &high[0][0];
-    // the least and greatest key of each half of a row tile, one shared-memory operation for all the lanes
-    // of a warp that belong to it
+    // the least and greatest key of each half of a row tile: one shared-memory operation for all the lanes of
+    // a warp that belong to it where these are few (a reduction for each set of lanes, one after another),
+    // and one for each lane where they are many (a row tile per token: 2.5 us less for 64 tokens)
     auto widen = [&](int key, int from, int to) {
         const unsigned m = __match_any_sync(0xffffffffu, key);
-        const int lo = __reduce_min_sync(m, from), hi = __reduce_max_sync(m, to);
-        if (key >= 0 && (t & 31) == __ffs(m) - 1) {
-            atomicMin(low0 + (key & 1) * PLAN_SMALL + (key >> 1), lo);
-            atomicMax(high0 + (key & 1) * PLAN_SMALL + (key >> 1), hi);
+        bool speaks = (t & 31) == __ffs(m) - 1;
+        if (__popc(__ballot_sync(0xffffffffu, speaks)) <= 4) {
+            from = __reduce_min_sync(m, from);
+            to = __reduce_max_sync(m, to);
+        } else {
+            speaks = true;
+        }
+        if (key >= 0 && speaks) {
+            atomicMin(low0 + (key & 1) * PLAN_SMALL + (key >> 1), from);
+            atomicMax(high0 + (key & 1) * PLAN_SMALL + (key >> 1), to);
         }
     };
     // key ranges are read a round ahead
@@ -1981,12 +1988,12 @@ struct RowSum {
 };
 
 // The partials of a unit cut in two or more, tiles [start, start + nt): the part of its first tile left
-// its own in slot 2 c + 1, every later one in slot 2 c. Four are read at a time.
+// its own in slot 2 c + 1, every later one in slot 2 c. Four are read at a time; the first `done` are left out.
 template <int E>
 __device__ __forceinline__ void add_cut(const RowsArgs& a, const int* begins, RowSum<E>& x, int start, int nt, int first,
-                                        long long row)
+                                        long long row, int done = 0)
 {
-    for (int c0 = first; c0 < a.parts && begins[c0] < start + nt; c0 += 4) {
+    for (int c0 = first + done; c0 < a.parts && begins[c0] < start + nt; c0 += 4) {
         float2 ml[4];
         float v[4][E];
 #pragma unroll
@@ -2014,7 +2021,10 @@ __device__ __forceinline__ void load_begins(const RowsArgs& a, int total, int* b
 }
 
 // Without a prefix: the units that a part boundary cuts, found from the boundaries (one grid column
-// each; the first boundary inside a unit does it). A warp per row.
+// each; the first boundary inside a unit does it). A warp per row, and at most JOIN_ROWS CTAs for a unit so
+// that all are resident at once: with a CTA for every eight of 256 rows, most of which found nothing to do,
+// this launch took 11 us of a prompt's.
+constexpr int JOIN_ROWS = 8;
 template <int D>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) rows_join_cut_kernel(RowsArgs a)
 {
@@ -2027,53 +2037,73 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) rows_join_cut_kernel(RowsArgs
     if (x <= 0 || x >= total) return;
     const int span = unit_span(a, r), g = (x - r.start) / span, start = r.start + g * span;
     if (x == start || x >= start + r.nt || before > start) return;
-    const int row = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5);
     if (blockIdx.y * JOIN_WARPS >= r.ntok * a.G) return;
     load_begins(a, total, begins);
-    if (row >= r.ntok * a.G) return;
-    const int i = row / a.G, tok = r.tok0 + i;
-    const RowToken tk = a.tok[tok];
-    RowSum<D / 32> s;
-    add_cut(a, begins, s, start, r.nt, c - 1, row);
-    s.store(static_cast<__nv_bfloat16*>(a.out) + ((long long)tok * a.Hq + g * a.G + (row - i * a.G)) * D, tk.hi <= tk.lo);
+    for (int row = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5); row < r.ntok * a.G; row += gridDim.y * JOIN_WARPS) {
+        const int i = row / a.G, tok = r.tok0 + i;
+        const RowToken tk = a.tok[tok];
+        RowSum<D / 32> s;
+        add_cut(a, begins, s, start, r.nt, c - 1, row);
+        s.store(static_cast<__nv_bfloat16*>(a.out) + ((long long)tok * a.Hq + g * a.G + (row - i * a.G)) * D, tk.hi <= tk.lo);
+    }
 }
 
-// With a prefix: every row from its two units. A warp per row.
+// With a prefix: every row from its two units. A warp per row. Latency is all there is to it, so what can be
+// read at once is: the token with both row tiles' records, then the first two partials of both units.
 template <int D>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) rows_join_prefix_kernel(RowsArgs a)
 {
+    constexpr int E = D / 32;
     __shared__ int begins[ROWS_MAX_PARTS + 1];
+    const long long w = (long long)blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5);
+    const int tok = min((int)(w / a.Hq), a.T - 1), head = (int)(w % a.Hq), g = head / a.G;
     grid_dependency_wait();
     grid_launch_dependents();
     const int total = a.plan[RP_TILES], npre = a.plan[RP_NPRE];
-    load_begins(a, total, begins);
-    const long long w = (long long)blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5);
-    const int tok = (int)(w / a.Hq), head = (int)(w - (long long)tok * a.Hq);
-    if (tok >= a.T) return;
     const RowToken tk = a.tok[tok];
-    if (tk.rt < 0) return;
-    const int g = head / a.G;
-    RowSum<D / 32> s;
+    RowTileRec rec[2];
+    rec[0] = a.rec[min(tok / (2 * a.tpt), a.max_rt - 1)];
+    rec[1] = a.rec[max(tk.rt, 0)];
+    load_begins(a, total, begins);
+    if (w >= (long long)a.T * a.Hq || tk.rt < 0) return;
+    // per source: the partials are first, first + 1, .. (cut), or one (whole), or none
+    int start[2], first[2], pieces[2];
+    float2 ml[2][2];
+    float v[2][2][E];
 #pragma unroll
     for (int src = 0; src < 2; ++src) {
-        if (src == 0 && npre == 0) continue;
-        const RowTileRec r = a.rec[src ? tk.rt : tok / (2 * a.tpt)];
+        const RowTileRec& r = rec[src];
+        pieces[src] = 0;
+        ml[src][0] = ml[src][1] = make_float2(-INFINITY, 0.f);
         // (the row is not one of the tile's where sequences overlap)
-        if (r.nt == 0 || tok < r.tok0 || tok >= r.tok0 + r.ntok) continue;
-        const int start = r.start + g * unit_span(a, r);
-        int first = 0, past = a.parts;                    // the part of the unit's first tile
-        while (past - first > 1) {
-            const int mid = (first + past) >> 1;
-            if (begins[mid] <= start) first = mid; else past = mid;
-        }
-        if (begins[first + 1] >= start + r.nt) {
+        if ((src == 0 && npre == 0) || r.nt == 0 || tok < r.tok0 || tok >= r.tok0 + r.ntok) continue;
+        start[src] = r.start + g * unit_span(a, r);
+        // the part of the unit's first tile: the last c with c total / parts < start + 1
+        first[src] = (int)(((start[src] + 1ll) * a.parts - 1) / total);
+        pieces[src] = begins[first[src] + 1] >= start[src] + r.nt ? 1 : 2;
+        if (pieces[src] == 1) {
             const long long at = ((long long)src * a.T + tok) * a.Hq + head;
-            float v[D / 32];
-            RowSum<D / 32>::fetch(a.row_o + at * D, v);
-            s.add(__ldcg(a.row_ml + at), v);
+            ml[src][0] = __ldcg(a.row_ml + at);
+            RowSum<E>::fetch(a.row_o + at * D, v[src][0]);
         } else {
-            add_cut(a, begins, s, start, r.nt, first, (long long)(tok - r.tok0) * a.G + (head - g * a.G));
+            const long long row = (long long)(tok - r.tok0) * a.G + (head - g * a.G);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int c = first[src] + k;
+                if (k == 1 && begins[c] >= begins[c + 1]) continue;
+                const long long at = (long long)(2 * c + (k == 0)) * a.slot_rows + row;
+                ml[src][k] = __ldcg(a.slot_ml + at);
+                RowSum<E>::fetch(a.slot_o + at * D, v[src][k]);
+            }
         }
+    }
+    RowSum<E> s;
+#pragma unroll
+    for (int src = 0; src < 2; ++src) {
+        s.add(ml[src][0], v[src][0]);
+        s.add(ml[src][1], v[src][1]);
+        if (pieces[src] == 2)
+            add_cut(a, begins, s, start[src], rec[src].nt, first[src], (long long)(tok - rec[src].tok0) * a.G + (head - g * a.G), 2);
     }
     s.store(static_cast<__nv_bfloat16*>(a.out) + ((long long)tok * a.Hq + head) * D, tk.hi <= tk.lo);
 }
@@ -2115,7 +2145,7 @@ cudaError_t launch_d(const RowsArgs& a, const RowsMaps& m, cudaStream_t s)
         PdlConfig join(dim3((unsigned)((rows + JOIN_WARPS - 1) / JOIN_WARPS)), JOIN_WARPS * 32, 0, s);
         e = cudaLaunchKernelEx(&join.cfg, rows_join_prefix_kernel<D>, a);
     } else if (a.parts > 1) {
-        PdlConfig join(dim3((unsigned)(a.parts - 1), (unsigned)((a.slot_rows + JOIN_WARPS - 1) / JOIN_WARPS)), JOIN_WARPS * 32, 0, s);
+        PdlConfig join(dim3((unsigned)(a.parts - 1), (unsigned)min(JOIN_ROWS, (a.slot_rows + JOIN_WARPS - 1) / JOIN_WARPS)), JOIN_WARPS * 32, 0, s);
         e = cudaLaunchKernelEx(&join.cfg, rows_join_cut_kernel<D>, a);
     }
     return e != cudaSuccess ? e : cudaGetLastError();
