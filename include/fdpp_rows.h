@@ -19,10 +19,13 @@
  * sliding window a begin behind it. A token that sees no key gets a zero row.
  *
  * How. The rows of a kv head (its G heads of as many tokens as fit) fill 128-row tiles of tcgen05
- * MMAs; scores and accumulators live in tensor memory, K and V stream through a TMA ring. The
- * 128-key tiles of all (row tile, kv head) pairs are cut into one equal part per SM; a pair cut in
- * two, or one with a prefix and own keys, leaves partials that a second kernel joins. Scores that
- * a row does not see never enter its sums, whatever the caches hold there (NaN included).
+ * MMAs (up to 32 rows: with the operands exchanged, the keys on the lanes); scores and accumulators
+ * live in tensor memory, K and V stream through a TMA ring. The 128-key tiles of all (row tile, kv
+ * head) pairs are cut into one equal part per SM; a pair cut in two, or one with a prefix and own
+ * keys, leaves partials that a second kernel joins. Scores that a row does not see never enter its
+ * sums, whatever the caches hold there (NaN included), and a non-finite score or value that it sees
+ * has the formula's effect on that row alone. Results do not depend on timing: the same call gives
+ * the same bits. fp32 (and bf16 on request) takes a CUDA-core kernel instead.
  *
  * Conventions: as in fdpp.h; error bits as in fdpp_cache.h, read with fdpp_read_error.
  */
