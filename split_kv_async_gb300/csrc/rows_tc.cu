@@ -28,12 +28,12 @@
 // Few rows (32 at most): the same with the operands exchanged, the keys on the tensor-memory lanes. A
 // row per lane would leave one warp of four with all the work; a key per lane shares it evenly.
 //
-// What bounds it. Many rows: the tensor pipe (4 x 128 keys x 128 rows x d FLOP per row tile and key tile)
-// with the softmax beside it, whose 128 x 128 exponentials take the MUFU units as long (512 cycles of an SM) as
-// the products take the tensor cores, and whose other instructions take about as many issue slots again. A prompt of
-// 8192 tokens, 32 heads, 8 kv heads, d = 128: 428 us, 1.28 PFLOP/s of the 1.87 that a plain matrix product was
-// measured at; with a bias 475; with a cap 813 (an exponential and half a reciprocal more per score: 4 times
-// the MUFU cycles of the plain softmax for two scores). Few rows: HBM (K and V of a kv head are read once, at 512 bytes
+// What bounds it. Many rows: the tensor pipe (4 x 128 keys x 128 rows x d FLOP per row tile and key tile, 1024
+// cycles for d = 128; a half tile's Q K^T, N = 64, runs at two thirds of the rate, which makes them 1280) with the
+// softmax beside it (512 cycles of the MUFU units for the exponentials, and its other instructions). A prompt of
+// 8192 tokens, 32 heads, 8 kv heads, d = 128: 426 us, 1.28 PFLOP/s of the 1.87 that a plain matrix product was
+// measured at; with a bias 474; with a cap 770 (an exponential and half a reciprocal more for each score: three
+// times the MUFU cycles). Few rows: HBM (K and V of a kv head are read once, at 512 bytes
 // per key for d = 128): 64 sequences of 512 to 16384 keys, 64 heads, 8 kv heads, with a cap: 339.5 us, 6.48 TB/s,
 // 0.95 of a measured copy. Short calls: latency, of which the plan takes 3 to 8 us, a first tile with cold
 // instruction caches 5, the join 4 to 8.
@@ -72,8 +72,12 @@ constexpr float RW_LAG = 8.f;            // log2 of the growth of a row's max th
 enum { RH_KIND = 0, RH_G, RH_B, RH_TOK0, RH_NTOK, RH_LEN, RH_A0, RH_A1, RH_B0, RH_B1, RH_T0, RH_T1, RH_DEST,
        RH_FLAGS, RH_BASE, RH_WORDS };
 enum { RUN_ROWS = 0, RUN_END = 1 };
-// two row tiles; few rows (key-major); the first key tile goes to stream 1
-enum { RF_PAIR = 1, RF_NARROW = 2, RF_START = 4 };
+// two row tiles; few rows (key-major); the first key tile goes to stream 1; all of them do (else: to stream 0)
+enum { RF_PAIR = 1, RF_NARROW = 2, RF_START = 4, RF_SOLO = 8 };
+// A key-major run of at most this many key tiles that another run follows is one stream's alone, so that the
+// other begins the next meanwhile: a run's beginning and end take as long as two tiles. 64 single tokens with up
+// to 512 own keys behind a prefix: 1 us of 77 less; runs of five tiles, which both streams share, 1.5 of 61 more.
+constexpr int RW_SOLO_TILES = 4;
 enum { DEST_OUT = -1, DEST_ROWS = -2 };  // else a slot
 static_assert(RH_WORDS * 4 <= RW_HDR_BYTES, "header fits its slot");
 
@@ -720,6 +724,7 @@ struct RowsLoader {
                 }
                 const int t0 = r.k0 + ta, t1 = r.k0 + tb;
                 const bool pair = r.ntok > a.tpt, whole = ta == 0 && tb == r.nt;
+                const bool solo = narrow && tb == r.nt && next_pos < end && t1 - t0 <= RW_SOLO_TILES;
                 int* h = header();
                 if (!h) return false;
                 if (lane == 0) {
@@ -736,11 +741,11 @@ struct RowsLoader {
                     h[RH_T0] = t0;
                     h[RH_T1] = t1;
                     h[RH_DEST] = whole ? (a.prefix_len ? DEST_ROWS : DEST_OUT) : 2 * c + (ta == 0 ? 1 : 0);
-                    h[RH_FLAGS] = (pair ? RF_PAIR : (toggle ? RF_START : 0)) | (narrow ? RF_NARROW : 0);
+                    h[RH_FLAGS] = (pair ? RF_PAIR : (toggle ? RF_START : 0)) | (narrow ? RF_NARROW : 0) | (solo ? RF_SOLO : 0);
                     h[RH_BASE] = r.b < 0 ? 0 : P;
                 }
                 publish();
-                if (!pair) toggle = (toggle + (uint32_t)(t1 - t0)) & 1u;
+                if (!pair) toggle = (toggle + (solo ? 1u : (uint32_t)(t1 - t0))) & 1u;
                 int ent = a.block_table ? entry(r.b, r.len, t1 - 1) : 0;
                 if (narrow ? !query_narrow(tqn, g, r.tok0) : !query(tq, g, r.tok0)) return false;
                 if (pair && !query(tq, g, r.tok0 + a.tpt)) return false;
@@ -825,6 +830,7 @@ __device__ __forceinline__ uint32_t narrow_cols(int rows) { return rows <= 16 ? 
 // What the MMA warps take from a run's header: whose tiles are theirs, counted from the run's last.
 struct MmaRun {
     int kind, len, t1, n, j0, j1, last;
+    bool every;                                  // all of j0 .. j1, not every other
     bool pair;
     uint32_t ncols;                              // of a key-major run, else 0
 
@@ -839,11 +845,13 @@ struct MmaRun {
         pair = flags & RF_PAIR;
         const uint32_t start = (flags & RF_START) ? 1u : 0u;
         n = t1 - t0;
-        j0 = pair ? t1 - s1 : (int)(S ^ start);
+        const bool solo = flags & RF_SOLO;
+        every = pair || solo;
+        j0 = pair ? t1 - s1 : solo ? (S == start ? 0 : n) : (int)(S ^ start);
         j1 = pair ? t1 - s0 : n;
-        last = j0 >= j1 ? -1 : (pair ? j1 - 1 : j1 - 1 - ((j1 - 1 - j0) & 1));
+        last = j0 >= j1 ? -1 : (every ? j1 - 1 : j1 - 1 - ((j1 - 1 - j0) & 1));
     }
-    __device__ __forceinline__ bool mine(int j) const { return j >= j0 && j < j1 && (pair || ((uint32_t)(j - j0) & 1u) == 0u); }
+    __device__ __forceinline__ bool mine(int j) const { return j >= j0 && j < j1 && (every || ((uint32_t)(j - j0) & 1u) == 0u); }
 };
 
 // Q K^T of stream S: every half tile (a key-major run: tile) as soon as its keys are there and its score
@@ -875,7 +883,8 @@ struct RowsQk {
             uint32_t qd = 0, qbar = 0;
             if (r.ncols) {
                 const uint32_t i = nqn & 3u;
-                if (!rwait(bars.nqfull + 8 * i, (nqn >> 2) & 1u, misc, a)) return false;
+                // (without tiles of its own the slot may be refilled before this stream has looked)
+                if (r.last >= 0 && !rwait(bars.nqfull + 8 * i, (nqn >> 2) & 1u, misc, a)) return false;
                 qd = sw128_kmajor_lo(sbase + lay.q + RowsSmem<D>::slot(i));
                 ++nqn;
             } else {
@@ -1143,6 +1152,28 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
+}
+
+// v[0 .. NR) of every lane, each combined over the warp: row lane / (32 / NR)'s in every lane. Each step hands half
+// of the rows to the lane across, so that all rows together take NR + 1 exchanges at most (5 NR one by one).
+template <int NR, typename Op>
+__device__ __forceinline__ float warp_rows(float (&v)[NR], Op op)
+{
+    const int lane = threadIdx.x & 31;
+    int bit = 16;
+#pragma unroll
+    for (int k = NR / 2; k > 0; k >>= 1, bit >>= 1) {
+        const bool up = lane & bit;
+#pragma unroll
+        for (int i = 0; i < k; ++i) {
+            const float keep = up ? v[i + k] : v[i], give = up ? v[i] : v[i + k];
+            v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, bit));
+        }
+    }
+    float x = v[0];
+#pragma unroll
+    for (int b = 16 / NR; b > 0; b >>= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, b));
+    return x;
 }
 
 template <int NR>
@@ -1619,8 +1650,10 @@ struct Softmax {
         }
         const float rate = a.scale * LOG2E;
         const float cap_rate = MODE == MODE_CAP ? 2.f * LOG2E * a.scale / a.cap : 0.f;
+        const bool solo = run.flags & RF_SOLO;
+        const int step = solo ? 1 : 2, top = solo ? (S == start ? run.t1 - 1 : run.t0 - 1) : run.t1 - 1 - (S ^ start);
         int count = 0;
-        for (int t = run.t1 - 1 - (S ^ start); t >= run.t0; t -= 2, ++ntile, ++count) {
+        for (int t = top; t >= run.t0; t -= step, ++ntile, ++count) {
             if (!rwait(bars.sfull + 16 * S, ntile, misc, a)) return false;
             tc_fence_after();
             const int k0 = t * ROWS_KEYS, key = k0 + 32 * w + lane;
@@ -1673,19 +1706,15 @@ struct Softmax {
                 load(0, v);
             }
             if (move) {
-                float mine_max = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < NR; c += CH) {
                     if (CH < NR) load(c, v);
+                    float x[CH];
 #pragma unroll
-                    for (int i = 0; i < CH; ++i) {
-                        float x = v[i];
-#pragma unroll
-                        for (int k = 16; k > 0; k >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
-                        if (lane == c + i) mine_max = x;
-                    }
+                    for (int i = 0; i < CH; ++i) x[i] = v[i];
+                    const float top = warp_rows(x, [](float p, float q) { return fmaxf(p, q); });
+                    if (lane % (32 / CH) == 0) sh.wmax[S][w][c + lane / (32 / CH)] = top;
                 }
-                if (lane < NR) sh.wmax[S][w][lane] = mine_max;
                 if (!meet()) return false;
 #pragma unroll
                 for (int c = 0; c < NR; c += 8) {
@@ -1729,20 +1758,16 @@ struct Softmax {
         // ---- the run's end ----
         if (count > 0) {
             if (!rwait(bars.mlfree + 8 * S, (nml & 1u) ^ 1u, misc, a)) return false;
-            float mine_l = 0.f, mine_f = -INFINITY;
+            if (w == 0 && lane == 0) {
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                const float x = warp_sum(l[r]);
-                if (lane == r) { mine_l = x; mine_f = fr[r]; }
+                for (int r = 0; r < NR; ++r) sh.frame[S][r] = fr[r];
             }
-            if (lane < NR) {
-                sh.lsum[S][w][lane] = mine_l;
-                if (w == 0) sh.frame[S][lane] = mine_f;
-            }
+            const float x = warp_rows(l, [](float p, float q) { return p + q; });
+            if (lane % (32 / NR) == 0) sh.lsum[S][w][lane / (32 / NR)] = x;
             tell();
             ++nml;
         }
-        const bool other = run.t1 - run.t0 > 1;          // both streams had tiles
+        const bool other = !solo && run.t1 - run.t0 > 1; // both streams had tiles
         if (S != start) {
             if (count > 0) ++nacc;
             ++nacc_o;
