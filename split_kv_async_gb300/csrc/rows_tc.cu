@@ -1147,6 +1147,12 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 {
     uint64_t d;
@@ -1313,7 +1319,7 @@ struct Softmax {
                 // to tensor memory first, by a rolled loop, since code that few tiles need costs more to fetch
                 // than it saves.
                 const bool open = __all_sync(0xffffffffu, lo <= k0 && hi >= k0 + 64);
-                const bool ready_v = MODE == MODE_PLAIN || (open && (MODE == MODE_CAP || linear));
+                const bool ready_v = MODE == MODE_PLAIN || (open && (linear || !a.slopes));
                 if (!open || !ready_v) {
 #pragma unroll 1
                     for (int c = 0; c < 2; ++c) {
@@ -1349,14 +1355,27 @@ struct Softmax {
                 tmem_wait_ld();
                 reg_fence32(x);
                 reg_fence32(x + 32);
-                if (MODE == MODE_CAP && ready_v) {
-                    const float d0 = (float)(k0 - spos);
+                if (MODE == MODE_CAP && ready_v) {               // (as cap_pair, two operations at a time)
+                    const float top = LOG2E * a.cap;
+                    const uint64_t cr2 = pair2(cap_rate, cap_rate), one2 = pair2(1.f, 1.f), top2 = pair2(top, top),
+                                   slope_top2 = pair2(-2.f * top, -2.f * top);
 #pragma unroll
                     for (int i = 0; i < 64; i += 2) {
-                        float v0 = __uint_as_float(x[i]), v1 = __uint_as_float(x[i + 1]);
-                        cap_pair(v0, v1, cap_rate, LOG2E * a.cap);
-                        x[i] = __float_as_uint(fmaf(-slope, fabsf(d0 + (float)i), v0));
-                        x[i + 1] = __float_as_uint(fmaf(-slope, fabsf(d0 + (float)(i + 1)), v1));
+                        float t0, t1, e0, e1, v0, v1;
+                        unpair2(mul2(pair2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), cr2), t0, t1);
+                        asm("min.NaN.f32 %0, %0, 0f42700000;" : "+f"(t0));
+                        asm("min.NaN.f32 %0, %0, 0f42700000;" : "+f"(t1));
+                        unpair2(add2(pair2(ex2(t0), ex2(t1)), one2), e0, e1);
+                        const float r = rcp(e0 * e1);
+                        unpair2(fma2(mul2(pair2(e1, e0), pair2(r, r)), slope_top2, top2), v0, v1);
+                        x[i] = __float_as_uint(v0);
+                        x[i + 1] = __float_as_uint(v1);
+                    }
+                    if (a.slopes) {
+                        const float b0 = slope * (float)(k0 - spos);
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            x[i] = __float_as_uint(__uint_as_float(x[i]) + fmaf(slope, (float)i, b0));
                     }
                 }
                 if (MODE == MODE_BIAS && ready_v) {
