@@ -32,8 +32,8 @@
 // cycles for d = 128; a half tile's Q K^T, N = 64, runs at two thirds of the rate, which makes them 1280) with the
 // softmax beside it (512 cycles of the MUFU units for the exponentials, and its other instructions). A prompt of
 // 8192 tokens, 32 heads, 8 kv heads, d = 128: 426 us, 1.28 PFLOP/s of the 1.87 that a plain matrix product was
-// measured at; with a bias 474; with a cap 770 (an exponential and half a reciprocal more for each score: three
-// times the MUFU cycles). Few rows: HBM (K and V of a kv head are read once, at 512 bytes
+// measured at; with a bias 474; with a cap 642 (scores near it 755: an exponential and half a reciprocal more for each).
+// Few rows: HBM (K and V of a kv head are read once, at 512 bytes
 // per key for d = 128): 64 sequences of 512 to 16384 keys, 64 heads, 8 kv heads, with a cap: 339.5 us, 6.48 TB/s,
 // 0.95 of a measured copy. Short calls: latency, of which the plan takes 3 to 8 us, a first tile with cold
 // instruction caches 5, the join 4 to 8.
@@ -1217,6 +1217,23 @@ __device__ __forceinline__ void tmem_st_rows(uint32_t taddr, const uint32_t (&r)
 }
 
 // Ties the registers to the tcgen05.wait::ld before it.
+__device__ __forceinline__ float abs_max64(const uint32_t* y)
+{
+    float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 64; i += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(m[k]) : "f"(__uint_as_float(y[i + k])), "f"(__uint_as_float(y[i + 4 + k])));
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// Scores up to CAP_NEAR of their cap (most are far below it) are capped by tanh(z) / z as a polynomial in z^2,
+// interpolated at the Chebyshev points: 2^-23 of itself off. It takes five operations of the FMA pipe where the exact
+// form takes four and a half and two and a half of the MUFU: a prompt of 8192 tokens 642 us where all
+// scores are near, and 755 by the other form.
+constexpr float CAP_NEAR = 0.35f;
+
 template <int NR>
 __device__ __forceinline__ void reg_fence(uint32_t (&r)[NR])
 {
@@ -1355,21 +1372,40 @@ struct Softmax {
                 tmem_wait_ld();
                 reg_fence32(x);
                 reg_fence32(x + 32);
-                if (MODE == MODE_CAP && ready_v) {               // (as cap_pair, two operations at a time)
-                    const float top = LOG2E * a.cap;
-                    const uint64_t cr2 = pair2(cap_rate, cap_rate), one2 = pair2(1.f, 1.f), top2 = pair2(top, top),
-                                   slope_top2 = pair2(-2.f * top, -2.f * top);
+                if (MODE == MODE_CAP && ready_v) {
+                    // (the polynomial's coefficients stay normal numbers from this ratio on)
+                    if (a.scale >= 1e-5f * a.cap && __all_sync(0xffffffffu, abs_max64(x) * a.scale <= CAP_NEAR * a.cap)) {
+                        // v = y (rate p(z^2)), the coefficients taken with their powers of z / y
+                        const float zz = (a.scale / a.cap) * (a.scale / a.cap);
+                        const float k0_ = rate, k1_ = -0.333324194f * zz * rate, k2_ = 0.132957518f * zz * zz * rate,
+                                    k3_ = -0.048955638f * zz * zz * zz * rate;
 #pragma unroll
-                    for (int i = 0; i < 64; i += 2) {
-                        float t0, t1, e0, e1, v0, v1;
-                        unpair2(mul2(pair2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), cr2), t0, t1);
-                        asm("min.NaN.f32 %0, %0, 0f42700000;" : "+f"(t0));
-                        asm("min.NaN.f32 %0, %0, 0f42700000;" : "+f"(t1));
-                        unpair2(add2(pair2(ex2(t0), ex2(t1)), one2), e0, e1);
-                        const float r = rcp(e0 * e1);
-                        unpair2(fma2(mul2(pair2(e1, e0), pair2(r, r)), slope_top2, top2), v0, v1);
-                        x[i] = __float_as_uint(v0);
-                        x[i + 1] = __float_as_uint(v1);
+                        for (int i = 0; i < 64; i += 2) {
+                            const uint64_t y = pair2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), u = mul2(y, y);
+                            uint64_t p = fma2(u, pair2(k3_, k3_), pair2(k2_, k2_));
+                            p = fma2(p, u, pair2(k1_, k1_));
+                            p = fma2(p, u, pair2(k0_, k0_));
+                            float v0, v1;
+                            unpair2(mul2(y, p), v0, v1);
+                            x[i] = __float_as_uint(v0);
+                            x[i + 1] = __float_as_uint(v1);
+                        }
+                    } else {                             // (as cap_pair, two operations at a time)
+                        const float top = LOG2E * a.cap;
+                        const uint64_t cr2 = pair2(cap_rate, cap_rate), one2 = pair2(1.f, 1.f), top2 = pair2(top, top),
+                                       slope_top2 = pair2(-2.f * top, -2.f * top);
+#pragma unroll
+                        for (int i = 0; i < 64; i += 2) {
+                            float t0, t1, e0, e1, v0, v1;
+                            unpair2(mul2(pair2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), cr2), t0, t1);
+                            asm("min.NaN.f32 %0, %0, 0f42700000;" : "+f"(t0));
+                            asm("min.NaN.f32 %0, %0, 0f42700000;" : "+f"(t1));
+                            unpair2(add2(pair2(ex2(t0), ex2(t1)), one2), e0, e1);
+                            const float r = rcp(e0 * e1);
+                            unpair2(fma2(mul2(pair2(e1, e0), pair2(r, r)), slope_top2, top2), v0, v1);
+                            x[i] = __float_as_uint(v0);
+                            x[i + 1] = __float_as_uint(v1);
+                        }
                     }
                     if (a.slopes) {
                         const float b0 = slope * (float)(k0 - spos);

@@ -299,3 +299,12 @@ def test_capped_scores_in_fp32_keep_its_accuracy(cap):
     ref, spread = R.attention(x.host)
     err = np.abs(got.double().cpu().numpy() - ref)
     assert (err <= 2.0 ** -24 * np.abs(ref) + (2.0 ** -16 + 2.0 ** -19) * spread).all(), (err / spread).max()
+
+
+@pytest.mark.parametrize("gain", [0.5, 2.0, 8.0])
+@pytest.mark.parametrize("bias", [False, True])
+def test_caps_near_and_far(gain, bias):
+    # scores below half their cap, some above it, most above it: both forms of the cap, in one tile and in turn
+    seqs = [(300, 300), (150, 400)]
+    Problem(seqs, hq=4, hkv=1, d=128, block=16, cap=6.0, bias=bias, q_gain=gain, seed=12).check()
+    Problem(seqs, hq=4, hkv=2, d=64, cap=6.0, bias=bias, q_gain=gain, seed=13, prefix=140).check()
