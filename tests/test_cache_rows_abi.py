@@ -244,3 +244,13 @@ def test_rows_workspace():
 
 def test_read_error_rejects_null():
     assert F.lib.fdpp_read_error(None, None) == F.FDPP_ERR_INVALID_ARG
+
+
+def test_rows_softcap_limit_is_the_tensor_kernels():
+    big = 8.0 * F.FDPP_ROWS_MAX_SOFTCAP
+    assert F.fdpp_rows_workspace_size(_rows(softcap=F.FDPP_ROWS_MAX_SOFTCAP)) > 0
+    assert F.fdpp_rows_workspace_size(_rows(softcap=big, dtype=F.FDPP_F32)) > 0
+    assert F.fdpp_rows_workspace_size(_rows(softcap=big, kernel=F.FDPP_KERNEL_SIMT)) > 0
+    with pytest.raises(F.FdppError) as e:
+        F.fdpp_rows_workspace_size(_rows(softcap=big))
+    assert e.value.status == F.FDPP_ERR_UNSUPPORTED
