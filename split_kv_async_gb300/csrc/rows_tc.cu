@@ -1043,16 +1043,16 @@ struct RowsPv {
 // ------------------------------------------------------------------------------------------
 // softmax warps
 // ------------------------------------------------------------------------------------------
-// Whether V of a key that a row does not see, in [k0, lo) or [hi, k1), is not finite in this warp's columns
+// Whether V of a key of [k0, k1) that a row does not see, outside [lo, hi), is not finite in this warp's columns
 // col + 32 i, or is not known (its block lies outside the pool). If not, a row that is not finite got there
-// by the keys that it sees.
+// by the keys that it sees. (Any lo and hi: t only grows.)
 template <int D, int NC>
 __device__ __noinline__ bool unseen_values(const RowsArgs& a, int b, int g, int k0, int lo, int hi, int k1, int col)
 {
     const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(b < 0 && a.pv ? a.pv : a.v);
     bool found = false;
     for (int t = k0; t < k1; ++t) {
-        if (t == lo) t = hi;
+        if (t >= lo && t < hi) t = hi;
         if (t >= k1) break;
         const long long off = key_offset(a, b, t, g);
         found = found || off < 0;
@@ -1597,7 +1597,9 @@ struct Softmax {
         }
         // Rows that may have met a non-finite V of a key they do not see
         const int seen0 = (pair ? run.s0 : t0) * ROWS_KEYS, seen1 = min((pair ? run.s1 : t1) * ROWS_KEYS, run.len);
-        const bool again = mine && count > 0 && !fine && !empty && fabsf(l) < INFINITY && (lo > seen0 || hi < seen1);
+        // (one that sees none of the run's keys leaves an empty partial, which the join passes over)
+        const bool again = mine && count > 0 && !fine && max(lo, seen0) < min(hi, seen1) && fabsf(l) < INFINITY &&
+                           (lo > seen0 || hi < seen1);
         unsigned todo = __ballot_sync(0xffffffffu, again);
         while (todo) {
             const int j = __ffs(todo) - 1;
@@ -1897,7 +1899,8 @@ struct Softmax {
         }
         // Rows that may have met a non-finite V of a key they do not see: this warp's columns again
         const int seen0 = run.t0 * ROWS_KEYS, seen1 = min(run.t1 * ROWS_KEYS, run.len);
-        todo &= __ballot_sync(0xffffffffu, mine && !empty_l && fabsf(lt) < INFINITY && (lo > seen0 || hi < seen1));
+        todo &= __ballot_sync(0xffffffffu, mine && max(lo, seen0) < min(hi, seen1) && fabsf(lt) < INFINITY &&
+                                               (lo > seen0 || hi < seen1));
         __syncwarp();
         while (todo) {
             const int j = __ffs(todo) - 1;

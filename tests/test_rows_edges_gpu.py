@@ -1,0 +1,69 @@
+"""Rows attention where a unit is cut between CTAs, where tiles hold lanes without a row, where tables and
+offsets are wrong, and at the ends of the parameters' ranges (bounds in rows_harness)."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import split_kv_async_gb300 as F
+    from rows_harness import Problem, ints
+
+
+def _hide(x, b, t, value):
+    """V of key t of sequence b (-1: the prefix) of problem x becomes `value` in every column."""
+    block = x.p.block_size
+    if b < 0:
+        x.host.pv[t] = value
+        if block:
+            x.v_d[int(x.prefix_table[t // block]), t % block] = value
+        else:
+            x.pv[t] = value
+    else:
+        x.host.v[b][t] = value
+        if block:
+            x.v_d[int(x.table[b, t // block]), t % block] = value
+        else:
+            x.v_d[b, t] = value
+
+
+def _ends(row, pos, total):        # even rows see the last 60 keys, odd ones the first 60
+    return (0, 60) if row % 2 else (total - 60, total)
+
+
+def _begin_or_end(row, pos, total):
+    return (0, 90) if row % 2 else (300, total)
+
+
+def _begin_or_all(row, pos, total):
+    return (0, 90) if row % 2 else (0, total)
+
+
+def _name(x):
+    return "-".join(f"{k}={getattr(v, '__name__', v)}".replace(" ", "") for k, v in x.items()) if isinstance(x, dict) else str(x)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("block", [0, 16])
+@pytest.mark.parametrize("kw,b,t", [
+    # positions on both sides of key 128, and a key that only the later ones see: with so few key tiles each is
+    # a part of its own, and the second tile's part holds rows that see none of its keys
+    (dict(seqs=[(5, 131)], hq=4, hkv=2), 0, 130),
+    (dict(seqs=[(9, 133)], hq=2, hkv=2), 0, 132),
+    (dict(seqs=[(20, 140)], hq=4, hkv=2), 0, 139),
+    (dict(seqs=[(40, 290)], hq=4, hkv=1), 0, 270),
+    (dict(seqs=[(150, 150)], hq=4, hkv=1), 0, 140),
+    # keys that no row sees between the two ranges that the rows see
+    (dict(seqs=[(6, 400)], hq=4, hkv=2, mask=_ends), 0, 200),
+    (dict(seqs=[(60, 400)], hq=4, hkv=2, mask=_ends), 0, 200),
+    (dict(seqs=[(60, 700)], hq=2, hkv=1, mask=_ends), 0, 300),
+    # the same in a prefix, which rows see the beginning or the end of
+    (dict(seqs=[(6, 20), (50, 50)], hq=4, hkv=2, prefix=420, mask=_begin_or_end), -1, 200),
+    (dict(seqs=[(3, 20), (2, 70)], hq=4, hkv=2, prefix=300, mask=_begin_or_all), -1, 299),
+], ids=_name)
+def test_hidden_values_in_cut_units(kw, b, t, block, value):
+    for d in (128, 64):
+        x = Problem(**kw, block=block, d=d, seed=21)
+        _hide(x, b, t, value)
+        x.check()
