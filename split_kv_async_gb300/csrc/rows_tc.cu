@@ -1310,7 +1310,8 @@ struct Softmax {
         RowToken tk{0, 0, 0, -1};
         if (live) tk = a.tok[tok];
         const bool mine = live && tk.rt >= 0;
-        // keys of this source that the row sees; a row that is not one masks nothing and is not written
+        // keys of this source that the row sees; a lane without a row masks nothing, is not written, and has no say in
+        // what the warp does for its rows (its scores may come from what shared memory held before the call)
         int lo = mine ? max(tk.lo - base, 0) : 0, hi = mine ? min(tk.hi - base, run.len) : INT32_MAX;
         if (mine && hi <= lo) lo = hi = 0;
         const bool empty = hi <= lo;
@@ -1374,7 +1375,7 @@ struct Softmax {
                 reg_fence32(x + 32);
                 if (MODE == MODE_CAP && ready_v) {
                     // (the polynomial's coefficients stay normal numbers from this ratio on)
-                    if (a.scale >= 1e-5f * a.cap && __all_sync(0xffffffffu, abs_max64(x) * a.scale <= CAP_NEAR * a.cap)) {
+                    if (a.scale >= 1e-5f * a.cap && __all_sync(0xffffffffu, !mine || abs_max64(x) * a.scale <= CAP_NEAR * a.cap)) {
                         // v = y (rate p(z^2)), the coefficients taken with their powers of z / y
                         const float zz = (a.scale / a.cap) * (a.scale / a.cap);
                         const float k0_ = rate, k1_ = -0.333324194f * zz * rate, k2_ = 0.132957518f * zz * zz * rate,
@@ -1430,7 +1431,7 @@ struct Softmax {
                 if (MODE == MODE_PLAIN) top *= rate;
                 if (count == 0) {
                     m = top;
-                } else if (__any_sync(0xffffffffu, top > (m == -INFINITY ? -INFINITY : m + RW_LAG))) {
+                } else if (__any_sync(0xffffffffu, mine && top > (m == -INFINITY ? -INFINITY : m + RW_LAG))) {
                     // move the frame, once the P V of the half before is complete (the one before that is: its
                     // buffer has held these scores since)
                     if (!rwait(bars.pvdone + 16 * S + 8 * (buf ^ 1u), (half ? nlow : ntile) - 1u, misc, a)) return false;

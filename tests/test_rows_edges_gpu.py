@@ -67,3 +67,42 @@ def test_hidden_values_in_cut_units(kw, b, t, block, value):
         x = Problem(**kw, block=block, d=d, seed=21)
         _hide(x, b, t, value)
         x.check()
+
+
+def _same_bits(x, between):
+    """x's output is the same, bit for bit, after each of the calls in `between`."""
+    outs = []
+    for f in between:
+        f()
+        x.out.fill_(x.fill)
+        outs.append(x.call().clone())
+    torch.cuda.synchronize()
+    assert F.fdpp_read_error(x.ws) == 0
+    for o in outs[1:]:
+        assert torch.equal(o.view(torch.int16), outs[0].view(torch.int16))
+    x.check()
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(cap=20.0), dict(cap=6.0, bias=True), dict(bias=True)], ids=_name)
+@pytest.mark.parametrize("hq,hkv,block", [(14, 2, 0), (3, 1, 16), (5, 1, 0), (6, 2, 16)])
+def test_bits_do_not_depend_on_what_shared_memory_held(hq, hkv, block, kw):
+    # 3, 5, 6 and 7 heads do not divide 128: a tile's last lanes hold no row, and their operand is what the SM's
+    # shared memory held before: here queries of next to no size, or of a size that grows a maximum by far more
+    # than the frames' lag from tile to tile; and keys past a sequence's end likewise
+    others = [Problem([(64, 600)] * 8, hq=32, hkv=8, d=128, block=block, q_gain=g, seed=31) for g in (1e-3, 60.0, 0.0)]
+    x = Problem([(90, 907), (40, 333), (7, 1001), (130, 130)], hq=hq, hkv=hkv, d=128, block=block, seed=32, **kw)
+    _same_bits(x, [o.call for o in others] * 2)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(cap=20.0)], ids=_name)
+@pytest.mark.parametrize("prefix", [0, 700])
+def test_bits_do_not_depend_on_rows_of_no_sequence(prefix, kw):
+    # (a tile's lanes past a sequence's last token hold the rows that follow)
+    x = Problem([(10, 907), (37, 611)], hq=4, hkv=1, d=128, prefix=prefix, lead=9, tail=30, seed=33, **kw)
+
+    def fill(gain):
+        gen = torch.Generator().manual_seed(5)
+        rows = (gain * torch.randn(39, 4, 128, generator=gen)).bfloat16().cuda()
+        x.q_d[:9], x.q_d[-30:] = rows[:9], rows[9:]
+
+    _same_bits(x, [lambda: fill(1e-3), lambda: fill(60.0), lambda: fill(float("nan"))])
