@@ -104,13 +104,14 @@ __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
     }
     const float cap_rate = a.cap > 0.f ? a.scale / a.cap : 0.f;
     const unsigned gmask = 0xffu << (lane & ~(LANES - 1));
+    unsigned bad_block = 0;
 
 #pragma unroll 2
     for (int t = k0 + grp; t < k1; t += GROUPS) {
         const bool pre = t < P;
         const long long off = key_offset(a, pre ? -1 : b, pre ? t : t - P, g);
         if (off < 0) {
-            bad |= FDPP_ERRBIT_BLOCK_TABLE;
+            bad_block = FDPP_ERRBIT_BLOCK_TABLE;
             continue;
         }
         const T* kp = static_cast<const T*>(pre && a.pk ? a.pk : a.k) + off;
@@ -163,6 +164,8 @@ __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
             for (int e = 0; e < E; ++e) o[h][e] = fmaf(p, vx[e], o[h][e]);
         }
     }
+    // a bad block is known to the groups that came by it alone
+    if (j == 0) rows_error(a, bad_block);
     __syncwarp();
 
     // join the groups: all of a head's maxima first, then sums in the common frame

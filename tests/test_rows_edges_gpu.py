@@ -106,3 +106,25 @@ def test_bits_do_not_depend_on_rows_of_no_sequence(prefix, kw):
         x.q_d[:9], x.q_d[-30:] = rows[:9], rows[9:]
 
     _same_bits(x, [lambda: fill(1e-3), lambda: fill(60.0), lambda: fill(float("nan"))])
+
+
+@pytest.mark.parametrize("dtype,kernel", [("f32", "AUTO"), ("bf16", "SIMT"), ("bf16", "TENSOR")])
+@pytest.mark.parametrize("kw,entry", [
+    # one key of the bad block is seen, or few, and not by the lanes that hold the first key of every sixteen
+    (dict(seqs=[(1, 17), (1, 50)], mask=lambda row, pos, total: (5 if total == 17 else 0, total)), 1),
+    (dict(seqs=[(1, 3), (1, 50)], prefix=500), 0),
+    (dict(seqs=[(1, 1000), (1, 50)], spare_len=1048), 62),
+    (dict(seqs=[(3, 33), (2, 50)]), 2),
+], ids=["begin", "prefix", "split", "tokens"])
+def test_bad_blocks_are_reported_by_every_kernel(kw, entry, dtype, kernel):
+    for bad in (-5, 1 << 20):
+        x = Problem(hq=4, hkv=2, d=64, block=16, dtype=dtype, kernel=getattr(F, "FDPP_KERNEL_" + kernel), seed=41, **kw)
+        x.check()
+        x.table[0, entry] = bad
+        got = x.call().clone()
+        torch.cuda.synchronize()
+        assert F.fdpp_read_error(x.ws) == F.FDPP_ERRBIT_BLOCK_TABLE
+        # the other sequence's rows are what they were
+        n = x.host.cu[1]
+        x.table[0, entry] = 0
+        assert torch.equal(got[n:], x.call()[n:])
