@@ -6,7 +6,8 @@
 // so K and V are read once for the four), sixteen keys are in flight per CTA, and each eight-lane
 // group keeps its own running max, sum and accumulator (the online softmax of every sixteenth key);
 // they are joined in a fixed order at the end. With few rows the keys are split over CTAs, and the
-// last CTA of a row to finish joins the splits, again in a fixed order. Bounded by latency on short
+// last CTA of a row to finish joins the splits, again in a fixed order. One CTA more checks the offsets
+// and lengths of all sequences (in the others it would cost them latency). Bounded by latency on short
 // contexts and by the L2's rate on long ones: the four-head chunks of a wide group each read the keys.
 #include <cuda_bf16.h>
 
@@ -56,6 +57,19 @@ __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = threadIdx.x / LANES, j = lane % LANES;
     const int chunks = (a.G + SH - 1) / SH;
     grid_dependency_wait();
+    if (blockIdx.x == gridDim.x - 1) {           // looks at all offsets and lengths, those without rows too
+        unsigned bad = 0;
+        if (blockIdx.y == 0) {
+            prefix_keys(a, bad);
+            for (int b = threadIdx.x; b < a.B; b += SW * 32) {
+                int c0;
+                seq_rows(a, b, c0, bad);
+                own_len(a, b, bad);
+            }
+        }
+        rows_error(a, bad);
+        return;
+    }
     long long unit = blockIdx.x;
     const int chunk = (int)(unit % chunks);
     unit /= chunks;
@@ -63,7 +77,7 @@ __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
     const int h0 = g * a.G + chunk * SH, nh = min(SH, a.G - chunk * SH);
 
     // the row's sequence: the last one that starts at or before it and has rows
-    unsigned bad = 0;
+    unsigned bad = 0;                            // (reported by the last CTA)
     int b = 0, c0 = 0, n = 0;
     if (a.cu) {
         int lo = 0, hi = a.B;
@@ -76,10 +90,7 @@ __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
         b = row / a.per_seq;
     }
     n = seq_rows(a, b, c0, bad);
-    if (row < c0 || row >= c0 + n) {             // a row of no sequence: left as it was
-        if (threadIdx.x == 0) rows_error(a, bad);
-        return;
-    }
+    if (row < c0 || row >= c0 + n) return;       // a row of no sequence: left as it was
     const int P = prefix_keys(a, bad), L = own_len(a, b, bad);
     const int pos = P + L - n + (row - c0);
     int lo, hi;
@@ -213,7 +224,6 @@ __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
         }
         if (a.splits > 1 && threadIdx.x == 0) a.row_ml[slot0 + h * a.splits + split] = make_float2(m[h], l[h]);
     }
-    if (threadIdx.x == 0) rows_error(a, bad);
     if (a.splits == 1) return;
 
     // the last CTA of the row joins its splits
@@ -270,7 +280,7 @@ cudaError_t launch_rows_simt(const RowsArgs& a, int dtype, cudaStream_t s)
                                                              : rows_simt_kernel<__nv_bfloat16, 64>);
     const int chunks = (a.G + ROWS_SIMT_HEADS - 1) / ROWS_SIMT_HEADS;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)a.T * a.Hkv * chunks), (unsigned)a.splits);
+    cfg.gridDim = dim3((unsigned)((long long)a.T * a.Hkv * chunks + 1), (unsigned)a.splits);      // (the last one checks)
     cfg.blockDim = dim3(SW * 32);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

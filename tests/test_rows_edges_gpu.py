@@ -128,3 +128,29 @@ def test_bad_blocks_are_reported_by_every_kernel(kw, entry, dtype, kernel):
         n = x.host.cu[1]
         x.table[0, entry] = 0
         assert torch.equal(got[n:], x.call()[n:])
+
+
+@pytest.mark.parametrize("kernel", ["TENSOR", "SIMT"])
+def test_bad_offsets_and_lengths_are_reported_by_every_kernel(kernel):
+    kernel = getattr(F, "FDPP_KERNEL_" + kernel)
+    for cu in ([0, 2, 1], [-4, 1, 2], [0, 9, 2], [0, 1, 9], [2, 1, 0], [0, 0, -1], [5, 2, 2]):
+        x = Problem([(1, 40), (1, 50)], hq=2, hkv=1, seed=1, kernel=kernel)
+        x.cu_d.copy_(ints(cu))
+        x.call()
+        torch.cuda.synchronize()
+        assert F.fdpp_read_error(x.ws) == F.FDPP_ERRBIT_TOKENS, cu
+    # lengths of sequences with tokens and without
+    for at in (0, 1, 170):
+        x = Problem([(1, 40)] + [(0, 50)] * 180, hq=2, hkv=1, seed=1, kernel=kernel)
+        x.check()
+        x.lens_d[at] = 51 if at else -3
+        x.call()
+        torch.cuda.synchronize()
+        assert F.fdpp_read_error(x.ws) == F.FDPP_ERRBIT_SEQ_LEN, at
+    # a batch in which no sequence has tokens
+    x = Problem([(0, 40), (0, 50)], hq=2, hkv=1, seed=1, kernel=kernel, tail=1, prefix=20)
+    x.check()
+    x.plen_d.fill_(21)
+    x.call()
+    torch.cuda.synchronize()
+    assert F.fdpp_read_error(x.ws) == F.FDPP_ERRBIT_PREFIX
