@@ -1374,8 +1374,9 @@ struct Softmax {
                 reg_fence32(x);
                 reg_fence32(x + 32);
                 if (MODE == MODE_CAP && ready_v) {
-                    // (the polynomial's coefficients stay normal numbers from this ratio on)
-                    if (a.scale >= 1e-5f * a.cap && __all_sync(0xffffffffu, !mine || abs_max64(x) * a.scale <= CAP_NEAR * a.cap)) {
+                    // (between these ratios the polynomial's coefficients are normal numbers: (scale / cap)^6 and the
+                    // largest cap leave them below 2^125)
+                    if (a.scale >= 1e-5f * a.cap && a.scale <= 1e5f * a.cap && __all_sync(0xffffffffu, !mine || abs_max64(x) * a.scale <= CAP_NEAR * a.cap)) {
                         // v = y (rate p(z^2)), the coefficients taken with their powers of z / y
                         const float zz = (a.scale / a.cap) * (a.scale / a.cap);
                         const float k0_ = rate, k1_ = -0.333324194f * zz * rate, k2_ = 0.132957518f * zz * zz * rate,

@@ -154,3 +154,24 @@ def test_bad_offsets_and_lengths_are_reported_by_every_kernel(kernel):
     x.call()
     torch.cuda.synchronize()
     assert F.fdpp_read_error(x.ws) == F.FDPP_ERRBIT_PREFIX
+
+
+@pytest.mark.parametrize("scale,cap", [(10.0, 1e-6), (1.0, 1e-9), (3.0, 1e-5), (1e-6, 4000.0), (4e8, 4000.0)])
+def test_caps_far_from_their_scale(scale, cap):
+    # 64 tokens with queries of size zero before the others (whole tiles of them): their scores are 0 whatever the
+    # ratio of scale and cap
+    for d, seqs in ((128, [(100, 300), (1, 200)]), (64, [(150, 400)])):
+        x = Problem(seqs, hq=4, hkv=1, d=d, scale=scale, cap=cap, seed=51)
+        for t in (x.q_d, x.q, x.host.q):
+            t[:64] = 0
+        if cap < 1:
+            x.check()
+            continue
+        # scores far below their cap, or at it (the scores of a row are equal then): finite, and the rows of
+        # zeros the mean of their values
+        got = x.call()
+        torch.cuda.synchronize()
+        assert F.fdpp_read_error(x.ws) == 0 and torch.isfinite(got.float()).all()
+        ref, spread = __import__("rows_reference").attention(x.host)
+        err = np.abs(got.double().cpu().numpy() - ref)
+        assert (err <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * spread)[:64].all()
