@@ -688,8 +688,11 @@ fdpp_status fdpp_rope_append(const void* q, const void* k, const void* v, const 
 fdpp_status fdpp_read_error(const void* workspace, uint32_t* error_bits)
 {
     if (!workspace || !error_bits) return cfail(FDPP_ERR_INVALID_ARG, "null pointer");
-    const cudaError_t e = cudaMemcpy(error_bits, workspace, 4, cudaMemcpyDeviceToHost);
-    if (e != cudaSuccess) return cfail(FDPP_ERR_CUDA, "cudaMemcpy: %s", cudaGetErrorString(e));
+    // the copy waits for the legacy stream alone, not for non-blocking streams
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return cfail(FDPP_ERR_CUDA, "cudaDeviceSynchronize: %s", cudaGetErrorString(e));
+    if ((e = cudaMemcpy(error_bits, workspace, 4, cudaMemcpyDeviceToHost)) != cudaSuccess)
+        return cfail(FDPP_ERR_CUDA, "cudaMemcpy: %s", cudaGetErrorString(e));
     return FDPP_OK;
 }
 
