@@ -518,8 +518,11 @@ fdpp_status fdpp_flat_gemm(const void* x, const void* w, void* y, int M, int N, 
 fdpp_status fdpp_flat_gemm_read_error(const void* workspace, uint32_t* error_bits)
 {
     if (!workspace || !error_bits) return gfail(FDPP_ERR_INVALID_ARG, "null pointer");
-    cudaError_t e = cudaMemcpy(error_bits, workspace, 4, cudaMemcpyDeviceToHost);
-    if (e != cudaSuccess) return gfail(FDPP_ERR_CUDA, "cudaMemcpy: %s", cudaGetErrorString(e));
+    // the copy waits for the legacy stream alone, not for non-blocking streams
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return gfail(FDPP_ERR_CUDA, "cudaDeviceSynchronize: %s", cudaGetErrorString(e));
+    if ((e = cudaMemcpy(error_bits, workspace, 4, cudaMemcpyDeviceToHost)) != cudaSuccess)
+        return gfail(FDPP_ERR_CUDA, "cudaMemcpy: %s", cudaGetErrorString(e));
     return FDPP_OK;
 }
 

@@ -30,3 +30,17 @@ def test_reading_errors_waits_for_every_stream():
     call()
     assert F.fdpp_read_error(ws) == F.FDPP_ERRBIT_SLOT
     assert s.query()
+
+
+def test_reading_a_linears_errors_waits_for_every_stream():
+    M, N, K = 8, 256, 256
+    x, w = torch.randn(M, K).bfloat16().cuda(), torch.randn(N, K).bfloat16().cuda()
+    y, ws, s = torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), F.alloc_flat_gemm_workspace(M, N, K), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    F.fdpp_flat_gemm(x, w, y, ws, stream=s)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)
+    F.fdpp_flat_gemm(x, w, y, ws, stream=s)
+    assert F.fdpp_flat_gemm_read_error(ws) == 0
+    assert s.query()                        # the call is over
