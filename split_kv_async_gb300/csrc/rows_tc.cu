@@ -50,7 +50,8 @@
 // columns computed again from the keys that it sees.
 //
 // Every wait is bounded; a wait that runs out sets FDPP_ERRBIT_TIMEOUT, and the CTA lets its copies and
-// MMAs land, frees its tensor memory and exits.
+// MMAs land, frees its tensor memory and exits. Rows that are computed again can hold the others up for longer
+// (128 rows of 16384 keys, d = 128: 0.3 s), so a wait begins anew as long as their warps show signs of life.
 #include <cuda_bf16.h>
 
 #include "rows_common.cuh"
@@ -153,14 +154,41 @@ struct RowsBars {
     }
 };
 
+// Shared words besides the barriers: the CTA gives up; signs of life of warps that compute rows again (which can
+// take seconds: every key of a long context, for each row); runs whose sums a warp has told.
+enum { MISC_ABORT = 0, MISC_BEAT = 1, MISC_TOLD = 4 };
+
+__device__ __forceinline__ void beat(volatile int* misc)
+{
+    if ((threadIdx.x & 31) == 0) atomicAdd(const_cast<int*>(misc) + MISC_BEAT, 1);
+}
+
+// Whether a wait that began at t0 has run out: no sign of life for FDPP_WAIT_NS. last: beats at the check before.
+__device__ __forceinline__ bool run_out(volatile int* misc, uint64_t& t0, int& last)
+{
+    if (global_ns() - t0 <= FDPP_WAIT_NS) return false;
+    const int now = misc[MISC_BEAT];
+    if (now == last) return true;
+    last = now;
+    t0 = global_ns();
+    return false;
+}
+
 // All lanes wait. A wait that is over when asked for costs two instructions; otherwise it is bounded, and
 // one that runs out aborts the CTA (warp-uniform result).
 __device__ __forceinline__ bool rwait_slow(uint32_t bar, uint32_t parity, volatile int* misc, unsigned* err)
 {
-    bool ok = (misc[0] == 0) && mbar_wait(bar, parity);
+    bool ok = misc[MISC_ABORT] == 0;
+    if (ok) {
+        uint64_t t0 = global_ns();
+        int last = 0;
+        for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+            if ((it & 63u) == 0 && run_out(misc, t0, last)) { ok = false; break; }
+        }
+    }
     ok = __all_sync(0xffffffffu, ok);
     if (!ok && (threadIdx.x & 31) == 0) {
-        misc[0] = 1;
+        misc[MISC_ABORT] = 1;
         atomicOr(err, FDPP_ERRBIT_TIMEOUT);
     }
     return ok;
@@ -1047,13 +1075,15 @@ struct RowsPv {
 // col + 32 i, or is not known (its block lies outside the pool). If not, a row that is not finite got there
 // by the keys that it sees. (Any lo and hi: t only grows.)
 template <int D, int NC>
-__device__ __noinline__ bool unseen_values(const RowsArgs& a, int b, int g, int k0, int lo, int hi, int k1, int col)
+__device__ __noinline__ bool unseen_values(const RowsArgs& a, int b, int g, int k0, int lo, int hi, int k1, int col,
+                                           volatile int* misc)
 {
     const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(b < 0 && a.pv ? a.pv : a.v);
     bool found = false;
     for (int t = k0; t < k1; ++t) {
         if (t >= lo && t < hi) t = hi;
         if (t >= k1) break;
+        if (((t - k0) & 1023) == 0) beat(misc);
         const long long off = key_offset(a, b, t, g);
         found = found || off < 0;
         if (off >= 0)
@@ -1068,7 +1098,7 @@ __device__ __noinline__ bool unseen_values(const RowsArgs& a, int b, int g, int 
 // o: its columns col + 32 i of each lane.
 template <int D, int NC>
 __device__ __noinline__ void redo_row(const RowsArgs& a, int b, int g, int h, int row, int pos, int k0, int k1, int base,
-                                      float M, int col, float (&o)[NC])
+                                      float M, int col, float (&o)[NC], volatile int* misc)
 {
     const int lane = threadIdx.x & 31;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + ((long long)row * a.Hq + h) * D;
@@ -1081,6 +1111,7 @@ __device__ __noinline__ void redo_row(const RowsArgs& a, int b, int g, int h, in
 #pragma unroll
     for (int i = 0; i < NC; ++i) o[i] = 0.f;
     for (int t = k0; t < k1; t += 4) {
+        if (((t - k0) & 4095) == 0) beat(misc);
         long long off[4];
         float s[4], v[4][NC];
 #pragma unroll
@@ -1604,6 +1635,7 @@ struct Softmax {
                            (lo > seen0 || hi < seen1);
         unsigned todo = __ballot_sync(0xffffffffu, again);
         while (todo) {
+            beat(misc);
             const int j = __ffs(todo) - 1;
             todo &= todo - 1;
             const int jtok = __shfl_sync(0xffffffffu, tok, j), jhead = __shfl_sync(0xffffffffu, head, j);
@@ -1611,9 +1643,9 @@ struct Softmax {
             const int jlo = max(__shfl_sync(0xffffffffu, lo, j), seen0), jhi = min(__shfl_sync(0xffffffffu, hi, j), seen1);
             const float jm = __shfl_sync(0xffffffffu, m, j), jl = __shfl_sync(0xffffffffu, l, j);
             const long long jat = __shfl_sync(0xffffffffu, at, j);
-            if (!unseen_values<D, D / 32>(a, run.b, run.g, seen0, jlo, jhi, seen1, lane)) continue;
+            if (!unseen_values<D, D / 32>(a, run.b, run.g, seen0, jlo, jhi, seen1, lane, misc)) continue;
             float o[D / 32];
-            redo_row<D, D / 32>(a, run.b, run.g, jhead, jtok, jpos, jlo, jhi, base, jm == -INFINITY ? 0.f : jm, lane, o);
+            redo_row<D, D / 32>(a, run.b, run.g, jhead, jtok, jpos, jlo, jhi, base, jm == -INFINITY ? 0.f : jm, lane, o, misc);
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 if (direct) static_cast<__nv_bfloat16*>(a.out)[jat * D + lane + 32 * i] = __float2bfloat16_rn(o[i] / jl);
@@ -1633,22 +1665,23 @@ struct Softmax {
         __syncwarp();
         if ((threadIdx.x & 31) == 0) {
             __threadfence_block();
-            misc[4 + (threadIdx.x >> 5)] = (int)nh + 1;
+            misc[MISC_TOLD + (threadIdx.x >> 5)] = (int)nh + 1;
         }
         __syncwarp();
     }
     __device__ __forceinline__ bool told(int s) const
     {
         const int lane = threadIdx.x & 31;
-        const uint64_t t0 = global_ns();
+        uint64_t t0 = global_ns();
+        int last = 0;
         for (uint32_t it = 1;; ++it) {
-            const int v = lane < 4 ? misc[4 + 4 * s + lane] : INT32_MAX;
+            const int v = lane < 4 ? misc[MISC_TOLD + 4 * s + lane] : INT32_MAX;
             if (__all_sync(0xffffffffu, v > (int)nh)) break;
             if ((it & 63u) == 0) {
-                const bool late = misc[0] != 0 || global_ns() - t0 > FDPP_WAIT_NS;
+                const bool late = misc[MISC_ABORT] != 0 || run_out(misc, t0, last);
                 if (__any_sync(0xffffffffu, late)) {
                     if (lane == 0) {
-                        misc[0] = 1;
+                        misc[MISC_ABORT] = 1;
                         rows_error(a, FDPP_ERRBIT_TIMEOUT);
                     }
                     return false;
@@ -1905,6 +1938,7 @@ struct Softmax {
                                                (lo > seen0 || hi < seen1));
         __syncwarp();
         while (todo) {
+            beat(misc);
             const int j = __ffs(todo) - 1;
             todo &= todo - 1;
             const int jtok = __shfl_sync(0xffffffffu, tok, j), jhead = __shfl_sync(0xffffffffu, head, j);
@@ -1912,9 +1946,9 @@ struct Softmax {
             const int jlo = max(__shfl_sync(0xffffffffu, lo, j), seen0), jhi = min(__shfl_sync(0xffffffffu, hi, j), seen1);
             const float jm = __shfl_sync(0xffffffffu, m, j), inv = __shfl_sync(0xffffffffu, inv_l, j);
             const long long jat = __shfl_sync(0xffffffffu, at, j);
-            if (!unseen_values<D, 1>(a, run.b, run.g, seen0, jlo, jhi, seen1, d)) continue;
+            if (!unseen_values<D, 1>(a, run.b, run.g, seen0, jlo, jhi, seen1, d, misc)) continue;
             float o[1];
-            redo_row<D, 1>(a, run.b, run.g, jhead, jtok, jpos, jlo, jhi, base, jm == -INFINITY ? 0.f : jm, d, o);
+            redo_row<D, 1>(a, run.b, run.g, jhead, jtok, jpos, jlo, jhi, base, jm == -INFINITY ? 0.f : jm, d, o, misc);
             if (has) {
                 if (direct) static_cast<__nv_bfloat16*>(a.out)[jat * D + d] = __float2bfloat16_rn(o[0] * inv);
                 else pbase[jat * D + d] = o[0];

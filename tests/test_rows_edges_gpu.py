@@ -175,3 +175,33 @@ def test_caps_far_from_their_scale(scale, cap):
         ref, spread = __import__("rows_reference").attention(x.host)
         err = np.abs(got.double().cpu().numpy() - ref)
         assert (err <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * spread)[:64].all()
+
+
+def test_rows_computed_again_may_take_longer_than_a_wait():
+    # the newest token of every sequence holds a NaN, 160000 keys behind it: the rows that do not see it are
+    # computed again, for some seconds, while the warps that feed the next unit wait
+    B, L, n, G, hkv, d, pool, block = 24, 160000, 16, 8, 8, 64, 64, 256
+    width = L // block
+    gen = torch.Generator("cuda").manual_seed(61)
+    k, v = (torch.randn(pool, block, hkv, d, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    table = np.random.default_rng(61).integers(0, pool - 1, (B, width))
+    table[:, -1] = pool - 1                                  # the block with the NaN, nowhere else
+    q = torch.randn(B * n, G * hkv, d, generator=gen, device="cuda").bfloat16()
+    p = F.make_rows_params(batch=B, num_q_heads=G * hkv, num_kv_heads=hkv, head_dim=d, dtype=F.FDPP_BF16, num_tokens=B * n,
+                           max_seq_len=L, scale=d ** -0.5, block_size=block, max_blocks_per_seq=width, num_kv_blocks=pool)
+    ws, table, lens = F.alloc_rows_workspace(p), ints(table), ints([L] * B)
+
+    def call(values):
+        out = torch.empty_like(q)
+        F.fdpp_rows_attn(q, k, values, table, lens, None, p, ws, out)
+        torch.cuda.synchronize()
+        assert F.fdpp_read_error(ws) == 0
+        return out.double().view(B, n, G * hkv, d)
+
+    clean, spread = call(v), call(v.abs())                   # (spread: sum_t p_t |v_t|, 2^-7 of itself off)
+    v[pool - 1, block - 1] = float("nan")
+    got = call(v)
+    assert torch.isnan(got[:, -1]).all()
+    # both calls are within the operator's bounds of the formula
+    bound = 2.0 ** -8 * 2 * clean.abs() + 2 * (2.0 ** -8 + 2.0 ** -12) * (1 + 2.0 ** -6) * spread
+    assert ((got - clean).abs() <= bound)[:, :-1].all()
