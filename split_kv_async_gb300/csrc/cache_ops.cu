@@ -112,7 +112,8 @@ __device__ __forceinline__ unsigned map_rows(const MapArgs& a, int first, int st
     unsigned bad = 0;
     const int total = a.p_cu[a.B], bs = 1 << a.shift;
     const int head = a.p_pool[0];
-    for (int r = first; r < a.room; r += step) {
+    for (unsigned r0 = first; r0 < (unsigned)a.room; r0 += step) {       // (unsigned: room may be 2^31 - 1)
+        const int r = (int)r0;
         int b = -1, pos = 0;
         long long slot = -1;
         if (r < total) {
@@ -123,7 +124,7 @@ __device__ __forceinline__ unsigned map_rows(const MapArgs& a, int first, int st
             }
             b = lo;
             pos = a.p_held[b] + (r - a.p_cu[b]);
-            const int j = pos >> a.shift, had = (a.p_held[b] + bs - 1) >> a.shift;
+            const int j = pos >> a.shift, had = (int)(((long long)a.p_held[b] + bs - 1) >> a.shift);
             int block;
             if (j < had) {
                 block = a.table[(long long)b * a.width + j];
@@ -140,7 +141,8 @@ __device__ __forceinline__ unsigned map_rows(const MapArgs& a, int first, int st
     }
     // freed blocks, behind the free ones: the queue entries written are none of those read above
     const int freed = a.p_back[a.B], tail = wrap((long long)head + a.p_pool[1], a.cap);
-    for (int i = first; i < freed; i += step) {
+    for (unsigned i0 = first; i0 < (unsigned)freed; i0 += step) {
+        const int i = (int)i0;
         int lo = 0, hi = a.B;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -556,14 +558,14 @@ fdpp_status fdpp_block_map(const int32_t* held_lens, const int32_t* want_lens, c
         const bool one = a.room <= MAP_ONE_CTA_ROWS;
         const int work = one ? std::max(a.B, a.room) : std::max(a.B, 256);
         const int threads = std::min(MAP_THREADS, std::max(64, (work + 31) / 32 * 32));
-        const int grid = one ? 1 : std::min(2 * sms, (a.room + threads - 1) / threads);
+        const int grid = one ? 1 : (int)std::min<long long>(2 * sms, ((long long)a.room + threads - 1) / threads);
         e = launch_pdl(block_map_kernel<true, true>, dim3((unsigned)grid), threads, s, a);
     } else if (a.room <= MAP_ONE_CTA_ROWS) {
         e = launch_pdl(block_map_kernel<true, false>, dim3(1), MAP_THREADS, s, a);
     } else {
         e = launch_pdl(block_map_kernel<false, false>, dim3(1), MAP_THREADS, s, a);
         if (e == cudaSuccess) {
-            const int grid = std::min((a.room + 255) / 256, sms * 8);
+            const int grid = (int)std::min<long long>(((long long)a.room + 255) / 256, sms * 8);
             e = launch_pdl(block_map_rows_kernel, dim3((unsigned)grid), 256, s, a);
         }
     }
