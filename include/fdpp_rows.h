@@ -64,9 +64,9 @@ typedef struct fdpp_rows_params {
     int max_prefix_len;      /* fdpp_prefix_attn: an upper bound on the prefix length, and the row
                                 count of prefix_k and prefix_v (contiguous) or
                                 ceil(max_prefix_len / block_size) the length of prefix_blocks */
-    float scale;             /* positive and finite */
-    float softcap;           /* > 0: scores are capped at +-softcap (tensor kernel:
-                                at most FDPP_ROWS_MAX_SOFTCAP); 0: not */
+    float scale;             /* positive; scale log2(e) must be finite */
+    float softcap;           /* > 0: scores are capped at +-softcap (softcap log2(e) must be
+                                finite; tensor kernel: at most FDPP_ROWS_MAX_SOFTCAP); 0: not */
     const float* slopes;     /* DEVICE float [Hq], 4-byte aligned, or NULL */
     const int32_t* key_begin;  /* DEVICE int32 [T], 4-byte aligned: first key each token row sees,
                                 or NULL (0) */

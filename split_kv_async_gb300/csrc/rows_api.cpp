@@ -61,10 +61,11 @@ fdpp_status check_params(const fdpp_rows_params* p)
     if (p->num_tokens < 1) return rfail(FDPP_ERR_INVALID_ARG, "num_tokens must be >= 1");
     if (p->max_seq_len < 1) return rfail(FDPP_ERR_INVALID_ARG, "max_seq_len must be >= 1");
     if (p->max_prefix_len < 0) return rfail(FDPP_ERR_INVALID_ARG, "max_prefix_len must be >= 0");
-    if (!std::isfinite(p->scale) || !(p->scale > 0.f))
-        return rfail(FDPP_ERR_INVALID_ARG, "scale must be positive and finite (got %g)", (double)p->scale);
-    if (!std::isfinite(p->softcap) || p->softcap < 0.f)
-        return rfail(FDPP_ERR_INVALID_ARG, "softcap must be 0 or positive and finite (got %g)", (double)p->softcap);
+    // (both are turned into units of log2: an infinite factor would make NaN of a score of 0)
+    if (!std::isfinite(p->scale * 1.4426950f) || !(p->scale > 0.f))
+        return rfail(FDPP_ERR_INVALID_ARG, "scale must be positive, and scale * log2(e) finite (got %g)", (double)p->scale);
+    if (!std::isfinite(p->softcap * 1.4426950f) || p->softcap < 0.f)
+        return rfail(FDPP_ERR_INVALID_ARG, "softcap must be 0 or positive, and softcap * log2(e) finite (got %g)", (double)p->softcap);
     // the tensor kernel's tanh is off by a few 2^-23 softcap: above this limit by more than its weights are
     if (tensor_kernel(*p) && p->softcap > FDPP_ROWS_MAX_SOFTCAP)
         return rfail(FDPP_ERR_UNSUPPORTED, "softcap %g > %g", (double)p->softcap, (double)FDPP_ROWS_MAX_SOFTCAP);

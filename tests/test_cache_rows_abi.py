@@ -254,3 +254,14 @@ def test_rows_softcap_limit_is_the_tensor_kernels():
     with pytest.raises(F.FdppError) as e:
         F.fdpp_rows_workspace_size(_rows(softcap=big))
     assert e.value.status == F.FDPP_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("field", ["scale", "softcap"])
+def test_rows_reject_factors_that_overflow(field):
+    # the kernels work in units of log2: a factor times log2(e) beyond fp32 would make NaN of a score of 0
+    for dtype in (F.FDPP_F32, F.FDPP_BF16):
+        p = _rows(dtype=dtype, **{"scale": 0.1, field: 3e38})
+        n = ctypes.c_size_t(0)
+        assert F.lib.fdpp_rows_workspace_size(ctypes.byref(p), ctypes.byref(n)) == F.FDPP_ERR_INVALID_ARG
+        assert _attend(p) == F.FDPP_ERR_INVALID_ARG
+    assert F.fdpp_rows_workspace_size(_rows(**{"scale": 0.1, "dtype": F.FDPP_F32, field: 2e38})) > 0
