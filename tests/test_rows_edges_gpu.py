@@ -205,3 +205,12 @@ def test_rows_computed_again_may_take_longer_than_a_wait():
     # both calls are within the operator's bounds of the formula
     bound = 2.0 ** -8 * 2 * clean.abs() + 2 * (2.0 ** -8 + 2.0 ** -12) * (1 + 2.0 ** -6) * spread
     assert ((got - clean).abs() <= bound)[:, :-1].all()
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(prefix=140), dict(mask=_begin_or_all)], ids=_name)
+@pytest.mark.parametrize("uniform", [False, True])
+def test_plans_of_more_sequences_than_their_shared_memory_holds(kw, uniform):
+    # 2100 sequences and more: lengths, offsets and the row tiles' starts are read from global memory
+    rng = np.random.default_rng(71)
+    seqs = [(2 if uniform else int(rng.integers(0, 4)), int(rng.integers(0, 150))) for _ in range(2100)]
+    Problem(seqs, hq=2, hkv=1, d=64, block=16, seed=71, uniform=uniform, **kw).check()
