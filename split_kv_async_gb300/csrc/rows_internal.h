@@ -51,7 +51,7 @@ constexpr size_t ROWS_OFF_COUNTERS = 256;
 constexpr size_t ROWS_OFF_PLAN = ROWS_OFF_COUNTERS + ROWS_COUNTERS * 4;
 
 // Plan header words, then the first row tile of each part.
-enum { RP_NRT = 0, RP_NPRE = 1, RP_TILES = 2, RP_PREFIX = 3, RP_ROWS = 4, RP_WORDS = 16 };
+enum { RP_NRT = 0, RP_NPRE = 1, RP_TILES = 2, RP_PREFIX = 3, RP_WORDS = 16 };
 
 struct RowsArgs {
     const void* q;
@@ -79,7 +79,7 @@ struct RowsArgs {
     float* row_o;                   // [2][T][Hq][D]: whole units of a call with a prefix (prefix, own)
     float2* row_ml;                 // [2][T][Hq]
     int B, Hq, Hkv, G, D, T, per_seq;
-    int max_seq_len, block_size, max_blocks, num_blocks, max_prefix, prefix_width;
+    int max_seq_len, block_size, max_blocks, num_blocks, max_prefix;
     int tpt, tpn;                   // tokens per 128-row tile and per key-major run: floor(128 / G), floor(32 / G)
     int max_rt, slot_rows, parts, splits, stages;
     float scale, cap;

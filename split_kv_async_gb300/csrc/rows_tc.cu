@@ -20,8 +20,10 @@
 //            scores, and a stream's softmax and MMAs took turns; and with one warp for both products its
 //            own instructions, between those of two busy softmax warps, set the pace.
 //   warps 0-3, 4-7   the softmax of streams 0 and 1: a thread owns a row (tensor-memory lane), reads its
-//            64 scores, and writes P as bf16 over them. P's rounding (2^-9 of each weight, independent)
-//            leaves an error of the order of the output's own rounding; l sums the unrounded weights.
+//            64 scores, and writes P as bf16 over them. P's rounding (up to half a step, 2^-8 of each weight,
+//            independent) leaves at most as much of sum_t p_t |v_t|, and an error of the order of the output's own
+//            rounding on average (its two bf16 parts, which the decode kernels keep, would take a second P V: half
+//            as many MMAs again in what bounds prompts); l sums the unrounded weights.
 // With more than 128 rows a unit is a pair: two row tiles, one per stream, share every K/V tile. With
 // fewer, both streams take the same rows, alternate key tiles and are joined at the run's end.
 //
@@ -845,9 +847,9 @@ struct RowsLoader {
 // ------------------------------------------------------------------------------------------
 // MMA warp
 // ------------------------------------------------------------------------------------------
-// Tensor memory: the scores of streams 0 and 1 (128 columns each; P takes the first 64 of them, or the
-// first 16 or 32 hold S^T of a key-major run), then their accumulators (D columns each; O^T of a key-major
-// run takes 16 or 32).
+// Tensor memory: the scores of streams 0 and 1 (128 columns each: two buffers of 64, the first 32 columns of
+// which P takes over; a key-major run's S^T has the first 16 or 32 of the 128), then their accumulators (D
+// columns each; O^T of a key-major run takes 16 or 32).
 constexpr uint32_t TM_S = ROWS_KEYS;
 
 // A value that is the same in all lanes, told to the compiler.
@@ -1247,7 +1249,6 @@ __device__ __forceinline__ void tmem_st_rows(uint32_t taddr, const uint32_t (&r)
                      : "memory");
 }
 
-// Ties the registers to the tcgen05.wait::ld before it.
 __device__ __forceinline__ float abs_max64(const uint32_t* y)
 {
     float m[4] = {0.f, 0.f, 0.f, 0.f};
@@ -1265,6 +1266,7 @@ __device__ __forceinline__ float abs_max64(const uint32_t* y)
 // scores are near, and 755 by the other form.
 constexpr float CAP_NEAR = 0.35f;
 
+// Ties the registers to the tcgen05.wait::ld before it.
 template <int NR>
 __device__ __forceinline__ void reg_fence(uint32_t (&r)[NR])
 {
@@ -1284,8 +1286,8 @@ struct Softmax {
     uint32_t tmem;
     volatile int* misc;
     int S;                   // the stream
-    // phases passed: headers, this stream's tiles, and the lower halves of those in 128-row runs, runs of either stream's accumulator, its own
-    // hand-overs, meetings of this stream's warps, Q buffers
+    // phases passed: headers, this stream's tiles, and the lower halves of those in 128-row runs, runs of either
+    // stream's accumulator, its own hand-overs, meetings of this stream's warps, Q buffers
     uint32_t nh = 0, ntile = 0, nlow = 0, nacc = 0, nacc_o = 0, nml = 0, nvote = 0, nqn = 0;
 
     struct Run {
