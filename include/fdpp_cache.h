@@ -93,7 +93,9 @@ typedef enum {
     FDPP_ROPE_PARTS = 3      /* theta_i (k_i + (1 - k_i) / factor), where
                                 k_i = clamp((turns_i - low_turns) / (high_turns - low_turns), 0, 1)
                                 and turns_i = context theta_i / (2 pi): pairs that turn often
-                                within the trained context keep their angle */
+                                within the trained context keep their angle. (Code that ramps over
+                                the pair's index i between two borders makes other angles: fill the
+                                table for it yourself.) */
 } fdpp_rope_scaling;
 
 /* Angles of the rotation (host only, no CUDA call), computed in 64 bits. table: HOST float

@@ -8,7 +8,9 @@
 // they are joined in a fixed order at the end. With few rows the keys are split over CTAs, and the
 // last CTA of a row to finish joins the splits, again in a fixed order. One CTA more checks the offsets
 // and lengths of all sequences (in the others it would cost them latency). Bounded by latency on short
-// contexts and by the L2's rate on long ones: the four-head chunks of a wide group each read the keys.
+// contexts (one token on 256 keys, 4 heads of 64: 6.5 us, two dependent passes over L2) and by the L2's rate on
+// long ones: the four-head chunks of a wide group, and the tokens of a prompt or behind a prefix, each read the
+// keys again.
 #include <cuda_bf16.h>
 
 #include "rows_common.cuh"

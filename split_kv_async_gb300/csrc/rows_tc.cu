@@ -33,10 +33,10 @@
 // What bounds it. Many rows: the tensor pipe (4 x 128 keys x 128 rows x d FLOP per row tile and key tile, 1024
 // cycles for d = 128; a half tile's Q K^T, N = 64, runs at two thirds of the rate, which makes them 1280) with the
 // softmax beside it (512 cycles of the MUFU units for the exponentials, and its other instructions). A prompt of
-// 8192 tokens, 32 heads, 8 kv heads, d = 128: 426 us, 1.28 PFLOP/s of the 1.87 that a plain matrix product was
-// measured at; with a bias 474; with a cap 642 (scores near it 755: an exponential and half a reciprocal more for each).
+// 8192 tokens, 32 heads, 8 kv heads, d = 128: 426 us, 1.29 PFLOP/s of the 1.87 that a plain matrix product was
+// measured at; with a bias 485; with a cap 631 (scores near it 838: an exponential and half a reciprocal more for each).
 // Few rows: HBM (K and V of a kv head are read once, at 512 bytes
-// per key for d = 128): 64 sequences of 512 to 16384 keys, 64 heads, 8 kv heads, with a cap: 339.5 us, 6.48 TB/s,
+// per key for d = 128): 64 sequences of 512 to 16384 keys, 64 heads, 8 kv heads, with a cap: 338.5 us, 6.50 TB/s,
 // 0.95 of a measured copy. Short calls: latency, of which the plan takes 3 to 8 us, a first tile with cold
 // instruction caches 5, the join 4 to 8.
 //
@@ -1262,8 +1262,8 @@ __device__ __forceinline__ float abs_max64(const uint32_t* y)
 
 // Scores up to CAP_NEAR of their cap (most are far below it) are capped by tanh(z) / z as a polynomial in z^2,
 // interpolated at the Chebyshev points: 2^-23 of itself off. It takes five operations of the FMA pipe where the exact
-// form takes four and a half and two and a half of the MUFU: a prompt of 8192 tokens 642 us where all
-// scores are near, and 755 by the other form.
+// form takes four and a half and two and a half of the MUFU: a prompt of 8192 tokens 631 us where all
+// scores are near (a cap of 30), and 838 where few half tiles have none beyond (a cap of 2).
 constexpr float CAP_NEAR = 0.35f;
 
 // Ties the registers to the tcgen05.wait::ld before it.
