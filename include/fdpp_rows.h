@@ -26,8 +26,9 @@
  * sums, whatever the caches hold there (NaN included), and a non-finite score or value that it sees
  * has the formula's effect on that row alone (weights are in fp32: one below 2^-126 of the largest counts
  * as 0). Where a value that is not finite is seen by some rows of a tile only, the others are computed
- * again key by key, which takes long: 0.3 s for 128 rows of 16384 keys. Results do not depend on timing
- * or on former calls: the same call gives the same bits.
+ * again key by key, which takes long: 0.3 s for 128 rows of 16384 keys (a wait for such rows does not run
+ * out as long as they get on). Results do not depend on timing or on former calls: the same call gives
+ * the same bits.
  *
  * fp32 (and bf16 on request) takes a CUDA-core kernel instead. There every token row reads its keys for
  * itself, the shared prefix's too.
