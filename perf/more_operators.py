@@ -231,8 +231,8 @@ def _prepare_linear(case, gen, perm):
     s = dict(case=case, x=x, sx=sx, w=w, sw=sw, y=torch.zeros(M, N, device="cuda", dtype=TYPES[case["out"]]))
     if own:
         import split_kv_async_gb300 as F
-        s["p"] = F.make_fp8_gemm_params(M=M, N=N, K=K, out_dtype=_code(case["out"]))
-        s["ws"] = F.alloc_fp8_gemm_workspace(s["p"])
+        s["p"] = F.make_scaled_gemm_params(M=M, N=N, K=K, out_dtype=_code(case["out"]))
+        s["ws"] = F.alloc_scaled_gemm_workspace(s["p"])
     return s
 
 
@@ -346,7 +346,7 @@ def _run_norm(s):
 def _run_linear(s):
     if own:
         import split_kv_async_gb300 as F
-        F.fdpp_fp8_gemm(s["x"], s["sx"], s["w"], s["sw"], s["p"], s["ws"], s["y"])
+        F.fdpp_scaled_gemm(s["x"], s["sx"], s["w"], s["sw"], s["p"], s["ws"], s["y"])
         return s["y"]
     M, N, K = (s["case"][x] for x in "MNK")
     x = s["x"].float() * s["sx"].repeat_interleave(GROUP, 1)[:, :K]
