@@ -22,6 +22,8 @@ LIB_PATH = os.path.join(HERE, "libfdpp.so")
 
 FDPP_OK, FDPP_ERR_INVALID_ARG, FDPP_ERR_UNSUPPORTED, FDPP_ERR_WORKSPACE, FDPP_ERR_CUDA = range(5)
 FDPP_F32, FDPP_BF16 = 0, 1
+FDPP_E4M3 = 2
+FDPP_SCALE_BLOCK, FDPP_NORM_MAX_DIM = 128, 32768
 FDPP_MODE_NORMAL, FDPP_MODE_FORCE_FAST, FDPP_MODE_FORCE_ONLINE = 0, 1, 2
 FDPP_KERNEL_AUTO, FDPP_KERNEL_TENSOR, FDPP_KERNEL_SIMT = 0, 1, 2
 FDPP_TC_MMA_AUTO, FDPP_TC_MMA_SYNC, FDPP_TC_MMA_TCGEN05 = 0, 1, 2
@@ -42,7 +44,8 @@ EXPORTED = ("fdpp_max_splits", "fdpp_workspace_size", "fdpp_workspace_init", "fd
             "fdpp_flat_gemm_split_k", "fdpp_flat_gemm_workspace_size", "fdpp_flat_gemm",
             "fdpp_flat_gemm_set_lut", "fdpp_flat_gemm_read_error",
             "fdpp_block_map_workspace_size", "fdpp_block_map", "fdpp_rope_table", "fdpp_rope_append",
-            "fdpp_read_error", "fdpp_rows_workspace_size", "fdpp_rows_attn", "fdpp_prefix_attn")
+            "fdpp_read_error", "fdpp_rows_workspace_size", "fdpp_rows_attn", "fdpp_prefix_attn",
+            "fdpp_rms_norm", "fdpp_scaled_gemm_workspace_size", "fdpp_scaled_gemm")
 FDPP_GEMM_MAX_M = 128
 FDPP_NOALLOC_WORKSPACE_BYTES = 16 << 20
 FDPP_TC_MAX_PARTS = 512
@@ -117,6 +120,23 @@ class fdpp_rows_params(ctypes.Structure):
     ]
 
 
+class fdpp_norm_params(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int), ("dim", ctypes.c_int), ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+        ("x_stride", ctypes.c_longlong), ("residual_stride", ctypes.c_longlong), ("out_stride", ctypes.c_longlong),
+        ("sum_stride", ctypes.c_longlong), ("scale_stride", ctypes.c_longlong), ("eps", ctypes.c_float),
+        ("weight_offset", ctypes.c_float),
+    ]
+
+
+class fdpp_scaled_gemm_params(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int), ("out_dtype", ctypes.c_int),
+        ("x_stride", ctypes.c_longlong), ("w_stride", ctypes.c_longlong), ("y_stride", ctypes.c_longlong),
+        ("x_scale_stride", ctypes.c_longlong), ("split_k", ctypes.c_int),
+    ]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -184,6 +204,13 @@ def _load() -> ctypes.CDLL:
     lib.fdpp_rows_attn.restype = ci
     lib.fdpp_prefix_attn.argtypes = [vp] * 10 + [PA, vp, cz, vp, vp]
     lib.fdpp_prefix_attn.restype = ci
+    PN, PS = ctypes.POINTER(fdpp_norm_params), ctypes.POINTER(fdpp_scaled_gemm_params)
+    lib.fdpp_rms_norm.argtypes = [vp, vp, vp, PN, vp, vp, vp, vp]
+    lib.fdpp_rms_norm.restype = ci
+    lib.fdpp_scaled_gemm_workspace_size.argtypes = [PS]
+    lib.fdpp_scaled_gemm_workspace_size.restype = cz
+    lib.fdpp_scaled_gemm.argtypes = [vp, vp, vp, vp, PS, vp, cz, vp, vp]
+    lib.fdpp_scaled_gemm.restype = ci
     return lib
 
 
@@ -535,3 +562,58 @@ def fdpp_prefix_attn(q, prefix_k, prefix_v, prefix_blocks, prefix_len, k_cache, 
                                 prefix_len.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(block_table),
                                 seq_lens.data_ptr(), _ptr(cu_tokens), p, workspace.data_ptr(),
                                 _bytes(workspace), out.data_ptr(), _stream_handle(stream)), "fdpp_prefix_attn")
+
+
+# ---- 8-bit linear layers (include/fdpp_linear.h) --------------------------------------------
+
+def _scale_blocks(n: int) -> int:
+    return (n + FDPP_SCALE_BLOCK - 1) // FDPP_SCALE_BLOCK
+
+
+def make_norm_params(*, num_tokens, dim, dtype, out_dtype=None, eps=1e-6, weight_offset=0.0, x_stride=None,
+                     residual_stride=None, out_stride=None, sum_stride=None, scale_stride=None) -> fdpp_norm_params:
+    """out_dtype: dtype where None, or FDPP_E4M3. Strides in elements from one row to the next (scale_stride
+    in scales); None: contiguous rows, an e4m3 output's rounded up to 16 channels."""
+    out_dtype = dtype if out_dtype is None else out_dtype
+    packed = (dim + 15) // 16 * 16 if out_dtype == FDPP_E4M3 else dim
+    return fdpp_norm_params(num_tokens, dim, dtype, out_dtype, dim if x_stride is None else x_stride,
+                            dim if residual_stride is None else residual_stride,
+                            packed if out_stride is None else out_stride, dim if sum_stride is None else sum_stride,
+                            _scale_blocks(dim) if scale_stride is None else scale_stride, eps, weight_offset)
+
+
+def fdpp_rms_norm(x, residual, weight, p: fdpp_norm_params, out, scales=None, sum_out=None, stream=None) -> None:
+    """RMS norm of the rows x + residual (device tensors with the strides of `p`; residual, weight and
+    sum_out may be None). scales: float32, for an e4m3 `out` (a float8_e4m3fn or uint8 tensor)."""
+    _check(lib.fdpp_rms_norm(x.data_ptr(), _ptr(residual), _ptr(weight), p, out.data_ptr(), _ptr(scales), _ptr(sum_out),
+                             _stream_handle(stream)), "fdpp_rms_norm")
+
+
+def make_scaled_gemm_params(*, M, N, K, out_dtype=FDPP_BF16, x_stride=None, w_stride=None, y_stride=None,
+                            x_scale_stride=None, split_k=0) -> fdpp_scaled_gemm_params:
+    """Strides from one row to the next: of x and w in bytes, of y in elements, of x's scales in floats;
+    None: contiguous rows."""
+    return fdpp_scaled_gemm_params(M, N, K, out_dtype, K if x_stride is None else x_stride, K if w_stride is None else w_stride,
+                                   N if y_stride is None else y_stride,
+                                   _scale_blocks(K) if x_scale_stride is None else x_scale_stride, split_k)
+
+
+def fdpp_scaled_gemm_workspace_size(p: fdpp_scaled_gemm_params) -> int:
+    return int(lib.fdpp_scaled_gemm_workspace_size(p))
+
+
+def alloc_scaled_gemm_workspace(p: fdpp_scaled_gemm_params, device="cuda"):
+    """A zeroed uint8 device tensor large enough for fdpp_scaled_gemm with `p`."""
+    import torch
+    n = fdpp_scaled_gemm_workspace_size(p)
+    if n == 0:
+        raise FdppError(FDPP_ERR_INVALID_ARG, "fdpp_scaled_gemm_workspace_size", lib.fdpp_last_error().decode())
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def fdpp_scaled_gemm(x, x_scales, w, w_scales, p: fdpp_scaled_gemm_params, workspace, y, stream=None) -> None:
+    """y = x W^T of e4m3 x [M][K] and w [N][K] with their block scales (device tensors with the strides of
+    `p`; errors on the device: fdpp_read_error)."""
+    _check(lib.fdpp_scaled_gemm(x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), p,
+                                workspace.data_ptr(), _bytes(workspace), y.data_ptr(), _stream_handle(stream)),
+           "fdpp_scaled_gemm")

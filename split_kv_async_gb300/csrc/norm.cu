@@ -1,0 +1,293 @@
+// norm.cu -- RMS norm with the residual's addition (fdpp_linear.h), output in the input's type or in
+// e4m3 with a scale for every 128 channels.
+//
+//     r = x + residual,  y = r (mean(r^2) + eps)^(-1/2) w,  scale_g = max |y| of block g / 448
+//
+// A row is read once and stays in registers: each thread holds V vectors of 8 channels, thread i of the
+// row's R takes vectors i, i + R, .. so that a warp reads whole lines, and the 16 lanes of a half warp hold
+// a block of 128 channels, whose largest |y| takes four exchanges. The sum of squares is the only thing
+// that the row's threads have to wait for.
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "device_common.cuh"
+#include "fdpp_linear.h"
+
+namespace fdpp {
+namespace {
+
+constexpr float E4M3_MAX = 448.f;
+constexpr float LEAST_SCALE = 1.17549435e-38f;       // 2^-126: its reciprocal is finite
+constexpr int NORM_MAX_THREADS = 1024;
+constexpr int NORM_WARP_ROWS = 8;                    // rows of a CTA where each is one warp's
+
+struct NormArgs {
+    const void* x;
+    const void* residual;
+    const void* weight;
+    void* out;
+    float* scales;
+    void* sum_out;
+    long long x_stride, residual_stride, out_stride, sum_stride, scale_stride;
+    int T, dim;
+    float eps, offset;
+};
+
+// Eight consecutive elements as fp32, and back.
+__device__ __forceinline__ void load8(const float* p, float (&v)[8])
+{
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8])
+{
+    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ void store8(float* p, const float (&v)[8])
+{
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8])
+{
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d)
+{
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// WARP: a row is one warp's, NORM_WARP_ROWS rows to a CTA; otherwise a row is the CTA's.
+template <typename T, bool E4M3, int V, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * NORM_WARP_ROWS : NORM_MAX_THREADS) rms_norm_kernel(NormArgs a)
+{
+    __shared__ float part[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int R = WARP ? 32 : blockDim.x, me = WARP ? lane : threadIdx.x;
+    const long long t = WARP ? (long long)blockIdx.x * NORM_WARP_ROWS + warp : blockIdx.x;
+    grid_dependency_wait();
+    if (WARP && t >= a.T) return;
+    const int vectors = a.dim / 8;
+    const T* x = static_cast<const T*>(a.x) + t * a.x_stride;
+    float r[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) r[i][k] = 0.f;
+        if (me + i * R < vectors) load8(x + (me + i * R) * 8, r[i]);
+    }
+    if (a.residual) {
+        const T* res = static_cast<const T*>(a.residual) + t * a.residual_stride;
+        float s[V][8];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (me + i * R < vectors) load8(res + (me + i * R) * 8, s[i]);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (me + i * R < vectors)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) r[i][k] += s[i][k];
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum = fmaf(r[i][k], r[i][k], sum);
+    sum = warp_sum(sum);
+    if (!WARP) {
+        if (lane == 0) part[warp] = sum;
+        __syncthreads();
+        sum = lane < (R >> 5) ? part[lane] : 0.f;
+        sum = warp_sum(sum);
+    }
+    const float inv = 1.f / sqrtf(sum / (float)a.dim + a.eps);
+    if (a.sum_out) {
+        T* so = static_cast<T*>(a.sum_out) + t * a.sum_stride;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (me + i * R < vectors) store8(so + (me + i * R) * 8, r[i]);
+    }
+    const T* w = static_cast<const T*>(a.weight);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int at = me + i * R;
+        const bool in = at < vectors;
+        float y[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = r[i][k] * inv;
+        if (w && in) {
+            float g[8];
+            if constexpr (sizeof(T) == 4) {
+                const float4 p = __ldg(reinterpret_cast<const float4*>(w + at * 8));
+                const float4 q = __ldg(reinterpret_cast<const float4*>(w + at * 8) + 1);
+                g[0] = p.x; g[1] = p.y; g[2] = p.z; g[3] = p.w;
+                g[4] = q.x; g[5] = q.y; g[6] = q.z; g[7] = q.w;
+            } else {
+                const uint4 p = __ldg(reinterpret_cast<const uint4*>(w + at * 8));
+                const uint32_t u[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    g[2 * k] = __uint_as_float(u[k] << 16);
+                    g[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] *= g[k] + a.offset;
+        }
+        if constexpr (!E4M3) {
+            if (in) store8(static_cast<T*>(a.out) + t * a.out_stride + at * 8, y);
+        } else {
+            // a block's 16 lanes (those past the row hold zeros)
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = max_nan(top, fabsf(y[k]));
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float scale = max_nan(top / E4M3_MAX, LEAST_SCALE), over = 1.f / scale;
+            if (in) {
+                uint2 v;
+                v.x = pack_e4m3x4(y[0] * over, y[1] * over, y[2] * over, y[3] * over);
+                v.y = pack_e4m3x4(y[4] * over, y[5] * over, y[6] * over, y[7] * over);
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + t * a.out_stride + at * 8) = v;
+                if ((at & 15) == 0) a.scales[t * a.scale_stride + (at >> 4)] = scale;
+            }
+        }
+    }
+}
+
+fdpp_status nfail(fdpp_status s, const char* fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    std::vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    set_last_error(buf);
+    return s;
+}
+
+template <typename T, bool E4M3>
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t s)
+{
+    const int vectors = a.dim / 8;
+    void (*kern)(NormArgs);
+    unsigned grid, threads;
+    if (vectors <= 128) {
+        kern = vectors <= 32   ? rms_norm_kernel<T, E4M3, 1, true>
+               : vectors <= 64 ? rms_norm_kernel<T, E4M3, 2, true>
+                               : rms_norm_kernel<T, E4M3, 4, true>;
+        grid = (unsigned)((a.T + NORM_WARP_ROWS - 1) / NORM_WARP_ROWS);
+        threads = 32 * NORM_WARP_ROWS;
+    } else {
+        const int v = vectors <= 512 ? 1 : vectors <= 2048 ? 2 : 4;
+        kern = v == 1 ? rms_norm_kernel<T, E4M3, 1, false>
+               : v == 2 ? rms_norm_kernel<T, E4M3, 2, false>
+                        : rms_norm_kernel<T, E4M3, 4, false>;
+        grid = (unsigned)a.T;
+        threads = (unsigned)((vectors + v - 1) / v + 31) / 32 * 32;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace fdpp
+
+using namespace fdpp;
+
+extern "C" fdpp_status fdpp_rms_norm(const void* x, const void* residual, const void* weight, const fdpp_norm_params* p,
+                                     void* out, float* scales, void* sum_out, fdpp_stream stream)
+{
+    if (!p) return nfail(FDPP_ERR_INVALID_ARG, "params is NULL");
+    if (p->num_tokens < 0) return nfail(FDPP_ERR_INVALID_ARG, "num_tokens must be >= 0 (got %d)", p->num_tokens);
+    if (p->dim < 8 || p->dim % 8) return nfail(FDPP_ERR_INVALID_ARG, "dim must be a positive multiple of 8 (got %d)", p->dim);
+    if (p->dim > FDPP_NORM_MAX_DIM)
+        return nfail(FDPP_ERR_UNSUPPORTED, "dim %d > %d", p->dim, FDPP_NORM_MAX_DIM);
+    if (p->dtype != FDPP_F32 && p->dtype != FDPP_BF16)
+        return nfail(FDPP_ERR_INVALID_ARG, "dtype must be FDPP_F32 or FDPP_BF16 (got %d)", p->dtype);
+    const bool e4m3 = p->out_dtype == FDPP_E4M3;
+    if (!e4m3 && p->out_dtype != p->dtype)
+        return nfail(FDPP_ERR_INVALID_ARG, "out_dtype must be dtype or FDPP_E4M3 (got %d)", p->out_dtype);
+    if (!(p->eps >= 0.f) || !std::isfinite(p->eps)) return nfail(FDPP_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (!std::isfinite(p->weight_offset)) return nfail(FDPP_ERR_INVALID_ARG, "weight_offset must be finite");
+    const long long vec = p->dtype == FDPP_F32 ? 4 : 8, out_vec = e4m3 ? 16 : vec, most = 1ll << 40;
+    auto stride_ok = [&](long long stride, long long v) { return stride >= p->dim && stride % v == 0 && stride <= most; };
+    if (!stride_ok(p->x_stride, vec) || !stride_ok(p->out_stride, out_vec) ||
+        (residual && !stride_ok(p->residual_stride, vec)) || (sum_out && !stride_ok(p->sum_stride, vec)))
+        return nfail(FDPP_ERR_INVALID_ARG, "strides must cover a row and be multiples of 16 bytes");
+    if (!x || !out) return nfail(FDPP_ERR_INVALID_ARG, "x and out must be non-NULL");
+    if (((uintptr_t)x | (uintptr_t)residual | (uintptr_t)weight | (uintptr_t)out | (uintptr_t)sum_out) % 16 != 0)
+        return nfail(FDPP_ERR_INVALID_ARG, "x, residual, weight, out and sum_out must be 16-byte aligned");
+    if (e4m3) {
+        if (!scales || (uintptr_t)scales % 4 != 0)
+            return nfail(FDPP_ERR_INVALID_ARG, "an e4m3 output needs scales, 4-byte aligned");
+        if (p->scale_stride < (p->dim + FDPP_SCALE_BLOCK - 1) / FDPP_SCALE_BLOCK || p->scale_stride > most)
+            return nfail(FDPP_ERR_INVALID_ARG, "scale_stride must cover a row's scales");
+    } else if (scales) {
+        return nfail(FDPP_ERR_INVALID_ARG, "scales are of an e4m3 output only");
+    }
+    if ((out == x && (e4m3 || p->out_stride != p->x_stride)) || (sum_out && sum_out == x && p->sum_stride != p->x_stride) ||
+        (sum_out && sum_out == residual && p->sum_stride != p->residual_stride) || out == residual || out == sum_out)
+        return nfail(FDPP_ERR_INVALID_ARG, "out may be x, and sum_out residual or x, where types and strides are the same");
+    int sms = 0, unused = 0;
+    const fdpp_status st = query_device(&sms, &unused, &unused);
+    if (st != FDPP_OK) return st;
+    if (p->num_tokens == 0) return FDPP_OK;
+
+    NormArgs a{};
+    a.x = x;
+    a.residual = residual;
+    a.weight = weight;
+    a.out = out;
+    a.scales = scales;
+    a.sum_out = sum_out;
+    a.x_stride = p->x_stride;
+    a.residual_stride = p->residual_stride;
+    a.out_stride = p->out_stride;
+    a.sum_stride = p->sum_stride;
+    a.scale_stride = p->scale_stride;
+    a.T = p->num_tokens;
+    a.dim = p->dim;
+    a.eps = p->eps;
+    a.offset = p->weight_offset;
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e;
+    if (p->dtype == FDPP_F32) e = e4m3 ? launch_norm<float, true>(a, s) : launch_norm<float, false>(a, s);
+    else e = e4m3 ? launch_norm<__nv_bfloat16, true>(a, s) : launch_norm<__nv_bfloat16, false>(a, s);
+    if (e != cudaSuccess) return nfail(FDPP_ERR_CUDA, "RMS norm launch: %s", cudaGetErrorString(e));
+    return FDPP_OK;
+}

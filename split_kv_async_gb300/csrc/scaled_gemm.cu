@@ -1,0 +1,776 @@
+// scaled_gemm.cu -- the linear layer on 8-bit operands with block scales (fdpp_linear.h), on tcgen05
+// tensor cores:
+//
+//     y[m][n] = sum_b sx[m][b] sw[n / 128][b] sum_{k in block b} x[m][k] w[n][k]
+//
+// Both kernels stream blocks of 128 channels (128-byte rows, 128-byte swizzle) of x and w through a TMA
+// ring; a block is four MMAs of K = 32 into a tensor-memory buffer of its own, which other warps read,
+// scale by sx sw and add to fp32 sums in registers while the tensor cores work on the next block's buffer.
+// The scales are any fp32 numbers, so they cannot be left to the tensor cores (whose block scales are
+// powers of two).
+//
+//   rows kernel (M <= 128): y^T = w x^T. 128 weight rows on the tensor-memory lanes, the rows of x on N,
+//     padded to the next 16 only; the work is the stream of w. When the weight tiles are too few for the GPU, K is
+//     cut into ranges whose CTAs form a cluster and add their sums through distributed shared memory, in
+//     range order.
+//   tile kernel (M > 128): 128 rows of x on the lanes, BN weight rows on N, one persistent CTA per SM.
+//
+// Every wait is bounded: on a timeout the CTA records FDPP_ERRBIT_TIMEOUT, lets its copies and MMAs land,
+// frees its tensor memory and exits.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cstdarg>
+#include <cstdio>
+#include <map>
+#include <mutex>
+
+#include "device_common.cuh"
+#include "fdpp_linear.h"
+#include "gemm_common.cuh"
+#include "tcgen05.cuh"
+
+namespace fdpp {
+namespace {
+
+constexpr int SB = FDPP_SCALE_BLOCK;     // channels of a block: one 128-byte swizzle row
+constexpr int SG_N = 128;                // weight rows that share a scale; the rows kernel's weight tile
+constexpr int SG_ROWS = 128;             // most rows of x of the rows kernel; the tile kernel's row tile
+constexpr int SG_MAX_SPLIT = 8;          // K ranges per weight tile (a portable cluster)
+constexpr int SG_MAX_STAGES = 8;
+
+struct ScaledArgs {
+    const float* sx;
+    const float* sw;
+    void* y;
+    unsigned* err;                       // sticky FDPP_ERRBIT_*
+    long long y_stride, sx_stride;
+    int M, N, kb;                        // kb: blocks of K
+    int Mp, split_k, nstage;             // rows kernel: x rows padded; K ranges
+    int m_tiles, n_tiles;                // tile kernel
+};
+
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor of kind f8f6f4 with e4m3 A and B (types 0), both K-major, fp32 sums, M x N.
+__host__ __device__ constexpr uint32_t umma_idesc_e4m3(int M, int N)
+{
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// A block of 128 channels: four MMAs of 32.
+__device__ __forceinline__ void umma_block(uint32_t d_tmem, uint32_t a0, uint32_t b0, uint32_t idesc)
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        umma_e4m3(d_tmem, sw128_kmajor_desc(a0 + k * 32), sw128_kmajor_desc(b0 + k * 32), idesc, k > 0 ? 1u : 0u);
+}
+
+__device__ __forceinline__ uint64_t pack2(float x, float y)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+    return d;
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t x, uint32_t y)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(x), "r"(y));
+    return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t d)
+{
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(d));
+    return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// Every lane waits; one that runs out aborts the CTA (warp-uniform result).
+__device__ __forceinline__ bool gwait(uint32_t bar, uint32_t parity, volatile int* abort_, unsigned* err)
+{
+    bool ok = *abort_ == 0 && mbar_wait(bar, parity & 1u);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok && (threadIdx.x & 31) == 0) {
+        *abort_ = 1;
+        atomicOr(err, FDPP_ERRBIT_TIMEOUT);
+    }
+    return ok;
+}
+
+__device__ __forceinline__ void store_y(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store_y(float* p, float v) { *p = v; }
+
+// ---- rows kernel --------------------------------------------------------------------------
+
+constexpr int R_THREADS = 192;           // producer warp, MMA warp, 4 warps that scale and add
+constexpr int RW_BYTES = SG_N * SB;      // weight slice of a stage
+
+// Shared memory (dynamic, 1024-byte aligned base): nstage stages of [w slice 16 KB | x slice Mp x 128 B],
+// then the scales of two blocks, the barriers, the TMEM address and the abort flag. Once every MMA has
+// completed, the stages hold this CTA's fp32 sums [M][128] for the cluster's reduction.
+template <typename T, int NR>
+__global__ void __launch_bounds__(R_THREADS, 2)
+    scaled_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                       const ScaledArgs g)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(sm);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int stage_bytes = RW_BYTES + g.Mp * SB;
+    float* scale = reinterpret_cast<float*>(sm + g.nstage * stage_bytes);        // [2][SG_ROWS]
+    const int bar_off = g.nstage * stage_bytes + 2 * SG_ROWS * 4;
+    const uint32_t bars = sbase + bar_off;
+    const uint32_t full = bars, empty = bars + 8 * g.nstage, accf = bars + 16 * g.nstage, acce = accf + 16;
+    volatile uint32_t* tslot = reinterpret_cast<volatile uint32_t*>(sm + bar_off + 16 * g.nstage + 32);
+    volatile int* abort_ = reinterpret_cast<volatile int*>(sm + bar_off + 16 * g.nstage + 40);
+
+    const int tile = blockIdx.x / g.split_k;
+    const int ks = g.split_k > 1 ? (int)cluster_rank() : 0;
+    const int n0 = tile * SG_N;
+    const int kb0 = (int)((long long)ks * g.kb / g.split_k), kb1 = (int)((long long)(ks + 1) * g.kb / g.split_k);
+    const int nkb = kb1 - kb0;
+    uint32_t ncols = 32;                 // two buffers of Mp columns
+    while ((int)ncols < 2 * g.Mp) ncols <<= 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < g.nstage; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(accf + 8 * b, 1);
+            mbar_init(acce + 8 * b, 4);
+        }
+        *abort_ = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&tmW);
+        prefetch_tensormap(&tmX);
+    }
+    if (warp == 1) tmem_alloc(smem_u32((const void*)tslot), ncols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+
+    int issued = 0;                      // producer: slices issued
+    if (warp == 0) {
+        if (lane == 0) {
+            // w is not written by the kernel before this one on the stream: the first ring's worth of it
+            // streams while that kernel finishes
+            const int pre = nkb < g.nstage ? nkb : g.nstage;
+            for (int i = 0; i < pre; ++i) {
+                mbar_arrive_expect_tx(full + 8 * i, (uint32_t)stage_bytes);
+                tma_load_2d(sbase + i * stage_bytes, &tmW, (kb0 + i) * SB, n0, full + 8 * i);
+            }
+            grid_dependency_wait();
+            for (int i = 0; i < pre; ++i)
+                tma_load_2d(sbase + i * stage_bytes + RW_BYTES, &tmX, (kb0 + i) * SB, 0, full + 8 * i);
+            issued = pre;
+            for (int i = pre; i < nkb; ++i) {
+                const int s = i % g.nstage;
+                const uint32_t par = (uint32_t)(i / g.nstage) & 1u;
+                if (*abort_ || !mbar_wait(empty + 8 * s, par ^ 1u)) {
+                    atomicOr(g.err, FDPP_ERRBIT_TIMEOUT);
+                    *abort_ = 1;
+                    break;
+                }
+                const uint32_t dst = sbase + s * stage_bytes;
+                const int k = (kb0 + i) * SB;
+                mbar_arrive_expect_tx(full + 8 * s, (uint32_t)stage_bytes);
+                tma_load_2d(dst, &tmW, k, n0, full + 8 * s);
+                tma_load_2d(dst + RW_BYTES, &tmX, k, 0, full + 8 * s);
+                ++issued;
+            }
+            grid_launch_dependents();
+        } else {
+            grid_dependency_wait();
+        }
+    } else if (warp == 1) {
+        grid_dependency_wait();
+        if (lane == 0) {
+            const uint32_t idesc = umma_idesc_e4m3(SG_N, g.Mp);
+            int done = 0;
+            for (; done < nkb; ++done) {
+                const int s = done % g.nstage, b = done & 1;
+                const uint32_t par = (uint32_t)(done / g.nstage) & 1u;
+                if (*abort_ || !mbar_wait(acce + 8 * b, ((uint32_t)(done >> 1) & 1u) ^ 1u) || !mbar_wait(full + 8 * s, par)) {
+                    atomicOr(g.err, FDPP_ERRBIT_TIMEOUT);
+                    *abort_ = 1;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t a0 = sbase + s * stage_bytes;
+                umma_block(tmem + b * g.Mp, a0, a0 + RW_BYTES, idesc);
+                umma_commit(empty + 8 * s);
+                umma_commit(accf + 8 * b);
+            }
+            // after an abort the MMAs issued land before the CTA ends
+            if (*abort_ && done > 0) {
+                const int last = done - 1;
+                if (!mbar_wait(accf + 8 * (last & 1), (uint32_t)(last >> 1) & 1u)) atomicOr(g.err, FDPP_ERRBIT_TIMEOUT);
+            }
+        }
+    } else {
+        grid_dependency_wait();
+        // ---- TMEM lanes 32 (warp % 4) .. hold weight rows n0 + that lane ----
+        const int q = warp & 3, t = threadIdx.x - 64;
+        const int n = n0 + 32 * q + lane;
+        const uint32_t trow = tmem + ((uint32_t)(32 * q) << 16);
+        const float* sx = g.sx + (long long)t * g.sx_stride;
+        const float* sw = g.sw + (long long)tile * g.kb;
+        uint64_t acc[NR / 2];
+#pragma unroll
+        for (int j = 0; j < NR / 2; ++j) acc[j] = 0ull;
+        float next = t < g.M ? sx[kb0] * sw[kb0] : 0.f;
+        bool ok = true;
+        for (int i = 0; i < nkb; ++i) {
+            const int b = i & 1;
+            float* sc = scale + b * SG_ROWS;
+            sc[t] = next;
+            if (t < g.M && i + 1 < nkb) next = sx[kb0 + i + 1] * sw[kb0 + i + 1];
+            named_bar_sync(1, 128);      // (buffer b was last read two blocks ago, before the barrier between)
+            ok = gwait(accf + 8 * b, (uint32_t)(i >> 1), abort_, g.err) && ok;
+            if (ok) {
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < NR; c += 16) {
+                    if (c >= g.Mp) break;
+                    uint32_t v[16];
+                    tmem_ld16_async(trow + b * g.Mp + c, v);
+                    tmem_wait_ld();
+                    reg_fence16(v);
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 s = *reinterpret_cast<const float4*>(sc + c + j);
+                        acc[(c + j) / 2] = fma2(pack2(v[j], v[j + 1]), pack2(s.x, s.y), acc[(c + j) / 2]);
+                        acc[(c + j) / 2 + 1] = fma2(pack2(v[j + 2], v[j + 3]), pack2(s.z, s.w), acc[(c + j) / 2 + 1]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acce + 8 * b);
+            }
+        }
+        // the tensor cores' reads of the stages are complete (the last block's barrier); the sums of a
+        // split tile reuse that memory
+        fence_proxy_async_smem();
+        float* red = reinterpret_cast<float*>(sm);
+        T* y = static_cast<T*>(g.y);
+        if (ok) {
+#pragma unroll
+            for (int j = 0; j < NR; ++j) {
+                const float2 p = unpack2(acc[j / 2]);
+                const float v = j & 1 ? p.y : p.x;
+                if (j < g.M) {
+                    if (g.split_k > 1) red[j * SG_N + 32 * q + lane] = v;
+                    else if (n < g.N) store_y(y + (long long)j * g.y_stride + n, v);
+                }
+            }
+        }
+    }
+
+    // ---- split tile: every member adds its share of the outputs from all members' sums ----
+    __syncthreads();
+    if (g.split_k > 1) {
+        // every thread of every member passes both cluster barriers, whatever happened before
+        cluster_sync_all();
+        if (!*abort_) {
+            const int P = g.M * (SG_N / 4);
+            const int p0 = (int)((long long)ks * P / g.split_k), p1 = (int)((long long)(ks + 1) * P / g.split_k);
+            for (int i = p0 + (int)threadIdx.x; i < p1; i += R_THREADS) {
+                const int m = i / (SG_N / 4), c = 4 * (i - m * (SG_N / 4)), n = n0 + c;
+                if (n >= g.N) continue;
+                const uint32_t off = sbase + (uint32_t)((m * SG_N + c) * 4);
+                float4 t[SG_MAX_SPLIT];
+#pragma unroll
+                for (int r = 0; r < SG_MAX_SPLIT; ++r)
+                    if (r < g.split_k) t[r] = ld_dsmem_f4(dsmem_addr(off, (uint32_t)r));
+                float4 s = t[0];
+#pragma unroll
+                for (int r = 1; r < SG_MAX_SPLIT; ++r)
+                    if (r < g.split_k) {
+                        s.x += t[r].x; s.y += t[r].y; s.z += t[r].z; s.w += t[r].w;
+                    }
+                T* yp = static_cast<T*>(g.y) + (long long)m * g.y_stride + n;
+                const float v[4] = {s.x, s.y, s.z, s.w};
+                if (n + 3 < g.N && (reinterpret_cast<uintptr_t>(yp) & (4 * sizeof(T) - 1)) == 0) {
+                    if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(yp) = s;
+                    else *reinterpret_cast<uint2*>(yp) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (n + u < g.N) store_y(yp + u, v[u]);
+                }
+            }
+        }
+        // no member leaves (releasing its shared memory) while another still reads it
+        cluster_sync_all();
+    }
+
+    // ---- teardown: copies and MMAs landed, tensor memory freed ----
+    if (*abort_ && warp == 0 && lane == 0) {
+        for (int i = issued > g.nstage ? issued - g.nstage : 0; i < issued; ++i) {
+            const uint64_t t0 = global_ns();
+            while (!mbar_try_wait(full + 8 * (i % g.nstage), (uint32_t)(i / g.nstage) & 1u) && global_ns() - t0 < 100000000ull) {
+            }
+        }
+    }
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, ncols);
+}
+
+// ---- tile kernel --------------------------------------------------------------------------
+
+constexpr int T_THREADS = 384;           // producer, MMA, two idle warps; 8 warps that scale and add
+constexpr int T_HELP_REGS = 80, T_SUM_REGS = 208;    // 128 x 80 + 256 x 208 = 63488 of the launch's 384 x 168
+constexpr int T_GROUP = 16;              // row tiles that a run of weight tiles is shared by (see tile_at)
+
+template <int BN>
+struct TileSmem {
+    static constexpr int STAGE = (SG_ROWS + BN) * SB;
+    static constexpr int TURN = 32 * 128;                // a warp's rows, 128 bytes of each
+    static constexpr int STAGES = BN == 256 ? 4 : 6;
+    static constexpr int NBUF = 512 / BN;                // tensor-memory buffers of BN columns
+    static constexpr int BARS = STAGES * STAGE + 8 * TURN;
+    static constexpr int TOTAL = BARS + (2 * STAGES + 2 * NBUF) * 8 + 32 + 1024;
+};
+
+// Tile i of the order: T_GROUP row tiles at a time, the weight tiles outside, so that the CTAs at work
+// together read few of either.
+__device__ __forceinline__ void tile_at(const ScaledArgs& g, int i, int& mt, int& nt)
+{
+    const int per = T_GROUP * g.n_tiles, group = i / per, first = group * T_GROUP;
+    const int rows = min(T_GROUP, g.m_tiles - first), r = i - group * per;
+    nt = r / rows;
+    mt = first + r - nt * rows;
+}
+
+template <typename T, int BN>
+__global__ void __launch_bounds__(T_THREADS, 1)
+    scaled_tile_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const ScaledArgs g)
+{
+    using L = TileSmem<BN>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(sm);
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t full = sbase + L::BARS, empty = full + 8 * L::STAGES, accf = empty + 8 * L::STAGES, acce = accf + 8 * L::NBUF;
+    volatile uint32_t* tslot = reinterpret_cast<volatile uint32_t*>(sm + L::BARS + (2 * L::STAGES + 2 * L::NBUF) * 8);
+    volatile int* abort_ = reinterpret_cast<volatile int*>(tslot + 2);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < L::STAGES; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        for (int b = 0; b < L::NBUF; ++b) {
+            mbar_init(accf + 8 * b, 1);
+            mbar_init(acce + 8 * b, 8);
+        }
+        *abort_ = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&tmW);
+        prefetch_tensormap(&tmX);
+    }
+    if (warp == 1) tmem_alloc(smem_u32((const void*)tslot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int tiles = g.m_tiles * g.n_tiles;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(T_HELP_REGS));
+        if (warp == 0 && lane == 0) {
+            uint32_t i = 0;              // blocks issued
+            bool ok = true;
+            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                int mt, nt;
+                tile_at(g, t, mt, nt);
+                for (int k = 0; k < g.kb; ++k, ++i) {
+                    const uint32_t s = i % L::STAGES, par = (i / L::STAGES) & 1u;
+                    if (*abort_ || !mbar_wait(empty + 8 * s, par ^ 1u)) {
+                        atomicOr(g.err, FDPP_ERRBIT_TIMEOUT);
+                        *abort_ = 1;
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = sbase + s * L::STAGE;
+                    mbar_arrive_expect_tx(full + 8 * s, (uint32_t)L::STAGE);
+                    tma_load_2d(dst, &tmX, k * SB, mt * SG_ROWS, full + 8 * s);
+                    tma_load_2d(dst + SG_ROWS * SB, &tmW, k * SB, nt * BN, full + 8 * s);
+                }
+            }
+            if (!ok) {                   // every slice issued lands before the CTA ends
+                for (uint32_t j = i > L::STAGES ? i - L::STAGES : 0; j < i; ++j) {
+                    const uint64_t t0 = global_ns();
+                    while (!mbar_try_wait(full + 8 * (j % L::STAGES), (j / L::STAGES) & 1u) && global_ns() - t0 < 100000000ull) {
+                    }
+                }
+            }
+        } else if (warp == 1 && lane == 0) {
+            constexpr uint32_t IDESC = umma_idesc_e4m3(SG_ROWS, BN);
+            uint32_t i = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                for (int k = 0; k < g.kb; ++k, ++i) {
+                    const uint32_t s = i % L::STAGES, b = i % L::NBUF;
+                    if (*abort_ || !mbar_wait(acce + 8 * b, ((i / L::NBUF) & 1u) ^ 1u) || !mbar_wait(full + 8 * s, (i / L::STAGES) & 1u)) {
+                        atomicOr(g.err, FDPP_ERRBIT_TIMEOUT);
+                        *abort_ = 1;
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a0 = sbase + s * L::STAGE;
+                    umma_block(tmem + b * BN, a0, a0 + SG_ROWS * SB, IDESC);
+                    umma_commit(empty + 8 * s);
+                    umma_commit(accf + 8 * b);
+                }
+            }
+            // after an abort the MMAs issued land before the CTA ends
+            if (!ok && i > 0 && !mbar_wait(accf + 8 * ((i - 1) % L::NBUF), ((i - 1) / L::NBUF) & 1u))
+                atomicOr(g.err, FDPP_ERRBIT_TIMEOUT);
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(T_SUM_REGS));
+        constexpr int COLS = BN / 2;     // a warpgroup's columns
+        const int w = warp - 4, q = w & 3, half = w >> 2;
+        const uint32_t trow = tmem + ((uint32_t)(32 * q) << 16) + half * COLS;
+        uint8_t* turn = sm + L::STAGES * L::STAGE + w * L::TURN;
+        T* y = static_cast<T*>(g.y);
+        // 16-byte stores where y and its rows allow them
+        const bool wide = ((reinterpret_cast<uintptr_t>(y) | (uintptr_t)(g.y_stride * (long long)sizeof(T))) & 15u) == 0;
+        uint32_t i = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+            int mt, nt;
+            tile_at(g, t, mt, nt);
+            const int m0 = mt * SG_ROWS + 32 * q, n0 = nt * BN + half * COLS;
+            const bool row_in = m0 + lane < g.M;
+            const float* sx = g.sx + (long long)(row_in ? m0 + lane : 0) * g.sx_stride;
+            // (a half past the last weight row has no scale of its own and is not stored)
+            const float* sw = g.sw + (long long)min(n0 / SG_N, (g.N - 1) / SG_N) * g.kb;
+            uint64_t acc[COLS / 2];
+#pragma unroll
+            for (int j = 0; j < COLS / 2; ++j) acc[j] = 0ull;
+            float x_next = sx[0], w_next = sw[0];
+            for (int k = 0; k < g.kb; ++k, ++i) {
+                const uint32_t b = i % L::NBUF;
+                const float s = x_next * w_next;
+                if (k + 1 < g.kb) {
+                    x_next = sx[k + 1];
+                    w_next = sw[k + 1];
+                }
+                if (!gwait(accf + 8 * b, i / L::NBUF, abort_, g.err)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t s2 = pack2(s, s);
+                uint32_t v[2][32];
+                tmem_ld32_async(trow + b * BN, v[0]);
+#pragma unroll
+                for (int c = 0; c < COLS / 32; ++c) {
+                    tmem_wait_ld();
+                    reg_fence32(v[c & 1]);
+                    if (c + 1 < COLS / 32) tmem_ld32_async(trow + b * BN + 32 * (c + 1), v[(c + 1) & 1]);
+                    if (c + 1 == COLS / 32) {            // the buffer is read out
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(acce + 8 * b);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2)
+                        acc[16 * c + j / 2] = fma2(pack2(v[c & 1][j], v[c & 1][j + 1]), s2, acc[16 * c + j / 2]);
+                }
+            }
+            if (!ok) break;
+            // 128 bytes of every row at a time, turned through shared memory (16-byte pieces of row r at piece
+            // ^ (r & 7)), so that a store instruction writes whole lines
+            constexpr int PC = 128 / (int)sizeof(T), PIECE = 16 / (int)sizeof(T);        // columns of 128 and of 16 bytes
+#pragma unroll
+            for (int c = 0; c < COLS; c += PC) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    uint4 v;
+                    const int at = (c + k * PIECE) / 2;
+                    if constexpr (sizeof(T) == 4) {
+                        const float2 p0 = unpack2(acc[at]), p1 = unpack2(acc[at + 1]);
+                        v = make_uint4(__float_as_uint(p0.x), __float_as_uint(p0.y), __float_as_uint(p1.x), __float_as_uint(p1.y));
+                    } else {
+                        const float2 p0 = unpack2(acc[at]), p1 = unpack2(acc[at + 1]), p2 = unpack2(acc[at + 2]), p3 = unpack2(acc[at + 3]);
+                        v = make_uint4(pack_bf16x2(p0.x, p0.y), pack_bf16x2(p1.x, p1.y), pack_bf16x2(p2.x, p2.y), pack_bf16x2(p3.x, p3.y));
+                    }
+                    *reinterpret_cast<uint4*>(turn + lane * 128 + ((k ^ (lane & 7)) << 4)) = v;
+                }
+                __syncwarp();
+                if (wide && n0 + c + PC <= g.N) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        const int row = k + (lane >> 3), piece = lane & 7;
+                        const uint4 v = *reinterpret_cast<const uint4*>(turn + row * 128 + ((piece ^ (row & 7)) << 4));
+                        if (m0 + row < g.M)
+                            *reinterpret_cast<uint4*>(y + (long long)(m0 + row) * g.y_stride + n0 + c + piece * PIECE) = v;
+                    }
+                } else {                 // element by element, neighbours on neighbouring lanes
+                    for (int row = 0; row < 32 && m0 + row < g.M; ++row)
+#pragma unroll
+                        for (int e = lane; e < PC; e += 32) {
+                            const T v = *reinterpret_cast<const T*>(turn + row * 128 + (((e / PIECE) ^ (row & 7)) << 4) + (e % PIECE) * (int)sizeof(T));
+                            if (n0 + c + e < g.N) y[(long long)(m0 + row) * g.y_stride + n0 + c + e] = v;
+                        }
+                }
+                __syncwarp();
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---- host ---------------------------------------------------------------------------------
+
+fdpp_status sfail(fdpp_status s, const char* fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    set_last_error(buf);
+    return s;
+}
+
+int blocks_of(int K) { return (K + SB - 1) / SB; }
+
+fdpp_status check_params(const fdpp_scaled_gemm_params* p)
+{
+    if (!p) return sfail(FDPP_ERR_INVALID_ARG, "params is NULL");
+    if (p->M < 0 || p->N < 1 || p->K < 16 || p->K % 16)
+        return sfail(FDPP_ERR_INVALID_ARG, "scaled GEMM shape M=%d N=%d K=%d (M >= 0, N >= 1, K >= 16, K %% 16 == 0)", p->M,
+                     p->N, p->K);
+    if (p->N > (1 << 30) || p->K > (1 << 30) || p->M > (1 << 30)) return sfail(FDPP_ERR_INVALID_ARG, "problem too large for one call");
+    if (p->out_dtype != FDPP_F32 && p->out_dtype != FDPP_BF16)
+        return sfail(FDPP_ERR_INVALID_ARG, "out_dtype must be FDPP_F32 or FDPP_BF16 (got %d)", p->out_dtype);
+    const long long most = 1ll << 39;    // of a tensor map's strides
+    if (p->x_stride < p->K || p->w_stride < p->K || p->x_stride % 16 || p->w_stride % 16 || p->x_stride > most || p->w_stride > most)
+        return sfail(FDPP_ERR_INVALID_ARG, "x_stride and w_stride must cover a row and be multiples of 16 bytes");
+    if (p->y_stride < p->N || p->y_stride > most) return sfail(FDPP_ERR_INVALID_ARG, "y_stride must cover a row");
+    if (p->x_scale_stride < blocks_of(p->K) || p->x_scale_stride > most)
+        return sfail(FDPP_ERR_INVALID_ARG, "x_scale_stride must cover a row's scales");
+    if (p->split_k < 0 || p->split_k > std::min(blocks_of(p->K), SG_MAX_SPLIT))
+        return sfail(FDPP_ERR_INVALID_ARG, "split_k %d outside 0 .. %d", p->split_k, std::min(blocks_of(p->K), SG_MAX_SPLIT));
+    return FDPP_OK;
+}
+
+fdpp_status encode_rows(CUtensorMap* map, const void* base, int rows, int K, long long stride, int box_rows)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    const fdpp_status st = get_tensor_map_encoder(&enc);
+    if (st != FDPP_OK) return st;
+    cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)stride};
+    cuuint32_t box[2] = {SB, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return sfail(FDPP_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return FDPP_OK;
+}
+
+using RowsKernel = void (*)(const CUtensorMap, const CUtensorMap, const ScaledArgs);
+
+template <typename T>
+RowsKernel rows_kernel(int Mp)
+{
+    return Mp <= 16 ? scaled_rows_kernel<T, 16> : Mp <= 32 ? scaled_rows_kernel<T, 32> : Mp <= 64 ? scaled_rows_kernel<T, 64>
+                                                                                                 : scaled_rows_kernel<T, 128>;
+}
+
+int rows_smem(int Mp, int nstage) { return nstage * (RW_BYTES + Mp * SB) + 2 * SG_ROWS * 4 + 16 * nstage + 64 + 1024; }
+
+// Ring depth for two CTAs per SM.
+int rows_stages(int Mp, int smem_per_sm, int smem_per_block)
+{
+    const int budget = std::min(smem_per_sm / 2 - 1024, smem_per_block) - rows_smem(Mp, 0) - 16 * SG_MAX_STAGES;
+    return std::max(2, std::min(SG_MAX_STAGES, budget / (RW_BYTES + Mp * SB)));
+}
+
+// Clusters of `split` CTAs that the GPU holds at once (0 if the query fails); cached.
+int max_clusters(RowsKernel kern, int split, int smem)
+{
+    static std::mutex mu;
+    static std::map<std::pair<RowsKernel, std::pair<int, long long>>, int> cache;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const auto key = std::make_pair(kern, std::make_pair(dev, ((long long)split << 32) | smem));
+    std::lock_guard<std::mutex> lk(mu);
+    const auto it = cache.find(key);
+    if (it != cache.end()) return it->second;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)split);
+    cfg.blockDim = dim3(R_THREADS);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+        n = 0;
+        cudaGetLastError();
+    }
+    cache[key] = n;
+    return n;
+}
+
+fdpp_status launch_rows(const fdpp_scaled_gemm_params& p, ScaledArgs& g, const void* x, const void* w, int smem_sm, int smem_blk,
+                        cudaStream_t s)
+{
+    g.Mp = (p.M + 15) / 16 * 16;
+    g.nstage = rows_stages(g.Mp, smem_sm, smem_blk);
+    const int smem = rows_smem(g.Mp, g.nstage), tiles = (p.N + SG_N - 1) / SG_N;
+    const RowsKernel kern = p.out_dtype == FDPP_F32 ? rows_kernel<float>(g.Mp) : rows_kernel<__nv_bfloat16>(g.Mp);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return sfail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    g.split_k = p.split_k;
+    if (!g.split_k) {
+        // as many ranges as keep all clusters on the GPU at once, with two blocks each at least
+        g.split_k = 1;
+        for (int n = std::min(SG_MAX_SPLIT, g.kb / 2); n > 1; --n)
+            if (tiles <= max_clusters(kern, n, smem)) {
+                g.split_k = n;
+                break;
+            }
+    }
+    CUtensorMap tw, tx;
+    fdpp_status st;
+    if ((st = encode_rows(&tw, w, p.N, p.K, p.w_stride, SG_N)) != FDPP_OK) return st;
+    if ((st = encode_rows(&tx, x, p.M, p.K, p.x_stride, g.Mp)) != FDPP_OK) return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)tiles * g.split_k);
+    cfg.blockDim = dim3(R_THREADS);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)g.split_k;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, kern, tw, tx, g);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return sfail(FDPP_ERR_CUDA, "scaled GEMM launch: %s", cudaGetErrorString(e));
+    return FDPP_OK;
+}
+
+template <typename T, int BN>
+fdpp_status launch_tile(const fdpp_scaled_gemm_params& p, ScaledArgs& g, const void* x, const void* w, int sms, int smem_blk,
+                        cudaStream_t s)
+{
+    constexpr int smem = TileSmem<BN>::TOTAL;
+    if (smem > smem_blk) return sfail(FDPP_ERR_UNSUPPORTED, "too little shared memory for the tile kernel");
+    const long long m_tiles = ((long long)p.M + SG_ROWS - 1) / SG_ROWS, n_tiles = ((long long)p.N + BN - 1) / BN;
+    if (m_tiles * n_tiles >= (1ll << 31) - sms || T_GROUP * n_tiles >= (1ll << 31))
+        return sfail(FDPP_ERR_INVALID_ARG, "problem too large for one call");
+    g.m_tiles = (int)m_tiles;
+    g.n_tiles = (int)n_tiles;
+    CUtensorMap tw, tx;
+    fdpp_status st;
+    if ((st = encode_rows(&tw, w, p.N, p.K, p.w_stride, BN)) != FDPP_OK) return st;
+    if ((st = encode_rows(&tx, x, p.M, p.K, p.x_stride, SG_ROWS)) != FDPP_OK) return st;
+    auto kern = scaled_tile_kernel<T, BN>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return sfail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::min<long long>(sms, m_tiles * n_tiles));
+    cfg.blockDim = dim3(T_THREADS);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, tx, tw, g);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return sfail(FDPP_ERR_CUDA, "scaled GEMM launch: %s", cudaGetErrorString(e));
+    return FDPP_OK;
+}
+
+}  // namespace
+}  // namespace fdpp
+
+using namespace fdpp;
+
+extern "C" {
+
+size_t fdpp_scaled_gemm_workspace_size(const fdpp_scaled_gemm_params* p) { return check_params(p) == FDPP_OK ? 256 : 0; }
+
+fdpp_status fdpp_scaled_gemm(const void* x, const float* x_scales, const void* w, const float* w_scales,
+                             const fdpp_scaled_gemm_params* p, void* workspace, size_t workspace_bytes, void* y,
+                             fdpp_stream stream)
+{
+    fdpp_status st = check_params(p);
+    if (st != FDPP_OK) return st;
+    if (!x || !x_scales || !w || !w_scales || !y) return sfail(FDPP_ERR_INVALID_ARG, "x, w, their scales and y must be non-NULL");
+    if (((uintptr_t)x | (uintptr_t)w) % 16 != 0) return sfail(FDPP_ERR_INVALID_ARG, "x and w must be 16-byte aligned");
+    if (((uintptr_t)x_scales | (uintptr_t)w_scales) % 4 != 0) return sfail(FDPP_ERR_INVALID_ARG, "scales must be 4-byte aligned");
+    if ((uintptr_t)y % (p->out_dtype == FDPP_F32 ? 4 : 2) != 0) return sfail(FDPP_ERR_INVALID_ARG, "y must be aligned to its elements");
+    if (!workspace) return sfail(FDPP_ERR_WORKSPACE, "workspace is NULL");
+    if ((uintptr_t)workspace % 256 != 0) return sfail(FDPP_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (workspace_bytes < 256) return sfail(FDPP_ERR_WORKSPACE, "workspace has %zu bytes, 256 needed", workspace_bytes);
+    int sms = 0, smem_sm = 0, smem_blk = 0;
+    if ((st = query_device(&sms, &smem_sm, &smem_blk)) != FDPP_OK) return st;
+    if (p->M == 0) return FDPP_OK;
+
+    ScaledArgs g{};
+    g.sx = x_scales;
+    g.sw = w_scales;
+    g.y = y;
+    g.err = static_cast<unsigned*>(workspace);
+    g.y_stride = p->y_stride;
+    g.sx_stride = p->x_scale_stride;
+    g.M = p->M;
+    g.N = p->N;
+    g.kb = blocks_of(p->K);
+    cudaStream_t s = (cudaStream_t)stream;
+    if (p->M <= SG_ROWS) return launch_rows(*p, g, x, w, smem_sm, smem_blk, s);
+    // weight tiles of 256 where they alone are at least a tile per SM, else of 128
+    const long long tiles = ((p->M + (long long)SG_ROWS - 1) / SG_ROWS) * ((p->N + 255ll) / 256);
+    const bool big = tiles >= sms;
+    if (p->out_dtype == FDPP_F32)
+        return big ? launch_tile<float, 256>(*p, g, x, w, sms, smem_blk, s) : launch_tile<float, 128>(*p, g, x, w, sms, smem_blk, s);
+    return big ? launch_tile<__nv_bfloat16, 256>(*p, g, x, w, sms, smem_blk, s)
+               : launch_tile<__nv_bfloat16, 128>(*p, g, x, w, sms, smem_blk, s);
+}
+
+}  // extern "C"
