@@ -31,9 +31,11 @@ FDPP_FLAG_OUT, FDPP_FLAG_ABOVE, FDPP_FLAG_BELOW, FDPP_FLAG_NAN, FDPP_FLAG_RECOMP
 FDPP_FLAG_SLOT = 32
 FDPP_ERRBIT_SEQ_LEN, FDPP_ERRBIT_BLOCK_TABLE, FDPP_ERRBIT_TIMEOUT = 1, 2, 4
 FDPP_ERRBIT_POOL, FDPP_ERRBIT_ROOM, FDPP_ERRBIT_SLOT, FDPP_ERRBIT_TOKENS, FDPP_ERRBIT_PREFIX = 8, 16, 32, 64, 128
+FDPP_ERRBIT_TREE = 256
 FDPP_ROPE_PLAIN, FDPP_ROPE_LINEAR, FDPP_ROPE_NTK, FDPP_ROPE_PARTS = 0, 1, 2, 3
 FDPP_ROWS_MAX_GROUP = 128
 FDPP_ROWS_MAX_SOFTCAP = 4096.0
+FDPP_TREE_MAX_TOKENS, FDPP_TREE_MAX_CACHES = 256, 256
 FDPP_AUTO_UNITS_PER_SM, FDPP_AUTO_GRANULE, FDPP_AUTO_MIN_SPLIT = 4, 64, 256
 
 # Names every build of the library exports (the C ABI of the headers in include/).
@@ -45,7 +47,8 @@ EXPORTED = ("fdpp_max_splits", "fdpp_workspace_size", "fdpp_workspace_init", "fd
             "fdpp_flat_gemm_set_lut", "fdpp_flat_gemm_read_error",
             "fdpp_block_map_workspace_size", "fdpp_block_map", "fdpp_rope_table", "fdpp_rope_append",
             "fdpp_read_error", "fdpp_rows_workspace_size", "fdpp_rows_attn", "fdpp_prefix_attn",
-            "fdpp_rms_norm", "fdpp_scaled_gemm_workspace_size", "fdpp_scaled_gemm")
+            "fdpp_rms_norm", "fdpp_scaled_gemm_workspace_size", "fdpp_scaled_gemm",
+            "fdpp_tree_workspace_size", "fdpp_tree_attn", "fdpp_commit_workspace_size", "fdpp_tree_commit")
 FDPP_GEMM_MAX_M = 128
 FDPP_NOALLOC_WORKSPACE_BYTES = 16 << 20
 FDPP_TC_MAX_PARTS = 512
@@ -137,6 +140,11 @@ class fdpp_scaled_gemm_params(ctypes.Structure):
     ]
 
 
+class fdpp_commit_params(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int) for name in ("batch", "num_tokens", "max_seq_len", "block_size", "max_blocks_per_seq",
+                                                  "num_kv_blocks")] + [("row_bytes", ctypes.c_longlong)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -211,6 +219,15 @@ def _load() -> ctypes.CDLL:
     lib.fdpp_scaled_gemm_workspace_size.restype = cz
     lib.fdpp_scaled_gemm.argtypes = [vp, vp, vp, vp, PS, vp, cz, vp, vp]
     lib.fdpp_scaled_gemm.restype = ci
+    PC = ctypes.POINTER(fdpp_commit_params)
+    lib.fdpp_tree_workspace_size.argtypes = [PA, ctypes.POINTER(cz)]
+    lib.fdpp_tree_workspace_size.restype = ci
+    lib.fdpp_tree_attn.argtypes = [vp] * 7 + [PA, vp, cz, vp, vp]
+    lib.fdpp_tree_attn.restype = ci
+    lib.fdpp_commit_workspace_size.argtypes = [PC]
+    lib.fdpp_commit_workspace_size.restype = cz
+    lib.fdpp_tree_commit.argtypes = [vp] * 7 + [ci, PC, vp, cz] + [vp] * 5
+    lib.fdpp_tree_commit.restype = ci
     return lib
 
 
@@ -617,3 +634,60 @@ def fdpp_scaled_gemm(x, x_scales, w, w_scales, p: fdpp_scaled_gemm_params, works
     _check(lib.fdpp_scaled_gemm(x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), p,
                                 workspace.data_ptr(), _bytes(workspace), y.data_ptr(), _stream_handle(stream)),
            "fdpp_scaled_gemm")
+
+
+# ---- trees of drafted tokens (include/fdpp_tree.h) ------------------------------------------
+
+def fdpp_tree_workspace_size(p: fdpp_rows_params) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib.fdpp_tree_workspace_size(ctypes.byref(p), ctypes.byref(n)), "fdpp_tree_workspace_size")
+    return n.value
+
+
+def alloc_tree_workspace(p: fdpp_rows_params, device="cuda", stream=None):
+    """Allocates (torch) and zeroes a workspace of fdpp_tree_attn for `p`."""
+    import torch
+    ws = torch.empty(fdpp_tree_workspace_size(p), dtype=torch.uint8, device=device)
+    fdpp_workspace_init(ws, stream)
+    return ws
+
+
+def fdpp_tree_attn(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, parents, p: fdpp_rows_params, workspace, out,
+                   stream=None) -> None:
+    """fdpp_rows_attn of trees of drafted tokens: each token sees its sequence's cache, its ancestors and
+    itself (parents: int32 device tensor [T], indices within the sequence's tokens, -1 for a root)."""
+    _check(lib.fdpp_tree_attn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(block_table), seq_lens.data_ptr(),
+                              _ptr(cu_tokens), parents.data_ptr(), p, workspace.data_ptr(), _bytes(workspace),
+                              out.data_ptr(), _stream_handle(stream)), "fdpp_tree_attn")
+
+
+def make_commit_params(*, batch, num_tokens, max_seq_len, row_bytes, block_size=0, max_blocks_per_seq=0,
+                       num_kv_blocks=0) -> fdpp_commit_params:
+    """row_bytes: bytes of a token's row in each cache (num_kv_heads * head_dim * element size)."""
+    return fdpp_commit_params(batch, num_tokens, max_seq_len, block_size, max_blocks_per_seq, num_kv_blocks, row_bytes)
+
+
+def make_cache_list(caches):
+    """The K and V caches of a model's layers (contiguous device tensors, all different) as the array that
+    fdpp_tree_commit takes; the caller keeps them alive as long as it is used."""
+    caches = list(caches)
+    return (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches])
+
+
+def alloc_commit_workspace(p: fdpp_commit_params, device="cuda"):
+    """A zeroed uint8 device tensor large enough for fdpp_tree_commit with `p`."""
+    import torch
+    n = int(lib.fdpp_commit_workspace_size(p))
+    if n == 0:
+        raise FdppError(FDPP_ERR_INVALID_ARG, "fdpp_commit_workspace_size", lib.fdpp_last_error().decode())
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def fdpp_tree_commit(parents, tokens, choices, seq_lens, cu_tokens, block_table, caches, p: fdpp_commit_params, workspace,
+                     new_lens, accepted, path, chosen, stream=None) -> None:
+    """Follows the choices down each tree and moves the accepted tokens' rows of all `caches`
+    (make_cache_list) together (int32 device tensors; cu_tokens and block_table may be None)."""
+    _check(lib.fdpp_tree_commit(parents.data_ptr(), tokens.data_ptr(), choices.data_ptr(), seq_lens.data_ptr(),
+                                _ptr(cu_tokens), _ptr(block_table), caches, len(caches), p, workspace.data_ptr(),
+                                _bytes(workspace), new_lens.data_ptr(), accepted.data_ptr(), path.data_ptr(),
+                                chosen.data_ptr(), _stream_handle(stream)), "fdpp_tree_commit")

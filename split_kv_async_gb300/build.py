@@ -20,10 +20,10 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfdpp.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cpp", "split_tc.cu", "split_um.cu", "split_simt.cu", "combine.cu", "no_alloc.cu",
-           "flat_gemm.cu", "cache_ops.cu", "rows_api.cpp", "rows_simt.cu", "rows_tc.cu", "norm.cu",
-           "scaled_gemm.cu"]
+           "flat_gemm.cu", "cache_ops.cu", "rows_api.cpp", "rows_simt.cu", "rows_tc.cu", "rows_tree.cu", "norm.cu",
+           "scaled_gemm.cu", "tree.cu"]
 HEADERS = ["fdpp_internal.h", "device_common.cuh", "split_tc_common.cuh", "tcgen05.cuh", "rows_internal.h",
-           "rows_common.cuh", "gemm_common.cuh"]
+           "rows_common.cuh", "rows_tc.cuh", "gemm_common.cuh"]
 
 
 def _nvcc() -> str:
@@ -36,7 +36,7 @@ def _nvcc() -> str:
 def _newest_input() -> float:
     paths = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
     paths += [os.path.join(INCLUDE, h) for h in ("fdpp.h", "fdpp_gemm.h", "fdpp_cache.h", "fdpp_rows.h",
-                                                "fdpp_linear.h")]
+                                                "fdpp_linear.h", "fdpp_tree.h")]
     paths.append(os.path.abspath(__file__))
     return max(os.path.getmtime(p) for p in paths)
 

@@ -87,6 +87,15 @@ fdpp_status check_params(const fdpp_rows_params* p)
     return FDPP_OK;
 }
 
+fdpp_status check_tree(const fdpp_rows_params* p)
+{
+    const fdpp_status st = check_params(p);
+    if (st != FDPP_OK) return st;
+    if (p->slopes) return rfail(FDPP_ERR_UNSUPPORTED, "a tree's keys have no bias on distance: slopes must be NULL");
+    if (p->key_end) return rfail(FDPP_ERR_INVALID_ARG, "the tree says which keys a token sees last: key_end must be NULL");
+    return FDPP_OK;
+}
+
 fdpp_status check_paged(const fdpp_rows_params* p)
 {
     if (p->block_size < 16 || p->block_size > 256 || (p->block_size & (p->block_size - 1)))
@@ -137,9 +146,12 @@ fdpp_status encode_q(CUtensorMap* map, const void* q, const fdpp_rows_params& p,
     return FDPP_OK;
 }
 
+// A call with trees: the lines of ancestors lie behind the rest.
+size_t tree_bytes(const fdpp_rows_params& p) { return align256(rows_layout(p).total + (size_t)p.num_tokens * LINE_WORDS * 4); }
+
 fdpp_status attend(const void* q, const void* prefix_k, const void* prefix_v, const int32_t* prefix_blocks,
                    const int32_t* prefix_len, bool prefix, const void* k_cache, const void* v_cache,
-                   const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_tokens,
+                   const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_tokens, const int32_t* parents,
                    const fdpp_rows_params* p, void* workspace, size_t workspace_bytes, void* out, fdpp_stream stream)
 {
     fdpp_status st = check_params(p);
@@ -169,8 +181,9 @@ fdpp_status attend(const void* q, const void* prefix_k, const void* prefix_v, co
     if (!workspace) return rfail(FDPP_ERR_WORKSPACE, "workspace is NULL");
     if (!aligned(workspace, 256)) return rfail(FDPP_ERR_WORKSPACE, "workspace must be 256-byte aligned");
     const RowsLayout w = rows_layout(*p);
-    if (workspace_bytes < w.total)
-        return rfail(FDPP_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, w.total);
+    const size_t need = parents ? tree_bytes(*p) : w.total;
+    if (workspace_bytes < need)
+        return rfail(FDPP_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
     int sms = 0, smem_sm = 0, smem_blk = 0;
     if ((st = query_device(&sms, &smem_sm, &smem_blk)) != FDPP_OK) return st;
 
@@ -220,6 +233,12 @@ fdpp_status attend(const void* q, const void* prefix_k, const void* prefix_v, co
     a.cap = p->softcap;
 
     cudaStream_t s = (cudaStream_t)stream;
+    if (parents) {
+        a.parents = parents;
+        a.lineage = reinterpret_cast<uint32_t*>(ws + w.total);
+        const cudaError_t e = launch_lineage(a, s);
+        if (e != cudaSuccess) return rfail(FDPP_ERR_CUDA, "lineage kernel launch: %s", cudaGetErrorString(e));
+    }
     if (!tensor_kernel(*p)) {
         a.splits = simt_splits(*p);
         const cudaError_t e = launch_rows_simt(a, p->dtype, s);
@@ -303,8 +322,8 @@ fdpp_status fdpp_rows_attn(const void* q, const void* k_cache, const void* v_cac
                            const int32_t* seq_lens, const int32_t* cu_tokens, const fdpp_rows_params* p, void* workspace,
                            size_t workspace_bytes, void* out, fdpp_stream stream)
 {
-    return attend(q, nullptr, nullptr, nullptr, nullptr, false, k_cache, v_cache, block_table, seq_lens, cu_tokens, p,
-                  workspace, workspace_bytes, out, stream);
+    return attend(q, nullptr, nullptr, nullptr, nullptr, false, k_cache, v_cache, block_table, seq_lens, cu_tokens, nullptr,
+                  p, workspace, workspace_bytes, out, stream);
 }
 
 fdpp_status fdpp_prefix_attn(const void* q, const void* prefix_k, const void* prefix_v, const int32_t* prefix_blocks,
@@ -314,7 +333,28 @@ fdpp_status fdpp_prefix_attn(const void* q, const void* prefix_k, const void* pr
                              fdpp_stream stream)
 {
     return attend(q, prefix_k, prefix_v, prefix_blocks, prefix_len, true, k_cache, v_cache, block_table, seq_lens,
-                  cu_tokens, p, workspace, workspace_bytes, out, stream);
+                  cu_tokens, nullptr, p, workspace, workspace_bytes, out, stream);
+}
+
+fdpp_status fdpp_tree_workspace_size(const fdpp_rows_params* p, size_t* bytes)
+{
+    const fdpp_status st = check_tree(p);
+    if (st != FDPP_OK) return st;
+    if (!bytes) return rfail(FDPP_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = tree_bytes(*p);
+    return FDPP_OK;
+}
+
+fdpp_status fdpp_tree_attn(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                           const int32_t* seq_lens, const int32_t* cu_tokens, const int32_t* parents,
+                           const fdpp_rows_params* p, void* workspace, size_t workspace_bytes, void* out,
+                           fdpp_stream stream)
+{
+    const fdpp_status st = check_tree(p);
+    if (st != FDPP_OK) return st;
+    if (!parents || !aligned(parents, 4)) return rfail(FDPP_ERR_INVALID_ARG, "parents must be non-NULL and 4-byte aligned");
+    return attend(q, nullptr, nullptr, nullptr, nullptr, false, k_cache, v_cache, block_table, seq_lens, cu_tokens, parents,
+                  p, workspace, workspace_bytes, out, stream);
 }
 
 }  // extern "C"

@@ -6,6 +6,7 @@
 
 #include "fdpp_internal.h"
 #include "fdpp_rows.h"
+#include "fdpp_tree.h"
 
 namespace fdpp {
 
@@ -83,10 +84,19 @@ struct RowsArgs {
     int tpt, tpn;                   // tokens per 128-row tile and per key-major run: floor(128 / G), floor(32 / G)
     int max_rt, slot_rows, parts, splits, stages;
     float scale, cap;
+    // trees of drafted tokens (fdpp_tree.h): nullptr without
+    const int32_t* parents;
+    uint32_t* lineage;              // [T][LINE_WORDS]
 };
+
+// A token's line of ancestors: the key of its sequence's node 0, then a bit for every node that is the token
+// itself or one of its ancestors.
+constexpr int LINE_WORDS = 1 + FDPP_TREE_MAX_TOKENS / 32;
 
 RowsLayout rows_layout(const fdpp_rows_params& p);
 
+// The tokens' lines of ancestors, before either kernel of a call with trees.
+cudaError_t launch_lineage(const RowsArgs& a, cudaStream_t s);
 cudaError_t launch_rows_simt(const RowsArgs& a, int dtype, cudaStream_t s);
 // Plan, tile kernel and join.
 struct RowsMaps {
@@ -95,6 +105,7 @@ struct RowsMaps {
     CUtensorMap pk, pv;    // the prefix (the pools again for paged caches)
 };
 cudaError_t launch_rows_tc(const RowsArgs& a, const RowsMaps& m, cudaStream_t s);
+cudaError_t launch_rows_tree(const RowsArgs& a, const RowsMaps& m, cudaStream_t s);
 // K/V stages that fit the device's shared memory per block.
 int rows_tc_stages(int head_dim, int smem_per_block);
 

@@ -47,7 +47,7 @@ __device__ __forceinline__ void store_one(__nv_bfloat16* p, float x) { *p = __fl
 // Weight of a partial with max m in the frame M (M = -inf: no key yet).
 __device__ __forceinline__ float join_weight(float m, float M) { return m == M ? 1.f : ex2(m - M); }
 
-template <typename T, int D>
+template <typename T, int D, bool TREE>
 __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
 {
     constexpr int NV = D / (LANES * 4);        // 4-element pieces per lane
@@ -97,6 +97,8 @@ __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
     const int pos = P + L - n + (row - c0);
     int lo, hi;
     row_keys(a, row, pos, P + L, lo, hi);
+    if (TREE && tree_too_large(a, n)) lo = hi = 0;
+    const uint32_t* line = TREE ? a.lineage + (long long)row * LINE_WORDS : nullptr;
     const int len = hi - lo;
     const int k0 = lo + (int)((long long)len * split / a.splits), k1 = lo + (int)((long long)len * (split + 1) / a.splits);
 
@@ -121,6 +123,7 @@ __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
 
 #pragma unroll 2
     for (int t = k0 + grp; t < k1; t += GROUPS) {
+        if (TREE && !line_sees(line, t)) continue;
         const bool pre = t < P;
         const long long off = key_offset(a, pre ? -1 : b, pre ? t : t - P, g);
         if (off < 0) {
@@ -277,9 +280,15 @@ __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
 
 cudaError_t launch_rows_simt(const RowsArgs& a, int dtype, cudaStream_t s)
 {
-    void (*kern)(RowsArgs) = dtype == FDPP_F32 ? (a.D == 128 ? rows_simt_kernel<float, 128> : rows_simt_kernel<float, 64>)
-                                               : (a.D == 128 ? rows_simt_kernel<__nv_bfloat16, 128>
-                                                             : rows_simt_kernel<__nv_bfloat16, 64>);
+    void (*kern)(RowsArgs);
+    if (a.parents)
+        kern = dtype == FDPP_F32 ? (a.D == 128 ? rows_simt_kernel<float, 128, true> : rows_simt_kernel<float, 64, true>)
+                                 : (a.D == 128 ? rows_simt_kernel<__nv_bfloat16, 128, true>
+                                               : rows_simt_kernel<__nv_bfloat16, 64, true>);
+    else
+        kern = dtype == FDPP_F32 ? (a.D == 128 ? rows_simt_kernel<float, 128, false> : rows_simt_kernel<float, 64, false>)
+                                 : (a.D == 128 ? rows_simt_kernel<__nv_bfloat16, 128, false>
+                                               : rows_simt_kernel<__nv_bfloat16, 64, false>);
     const int chunks = (a.G + ROWS_SIMT_HEADS - 1) / ROWS_SIMT_HEADS;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)a.T * a.Hkv * chunks + 1), (unsigned)a.splits);      // (the last one checks)
