@@ -14,6 +14,21 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// mbar_wait for hand-overs of a few hundred cycles: the clock, whose reading takes as long, is first read
+// after 64 tries.
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity)
+{
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            const uint64_t now = global_ns();
+            if (t0 == 0) t0 = now;
+            else if (now - t0 > FDPP_WAIT_NS) return false;
+        }
+    }
+}
+
 // Barrier of every thread of the cluster; the arrive releases and the wait acquires this
 // thread's (and, through them, the CTA's) shared-memory writes at cluster scope.
 __device__ __forceinline__ void cluster_sync_all()

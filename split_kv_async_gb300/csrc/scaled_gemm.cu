@@ -50,14 +50,75 @@ struct ScaledArgs {
     int m_tiles, n_tiles;                // tile kernel
 };
 
-__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+// D (+)= A B^T of 32 channels, issued by the lane where `lead` is set: the whole warp runs the code around it, so
+// that the operands stay in uniform registers. A and B: the descriptors' low words. PAIR: two CTAs as one operand
+// (cta_group::2), issued by the first.
+template <bool PAIR>
+__device__ __forceinline__ void umma_e4m3(bool lead, uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t accumulate)
+{
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "setp.ne.b32 q, %6, 0;\n\t"
+            "mov.b64 da, {%1, %5};\n\t"
+            "mov.b64 db, {%2, %5};\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+            "r"(alo), "r"(blo), "r"(idesc), "r"(accumulate), "n"(SW128_DESC_HI), "r"((uint32_t)lead)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "setp.ne.b32 q, %6, 0;\n\t"
+            "mov.b64 da, {%1, %5};\n\t"
+            "mov.b64 db, {%2, %5};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+            "r"(alo), "r"(blo), "r"(idesc), "r"(accumulate), "n"(SW128_DESC_HI), "r"((uint32_t)lead)
+            : "memory");
+}
+
+// An arrival at the barrier, of both CTAs of a pair, when the MMAs issued so far have completed.
+template <bool PAIR>
+__device__ __forceinline__ void umma_done(bool lead, uint32_t bar)
+{
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %2, 0;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+            "h"((uint16_t)3), "r"((uint32_t)lead)
+            : "memory");
+    else
+        umma_commit(lead, bar);
+}
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// A load into this CTA's shared memory that completes on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
+}
+
+// An arrival at a barrier of either CTA. (Released to the CTA only, as what it tells of is not memory but that the
+// tensor-memory loads before it have completed; a release to the cluster waits a microsecond for the L2.)
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // Instruction descriptor of kind f8f6f4 with e4m3 A and B (types 0), both K-major, fp32 sums, M x N.
@@ -67,11 +128,12 @@ __host__ __device__ constexpr uint32_t umma_idesc_e4m3(int M, int N)
 }
 
 // A block of 128 channels: four MMAs of 32.
-__device__ __forceinline__ void umma_block(uint32_t d_tmem, uint32_t a0, uint32_t b0, uint32_t idesc)
+template <bool PAIR>
+__device__ __forceinline__ void umma_block(bool lead, uint32_t d_tmem, uint32_t a0, uint32_t b0, uint32_t idesc)
 {
+    const uint32_t alo = sw128_kmajor_lo(a0), blo = sw128_kmajor_lo(b0);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        umma_e4m3(d_tmem, sw128_kmajor_desc(a0 + k * 32), sw128_kmajor_desc(b0 + k * 32), idesc, k > 0 ? 1u : 0u);
+    for (int k = 0; k < 4; ++k) umma_e4m3<PAIR>(lead, d_tmem, alo + 2 * k, blo + 2 * k, idesc, k > 0 ? 1u : 0u);
 }
 
 __device__ __forceinline__ uint64_t pack2(float x, float y)
@@ -99,10 +161,46 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     return d;
 }
 
+// acc += s v for the 64 consecutive columns v of this thread's tensor-memory lane, two columns to an operation (s2: s
+// twice). One statement from the load to the sums: with the columns handed to C++ in between, a third of the
+// instructions were moves from register to register (per block of 128 x 256: 231 of a warp's, against 130), and two loads
+// of 32 columns wait for tensor memory twice as often.
+#define SUM2(acc, lo, hi) "mov.b64 d, {t" #lo ", t" #hi "};\n\tfma.rn.f32x2 %" #acc ", d, %32, %" #acc ";\n\t"
+#define SUM8(a0, a1, a2, a3, c0, c1, c2, c3, c4, c5, c6, c7) SUM2(a0, c0, c1) SUM2(a1, c2, c3) SUM2(a2, c4, c5) SUM2(a3, c6, c7)
+__device__ __forceinline__ void tmem_sum64(uint32_t taddr, uint64_t s2, uint64_t* a)
+{
+    asm volatile(
+        "{\n\t.reg .b32 t<64>;\n\t.reg .b64 d;\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+        "t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, t12, t13, t14, t15, "
+        "t16, t17, t18, t19, t20, t21, t22, t23, t24, t25, t26, t27, t28, t29, t30, t31, "
+        "t32, t33, t34, t35, t36, t37, t38, t39, t40, t41, t42, t43, t44, t45, t46, t47, "
+        "t48, t49, t50, t51, t52, t53, t54, t55, t56, t57, t58, t59, t60, t61, t62, t63}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n\t"
+        SUM8(0, 1, 2, 3, 0, 1, 2, 3, 4, 5, 6, 7)
+        SUM8(4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15)
+        SUM8(8, 9, 10, 11, 16, 17, 18, 19, 20, 21, 22, 23)
+        SUM8(12, 13, 14, 15, 24, 25, 26, 27, 28, 29, 30, 31)
+        SUM8(16, 17, 18, 19, 32, 33, 34, 35, 36, 37, 38, 39)
+        SUM8(20, 21, 22, 23, 40, 41, 42, 43, 44, 45, 46, 47)
+        SUM8(24, 25, 26, 27, 48, 49, 50, 51, 52, 53, 54, 55)
+        SUM8(28, 29, 30, 31, 56, 57, 58, 59, 60, 61, 62, 63)
+        "}"
+        : "+l"(a[0]), "+l"(a[1]), "+l"(a[2]), "+l"(a[3]), "+l"(a[4]), "+l"(a[5]), "+l"(a[6]), "+l"(a[7]),
+          "+l"(a[8]), "+l"(a[9]), "+l"(a[10]), "+l"(a[11]), "+l"(a[12]), "+l"(a[13]), "+l"(a[14]), "+l"(a[15]),
+          "+l"(a[16]), "+l"(a[17]), "+l"(a[18]), "+l"(a[19]), "+l"(a[20]), "+l"(a[21]), "+l"(a[22]), "+l"(a[23]),
+          "+l"(a[24]), "+l"(a[25]), "+l"(a[26]), "+l"(a[27]), "+l"(a[28]), "+l"(a[29]), "+l"(a[30]), "+l"(a[31])
+        : "l"(s2), "r"(taddr)
+        : "memory");
+}
+#undef SUM8
+#undef SUM2
+
 // Every lane waits; one that runs out aborts the CTA (warp-uniform result).
 __device__ __forceinline__ bool gwait(uint32_t bar, uint32_t parity, volatile int* abort_, unsigned* err)
 {
-    bool ok = *abort_ == 0 && mbar_wait(bar, parity & 1u);
+    if (__builtin_expect(__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u)), 1)) return true;
+    bool ok = *abort_ == 0 && mbar_wait_short(bar, parity & 1u);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok && (threadIdx.x & 31) == 0) {
         *abort_ = 1;
@@ -117,10 +215,11 @@ __device__ __forceinline__ void store_y(float* p, float v) { *p = v; }
 // ---- rows kernel --------------------------------------------------------------------------
 
 constexpr int R_THREADS = 192;           // producer warp, MMA warp, 4 warps that scale and add
+constexpr int R_SCALES = 8;              // blocks of K whose scales are loaded together
 constexpr int RW_BYTES = SG_N * SB;      // weight slice of a stage
 
 // Shared memory (dynamic, 1024-byte aligned base): nstage stages of [w slice 16 KB | x slice Mp x 128 B],
-// then the scales of two blocks, the barriers, the TMEM address and the abort flag. Once every MMA has
+// then the scales of 16 blocks, the barriers, the TMEM address and the abort flag. Once every MMA has
 // completed, the stages hold this CTA's fp32 sums [M][128] for the cluster's reduction.
 template <typename T, int NR>
 __global__ void __launch_bounds__(R_THREADS, 2)
@@ -132,8 +231,8 @@ __global__ void __launch_bounds__(R_THREADS, 2)
     const uint32_t sbase = smem_u32(sm);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int stage_bytes = RW_BYTES + g.Mp * SB;
-    float* scale = reinterpret_cast<float*>(sm + g.nstage * stage_bytes);        // [2][SG_ROWS]
-    const int bar_off = g.nstage * stage_bytes + 2 * SG_ROWS * 4;
+    float* scale = reinterpret_cast<float*>(sm + g.nstage * stage_bytes);        // [2 R_SCALES][SG_ROWS]
+    const int bar_off = g.nstage * stage_bytes + 2 * R_SCALES * SG_ROWS * 4;
     const uint32_t bars = sbase + bar_off;
     const uint32_t full = bars, empty = bars + 8 * g.nstage, accf = bars + 16 * g.nstage, acce = accf + 16;
     volatile uint32_t* tslot = reinterpret_cast<volatile uint32_t*>(sm + bar_off + 16 * g.nstage + 32);
@@ -184,7 +283,7 @@ __global__ void __launch_bounds__(R_THREADS, 2)
             for (int i = pre; i < nkb; ++i) {
                 const int s = i % g.nstage;
                 const uint32_t par = (uint32_t)(i / g.nstage) & 1u;
-                if (*abort_ || !mbar_wait(empty + 8 * s, par ^ 1u)) {
+                if (*abort_ || !mbar_wait_short(empty + 8 * s, par ^ 1u)) {
                     atomicOr(g.err, FDPP_ERRBIT_TIMEOUT);
                     *abort_ = 1;
                     break;
@@ -202,29 +301,25 @@ __global__ void __launch_bounds__(R_THREADS, 2)
         }
     } else if (warp == 1) {
         grid_dependency_wait();
-        if (lane == 0) {
-            const uint32_t idesc = umma_idesc_e4m3(SG_N, g.Mp);
-            int done = 0;
-            for (; done < nkb; ++done) {
-                const int s = done % g.nstage, b = done & 1;
-                const uint32_t par = (uint32_t)(done / g.nstage) & 1u;
-                if (*abort_ || !mbar_wait(acce + 8 * b, ((uint32_t)(done >> 1) & 1u) ^ 1u) || !mbar_wait(full + 8 * s, par)) {
-                    atomicOr(g.err, FDPP_ERRBIT_TIMEOUT);
-                    *abort_ = 1;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t a0 = sbase + s * stage_bytes;
-                umma_block(tmem + b * g.Mp, a0, a0 + RW_BYTES, idesc);
-                umma_commit(empty + 8 * s);
-                umma_commit(accf + 8 * b);
-            }
-            // after an abort the MMAs issued land before the CTA ends
-            if (*abort_ && done > 0) {
-                const int last = done - 1;
-                if (!mbar_wait(accf + 8 * (last & 1), (uint32_t)(last >> 1) & 1u)) atomicOr(g.err, FDPP_ERRBIT_TIMEOUT);
-            }
+        const uint32_t idesc = umma_idesc_e4m3(SG_N, g.Mp);
+        int done = 0;
+        for (; done < nkb; ++done) {
+            const int s = done % g.nstage, b = done & 1;
+            if (!gwait(acce + 8 * b, ((uint32_t)(done >> 1) & 1u) ^ 1u, abort_, g.err) ||
+                !gwait(full + 8 * s, (uint32_t)(done / g.nstage), abort_, g.err))
+                break;
+            tc_fence_after();
+            const bool lead = elect_one();
+            const uint32_t a0 = sbase + s * stage_bytes;
+            umma_block<false>(lead, tmem + b * g.Mp, a0, a0 + RW_BYTES, idesc);
+            umma_commit(lead, empty + 8 * s);
+            umma_commit(lead, accf + 8 * b);
+            __syncwarp();
         }
+        // after an abort the MMAs issued land before the CTA ends
+        if (*abort_ && done > 0 && !mbar_wait_short(accf + 8 * ((done - 1) & 1), (uint32_t)((done - 1) >> 1) & 1u))
+            atomicOr(g.err, FDPP_ERRBIT_TIMEOUT);
+        __syncwarp();
     } else {
         grid_dependency_wait();
         // ---- TMEM lanes 32 (warp % 4) .. hold weight rows n0 + that lane ----
@@ -236,14 +331,26 @@ __global__ void __launch_bounds__(R_THREADS, 2)
         uint64_t acc[NR / 2];
 #pragma unroll
         for (int j = 0; j < NR / 2; ++j) acc[j] = 0ull;
-        float next = t < g.M ? sx[kb0] * sw[kb0] : 0.f;
+        // the scales of eight blocks at a time, loaded eight blocks ahead: a load takes longer than a block's
+        // MMAs while the ring keeps the memory busy
+        float next[R_SCALES];
+#pragma unroll
+        for (int j = 0; j < R_SCALES; ++j) next[j] = t < g.M && j < nkb ? sx[kb0 + j] * sw[kb0 + j] : 0.f;
         bool ok = true;
         for (int i = 0; i < nkb; ++i) {
             const int b = i & 1;
-            float* sc = scale + b * SG_ROWS;
-            sc[t] = next;
-            if (t < g.M && i + 1 < nkb) next = sx[kb0 + i + 1] * sw[kb0 + i + 1];
-            named_bar_sync(1, 128);      // (buffer b was last read two blocks ago, before the barrier between)
+            if (i % R_SCALES == 0) {
+                float* to = scale + (i / R_SCALES & 1) * R_SCALES * SG_ROWS + t;
+#pragma unroll
+                for (int j = 0; j < R_SCALES; ++j) to[j * SG_ROWS] = next[j];
+                named_bar_sync(1, 128);  // (this half was last read before the barrier eight blocks ago)
+#pragma unroll
+                for (int j = 0; j < R_SCALES; ++j) {
+                    const int k = i + R_SCALES + j;
+                    next[j] = t < g.M && k < nkb ? sx[kb0 + k] * sw[kb0 + k] : 0.f;
+                }
+            }
+            const float* sc = scale + (i % (2 * R_SCALES)) * SG_ROWS;
             ok = gwait(accf + 8 * b, (uint32_t)(i >> 1), abort_, g.err) && ok;
             if (ok) {
                 tc_fence_after();
@@ -335,19 +442,29 @@ __global__ void __launch_bounds__(R_THREADS, 2)
 }
 
 // ---- tile kernel --------------------------------------------------------------------------
+// PAIR: two CTAs (a cluster, on neighbouring SMs) work on 256 rows as one tensor-core operand. Each holds its
+// 128 rows of x and half of the BN weight rows; the first one's MMA thread issues for both, each half's sums lie in its
+// own CTA's tensor memory. What this saves is shared-memory bandwidth: a block of 128 x 256 sums takes 512
+// cycles of the tensor cores, and 48 kB written and read again alone would be 768 at 128 bytes a cycle; with
+// half of w it is 32 kB, 512 cycles.
 
 constexpr int T_THREADS = 384;           // producer, MMA, two idle warps; 8 warps that scale and add
 constexpr int T_HELP_REGS = 80, T_SUM_REGS = 208;    // 128 x 80 + 256 x 208 = 63488 of the launch's 384 x 168
+constexpr int T_SCALES = 8;              // blocks of K whose scales are loaded together
 constexpr int T_GROUP = 16;              // row tiles that a run of weight tiles is shared by (see tile_at)
 
-template <int BN>
+template <int BN, bool PAIR>
 struct TileSmem {
-    static constexpr int STAGE = (SG_ROWS + BN) * SB;
+    static constexpr int W_ROWS = PAIR ? BN / 2 : BN;    // weight rows that a CTA holds
+    static constexpr int STAGE = (SG_ROWS + W_ROWS) * SB;
     static constexpr int TURN = 32 * 128;                // a warp's rows, 128 bytes of each
-    static constexpr int STAGES = BN == 256 ? 4 : 6;
+    static constexpr int STAGES = (163840 / STAGE) < SG_MAX_STAGES ? 163840 / STAGE : SG_MAX_STAGES;
     static constexpr int NBUF = 512 / BN;                // tensor-memory buffers of BN columns
-    static constexpr int BARS = STAGES * STAGE + 8 * TURN;
-    static constexpr int TOTAL = BARS + (2 * STAGES + 2 * NBUF) * 8 + 32 + 1024;
+    static constexpr int W_SCALES = BN / SG_N;           // a weight tile's scales
+    static constexpr int SCALES = T_SCALES * (SG_ROWS + W_SCALES);   // of T_SCALES blocks: [block][row], then w's [half][block]
+    static constexpr int SCALES_OFF = STAGES * STAGE + 8 * TURN;
+    static constexpr int BARS = SCALES_OFF + 2 * SCALES * 4;
+    static constexpr int TOTAL = BARS + (2 * STAGES + 2 * NBUF + 4) * 8 + 32 + 1024;
 };
 
 // Tile i of the order: T_GROUP row tiles at a time, the weight tiles outside, so that the CTAs at work
@@ -360,18 +477,23 @@ __device__ __forceinline__ void tile_at(const ScaledArgs& g, int i, int& mt, int
     mt = first + r - nt * rows;
 }
 
-template <typename T, int BN>
+template <typename T, int BN, bool PAIR>
 __global__ void __launch_bounds__(T_THREADS, 1)
     scaled_tile_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const ScaledArgs g)
 {
-    using L = TileSmem<BN>;
+    using L = TileSmem<BN, PAIR>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(sm);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t full = sbase + L::BARS, empty = full + 8 * L::STAGES, accf = empty + 8 * L::STAGES, acce = accf + 8 * L::NBUF;
-    volatile uint32_t* tslot = reinterpret_cast<volatile uint32_t*>(sm + L::BARS + (2 * L::STAGES + 2 * L::NBUF) * 8);
+    const uint32_t scf = acce + 8 * L::NBUF, sce = scf + 16;
+    volatile uint32_t* tslot = reinterpret_cast<volatile uint32_t*>(sm + L::BARS + (2 * L::STAGES + 2 * L::NBUF + 4) * 8);
+    float* scales = reinterpret_cast<float*>(sm + L::SCALES_OFF);
     volatile int* abort_ = reinterpret_cast<volatile int*>(tslot + 2);
+    const int rank = PAIR ? (int)cluster_rank() : 0;
+    // (both CTAs' loads complete on the first one's barriers, which its MMA thread waits for)
+    const uint32_t full0 = PAIR ? dsmem_addr(full, 0) : full, acce0 = PAIR ? dsmem_addr(acce, 0) : acce;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::STAGES; ++s) {
@@ -380,74 +502,125 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         }
         for (int b = 0; b < L::NBUF; ++b) {
             mbar_init(accf + 8 * b, 1);
-            mbar_init(acce + 8 * b, 8);
+            mbar_init(acce + 8 * b, PAIR ? 16 : 8);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(scf + 8 * b, 2);
+            mbar_init(sce + 8 * b, 8);
         }
         *abort_ = 0;
         fence_mbar_init();
         prefetch_tensormap(&tmW);
         prefetch_tensormap(&tmX);
     }
-    if (warp == 1) tmem_alloc(smem_u32((const void*)tslot), 512);
+    if (warp == 1) {
+        if (PAIR) tmem_alloc_pair(smem_u32((const void*)tslot), 512);
+        else tmem_alloc(smem_u32((const void*)tslot), 512);
+    }
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tslot;
     grid_dependency_wait();
     grid_launch_dependents();
     const int tiles = g.m_tiles * g.n_tiles;
+    const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(T_HELP_REGS));
         if (warp == 0 && lane == 0) {
             uint32_t i = 0;              // blocks issued
             bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int t = first; t < tiles && ok; t += step) {
                 int mt, nt;
                 tile_at(g, t, mt, nt);
+                const int m0 = (PAIR ? 2 * mt + rank : mt) * SG_ROWS, n0 = nt * BN + rank * L::W_ROWS;
                 for (int k = 0; k < g.kb; ++k, ++i) {
                     const uint32_t s = i % L::STAGES, par = (i / L::STAGES) & 1u;
-                    if (*abort_ || !mbar_wait(empty + 8 * s, par ^ 1u)) {
+                    if (*abort_ || !mbar_wait_short(empty + 8 * s, par ^ 1u)) {
                         atomicOr(g.err, FDPP_ERRBIT_TIMEOUT);
                         *abort_ = 1;
                         ok = false;
                         break;
                     }
                     const uint32_t dst = sbase + s * L::STAGE;
-                    mbar_arrive_expect_tx(full + 8 * s, (uint32_t)L::STAGE);
-                    tma_load_2d(dst, &tmX, k * SB, mt * SG_ROWS, full + 8 * s);
-                    tma_load_2d(dst + SG_ROWS * SB, &tmW, k * SB, nt * BN, full + 8 * s);
+                    if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, (uint32_t)((PAIR ? 2 : 1) * L::STAGE));
+                    if (PAIR) {
+                        tma_load_2d_pair(dst, &tmX, k * SB, m0, full0 + 8 * s);
+                        tma_load_2d_pair(dst + SG_ROWS * SB, &tmW, k * SB, n0, full0 + 8 * s);
+                    } else {
+                        tma_load_2d(dst, &tmX, k * SB, m0, full + 8 * s);
+                        tma_load_2d(dst + SG_ROWS * SB, &tmW, k * SB, n0, full + 8 * s);
+                    }
                 }
             }
-            if (!ok) {                   // every slice issued lands before the CTA ends
+            if (!ok && rank == 0) {      // every slice issued lands before the CTAs end
                 for (uint32_t j = i > L::STAGES ? i - L::STAGES : 0; j < i; ++j) {
                     const uint64_t t0 = global_ns();
                     while (!mbar_try_wait(full + 8 * (j % L::STAGES), (j / L::STAGES) & 1u) && global_ns() - t0 < 100000000ull) {
                     }
                 }
             }
-        } else if (warp == 1 && lane == 0) {
-            constexpr uint32_t IDESC = umma_idesc_e4m3(SG_ROWS, BN);
+        } else if (warp == 1 && rank == 0) {
+            constexpr uint32_t IDESC = umma_idesc_e4m3(PAIR ? 2 * SG_ROWS : SG_ROWS, BN);
             uint32_t i = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int t = first; t < tiles && ok; t += step) {
                 for (int k = 0; k < g.kb; ++k, ++i) {
                     const uint32_t s = i % L::STAGES, b = i % L::NBUF;
-                    if (*abort_ || !mbar_wait(acce + 8 * b, ((i / L::NBUF) & 1u) ^ 1u) || !mbar_wait(full + 8 * s, (i / L::STAGES) & 1u)) {
-                        atomicOr(g.err, FDPP_ERRBIT_TIMEOUT);
-                        *abort_ = 1;
+                    if (!gwait(acce + 8 * b, (i / L::NBUF) ^ 1u, abort_, g.err) || !gwait(full + 8 * s, i / L::STAGES, abort_, g.err)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
+                    const bool lead = elect_one();
                     const uint32_t a0 = sbase + s * L::STAGE;
-                    umma_block(tmem + b * BN, a0, a0 + SG_ROWS * SB, IDESC);
-                    umma_commit(empty + 8 * s);
-                    umma_commit(accf + 8 * b);
+                    umma_block<PAIR>(lead, tmem + b * BN, a0, a0 + SG_ROWS * SB, IDESC);
+                    umma_done<PAIR>(lead, empty + 8 * s);
+                    umma_done<PAIR>(lead, accf + 8 * b);
+                    __syncwarp();
                 }
             }
-            // after an abort the MMAs issued land before the CTA ends
-            if (!ok && i > 0 && !mbar_wait(accf + 8 * ((i - 1) % L::NBUF), ((i - 1) / L::NBUF) & 1u))
+            // after an abort the MMAs issued land before the CTAs end
+            if (!ok && i > 0 && !mbar_wait_short(accf + 8 * ((i - 1) % L::NBUF), ((i - 1) / L::NBUF) & 1u))
                 atomicOr(g.err, FDPP_ERRBIT_TIMEOUT);
+        } else if (warp >= 2) {
+            // ---- the scales, T_SCALES blocks of K at a time, well ahead of the sums: a load takes longer
+            // than a block's MMAs while the ring keeps the memory busy ----
+            const int r0 = threadIdx.x - 64;             // rows r0 and r0 + 64
+            uint32_t c = 0;
+            bool ok = true;
+            for (int t = first; t < tiles && ok; t += step) {
+                int mt, nt;
+                tile_at(g, t, mt, nt);
+                const int m0 = (PAIR ? 2 * mt + rank : mt) * SG_ROWS;
+                const float* sx[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) sx[h] = g.sx + (long long)(m0 + r0 + 64 * h < g.M ? m0 + r0 + 64 * h : 0) * g.sx_stride;
+                for (int k0 = 0; k0 < g.kb; k0 += T_SCALES, ++c) {
+                    float v[2][T_SCALES], w = 0.f;
+#pragma unroll
+                    for (int j = 0; j < T_SCALES; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) v[h][j] = k0 + j < g.kb ? sx[h][k0 + j] : 0.f;
+                    // (weight rows past the last block have no scale of their own and are not stored)
+                    if (r0 < L::W_SCALES * T_SCALES && k0 + r0 % T_SCALES < g.kb)
+                        w = g.sw[(long long)min(nt * L::W_SCALES + r0 / T_SCALES, (g.N - 1) / SG_N) * g.kb + k0 + r0 % T_SCALES];
+                    float* to = scales + (c & 1) * L::SCALES;
+                    if (!gwait(sce + 8 * (c & 1), (c >> 1) ^ 1u, abort_, g.err)) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int j = 0; j < T_SCALES; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) to[j * SG_ROWS + r0 + 64 * h] = v[h][j];
+                    if (r0 < L::W_SCALES * T_SCALES) to[T_SCALES * SG_ROWS + r0] = w;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(scf + 8 * (c & 1));
+                }
+            }
         }
         __syncwarp();
     } else {
@@ -459,26 +632,28 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         T* y = static_cast<T*>(g.y);
         // 16-byte stores where y and its rows allow them
         const bool wide = ((reinterpret_cast<uintptr_t>(y) | (uintptr_t)(g.y_stride * (long long)sizeof(T))) & 15u) == 0;
-        uint32_t i = 0;
+        uint32_t i = 0, c = 0;           // blocks, and sets of scales
         bool ok = true;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+        for (int t = first; t < tiles; t += step) {
             int mt, nt;
             tile_at(g, t, mt, nt);
-            const int m0 = mt * SG_ROWS + 32 * q, n0 = nt * BN + half * COLS;
-            const bool row_in = m0 + lane < g.M;
-            const float* sx = g.sx + (long long)(row_in ? m0 + lane : 0) * g.sx_stride;
-            // (a half past the last weight row has no scale of its own and is not stored)
-            const float* sw = g.sw + (long long)min(n0 / SG_N, (g.N - 1) / SG_N) * g.kb;
+            const int m0 = (PAIR ? 2 * mt + rank : mt) * SG_ROWS + 32 * q, n0 = nt * BN + half * COLS;
             uint64_t acc[COLS / 2];
 #pragma unroll
             for (int j = 0; j < COLS / 2; ++j) acc[j] = 0ull;
-            float x_next = sx[0], w_next = sw[0];
             for (int k = 0; k < g.kb; ++k, ++i) {
                 const uint32_t b = i % L::NBUF;
-                const float s = x_next * w_next;
-                if (k + 1 < g.kb) {
-                    x_next = sx[k + 1];
-                    w_next = sw[k + 1];
+                if (k % T_SCALES == 0 && !gwait(scf + 8 * (c & 1), c >> 1, abort_, g.err)) {
+                    ok = false;
+                    break;
+                }
+                const float* sc = scales + (c & 1) * L::SCALES;
+                const float s = sc[k % T_SCALES * SG_ROWS + 32 * q + lane] *
+                                sc[T_SCALES * SG_ROWS + (half * L::W_SCALES >> 1) * T_SCALES + k % T_SCALES];
+                if (k % T_SCALES == T_SCALES - 1 || k + 1 == g.kb) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sce + 8 * (c & 1));
+                    ++c;
                 }
                 if (!gwait(accf + 8 * b, i / L::NBUF, abort_, g.err)) {
                     ok = false;
@@ -486,21 +661,13 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                 }
                 tc_fence_after();
                 const uint64_t s2 = pack2(s, s);
-                uint32_t v[2][32];
-                tmem_ld32_async(trow + b * BN, v[0]);
 #pragma unroll
-                for (int c = 0; c < COLS / 32; ++c) {
-                    tmem_wait_ld();
-                    reg_fence32(v[c & 1]);
-                    if (c + 1 < COLS / 32) tmem_ld32_async(trow + b * BN + 32 * (c + 1), v[(c + 1) & 1]);
-                    if (c + 1 == COLS / 32) {            // the buffer is read out
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(acce + 8 * b);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2)
-                        acc[16 * c + j / 2] = fma2(pack2(v[c & 1][j], v[c & 1][j + 1]), s2, acc[16 * c + j / 2]);
+                for (int h = 0; h < COLS / 64; ++h) tmem_sum64(trow + b * BN + 64 * h, s2, acc + 32 * h);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {                         // the buffer is read out
+                    if (PAIR) mbar_arrive_cluster(acce0 + 8 * b);
+                    else mbar_arrive(acce + 8 * b);
                 }
             }
             if (!ok) break;
@@ -508,11 +675,11 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             // ^ (r & 7)), so that a store instruction writes whole lines
             constexpr int PC = 128 / (int)sizeof(T), PIECE = 16 / (int)sizeof(T);        // columns of 128 and of 16 bytes
 #pragma unroll
-            for (int c = 0; c < COLS; c += PC) {
+            for (int col = 0; col < COLS; col += PC) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     uint4 v;
-                    const int at = (c + k * PIECE) / 2;
+                    const int at = (col + k * PIECE) / 2;
                     if constexpr (sizeof(T) == 4) {
                         const float2 p0 = unpack2(acc[at]), p1 = unpack2(acc[at + 1]);
                         v = make_uint4(__float_as_uint(p0.x), __float_as_uint(p0.y), __float_as_uint(p1.x), __float_as_uint(p1.y));
@@ -523,20 +690,20 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                     *reinterpret_cast<uint4*>(turn + lane * 128 + ((k ^ (lane & 7)) << 4)) = v;
                 }
                 __syncwarp();
-                if (wide && n0 + c + PC <= g.N) {
+                if (wide && n0 + col + PC <= g.N) {
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) {
                         const int row = k + (lane >> 3), piece = lane & 7;
                         const uint4 v = *reinterpret_cast<const uint4*>(turn + row * 128 + ((piece ^ (row & 7)) << 4));
                         if (m0 + row < g.M)
-                            *reinterpret_cast<uint4*>(y + (long long)(m0 + row) * g.y_stride + n0 + c + piece * PIECE) = v;
+                            *reinterpret_cast<uint4*>(y + (long long)(m0 + row) * g.y_stride + n0 + col + piece * PIECE) = v;
                     }
                 } else {                 // element by element, neighbours on neighbouring lanes
                     for (int row = 0; row < 32 && m0 + row < g.M; ++row)
 #pragma unroll
                         for (int e = lane; e < PC; e += 32) {
                             const T v = *reinterpret_cast<const T*>(turn + row * 128 + (((e / PIECE) ^ (row & 7)) << 4) + (e % PIECE) * (int)sizeof(T));
-                            if (n0 + c + e < g.N) y[(long long)(m0 + row) * g.y_stride + n0 + c + e] = v;
+                            if (n0 + col + e < g.N) y[(long long)(m0 + row) * g.y_stride + n0 + col + e] = v;
                         }
                 }
                 __syncwarp();
@@ -545,9 +712,11 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         tc_fence_before();
     }
     __syncthreads();
+    if (PAIR) cluster_sync_all();        // neither CTA's shared or tensor memory goes while the other uses it
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        if (PAIR) tmem_dealloc_pair(tmem, 512);
+        else tmem_dealloc(tmem, 512);
     }
 }
 
@@ -611,7 +780,7 @@ RowsKernel rows_kernel(int Mp)
                                                                                                  : scaled_rows_kernel<T, 128>;
 }
 
-int rows_smem(int Mp, int nstage) { return nstage * (RW_BYTES + Mp * SB) + 2 * SG_ROWS * 4 + 16 * nstage + 64 + 1024; }
+int rows_smem(int Mp, int nstage) { return nstage * (RW_BYTES + Mp * SB) + 2 * R_SCALES * SG_ROWS * 4 + 16 * nstage + 64 + 1024; }
 
 // Ring depth for two CTAs per SM.
 int rows_stages(int Mp, int smem_per_sm, int smem_per_block)
@@ -692,34 +861,37 @@ fdpp_status launch_rows(const fdpp_scaled_gemm_params& p, ScaledArgs& g, const v
     return FDPP_OK;
 }
 
-template <typename T, int BN>
+template <typename T, int BN, bool PAIR>
 fdpp_status launch_tile(const fdpp_scaled_gemm_params& p, ScaledArgs& g, const void* x, const void* w, int sms, int smem_blk,
                         cudaStream_t s)
 {
-    constexpr int smem = TileSmem<BN>::TOTAL;
+    constexpr int smem = TileSmem<BN, PAIR>::TOTAL, rows = PAIR ? 2 * SG_ROWS : SG_ROWS;
     if (smem > smem_blk) return sfail(FDPP_ERR_UNSUPPORTED, "too little shared memory for the tile kernel");
-    const long long m_tiles = ((long long)p.M + SG_ROWS - 1) / SG_ROWS, n_tiles = ((long long)p.N + BN - 1) / BN;
+    const long long m_tiles = ((long long)p.M + rows - 1) / rows, n_tiles = ((long long)p.N + BN - 1) / BN;
     if (m_tiles * n_tiles >= (1ll << 31) - sms || T_GROUP * n_tiles >= (1ll << 31))
         return sfail(FDPP_ERR_INVALID_ARG, "problem too large for one call");
     g.m_tiles = (int)m_tiles;
     g.n_tiles = (int)n_tiles;
     CUtensorMap tw, tx;
     fdpp_status st;
-    if ((st = encode_rows(&tw, w, p.N, p.K, p.w_stride, BN)) != FDPP_OK) return st;
+    if ((st = encode_rows(&tw, w, p.N, p.K, p.w_stride, TileSmem<BN, PAIR>::W_ROWS)) != FDPP_OK) return st;
     if ((st = encode_rows(&tx, x, p.M, p.K, p.x_stride, SG_ROWS)) != FDPP_OK) return st;
-    auto kern = scaled_tile_kernel<T, BN>;
+    auto kern = scaled_tile_kernel<T, BN, PAIR>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return sfail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<long long>(sms, m_tiles * n_tiles));
+    cfg.gridDim = dim3((unsigned)(PAIR ? 2 * std::min<long long>(sms / 2, m_tiles * n_tiles) : std::min<long long>(sms, m_tiles * n_tiles)));
     cfg.blockDim = dim3(T_THREADS);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = PAIR ? 2 : 1;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = PAIR ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, kern, tx, tw, g);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return sfail(FDPP_ERR_CUDA, "scaled GEMM launch: %s", cudaGetErrorString(e));
@@ -764,13 +936,14 @@ fdpp_status fdpp_scaled_gemm(const void* x, const float* x_scales, const void* w
     g.kb = blocks_of(p->K);
     cudaStream_t s = (cudaStream_t)stream;
     if (p->M <= SG_ROWS) return launch_rows(*p, g, x, w, smem_sm, smem_blk, s);
-    // weight tiles of 256 where they alone are at least a tile per SM, else of 128
-    const long long tiles = ((p->M + (long long)SG_ROWS - 1) / SG_ROWS) * ((p->N + 255ll) / 256);
-    const bool big = tiles >= sms;
+    // weight tiles of 256 where they alone are at least a tile per pair of SMs, else of 128
+    const long long tiles = ((p->M + 255ll) / 256) * ((p->N + 255ll) / 256);
+    const bool big = tiles >= sms / 2;
     if (p->out_dtype == FDPP_F32)
-        return big ? launch_tile<float, 256>(*p, g, x, w, sms, smem_blk, s) : launch_tile<float, 128>(*p, g, x, w, sms, smem_blk, s);
-    return big ? launch_tile<__nv_bfloat16, 256>(*p, g, x, w, sms, smem_blk, s)
-               : launch_tile<__nv_bfloat16, 128>(*p, g, x, w, sms, smem_blk, s);
+        return big ? launch_tile<float, 256, true>(*p, g, x, w, sms, smem_blk, s)
+                   : launch_tile<float, 128, false>(*p, g, x, w, sms, smem_blk, s);
+    return big ? launch_tile<__nv_bfloat16, 256, true>(*p, g, x, w, sms, smem_blk, s)
+               : launch_tile<__nv_bfloat16, 128, false>(*p, g, x, w, sms, smem_blk, s);
 }
 
 }  // extern "C"
