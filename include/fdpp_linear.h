@@ -40,7 +40,8 @@ typedef struct fdpp_norm_params {
     int dtype;               /* fdpp_dtype of x, residual, weight and sum_out */
     int out_dtype;           /* dtype, or FDPP_E4M3 */
     long long x_stride, residual_stride, out_stride, sum_stride;
-                             /* elements from one row to the next: >= dim, and multiples of 16 bytes */
+                             /* elements from one row to the next: >= dim, and multiples of 16 bytes (an e4m3
+                                output's: of 8; fdpp_scaled_gemm takes multiples of 16) */
     long long scale_stride;  /* floats from one row's scales to the next, >= ceil(dim / 128) (E4M3) */
     float eps;               /* >= 0, finite */
     float weight_offset;     /* added to every weight (1 where weights are stored as w - 1) */
@@ -69,8 +70,8 @@ typedef struct fdpp_scaled_gemm_params {
     long long x_stride, w_stride;   /* bytes from one row to the next: >= K, multiples of 16 */
     long long y_stride;      /* elements from one row of y to the next, >= N */
     long long x_scale_stride;       /* floats from one row's scales to the next, >= ceil(K / 128) */
-    int split_k;             /* ranges of K per weight tile for M <= 128: 0 chooses, otherwise
-                                1 .. min(ceil(K / 128), 8) */
+    int split_k;             /* ranges of K that an output tile is made of, added up in order: 0 chooses, otherwise
+                                1 .. min(ceil(K / 128), 8); not followed where the tiles alone fill the GPU */
 } fdpp_scaled_gemm_params;
 
 /* Bytes of workspace (the sticky error word). 0 if the parameters are invalid. */

@@ -590,12 +590,10 @@ def _scale_blocks(n: int) -> int:
 def make_norm_params(*, num_tokens, dim, dtype, out_dtype=None, eps=1e-6, weight_offset=0.0, x_stride=None,
                      residual_stride=None, out_stride=None, sum_stride=None, scale_stride=None) -> fdpp_norm_params:
     """out_dtype: dtype where None, or FDPP_E4M3. Strides in elements from one row to the next (scale_stride
-    in scales); None: contiguous rows, an e4m3 output's rounded up to 16 channels."""
-    out_dtype = dtype if out_dtype is None else out_dtype
-    packed = (dim + 15) // 16 * 16 if out_dtype == FDPP_E4M3 else dim
-    return fdpp_norm_params(num_tokens, dim, dtype, out_dtype, dim if x_stride is None else x_stride,
-                            dim if residual_stride is None else residual_stride,
-                            packed if out_stride is None else out_stride, dim if sum_stride is None else sum_stride,
+    in scales); None: contiguous rows."""
+    return fdpp_norm_params(num_tokens, dim, dtype, dtype if out_dtype is None else out_dtype,
+                            dim if x_stride is None else x_stride, dim if residual_stride is None else residual_stride,
+                            dim if out_stride is None else out_stride, dim if sum_stride is None else sum_stride,
                             _scale_blocks(dim) if scale_stride is None else scale_stride, eps, weight_offset)
 
 

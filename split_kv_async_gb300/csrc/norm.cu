@@ -6,7 +6,12 @@
 // A row is read once and stays in registers: each thread holds V vectors of 8 channels, thread i of the
 // row's R takes vectors i, i + R, .. so that a warp reads whole lines, and the 16 lanes of a half warp hold
 // a block of 128 channels, whose largest |y| takes four exchanges. The sum of squares is the only thing
-// that the row's threads have to wait for.
+// that the row's threads have to wait for; the row after is on its way meanwhile.
+//
+// What bounds it: HBM. 16384 rows of 8192 bf16 channels with a residual, its sum written back and the output in e4m3:
+// 145 us, 6.47 TB/s, 0.97 of a measured copy (a CTA for each row, without the row ahead: 209). One row of 4096: the
+// launch (2.2 us in a graph).
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -22,7 +27,8 @@ namespace {
 
 constexpr float E4M3_MAX = 448.f;
 constexpr float LEAST_SCALE = 1.17549435e-38f;       // 2^-126: its reciprocal is finite
-constexpr int NORM_MAX_THREADS = 1024;
+constexpr int NORM_THREADS = 512, NORM_MAX_THREADS = 1024;     // of a CTA
+constexpr int NORM_RESIDENT = 2048;                  // threads of an SM
 constexpr int NORM_WARP_ROWS = 8;                    // rows of a CTA where each is one warp's
 
 struct NormArgs {
@@ -37,24 +43,45 @@ struct NormArgs {
     float eps, offset;
 };
 
-// Eight consecutive elements as fp32, and back.
-__device__ __forceinline__ void load8(const float* p, float (&v)[8])
-{
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
+// Eight consecutive elements as they lie in memory, as fp32, and back.
+template <typename T>
+struct Raw8;
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8])
-{
-    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+template <>
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p)
+    {
+        a = __ldcs(reinterpret_cast<const float4*>(p));
+        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
     }
-}
+    __device__ __forceinline__ void keep(const float* p)
+    {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+};
+
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldcs(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void keep(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
 
 __device__ __forceinline__ void store8(float* p, const float (&v)[8])
 {
@@ -82,99 +109,103 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return d;
 }
 
-// WARP: a row is one warp's, NORM_WARP_ROWS rows to a CTA; otherwise a row is the CTA's.
-template <typename T, bool E4M3, int V, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * NORM_WARP_ROWS : NORM_MAX_THREADS) rms_norm_kernel(NormArgs a)
+// WARP: a row is one warp's, NORM_WARP_ROWS rows to a CTA; otherwise a row is the CTA's, and the next one is loaded
+// while this one is added up and written.
+template <typename T, bool E4M3, int V, bool WARP, int MOST = WARP ? 32 * NORM_WARP_ROWS : NORM_THREADS>
+__global__ void __launch_bounds__(MOST)
+    rms_norm_kernel(const __grid_constant__ NormArgs a)
 {
-    __shared__ float part[32];
+    __shared__ float part[2][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int R = WARP ? 32 : blockDim.x, me = WARP ? lane : threadIdx.x;
-    const long long t = WARP ? (long long)blockIdx.x * NORM_WARP_ROWS + warp : blockIdx.x;
+    const long long step = WARP ? (long long)gridDim.x * NORM_WARP_ROWS : gridDim.x;
+    long long t = WARP ? (long long)blockIdx.x * NORM_WARP_ROWS + warp : blockIdx.x;
     grid_dependency_wait();
-    if (WARP && t >= a.T) return;
+    grid_launch_dependents();
     const int vectors = a.dim / 8;
-    const T* x = static_cast<const T*>(a.x) + t * a.x_stride;
-    float r[V][8];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) r[i][k] = 0.f;
-        if (me + i * R < vectors) load8(x + (me + i * R) * 8, r[i]);
-    }
-    if (a.residual) {
-        const T* res = static_cast<const T*>(a.residual) + t * a.residual_stride;
-        float s[V][8];
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (me + i * R < vectors) load8(res + (me + i * R) * 8, s[i]);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (me + i * R < vectors)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) r[i][k] += s[i][k];
-    }
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum = fmaf(r[i][k], r[i][k], sum);
-    sum = warp_sum(sum);
-    if (!WARP) {
-        if (lane == 0) part[warp] = sum;
-        __syncthreads();
-        sum = lane < (R >> 5) ? part[lane] : 0.f;
-        sum = warp_sum(sum);
-    }
-    const float inv = 1.f / sqrtf(sum / (float)a.dim + a.eps);
-    if (a.sum_out) {
-        T* so = static_cast<T*>(a.sum_out) + t * a.sum_stride;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (me + i * R < vectors) store8(so + (me + i * R) * 8, r[i]);
-    }
+    // (four vectors a thread: as many registers as there are, without a row ahead)
+    constexpr bool AHEAD = V < 4 || WARP;
     const T* w = static_cast<const T*>(a.weight);
+    Raw8<T> x[V], res[V], g[V];
+    auto load = [&](long long row) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int at = me + i * R;
-        const bool in = at < vectors;
-        float y[8];
+        for (int i = 0; i < V; ++i)
+            if (me + i * R < vectors) {
+                x[i].load(static_cast<const T*>(a.x) + row * a.x_stride + (me + i * R) * 8);
+                if (a.residual) res[i].load(static_cast<const T*>(a.residual) + row * a.residual_stride + (me + i * R) * 8);
+            }
+    };
+    if (AHEAD && t < a.T) load(t);
+    if (AHEAD && w)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = r[i][k] * inv;
-        if (w && in) {
-            float g[8];
-            if constexpr (sizeof(T) == 4) {
-                const float4 p = __ldg(reinterpret_cast<const float4*>(w + at * 8));
-                const float4 q = __ldg(reinterpret_cast<const float4*>(w + at * 8) + 1);
-                g[0] = p.x; g[1] = p.y; g[2] = p.z; g[3] = p.w;
-                g[4] = q.x; g[5] = q.y; g[6] = q.z; g[7] = q.w;
-            } else {
-                const uint4 p = __ldg(reinterpret_cast<const uint4*>(w + at * 8));
-                const uint32_t u[4] = {p.x, p.y, p.z, p.w};
+        for (int i = 0; i < V; ++i)
+            if (me + i * R < vectors) g[i].keep(w + (me + i * R) * 8);
+    for (int turn = 0; t < a.T; t += step, turn ^= 1) {
+        if (!AHEAD) load(t);
+        float r[V][8];
+        float sum = 0.f;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    g[2 * k] = __uint_as_float(u[k] << 16);
-                    g[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+        for (int i = 0; i < V; ++i) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) r[i][k] = 0.f;
+            if (me + i * R < vectors) {
+                x[i].get(r[i]);
+                if (a.residual) {
+                    float s[8];
+                    res[i].get(s);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) r[i][k] += s[k];
                 }
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] *= g[k] + a.offset;
+            for (int k = 0; k < 8; ++k) sum = fmaf(r[i][k], r[i][k], sum);
         }
-        if constexpr (!E4M3) {
-            if (in) store8(static_cast<T*>(a.out) + t * a.out_stride + at * 8, y);
-        } else {
-            // a block's 16 lanes (those past the row hold zeros)
-            float top = 0.f;
+        if (AHEAD && t + step < a.T) load(t + step);
+        sum = warp_sum(sum);
+        if (!WARP) {
+            if (lane == 0) part[turn][warp] = sum;
+            __syncthreads();                             // (the other half is read before the next barrier)
+            sum = lane < (R >> 5) ? part[turn][lane] : 0.f;
+            sum = warp_sum(sum);
+        }
+        const float inv = 1.f / sqrtf(sum / (float)a.dim + a.eps);
+        if (a.sum_out) {
+            T* so = static_cast<T*>(a.sum_out) + t * a.sum_stride;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) top = max_nan(top, fabsf(y[k]));
+            for (int i = 0; i < V; ++i)
+                if (me + i * R < vectors) store8(so + (me + i * R) * 8, r[i]);
+        }
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float scale = max_nan(top / E4M3_MAX, LEAST_SCALE), over = 1.f / scale;
-            if (in) {
-                uint2 v;
-                v.x = pack_e4m3x4(y[0] * over, y[1] * over, y[2] * over, y[3] * over);
-                v.y = pack_e4m3x4(y[4] * over, y[5] * over, y[6] * over, y[7] * over);
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + t * a.out_stride + at * 8) = v;
-                if ((at & 15) == 0) a.scales[t * a.scale_stride + (at >> 4)] = scale;
+        for (int i = 0; i < V; ++i) {
+            const int at = me + i * R;
+            const bool in = at < vectors;
+            float y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = r[i][k] * inv;
+            if (w && in) {
+                float f[8];
+                if (!AHEAD) g[i].keep(w + at * 8);
+                g[i].get(f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] *= f[k] + a.offset;
+            }
+            if constexpr (!E4M3) {
+                if (in) store8(static_cast<T*>(a.out) + t * a.out_stride + at * 8, y);
+            } else {
+                // a block's 16 lanes (those past the row hold zeros)
+                float top = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) top = max_nan(top, fabsf(y[k]));
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float scale = max_nan(top / E4M3_MAX, LEAST_SCALE), over = 1.f / scale;
+                if (in) {
+                    uint2 v;
+                    v.x = pack_e4m3x4(y[0] * over, y[1] * over, y[2] * over, y[3] * over);
+                    v.y = pack_e4m3x4(y[4] * over, y[5] * over, y[6] * over, y[7] * over);
+                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + t * a.out_stride + at * 8) = v;
+                    if ((at & 15) == 0) a.scales[t * a.scale_stride + (at >> 4)] = scale;
+                }
             }
         }
     }
@@ -192,7 +223,7 @@ fdpp_status nfail(fdpp_status s, const char* fmt, ...)
 }
 
 template <typename T, bool E4M3>
-cudaError_t launch_norm(const NormArgs& a, cudaStream_t s)
+cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t s)
 {
     const int vectors = a.dim / 8;
     void (*kern)(NormArgs);
@@ -201,15 +232,19 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s)
         kern = vectors <= 32   ? rms_norm_kernel<T, E4M3, 1, true>
                : vectors <= 64 ? rms_norm_kernel<T, E4M3, 2, true>
                                : rms_norm_kernel<T, E4M3, 4, true>;
-        grid = (unsigned)((a.T + NORM_WARP_ROWS - 1) / NORM_WARP_ROWS);
+        grid = (unsigned)std::min((a.T + NORM_WARP_ROWS - 1) / NORM_WARP_ROWS, 8 * sms);
         threads = 32 * NORM_WARP_ROWS;
     } else {
-        const int v = vectors <= 512 ? 1 : vectors <= 2048 ? 2 : 4;
-        kern = v == 1 ? rms_norm_kernel<T, E4M3, 1, false>
-               : v == 2 ? rms_norm_kernel<T, E4M3, 2, false>
-                        : rms_norm_kernel<T, E4M3, 4, false>;
-        grid = (unsigned)a.T;
+        // Channels a thread holds, by what was fastest on 2^27 bf16 elements into e4m3: rows of 4096 in 512 threads of 8
+        // channels 79 us, in 256 of 16 75; of 8192 in 512 of 16 145, in 1024 of 8 159, in 256 of 32 235; of 16384 in 1024
+        // of 16 144, of 32 253.
+        const int v = vectors <= 256 ? 1 : vectors <= 2 * NORM_MAX_THREADS ? 2 : 4;
+        kern = v == 1                         ? rms_norm_kernel<T, E4M3, 1, false>
+               : vectors <= 2 * NORM_THREADS  ? rms_norm_kernel<T, E4M3, 2, false>
+               : v == 2                       ? rms_norm_kernel<T, E4M3, 2, false, NORM_MAX_THREADS>
+                                              : rms_norm_kernel<T, E4M3, 4, false, NORM_MAX_THREADS>;
         threads = (unsigned)((vectors + v - 1) / v + 31) / 32 * 32;
+        grid = (unsigned)std::min(a.T, std::max(1, NORM_RESIDENT / (int)threads) * sms);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -244,11 +279,11 @@ extern "C" fdpp_status fdpp_rms_norm(const void* x, const void* residual, const 
         return nfail(FDPP_ERR_INVALID_ARG, "out_dtype must be dtype or FDPP_E4M3 (got %d)", p->out_dtype);
     if (!(p->eps >= 0.f) || !std::isfinite(p->eps)) return nfail(FDPP_ERR_INVALID_ARG, "eps must be finite and >= 0");
     if (!std::isfinite(p->weight_offset)) return nfail(FDPP_ERR_INVALID_ARG, "weight_offset must be finite");
-    const long long vec = p->dtype == FDPP_F32 ? 4 : 8, out_vec = e4m3 ? 16 : vec, most = 1ll << 40;
+    const long long vec = p->dtype == FDPP_F32 ? 4 : 8, out_vec = e4m3 ? 8 : vec, most = 1ll << 40;
     auto stride_ok = [&](long long stride, long long v) { return stride >= p->dim && stride % v == 0 && stride <= most; };
     if (!stride_ok(p->x_stride, vec) || !stride_ok(p->out_stride, out_vec) ||
         (residual && !stride_ok(p->residual_stride, vec)) || (sum_out && !stride_ok(p->sum_stride, vec)))
-        return nfail(FDPP_ERR_INVALID_ARG, "strides must cover a row and be multiples of 16 bytes");
+        return nfail(FDPP_ERR_INVALID_ARG, "strides must cover a row and be multiples of 16 bytes (an e4m3 output's: of 8)");
     if (!x || !out) return nfail(FDPP_ERR_INVALID_ARG, "x and out must be non-NULL");
     if (((uintptr_t)x | (uintptr_t)residual | (uintptr_t)weight | (uintptr_t)out | (uintptr_t)sum_out) % 16 != 0)
         return nfail(FDPP_ERR_INVALID_ARG, "x, residual, weight, out and sum_out must be 16-byte aligned");
@@ -286,8 +321,8 @@ extern "C" fdpp_status fdpp_rms_norm(const void* x, const void* residual, const 
     a.offset = p->weight_offset;
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
-    if (p->dtype == FDPP_F32) e = e4m3 ? launch_norm<float, true>(a, s) : launch_norm<float, false>(a, s);
-    else e = e4m3 ? launch_norm<__nv_bfloat16, true>(a, s) : launch_norm<__nv_bfloat16, false>(a, s);
+    if (p->dtype == FDPP_F32) e = e4m3 ? launch_norm<float, true>(a, sms, s) : launch_norm<float, false>(a, sms, s);
+    else e = e4m3 ? launch_norm<__nv_bfloat16, true>(a, sms, s) : launch_norm<__nv_bfloat16, false>(a, sms, s);
     if (e != cudaSuccess) return nfail(FDPP_ERR_CUDA, "RMS norm launch: %s", cudaGetErrorString(e));
     return FDPP_OK;
 }

@@ -9,11 +9,19 @@
 // The scales are any fp32 numbers, so they cannot be left to the tensor cores (whose block scales are
 // powers of two).
 //
-//   rows kernel (M <= 128): y^T = w x^T. 128 weight rows on the tensor-memory lanes, the rows of x on N,
-//     padded to the next 16 only; the work is the stream of w. When the weight tiles are too few for the GPU, K is
-//     cut into ranges whose CTAs form a cluster and add their sums through distributed shared memory, in
-//     range order.
-//   tile kernel (M > 128): 128 rows of x on the lanes, BN weight rows on N, one persistent CTA per SM.
+//   rows kernel (few rows): y^T = w x^T. 128 weight rows on the tensor-memory lanes, the rows of x on N, padded to the
+//     next 16 only; two CTAs per SM.
+//   tile kernel: 128 rows of x on the lanes, BN weight rows on N, one persistent CTA per SM, or two as a pair.
+// Where the tiles are too few for the GPU, K is cut into ranges whose CTAs form a cluster and add their sums through
+// distributed shared memory, in range order.
+//
+// What bounds it. Few rows: HBM (28672 x 4096 weights: 8 rows 21 us, 0.84 of a measured copy, 64 rows 25), and for small
+// weights the start and the end of a CTA (4096 x 4096, 8 rows: 6.1 us in a graph, of which the bytes take 2.5). Many rows: the
+// hand-over between the tensor cores and the sums. 8192 x 28672 x 4096 takes 680 us, 2.8 PFLOP/s; the MMAs alone, on
+// data that lies there, 4.6, with the loads 3.5 to 3.7 (128 bytes of shared memory a cycle, written and read). Two buffers of
+// 256 columns are all the tensor memory, so a block's sums have the 512 cycles of the next block's MMAs from the commit to the
+// release, and take more: two loads of 64 columns and 128 sums per thread, and a hundred cycles for each barrier asked, with
+// shared memory as busy as it is. Tried: 192 columns and twelve warps of sums 782 us, sixteen warps of 64 columns 915.
 //
 // Every wait is bounded: on a timeout the CTA records FDPP_ERRBIT_TIMEOUT, lets its copies and MMAs land,
 // frees its tensor memory and exits.
@@ -35,7 +43,8 @@ namespace {
 
 constexpr int SB = FDPP_SCALE_BLOCK;     // channels of a block: one 128-byte swizzle row
 constexpr int SG_N = 128;                // weight rows that share a scale; the rows kernel's weight tile
-constexpr int SG_ROWS = 128;             // most rows of x of the rows kernel; the tile kernel's row tile
+constexpr int SG_ROWS = 128;             // the tile kernel's rows of x in a CTA
+constexpr int SG_GROUP = 64;             // most rows of x of the rows kernel
 constexpr int SG_MAX_SPLIT = 8;          // K ranges per weight tile (a portable cluster)
 constexpr int SG_MAX_STAGES = 8;
 
@@ -46,7 +55,7 @@ struct ScaledArgs {
     unsigned* err;                       // sticky FDPP_ERRBIT_*
     long long y_stride, sx_stride;
     int M, N, kb;                        // kb: blocks of K
-    int Mp, split_k, nstage;             // rows kernel: x rows padded; K ranges
+    int Mp, split_k, nstage;             // rows kernel: rows of x, padded; K ranges of a tile
     int m_tiles, n_tiles;                // tile kernel
 };
 
@@ -142,29 +151,15 @@ __device__ __forceinline__ uint64_t pack2(float x, float y)
     asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
     return d;
 }
-__device__ __forceinline__ uint64_t pack2(uint32_t x, uint32_t y)
-{
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(x), "r"(y));
-    return d;
-}
 __device__ __forceinline__ float2 unpack2(uint64_t d)
 {
     float2 v;
     asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(d));
     return v;
 }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-
 // acc += s v for the 64 consecutive columns v of this thread's tensor-memory lane, two columns to an operation (s2: s
 // twice). One statement from the load to the sums: with the columns handed to C++ in between, a third of the
-// instructions were moves from register to register (per block of 128 x 256: 231 of a warp's, against 130), and two loads
-// of 32 columns wait for tensor memory twice as often.
+// instructions were moves from register to register, and two loads of 32 columns wait for tensor memory twice as often.
 #define SUM2(acc, lo, hi) "mov.b64 d, {t" #lo ", t" #hi "};\n\tfma.rn.f32x2 %" #acc ", d, %32, %" #acc ";\n\t"
 #define SUM8(a0, a1, a2, a3, c0, c1, c2, c3, c4, c5, c6, c7) SUM2(a0, c0, c1) SUM2(a1, c2, c3) SUM2(a2, c4, c5) SUM2(a3, c6, c7)
 __device__ __forceinline__ void tmem_sum64(uint32_t taddr, uint64_t s2, uint64_t* a)
@@ -196,6 +191,18 @@ __device__ __forceinline__ void tmem_sum64(uint32_t taddr, uint64_t s2, uint64_t
 #undef SUM8
 #undef SUM2
 
+// 16 consecutive fp32 columns of this thread's TMEM lane, the wait in the same statement (see above).
+__device__ __forceinline__ void tmem_ld16w(uint32_t taddr, float (&v)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
+
 // Every lane waits; one that runs out aborts the CTA (warp-uniform result).
 __device__ __forceinline__ bool gwait(uint32_t bar, uint32_t parity, volatile int* abort_, unsigned* err)
 {
@@ -211,6 +218,28 @@ __device__ __forceinline__ bool gwait(uint32_t bar, uint32_t parity, volatile in
 
 __device__ __forceinline__ void store_y(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store_y(float* p, float v) { *p = v; }
+
+// The sums of g.split_k ranges, added in order, into y[m][n .. n + 3].
+template <typename T>
+__device__ __forceinline__ void store_sum4(const ScaledArgs& g, const float4 (&t)[SG_MAX_SPLIT], int m, int n, T* y)
+{
+    float4 s = t[0];
+#pragma unroll
+    for (int r = 1; r < SG_MAX_SPLIT; ++r)
+        if (r < g.split_k) {
+            s.x += t[r].x; s.y += t[r].y; s.z += t[r].z; s.w += t[r].w;
+        }
+    T* yp = y + (long long)m * g.y_stride + n;
+    const float v[4] = {s.x, s.y, s.z, s.w};
+    if (n + 3 < g.N && (reinterpret_cast<uintptr_t>(yp) & (4 * sizeof(T) - 1)) == 0) {
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(yp) = s;
+        else *reinterpret_cast<uint2*>(yp) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (n + u < g.N) store_y(yp + u, v[u]);
+    }
+}
 
 // ---- rows kernel --------------------------------------------------------------------------
 
@@ -231,8 +260,8 @@ __global__ void __launch_bounds__(R_THREADS, 2)
     const uint32_t sbase = smem_u32(sm);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int stage_bytes = RW_BYTES + g.Mp * SB;
-    float* scale = reinterpret_cast<float*>(sm + g.nstage * stage_bytes);        // [2 R_SCALES][SG_ROWS]
-    const int bar_off = g.nstage * stage_bytes + 2 * R_SCALES * SG_ROWS * 4;
+    float* scale = reinterpret_cast<float*>(sm + g.nstage * stage_bytes);        // [2 R_SCALES][SG_GROUP]
+    const int bar_off = g.nstage * stage_bytes + 2 * R_SCALES * SG_GROUP * 4;
     const uint32_t bars = sbase + bar_off;
     const uint32_t full = bars, empty = bars + 8 * g.nstage, accf = bars + 16 * g.nstage, acce = accf + 16;
     volatile uint32_t* tslot = reinterpret_cast<volatile uint32_t*>(sm + bar_off + 16 * g.nstage + 32);
@@ -328,9 +357,9 @@ __global__ void __launch_bounds__(R_THREADS, 2)
         const uint32_t trow = tmem + ((uint32_t)(32 * q) << 16);
         const float* sx = g.sx + (long long)t * g.sx_stride;
         const float* sw = g.sw + (long long)tile * g.kb;
-        uint64_t acc[NR / 2];
+        float acc[NR];
 #pragma unroll
-        for (int j = 0; j < NR / 2; ++j) acc[j] = 0ull;
+        for (int j = 0; j < NR; ++j) acc[j] = 0.f;
         // the scales of eight blocks at a time, loaded eight blocks ahead: a load takes longer than a block's
         // MMAs while the ring keeps the memory busy
         float next[R_SCALES];
@@ -340,9 +369,10 @@ __global__ void __launch_bounds__(R_THREADS, 2)
         for (int i = 0; i < nkb; ++i) {
             const int b = i & 1;
             if (i % R_SCALES == 0) {
-                float* to = scale + (i / R_SCALES & 1) * R_SCALES * SG_ROWS + t;
+                float* to = scale + (i / R_SCALES & 1) * R_SCALES * SG_GROUP + t;
+                if (t < SG_GROUP)
 #pragma unroll
-                for (int j = 0; j < R_SCALES; ++j) to[j * SG_ROWS] = next[j];
+                    for (int j = 0; j < R_SCALES; ++j) to[j * SG_GROUP] = next[j];
                 named_bar_sync(1, 128);  // (this half was last read before the barrier eight blocks ago)
 #pragma unroll
                 for (int j = 0; j < R_SCALES; ++j) {
@@ -350,22 +380,22 @@ __global__ void __launch_bounds__(R_THREADS, 2)
                     next[j] = t < g.M && k < nkb ? sx[kb0 + k] * sw[kb0 + k] : 0.f;
                 }
             }
-            const float* sc = scale + (i % (2 * R_SCALES)) * SG_ROWS;
+            const float* sc = scale + (i % (2 * R_SCALES)) * SG_GROUP;
             ok = gwait(accf + 8 * b, (uint32_t)(i >> 1), abort_, g.err) && ok;
             if (ok) {
                 tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < NR; c += 16) {
                     if (c >= g.Mp) break;
-                    uint32_t v[16];
-                    tmem_ld16_async(trow + b * g.Mp + c, v);
-                    tmem_wait_ld();
-                    reg_fence16(v);
+                    float v[16];
+                    tmem_ld16w(trow + b * g.Mp + c, v);
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
                         const float4 s = *reinterpret_cast<const float4*>(sc + c + j);
-                        acc[(c + j) / 2] = fma2(pack2(v[j], v[j + 1]), pack2(s.x, s.y), acc[(c + j) / 2]);
-                        acc[(c + j) / 2 + 1] = fma2(pack2(v[j + 2], v[j + 3]), pack2(s.z, s.w), acc[(c + j) / 2 + 1]);
+                        acc[c + j] = fmaf(v[j], s.x, acc[c + j]);
+                        acc[c + j + 1] = fmaf(v[j + 1], s.y, acc[c + j + 1]);
+                        acc[c + j + 2] = fmaf(v[j + 2], s.z, acc[c + j + 2]);
+                        acc[c + j + 3] = fmaf(v[j + 3], s.w, acc[c + j + 3]);
                     }
                 }
                 tc_fence_before();
@@ -381,8 +411,7 @@ __global__ void __launch_bounds__(R_THREADS, 2)
         if (ok) {
 #pragma unroll
             for (int j = 0; j < NR; ++j) {
-                const float2 p = unpack2(acc[j / 2]);
-                const float v = j & 1 ? p.y : p.x;
+                const float v = acc[j];
                 if (j < g.M) {
                     if (g.split_k > 1) red[j * SG_N + 32 * q + lane] = v;
                     else if (n < g.N) store_y(y + (long long)j * g.y_stride + n, v);
@@ -407,22 +436,7 @@ __global__ void __launch_bounds__(R_THREADS, 2)
 #pragma unroll
                 for (int r = 0; r < SG_MAX_SPLIT; ++r)
                     if (r < g.split_k) t[r] = ld_dsmem_f4(dsmem_addr(off, (uint32_t)r));
-                float4 s = t[0];
-#pragma unroll
-                for (int r = 1; r < SG_MAX_SPLIT; ++r)
-                    if (r < g.split_k) {
-                        s.x += t[r].x; s.y += t[r].y; s.z += t[r].z; s.w += t[r].w;
-                    }
-                T* yp = static_cast<T*>(g.y) + (long long)m * g.y_stride + n;
-                const float v[4] = {s.x, s.y, s.z, s.w};
-                if (n + 3 < g.N && (reinterpret_cast<uintptr_t>(yp) & (4 * sizeof(T) - 1)) == 0) {
-                    if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(yp) = s;
-                    else *reinterpret_cast<uint2*>(yp) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (n + u < g.N) store_y(yp + u, v[u]);
-                }
+                store_sum4(g, t, m, n, static_cast<T*>(g.y));
             }
         }
         // no member leaves (releasing its shared memory) while another still reads it
@@ -448,21 +462,27 @@ __global__ void __launch_bounds__(R_THREADS, 2)
 // cycles of the tensor cores, and 48 kB written and read again alone would be 768 at 128 bytes a cycle; with
 // half of w it is 32 kB, 512 cycles.
 
-constexpr int T_THREADS = 384;           // producer, MMA, two idle warps; 8 warps that scale and add
-constexpr int T_HELP_REGS = 80, T_SUM_REGS = 208;    // 128 x 80 + 256 x 208 = 63488 of the launch's 384 x 168
-constexpr int T_SCALES = 8;              // blocks of K whose scales are loaded together
+// Warps: one loads, one issues the MMAs, two load scales; eight scale and add, each 32 rows and half of the columns.
+constexpr int T_SCALES = 4;              // blocks of K whose scales are loaded together
 constexpr int T_GROUP = 16;              // row tiles that a run of weight tiles is shared by (see tile_at)
 
 template <int BN, bool PAIR>
 struct TileSmem {
+    static constexpr int COLS = BN / 2;                  // columns of a warp's sums
+    static constexpr int SUM_WARPS = 8;
+    static constexpr int THREADS = 128 + 32 * SUM_WARPS;
+    // 128 x 56 + 256 x 224 = 64512, the launch's 384 x 168 registers; 128 x 80 + 256 x 200 = 61440 of them. (A spill in either part
+    // shows: shared memory and the L1 cache are busy, and what should take 40 cycles takes hundreds. With 28 bytes of
+    // them the largest prompt took 835 us instead of 696.)
+    static constexpr int HELP_REGS = BN == 256 ? 56 : 80, SUM_REGS = BN == 256 ? 224 : 200;
     static constexpr int W_ROWS = PAIR ? BN / 2 : BN;    // weight rows that a CTA holds
     static constexpr int STAGE = (SG_ROWS + W_ROWS) * SB;
-    static constexpr int TURN = 32 * 128;                // a warp's rows, 128 bytes of each
-    static constexpr int STAGES = (163840 / STAGE) < SG_MAX_STAGES ? 163840 / STAGE : SG_MAX_STAGES;
+    static constexpr int TURN = 32 * 64;                 // a warp's rows, 64 bytes of each
     static constexpr int NBUF = 512 / BN;                // tensor-memory buffers of BN columns
-    static constexpr int W_SCALES = BN / SG_N;           // a weight tile's scales
-    static constexpr int SCALES = T_SCALES * (SG_ROWS + W_SCALES);   // of T_SCALES blocks: [block][row], then w's [half][block]
-    static constexpr int SCALES_OFF = STAGES * STAGE + 8 * TURN;
+    static constexpr int W_SCALES = (BN + SG_N - 1) / SG_N;          // blocks of 128 weight rows that a tile lies in
+    static constexpr int SCALES = T_SCALES * W_SCALES * SG_ROWS;     // of T_SCALES blocks: sx sw by [block][128 of w][row]
+    static constexpr int STAGES = 196608 / STAGE < SG_MAX_STAGES ? 196608 / STAGE : SG_MAX_STAGES;
+    static constexpr int SCALES_OFF = STAGES * STAGE + SUM_WARPS * TURN;
     static constexpr int BARS = SCALES_OFF + 2 * SCALES * 4;
     static constexpr int TOTAL = BARS + (2 * STAGES + 2 * NBUF + 4) * 8 + 32 + 1024;
 };
@@ -477,8 +497,10 @@ __device__ __forceinline__ void tile_at(const ScaledArgs& g, int i, int& mt, int
     mt = first + r - nt * rows;
 }
 
-template <typename T, int BN, bool PAIR>
-__global__ void __launch_bounds__(T_THREADS, 1)
+// SPLIT: the g.split_k CTAs of a cluster share a tile's blocks of K and add their sums through distributed shared
+// memory, in the order of their ranges.
+template <typename T, int BN, bool PAIR, bool SPLIT>
+__global__ void __launch_bounds__(TileSmem<BN, PAIR>::THREADS, 1)
     scaled_tile_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const ScaledArgs g)
 {
     using L = TileSmem<BN, PAIR>;
@@ -502,11 +524,11 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         }
         for (int b = 0; b < L::NBUF; ++b) {
             mbar_init(accf + 8 * b, 1);
-            mbar_init(acce + 8 * b, PAIR ? 16 : 8);
+            mbar_init(acce + 8 * b, (PAIR ? 2 : 1) * L::SUM_WARPS);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(scf + 8 * b, 2);
-            mbar_init(sce + 8 * b, 8);
+            mbar_init(sce + 8 * b, L::SUM_WARPS);
         }
         *abort_ = 0;
         fence_mbar_init();
@@ -524,11 +546,17 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     const uint32_t tmem = *tslot;
     grid_dependency_wait();
     grid_launch_dependents();
+    static_assert(!(PAIR && SPLIT), "a cluster is a pair or shares out K");
     const int tiles = g.m_tiles * g.n_tiles;
-    const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
+    // (with shared K a cluster has one tile: its sums take the place of the ring's stages)
+    const int first = PAIR ? blockIdx.x >> 1 : SPLIT ? blockIdx.x / g.split_k : blockIdx.x;
+    const int step = PAIR ? gridDim.x >> 1 : SPLIT ? tiles : gridDim.x;
+    const int ks = SPLIT ? (int)cluster_rank() : 0;
+    const int kb0 = SPLIT ? (int)((long long)ks * g.kb / g.split_k) : 0;
+    const int nkb = (SPLIT ? (int)((long long)(ks + 1) * g.kb / g.split_k) : g.kb) - kb0;
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(T_HELP_REGS));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::HELP_REGS));
         if (warp == 0 && lane == 0) {
             uint32_t i = 0;              // blocks issued
             bool ok = true;
@@ -536,7 +564,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                 int mt, nt;
                 tile_at(g, t, mt, nt);
                 const int m0 = (PAIR ? 2 * mt + rank : mt) * SG_ROWS, n0 = nt * BN + rank * L::W_ROWS;
-                for (int k = 0; k < g.kb; ++k, ++i) {
+                for (int k = kb0; k < kb0 + nkb; ++k, ++i) {
                     const uint32_t s = i % L::STAGES, par = (i / L::STAGES) & 1u;
                     if (*abort_ || !mbar_wait_short(empty + 8 * s, par ^ 1u)) {
                         atomicOr(g.err, FDPP_ERRBIT_TIMEOUT);
@@ -564,22 +592,23 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             }
         } else if (warp == 1 && rank == 0) {
             constexpr uint32_t IDESC = umma_idesc_e4m3(PAIR ? 2 * SG_ROWS : SG_ROWS, BN);
-            uint32_t i = 0;
+            uint32_t st = 0, sp = 0, b = 0, bp = 0, i = 0;       // stage and buffer, with their phases; blocks issued
             bool ok = true;
             for (int t = first; t < tiles && ok; t += step) {
-                for (int k = 0; k < g.kb; ++k, ++i) {
-                    const uint32_t s = i % L::STAGES, b = i % L::NBUF;
-                    if (!gwait(acce + 8 * b, (i / L::NBUF) ^ 1u, abort_, g.err) || !gwait(full + 8 * s, i / L::STAGES, abort_, g.err)) {
+                for (int k = 0; k < nkb; ++k, ++i) {
+                    if (!gwait(full + 8 * st, sp, abort_, g.err) || !gwait(acce + 8 * b, bp ^ 1u, abort_, g.err)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const bool lead = elect_one();
-                    const uint32_t a0 = sbase + s * L::STAGE;
+                    const uint32_t a0 = sbase + st * L::STAGE;
                     umma_block<PAIR>(lead, tmem + b * BN, a0, a0 + SG_ROWS * SB, IDESC);
-                    umma_done<PAIR>(lead, empty + 8 * s);
                     umma_done<PAIR>(lead, accf + 8 * b);
+                    umma_done<PAIR>(lead, empty + 8 * st);
                     __syncwarp();
+                    if (++st == (uint32_t)L::STAGES) { st = 0; sp ^= 1u; }
+                    if (++b == (uint32_t)L::NBUF) { b = 0; bp ^= 1u; }
                 }
             }
             // after an abort the MMAs issued land before the CTAs end
@@ -598,15 +627,18 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                 const float* sx[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) sx[h] = g.sx + (long long)(m0 + r0 + 64 * h < g.M ? m0 + r0 + 64 * h : 0) * g.sx_stride;
-                for (int k0 = 0; k0 < g.kb; k0 += T_SCALES, ++c) {
-                    float v[2][T_SCALES], w = 0.f;
+                for (int k0 = 0; k0 < nkb; k0 += T_SCALES, ++c) {
+                    float v[2][T_SCALES], w[L::W_SCALES][T_SCALES];
 #pragma unroll
-                    for (int j = 0; j < T_SCALES; ++j)
+                    for (int j = 0; j < T_SCALES; ++j) {
+                        const int k = kb0 + min(k0 + j, nkb - 1);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) v[h][j] = k0 + j < g.kb ? sx[h][k0 + j] : 0.f;
-                    // (weight rows past the last block have no scale of their own and are not stored)
-                    if (r0 < L::W_SCALES * T_SCALES && k0 + r0 % T_SCALES < g.kb)
-                        w = g.sw[(long long)min(nt * L::W_SCALES + r0 / T_SCALES, (g.N - 1) / SG_N) * g.kb + k0 + r0 % T_SCALES];
+                        for (int h = 0; h < 2; ++h) v[h][j] = sx[h][k];
+                        // (weight rows past the last block have no scale of their own and are not stored)
+#pragma unroll
+                        for (int n = 0; n < L::W_SCALES; ++n)
+                            w[n][j] = g.sw[(long long)min(nt * BN / SG_N + n, (g.N - 1) / SG_N) * g.kb + k];
+                    }
                     float* to = scales + (c & 1) * L::SCALES;
                     if (!gwait(sce + 8 * (c & 1), (c >> 1) ^ 1u, abort_, g.err)) {
                         ok = false;
@@ -615,8 +647,9 @@ __global__ void __launch_bounds__(T_THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < T_SCALES; ++j)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) to[j * SG_ROWS + r0 + 64 * h] = v[h][j];
-                    if (r0 < L::W_SCALES * T_SCALES) to[T_SCALES * SG_ROWS + r0] = w;
+                        for (int n = 0; n < L::W_SCALES; ++n)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) to[(j * L::W_SCALES + n) * SG_ROWS + r0 + 64 * h] = v[h][j] * w[n][j];
                     __syncwarp();
                     if (lane == 0) mbar_arrive(scf + 8 * (c & 1));
                 }
@@ -624,87 +657,96 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         }
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(T_SUM_REGS));
-        constexpr int COLS = BN / 2;     // a warpgroup's columns
-        const int w = warp - 4, q = w & 3, half = w >> 2;
-        const uint32_t trow = tmem + ((uint32_t)(32 * q) << 16) + half * COLS;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::SUM_REGS));
+        constexpr int COLS = L::COLS;
+        const int w = warp - 4, q = w & 3, part = w >> 2;        // lanes 32 q .., columns COLS part ..
+        const uint32_t trow = tmem + ((uint32_t)(32 * q) << 16) + part * COLS;
         uint8_t* turn = sm + L::STAGES * L::STAGE + w * L::TURN;
         T* y = static_cast<T*>(g.y);
         // 16-byte stores where y and its rows allow them
         const bool wide = ((reinterpret_cast<uintptr_t>(y) | (uintptr_t)(g.y_stride * (long long)sizeof(T))) & 15u) == 0;
-        uint32_t i = 0, c = 0;           // blocks, and sets of scales
+        uint32_t b = 0, bp = 0, c = 0;   // buffer and its phase, sets of scales
         bool ok = true;
         for (int t = first; t < tiles; t += step) {
             int mt, nt;
             tile_at(g, t, mt, nt);
-            const int m0 = (PAIR ? 2 * mt + rank : mt) * SG_ROWS + 32 * q, n0 = nt * BN + half * COLS;
+            const int m0 = (PAIR ? 2 * mt + rank : mt) * SG_ROWS + 32 * q, n0 = nt * BN + part * COLS;
             uint64_t acc[COLS / 2];
 #pragma unroll
             for (int j = 0; j < COLS / 2; ++j) acc[j] = 0ull;
-            for (int k = 0; k < g.kb; ++k, ++i) {
-                const uint32_t b = i % L::NBUF;
-                if (k % T_SCALES == 0 && !gwait(scf + 8 * (c & 1), c >> 1, abort_, g.err)) {
-                    ok = false;
-                    break;
-                }
-                const float* sc = scales + (c & 1) * L::SCALES;
-                const float s = sc[k % T_SCALES * SG_ROWS + 32 * q + lane] *
-                                sc[T_SCALES * SG_ROWS + (half * L::W_SCALES >> 1) * T_SCALES + k % T_SCALES];
-                if (k % T_SCALES == T_SCALES - 1 || k + 1 == g.kb) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(sce + 8 * (c & 1));
-                    ++c;
-                }
-                if (!gwait(accf + 8 * b, i / L::NBUF, abort_, g.err)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint64_t s2 = pack2(s, s);
+            // (One way through these loops, whatever a wait says: with a way out of them the sums move to other registers.)
+#pragma unroll 1
+            for (int k0 = 0; k0 < nkb; k0 += T_SCALES, ++c) {
+                ok = gwait(scf + 8 * (c & 1), c >> 1, abort_, g.err) && ok;
+                const float* sc = scales + (c & 1) * L::SCALES + (n0 / SG_N - nt * BN / SG_N) * SG_ROWS + 32 * q + lane;
+                float s = *sc;
+#pragma unroll 1
+                for (int k = min(T_SCALES, nkb - k0); k > 0; --k) {
+                    ok = gwait(accf + 8 * b, bp, abort_, g.err) && ok;
+                    tc_fence_after();
+                    const uint64_t s2 = pack2(s, s);
+                    sc += L::W_SCALES * SG_ROWS;
+                    if (k > 1) s = *sc;                  // (the next block's: an answer of shared memory takes long)
 #pragma unroll
-                for (int h = 0; h < COLS / 64; ++h) tmem_sum64(trow + b * BN + 64 * h, s2, acc + 32 * h);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {                         // the buffer is read out
-                    if (PAIR) mbar_arrive_cluster(acce0 + 8 * b);
-                    else mbar_arrive(acce + 8 * b);
+                    for (int h = 0; h < COLS / 64; ++h) tmem_sum64(trow + b * BN + 64 * h, s2, acc + 32 * h);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {                     // the buffer is read out
+                        if (PAIR) mbar_arrive_cluster(acce0 + 8 * b);
+                        else mbar_arrive(acce + 8 * b);
+                    }
+                    if (++b == (uint32_t)L::NBUF) { b = 0; bp ^= 1u; }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sce + 8 * (c & 1));
             }
             if (!ok) break;
-            // 128 bytes of every row at a time, turned through shared memory (16-byte pieces of row r at piece
-            // ^ (r & 7)), so that a store instruction writes whole lines
-            constexpr int PC = 128 / (int)sizeof(T), PIECE = 16 / (int)sizeof(T);        // columns of 128 and of 16 bytes
+            if constexpr (SPLIT) {
+                // the tensor cores' reads of the stages are complete (the last block's barrier). Row r's 16-byte pieces lie
+                // at piece ^ (r & 7)
+                fence_proxy_async_smem();
+                const int row = 32 * q + lane;
+                float* to = reinterpret_cast<float*>(sm) + row * BN;
+#pragma unroll
+                for (int j = 0; j < COLS / 4; ++j) {
+                    const float2 p0 = unpack2(acc[2 * j]), p1 = unpack2(acc[2 * j + 1]);
+                    *reinterpret_cast<float4*>(to + (((part * COLS / 4 + j) ^ (row & 7)) << 2)) = make_float4(p0.x, p0.y, p1.x, p1.y);
+                }
+                continue;
+            }
+            // 64 bytes of every row at a time, turned through shared memory (16-byte pieces of row r at piece
+            // ^ (r / 2 % 4)), so that a store instruction writes whole sectors
+            constexpr int PC = 64 / (int)sizeof(T), PIECE = 16 / (int)sizeof(T);         // columns of 64 and of 16 bytes
 #pragma unroll
             for (int col = 0; col < COLS; col += PC) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 4; ++k) {
                     uint4 v;
-                    const int at = (col + k * PIECE) / 2;
+                    const uint64_t* x = acc + (col + k * PIECE) / 2;
+                    const float2 p0 = unpack2(x[0]), p1 = unpack2(x[1]);
                     if constexpr (sizeof(T) == 4) {
-                        const float2 p0 = unpack2(acc[at]), p1 = unpack2(acc[at + 1]);
                         v = make_uint4(__float_as_uint(p0.x), __float_as_uint(p0.y), __float_as_uint(p1.x), __float_as_uint(p1.y));
                     } else {
-                        const float2 p0 = unpack2(acc[at]), p1 = unpack2(acc[at + 1]), p2 = unpack2(acc[at + 2]), p3 = unpack2(acc[at + 3]);
+                        const float2 p2 = unpack2(x[2]), p3 = unpack2(x[3]);
                         v = make_uint4(pack_bf16x2(p0.x, p0.y), pack_bf16x2(p1.x, p1.y), pack_bf16x2(p2.x, p2.y), pack_bf16x2(p3.x, p3.y));
                     }
-                    *reinterpret_cast<uint4*>(turn + lane * 128 + ((k ^ (lane & 7)) << 4)) = v;
+                    *reinterpret_cast<uint4*>(turn + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4)) = v;
                 }
                 __syncwarp();
-                if (wide && n0 + col + PC <= g.N) {
+                const int n1 = n0 + col;
+                if (wide && n1 + PC <= g.N) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        const int row = k + (lane >> 3), piece = lane & 7;
-                        const uint4 v = *reinterpret_cast<const uint4*>(turn + row * 128 + ((piece ^ (row & 7)) << 4));
-                        if (m0 + row < g.M)
-                            *reinterpret_cast<uint4*>(y + (long long)(m0 + row) * g.y_stride + n0 + col + piece * PIECE) = v;
+                    for (int k = 0; k < 32; k += 8) {
+                        const int row = k + (lane >> 2), piece = lane & 3;
+                        const uint4 v = *reinterpret_cast<const uint4*>(turn + row * 64 + ((piece ^ (row >> 1 & 3)) << 4));
+                        if (m0 + row < g.M) *reinterpret_cast<uint4*>(y + (long long)(m0 + row) * g.y_stride + n1 + piece * PIECE) = v;
                     }
                 } else {                 // element by element, neighbours on neighbouring lanes
-                    for (int row = 0; row < 32 && m0 + row < g.M; ++row)
-#pragma unroll
-                        for (int e = lane; e < PC; e += 32) {
-                            const T v = *reinterpret_cast<const T*>(turn + row * 128 + (((e / PIECE) ^ (row & 7)) << 4) + (e % PIECE) * (int)sizeof(T));
-                            if (n0 + col + e < g.N) y[(long long)(m0 + row) * g.y_stride + n0 + col + e] = v;
-                        }
+                    for (int e = lane; e < 32 * PC; e += 32) {
+                        const int row = e / PC, x = e % PC;
+                        const T v = *reinterpret_cast<const T*>(turn + row * 64 + (((x / PIECE) ^ (row >> 1 & 3)) << 4) + (x % PIECE) * (int)sizeof(T));
+                        if (m0 + row < g.M && n1 + x < g.N) y[(long long)(m0 + row) * g.y_stride + n1 + x] = v;
+                    }
                 }
                 __syncwarp();
             }
@@ -713,6 +755,26 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     }
     __syncthreads();
     if (PAIR) cluster_sync_all();        // neither CTA's shared or tensor memory goes while the other uses it
+    if constexpr (SPLIT) {
+        // every thread of every member passes both cluster barriers, whatever happened before
+        cluster_sync_all();
+        if (!*abort_) {
+            int mt, nt;
+            tile_at(g, first, mt, nt);
+            const int r0 = ks * SG_ROWS / g.split_k, r1 = (ks + 1) * SG_ROWS / g.split_k;
+            for (int i = r0 * (BN / 4) + (int)threadIdx.x; i < r1 * (BN / 4); i += L::THREADS) {
+                const int row = i / (BN / 4), piece = i % (BN / 4), m = mt * SG_ROWS + row, n = nt * BN + 4 * piece;
+                if (m >= g.M || n >= g.N) continue;
+                const uint32_t off = sbase + (uint32_t)((row * BN + ((piece ^ (row & 7)) << 2)) * 4);
+                float4 t[SG_MAX_SPLIT];
+#pragma unroll
+                for (int r = 0; r < SG_MAX_SPLIT; ++r)
+                    if (r < g.split_k) t[r] = ld_dsmem_f4(dsmem_addr(off, (uint32_t)r));
+                store_sum4(g, t, m, n, static_cast<T*>(g.y));
+            }
+        }
+        cluster_sync_all();
+    }
     if (warp == 1) {
         tc_fence_after();
         if (PAIR) tmem_dealloc_pair(tmem, 512);
@@ -771,16 +833,15 @@ fdpp_status encode_rows(CUtensorMap* map, const void* base, int rows, int K, lon
     return FDPP_OK;
 }
 
-using RowsKernel = void (*)(const CUtensorMap, const CUtensorMap, const ScaledArgs);
+using SgKernel = void (*)(const CUtensorMap, const CUtensorMap, const ScaledArgs);
 
 template <typename T>
-RowsKernel rows_kernel(int Mp)
+SgKernel rows_kernel(int Mp)
 {
-    return Mp <= 16 ? scaled_rows_kernel<T, 16> : Mp <= 32 ? scaled_rows_kernel<T, 32> : Mp <= 64 ? scaled_rows_kernel<T, 64>
-                                                                                                 : scaled_rows_kernel<T, 128>;
+    return Mp <= 16 ? scaled_rows_kernel<T, 16> : Mp <= 32 ? scaled_rows_kernel<T, 32> : scaled_rows_kernel<T, 64>;
 }
 
-int rows_smem(int Mp, int nstage) { return nstage * (RW_BYTES + Mp * SB) + 2 * R_SCALES * SG_ROWS * 4 + 16 * nstage + 64 + 1024; }
+int rows_smem(int Mp, int nstage) { return nstage * (RW_BYTES + Mp * SB) + 2 * R_SCALES * SG_GROUP * 4 + 16 * nstage + 64 + 1024; }
 
 // Ring depth for two CTAs per SM.
 int rows_stages(int Mp, int smem_per_sm, int smem_per_block)
@@ -790,10 +851,10 @@ int rows_stages(int Mp, int smem_per_sm, int smem_per_block)
 }
 
 // Clusters of `split` CTAs that the GPU holds at once (0 if the query fails); cached.
-int max_clusters(RowsKernel kern, int split, int smem)
+int max_clusters(SgKernel kern, int split, int threads, int smem)
 {
     static std::mutex mu;
-    static std::map<std::pair<RowsKernel, std::pair<int, long long>>, int> cache;
+    static std::map<std::pair<SgKernel, std::pair<int, long long>>, int> cache;
     int dev = 0;
     cudaGetDevice(&dev);
     const auto key = std::make_pair(kern, std::make_pair(dev, ((long long)split << 32) | smem));
@@ -802,7 +863,7 @@ int max_clusters(RowsKernel kern, int split, int smem)
     if (it != cache.end()) return it->second;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)split);
-    cfg.blockDim = dim3(R_THREADS);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -819,31 +880,30 @@ int max_clusters(RowsKernel kern, int split, int smem)
     return n;
 }
 
+// Ranges of K for `tiles` output tiles: as many as keep all clusters on the GPU at once, two blocks each at least.
+int choose_split(SgKernel kern, long long tiles, int kb, int threads, int smem)
+{
+    for (int n = std::min(SG_MAX_SPLIT, kb / 2); n > 1; --n)
+        if (tiles <= max_clusters(kern, n, threads, smem)) return n;
+    return 1;
+}
+
 fdpp_status launch_rows(const fdpp_scaled_gemm_params& p, ScaledArgs& g, const void* x, const void* w, int smem_sm, int smem_blk,
                         cudaStream_t s)
 {
     g.Mp = (p.M + 15) / 16 * 16;
     g.nstage = rows_stages(g.Mp, smem_sm, smem_blk);
     const int smem = rows_smem(g.Mp, g.nstage), tiles = (p.N + SG_N - 1) / SG_N;
-    const RowsKernel kern = p.out_dtype == FDPP_F32 ? rows_kernel<float>(g.Mp) : rows_kernel<__nv_bfloat16>(g.Mp);
+    const SgKernel kern = p.out_dtype == FDPP_F32 ? rows_kernel<float>(g.Mp) : rows_kernel<__nv_bfloat16>(g.Mp);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return sfail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    g.split_k = p.split_k;
-    if (!g.split_k) {
-        // as many ranges as keep all clusters on the GPU at once, with two blocks each at least
-        g.split_k = 1;
-        for (int n = std::min(SG_MAX_SPLIT, g.kb / 2); n > 1; --n)
-            if (tiles <= max_clusters(kern, n, smem)) {
-                g.split_k = n;
-                break;
-            }
-    }
+    g.split_k = p.split_k ? p.split_k : choose_split(kern, tiles, g.kb, R_THREADS, smem);
     CUtensorMap tw, tx;
     fdpp_status st;
     if ((st = encode_rows(&tw, w, p.N, p.K, p.w_stride, SG_N)) != FDPP_OK) return st;
     if ((st = encode_rows(&tx, x, p.M, p.K, p.x_stride, g.Mp)) != FDPP_OK) return st;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)tiles * g.split_k);
+    cfg.gridDim = dim3((unsigned)(tiles * g.split_k));
     cfg.blockDim = dim3(R_THREADS);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
@@ -865,7 +925,7 @@ template <typename T, int BN, bool PAIR>
 fdpp_status launch_tile(const fdpp_scaled_gemm_params& p, ScaledArgs& g, const void* x, const void* w, int sms, int smem_blk,
                         cudaStream_t s)
 {
-    constexpr int smem = TileSmem<BN, PAIR>::TOTAL, rows = PAIR ? 2 * SG_ROWS : SG_ROWS;
+    constexpr int smem = TileSmem<BN, PAIR>::TOTAL, rows = PAIR ? 2 * SG_ROWS : SG_ROWS, threads = TileSmem<BN, PAIR>::THREADS;
     if (smem > smem_blk) return sfail(FDPP_ERR_UNSUPPORTED, "too little shared memory for the tile kernel");
     const long long m_tiles = ((long long)p.M + rows - 1) / rows, n_tiles = ((long long)p.N + BN - 1) / BN;
     if (m_tiles * n_tiles >= (1ll << 31) - sms || T_GROUP * n_tiles >= (1ll << 31))
@@ -876,22 +936,33 @@ fdpp_status launch_tile(const fdpp_scaled_gemm_params& p, ScaledArgs& g, const v
     fdpp_status st;
     if ((st = encode_rows(&tw, w, p.N, p.K, p.w_stride, TileSmem<BN, PAIR>::W_ROWS)) != FDPP_OK) return st;
     if ((st = encode_rows(&tx, x, p.M, p.K, p.x_stride, SG_ROWS)) != FDPP_OK) return st;
-    auto kern = scaled_tile_kernel<T, BN, PAIR>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return sfail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    SgKernel kern = scaled_tile_kernel<T, BN, PAIR, false>;
+    g.split_k = 1;
+    cudaError_t e;
+    if constexpr (!PAIR) {
+        const SgKernel split = scaled_tile_kernel<T, BN, PAIR, true>;
+        if ((e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+            return sfail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        g.split_k = p.split_k ? p.split_k : choose_split(split, m_tiles * n_tiles, g.kb, threads, smem);
+        if (g.split_k > 1) kern = split;
+    }
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+        return sfail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    const int cluster = PAIR ? 2 : g.split_k;
+    const long long tiles = m_tiles * n_tiles;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(PAIR ? 2 * std::min<long long>(sms / 2, m_tiles * n_tiles) : std::min<long long>(sms, m_tiles * n_tiles)));
-    cfg.blockDim = dim3(T_THREADS);
+    cfg.gridDim = dim3((unsigned)(cluster * (g.split_k > 1 ? tiles : std::min<long long>(sms / cluster, tiles))));
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = PAIR ? 2 : 1;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 2 : 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, kern, tx, tw, g);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return sfail(FDPP_ERR_CUDA, "scaled GEMM launch: %s", cudaGetErrorString(e));
@@ -935,8 +1006,12 @@ fdpp_status fdpp_scaled_gemm(const void* x, const float* x_scales, const void* w
     g.N = p->N;
     g.kb = blocks_of(p->K);
     cudaStream_t s = (cudaStream_t)stream;
-    if (p->M <= SG_ROWS) return launch_rows(*p, g, x, w, smem_sm, smem_blk, s);
-    // weight tiles of 256 where they alone are at least a tile per pair of SMs, else of 128
+    // Few rows: the rows kernel pads them least, the tile kernel's CTAs split K with less to add up. us a call, rows
+    // kernel against tile kernel: 32 rows of 4096 x 4096 6.9 and 7.8, of 28672 x 4096 21.9 and 30.9, of 4096 x 14336 17.0
+    // and 15.0; 64 rows 8.2 and 7.9, 25.4 and 31.6, 19.1 and 15.1. With weight tiles for all SMs it keeps the advantage.
+    const int w_tiles = (int)((p->N + SG_N - 1ll) / SG_N);
+    if (p->M <= 32 || (p->M <= SG_GROUP && w_tiles >= sms)) return launch_rows(*p, g, x, w, smem_sm, smem_blk, s);
+    // Pairs of CTAs on 256 x 256 tiles where these alone are enough for all SMs, else 128 x 128 ones.
     const long long tiles = ((p->M + 255ll) / 256) * ((p->N + 255ll) / 256);
     const bool big = tiles >= sms / 2;
     if (p->out_dtype == FDPP_F32)

@@ -43,7 +43,7 @@ E4M3 = dict(out_dtype=F.FDPP_E4M3, scales=6 * FAKE)
     dict(x_stride=260), dict(residual_stride=0), dict(out_stride=255), dict(sum_stride=8), dict(x=None), dict(out=None),
     dict(x=FAKE + 8), dict(residual=FAKE + 4), dict(weight=FAKE + 2), dict(out=FAKE + 8), dict(total=FAKE + 8),
     dict(scales=6 * FAKE), dict(out_dtype=F.FDPP_E4M3), {**E4M3, "scales": 6 * FAKE + 2}, {**E4M3, "scale_stride": 1},
-    {**E4M3, "dim": 264, "out_stride": 264}, {**E4M3, "out": FAKE}, dict(out=FAKE, x_stride=512), dict(total=FAKE, x_stride=512),
+    {**E4M3, "dim": 264, "out_stride": 268}, {**E4M3, "out": FAKE}, dict(out=FAKE, x_stride=512), dict(total=FAKE, x_stride=512),
     dict(total=2 * FAKE, sum_stride=512), dict(out=2 * FAKE), dict(out=5 * FAKE), dict(x_stride=1 << 50),
 ])
 def test_norm_rejects(kw):

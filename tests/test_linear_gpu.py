@@ -59,7 +59,7 @@ def check_norm(T, dim, dtype="bf16", out="same", residual=True, weight=True, off
         p = F.make_norm_params(out_stride=stride, **kw)
         o, scales = (x if in_place else filled(T, stride, tdt, 7.0)), None
     else:
-        p = F.make_norm_params(out_dtype=F.FDPP_E4M3, out_stride=-(-stride // 16) * 16 + 16, scale_stride=blocks + 3, **kw)
+        p = F.make_norm_params(out_dtype=F.FDPP_E4M3, out_stride=stride + 8, scale_stride=blocks + 3, **kw)
         o, scales = filled(T, p.out_stride, torch.uint8, 0xAB), filled(T, blocks + 3, torch.float32, 7.0)
     F.fdpp_rms_norm(x, res, w, p, o, scales, total)
     torch.cuda.synchronize()
@@ -120,6 +120,23 @@ def test_norm_of_zeros_and_of_values_that_are_not_finite():
     # the infinity's row: finite values over an infinite root are 0, the infinity itself inf / inf
     assert bool((v[3, :128] == 0).all()) and bool(v[3, 128:256].isnan().all()) and bool((v[3, 256:] == 0).all())
     assert bool((v[4] == 448).all())               # blocks of very different sizes: each by its own scale
+
+
+@pytest.mark.parametrize("dim", [8, 24, 136, 1000, 2056])
+def test_norm_contiguous_rows_end_where_the_buffer_does(dim):
+    """Contiguous e4m3 rows by the binding's defaults, of channels that are no multiple of 16: nothing behind them
+    is written."""
+    T = 9
+    x = torch.randn(T, dim, device="cuda")
+    p = F.make_norm_params(num_tokens=T, dim=dim, dtype=F.FDPP_F32, out_dtype=F.FDPP_E4M3)
+    buf, scales = torch.full((T * dim + 64,), 0xAB, device="cuda", dtype=torch.uint8), torch.empty(T, p.scale_stride, device="cuda")
+    F.fdpp_rms_norm(x, None, None, p, buf, scales)
+    torch.cuda.synchronize()
+    assert bool((buf[T * dim:] == 0xAB).all())
+    _, y = norm_reference(x, None, None, 1e-6, 0.0)
+    each = scales.double().repeat_interleave(128, 1)[:, :dim]
+    got = e4m3(buf[:T * dim].reshape(T, dim)).double() * each
+    assert bool(((got - y).abs() <= (2.0 ** -4 + 2.0 ** -16) * y.abs() + 2.0 ** -10 * each).all())
 
 
 def test_norm_of_nothing():
