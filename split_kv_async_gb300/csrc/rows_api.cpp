@@ -236,12 +236,11 @@ fdpp_status attend(const void* q, const void* prefix_k, const void* prefix_v, co
     if (parents) {
         a.parents = parents;
         a.lineage = reinterpret_cast<uint32_t*>(ws + w.total);
-        const cudaError_t e = launch_lineage(a, s);
-        if (e != cudaSuccess) return rfail(FDPP_ERR_CUDA, "lineage kernel launch: %s", cudaGetErrorString(e));
     }
     if (!tensor_kernel(*p)) {
         a.splits = simt_splits(*p);
-        const cudaError_t e = launch_rows_simt(a, p->dtype, s);
+        cudaError_t e = parents ? launch_lineage(a, false, s) : cudaSuccess;
+        if (e == cudaSuccess) e = launch_rows_simt(a, p->dtype, s);
         if (e != cudaSuccess) return rfail(FDPP_ERR_CUDA, "rows kernel launch: %s", cudaGetErrorString(e));
         return FDPP_OK;
     }

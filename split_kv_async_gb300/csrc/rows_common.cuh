@@ -69,22 +69,19 @@ __device__ __forceinline__ void row_keys(const RowsArgs& a, int row, int pos, in
 // A sequence of n tokens whose tree is too large: its tokens see nothing.
 __device__ __forceinline__ bool tree_too_large(const RowsArgs& a, int n) { return a.parents && n > FDPP_TREE_MAX_TOKENS; }
 
-// Whether a token with this line of ancestors sees key t, which lies in its key range.
-__device__ __forceinline__ bool line_sees(const uint32_t* line, int t)
+// Whether a token with this lineage, of a tree whose node 0 is key tree0, sees key t of its key range.
+__device__ __forceinline__ bool line_sees(const uint32_t* line, int tree0, int t)
 {
-    const int node = t - (int)line[0];
-    return node < 0 || (node < FDPP_TREE_MAX_TOKENS && (line[1 + (node >> 5)] >> (node & 31) & 1u));
+    const int node = t - tree0;
+    return node < 0 || (node < FDPP_TREE_MAX_TOKENS && (line[LINE_UP + (node >> 5)] >> (node & 31) & 1u));
 }
 
-// The same for the 32 keys from t on, a bit each.
-__device__ __forceinline__ uint32_t line_bits(const uint32_t* line, int t)
+// Bits [at, at + 32) of LINE_BITS words, zeros behind them.
+__device__ __forceinline__ uint32_t line_bits(const uint32_t* words, int at)
 {
-    const int node = t - (int)line[0];
-    if (node <= -32) return 0xffffffffu;
-    if (node < 0) return (line[1] << -node) | ((1u << -node) - 1u);
-    const int w = node >> 5;
-    const uint32_t lo = w + 1 < LINE_WORDS ? line[1 + w] : 0u, hi = w + 2 < LINE_WORDS ? line[2 + w] : 0u;
-    return __funnelshift_r(lo, hi, node & 31);
+    const int w = at >> 5;
+    const uint32_t lo = w < LINE_BITS ? words[w] : 0u, hi = w + 1 < LINE_BITS ? words[w + 1] : 0u;
+    return __funnelshift_r(lo, hi, at & 31);
 }
 
 // Element offset of key t (local to its source) of kv head g; -1: its block lies outside the pool.

@@ -89,14 +89,18 @@ struct RowsArgs {
     uint32_t* lineage;              // [T][LINE_WORDS]
 };
 
-// A token's line of ancestors: the key of its sequence's node 0, then a bit for every node that is the token
-// itself or one of its ancestors.
-constexpr int LINE_WORDS = 1 + FDPP_TREE_MAX_TOKENS / 32;
+// What is kept of a token, node i of its tree: the key of the tree's node 0, a bit for every node that is i itself
+// or one of its ancestors (the keys that it sees), and a bit for every node that is i itself or descends from
+// it (the tokens that see it).
+constexpr int LINE_BITS = FDPP_TREE_MAX_TOKENS / 32;
+constexpr int LINE_UP = 1, LINE_DOWN = 16, LINE_WORDS = 32;      // (whole sectors, the first with seven words of ancestors)
+static_assert(LINE_UP + LINE_BITS <= LINE_DOWN && LINE_DOWN + LINE_BITS <= LINE_WORDS, "a token's lineage fits its words");
 
 RowsLayout rows_layout(const fdpp_rows_params& p);
 
-// The tokens' lines of ancestors, before either kernel of a call with trees.
-cudaError_t launch_lineage(const RowsArgs& a, cudaStream_t s);
+// The tokens' lineage, before the kernels that mask by it. after_plan: enqueued behind the tensor kernel's plan, beside
+// which it runs.
+cudaError_t launch_lineage(const RowsArgs& a, bool after_plan, cudaStream_t s);
 cudaError_t launch_rows_simt(const RowsArgs& a, int dtype, cudaStream_t s);
 // Plan, tile kernel and join.
 struct RowsMaps {

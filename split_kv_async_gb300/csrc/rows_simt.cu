@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
     row_keys(a, row, pos, P + L, lo, hi);
     if (TREE && tree_too_large(a, n)) lo = hi = 0;
     const uint32_t* line = TREE ? a.lineage + (long long)row * LINE_WORDS : nullptr;
+    const int tree0 = L - n;
     const int len = hi - lo;
     const int k0 = lo + (int)((long long)len * split / a.splits), k1 = lo + (int)((long long)len * (split + 1) / a.splits);
 
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
 
 #pragma unroll 2
     for (int t = k0 + grp; t < k1; t += GROUPS) {
-        if (TREE && !line_sees(line, t)) continue;
+        if (TREE && !line_sees(line, tree0, t)) continue;
         const bool pre = t < P;
         const long long off = key_offset(a, pre ? -1 : b, pre ? t : t - P, g);
         if (off < 0) {

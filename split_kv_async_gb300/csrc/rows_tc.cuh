@@ -1082,16 +1082,16 @@ struct RowsPv {
 // by the keys that it sees. (Any lo and hi: t only grows.) line: the row's line of ancestors, with trees.
 template <int D, int NC, bool TREE>
 __device__ __noinline__ bool unseen_values(const RowsArgs& a, int b, int g, int k0, int lo, int hi, int k1, int col,
-                                           volatile int* misc, const uint32_t* line)
+                                           volatile int* misc, const uint32_t* line, int tree0)
 {
     const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(b < 0 && a.pv ? a.pv : a.v);
     bool found = false;
     for (int t = k0; t < k1; ++t) {
         if (TREE) {
             // of a tree's keys those on other branches count too
-            if (t >= lo && t < hi && t < (int)line[0]) t = min(hi, (int)line[0]);
+            if (t >= lo && t < hi && t < tree0) t = min(hi, tree0);
             if (t >= k1) break;
-            if (t >= lo && t < hi && line_sees(line, t)) continue;
+            if (t >= lo && t < hi && line_sees(line, tree0, t)) continue;
         } else {
             if (t >= lo && t < hi) t = hi;
             if (t >= k1) break;
@@ -1111,7 +1111,7 @@ __device__ __noinline__ bool unseen_values(const RowsArgs& a, int b, int g, int 
 // o: its columns col + 32 i of each lane.
 template <int D, int NC, bool TREE>
 __device__ __noinline__ void redo_row(const RowsArgs& a, int b, int g, int h, int row, int pos, int k0, int k1, int base,
-                                      float M, int col, float (&o)[NC], volatile int* misc, const uint32_t* line)
+                                      float M, int col, float (&o)[NC], volatile int* misc, const uint32_t* line, int tree0)
 {
     const int lane = threadIdx.x & 31;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + ((long long)row * a.Hq + h) * D;
@@ -1130,7 +1130,7 @@ __device__ __noinline__ void redo_row(const RowsArgs& a, int b, int g, int h, in
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             off[k] = t + k < k1 ? key_offset(a, b, t + k, g) : -1;      // (a block outside the pool: reported)
-            if (TREE && t + k < k1 && !line_sees(line, t + k)) off[k] = -1;
+            if (TREE && t + k < k1 && !line_sees(line, tree0, t + k)) off[k] = -1;
             s[k] = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i)
@@ -1286,6 +1286,20 @@ __device__ __forceinline__ void reg_fence(uint32_t (&r)[NR])
     for (int i = 0; i < NR; ++i) asm volatile("" : "+r"(r[i]) : : "memory");
 }
 
+// The rows (a bit each) of a key-major run of ntok tokens from row tok0 on, node node0, that see a node of their tree: by one
+// look at the node's own descendants (of every row by its ancestors they took 17 to 37 us a call more). Out of
+// line: in it, the loop of 128-row runs got other registers, and 64 trees behind 512 to 16384 keys took 336 us instead of 322.
+__device__ __noinline__ uint32_t rows_that_see(const RowsArgs& a, int tok0, int ntok, int node0, int node)
+{
+    const uint32_t row = (uint32_t)tok0 - (uint32_t)node0 + (uint32_t)node;
+    if (node0 < 0 || row >= (uint32_t)a.T) return 0u;    // (only where sequences overlap)
+    const uint32_t tokens = line_bits(a.lineage + (long long)row * LINE_WORDS + LINE_DOWN, node0);
+    const uint32_t heads = (a.G < 32 ? 1u << a.G : 0u) - 1u;
+    uint32_t sees = 0u;
+    for (int i = 0; i < ntok; ++i) sees |= tokens >> i & 1u ? heads << i * a.G : 0u;
+    return sees;
+}
+
 // How scores become v, in units of log2: scale alone; scale and bias; cap, scale and bias.
 enum { MODE_PLAIN = 0, MODE_BIAS = 1, MODE_CAP = 2 };
 
@@ -1360,9 +1374,12 @@ struct Softmax {
         int lo = mine ? max(tk.lo - base, 0) : 0, hi = mine ? min(tk.hi - base, run.len) : INT32_MAX;
         if (mine && hi <= lo) lo = hi = 0;
         const bool empty = hi <= lo;
-        // with trees: the row's line of ancestors, and the first key that it may hide
-        const uint32_t* line = TREE ? a.lineage + (long long)(mine ? tok : 0) * LINE_WORDS : nullptr;
-        const int tree0 = TREE && mine ? (int)line[0] : INT32_MAX;
+        // With trees the keys below hi are those that the row sees for certain, up to the tree's first; which it sees of
+        // the others its lineage says, read where it is needed (from the same sector: the L1 cache has it by then).
+        if (TREE && mine) {
+            hi = min(hi, (int)a.lineage[(long long)tok * LINE_WORDS]);
+            if (empty) lo = INT32_MAX;
+        }
         float slope = 0.f;
         if (MODE != MODE_PLAIN && a.slopes && live) slope = a.slopes[run.g * a.G + hh] * LOG2E;
         const int spos = tk.pos - base;                  // the position in this source's indexes
@@ -1387,7 +1404,7 @@ struct Softmax {
                 // Half tiles with masked scores, or a bias that is not linear in the key: v (masked: -inf) back
                 // to tensor memory first, by a rolled loop, since code that few tiles need costs more to fetch
                 // than it saves.
-                const bool open = __all_sync(0xffffffffu, lo <= k0 && hi >= k0 + 64 && (!TREE || tree0 >= k0 + 64));
+                const bool open = __all_sync(0xffffffffu, lo <= k0 && hi >= k0 + 64);
                 const bool ready_v = MODE == MODE_PLAIN || (open && (linear || !a.slopes));
                 if (!open || !ready_v) {
 #pragma unroll 1
@@ -1398,12 +1415,18 @@ struct Softmax {
                         reg_fence32(y);
                         const int kc = k0 + 32 * c, c0 = lo - kc, c1 = hi - kc;
                         const float d0 = (float)(kc - spos);
-                        const uint32_t bits = TREE && mine ? line_bits(line, kc) : 0xffffffffu;
+                        uint32_t bits = 0xffffffffu;
+                        if (TREE && mine && kc + 32 > hi) {
+                            const uint32_t* line = a.lineage + (long long)tok * LINE_WORDS;
+                            const int node = kc - (int)line[0];
+                            if (node > -32)
+                                bits = node < 0 ? (line[LINE_UP] << -node) | ((1u << -node) - 1u) : line_bits(line + LINE_UP, node);
+                        }
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
                             // a masked score may be anything, and one that is NaN would take its neighbour along
-                            const bool in0 = i >= c0 && i < c1 && (!TREE || (bits >> i & 1u));
-                            const bool in1 = i + 1 >= c0 && i + 1 < c1 && (!TREE || (bits >> (i + 1) & 1u));
+                            const bool in0 = i >= c0 && (TREE ? (bits >> i & 1u) != 0u : i < c1);
+                            const bool in1 = i + 1 >= c0 && (TREE ? (bits >> (i + 1) & 1u) != 0u : i + 1 < c1);
                             float v0 = in0 ? __uint_as_float(y[i]) : 0.f, v1 = in1 ? __uint_as_float(y[i + 1]) : 0.f;
                             if (MODE == MODE_CAP) {
                                 cap_pair(v0, v1, cap_rate, LOG2E * a.cap);
@@ -1654,8 +1677,10 @@ struct Softmax {
         // Rows that may have met a non-finite V of a key they do not see
         const int seen0 = (pair ? run.s0 : t0) * ROWS_KEYS, seen1 = min((pair ? run.s1 : t1) * ROWS_KEYS, run.len);
         // (one that sees none of the run's keys leaves an empty partial, which the join passes over)
+        const int hidden = hi;                           // the first key that the row may hide
+        if (TREE && mine) hi = empty ? 0 : min(tk.pos + 1 - base, run.len);
         const bool again = mine && count > 0 && !fine && max(lo, seen0) < min(hi, seen1) && fabsf(l) < INFINITY &&
-                           (lo > seen0 || hi < seen1 || (TREE && tree0 < seen1));
+                           (lo > seen0 || (TREE ? hidden : hi) < seen1);
         unsigned todo = __ballot_sync(0xffffffffu, again);
         while (todo) {
             beat(misc);
@@ -1667,10 +1692,11 @@ struct Softmax {
             const float jm = __shfl_sync(0xffffffffu, m, j), jl = __shfl_sync(0xffffffffu, l, j);
             const long long jat = __shfl_sync(0xffffffffu, at, j);
             const uint32_t* jline = TREE ? a.lineage + (long long)jtok * LINE_WORDS : nullptr;
-            if (!unseen_values<D, D / 32, TREE>(a, run.b, run.g, seen0, jlo, jhi, seen1, lane, misc, jline)) continue;
+            const int jtree0 = TREE ? (int)jline[0] : 0;
+            if (!unseen_values<D, D / 32, TREE>(a, run.b, run.g, seen0, jlo, jhi, seen1, lane, misc, jline, jtree0)) continue;
             float o[D / 32];
             redo_row<D, D / 32, TREE>(a, run.b, run.g, jhead, jtok, jpos, jlo, jhi, base, jm == -INFINITY ? 0.f : jm, lane, o, misc,
-                                      jline);
+                                      jline, jtree0);
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 if (direct) static_cast<__nv_bfloat16*>(a.out)[jat * D + lane + 32 * i] = __float2bfloat16_rn(o[i] / jl);
@@ -1756,9 +1782,9 @@ struct Softmax {
             if (hi <= lo) lo = hi = 0;
         }
         const int all_lo = warp_max(mine ? lo : 0), all_hi = warp_min(mine ? hi : INT32_MAX);
-        // with trees: the first key that a row may hide (its rows are tokens of one sequence)
-        const uint32_t* lines = TREE ? a.lineage + (long long)run.tok0 * LINE_WORDS : nullptr;
-        const int tree0 = TREE ? (int)lines[0] : INT32_MAX;
+        // with trees (the rows are tokens of one sequence): the first key that a row may hide, and the first token's node
+        const int tree0 = TREE ? (int)a.lineage[(long long)run.tok0 * LINE_WORDS] : INT32_MAX;
+        const int node0 = TREE ? __shfl_sync(0xffffffffu, tk.pos, 0) - tree0 : 0;
         float slope_l = 0.f;
         if (MODE != MODE_PLAIN && a.slopes && lane < R) slope_l = a.slopes[head] * LOG2E;
         const int spos_l = tk.pos - base;
@@ -1778,6 +1804,8 @@ struct Softmax {
             tc_fence_after();
             const int k0 = t * ROWS_KEYS, key = k0 + 32 * w + lane;
             const bool open = all_lo <= k0 && all_hi >= k0 + ROWS_KEYS && (!TREE || tree0 >= k0 + ROWS_KEYS);
+            uint32_t sees = 0xffffffffu;                 // with trees: the rows that see this thread's key
+            if (TREE && !open && key >= tree0) sees = key < run.len ? rows_that_see(a, run.tok0, run.ntok, node0, key - tree0) : 0u;
             // v of CH rows from row c on. Sixteen rows at most are held at a time: with 32 their scores are
             // read from tensor memory again for each step.
             auto load = [&](int c, float (&v)[CH]) {
@@ -1802,7 +1830,7 @@ struct Softmax {
                     for (int i = 0; i < CH; ++i) {
                         const int rlo = __shfl_sync(0xffffffffu, lo, c + i), rhi = __shfl_sync(0xffffffffu, hi, c + i);
                         if (key < rlo || key >= rhi) v[i] = -INFINITY;
-                        if (TREE && c + i < R && !line_sees(lines + (c + i) / a.G * LINE_WORDS, key)) v[i] = -INFINITY;
+                        if (TREE && !(sees >> (c + i) & 1u)) v[i] = -INFINITY;
                     }
                 }
             };
@@ -1976,9 +2004,10 @@ struct Softmax {
             const float jm = __shfl_sync(0xffffffffu, m, j), inv = __shfl_sync(0xffffffffu, inv_l, j);
             const long long jat = __shfl_sync(0xffffffffu, at, j);
             const uint32_t* jline = TREE ? a.lineage + (long long)jtok * LINE_WORDS : nullptr;
-            if (!unseen_values<D, 1, TREE>(a, run.b, run.g, seen0, jlo, jhi, seen1, d, misc, jline)) continue;
+            if (!unseen_values<D, 1, TREE>(a, run.b, run.g, seen0, jlo, jhi, seen1, d, misc, jline, tree0)) continue;
             float o[1];
-            redo_row<D, 1, TREE>(a, run.b, run.g, jhead, jtok, jpos, jlo, jhi, base, jm == -INFINITY ? 0.f : jm, d, o, misc, jline);
+            redo_row<D, 1, TREE>(a, run.b, run.g, jhead, jtok, jpos, jlo, jhi, base, jm == -INFINITY ? 0.f : jm, d, o, misc, jline,
+                              tree0);
             if (has) {
                 if (direct) static_cast<__nv_bfloat16*>(a.out)[jat * D + d] = __float2bfloat16_rn(o[0] * inv);
                 else pbase[jat * D + d] = o[0];
@@ -2290,6 +2319,7 @@ cudaError_t launch_d(const RowsArgs& a, const RowsMaps& m, cudaStream_t s)
     PdlConfig plan(dim3((unsigned)ranks), small ? PLAN_SMALL : PLAN_THREADS, 0, s, ranks);
     cudaError_t e = cudaLaunchKernelEx(&plan.cfg, small ? rows_plan_small_kernel : rows_plan_kernel, a);
     if (e != cudaSuccess) return e;
+    if (TREE && (e = launch_lineage(a, true, s)) != cudaSuccess) return e;
     auto kern = rows_tile_kernel<D, MODE, TREE>;
     const int smem = RowsSmem<D>(a.stages).total;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;

@@ -1,5 +1,5 @@
-// tree.cu -- trees of drafted tokens (fdpp_tree.h): the tokens' lines of ancestors, which the rows
-// attention's kernels mask by, and the commit of an accepted path.
+// tree.cu -- trees of drafted tokens (fdpp_tree.h): the tokens' lineage, which the rows attention's kernels mask
+// by, and the commit of an accepted path.
 #include <algorithm>
 #include <cstdarg>
 #include <cstdio>
@@ -11,41 +11,55 @@ namespace {
 
 constexpr int TREE = FDPP_TREE_MAX_TOKENS;
 
-// ---- lines of ancestors -------------------------------------------------------------------
-// A CTA per sequence, a thread per node: it walks up to the root through shared memory and sets a bit
-// for each node that it passes.
-__global__ void __launch_bounds__(TREE) lineage_kernel(RowsArgs a)
+// ---- lineage ------------------------------------------------------------------------------
+// A CTA per sequence, a thread per node: it walks up to the root through shared memory, sets a bit for each
+// node that it passes, and its own bit with each of them.
+//
+// AFTER_PLAN: on the stream behind the plan, which starts it as soon as what came before the plan has completed. So it
+// does its work first, beside the plan (its reads go past the L1 cache), and then waits for the plan: the kernel
+// behind it waits for it alone. It adds nothing to most calls then (as a launch of its own before the plan 2 to 3 us).
+template <bool AFTER_PLAN>
+__global__ void __launch_bounds__(TREE) lineage_kernel(const __grid_constant__ RowsArgs a)
 {
     __shared__ int up[TREE];
-    __shared__ uint32_t line[TREE * LINE_WORDS];         // (an odd number of words: no two rows in one bank)
+    constexpr int ROW = 1 + 2 * LINE_BITS;               // (an odd number of words: no two rows in one bank)
+    __shared__ uint32_t line[TREE * ROW];                // the tree's first key, ancestors, descendants
     const int b = blockIdx.x, i = threadIdx.x;
-    grid_dependency_wait();
+    if (!AFTER_PLAN) grid_dependency_wait();
     grid_launch_dependents();
-    unsigned bad = 0;
-    int c0;
-    const int n = seq_rows(a, b, c0, bad), L = own_len(a, b, bad);
-    bad = n > TREE ? FDPP_ERRBIT_TREE : 0;               // (the attention's kernels report the others)
-    if (bad) {
-        if (i == 0) rows_error(a, bad);
-        return;
+    int c0 = b * a.per_seq, n = a.per_seq;
+    if (a.cu) {
+        c0 = clamp_len(__ldcg(a.cu + b), a.T);
+        n = max(c0, clamp_len(__ldcg(a.cu + b + 1), a.T)) - c0;
     }
-    if (i < n) {
-        int p = a.parents[c0 + i];
-        if (p < -1 || p >= i) {
-            bad = FDPP_ERRBIT_TREE;
-            p = -1;
+    const int L = clamp_len(__ldcg(a.seq_lens + b), a.max_seq_len);
+    // (the attention's kernels report what is wrong with offsets and lengths)
+    unsigned bad = n > TREE ? FDPP_ERRBIT_TREE : 0;
+    if (n <= TREE) {
+        if (i < n) {
+            int p = __ldcg(a.parents + c0 + i);
+            if (p < -1 || p >= i) {
+                bad = FDPP_ERRBIT_TREE;
+                p = -1;
+            }
+            up[i] = p;
         }
-        up[i] = p;
-        for (int w = 0; w < LINE_WORDS; ++w) line[i * LINE_WORDS + w] = 0u;
-        line[i * LINE_WORDS] = (uint32_t)(L - n);
+        for (int w = i; w < n * ROW; w += TREE) line[w] = w % ROW == 0 ? (uint32_t)(L - n) : 0u;
+        __syncthreads();
+        if (i < n)
+            for (int j = i; j >= 0; j = up[j]) {
+                line[i * ROW + 1 + (j >> 5)] |= 1u << (j & 31);
+                atomicOr(&line[j * ROW + 1 + LINE_BITS + (i >> 5)], 1u << (i & 31));
+            }
+        __syncthreads();
+        uint32_t* to = a.lineage + (long long)c0 * LINE_WORDS;
+        for (int w = i; w < n * ROW; w += TREE) {
+            const int row = w / ROW, k = w - row * ROW;
+            to[row * LINE_WORDS + (k <= LINE_BITS ? k : k - 1 - LINE_BITS + LINE_DOWN)] = line[w];
+        }
     }
     rows_error(a, bad);
-    __syncthreads();
-    if (i < n)
-        for (int j = i; j >= 0; j = up[j]) line[i * LINE_WORDS + 1 + (j >> 5)] |= 1u << (j & 31);
-    __syncthreads();
-    uint32_t* to = a.lineage + (long long)c0 * LINE_WORDS;
-    for (int w = i; w < n * LINE_WORDS; w += TREE) to[w] = line[w];
+    if (AFTER_PLAN) grid_dependency_wait();
 }
 
 // ---- commit -------------------------------------------------------------------------------
@@ -231,9 +245,9 @@ bool repeated(void* const* p, int n)
 
 }  // namespace
 
-cudaError_t launch_lineage(const RowsArgs& a, cudaStream_t s)
+cudaError_t launch_lineage(const RowsArgs& a, bool after_plan, cudaStream_t s)
 {
-    return launch_pdl(lineage_kernel, dim3((unsigned)a.B), TREE, s, a);
+    return launch_pdl(after_plan ? lineage_kernel<true> : lineage_kernel<false>, dim3((unsigned)a.B), TREE, s, a);
 }
 
 }  // namespace fdpp
