@@ -53,8 +53,9 @@ fdpp_status fdpp_tree_workspace_size(const fdpp_rows_params* p, size_t* bytes);
 /* fdpp_rows_attn (fdpp_rows.h: layouts, arguments, accuracy, zero rows) with a tree's mask: token i of a sequence with L keys
  * and n tokens sees the keys t < L - n and those at L - n + j for every node j that is i itself or one
  * of its ancestors, of them those from key_begin[row] on where given (a sliding window). Parameters: key_end
- * and slopes must be NULL (a key's distance would depend on the tree). Keys that a token does not see never enter its sums,
- * whatever the cache holds there.
+ * and slopes must be NULL (a key's distance would depend on the tree); kernel FDPP_KERNEL_AUTO is the tensor kernel for
+ * bf16, except where num_tokens, the heads and max_seq_len leave so few keys to read that the CUDA-core kernel is done
+ * first. Keys that a token does not see never enter its sums, whatever the cache holds there.
  *   parents      DEVICE int32 [T], 4-byte aligned (see above). */
 fdpp_status fdpp_tree_attn(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
                            const int32_t* seq_lens, const int32_t* cu_tokens, const int32_t* parents,

@@ -96,6 +96,18 @@ fdpp_status check_tree(const fdpp_rows_params* p)
     return FDPP_OK;
 }
 
+// The kernel of a call with trees. bf16 takes the tensor cores, but where all tokens together have few keys to read
+// (each for itself on the CUDA cores) the tensor kernel's four launches take longer than these: of 75 drawn calls, 1 to
+// 60 sequences of 1 to 256 tokens, those with up to 1.5e6 elements of K took 6 to 16 us on the CUDA cores and 14 to 35 on
+// the tensor cores (but for one, 26 against 22), those with more than 2e6 16 to 780 and 16 to 90.
+constexpr long long TREE_SIMT_ELEMENTS = 1500000;
+fdpp_rows_params tree_params(const fdpp_rows_params& p)
+{
+    fdpp_rows_params t = p;
+    if (p.kernel == FDPP_KERNEL_AUTO && simt_units(p) <= TREE_SIMT_ELEMENTS / p.head_dim / p.max_seq_len) t.kernel = FDPP_KERNEL_SIMT;
+    return t;
+}
+
 fdpp_status check_paged(const fdpp_rows_params* p)
 {
     if (p->block_size < 16 || p->block_size > 256 || (p->block_size & (p->block_size - 1)))
@@ -340,7 +352,7 @@ fdpp_status fdpp_tree_workspace_size(const fdpp_rows_params* p, size_t* bytes)
     const fdpp_status st = check_tree(p);
     if (st != FDPP_OK) return st;
     if (!bytes) return rfail(FDPP_ERR_INVALID_ARG, "bytes is NULL");
-    *bytes = tree_bytes(*p);
+    *bytes = tree_bytes(tree_params(*p));
     return FDPP_OK;
 }
 
@@ -352,8 +364,9 @@ fdpp_status fdpp_tree_attn(const void* q, const void* k_cache, const void* v_cac
     const fdpp_status st = check_tree(p);
     if (st != FDPP_OK) return st;
     if (!parents || !aligned(parents, 4)) return rfail(FDPP_ERR_INVALID_ARG, "parents must be non-NULL and 4-byte aligned");
+    const fdpp_rows_params t = tree_params(*p);
     return attend(q, nullptr, nullptr, nullptr, nullptr, false, k_cache, v_cache, block_table, seq_lens, cu_tokens, parents,
-                  p, workspace, workspace_bytes, out, stream);
+                  &t, workspace, workspace_bytes, out, stream);
 }
 
 }  // extern "C"

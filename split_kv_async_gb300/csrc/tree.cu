@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(TREE) lineage_kernel(const __grid_constant__ R
 }
 
 // ---- commit -------------------------------------------------------------------------------
-// A CTA takes a sequence and 256 of the 16-byte columns of all caches' rows. Each finds the path for itself (a
+// A CTA takes a sequence and some of the 16-byte columns of all caches' rows. Each finds the path for itself (a
 // few hundred cycles through shared memory, less than a launch that waits for another): a node whose token
 // is its parent's choice enters itself as the parent's next one, the first such child winning, and one
 // thread follows the path. A thread then moves its column's rows in the order of the path. Node p_k >= k goes
@@ -71,8 +71,11 @@ __global__ void __launch_bounds__(TREE) lineage_kernel(const __grid_constant__ R
 // are read before the first of them is written, and no thread waits for another.
 constexpr int COMMIT_THREADS = 256;
 constexpr int COMMIT_AT_ONCE = 8;
+constexpr int COMMIT_RESIDENT = 8;       // CTAs of an SM (64 trees of 16 in 64 caches: 6.4 us; with four 7.3, two 8.8)
 static_assert(COMMIT_THREADS >= TREE, "a thread per node");
 
+// N: most caches (a launch with 2 kB of arguments takes the host a microsecond longer than one with 300 bytes).
+template <int N>
 struct CommitArgs {
     const int32_t* parents;
     const int32_t* tokens;
@@ -88,10 +91,11 @@ struct CommitArgs {
     long long row_bytes;
     int T, per_seq, max_seq_len, block_size, max_blocks, num_blocks;
     int columns, caches;                 // 16-byte columns of a row
-    void* cache[FDPP_TREE_MAX_CACHES];
+    void* cache[N];
 };
 
-__global__ void __launch_bounds__(COMMIT_THREADS) tree_commit_kernel(const __grid_constant__ CommitArgs a)
+template <int N>
+__global__ void __launch_bounds__(COMMIT_THREADS) tree_commit_kernel(const __grid_constant__ CommitArgs<N> a)
 {
     __shared__ int choice[TREE], next[TREE], path[TREE];
     __shared__ long long from[TREE], to[TREE];           // byte offsets of the path's rows, -1: not moved
@@ -178,18 +182,19 @@ __global__ void __launch_bounds__(COMMIT_THREADS) tree_commit_kernel(const __gri
         if (bad) atomicOr(a.err, bad);
     }
     __syncthreads();
-    const long long item = (long long)blockIdx.x * COMMIT_THREADS + i;
-    if (item >= (long long)a.caches * a.columns) return;
-    const int c = (int)(item / a.columns);
-    char* cache = static_cast<char*>(a.cache[c]) + (item - (long long)c * a.columns) * 16;
-    for (int k0 = start; k0 < count; k0 += COMMIT_AT_ONCE) {
-        uint4 v[COMMIT_AT_ONCE];
+    const long long items = (long long)a.caches * a.columns;
+    for (long long item = (long long)blockIdx.x * COMMIT_THREADS + i; item < items; item += (long long)gridDim.x * COMMIT_THREADS) {
+        const int c = (int)(item / a.columns);
+        char* cache = static_cast<char*>(a.cache[c]) + (item - (long long)c * a.columns) * 16;
+        for (int k0 = start; k0 < count; k0 += COMMIT_AT_ONCE) {
+            uint4 v[COMMIT_AT_ONCE];
 #pragma unroll
-        for (int k = 0; k < COMMIT_AT_ONCE; ++k)
-            if (k0 + k < count && from[k0 + k] >= 0) v[k] = *reinterpret_cast<const uint4*>(cache + from[k0 + k]);
+            for (int k = 0; k < COMMIT_AT_ONCE; ++k)
+                if (k0 + k < count && from[k0 + k] >= 0) v[k] = *reinterpret_cast<const uint4*>(cache + from[k0 + k]);
 #pragma unroll
-        for (int k = 0; k < COMMIT_AT_ONCE; ++k)
-            if (k0 + k < count && from[k0 + k] >= 0) *reinterpret_cast<uint4*>(cache + to[k0 + k]) = v[k];
+            for (int k = 0; k < COMMIT_AT_ONCE; ++k)
+                if (k0 + k < count && from[k0 + k] >= 0) *reinterpret_cast<uint4*>(cache + to[k0 + k]) = v[k];
+        }
     }
 }
 
@@ -299,31 +304,37 @@ fdpp_status fdpp_tree_commit(const int32_t* parents, const int32_t* tokens, cons
     int sms = 0, unused = 0;
     if ((st = query_device(&sms, &unused, &unused)) != FDPP_OK) return st;
 
-    CommitArgs a{};
-    a.parents = parents;
-    a.tokens = tokens;
-    a.choices = choices;
-    a.seq_lens = seq_lens;
-    a.cu = cu_tokens;
-    a.table = block_table;
-    a.new_lens = new_lens;
-    a.accepted = accepted;
-    a.path = path;
-    a.chosen = chosen;
-    a.err = static_cast<unsigned*>(workspace);
-    a.row_bytes = p->row_bytes;
-    a.T = p->num_tokens;
-    a.per_seq = p->num_tokens / p->batch;
-    a.max_seq_len = p->max_seq_len;
-    a.block_size = p->block_size;
-    a.max_blocks = p->max_blocks_per_seq;
-    a.num_blocks = p->num_kv_blocks;
-    a.columns = (int)(p->row_bytes / 16);
-    a.caches = num_caches;
-    for (int i = 0; i < num_caches; ++i) a.cache[i] = caches[i];
-    const long long grid = std::max(1ll, ((long long)num_caches * a.columns + COMMIT_THREADS - 1) / COMMIT_THREADS);
-    const cudaError_t e = launch_pdl(tree_commit_kernel, dim3((unsigned)grid, (unsigned)p->batch), COMMIT_THREADS,
-                                     (cudaStream_t)stream, a);
+    auto launch = [&](auto a) {
+        a.parents = parents;
+        a.tokens = tokens;
+        a.choices = choices;
+        a.seq_lens = seq_lens;
+        a.cu = cu_tokens;
+        a.table = block_table;
+        a.new_lens = new_lens;
+        a.accepted = accepted;
+        a.path = path;
+        a.chosen = chosen;
+        a.err = static_cast<unsigned*>(workspace);
+        a.row_bytes = p->row_bytes;
+        a.T = p->num_tokens;
+        a.per_seq = p->num_tokens / p->batch;
+        a.max_seq_len = p->max_seq_len;
+        a.block_size = p->block_size;
+        a.max_blocks = p->max_blocks_per_seq;
+        a.num_blocks = p->num_kv_blocks;
+        a.columns = (int)(p->row_bytes / 16);
+        a.caches = num_caches;
+        for (int i = 0; i < num_caches; ++i) a.cache[i] = caches[i];
+        // a CTA for every 256 columns, but no more than are on the GPU at once: each finds the path for itself
+        const long long all = ((long long)num_caches * a.columns + COMMIT_THREADS - 1) / COMMIT_THREADS;
+        const long long grid = std::max(1ll, std::min(all, (COMMIT_RESIDENT * (long long)sms + p->batch - 1) / p->batch));
+        return launch_pdl(tree_commit_kernel<sizeof a.cache / sizeof(void*)>, dim3((unsigned)grid, (unsigned)p->batch),
+                          COMMIT_THREADS, (cudaStream_t)stream, a);
+    };
+    const cudaError_t e = num_caches <= 16   ? launch(CommitArgs<16>{})
+                          : num_caches <= 64 ? launch(CommitArgs<64>{})
+                                             : launch(CommitArgs<FDPP_TREE_MAX_CACHES>{});
     if (e != cudaSuccess) return tfail(FDPP_ERR_CUDA, "tree commit launch: %s", cudaGetErrorString(e));
     return FDPP_OK;
 }

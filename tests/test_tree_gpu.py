@@ -68,6 +68,21 @@ def test_attention_bf16_on_the_cuda_cores():
     TreeProblem(trees_of(7, (11, 4)), (130, 20), kernel=SIMT, hq=8, hkv=2, d=128, block=16).check()
 
 
+@pytest.mark.parametrize("old", [20, 2000])
+def test_attention_kernel_chosen_by_the_library(old):
+    """Small problems on the CUDA cores, larger ones on the tensor cores: the same bits as when asked for, and a
+    workspace that fits either way."""
+    for kernel in (SIMT, F.FDPP_KERNEL_TENSOR):
+        x = TreeProblem(trees_of(15, (11, 4)), (old, 7), kernel=kernel, hq=8, hkv=2, d=128, block=16)
+        got = x.call().clone()
+        x.p.kernel = F.FDPP_KERNEL_AUTO
+        x.ws, x.simt = F.alloc_tree_workspace(x.p), old == 20          # (the bound of the kernel that is taken)
+        x.check()
+        same = torch.equal(x.call(), got)
+        torch.cuda.synchronize()
+        assert same == ((kernel == SIMT) == (old == 20))
+
+
 @pytest.mark.parametrize("hq", [2, 16])
 @pytest.mark.parametrize("what", ["k", "v"])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

@@ -53,9 +53,12 @@ def attention(x: R.Rows, trees):
 
 
 class TreeProblem(H.Problem):
-    """trees: parents of each sequence; old: keys before them; begin: first keys by row, or None."""
+    """trees: parents of each sequence; old: keys before them; begin: first keys by row, or None. bf16 takes the tensor
+    kernel unless another is asked for (left to itself the library takes the CUDA cores for small problems)."""
 
     def __init__(self, trees, old, begin=None, **kw):
+        if kw.get("kernel") is None and kw.get("dtype", "bf16") == "bf16":
+            kw["kernel"] = F.FDPP_KERNEL_TENSOR
         mask = None
         if begin is not None:
             mask = lambda row, pos, total: (begin(row, pos), 0)  # noqa: E731
