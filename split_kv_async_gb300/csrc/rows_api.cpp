@@ -158,8 +158,11 @@ fdpp_status encode_q(CUtensorMap* map, const void* q, const fdpp_rows_params& p,
     return FDPP_OK;
 }
 
-// A call with trees: the lines of ancestors lie behind the rest.
-size_t tree_bytes(const fdpp_rows_params& p) { return align256(rows_layout(p).total + (size_t)p.num_tokens * LINE_WORDS * 4); }
+// A call with trees: on the tensor cores the tokens' lineage lies behind the rest.
+size_t tree_bytes(const fdpp_rows_params& p)
+{
+    return align256(rows_layout(p).total + (tensor_kernel(p) ? (size_t)p.num_tokens * LINE_WORDS * 4 : 0));
+}
 
 fdpp_status attend(const void* q, const void* prefix_k, const void* prefix_v, const int32_t* prefix_blocks,
                    const int32_t* prefix_len, bool prefix, const void* k_cache, const void* v_cache,
@@ -251,8 +254,7 @@ fdpp_status attend(const void* q, const void* prefix_k, const void* prefix_v, co
     }
     if (!tensor_kernel(*p)) {
         a.splits = simt_splits(*p);
-        cudaError_t e = parents ? launch_lineage(a, false, s) : cudaSuccess;
-        if (e == cudaSuccess) e = launch_rows_simt(a, p->dtype, s);
+        const cudaError_t e = launch_rows_simt(a, p->dtype, s);
         if (e != cudaSuccess) return rfail(FDPP_ERR_CUDA, "rows kernel launch: %s", cudaGetErrorString(e));
         return FDPP_OK;
     }

@@ -98,9 +98,8 @@ static_assert(LINE_UP + LINE_BITS <= LINE_DOWN && LINE_DOWN + LINE_BITS <= LINE_
 
 RowsLayout rows_layout(const fdpp_rows_params& p);
 
-// The tokens' lineage, before the kernels that mask by it. after_plan: enqueued behind the tensor kernel's plan, beside
-// which it runs.
-cudaError_t launch_lineage(const RowsArgs& a, bool after_plan, cudaStream_t s);
+// The tokens' lineage for the tensor kernel: enqueued behind its plan, beside which it runs.
+cudaError_t launch_lineage(const RowsArgs& a, cudaStream_t s);
 cudaError_t launch_rows_simt(const RowsArgs& a, int dtype, cudaStream_t s);
 // Plan, tile kernel and join.
 struct RowsMaps {

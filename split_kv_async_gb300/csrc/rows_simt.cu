@@ -56,6 +56,8 @@ __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
     __shared__ float sm_o[SW][SH][D];
     __shared__ float sm_w[SH][ROWS_SIMT_MAX_SPLITS];
     __shared__ int last;
+    __shared__ int up[TREE ? FDPP_TREE_MAX_TOKENS : 1];
+    __shared__ uint32_t seen[LINE_BITS];       // with trees: the token itself and its ancestors
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = threadIdx.x / LANES, j = lane % LANES;
     const int chunks = (a.G + SH - 1) / SH;
     grid_dependency_wait();
@@ -97,9 +99,26 @@ __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
     const int pos = P + L - n + (row - c0);
     int lo, hi;
     row_keys(a, row, pos, P + L, lo, hi);
-    if (TREE && tree_too_large(a, n)) lo = hi = 0;
-    const uint32_t* line = TREE ? a.lineage + (long long)row * LINE_WORDS : nullptr;
     const int tree0 = L - n;
+    if (TREE) {
+        // the token's walk up to the root, through shared memory (each CTA its own: a launch that does it for all
+        // tokens before takes longer)
+        const bool large = tree_too_large(a, n);
+        if (large) lo = hi = 0;
+        unsigned wrong = large ? FDPP_ERRBIT_TREE : 0;
+        for (int i = threadIdx.x; i < n && !large; i += SW * 32) {
+            const int p = a.parents[c0 + i];
+            const bool ok = p >= -1 && p < i;
+            up[i] = ok ? p : -1;
+            if (!ok && i == row - c0) wrong = FDPP_ERRBIT_TREE;
+        }
+        if (threadIdx.x < LINE_BITS) seen[threadIdx.x] = 0u;
+        rows_error(a, wrong);
+        __syncthreads();
+        if (threadIdx.x == 0 && !large)
+            for (int i = row - c0; i >= 0; i = up[i]) seen[i >> 5] |= 1u << (i & 31);
+        __syncthreads();
+    }
     const int len = hi - lo;
     const int k0 = lo + (int)((long long)len * split / a.splits), k1 = lo + (int)((long long)len * (split + 1) / a.splits);
 
@@ -124,7 +143,7 @@ __global__ void __launch_bounds__(SW * 32) rows_simt_kernel(RowsArgs a)
 
 #pragma unroll 2
     for (int t = k0 + grp; t < k1; t += GROUPS) {
-        if (TREE && !line_sees(line, tree0, t)) continue;
+        if (TREE && t >= tree0 && !(seen[(t - tree0) >> 5] >> ((t - tree0) & 31) & 1u)) continue;
         const bool pre = t < P;
         const long long off = key_offset(a, pre ? -1 : b, pre ? t : t - P, g);
         if (off < 0) {

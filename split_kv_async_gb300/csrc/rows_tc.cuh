@@ -2319,7 +2319,7 @@ cudaError_t launch_d(const RowsArgs& a, const RowsMaps& m, cudaStream_t s)
     PdlConfig plan(dim3((unsigned)ranks), small ? PLAN_SMALL : PLAN_THREADS, 0, s, ranks);
     cudaError_t e = cudaLaunchKernelEx(&plan.cfg, small ? rows_plan_small_kernel : rows_plan_kernel, a);
     if (e != cudaSuccess) return e;
-    if (TREE && (e = launch_lineage(a, true, s)) != cudaSuccess) return e;
+    if (TREE && (e = launch_lineage(a, s)) != cudaSuccess) return e;
     auto kern = rows_tile_kernel<D, MODE, TREE>;
     const int smem = RowsSmem<D>(a.stages).total;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;

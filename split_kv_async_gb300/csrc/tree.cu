@@ -15,17 +15,15 @@ constexpr int TREE = FDPP_TREE_MAX_TOKENS;
 // A CTA per sequence, a thread per node: it walks up to the root through shared memory, sets a bit for each
 // node that it passes, and its own bit with each of them.
 //
-// AFTER_PLAN: on the stream behind the plan, which starts it as soon as what came before the plan has completed. So it
+// It lies on the stream behind the plan, which starts it as soon as what came before the plan has completed. So it
 // does its work first, beside the plan (its reads go past the L1 cache), and then waits for the plan: the kernel
 // behind it waits for it alone. It adds nothing to most calls then (as a launch of its own before the plan 2 to 3 us).
-template <bool AFTER_PLAN>
 __global__ void __launch_bounds__(TREE) lineage_kernel(const __grid_constant__ RowsArgs a)
 {
     __shared__ int up[TREE];
     constexpr int ROW = 1 + 2 * LINE_BITS;               // (an odd number of words: no two rows in one bank)
     __shared__ uint32_t line[TREE * ROW];                // the tree's first key, ancestors, descendants
     const int b = blockIdx.x, i = threadIdx.x;
-    if (!AFTER_PLAN) grid_dependency_wait();
     grid_launch_dependents();
     int c0 = b * a.per_seq, n = a.per_seq;
     if (a.cu) {
@@ -59,7 +57,7 @@ __global__ void __launch_bounds__(TREE) lineage_kernel(const __grid_constant__ R
         }
     }
     rows_error(a, bad);
-    if (AFTER_PLAN) grid_dependency_wait();
+    grid_dependency_wait();
 }
 
 // ---- commit -------------------------------------------------------------------------------
@@ -250,9 +248,9 @@ bool repeated(void* const* p, int n)
 
 }  // namespace
 
-cudaError_t launch_lineage(const RowsArgs& a, bool after_plan, cudaStream_t s)
+cudaError_t launch_lineage(const RowsArgs& a, cudaStream_t s)
 {
-    return launch_pdl(after_plan ? lineage_kernel<true> : lineage_kernel<false>, dim3((unsigned)a.B), TREE, s, a);
+    return launch_pdl(lineage_kernel, dim3((unsigned)a.B), TREE, s, a);
 }
 
 }  // namespace fdpp

@@ -60,13 +60,14 @@ def test_tree_rejects_bad_parameters(kw):
 def test_tree_workspace(dtype):
     p = _params(dtype=dtype)
     n = F.fdpp_tree_workspace_size(p)
-    assert n >= 10 * 4 * (1 + 2 * F.FDPP_TREE_MAX_TOKENS // 32)
     p.kernel = F.FDPP_KERNEL_SIMT
     assert n == F.fdpp_tree_workspace_size(p)                          # (few keys: the CUDA cores by themselves)
     p.max_seq_len = 100000
     if dtype == F.FDPP_BF16:
         p.kernel = F.FDPP_KERNEL_TENSOR
     large = F.fdpp_tree_workspace_size(p)
+    # (the tensor kernel keeps each token's line of ancestors and descendants)
+    assert large >= F.fdpp_rows_workspace_size(p) + (10 * 4 * (1 + 2 * F.FDPP_TREE_MAX_TOKENS // 32) if dtype == F.FDPP_BF16 else 0)
     p.kernel = F.FDPP_KERNEL_AUTO
     assert F.fdpp_tree_workspace_size(p) == large
     p.max_seq_len = 100
