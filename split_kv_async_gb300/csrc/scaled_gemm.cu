@@ -16,7 +16,7 @@
 // distributed shared memory, in range order.
 //
 // What bounds it. Few rows: HBM (28672 x 4096 weights: 8 rows 21 us, 0.84 of a measured copy, 64 rows 25), and for small
-// weights the start and the end of a CTA (4096 x 4096, 8 rows: 6.1 us in a graph, of which the bytes take 2.5). Many rows: the
+// weights the start and the end of a CTA (4096 x 4096, 8 rows: 5.8 us in a graph, of which the bytes take 2.5). Many rows: the
 // hand-over between the tensor cores and the sums. 8192 x 28672 x 4096 takes 680 us, 2.8 PFLOP/s; the MMAs alone, on
 // data that lies there, 4.6, with the loads 3.5 to 3.7 (128 bytes of shared memory a cycle, written and read). Two buffers of
 // 256 columns are all the tensor memory, so a block's sums have the 512 cycles of the next block's MMAs from the commit to the
@@ -44,7 +44,7 @@ namespace {
 constexpr int SB = FDPP_SCALE_BLOCK;     // channels of a block: one 128-byte swizzle row
 constexpr int SG_N = 128;                // weight rows that share a scale; the rows kernel's weight tile
 constexpr int SG_ROWS = 128;             // the tile kernel's rows of x in a CTA
-constexpr int SG_GROUP = 64;             // most rows of x of the rows kernel
+constexpr int SG_GROUP = 64, SG_FEW = 48;    // most rows of x that the rows kernel takes, and that it always takes
 constexpr int SG_MAX_SPLIT = 8;          // K ranges per weight tile (a portable cluster)
 constexpr int SG_MAX_STAGES = 8;
 
@@ -880,16 +880,23 @@ int max_clusters(SgKernel kern, int split, int threads, int smem)
     return n;
 }
 
-// Ranges of K for `tiles` output tiles: as many as keep all clusters on the GPU at once, two blocks each at least.
-int choose_split(SgKernel kern, long long tiles, int kb, int threads, int smem)
+// Ranges of K for `tiles` output tiles: as many as keep all clusters on the GPU at once. The driver's count of resident
+// clusters takes a kernel with tensor memory for one CTA per SM; of the rows kernel, whose CTAs share an SM by two, twice
+// as many fit, and as many as there are places for clusters of half the size. (8 rows, us: 4096 x 4096, 32 tiles, in 4 ranges
+// 7.8, in 8 6.7; 6144 x 4096, 48 tiles, in 4 8.3, in 5 8.2, in 6, which do not fit, 13.9; 4096 x 14336 in 4 15.4, in 8 12.4.)
+int choose_split(SgKernel kern, long long tiles, int kb, int threads, int smem, int ctas_per_sm, int sms)
 {
-    for (int n = std::min(SG_MAX_SPLIT, kb / 2); n > 1; --n)
-        if (tiles <= max_clusters(kern, n, threads, smem)) return n;
+    for (int n = std::min(SG_MAX_SPLIT, kb); n > 1; --n) {
+        if (tiles * n > (long long)ctas_per_sm * sms) continue;
+        int fit = max_clusters(kern, n, threads, smem);
+        if (ctas_per_sm == 2) fit = std::max(2 * fit, n > 2 ? max_clusters(kern, (n + 1) / 2, threads, smem) : 0);
+        if (tiles <= fit) return n;
+    }
     return 1;
 }
 
-fdpp_status launch_rows(const fdpp_scaled_gemm_params& p, ScaledArgs& g, const void* x, const void* w, int smem_sm, int smem_blk,
-                        cudaStream_t s)
+fdpp_status launch_rows(const fdpp_scaled_gemm_params& p, ScaledArgs& g, const void* x, const void* w, int sms, int smem_sm,
+                        int smem_blk, cudaStream_t s)
 {
     g.Mp = (p.M + 15) / 16 * 16;
     g.nstage = rows_stages(g.Mp, smem_sm, smem_blk);
@@ -897,7 +904,7 @@ fdpp_status launch_rows(const fdpp_scaled_gemm_params& p, ScaledArgs& g, const v
     const SgKernel kern = p.out_dtype == FDPP_F32 ? rows_kernel<float>(g.Mp) : rows_kernel<__nv_bfloat16>(g.Mp);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return sfail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    g.split_k = p.split_k ? p.split_k : choose_split(kern, tiles, g.kb, R_THREADS, smem);
+    g.split_k = p.split_k ? p.split_k : choose_split(kern, tiles, g.kb, R_THREADS, smem, 2, sms);
     CUtensorMap tw, tx;
     fdpp_status st;
     if ((st = encode_rows(&tw, w, p.N, p.K, p.w_stride, SG_N)) != FDPP_OK) return st;
@@ -943,7 +950,7 @@ fdpp_status launch_tile(const fdpp_scaled_gemm_params& p, ScaledArgs& g, const v
         const SgKernel split = scaled_tile_kernel<T, BN, PAIR, true>;
         if ((e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
             return sfail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-        g.split_k = p.split_k ? p.split_k : choose_split(split, m_tiles * n_tiles, g.kb, threads, smem);
+        g.split_k = p.split_k ? p.split_k : choose_split(split, m_tiles * n_tiles, g.kb, threads, smem, 1, sms);
         if (g.split_k > 1) kern = split;
     }
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
@@ -981,7 +988,7 @@ size_t fdpp_scaled_gemm_workspace_size(const fdpp_scaled_gemm_params* p) { retur
 fdpp_status fdpp_scaled_gemm(const void* x, const float* x_scales, const void* w, const float* w_scales,
                              const fdpp_scaled_gemm_params* p, void* workspace, size_t workspace_bytes, void* y,
                              fdpp_stream stream)
-{
+try {
     fdpp_status st = check_params(p);
     if (st != FDPP_OK) return st;
     if (!x || !x_scales || !w || !w_scales || !y) return sfail(FDPP_ERR_INVALID_ARG, "x, w, their scales and y must be non-NULL");
@@ -1007,10 +1014,11 @@ fdpp_status fdpp_scaled_gemm(const void* x, const float* x_scales, const void* w
     g.kb = blocks_of(p->K);
     cudaStream_t s = (cudaStream_t)stream;
     // Few rows: the rows kernel pads them least, the tile kernel's CTAs split K with less to add up. us a call, rows
-    // kernel against tile kernel: 32 rows of 4096 x 4096 6.9 and 7.8, of 28672 x 4096 21.9 and 30.9, of 4096 x 14336 17.0
-    // and 15.0; 64 rows 8.2 and 7.9, 25.4 and 31.6, 19.1 and 15.1. With weight tiles for all SMs it keeps the advantage.
+    // kernel against tile kernel: 48 rows of 4096 x 4096 7.9 and 7.8, of 6144 x 4096 9.1 and 10.0, of 4096 x 14336 14.4
+    // and 15.2; 64 rows 8.9 and 7.9, 10.3 and 10.5, 15.8 and 15.3. With weight tiles for all SMs it keeps the advantage (64
+    // rows of 28672 x 4096: 25.3 and 31.6).
     const int w_tiles = (int)((p->N + SG_N - 1ll) / SG_N);
-    if (p->M <= 32 || (p->M <= SG_GROUP && w_tiles >= sms)) return launch_rows(*p, g, x, w, smem_sm, smem_blk, s);
+    if (p->M <= SG_FEW || (p->M <= SG_GROUP && w_tiles >= sms)) return launch_rows(*p, g, x, w, sms, smem_sm, smem_blk, s);
     // Pairs of CTAs on 256 x 256 tiles where these alone are enough for all SMs, else 128 x 128 ones.
     const long long tiles = ((p->M + 255ll) / 256) * ((p->N + 255ll) / 256);
     const bool big = tiles >= sms / 2;
@@ -1019,6 +1027,8 @@ fdpp_status fdpp_scaled_gemm(const void* x, const float* x_scales, const void* w
                    : launch_tile<float, 128, false>(*p, g, x, w, sms, smem_blk, s);
     return big ? launch_tile<__nv_bfloat16, 256, true>(*p, g, x, w, sms, smem_blk, s)
                : launch_tile<__nv_bfloat16, 128, false>(*p, g, x, w, sms, smem_blk, s);
+} catch (...) {                          // (the cache of cluster counts allocates)
+    return sfail(FDPP_ERR_CUDA, "out of host memory");
 }
 
 }  // extern "C"
