@@ -232,7 +232,7 @@ cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t s)
         kern = vectors <= 32   ? rms_norm_kernel<T, E4M3, 1, true>
                : vectors <= 64 ? rms_norm_kernel<T, E4M3, 2, true>
                                : rms_norm_kernel<T, E4M3, 4, true>;
-        grid = (unsigned)std::min((a.T + NORM_WARP_ROWS - 1) / NORM_WARP_ROWS, 8 * sms);
+        grid = (unsigned)std::min((a.T - 1) / NORM_WARP_ROWS + 1, 8 * sms);
         threads = 32 * NORM_WARP_ROWS;
     } else {
         // Channels a thread holds, by what was fastest on 2^27 bf16 elements into e4m3: rows of 4096 in 512 threads of 8

@@ -758,11 +758,11 @@ __global__ void __launch_bounds__(TileSmem<BN, PAIR>::THREADS, 1)
     if constexpr (SPLIT) {
         // every thread of every member passes both cluster barriers, whatever happened before
         cluster_sync_all();
-        if (!*abort_) {
+        if (!*abort_ && warp >= 4) {                     // (the warps that have the registers for it)
             int mt, nt;
             tile_at(g, first, mt, nt);
             const int r0 = ks * SG_ROWS / g.split_k, r1 = (ks + 1) * SG_ROWS / g.split_k;
-            for (int i = r0 * (BN / 4) + (int)threadIdx.x; i < r1 * (BN / 4); i += L::THREADS) {
+            for (int i = r0 * (BN / 4) + (int)threadIdx.x - 128; i < r1 * (BN / 4); i += L::THREADS - 128) {
                 const int row = i / (BN / 4), piece = i % (BN / 4), m = mt * SG_ROWS + row, n = nt * BN + 4 * piece;
                 if (m >= g.M || n >= g.N) continue;
                 const uint32_t off = sbase + (uint32_t)((row * BN + ((piece ^ (row & 7)) << 2)) * 4);

@@ -311,3 +311,51 @@ def test_norm_into_linear_on_another_stream_and_in_a_graph():
     torch.cuda.synchronize()
     check()
     assert F.fdpp_read_error(ws) == 0
+
+
+def test_linear_two_streams_with_one_workspace():
+    """The workspace holds the error word alone: calls at once may share it."""
+    problems = [linear_problem(M, 1500, 2048, seed) for M, seed in ((8, 1), (300, 2))]
+    want = [run_linear(*p, out="f32") for p in problems]
+    params = [F.make_scaled_gemm_params(M=p[0].shape[0], N=1500, K=2048, out_dtype=F.FDPP_F32) for p in problems]
+    ws = F.alloc_scaled_gemm_workspace(params[0])
+    y = [torch.zeros_like(w) for w in want]
+    streams = [torch.cuda.Stream() for _ in problems]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for p, q, o, s in zip(problems, params, y, streams):
+            F.fdpp_scaled_gemm(*p, q, ws, o, stream=s)
+    assert F.fdpp_read_error(ws) == 0
+    assert all(bool(same(a, b).all()) for a, b in zip(y, want))
+
+
+@pytest.mark.parametrize("M,N", [(70000, 32768), (40, (1 << 31) // 40 + 128)])
+def test_linear_outputs_beyond_32_bits(M, N):
+    x, sx, w, sw = linear_problem(M, N, 16)
+    y = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    p = F.make_scaled_gemm_params(M=M, N=N, K=16)
+    ws = F.alloc_scaled_gemm_workspace(p)
+    F.fdpp_scaled_gemm(x, sx, w, sw, p, ws, y)
+    assert F.fdpp_read_error(ws) == 0
+    for rows in (slice(0, 3), slice(M - 3, M)):
+        for cols in (slice(0, 256), slice(N // 256 * 256 - 256, N)):
+            first = cols.start // 128
+            want, size = linear_reference(x[rows], sx[rows], w[cols], sw[first:])
+            got = y[rows, cols].double()
+            assert torch.equal(got.isnan(), want.isnan())
+            assert bool(((got - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -15 * size).nan_to_num(1).logical_or(want.isnan()).all())
+
+
+def test_norm_of_more_than_32_bits_of_elements():
+    T, dim = 70000, 32768
+    x = torch.randn(T, 1, device="cuda").bfloat16().expand(T, dim).contiguous()
+    x[:, ::3] *= -2
+    p = F.make_norm_params(num_tokens=T, dim=dim, dtype=F.FDPP_BF16, out_dtype=F.FDPP_E4M3)
+    out, scales = torch.zeros(T, dim, device="cuda", dtype=torch.uint8), torch.zeros(T, dim // 128, device="cuda")
+    F.fdpp_rms_norm(x, None, None, p, out, scales)
+    torch.cuda.synchronize()
+    for rows in (slice(0, 5), slice(T - 5, T)):
+        _, y = norm_reference(x[rows], None, None, 1e-6, 0.0)
+        each = scales[rows].double().repeat_interleave(128, 1)
+        got = e4m3(out[rows]).double() * each
+        assert bool(((got - y).abs() <= (2.0 ** -4 + 2.0 ** -16) * y.abs() + 2.0 ** -10 * each).all())

@@ -357,3 +357,37 @@ def test_commit_captured_on_another_stream():
     x.choices = [list(map(int, c)) for c in x.choices]
     graph.replay()
     x.check()
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_commit_in_caches_beyond_32_bits(paged):
+    """Rows that lie more than 2^32 bytes into a cache."""
+    row, keys = 1024, (1 << 32) // 2048 + 4096
+    kw = dict(block_size=256, max_blocks_per_seq=1, num_kv_blocks=keys // 256) if paged else {}
+    cache = torch.zeros(keys, row, dtype=torch.bfloat16, device="cuda")
+    n, parents, path = 6, [-1, 0, 0, 2, 2, 4], [0, 2, 4, 5]
+    L = 250 if paged else keys - 3
+    base = (keys // 256 - 1) * 256 + L - n if paged else L - n          # the last block, or the end of the one sequence
+    cache[base:base + n] = torch.arange(1, n + 1, device="cuda")[:, None].to(torch.bfloat16)
+    p = F.make_commit_params(batch=1, num_tokens=n, max_seq_len=256 if paged else keys, row_bytes=2 * row, **kw)
+    ws, out = F.alloc_commit_workspace(p), [ints([0]), ints([0]), ints([0] * n), ints([0] * n)]
+    tokens = ints([1 if i in path else 2 for i in range(n)])
+    F.fdpp_tree_commit(ints(parents), tokens, ints([1] * n), ints([L]), None, ints([[keys // 256 - 1]]) if paged else None,
+                       F.make_cache_list([cache]), p, ws, *out)
+    torch.cuda.synchronize()
+    assert F.fdpp_read_error(ws) == 0 and out[1].item() == 4 and out[2].tolist() == path + [-1, -1]
+    assert cache[base:base + n, ::97].float().mean(1).tolist() == [1, 3, 5, 6, 5, 6]
+    assert int(torch.count_nonzero(cache[:4096])) == 0
+
+
+def test_attention_two_streams():
+    xs = [TreeProblem(trees_of(40 + i, (9, 30), 3), (200, 77), hq=8, hkv=2, d=64 * (i + 1), block=16) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for x, s in zip(xs, streams):
+            x.call(stream=s)
+    torch.cuda.synchronize()
+    for x in xs:
+        assert F.fdpp_read_error(x.ws) == 0
+        x.check(x.out)
