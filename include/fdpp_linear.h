@@ -59,7 +59,7 @@ typedef struct fdpp_norm_params {
  *   out          DEVICE [T][dim] of out_dtype. May be x where the types and strides are the same.
  *   scales       DEVICE float [T][ceil(dim / 128)], 4-byte aligned (E4M3); otherwise NULL.
  *   sum_out      DEVICE [T][dim], or NULL. May be residual or x where the strides are the same.
- * Otherwise the buffers do not overlap. */
+ * Otherwise the buffers do not overlap. With T = 0 they may be NULL. */
 fdpp_status fdpp_rms_norm(const void* x, const void* residual, const void* weight, const fdpp_norm_params* p,
                           void* out, float* scales, void* sum_out, fdpp_stream stream);
 
@@ -89,7 +89,7 @@ size_t fdpp_scaled_gemm_workspace_size(const fdpp_scaled_gemm_params* p);
  *   workspace  DEVICE, 256-byte aligned, >= 256 bytes, zeroed before its first use (it collects the
  *              calls' error bits; read them with fdpp_read_error of fdpp_cache.h).
  *   y          DEVICE [M][N] of out_dtype, aligned to its elements (stores are wider where y and its rows
- *              are 16-byte aligned). */
+ *              are 16-byte aligned). With M = 0 it, x and x_scales may be NULL. */
 fdpp_status fdpp_scaled_gemm(const void* x, const float* x_scales, const void* w, const float* w_scales,
                              const fdpp_scaled_gemm_params* p, void* workspace, size_t workspace_bytes, void* y,
                              fdpp_stream stream);

@@ -96,7 +96,8 @@ size_t fdpp_commit_workspace_size(const fdpp_commit_params* p);
  *                or a pool [num_kv_blocks][block_size][row_bytes]. The pointers are copied by the call. No
  *                two sequences share a block that holds drafted tokens.
  *   workspace    DEVICE, 256-byte aligned, >= 256 bytes, zeroed before its first use.
- *   new_lens     DEVICE int32 [B], written: base + a. Not seq_lens itself.
+ *   new_lens     DEVICE int32 [B], written: base + a (a sequence of which nothing is accepted for its length or
+ *                its tree: L, kept in 0 .. max_seq_len). Not seq_lens itself.
  *   accepted     DEVICE int32 [B], written: a (0 for a sequence without tokens).
  *   path         DEVICE int32 [T], written: row k of a sequence has the path's node k, or -1 from a on.
  *   chosen       DEVICE int32 [T], written: choices of that node, or -1: the tokens that the step adds.

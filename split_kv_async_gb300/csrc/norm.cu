@@ -284,19 +284,21 @@ extern "C" fdpp_status fdpp_rms_norm(const void* x, const void* residual, const 
     if (!stride_ok(p->x_stride, vec) || !stride_ok(p->out_stride, out_vec) ||
         (residual && !stride_ok(p->residual_stride, vec)) || (sum_out && !stride_ok(p->sum_stride, vec)))
         return nfail(FDPP_ERR_INVALID_ARG, "strides must cover a row and be multiples of 16 bytes (an e4m3 output's: of 8)");
-    if (!x || !out) return nfail(FDPP_ERR_INVALID_ARG, "x and out must be non-NULL");
+    const bool some = p->num_tokens > 0;     // (an empty tensor's address may be NULL)
+    if (some && (!x || !out)) return nfail(FDPP_ERR_INVALID_ARG, "x and out must be non-NULL");
     if (((uintptr_t)x | (uintptr_t)residual | (uintptr_t)weight | (uintptr_t)out | (uintptr_t)sum_out) % 16 != 0)
         return nfail(FDPP_ERR_INVALID_ARG, "x, residual, weight, out and sum_out must be 16-byte aligned");
     if (e4m3) {
-        if (!scales || (uintptr_t)scales % 4 != 0)
+        if ((some && !scales) || (uintptr_t)scales % 4 != 0)
             return nfail(FDPP_ERR_INVALID_ARG, "an e4m3 output needs scales, 4-byte aligned");
         if (p->scale_stride < (p->dim + FDPP_SCALE_BLOCK - 1) / FDPP_SCALE_BLOCK || p->scale_stride > most)
             return nfail(FDPP_ERR_INVALID_ARG, "scale_stride must cover a row's scales");
     } else if (scales) {
         return nfail(FDPP_ERR_INVALID_ARG, "scales are of an e4m3 output only");
     }
-    if ((out == x && (e4m3 || p->out_stride != p->x_stride)) || (sum_out && sum_out == x && p->sum_stride != p->x_stride) ||
-        (sum_out && sum_out == residual && p->sum_stride != p->residual_stride) || out == residual || out == sum_out)
+    if (some &&
+        ((out == x && (e4m3 || p->out_stride != p->x_stride)) || (sum_out && sum_out == x && p->sum_stride != p->x_stride) ||
+         (sum_out && sum_out == residual && p->sum_stride != p->residual_stride) || out == residual || out == sum_out))
         return nfail(FDPP_ERR_INVALID_ARG, "out may be x, and sum_out residual or x, where types and strides are the same");
     int sms = 0, unused = 0;
     const fdpp_status st = query_device(&sms, &unused, &unused);

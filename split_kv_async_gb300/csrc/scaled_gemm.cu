@@ -880,7 +880,7 @@ int max_clusters(SgKernel kern, int split, int threads, int smem)
     return n;
 }
 
-// Ranges of K for `tiles` output tiles: as many as keep all clusters on the GPU at once. The driver's count of resident
+// Ranges of K for `tiles` output tiles: as many as keep all clusters on the GPU at once. The query for resident
 // clusters takes a kernel with tensor memory for one CTA per SM; of the rows kernel, whose CTAs share an SM by two, twice
 // as many fit, and as many as there are places for clusters of half the size. (8 rows, us: 4096 x 4096, 32 tiles, in 4 ranges
 // 7.8, in 8 6.7; 6144 x 4096, 48 tiles, in 4 8.3, in 5 8.2, in 6, which do not fit, 13.9; 4096 x 14336 in 4 15.4, in 8 12.4.)
@@ -991,7 +991,8 @@ fdpp_status fdpp_scaled_gemm(const void* x, const float* x_scales, const void* w
 try {
     fdpp_status st = check_params(p);
     if (st != FDPP_OK) return st;
-    if (!x || !x_scales || !w || !w_scales || !y) return sfail(FDPP_ERR_INVALID_ARG, "x, w, their scales and y must be non-NULL");
+    if (!w || !w_scales || (p->M > 0 && (!x || !x_scales || !y)))    // (an empty tensor's address may be NULL)
+        return sfail(FDPP_ERR_INVALID_ARG, "x, w, their scales and y must be non-NULL");
     if (((uintptr_t)x | (uintptr_t)w) % 16 != 0) return sfail(FDPP_ERR_INVALID_ARG, "x and w must be 16-byte aligned");
     if (((uintptr_t)x_scales | (uintptr_t)w_scales) % 4 != 0) return sfail(FDPP_ERR_INVALID_ARG, "scales must be 4-byte aligned");
     if ((uintptr_t)y % (p->out_dtype == FDPP_F32 ? 4 : 2) != 0) return sfail(FDPP_ERR_INVALID_ARG, "y must be aligned to its elements");

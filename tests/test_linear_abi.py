@@ -102,3 +102,10 @@ def test_gemm_workspace_errors_and_calls_that_pass():
     for kw in ({}, dict(M=0), dict(M=5000), dict(split_k=3), dict(y=FAKE + 2), dict(y_stride=1001), dict(x_stride=1024, w_stride=288),
                dict(K=16)):
         assert _gemm(**kw) == F.FDPP_ERR_CUDA      # as far as the device query
+
+
+def test_calls_on_empty_tensors_pass_without_addresses():
+    assert _norm(num_tokens=0, x=None, residual=None, out=None, total=None) == F.FDPP_ERR_CUDA
+    assert _norm(num_tokens=0, x=None, residual=None, out=None, total=None, out_dtype=F.FDPP_E4M3) == F.FDPP_ERR_CUDA
+    assert _gemm(M=0, x=None, sx=None, y=None) == F.FDPP_ERR_CUDA
+    assert _gemm(M=0, w=None) == F.FDPP_ERR_INVALID_ARG

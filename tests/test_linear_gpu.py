@@ -359,3 +359,20 @@ def test_norm_of_more_than_32_bits_of_elements():
         each = scales[rows].double().repeat_interleave(128, 1)
         got = e4m3(out[rows]).double() * each
         assert bool(((got - y).abs() <= (2.0 ** -4 + 2.0 ** -16) * y.abs() + 2.0 ** -10 * each).all())
+
+
+@pytest.mark.parametrize("dtype", [F.FDPP_F32, F.FDPP_E4M3])
+def test_empty_tensors(dtype):
+    """Tensors of no rows, whose address is NULL, through both calls."""
+    t = torch.bfloat16 if dtype == F.FDPP_E4M3 else torch.float32
+    x = torch.empty(0, 256, device="cuda", dtype=t)
+    out = torch.empty(0, 256, device="cuda", dtype=torch.uint8 if dtype == F.FDPP_E4M3 else t)
+    scales = torch.empty(0, 2, device="cuda") if dtype == F.FDPP_E4M3 else None
+    F.fdpp_rms_norm(x, None, None, F.make_norm_params(num_tokens=0, dim=256, dtype=F.FDPP_BF16 if dtype == F.FDPP_E4M3 else dtype,
+                                                      out_dtype=dtype), out, scales)
+    _, _, w, sw = linear_problem(1, 64, 256)
+    p = F.make_scaled_gemm_params(M=0, N=64, K=256)
+    ws = F.alloc_scaled_gemm_workspace(p)
+    e = torch.empty(0, 256, device="cuda", dtype=torch.uint8)
+    F.fdpp_scaled_gemm(e, torch.empty(0, 2, device="cuda"), w, sw, p, ws, torch.empty(0, 64, device="cuda", dtype=torch.bfloat16))
+    assert F.fdpp_read_error(ws) == 0
