@@ -15,7 +15,7 @@
 // Where the tiles are too few for the GPU, K is cut into ranges whose CTAs form a cluster and add their sums through
 // distributed shared memory, in range order.
 //
-// What bounds it. Few rows: HBM (28672 x 4096 weights: 8 rows 21 us, 0.84 of a measured copy, 64 rows 25), and for small
+// What bounds it. Few rows: HBM (28672 x 4096 weights: 8 rows 19.9 us, 0.88 of a measured copy, 64 rows 22.3), and for small
 // weights the start and the end of a CTA (4096 x 4096, 8 rows: 5.8 us in a graph, of which the bytes take 2.5). Many rows: the
 // hand-over between the tensor cores and the sums. 8192 x 28672 x 4096 takes 680 us, 2.8 PFLOP/s; the MMAs alone, on
 // data that lies there, 4.6, with the loads 3.5 to 3.7 (128 bytes of shared memory a cycle, written and read). Two buffers of
@@ -44,7 +44,7 @@ namespace {
 constexpr int SB = FDPP_SCALE_BLOCK;     // channels of a block: one 128-byte swizzle row
 constexpr int SG_N = 128;                // weight rows that share a scale; the rows kernel's weight tile
 constexpr int SG_ROWS = 128;             // the tile kernel's rows of x in a CTA
-constexpr int SG_GROUP = 64, SG_FEW = 48;    // most rows of x that the rows kernel takes, and that it always takes
+constexpr int SG_GROUP = 64;             // most rows of x that the rows kernel takes
 constexpr int SG_MAX_SPLIT = 8;          // K ranges per weight tile (a portable cluster)
 constexpr int SG_MAX_STAGES = 8;
 
@@ -243,7 +243,12 @@ __device__ __forceinline__ void store_sum4(const ScaledArgs& g, const float4 (&t
 
 // ---- rows kernel --------------------------------------------------------------------------
 
-constexpr int R_THREADS = 192;           // producer warp, MMA warp, 4 warps that scale and add
+constexpr int R_THREADS = 64;            // producer warp, MMA warp; then 128 threads that scale and add for every R_COLS rows of x
+// (A block's sums follow one another, 64 rows of x in four warps at 700 ns a block: 64 rows of 20480 x 4096 took 24.2 us,
+// of 28672 x 4096 24.7; with eight warps 20.8 and 22.3, with sixteen, which 56 registers leave spilling, 28.1 and 29.7. Half as many readings
+// of x, by CTAs of 256 weight rows, saved nothing: 25.5.)
+constexpr int R_COLS = 32;
+__host__ __device__ constexpr int rows_sets(int nr) { return nr < R_COLS ? 1 : nr / R_COLS; }
 constexpr int R_SCALES = 8;              // blocks of K whose scales are loaded together
 constexpr int RW_BYTES = SG_N * SB;      // weight slice of a stage
 
@@ -251,13 +256,14 @@ constexpr int RW_BYTES = SG_N * SB;      // weight slice of a stage
 // then the scales of 16 blocks, the barriers, the TMEM address and the abort flag. Once every MMA has
 // completed, the stages hold this CTA's fp32 sums [M][128] for the cluster's reduction.
 template <typename T, int NR>
-__global__ void __launch_bounds__(R_THREADS, 2)
+__global__ void __launch_bounds__(R_THREADS + 128 * rows_sets(NR), 2)
     scaled_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                        const ScaledArgs g)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(sm);
+    constexpr int SETS = rows_sets(NR), C = NR / SETS;     // C: rows of x whose sums a warp has (Mp is above NR - C)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int stage_bytes = RW_BYTES + g.Mp * SB;
     float* scale = reinterpret_cast<float*>(sm + g.nstage * stage_bytes);        // [2 R_SCALES][SG_GROUP]
@@ -282,7 +288,7 @@ __global__ void __launch_bounds__(R_THREADS, 2)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf + 8 * b, 1);
-            mbar_init(acce + 8 * b, 4);
+            mbar_init(acce + 8 * b, 4 * SETS);
         }
         *abort_ = 0;
         fence_mbar_init();
@@ -352,43 +358,50 @@ __global__ void __launch_bounds__(R_THREADS, 2)
     } else {
         grid_dependency_wait();
         // ---- TMEM lanes 32 (warp % 4) .. hold weight rows n0 + that lane ----
-        const int q = warp & 3, t = threadIdx.x - 64;
+        const int q = warp & 3, t = threadIdx.x - R_THREADS, c0 = C * (t >> 7);
         const int n = n0 + 32 * q + lane;
-        const uint32_t trow = tmem + ((uint32_t)(32 * q) << 16);
-        const float* sx = g.sx + (long long)t * g.sx_stride;
-        const float* sw = g.sw + (long long)tile * g.kb;
-        float acc[NR];
+        const uint32_t trow = tmem + ((uint32_t)(32 * q) << 16) + c0;
+        // the scales of R_SCALES blocks at a time, loaded as many blocks ahead, since a load takes longer than a block's MMAs
+        // while the ring keeps the memory busy: this thread's are those of rows
+        // t / R_SCALES, + APART in block t % R_SCALES
+        constexpr int PER = C / 16, APART = 128 * SETS / R_SCALES;
+        const int row = t / R_SCALES, j0 = t % R_SCALES;
+        const float* sx = g.sx + (long long)row * g.sx_stride + kb0 + j0;
+        const float* sw = g.sw + (long long)tile * g.kb + kb0 + j0;
+        float acc[C];
 #pragma unroll
-        for (int j = 0; j < NR; ++j) acc[j] = 0.f;
-        // the scales of eight blocks at a time, loaded eight blocks ahead: a load takes longer than a block's
-        // MMAs while the ring keeps the memory busy
-        float next[R_SCALES];
+        for (int j = 0; j < C; ++j) acc[j] = 0.f;
+        float next[PER];
+        auto load = [&](int k) {
 #pragma unroll
-        for (int j = 0; j < R_SCALES; ++j) next[j] = t < g.M && j < nkb ? sx[kb0 + j] * sw[kb0 + j] : 0.f;
+            for (int u = 0; u < PER; ++u)
+                next[u] = row + APART * u < g.M && k + j0 < nkb ? sx[APART * u * g.sx_stride + k] * sw[k] : 0.f;
+        };
+        load(0);
         bool ok = true;
         for (int i = 0; i < nkb; ++i) {
             const int b = i & 1;
             if (i % R_SCALES == 0) {
-                float* to = scale + (i / R_SCALES & 1) * R_SCALES * SG_GROUP + t;
-                if (t < SG_GROUP)
+                float* to = scale + (i / R_SCALES & 1) * R_SCALES * SG_GROUP + j0 * SG_GROUP + row;
 #pragma unroll
-                    for (int j = 0; j < R_SCALES; ++j) to[j * SG_GROUP] = next[j];
-                named_bar_sync(1, 128);  // (this half was last read before the barrier eight blocks ago)
-#pragma unroll
-                for (int j = 0; j < R_SCALES; ++j) {
-                    const int k = i + R_SCALES + j;
-                    next[j] = t < g.M && k < nkb ? sx[kb0 + k] * sw[kb0 + k] : 0.f;
-                }
+                for (int u = 0; u < PER; ++u) to[APART * u] = next[u];
+                named_bar_sync(1, 128 * SETS);   // (this half was last read before the barrier R_SCALES blocks ago)
+                load(i + R_SCALES);
             }
-            const float* sc = scale + (i % (2 * R_SCALES)) * SG_GROUP;
+            const float* sc = scale + (i % (2 * R_SCALES)) * SG_GROUP + c0;
             ok = gwait(accf + 8 * b, (uint32_t)(i >> 1), abort_, g.err) && ok;
             if (ok) {
                 tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < NR; c += 16) {
-                    if (c >= g.Mp) break;
+                for (int c = 0; c < C; c += 16) {
+                    if (c0 + c >= g.Mp) break;
                     float v[16];
                     tmem_ld16w(trow + b * g.Mp + c, v);
+                    if (c + 16 == C || c0 + c + 16 >= g.Mp) {    // the buffer is read out
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(acce + 8 * b);
+                    }
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
                         const float4 s = *reinterpret_cast<const float4*>(sc + c + j);
@@ -398,9 +411,6 @@ __global__ void __launch_bounds__(R_THREADS, 2)
                         acc[c + j + 3] = fmaf(v[j + 3], s.w, acc[c + j + 3]);
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(acce + 8 * b);
             }
         }
         // the tensor cores' reads of the stages are complete (the last block's barrier); the sums of a
@@ -410,11 +420,11 @@ __global__ void __launch_bounds__(R_THREADS, 2)
         T* y = static_cast<T*>(g.y);
         if (ok) {
 #pragma unroll
-            for (int j = 0; j < NR; ++j) {
+            for (int j = 0; j < C; ++j) {
                 const float v = acc[j];
-                if (j < g.M) {
-                    if (g.split_k > 1) red[j * SG_N + 32 * q + lane] = v;
-                    else if (n < g.N) store_y(y + (long long)j * g.y_stride + n, v);
+                if (c0 + j < g.M) {
+                    if (g.split_k > 1) red[(c0 + j) * SG_N + 32 * q + lane] = v;
+                    else if (n < g.N) store_y(y + (long long)(c0 + j) * g.y_stride + n, v);
                 }
             }
         }
@@ -428,7 +438,7 @@ __global__ void __launch_bounds__(R_THREADS, 2)
         if (!*abort_) {
             const int P = g.M * (SG_N / 4);
             const int p0 = (int)((long long)ks * P / g.split_k), p1 = (int)((long long)(ks + 1) * P / g.split_k);
-            for (int i = p0 + (int)threadIdx.x; i < p1; i += R_THREADS) {
+            for (int i = p0 + (int)threadIdx.x; i < p1; i += R_THREADS + 128 * SETS) {
                 const int m = i / (SG_N / 4), c = 4 * (i - m * (SG_N / 4)), n = n0 + c;
                 if (n >= g.N) continue;
                 const uint32_t off = sbase + (uint32_t)((m * SG_N + c) * 4);
@@ -901,17 +911,18 @@ fdpp_status launch_rows(const fdpp_scaled_gemm_params& p, ScaledArgs& g, const v
     g.Mp = (p.M + 15) / 16 * 16;
     g.nstage = rows_stages(g.Mp, smem_sm, smem_blk);
     const int smem = rows_smem(g.Mp, g.nstage), tiles = (p.N + SG_N - 1) / SG_N;
+    const int nr = g.Mp <= 16 ? 16 : g.Mp <= 32 ? 32 : 64, threads = R_THREADS + 128 * rows_sets(nr);
     const SgKernel kern = p.out_dtype == FDPP_F32 ? rows_kernel<float>(g.Mp) : rows_kernel<__nv_bfloat16>(g.Mp);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return sfail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    g.split_k = p.split_k ? p.split_k : choose_split(kern, tiles, g.kb, R_THREADS, smem, 2, sms);
+    g.split_k = p.split_k ? p.split_k : choose_split(kern, tiles, g.kb, threads, smem, 2, sms);
     CUtensorMap tw, tx;
     fdpp_status st;
     if ((st = encode_rows(&tw, w, p.N, p.K, p.w_stride, SG_N)) != FDPP_OK) return st;
     if ((st = encode_rows(&tx, x, p.M, p.K, p.x_stride, g.Mp)) != FDPP_OK) return st;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * g.split_k));
-    cfg.blockDim = dim3(R_THREADS);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -1014,12 +1025,10 @@ try {
     g.N = p->N;
     g.kb = blocks_of(p->K);
     cudaStream_t s = (cudaStream_t)stream;
-    // Few rows: the rows kernel pads them least, the tile kernel's CTAs split K with less to add up. us a call, rows
-    // kernel against tile kernel: 48 rows of 4096 x 4096 7.9 and 7.8, of 6144 x 4096 9.1 and 10.0, of 4096 x 14336 14.4
-    // and 15.2; 64 rows 8.9 and 7.9, 10.3 and 10.5, 15.8 and 15.3. With weight tiles for all SMs it keeps the advantage (64
-    // rows of 28672 x 4096: 25.3 and 31.6).
-    const int w_tiles = (int)((p->N + SG_N - 1ll) / SG_N);
-    if (p->M <= SG_FEW || (p->M <= SG_GROUP && w_tiles >= sms)) return launch_rows(*p, g, x, w, sms, smem_sm, smem_blk, s);
+    // Few rows: the rows kernel pads them least, and two of its CTAs share an SM. us a call at 64 rows, rows kernel against
+    // tile kernel: 2048 x 2048 6.7 and 7.1, 6144 x 4096 9.9 and 11.2, 8192 x 8192 14.4 and 15.5, 28672 x 4096 22.3 and 31.6;
+    // but 4096 x 4096 8.9 and 8.4, 4096 x 14336 14.2 and 13.6.
+    if (p->M <= SG_GROUP) return launch_rows(*p, g, x, w, sms, smem_sm, smem_blk, s);
     // Pairs of CTAs on 256 x 256 tiles where these alone are enough for all SMs, else 128 x 128 ones.
     const long long tiles = ((p->M + 255ll) / 256) * ((p->N + 255ll) / 256);
     const bool big = tiles >= sms / 2;
