@@ -2172,16 +2172,16 @@ struct RowSum {
 };
 
 // The partials of a unit cut in two or more, tiles [start, start + nt): the part of its first tile left
-// its own in slot 2 c + 1, every later one in slot 2 c. Four are read at a time; the first `done` are left out.
-template <int E>
+// its own in slot 2 c + 1, every later one in slot 2 c. N are read at a time; the first `done` are left out.
+template <int N, int E>
 __device__ __forceinline__ void add_cut(const RowsArgs& a, const int* begins, RowSum<E>& x, int start, int nt, int first,
                                         long long row, int done = 0)
 {
-    for (int c0 = first + done; c0 < a.parts && begins[c0] < start + nt; c0 += 4) {
-        float2 ml[4];
-        float v[4][E];
+    for (int c0 = first + done; c0 < a.parts && begins[c0] < start + nt; c0 += N) {
+        float2 ml[N];
+        float v[N][E];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < N; ++k) {
             const int c = min(c0 + k, a.parts - 1);
             const long long at = (long long)(2 * c + (c == first ? 1 : 0)) * a.slot_rows + row;
             ml[k] = make_float2(-INFINITY, 0.f);
@@ -2191,7 +2191,7 @@ __device__ __forceinline__ void add_cut(const RowsArgs& a, const int* begins, Ro
             }
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x.add(ml[k], v[k]);
+        for (int k = 0; k < N; ++k) x.add(ml[k], v[k]);
     }
 }
 
@@ -2204,30 +2204,53 @@ __device__ __forceinline__ void load_begins(const RowsArgs& a, int total, int* b
     __syncthreads();
 }
 
-// Without a prefix: the units that a part boundary cuts, found from the boundaries (one grid column
-// each; the first boundary inside a unit does it). A warp per row, and at most JOIN_ROWS CTAs for a unit so
-// that all are resident at once. Ragged prompts of 333 to 1500 tokens, 16 heads, 2 kv heads, d = 64, in all:
+// Without a prefix: the units that a part boundary cuts. A warp per row.
+//
+// BY_UNIT, for calls of few units (at most a quarter of the parts): a grid column for every unit, with JOIN_BY_UNIT CTAs of an
+// SM among them, so that every row of a tile has a warp, which reads eight partials at a time. Otherwise the units are found
+// from the boundaries, a column each (the first boundary inside a unit does it), and at most JOIN_ROWS CTAs for a unit so that
+// all are resident at once. us a call (d = 128, 8 kv heads of 4 but for the last), by boundaries and by units: 1 token behind
+// 8192 keys 20.9 and 20.2, 64 tokens 46.0 and 28.3, 128 behind 16384 56.1 and 48.8; a tree of 61 behind 8000 with a cap 49.8 and
+// 33.2; but 2 tokens each of 8 sequences (up to 72 units) 35.3 and 35.8, 512 tokens of 2 kv heads of 16 (66 units) 71.0 and 72.8.
+// JOIN_ROWS, ragged prompts of 333 to 1500 tokens, 16 heads, 2 kv heads, d = 64, in all:
 // with 4 CTAs for a unit 58.5 us, with 8 52.8, with 16 53.7, with 32 (a CTA for every eight rows) 55.3.
-constexpr int JOIN_ROWS = 8;
-template <int D>
+constexpr int JOIN_ROWS = 8, JOIN_BY_UNIT = 4;
+template <int D, bool BY_UNIT>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) rows_join_cut_kernel(RowsArgs a)
 {
     __shared__ int begins[ROWS_MAX_PARTS + 1];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int c = blockIdx.x + 1, total = a.plan[RP_TILES];
-    const RowTileRec r = a.rec[a.plan[RP_WORDS + c]];      // the row tile that part c begins in
-    const int x = part_begin(c, total, a.parts), before = part_begin(c - 1, total, a.parts);
-    if (x <= 0 || x >= total) return;
-    const int span = unit_span(a, r), g = (x - r.start) / span, start = r.start + g * span;
-    if (x == start || x >= start + r.nt || before > start) return;
+    const int total = a.plan[RP_TILES];
+    RowTileRec r;
+    int g, start, first;                                   // first: the part of the unit's first tile
+    if constexpr (BY_UNIT) {
+        const int rt = blockIdx.x / a.Hkv;
+        if (rt >= a.plan[RP_NRT]) return;
+        r = a.rec[rt];
+        if (r.nt == 0) return;
+        g = blockIdx.x - rt * a.Hkv;
+        start = r.start + g * unit_span(a, r);
+        first = (int)(((start + 1ll) * a.parts - 1) / total);      // the last c with c total / parts < start + 1
+        if (part_begin(first + 1, total, a.parts) >= start + r.nt) return;
+    } else {
+        const int c = blockIdx.x + 1;
+        r = a.rec[a.plan[RP_WORDS + c]];                   // the row tile that part c begins in
+        const int x = part_begin(c, total, a.parts), before = part_begin(c - 1, total, a.parts);
+        if (x <= 0 || x >= total) return;
+        const int span = unit_span(a, r);
+        g = (x - r.start) / span;
+        start = r.start + g * span;
+        first = c - 1;
+        if (x == start || x >= start + r.nt || before > start) return;
+    }
     if (blockIdx.y * JOIN_WARPS >= r.ntok * a.G) return;
     load_begins(a, total, begins);
     for (int row = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5); row < r.ntok * a.G; row += gridDim.y * JOIN_WARPS) {
         const int i = row / a.G, tok = r.tok0 + i;
         const RowToken tk = a.tok[tok];
         RowSum<D / 32> s;
-        add_cut(a, begins, s, start, r.nt, c - 1, row);
+        add_cut<BY_UNIT ? 8 : 4>(a, begins, s, start, r.nt, first, row);
         s.store(static_cast<__nv_bfloat16*>(a.out) + ((long long)tok * a.Hq + g * a.G + (row - i * a.G)) * D, tk.hi <= tk.lo);
     }
 }
@@ -2287,7 +2310,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) rows_join_prefix_kernel(RowsA
         s.add(ml[src][0], v[src][0]);
         s.add(ml[src][1], v[src][1]);
         if (pieces[src] == 2)
-            add_cut(a, begins, s, start[src], rec[src].nt, first[src], (long long)(tok - rec[src].tok0) * a.G + (head - g * a.G), 2);
+            add_cut<4>(a, begins, s, start[src], rec[src].nt, first[src], (long long)(tok - rec[src].tok0) * a.G + (head - g * a.G), 2);
     }
     s.store(static_cast<__nv_bfloat16*>(a.out) + ((long long)tok * a.Hq + head) * D, tk.hi <= tk.lo);
 }
@@ -2330,8 +2353,11 @@ cudaError_t launch_d(const RowsArgs& a, const RowsMaps& m, cudaStream_t s)
         PdlConfig join(dim3((unsigned)((rows + JOIN_WARPS - 1) / JOIN_WARPS)), JOIN_WARPS * 32, 0, s);
         e = cudaLaunchKernelEx(&join.cfg, rows_join_prefix_kernel<D>, a);
     } else if (a.parts > 1) {
-        PdlConfig join(dim3((unsigned)(a.parts - 1), (unsigned)min(JOIN_ROWS, (a.slot_rows + JOIN_WARPS - 1) / JOIN_WARPS)), JOIN_WARPS * 32, 0, s);
-        e = cudaLaunchKernelEx(&join.cfg, rows_join_cut_kernel<D>, a);
+        const long long units = (long long)a.max_rt * a.Hkv;
+        const bool by_unit = 4 * units <= a.parts;
+        const int columns = by_unit ? (int)units : a.parts - 1, most = by_unit ? JOIN_BY_UNIT * a.parts / columns : JOIN_ROWS;
+        PdlConfig join(dim3((unsigned)columns, (unsigned)min(most, (a.slot_rows + JOIN_WARPS - 1) / JOIN_WARPS)), JOIN_WARPS * 32, 0, s);
+        e = cudaLaunchKernelEx(&join.cfg, by_unit ? rows_join_cut_kernel<D, true> : rows_join_cut_kernel<D, false>, a);
     }
     return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -54,6 +54,21 @@ def test_attention_window(dtype, window):
                 dtype=dtype, block=16).check()
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(16, 2, 128), (8, 4, 64)])
+@pytest.mark.parametrize("sizes,old", [
+    ((61,), (5000,)),                                      # few units, each cut in many parts
+    ((1,), (9000,)), ((0, 40, 0), (700, 3000, 0)), ((256,), (1000,)), ((7, 90), (1, 2500)),
+    ((2,) * 12 + (61,), (10,) * 12 + (5000,)),             # many units, one of them long
+])
+def test_attention_cut_in_many_parts(hq, hkv, d, sizes, old):
+    x = TreeProblem(trees_of(9, sizes), old, hq=hq, hkv=hkv, d=d, block=64)
+    x.check()
+    first = x.out.clone()
+    x.out.fill_(float("nan"))
+    x.check()
+    assert bool((x.out[x.rows[0]:x.rows[1]] == first[x.rows[0]:x.rows[1]]).all())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attention_leaves_rows_of_no_sequence(dtype):
     TreeProblem(trees_of(5, (3, 8)), (40, 77), lead=4, tail=5, spare_len=30, dtype=dtype).check()
