@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(TREE) lineage_kernel(const __grid_constant__ R
 // are read before the first of them is written, and no thread waits for another.
 constexpr int COMMIT_THREADS = 256;
 constexpr int COMMIT_AT_ONCE = 8;
-constexpr int COMMIT_RESIDENT = 8;       // CTAs of an SM (64 trees of 16 in 64 caches: 6.4 us; with four 7.3, two 8.8)
+constexpr int COMMIT_RESIDENT = 8;       // CTAs of an SM (64 trees of 16 in 64 caches, us: eight 6.4, four 7.3, two 8.8)
 static_assert(COMMIT_THREADS >= TREE, "a thread per node");
 
 // N: most caches (a launch with 2 kB of arguments takes the host a microsecond longer than one with 300 bytes).
@@ -96,6 +96,7 @@ template <int N>
 __global__ void __launch_bounds__(COMMIT_THREADS) tree_commit_kernel(const __grid_constant__ CommitArgs<N> a)
 {
     __shared__ int choice[TREE], next[TREE], path[TREE];
+    __shared__ long long slot[TREE];                     // each node's row in the caches, -1: its block is not in the pool
     __shared__ long long from[TREE], to[TREE];           // byte offsets of the path's rows, -1: not moved
     __shared__ int taken, first_moved;
     const int b = blockIdx.y, i = threadIdx.x;
@@ -132,6 +133,15 @@ __global__ void __launch_bounds__(COMMIT_THREADS) tree_commit_kernel(const __gri
         token = a.tokens[c0 + i];
         choice[i] = a.choices[c0 + i];
         next[i] = TREE;
+        // all nodes' blocks, not only the path's, so that their reading does not wait for the path (the eight's 6.4 us
+        // above became 6.0)
+        const int pos = base + i;
+        long long at = (long long)b * a.max_seq_len + pos;
+        if (a.table) {
+            const int j = pos / a.block_size, blk = a.table[(long long)b * a.max_blocks + j];
+            at = blk >= 0 && blk < a.num_blocks ? (long long)blk * a.block_size + (pos - j * a.block_size) : -1;
+        }
+        slot[i] = at;
         if (up < -1 || up >= i) {
             bad |= FDPP_ERRBIT_TREE;
             up = -1;
@@ -152,21 +162,10 @@ __global__ void __launch_bounds__(COMMIT_THREADS) tree_commit_kernel(const __gri
     __syncthreads();
     const int count = taken, start = min(first_moved, count);
     if (i < count && i >= start) {
-        long long slot[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int pos = base + (k ? i : path[i]);
-            slot[k] = (long long)b * a.max_seq_len + pos;
-            if (a.table) {
-                const int j = pos / a.block_size, blk = a.table[(long long)b * a.max_blocks + j];
-                slot[k] = -1;
-                if (blk >= 0 && blk < a.num_blocks) slot[k] = (long long)blk * a.block_size + (pos - j * a.block_size);
-                else bad |= FDPP_ERRBIT_BLOCK_TABLE;
-            }
-        }
-        const bool both = slot[0] >= 0 && slot[1] >= 0;
-        from[i] = both ? slot[0] * a.row_bytes : -1;
-        to[i] = slot[1] * a.row_bytes;
+        const long long source = slot[path[i]], place = slot[i];
+        if (source < 0 || place < 0) bad |= FDPP_ERRBIT_BLOCK_TABLE;
+        from[i] = source >= 0 && place >= 0 ? source * a.row_bytes : -1;
+        to[i] = place * a.row_bytes;
     }
     if (tells) {
         if (i == 0) {
