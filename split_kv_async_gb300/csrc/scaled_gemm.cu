@@ -11,7 +11,7 @@
 //
 //   rows kernel (few rows): y^T = w x^T. 128 weight rows on the tensor-memory lanes, the rows of x on N, padded to the
 //     next 16 only; two CTAs per SM.
-//   tile kernel: 128 rows of x on the lanes, BN weight rows on N, one persistent CTA per SM, or two as a pair.
+//   tile kernel: 128 rows of x on the lanes, 128 or 256 weight rows on N, one persistent CTA per SM, or two as a pair.
 // Where the tiles are too few for the GPU, K is cut into ranges whose CTAs form a cluster and add their sums through
 // distributed shared memory, in range order.
 //
@@ -557,6 +557,7 @@ __global__ void __launch_bounds__(TileSmem<BN, PAIR>::THREADS, 1)
     grid_dependency_wait();
     grid_launch_dependents();
     static_assert(!(PAIR && SPLIT), "a cluster is a pair or shares out K");
+    static_assert(!SPLIT || SG_ROWS * BN * 4 <= L::STAGES * L::STAGE, "a split tile's sums take the place of the stages");
     const int tiles = g.m_tiles * g.n_tiles;
     // (with shared K a cluster has one tile: its sums take the place of the ring's stages)
     const int first = PAIR ? blockIdx.x >> 1 : SPLIT ? blockIdx.x / g.split_k : blockIdx.x;
@@ -1029,14 +1030,22 @@ try {
     // tile kernel: 2048 x 2048 6.7 and 7.1, 6144 x 4096 9.9 and 11.2, 8192 x 8192 14.4 and 15.5, 28672 x 4096 22.3 and 31.6;
     // but 4096 x 4096 8.9 and 8.4, 4096 x 14336 14.2 and 13.6.
     if (p->M <= SG_GROUP) return launch_rows(*p, g, x, w, sms, smem_sm, smem_blk, s);
-    // Pairs of CTAs on 256 x 256 tiles where these alone are enough for all SMs, else 128 x 128 ones.
-    const long long tiles = ((p->M + 255ll) / 256) * ((p->N + 255ll) / 256);
-    const bool big = tiles >= sms / 2;
-    if (p->out_dtype == FDPP_F32)
-        return big ? launch_tile<float, 256, true>(*p, g, x, w, sms, smem_blk, s)
-                   : launch_tile<float, 128, false>(*p, g, x, w, sms, smem_blk, s);
-    return big ? launch_tile<__nv_bfloat16, 256, true>(*p, g, x, w, sms, smem_blk, s)
-               : launch_tile<__nv_bfloat16, 128, false>(*p, g, x, w, sms, smem_blk, s);
+    // Tiles of 128 x 128 (whose sums join soonest where K is split) while each SM has one at most and K is short, then of
+    // 128 x 256, for which less is read; pairs of CTAs on 256 x 256 where those would be more than one for an SM too, unless
+    // the pairs' larger tiles take more turns. us a call, 128 x 128, 128 x 256 (four buffers of sums become two) and pairs:
+    // 512 x 4096 x 4096 14.9, 16.8, -; 512 x 4096 x 8192 25.6, 22.3, -; 512 x 4096 x 14336 40.6, 31.9, -; 1000 x 4096 x 4096
+    // 26.4, 16.9, -; 128 x 28672 x 4096 -, 25.0, 33.4; 128 x 128256 x 4096 -, 96.9, 109.8.
+    const long long m_tiles = (p->M + 127ll) / 128, tiles = m_tiles * ((p->N + 127ll) / 128);
+    const long long wide_tiles = m_tiles * ((p->N + 255ll) / 256), pair_tiles = (m_tiles + 1) / 2 * ((p->N + 255ll) / 256);
+    const bool pairs = wide_tiles > sms && (pair_tiles - 1) / std::max(1, sms / 2) <= (wide_tiles - 1) / sms;
+    const bool wide = tiles > sms || (2 * tiles > sms && g.kb >= 64);
+    auto launch = [&](auto type) {
+        using T = decltype(type);
+        return pairs ? launch_tile<T, 256, true>(*p, g, x, w, sms, smem_blk, s)
+               : wide ? launch_tile<T, 256, false>(*p, g, x, w, sms, smem_blk, s)
+                      : launch_tile<T, 128, false>(*p, g, x, w, sms, smem_blk, s);
+    };
+    return p->out_dtype == FDPP_F32 ? launch(float{}) : launch(__nv_bfloat16{});
 } catch (...) {                          // (the cache of cluster counts allocates)
     return sfail(FDPP_ERR_CUDA, "out of host memory");
 }

@@ -232,6 +232,22 @@ def test_linear_many_tiles(M, N, K):
     check_linear(M, N, K)
 
 
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [
+    (1000, 4096, 272), (70, 20000, 144), (129, 10250, 400),      # 128 x 256 tiles, one for an SM at most
+    (260, 4000, 8208), (130, 6300, 9216),                        # .. that share out a long K
+    (70, 40000, 144),                                            # .. two for an SM: pairs would be half empty
+    (1200, 4000, 272),                                           # pairs
+])
+def test_linear_tiles_of_every_kind(M, N, K, out):
+    check_linear(M, N, K, out, ypad=3 if M == 130 else 0)
+
+
+@pytest.mark.parametrize("split_k", [1, 2, 5, 8])
+def test_linear_splits_of_wide_tiles(split_k):
+    check_linear(300, 6000, 1168, "f32", split_k=split_k)
+
+
 @pytest.mark.parametrize("M", [9, 150])
 def test_linear_scales_of_every_size(M):
     check_linear(M, 520, 900 // 16 * 16, "f32", spread=12.0)
