@@ -243,12 +243,40 @@ struct DeviceInfo {
 std::mutex g_dev_mutex;
 DeviceInfo g_dev[64];
 
+// A function of the driver by its name (nullptr: not there).
+void* driver_function(const char* name)
+{
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion(name, &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+        cudaGetLastError();
+        return nullptr;
+    }
+    return f;
+}
+
+// The driver's own functions (the tensor maps' encoder) need a current context, which a host thread that has
+// made no CUDA call yet does not have: it gets its device's primary one, as the runtime's launches would give it. A context
+// that is current, the caller's own too, stays.
+fdpp_status context_of_thread(int dev)
+{
+    static const auto current = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(driver_function("cuCtxGetCurrent"));
+    CUcontext ctx = nullptr;
+    if (current && current(&ctx) == CUDA_SUCCESS && ctx) return FDPP_OK;
+    const cudaError_t e = cudaSetDevice(dev);
+    if (e != cudaSuccess) return fail(FDPP_ERR_CUDA, "cudaSetDevice: %s", cudaGetErrorString(e));
+    return FDPP_OK;
+}
+
 fdpp_status device_info(DeviceInfo& out)
 {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return fail(FDPP_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
     if (dev < 0 || dev >= 64) return fail(FDPP_ERR_CUDA, "device index %d out of range", dev);
+    const fdpp_status st = context_of_thread(dev);
+    if (st != FDPP_OK) return st;
     std::lock_guard<std::mutex> lk(g_dev_mutex);
     DeviceInfo& d = g_dev[dev];
     if (!d.valid) {
@@ -274,12 +302,7 @@ std::once_flag g_encode_once;
 fdpp_status tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000& fn)
 {
     std::call_once(g_encode_once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+        g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(driver_function("cuTensorMapEncodeTiled"));
     });
     if (!g_encode) return fail(FDPP_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
     fn = g_encode;
