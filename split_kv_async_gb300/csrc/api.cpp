@@ -433,6 +433,13 @@ fdpp_status query_device(int* sms, int* smem_per_sm, int* smem_per_block)
     return FDPP_OK;
 }
 
+cudaError_t allow_dynamic_smem(const void* kern)
+{
+    DeviceInfo d;
+    if (device_info(d) != FDPP_OK) return cudaErrorInvalidDevice;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem_per_block);
+}
+
 fdpp_status get_tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn)
 {
     return tensor_map_encoder(*fn);

@@ -127,6 +127,10 @@ int score_ranges_ctas_per_sm(const KernelArgs& a, int dtype);
 
 // The current device's SM count and shared-memory limits (sm_103a checked; cached per device).
 fdpp_status query_device(int* sms, int* smem_per_sm, int* smem_per_block);
+// Lets launches of `kern` (without static shared memory) take what the device has for a block. The limit belongs to the
+// kernel, not to a launch: a call that set what it needs itself could lower it between another thread's setting
+// and launch.
+cudaError_t allow_dynamic_smem(const void* kern);
 // The driver's cuTensorMapEncodeTiled (looked up once).
 fdpp_status get_tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn);
 

@@ -289,7 +289,7 @@ int gemm_stages(int Mp, int smem_per_sm, int smem_per_block)
 
 int gemm_smem_bytes(int Mp, int nstage) { return nstage * (GW_BYTES + Mp * GB_K * 2) + 16 * nstage + 32 + 1024; }
 
-// Clusters of `split` CTAs the GPU holds at once for this ring (0 if the query fails); cached.
+// Clusters of `split` CTAs the GPU holds at once for this ring; cached (0 if the query fails, which is not).
 int max_active_clusters(int split, int Mp, int nstage)
 {
     static std::mutex mu;
@@ -302,7 +302,7 @@ int max_active_clusters(int split, int Mp, int nstage)
     if (it != cache.end()) return it->second;
     const int smem = gemm_smem_bytes(Mp, nstage);
     int n = 0;
-    if (cudaFuncSetAttribute(flat_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess) {
+    if (allow_dynamic_smem((const void*)flat_gemm_kernel) == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)split);
         cfg.blockDim = dim3(G_THREADS);
@@ -314,11 +314,10 @@ int max_active_clusters(int split, int Mp, int nstage)
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, flat_gemm_kernel, &cfg) != cudaSuccess) n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, flat_gemm_kernel, &cfg) == cudaSuccess) return cache[key] = n;
     }
     cudaGetLastError();
-    cache[key] = n;
-    return n;
+    return 0;
 }
 
 // Heuristic split: the largest number of K ranges (at most G_MAX_SPLIT, at least two K slices
@@ -451,7 +450,7 @@ fdpp_status fdpp_flat_gemm(const void* x, const void* w, void* y, int M, int N, 
     if ((st = encode_2d(&tw, w, N, K, GB_N)) != FDPP_OK) return st;
     if ((st = encode_2d(&tx, x, M, K, g.Mp)) != FDPP_OK) return st;
     const int smem = gemm_smem_bytes(Mp, nstage);
-    cudaError_t e = cudaFuncSetAttribute(flat_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_dynamic_smem((const void*)flat_gemm_kernel);
     if (e != cudaSuccess) return gfail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     // a programmatic dependent of the kernel before it on the stream (see the producer)
     cudaLaunchConfig_t cfg = {};

@@ -2345,7 +2345,7 @@ cudaError_t launch_d(const RowsArgs& a, const RowsMaps& m, cudaStream_t s)
     if (TREE && (e = launch_lineage(a, s)) != cudaSuccess) return e;
     auto kern = rows_tile_kernel<D, MODE, TREE>;
     const int smem = RowsSmem<D>(a.stages).total;
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    if ((e = allow_dynamic_smem((const void*)kern)) != cudaSuccess) return e;
     PdlConfig tile(dim3((unsigned)a.parts), RW_THREADS, (size_t)smem, s);
     if ((e = cudaLaunchKernelEx(&tile.cfg, kern, m.q, m.qn, m.k, m.v, m.pk, m.pv, a)) != cudaSuccess) return e;
     if (a.prefix_len) {

@@ -861,7 +861,7 @@ int rows_stages(int Mp, int smem_per_sm, int smem_per_block)
     return std::max(2, std::min(SG_MAX_STAGES, budget / (RW_BYTES + Mp * SB)));
 }
 
-// Clusters of `split` CTAs that the GPU holds at once (0 if the query fails); cached.
+// Clusters of `split` CTAs that the GPU holds at once; cached (0 if the query fails, which is not).
 int max_clusters(SgKernel kern, int split, int threads, int smem)
 {
     static std::mutex mu;
@@ -883,12 +883,9 @@ int max_clusters(SgKernel kern, int split, int threads, int smem)
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
-        n = 0;
-        cudaGetLastError();
-    }
-    cache[key] = n;
-    return n;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess) return cache[key] = n;
+    cudaGetLastError();
+    return 0;
 }
 
 // Ranges of K for `tiles` output tiles: as many as keep all clusters on the GPU at once. The query for resident
@@ -914,7 +911,7 @@ fdpp_status launch_rows(const fdpp_scaled_gemm_params& p, ScaledArgs& g, const v
     const int smem = rows_smem(g.Mp, g.nstage), tiles = (p.N + SG_N - 1) / SG_N;
     const int nr = g.Mp <= 16 ? 16 : g.Mp <= 32 ? 32 : 64, threads = R_THREADS + 128 * rows_sets(nr);
     const SgKernel kern = p.out_dtype == FDPP_F32 ? rows_kernel<float>(g.Mp) : rows_kernel<__nv_bfloat16>(g.Mp);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_dynamic_smem((const void*)kern);
     if (e != cudaSuccess) return sfail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     g.split_k = p.split_k ? p.split_k : choose_split(kern, tiles, g.kb, threads, smem, 2, sms);
     CUtensorMap tw, tx;
@@ -960,12 +957,12 @@ fdpp_status launch_tile(const fdpp_scaled_gemm_params& p, ScaledArgs& g, const v
     cudaError_t e;
     if constexpr (!PAIR) {
         const SgKernel split = scaled_tile_kernel<T, BN, PAIR, true>;
-        if ((e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+        if ((e = allow_dynamic_smem((const void*)split)) != cudaSuccess)
             return sfail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         g.split_k = p.split_k ? p.split_k : choose_split(split, m_tiles * n_tiles, g.kb, threads, smem, 1, sms);
         if (g.split_k > 1) kern = split;
     }
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+    if ((e = allow_dynamic_smem((const void*)kern)) != cudaSuccess)
         return sfail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     const int cluster = PAIR ? 2 : g.split_k;
     const long long tiles = m_tiles * n_tiles;

@@ -604,7 +604,7 @@ cudaError_t launch_t(const KernelArgs& a, const CUtensorMap& tk, const CUtensorM
     auto kern = a.NRG > 1 ? (two ? split_tc_kernel<D, PAGED, 2, true, true> : split_tc_kernel<D, PAGED, 1, true, true>)
               : a.Tq > 1  ? (two ? split_tc_kernel<D, PAGED, 2, true, false> : split_tc_kernel<D, PAGED, 1, true, false>)
                           : (two ? split_tc_kernel<D, PAGED, 2, false, false> : split_tc_kernel<D, PAGED, 1, false, false>);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_dynamic_smem((const void*)kern);
     if (e != cudaSuccess) return e;
     // a programmatic dependent of the previous kernel on the stream (the previous call's combine
     // lets it launch early): its CTAs start while that kernel finishes and wait for it to

@@ -882,7 +882,7 @@ cudaError_t launch_np(const KernelArgs& a, const CUtensorMap& tk, const CUtensor
                       int grid, int smem, cudaStream_t s)
 {
     auto kern = split_um_kernel<NP, PAGED>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_dynamic_smem((const void*)kern);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);

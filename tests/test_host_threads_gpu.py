@@ -1,10 +1,26 @@
-"""Calls from host threads: a thread's first CUDA call may be one of the library's."""
+"""Calls from host threads.
+
+A thread's first CUDA call may be one of the library's: it passes, on the device's primary context.
+
+Two threads call the same operator at once, each on its own stream with buffers of its own, at sizes
+whose kernels need different amounts of shared memory: every call passes, and gives the bits of a call alone.
+Each set of calls runs in a process of its own, so that nothing that the library keeps of the device (which
+clusters fit) is there when the threads begin."""
+import hashlib
+import json
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+REPEATS = 3000
+KINDS = ("scaled_gemm", "flat_gemm", "attention_sync", "attention_tcgen05")
 
 
 def _call(kind, which):
@@ -73,3 +89,63 @@ def test_first_call_of_a_thread(kind, which):
     torch.cuda.synchronize()
     assert not raised and error_bits() == 0, raised
     assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+
+
+def child(at_once):
+    report = {}
+    for kind in KINDS:
+        calls = [_call(kind, which) for which in (0, 1)]
+        streams = [torch.cuda.Stream() for _ in calls]
+        torch.cuda.synchronize()
+        failed = []
+        start = threading.Barrier(2)
+
+        def work(call, stream):
+            if at_once:
+                start.wait()
+            for i in range(REPEATS if at_once else 1):
+                try:
+                    call(stream)
+                except Exception as e:
+                    failed.append(str(e))
+                if i % 200 == 199:
+                    stream.synchronize()
+
+        threads = [threading.Thread(target=work, args=(c[0], s)) for c, s in zip(calls, streams)]
+        for t in threads:
+            t.start()
+            if not at_once:
+                t.join()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+        failures = len(failed)
+        for c, s in zip(calls, streams):         # and once more, alone
+            c[0](s)
+        torch.cuda.synchronize()
+        bits = [hashlib.sha256(out.view(torch.int16).cpu().numpy().tobytes()).hexdigest() for _, out, _ in calls]
+        report[kind] = dict(failures=failures, first=failed[:1], bits=bits, errors=[e() for _, _, e in calls])
+    print("REPORT " + json.dumps(report))
+
+
+def _run(at_once):
+    code = f"import sys; sys.path[:0] = [{os.path.dirname(HERE)!r}, {HERE!r}]; import test_host_threads_gpu as t; t.child({at_once})"
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=600)
+    lines = [x for x in r.stdout.splitlines() if x.startswith("REPORT ")]
+    assert r.returncode == 0 and lines, r.stdout[-2000:] + r.stderr[-2000:]
+    return json.loads(lines[0][7:])
+
+
+@pytest.fixture(scope="module")
+def reports():
+    return _run(False), _run(True)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_calls_of_two_threads_at_once(reports, kind):
+    alone, together = (r[kind] for r in reports)
+    assert alone["failures"] == 0, alone["first"]
+    assert alone["errors"] == [0, 0]
+    assert together["failures"] == 0, (together["failures"], together["first"])
+    assert together["errors"] == [0, 0]
+    assert together["bits"] == alone["bits"]
