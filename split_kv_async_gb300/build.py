@@ -23,7 +23,7 @@ SOURCES = ["api.cpp", "split_tc.cu", "split_um.cu", "split_simt.cu", "combine.cu
            "flat_gemm.cu", "cache_ops.cu", "rows_api.cpp", "rows_simt.cu", "rows_tc.cu", "rows_tree.cu", "norm.cu",
            "scaled_gemm.cu", "tree.cu"]
 HEADERS = ["fdpp_internal.h", "device_common.cuh", "split_tc_common.cuh", "tcgen05.cuh", "rows_internal.h",
-           "rows_common.cuh", "rows_tc.cuh", "gemm_common.cuh"]
+           "rows_common.cuh", "rows_tc.cuh", "gemm_common.cuh", "ring_end.h"]
 
 
 def _nvcc() -> str:

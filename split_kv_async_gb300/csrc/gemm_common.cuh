@@ -2,6 +2,7 @@
 #pragma once
 
 #include "device_common.cuh"
+#include "ring_end.h"
 
 namespace fdpp {
 
@@ -73,6 +74,49 @@ __device__ __forceinline__ float4 ld_dsmem_f4(uint32_t addr)
                  : "r"(addr)
                  : "memory");
     return v;
+}
+
+__device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_dsmem_u32(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// The barriers of a ring's stages, for what is under way when a CTA ends (ring_end.h). bytes: of one CTA's copies.
+struct RingBarriers {
+    uint32_t bars, bytes;
+
+    __device__ __forceinline__ void announce(uint32_t stage) { mbar_arrive_expect_tx(bars + 8 * stage, bytes); }
+    __device__ __forceinline__ void excuse(uint32_t stage)
+    {
+        asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bars + 8 * stage), "r"(bytes) : "memory");
+    }
+    __device__ __forceinline__ void landed(uint32_t stage, uint32_t parity)
+    {
+        const uint64_t t0 = global_ns();
+        while (!mbar_try_wait(bars + 8 * stage, parity) && global_ns() - t0 < 100000000ull) {
+        }
+    }
+    // the last turn of a ring of `depth` barriers that completed `count` phases in all, whose arrivals are on their way
+    __device__ __forceinline__ void arrived(uint32_t count, uint32_t depth)
+    {
+        for (uint32_t i = ring_last_turn(count, depth); i < count; ++i) landed(i % depth, (i / depth) & 1u);
+    }
+};
+
+// The producer's last act: every stage that it filled has been used, so that neither copies nor the tensor cores' arrivals
+// are under way when the CTA ends (false: the wait ran out).
+__device__ __forceinline__ bool ring_used(uint32_t empty, uint32_t issued, uint32_t stages)
+{
+    for (uint32_t i = ring_last_turn(issued, stages); i < issued; ++i)
+        if (!mbar_wait_short(empty + 8 * (i % stages), (i / stages) & 1u)) return false;
+    return true;
 }
 
 }  // namespace fdpp

@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(R_THREADS + 128 * rows_sets(NR), 2)
     const uint32_t full = bars, empty = bars + 8 * g.nstage, accf = bars + 16 * g.nstage, acce = accf + 16;
     volatile uint32_t* tslot = reinterpret_cast<volatile uint32_t*>(sm + bar_off + 16 * g.nstage + 32);
     volatile int* abort_ = reinterpret_cast<volatile int*>(sm + bar_off + 16 * g.nstage + 40);
+    volatile int* blocks_ = abort_ + 1;  // blocks whose MMAs were issued
 
     const int tile = blockIdx.x / g.split_k;
     const int ks = g.split_k > 1 ? (int)cluster_rank() : 0;
@@ -331,6 +332,10 @@ __global__ void __launch_bounds__(R_THREADS + 128 * rows_sets(NR), 2)
                 ++issued;
             }
             grid_launch_dependents();
+            if (!*abort_ && !ring_used(empty, (uint32_t)issued, (uint32_t)g.nstage)) {
+                atomicOr(g.err, FDPP_ERRBIT_TIMEOUT);
+                *abort_ = 1;
+            }
         } else {
             grid_dependency_wait();
         }
@@ -351,9 +356,7 @@ __global__ void __launch_bounds__(R_THREADS + 128 * rows_sets(NR), 2)
             umma_commit(lead, accf + 8 * b);
             __syncwarp();
         }
-        // after an abort the MMAs issued land before the CTA ends
-        if (*abort_ && done > 0 && !mbar_wait_short(accf + 8 * ((done - 1) & 1), (uint32_t)((done - 1) >> 1) & 1u))
-            atomicOr(g.err, FDPP_ERRBIT_TIMEOUT);
+        if (lane == 0) *blocks_ = done;
         __syncwarp();
     } else {
         grid_dependency_wait();
@@ -453,13 +456,15 @@ __global__ void __launch_bounds__(R_THREADS + 128 * rows_sets(NR), 2)
         cluster_sync_all();
     }
 
-    // ---- teardown: copies and MMAs landed, tensor memory freed ----
-    if (*abort_ && warp == 0 && lane == 0) {
-        for (int i = issued > g.nstage ? issued - g.nstage : 0; i < issued; ++i) {
-            const uint64_t t0 = global_ns();
-            while (!mbar_try_wait(full + 8 * (i % g.nstage), (uint32_t)(i / g.nstage) & 1u) && global_ns() - t0 < 100000000ull) {
-            }
+    // ---- teardown: copies and MMAs landed (without an abort they have), tensor memory freed ----
+    if (*abort_ && warp < 2) {
+        RingBarriers slices{full, (uint32_t)stage_bytes};
+        if (warp == 0 && lane == 0) land_ring(slices, (uint32_t)issued, (uint32_t)issued, (uint32_t)g.nstage);
+        if (warp == 1) {
+            RingBarriers{empty, 0u}.arrived((uint32_t)*blocks_, (uint32_t)g.nstage);
+            RingBarriers{accf, 0u}.arrived((uint32_t)*blocks_, 2u);
         }
+        __syncwarp();
     }
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, ncols);
@@ -523,6 +528,8 @@ __global__ void __launch_bounds__(TileSmem<BN, PAIR>::THREADS, 1)
     volatile uint32_t* tslot = reinterpret_cast<volatile uint32_t*>(sm + L::BARS + (2 * L::STAGES + 2 * L::NBUF + 4) * 8);
     float* scales = reinterpret_cast<float*>(sm + L::SCALES_OFF);
     volatile int* abort_ = reinterpret_cast<volatile int*>(tslot + 2);
+    volatile uint32_t* slices_ = tslot + 3;              // slices that this CTA issued, blocks whose MMAs were issued
+    volatile uint32_t* blocks_ = tslot + 4;
     const int rank = PAIR ? (int)cluster_rank() : 0;
     // (both CTAs' loads complete on the first one's barriers, which its MMA thread waits for)
     const uint32_t full0 = PAIR ? dsmem_addr(full, 0) : full, acce0 = PAIR ? dsmem_addr(acce, 0) : acce;
@@ -594,12 +601,10 @@ __global__ void __launch_bounds__(TileSmem<BN, PAIR>::THREADS, 1)
                     }
                 }
             }
-            if (!ok && rank == 0) {      // every slice issued lands before the CTAs end
-                for (uint32_t j = i > L::STAGES ? i - L::STAGES : 0; j < i; ++j) {
-                    const uint64_t t0 = global_ns();
-                    while (!mbar_try_wait(full + 8 * (j % L::STAGES), (j / L::STAGES) & 1u) && global_ns() - t0 < 100000000ull) {
-                    }
-                }
+            *slices_ = i;
+            if (ok && !*abort_ && !ring_used(empty, i, L::STAGES)) {
+                atomicOr(g.err, FDPP_ERRBIT_TIMEOUT);
+                *abort_ = 1;
             }
         } else if (warp == 1 && rank == 0) {
             constexpr uint32_t IDESC = umma_idesc_e4m3(PAIR ? 2 * SG_ROWS : SG_ROWS, BN);
@@ -622,9 +627,7 @@ __global__ void __launch_bounds__(TileSmem<BN, PAIR>::THREADS, 1)
                     if (++b == (uint32_t)L::NBUF) { b = 0; bp ^= 1u; }
                 }
             }
-            // after an abort the MMAs issued land before the CTAs end
-            if (!ok && i > 0 && !mbar_wait_short(accf + 8 * ((i - 1) % L::NBUF), ((i - 1) / L::NBUF) & 1u))
-                atomicOr(g.err, FDPP_ERRBIT_TIMEOUT);
+            if (lane == 0) *blocks_ = i;
         } else if (warp >= 2) {
             // ---- the scales, T_SCALES blocks of K at a time, well ahead of the sums: a load takes longer
             // than a block's MMAs while the ring keeps the memory busy ----
@@ -765,7 +768,25 @@ __global__ void __launch_bounds__(TileSmem<BN, PAIR>::THREADS, 1)
         tc_fence_before();
     }
     __syncthreads();
-    if (PAIR) cluster_sync_all();        // neither CTA's shared or tensor memory goes while the other uses it
+    if (PAIR) {
+        // neither CTA's shared or tensor memory goes while the other uses it, and if one gave up, so has the other
+        if (threadIdx.x == 0 && *abort_) st_dsmem_u32(dsmem_addr(smem_u32((const void*)abort_), rank ^ 1u), 1u);
+        cluster_sync_all();
+    }
+    if (*abort_) {                       // copies and MMAs land before the CTAs end (without an abort they have)
+        if (warp == 0 && lane == 0 && rank == 0) {
+            RingBarriers slices{full, (uint32_t)L::STAGE};
+            land_ring(slices, *slices_, PAIR ? ld_dsmem_u32(dsmem_addr(smem_u32((const void*)slices_), 1u)) : *slices_,
+                      (uint32_t)L::STAGES);
+        }
+        if (warp == 1) {                 // (of a pair each CTA gets the first one's arrivals)
+            const uint32_t n = PAIR ? ld_dsmem_u32(dsmem_addr(smem_u32((const void*)blocks_), 0u)) : *blocks_;
+            RingBarriers{empty, 0u}.arrived(n, L::STAGES);
+            RingBarriers{accf, 0u}.arrived(n, L::NBUF);
+        }
+        __syncwarp();
+        if (PAIR) cluster_sync_all();
+    }
     if constexpr (SPLIT) {
         // every thread of every member passes both cluster barriers, whatever happened before
         cluster_sync_all();
