@@ -48,7 +48,8 @@ typedef struct fdpp_norm_params {
 } fdpp_norm_params;
 
 /* For every row: r = x + residual, y = r / sqrt(mean(r^2) + eps) (weight + weight_offset), in fp32 (r
- * before it is rounded; the squares are summed in fp32: beyond |r| = 2^63 / sqrt(dim) their sum is infinite and y 0);
+ * before it is rounded; the squares are summed in fp32: where their sum reaches 2^128, as with |r| = 2^64 / sqrt(dim)
+ * throughout, it is infinite and y 0. Small r keep their accuracy with any eps; a row of zeros with eps 0 is 0 / 0, NaN);
  * sum_out = r and out = y, each rounded once. With out_dtype FDPP_E4M3, for every
  * block of 128 channels (the last may be shorter)
  *     scale = max(max |y| / 448, 2^-126),   out = y (1 / scale) rounded to nearest even,

@@ -27,6 +27,10 @@ namespace {
 
 constexpr float E4M3_MAX = 448.f;
 constexpr float LEAST_SCALE = 1.17549435e-38f;       // 2^-126: its reciprocal is finite
+// With an epsilon below EPS_SMALL a row's mean square may come from squares that fp32 does not hold: below 2^-126 they lose
+// bits, at most 2^-150 each, which shows where mean and epsilon stay below 2^-100. Such a row (of values below 2^-42) is
+// taken times 2^100: then its values lie in 2^-49 .. 2^58.
+constexpr float EPS_SMALL = 7.8886091e-31f, SMALL_ROWS = 1.2676506e30f;      // 2^-100, 2^100
 constexpr int NORM_THREADS = 512, NORM_MAX_THREADS = 1024;     // of a CTA
 constexpr int NORM_RESIDENT = 2048;                  // threads of an SM
 constexpr int NORM_WARP_ROWS = 8;                    // rows of a CTA where each is one warp's
@@ -111,11 +115,14 @@ __device__ __forceinline__ float max_nan(float a, float b)
 
 // WARP: a row is one warp's, NORM_WARP_ROWS rows to a CTA; otherwise a row is the CTA's, and the next one is loaded
 // while this one is added up and written.
-template <typename T, bool E4M3, int V, bool WARP, int MOST = WARP ? 32 * NORM_WARP_ROWS : NORM_THREADS>
+// SMALL: for an epsilon below EPS_SMALL, with a second sum of squares. (A build of its own: the second sum behind a flag
+// of the call took single rows 0 to 8 % longer and many rows of 128 channels up to 13 %; rows summed again behind a branch
+// up to 62 %, 65536 fp32 rows of 1024 into e4m3 138 to 224 us.)
+template <typename T, bool E4M3, int V, bool WARP, bool SMALL, int MOST = WARP ? 32 * NORM_WARP_ROWS : NORM_THREADS>
 __global__ void __launch_bounds__(MOST)
     rms_norm_kernel(const __grid_constant__ NormArgs a)
 {
-    __shared__ float part[2][32];
+    __shared__ float part[2][SMALL ? 64 : 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int R = WARP ? 32 : blockDim.x, me = WARP ? lane : threadIdx.x;
     const long long step = WARP ? (long long)gridDim.x * NORM_WARP_ROWS : gridDim.x;
@@ -143,7 +150,7 @@ __global__ void __launch_bounds__(MOST)
     for (int turn = 0; t < a.T; t += step, turn ^= 1) {
         if (!AHEAD) load(t);
         float r[V][8];
-        float sum = 0.f;
+        float sum = 0.f, times = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
 #pragma unroll
@@ -159,16 +166,29 @@ __global__ void __launch_bounds__(MOST)
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) sum = fmaf(r[i][k], r[i][k], sum);
+            if constexpr (SMALL)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) times = fmaf(r[i][k] * SMALL_ROWS, r[i][k] * SMALL_ROWS, times);
         }
         if (AHEAD && t + step < a.T) load(t + step);
         sum = warp_sum(sum);
+        if constexpr (SMALL) times = warp_sum(times);
         if (!WARP) {
-            if (lane == 0) part[turn][warp] = sum;
+            if (lane == 0) {
+                part[turn][warp] = sum;
+                if constexpr (SMALL) part[turn][32 + warp] = times;
+            }
             __syncthreads();                             // (the other half is read before the next barrier)
             sum = lane < (R >> 5) ? part[turn][lane] : 0.f;
             sum = warp_sum(sum);
+            if constexpr (SMALL) times = warp_sum(lane < (R >> 5) ? part[turn][32 + lane] : 0.f);
         }
-        const float inv = 1.f / sqrtf(sum / (float)a.dim + a.eps);
+        float mean = sum / (float)a.dim + a.eps, f = 1.f;
+        if (SMALL && mean < EPS_SMALL) {
+            f = SMALL_ROWS;
+            mean = times / (float)a.dim + f * a.eps * f;
+        }
+        const float inv = 1.f / sqrtf(mean);
         if (a.sum_out) {
             T* so = static_cast<T*>(a.sum_out) + t * a.sum_stride;
 #pragma unroll
@@ -181,13 +201,13 @@ __global__ void __launch_bounds__(MOST)
             const bool in = at < vectors;
             float y[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = r[i][k] * inv;
+            for (int k = 0; k < 8; ++k) y[k] = (SMALL ? r[i][k] * f : r[i][k]) * inv;
             if (w && in) {
-                float f[8];
+                float gain[8];
                 if (!AHEAD) g[i].keep(w + at * 8);
-                g[i].get(f);
+                g[i].get(gain);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] *= f[k] + a.offset;
+                for (int k = 0; k < 8; ++k) y[k] *= gain[k] + a.offset;
             }
             if constexpr (!E4M3) {
                 if (in) store8(static_cast<T*>(a.out) + t * a.out_stride + at * 8, y);
@@ -222,16 +242,16 @@ fdpp_status nfail(fdpp_status s, const char* fmt, ...)
     return s;
 }
 
-template <typename T, bool E4M3>
+template <typename T, bool E4M3, bool SMALL>
 cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t s)
 {
     const int vectors = a.dim / 8;
     void (*kern)(NormArgs);
     unsigned grid, threads;
     if (vectors <= 128) {
-        kern = vectors <= 32   ? rms_norm_kernel<T, E4M3, 1, true>
-               : vectors <= 64 ? rms_norm_kernel<T, E4M3, 2, true>
-                               : rms_norm_kernel<T, E4M3, 4, true>;
+        kern = vectors <= 32   ? rms_norm_kernel<T, E4M3, 1, true, SMALL>
+               : vectors <= 64 ? rms_norm_kernel<T, E4M3, 2, true, SMALL>
+                               : rms_norm_kernel<T, E4M3, 4, true, SMALL>;
         grid = (unsigned)std::min((a.T - 1) / NORM_WARP_ROWS + 1, 8 * sms);
         threads = 32 * NORM_WARP_ROWS;
     } else {
@@ -239,10 +259,10 @@ cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t s)
         // channels 79 us, in 256 of 16 75; of 8192 in 512 of 16 145, in 1024 of 8 159, in 256 of 32 235; of 16384 in 1024
         // of 16 144, of 32 253.
         const int v = vectors <= 256 ? 1 : vectors <= 2 * NORM_MAX_THREADS ? 2 : 4;
-        kern = v == 1                         ? rms_norm_kernel<T, E4M3, 1, false>
-               : vectors <= 2 * NORM_THREADS  ? rms_norm_kernel<T, E4M3, 2, false>
-               : v == 2                       ? rms_norm_kernel<T, E4M3, 2, false, NORM_MAX_THREADS>
-                                              : rms_norm_kernel<T, E4M3, 4, false, NORM_MAX_THREADS>;
+        kern = v == 1                         ? rms_norm_kernel<T, E4M3, 1, false, SMALL>
+               : vectors <= 2 * NORM_THREADS  ? rms_norm_kernel<T, E4M3, 2, false, SMALL>
+               : v == 2                       ? rms_norm_kernel<T, E4M3, 2, false, SMALL, NORM_MAX_THREADS>
+                                              : rms_norm_kernel<T, E4M3, 4, false, SMALL, NORM_MAX_THREADS>;
         threads = (unsigned)((vectors + v - 1) / v + 31) / 32 * 32;
         grid = (unsigned)std::min(a.T, std::max(1, NORM_RESIDENT / (int)threads) * sms);
     }
@@ -322,9 +342,12 @@ extern "C" fdpp_status fdpp_rms_norm(const void* x, const void* residual, const 
     a.eps = p->eps;
     a.offset = p->weight_offset;
     cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t e;
-    if (p->dtype == FDPP_F32) e = e4m3 ? launch_norm<float, true>(a, sms, s) : launch_norm<float, false>(a, sms, s);
-    else e = e4m3 ? launch_norm<__nv_bfloat16, true>(a, sms, s) : launch_norm<__nv_bfloat16, false>(a, sms, s);
+    auto launch = [&](auto type) {
+        using T = decltype(type);
+        if (a.eps < EPS_SMALL) return e4m3 ? launch_norm<T, true, true>(a, sms, s) : launch_norm<T, false, true>(a, sms, s);
+        return e4m3 ? launch_norm<T, true, false>(a, sms, s) : launch_norm<T, false, false>(a, sms, s);
+    };
+    const cudaError_t e = p->dtype == FDPP_F32 ? launch(float{}) : launch(__nv_bfloat16{});
     if (e != cudaSuccess) return nfail(FDPP_ERR_CUDA, "RMS norm launch: %s", cudaGetErrorString(e));
     return FDPP_OK;
 }
