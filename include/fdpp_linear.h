@@ -81,6 +81,8 @@ size_t fdpp_scaled_gemm_workspace_size(const fdpp_scaled_gemm_params* p);
 
 /* y[m][n] = sum_b x_scales[m][b] w_scales[n / 128][b] sum_{k in block b} x[m][k] w[n][k]: each block's
  * products are summed by the tensor cores in fp32, then scaled and added in fp32; y is rounded once.
+ * The two scales' product is taken in fp32, of any two scales whose product is finite or one of which is 0. Below 2^-126 it
+ * has fewer bits, which is less than 2^-125 of y for each block; an infinite one makes the block's part infinite, or NaN.
  *   x          DEVICE e4m3 [M][K], 16-byte aligned.
  *   x_scales   DEVICE float [M][ceil(K / 128)], 4-byte aligned.
  *   w          DEVICE e4m3 [N][K] (a linear layer's weight as stored), 16-byte aligned. As in

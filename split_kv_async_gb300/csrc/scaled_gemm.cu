@@ -6,8 +6,8 @@
 // Both kernels stream blocks of 128 channels (128-byte rows, 128-byte swizzle) of x and w through a TMA
 // ring; a block is four MMAs of K = 32 into a tensor-memory buffer of its own, which other warps read,
 // scale by sx sw and add to fp32 sums in registers while the tensor cores work on the next block's buffer.
-// The scales are any fp32 numbers, so they cannot be left to the tensor cores (whose block scales are
-// powers of two).
+// The scales are fp32 numbers, so they cannot be left to the tensor cores (whose block scales are
+// powers of two); sx sw is one product in fp32 for each row, block of w and block of K.
 //
 //   rows kernel (few rows): y^T = w x^T. 128 weight rows on the tensor-memory lanes, the rows of x on N, padded to the
 //     next 16 only; two CTAs per SM.

@@ -1,12 +1,14 @@
-"""The RMS norm at the ends of fp32's range, against 64 bits.
+"""The RMS norm and the 8-bit linear layer at the ends of fp32's range, against 64 bits.
 
 Bounds: those at the head of test_linear_gpu.py. Norm: a row whose squares fp32 does not hold is taken times 2^100, which is
-exact."""
+exact. Linear: a block's product of scales below 2^-126 is a multiple of 2^-149, so off by at
+most 2^-150, of a block's sum of at most 128 x 448^2 < 2^24.62, and the product with that sum by 2^-150 more: 2^-125.25 for
+each block. What of it is a normal product's is 2^-150 a block."""
 import pytest
 import torch
 
 import split_kv_async_gb300 as F
-from test_linear_gpu import HALF, check_norm, e4m3, norm_reference
+from test_linear_gpu import CODES, HALF, TYPES, check_norm, e4m3, linear_problem, linear_reference, norm_reference, run_linear
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +68,66 @@ def test_norm_at_the_largest_sum_of_squares(eps, dim, out):
     torch.cuda.synchronize()
     y = e4m3(o).double() * scales.double().repeat_interleave(128, 1) if out == "e4m3" else o.double()
     assert bool(((y[0] - 1).abs() <= 2.0 ** -16).all()) and bool((y[1:] == 0).all())
+
+
+# ---- linear layer ------------------------------------------------------------------------------
+
+def finite_problem(M, N, K, seed):
+    x, sx, w, sw = linear_problem(M, N, K, seed)
+    return tuple(torch.where((t & 0x7F) == 0x7F, 0, t) if t.dtype == torch.uint8 else t for t in (x, sx, w, sw))
+
+
+def about(like, power):
+    """Scales of 1 to 1.25 times 2^power (in 64 bits, then rounded: the least ones are subnormal)."""
+    return ((1 + torch.rand_like(like).double() / 4) * 2.0 ** power).float()
+
+
+@pytest.mark.parametrize("M", [9, 40, 150, 300])
+@pytest.mark.parametrize("px,pw", [(-80, -45), (-126, 1), (-1, -125), (70, 25), (126, -126), (-126, 126)])
+def test_linear_scales_whose_product_is_normal(M, px, pw):
+    """The stated accuracy holds as long as the scales' product is a normal number (here the least and some large ones),
+    whatever each of them is."""
+    x, sx, w, sw = finite_problem(M, 392, 528, 3)
+    sx, sw = about(sx, px), about(sw, pw)
+    got = run_linear(x, sx, w, sw, "f32")
+    want, size = linear_reference(x, sx, w, sw)
+    bound = 2.0 ** -24 * want.abs() + 2.0 ** -15 * size + sx.shape[1] * 2.0 ** -150
+    assert bool(((got.double() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("M", [9, 40, 150, 300])
+@pytest.mark.parametrize("px,pw", [(-80, -60), (-126, -8), (-140, 10), (-149, 0), (-100, -100)])
+def test_linear_scales_whose_product_is_subnormal(M, px, pw):
+    x, sx, w, sw = finite_problem(M, 392, 528, 4)
+    sx, sw = about(sx, px), about(sw, pw)
+    got = run_linear(x, sx, w, sw, "f32")
+    want, size = linear_reference(x, sx, w, sw)
+    bound = 2.0 ** -24 * want.abs() + 2.0 ** -15 * size + sx.shape[1] * 2.0 ** -125.25
+    assert bool(((got.double() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("M", [9, 150])
+def test_linear_zero_scales(M):
+    """A zero scale takes its block out, beside the largest finite one as well."""
+    x, sx, w, sw = finite_problem(M, 200, 528, 5)
+    sx[:, 1] = 0.0
+    sw[:, 1] = 3.4e38
+    sw[:, 2] = 0.0
+    got = run_linear(x, sx, w, sw, "f32")
+    want, size = linear_reference(x, sx, w, sw)
+    assert bool(((got.double() - want).abs() <= 2.0 ** -24 * want.abs() + 2.0 ** -15 * size).all())
+
+
+@pytest.mark.parametrize("M", [9, 40, 150, 300])
+def test_linear_scales_whose_product_is_infinite(M):
+    """Infinite, or NaN where the block's sum is 0, in the rows and weight blocks concerned and no others."""
+    x, sx, w, sw = finite_problem(M, 392, 528, 6)
+    clean = run_linear(x, sx, w, sw, "f32")
+    sw[1, 2] = 2.0 ** 30
+    sx[3, 2] = 2.0 ** 100
+    other = run_linear(x, sx, w, sw, "f32")
+    assert not bool(other[3, 128:256].isfinite().any())
+    rows = torch.arange(M, device="cuda") != 3
+    assert bool(other[rows].isfinite().all()) and bool(other[3, :128].isfinite().all()) and bool(other[3, 256:].isfinite().all())
+    cols = (torch.arange(392, device="cuda") // 128) != 1
+    assert torch.equal(other[rows][:, cols], clean[rows][:, cols])
