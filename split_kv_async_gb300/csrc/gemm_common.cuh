@@ -15,20 +15,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// Whether the phase of `parity` has completed. (mbarrier.try_wait suspends the thread for a while if it has not.)
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // mbar_wait for hand-overs of a few hundred cycles: the clock, whose reading takes as long, is first read
 // after 64 tries.
 __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity)
