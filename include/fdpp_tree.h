@@ -52,7 +52,8 @@ fdpp_status fdpp_tree_workspace_size(const fdpp_rows_params* p, size_t* bytes);
 
 /* fdpp_rows_attn (fdpp_rows.h: layouts, arguments, accuracy, zero rows) with a tree's mask: token i of a sequence with L keys
  * and n tokens sees the keys t < L - n and those at L - n + j for every node j that is i itself or one
- * of its ancestors, of them those from key_begin[row] on where given (a sliding window). Parameters: key_end
+ * of its ancestors, of them those from key_begin[row] on where given. (That is a sliding window by place: an ancestor
+ * among the nodes is cut by its index, not by its depth, which differs once the window ends inside the tree.) Parameters: key_end
  * and slopes must be NULL (a key's distance would depend on the tree); kernel FDPP_KERNEL_AUTO is the tensor kernel for
  * bf16, except where num_tokens, the heads and max_seq_len leave so few keys to read that the CUDA-core kernel is done
  * first. Keys that a token does not see never enter its sums, whatever the cache holds there.
@@ -65,14 +66,14 @@ fdpp_status fdpp_tree_attn(const void* q, const void* k_cache, const void* v_cac
 /* ---- commit --------------------------------------------------------------------------------- */
 
 typedef struct fdpp_commit_params {
-    int batch;               /* B >= 1 sequences */
+    int batch;               /* B sequences: 1 .. 65535 */
     int num_tokens;          /* T >= 0 token rows. Without cu_tokens: a multiple of B */
     int max_seq_len;         /* as in fdpp_rows_params */
     int block_size;          /* paged only, as in fdpp_params */
     int max_blocks_per_seq;
     int num_kv_blocks;
     long long row_bytes;     /* bytes of a token's row in each cache (Hkv d x element size): a positive
-                                multiple of 16 */
+                                multiple of 16, at most 2^24 */
 } fdpp_commit_params;
 
 /* Bytes of workspace (the sticky error word). 0 if the parameters are invalid. */
