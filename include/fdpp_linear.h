@@ -73,7 +73,8 @@ typedef struct fdpp_scaled_gemm_params {
     long long y_stride;      /* elements from one row of y to the next, >= N */
     long long x_scale_stride;       /* floats from one row's scales to the next, >= ceil(K / 128) */
     int split_k;             /* ranges of K that an output tile is made of, added up in order: 0 chooses, otherwise
-                                1 .. min(ceil(K / 128), 8); not followed where the tiles alone fill the GPU */
+                                1 .. min(ceil(K / 128), 8); not followed where, with M > 64, tiles of 256 x 256 by
+                                pairs of CTAs fill the GPU by themselves */
 } fdpp_scaled_gemm_params;
 
 /* Bytes of workspace (the sticky error word). 0 if the parameters are invalid. */
