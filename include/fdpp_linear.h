@@ -8,7 +8,8 @@
  *
  * 8-bit operands are e4m3 (4 exponent bits, 3 of mantissa, largest value 448), each with one fp32 scale
  * for FDPP_SCALE_BLOCK consecutive channels: a value stands for e4m3 x scale. Activations have a scale for
- * every row and block of channels, weights one for every block of rows and block of channels.
+ * every row and block of channels, weights one for every block of rows and block of channels. (The norm is the only call
+ * here that makes such operands; where no norm precedes a layer they are the caller's.)
  *
  * Conventions: as in fdpp.h (caller-owned DEVICE buffers, stream-ordered calls without a host
  * synchronisation, synchronous argument errors with fdpp_last_error()). Offsets are 64-bit.

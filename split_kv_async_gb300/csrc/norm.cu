@@ -32,7 +32,7 @@ constexpr float LEAST_SCALE = 1.17549435e-38f;       // 2^-126: its reciprocal i
 // taken times 2^100: then its values lie in 2^-49 .. 2^58.
 constexpr float EPS_SMALL = 7.8886091e-31f, SMALL_ROWS = 1.2676506e30f;      // 2^-100, 2^100
 constexpr int NORM_THREADS = 512, NORM_MAX_THREADS = 1024;     // of a CTA
-constexpr int NORM_RESIDENT = 2048;                  // threads of an SM
+constexpr int NORM_RESIDENT = 2048;                  // threads of the grid for an SM: all at once with 32 registers, in two turns with 64
 constexpr int NORM_WARP_ROWS = 8;                    // rows of a CTA where each is one warp's
 
 struct NormArgs {

@@ -97,9 +97,12 @@ fdpp_status check_tree(const fdpp_rows_params* p)
 }
 
 // The kernel of a call with trees. bf16 takes the tensor cores, but where all tokens together have few keys to read
-// (each for itself on the CUDA cores) the tensor kernel's four launches take longer than these: of 75 drawn calls, 1 to
-// 60 sequences of 1 to 256 tokens, those with up to 1.5e6 elements of K took 6 to 16 us on the CUDA cores and 14 to 35 on
-// the tensor cores (but for one, 26 against 22), those with more than 2e6 16 to 780 and 16 to 90.
+// (each for itself on the CUDA cores) the tensor kernel's four launches take longer than these. Of some 120 drawn calls, 1 to 32
+// sequences of 1 to 64 tokens, us in a graph, by the elements of K that max_seq_len lets them read: up to 1.5e6 5 to 19 on the
+// CUDA cores and 13 to 38 on the tensor cores (one was slower on the CUDA cores, 19.2 against 17.8); 1.5e6 to 2.5e6 8 to 21 and
+// 15 to 32 (the CUDA cores ahead in 11 of 16, at most by half the time, behind by 17 % at most); 2.5e6 to 5e6 11 to 33 and 16
+// to 31, the tensor cores ahead in 18 of 25, at most by 1.75 times, behind by 2.4 where most of max_seq_len is not used; from there
+// on 17 to 181 and 15 to 41.
 constexpr long long TREE_SIMT_ELEMENTS = 1500000;
 fdpp_rows_params tree_params(const fdpp_rows_params& p)
 {

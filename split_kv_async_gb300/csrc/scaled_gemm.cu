@@ -16,12 +16,14 @@
 // distributed shared memory, in range order.
 //
 // What bounds it. Few rows: HBM (28672 x 4096 weights: 8 rows 19.9 us, 0.88 of a measured copy, 64 rows 22.3), and for small
-// weights the start and the end of a CTA (4096 x 4096, 8 rows: 5.8 us in a graph, of which the bytes take 2.5). Many rows: the
-// hand-over between the tensor cores and the sums. 8192 x 28672 x 4096 takes 680 us, 2.8 PFLOP/s; the MMAs alone, on
-// data that lies there, 4.6, with the loads 3.5 to 3.7 (128 bytes of shared memory a cycle, written and read). Two buffers of
-// 256 columns are all the tensor memory, so a block's sums have the 512 cycles of the next block's MMAs from the commit to the
-// release, and take more: two loads of 64 columns and 128 sums per thread, and a hundred cycles for each barrier asked, with
-// shared memory as busy as it is. Tried: 192 columns and twelve warps of sums 782 us, sixteen warps of 64 columns 915.
+// weights the start and the end of a CTA (4096 x 4096, 8 rows: 5.8 us in a graph, of which the bytes take 2.5). Many rows: 8192 x
+// 28672 x 4096 takes 680 to 700 us in ten calls after a rest, 2.8 PFLOP/s, and 755 one call after the other, when the power
+// limit holds the clock at 1740 MHz: 855 cycles for a block of K, a 32nd of a tile's stores among them. Two buffers of 256
+// columns are all the tensor memory, so a block's sums have the 512 cycles of the next block's MMAs from the commit to the
+// release. Neither is the bound by itself: the MMAs alone run at 4.6 PFLOP/s on data that lies there, at 3.5 to 3.7 with the
+// loads (128 bytes of shared memory a cycle, written and read), and one CTA's hand-over alone, with its sums, takes 465 cycles
+// a block; what they add to one another and the stores add was not measured apart. Tried: 192 columns and twelve warps
+// of sums 782 us, sixteen warps of 64 columns 915, a buffer released before its last 64 sums 674 (673 to 684 without).
 //
 // Every wait is bounded: on a timeout the CTA records FDPP_ERRBIT_TIMEOUT, lets its copies and MMAs land,
 // frees its tensor memory and exits.
@@ -911,8 +913,9 @@ int max_clusters(SgKernel kern, int split, int threads, int smem)
 
 // Ranges of K for `tiles` output tiles: as many as keep all clusters on the GPU at once. The query for resident
 // clusters takes a kernel with tensor memory for one CTA per SM; of the rows kernel, whose CTAs share an SM by two, twice
-// as many fit, and as many as there are places for clusters of half the size. (8 rows, us: 4096 x 4096, 32 tiles, in 4 ranges
-// 7.8, in 8 6.7; 6144 x 4096, 48 tiles, in 4 8.3, in 5 8.2, in 6, which do not fit, 13.9; 4096 x 14336 in 4 15.4, in 8 12.4.)
+// as many fit, and as many as there are places for clusters of half the size. (8 rows, us in a graph: 4096 x 4096, 32 tiles, in
+// 2 ranges 8.3, in 4 6.0, in 8 5.8; 6144 x 4096, 48 tiles, in 4 or 5 7.6, in 6, which do not fit, 12.4; 4096 x 14336 in 4 15.3,
+// in 8 12.4. The rule does not look at the rows: 64 of 4096 x 4096 take 7.5 in 4 ranges and 8.6 in the 8 that it gives.)
 int choose_split(SgKernel kern, long long tiles, int kb, int threads, int smem, int ctas_per_sm, int sms)
 {
     for (int n = std::min(SG_MAX_SPLIT, kb); n > 1; --n) {
@@ -1050,9 +1053,12 @@ try {
     if (p->M <= SG_GROUP) return launch_rows(*p, g, x, w, sms, smem_sm, smem_blk, s);
     // Tiles of 128 x 128 (whose sums join soonest where K is split) while each SM has one at most and K is short, then of
     // 128 x 256, for which less is read; pairs of CTAs on 256 x 256 where those would be more than one for an SM too, unless
-    // the pairs' larger tiles take more turns. us a call, 128 x 128, 128 x 256 (four buffers of sums become two) and pairs:
-    // 512 x 4096 x 4096 14.9, 16.8, -; 512 x 4096 x 8192 25.6, 22.3, -; 512 x 4096 x 14336 40.6, 31.9, -; 1000 x 4096 x 4096
-    // 26.4, 16.9, -; 128 x 28672 x 4096 -, 25.0, 33.4; 128 x 128256 x 4096 -, 96.9, 109.8.
+    // the pairs' larger tiles take more turns. us a call in a graph, 128 x 128, 128 x 256 (four buffers of sums become two) and
+    // pairs: 512 x 4096 x 4096 14.4, 17.3, 16.3; 512 x 4096 x 8192 25.0, 23.3, 27.3; 512 x 4096 x 14336 40.3, 32.7, 43.5;
+    // 640 x 4096 x 14336 77.0, 45.6, 44.6; 1000 x 4096 x 4096 25.8, 17.4, 17.6; 1100 x 4096 x 4096 26.0, 17.6, 30.5;
+    // 256 x 14336 x 4096 25.9, 19.2, 18.3; 128 x 28672 x 4096 28.3, 25.1, 32.6; 256 x 28672 x 4096 37.4, 36.0, 33.6;
+    // 128 x 128256 x 4096 91.4, 94.9, 105.9; 2048 x 14336 x 4096 140, 90.3, 87.8 to 92.2. With one 128 x 256 tile for an SM
+    // at most, pairs take 2 to 5 % less where they are full (640 and 256 rows), and 17 to 33 % more where the single tiles split K.
     const long long m_tiles = (p->M + 127ll) / 128, tiles = m_tiles * ((p->N + 127ll) / 128);
     const long long wide_tiles = m_tiles * ((p->N + 255ll) / 256), pair_tiles = (m_tiles + 1) / 2 * ((p->N + 255ll) / 256);
     const bool pairs = wide_tiles > sms && (pair_tiles - 1) / std::max(1, sms / 2) <= (wide_tiles - 1) / sms;
