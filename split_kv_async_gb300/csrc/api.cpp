@@ -23,22 +23,23 @@
 #include "fdpp.h"
 #include "fdpp_internal.h"
 
+namespace fdpp {
+namespace {
+thread_local char g_last_error[512];
+}
+fdpp_status fail(fdpp_status s, const char* fmt, ...)
+{
+    va_list ap;
+    va_start(ap, fmt);
+    std::vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
+    va_end(ap);
+    return s;
+}
+}  // namespace fdpp
+
 using namespace fdpp;
 
 namespace {
-
-thread_local std::string g_last_error;
-
-fdpp_status fail(fdpp_status s, const char* fmt, ...)
-{
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    std::vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    g_last_error = buf;
-    return s;
-}
 
 bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 
@@ -450,8 +451,6 @@ size_t workspace_zero_prefix(const fdpp_params& p) { return layout_of(p).flags; 
 // Offset of the start-up hint region: everything before it (header, plan, fallback lists) is
 // the state that a call must find zeroed or written by the call before it.
 size_t workspace_hint_offset(const fdpp_params& p) { return layout_of(p).hint; }
-// Sets the reason fdpp_last_error() reports on this thread.
-void set_last_error(const char* what) { g_last_error = what; }
 }  // namespace fdpp
 
 extern "C" {
@@ -468,7 +467,7 @@ const char* fdpp_status_str(fdpp_status s)
     return "FDPP_UNKNOWN_STATUS";
 }
 
-const char* fdpp_last_error(void) { return g_last_error.c_str(); }
+const char* fdpp_last_error(void) { return g_last_error; }
 
 fdpp_status fdpp_attn_set_lut(const fdpp_attn_lut_row* rows, int n)
 {

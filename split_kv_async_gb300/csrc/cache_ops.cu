@@ -2,25 +2,12 @@
 // maps and token rows from request lengths) and rotary positions with the append to the cache.
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 
 #include "device_common.cuh"
 #include "fdpp_cache.h"
 
 namespace fdpp {
 namespace {
-
-fdpp_status cfail(fdpp_status s, const char* fmt, ...)
-{
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    std::vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    set_last_error(buf);
-    return s;
-}
 
 __device__ __forceinline__ void raise(unsigned* err, unsigned bits)
 {
@@ -469,22 +456,6 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32) rope_append_kernel(RopeArgs a
     }
 }
 
-template <typename... Args>
-cudaError_t launch_pdl(void (*kern)(Args...), dim3 grid, int threads, cudaStream_t s, Args... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-    return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 }  // namespace
 }  // namespace fdpp
 
@@ -503,25 +474,25 @@ fdpp_status fdpp_block_map(const int32_t* held_lens, const int32_t* want_lens, c
                            int32_t* positions, int64_t* slots, void* workspace, size_t workspace_bytes,
                            fdpp_stream stream)
 {
-    if (!p) return cfail(FDPP_ERR_INVALID_ARG, "params is NULL");
+    if (!p) return fail(FDPP_ERR_INVALID_ARG, "params is NULL");
     if (!block_params_ok(p))
-        return cfail(FDPP_ERR_INVALID_ARG,
+        return fail(FDPP_ERR_INVALID_ARG,
                      "block map of batch %d, block_size %d (a power of two in [16, 256]), %d blocks per sequence, "
                      "%d blocks, %d rows (batch x blocks per sequence below 2^31)",
                      p->batch, p->block_size, p->max_blocks_per_seq, p->num_kv_blocks, p->max_tokens);
     if (!held_lens || !want_lens || !pool_in || !block_table || !pool_queue || !seq_lens || !pool_out || !cu_tokens)
-        return cfail(FDPP_ERR_INVALID_ARG, "lengths, pool state, block_table, pool_queue and cu_tokens must be non-NULL");
+        return fail(FDPP_ERR_INVALID_ARG, "lengths, pool state, block_table, pool_queue and cu_tokens must be non-NULL");
     if (p->max_tokens > 0 && (!token_seq || !positions || !slots))
-        return cfail(FDPP_ERR_INVALID_ARG, "token_seq, positions and slots must be non-NULL");
-    if (want_lens == seq_lens) return cfail(FDPP_ERR_INVALID_ARG, "seq_lens must not be want_lens");
+        return fail(FDPP_ERR_INVALID_ARG, "token_seq, positions and slots must be non-NULL");
+    if (want_lens == seq_lens) return fail(FDPP_ERR_INVALID_ARG, "seq_lens must not be want_lens");
     if ((((uintptr_t)held_lens | (uintptr_t)want_lens | (uintptr_t)pool_in | (uintptr_t)block_table |
           (uintptr_t)pool_queue | (uintptr_t)seq_lens | (uintptr_t)pool_out | (uintptr_t)cu_tokens |
           (uintptr_t)token_seq | (uintptr_t)positions) % 4) != 0 || ((uintptr_t)slots % 8) != 0)
-        return cfail(FDPP_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned, slots 8-byte aligned");
-    if (!workspace) return cfail(FDPP_ERR_WORKSPACE, "workspace is NULL");
-    if ((uintptr_t)workspace % 256 != 0) return cfail(FDPP_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+        return fail(FDPP_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned, slots 8-byte aligned");
+    if (!workspace) return fail(FDPP_ERR_WORKSPACE, "workspace is NULL");
+    if ((uintptr_t)workspace % 256 != 0) return fail(FDPP_ERR_WORKSPACE, "workspace must be 256-byte aligned");
     if (workspace_bytes < block_ws_bytes(*p))
-        return cfail(FDPP_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, block_ws_bytes(*p));
+        return fail(FDPP_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, block_ws_bytes(*p));
     int sms = 0, unused = 0;
     const fdpp_status st = query_device(&sms, &unused, &unused);
     if (st != FDPP_OK) return st;
@@ -569,24 +540,24 @@ fdpp_status fdpp_block_map(const int32_t* held_lens, const int32_t* want_lens, c
             e = launch_pdl(block_map_rows_kernel, dim3((unsigned)grid), 256, s, a);
         }
     }
-    if (e != cudaSuccess) return cfail(FDPP_ERR_CUDA, "block map launch: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return fail(FDPP_ERR_CUDA, "block map launch: %s", cudaGetErrorString(e));
     return FDPP_OK;
 }
 
 fdpp_status fdpp_rope_table(int rot_dim, double base, int scaling, double factor, int context, double low_turns,
                             double high_turns, float* table)
 {
-    if (!table) return cfail(FDPP_ERR_INVALID_ARG, "table is NULL");
+    if (!table) return fail(FDPP_ERR_INVALID_ARG, "table is NULL");
     if (rot_dim < 16 || rot_dim > 128 || rot_dim % 16)
-        return cfail(FDPP_ERR_INVALID_ARG, "rot_dim must be a multiple of 16 in [16, 128] (got %d)", rot_dim);
-    if (!(base > 1.0) || !std::isfinite(base)) return cfail(FDPP_ERR_INVALID_ARG, "base must be finite and above 1");
+        return fail(FDPP_ERR_INVALID_ARG, "rot_dim must be a multiple of 16 in [16, 128] (got %d)", rot_dim);
+    if (!(base > 1.0) || !std::isfinite(base)) return fail(FDPP_ERR_INVALID_ARG, "base must be finite and above 1");
     if (scaling < FDPP_ROPE_PLAIN || scaling > FDPP_ROPE_PARTS)
-        return cfail(FDPP_ERR_INVALID_ARG, "unknown scaling %d", scaling);
+        return fail(FDPP_ERR_INVALID_ARG, "unknown scaling %d", scaling);
     if (scaling != FDPP_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
-        return cfail(FDPP_ERR_INVALID_ARG, "factor must be finite and at least 1");
+        return fail(FDPP_ERR_INVALID_ARG, "factor must be finite and at least 1");
     if (scaling == FDPP_ROPE_PARTS && (context < 1 || !(low_turns < high_turns) || !std::isfinite(low_turns) ||
                                        !std::isfinite(high_turns)))
-        return cfail(FDPP_ERR_INVALID_ARG, "PARTS needs context >= 1 and finite low_turns < high_turns");
+        return fail(FDPP_ERR_INVALID_ARG, "PARTS needs context >= 1 and finite low_turns < high_turns");
     const double two_pi = 6.283185307179586476925286766559;
     if (scaling == FDPP_ROPE_NTK) base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
     for (int i = 0; i < rot_dim / 2; ++i) {
@@ -609,38 +580,38 @@ fdpp_status fdpp_rope_append(const void* q, const void* k, const void* v, const 
                              void* k_cache, void* v_cache, void* workspace, size_t workspace_bytes,
                              fdpp_stream stream)
 {
-    if (!p) return cfail(FDPP_ERR_INVALID_ARG, "params is NULL");
+    if (!p) return fail(FDPP_ERR_INVALID_ARG, "params is NULL");
     if (p->num_tokens < 0 || p->num_q_heads < 1 || p->num_kv_heads < 1)
-        return cfail(FDPP_ERR_INVALID_ARG, "num_tokens must be >= 0 and head counts >= 1");
+        return fail(FDPP_ERR_INVALID_ARG, "num_tokens must be >= 0 and head counts >= 1");
     if (p->dtype != FDPP_F32 && p->dtype != FDPP_BF16)
-        return cfail(FDPP_ERR_INVALID_ARG, "dtype must be FDPP_F32 or FDPP_BF16 (got %d)", p->dtype);
+        return fail(FDPP_ERR_INVALID_ARG, "dtype must be FDPP_F32 or FDPP_BF16 (got %d)", p->dtype);
     if (p->head_dim != 64 && p->head_dim != 128)
-        return cfail(FDPP_ERR_UNSUPPORTED, "head_dim %d: only 64 and 128 are built", p->head_dim);
+        return fail(FDPP_ERR_UNSUPPORTED, "head_dim %d: only 64 and 128 are built", p->head_dim);
     if (p->rot_dim < 16 || p->rot_dim > p->head_dim || p->rot_dim % 16)
-        return cfail(FDPP_ERR_INVALID_ARG, "rot_dim must be a multiple of 16 in [16, %d] (got %d)", p->head_dim,
+        return fail(FDPP_ERR_INVALID_ARG, "rot_dim must be a multiple of 16 in [16, %d] (got %d)", p->head_dim,
                      p->rot_dim);
     if (p->interleaved != 0 && p->interleaved != 1)
-        return cfail(FDPP_ERR_INVALID_ARG, "interleaved must be 0 or 1 (got %d)", p->interleaved);
-    if (!std::isfinite(p->magnitude)) return cfail(FDPP_ERR_INVALID_ARG, "magnitude must be finite");
-    if (p->num_slots < 0) return cfail(FDPP_ERR_INVALID_ARG, "num_slots must be >= 0");
+        return fail(FDPP_ERR_INVALID_ARG, "interleaved must be 0 or 1 (got %d)", p->interleaved);
+    if (!std::isfinite(p->magnitude)) return fail(FDPP_ERR_INVALID_ARG, "magnitude must be finite");
+    if (p->num_slots < 0) return fail(FDPP_ERR_INVALID_ARG, "num_slots must be >= 0");
     const int vec = p->dtype == FDPP_F32 ? 4 : 8;
     const long long q_row = (long long)p->num_q_heads * p->head_dim, k_row = (long long)p->num_kv_heads * p->head_dim;
-    if (q_row > (1ll << 30) || k_row > (1ll << 30)) return cfail(FDPP_ERR_INVALID_ARG, "too many heads");
-    if (p->num_slots > (1ll << 62) / k_row) return cfail(FDPP_ERR_INVALID_ARG, "num_slots is too large");
+    if (q_row > (1ll << 30) || k_row > (1ll << 30)) return fail(FDPP_ERR_INVALID_ARG, "too many heads");
+    if (p->num_slots > (1ll << 62) / k_row) return fail(FDPP_ERR_INVALID_ARG, "num_slots is too large");
     if (p->q_stride < q_row || p->k_stride < k_row || p->v_stride < k_row || p->q_stride % vec || p->k_stride % vec ||
         p->v_stride % vec)
-        return cfail(FDPP_ERR_INVALID_ARG, "q, k and v strides must cover a row and be multiples of 16 bytes");
+        return fail(FDPP_ERR_INVALID_ARG, "q, k and v strides must cover a row and be multiples of 16 bytes");
     if (!q || !k || !v || !positions || !slots || !table || !q_out || !k_cache || !v_cache)
-        return cfail(FDPP_ERR_INVALID_ARG, "q, k, v, positions, slots, table, q_out and the caches must be non-NULL");
+        return fail(FDPP_ERR_INVALID_ARG, "q, k, v, positions, slots, table, q_out and the caches must be non-NULL");
     if ((((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)q_out | (uintptr_t)k_cache | (uintptr_t)v_cache) % 16) != 0)
-        return cfail(FDPP_ERR_INVALID_ARG, "q, k, v, q_out and the caches must be 16-byte aligned");
+        return fail(FDPP_ERR_INVALID_ARG, "q, k, v, q_out and the caches must be 16-byte aligned");
     if ((uintptr_t)positions % 4 != 0 || (uintptr_t)slots % 8 != 0 || (uintptr_t)table % 8 != 0)
-        return cfail(FDPP_ERR_INVALID_ARG, "positions must be 4-byte, slots and table 8-byte aligned");
+        return fail(FDPP_ERR_INVALID_ARG, "positions must be 4-byte, slots and table 8-byte aligned");
     if (q == q_out && p->q_stride != q_row)
-        return cfail(FDPP_ERR_INVALID_ARG, "q_out may be q only where q_stride is num_q_heads * head_dim");
-    if (!workspace) return cfail(FDPP_ERR_WORKSPACE, "workspace is NULL");
-    if ((uintptr_t)workspace % 256 != 0) return cfail(FDPP_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-    if (workspace_bytes < 256) return cfail(FDPP_ERR_WORKSPACE, "workspace has %zu bytes, 256 needed", workspace_bytes);
+        return fail(FDPP_ERR_INVALID_ARG, "q_out may be q only where q_stride is num_q_heads * head_dim");
+    if (!workspace) return fail(FDPP_ERR_WORKSPACE, "workspace is NULL");
+    if ((uintptr_t)workspace % 256 != 0) return fail(FDPP_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (workspace_bytes < 256) return fail(FDPP_ERR_WORKSPACE, "workspace has %zu bytes, 256 needed", workspace_bytes);
     int sms = 0, unused = 0;
     const fdpp_status st = query_device(&sms, &unused, &unused);
     if (st != FDPP_OK) return st;
@@ -673,7 +644,7 @@ fdpp_status fdpp_rope_append(const void* q, const void* k, const void* v, const 
     const long long fill = ((long long)sms * 64 + a.T - 1) / a.T;
     a.warps = (int)std::max(1ll, std::min<long long>(most, fill));
     const long long grid = ((long long)a.T * a.warps + ROPE_WARPS - 1) / ROPE_WARPS;
-    if (grid > INT32_MAX) return cfail(FDPP_ERR_INVALID_ARG, "too many tokens");
+    if (grid > INT32_MAX) return fail(FDPP_ERR_INVALID_ARG, "too many tokens");
     void (*kern)(RopeArgs) = nullptr;
     const bool il = p->interleaved == 1, wide = p->head_dim == 128;
     if (p->dtype == FDPP_F32)
@@ -683,18 +654,18 @@ fdpp_status fdpp_rope_append(const void* q, const void* k, const void* v, const 
         kern = wide ? (il ? rope_append_kernel<__nv_bfloat16, 128, true> : rope_append_kernel<__nv_bfloat16, 128, false>)
                     : (il ? rope_append_kernel<__nv_bfloat16, 64, true> : rope_append_kernel<__nv_bfloat16, 64, false>);
     const cudaError_t e = launch_pdl(kern, dim3((unsigned)grid), ROPE_WARPS * 32, (cudaStream_t)stream, a);
-    if (e != cudaSuccess) return cfail(FDPP_ERR_CUDA, "rope append launch: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return fail(FDPP_ERR_CUDA, "rope append launch: %s", cudaGetErrorString(e));
     return FDPP_OK;
 }
 
 fdpp_status fdpp_read_error(const void* workspace, uint32_t* error_bits)
 {
-    if (!workspace || !error_bits) return cfail(FDPP_ERR_INVALID_ARG, "null pointer");
+    if (!workspace || !error_bits) return fail(FDPP_ERR_INVALID_ARG, "null pointer");
     // the copy waits for the legacy stream alone, not for non-blocking streams
     cudaError_t e = cudaDeviceSynchronize();
-    if (e != cudaSuccess) return cfail(FDPP_ERR_CUDA, "cudaDeviceSynchronize: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return fail(FDPP_ERR_CUDA, "cudaDeviceSynchronize: %s", cudaGetErrorString(e));
     if ((e = cudaMemcpy(error_bits, workspace, 4, cudaMemcpyDeviceToHost)) != cudaSuccess)
-        return cfail(FDPP_ERR_CUDA, "cudaMemcpy: %s", cudaGetErrorString(e));
+        return fail(FDPP_ERR_CUDA, "cudaMemcpy: %s", cudaGetErrorString(e));
     return FDPP_OK;
 }
 

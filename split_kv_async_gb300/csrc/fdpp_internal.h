@@ -138,8 +138,8 @@ fdpp_status get_tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn);
 size_t workspace_zero_prefix(const fdpp_params& p);
 // Offset of the start-up hint region (the zero prefix minus the hint, which may stay stale).
 size_t workspace_hint_offset(const fdpp_params& p);
-// Sets the reason fdpp_last_error() reports on this thread.
-void set_last_error(const char* what);
+// `s`, with the reason that fdpp_last_error() reports on this thread.
+fdpp_status fail(fdpp_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 
 // Resident CTAs per SM of the SIMT split kernel for this shape (0 if it cannot launch).
 int split_simt_ctas_per_sm(const KernelArgs& a, int dtype);

@@ -24,8 +24,6 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <cstdarg>
-#include <cstdio>
 #include <map>
 #include <mutex>
 
@@ -264,17 +262,6 @@ __global__ void __launch_bounds__(G_THREADS, 2)
 
 // ---- host ---------------------------------------------------------------------------------
 
-fdpp_status gfail(fdpp_status s, const char* fmt, ...)
-{
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    set_last_error(buf);
-    return s;
-}
-
 bool shape_ok(int M, int N, int K) { return M >= 1 && M <= FDPP_GEMM_MAX_M && N >= 1 && K >= 8 && K % 8 == 0; }
 
 int padded_m(int M) { return (M + 15) / 16 * 16; }
@@ -369,7 +356,7 @@ fdpp_status encode_2d(CUtensorMap* map, const void* base, int rows, int K, int b
     CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
                      estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return gfail(FDPP_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    if (r != CUDA_SUCCESS) return fail(FDPP_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
     return FDPP_OK;
 }
 
@@ -398,11 +385,11 @@ size_t fdpp_flat_gemm_workspace_size(int M, int N, int K, int split_k_req)
 fdpp_status fdpp_flat_gemm_set_lut(const int32_t* entries, int n_entries)
 {
     if (n_entries < 0 || n_entries > 64 || (n_entries > 0 && !entries))
-        return gfail(FDPP_ERR_INVALID_ARG, "lookup table of %d entries (0 .. 64, 4 ints each)", n_entries);
+        return fail(FDPP_ERR_INVALID_ARG, "lookup table of %d entries (0 .. 64, 4 ints each)", n_entries);
     for (int i = 0; i < n_entries; ++i) {
         const int32_t* e = entries + 4 * i;
         if (e[0] < 1 || e[1] < 1 || e[2] < 8 || e[3] < 1)
-            return gfail(FDPP_ERR_INVALID_ARG, "lookup table entry %d is not (m_max, N, K, split_k) >= (1, 1, 8, 1)", i);
+            return fail(FDPP_ERR_INVALID_ARG, "lookup table entry %d is not (m_max, N, K, split_k) >= (1, 1, 8, 1)", i);
     }
     for (int i = 0; i < n_entries; ++i) g_lut[i] = LutEntry{entries[4 * i], entries[4 * i + 1], entries[4 * i + 2], entries[4 * i + 3]};
     g_lut_n = n_entries;
@@ -413,14 +400,14 @@ fdpp_status fdpp_flat_gemm(const void* x, const void* w, void* y, int M, int N, 
                            size_t workspace_bytes, fdpp_stream stream)
 {
     if (!shape_ok(M, N, K))
-        return gfail(FDPP_ERR_INVALID_ARG, "flat GEMM shape M=%d N=%d K=%d (1 <= M <= %d, N >= 1, K >= 8, K %% 8 == 0)",
+        return fail(FDPP_ERR_INVALID_ARG, "flat GEMM shape M=%d N=%d K=%d (1 <= M <= %d, N >= 1, K >= 8, K %% 8 == 0)",
                      M, N, K, FDPP_GEMM_MAX_M);
-    if (!x || !w || !y || !workspace) return gfail(FDPP_ERR_INVALID_ARG, "null pointer");
-    if (((uintptr_t)x | (uintptr_t)w) % 16 != 0) return gfail(FDPP_ERR_INVALID_ARG, "x and w must be 16-byte aligned");
-    if ((uintptr_t)workspace % 256 != 0) return gfail(FDPP_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (!x || !w || !y || !workspace) return fail(FDPP_ERR_INVALID_ARG, "null pointer");
+    if (((uintptr_t)x | (uintptr_t)w) % 16 != 0) return fail(FDPP_ERR_INVALID_ARG, "x and w must be 16-byte aligned");
+    if ((uintptr_t)workspace % 256 != 0) return fail(FDPP_ERR_WORKSPACE, "workspace must be 256-byte aligned");
     const int kb = (K + GB_K - 1) / GB_K;
     const int kmax = std::min(kb, G_MAX_SPLIT);
-    if (split_k < 0 || split_k > kmax) return gfail(FDPP_ERR_INVALID_ARG, "split_k %d outside 0 .. %d", split_k, kmax);
+    if (split_k < 0 || split_k > kmax) return fail(FDPP_ERR_INVALID_ARG, "split_k %d outside 0 .. %d", split_k, kmax);
     int sms = 0, smem_sm = 0, smem_blk = 0;
     fdpp_status st = query_device(&sms, &smem_sm, &smem_blk);
     if (st != FDPP_OK) return st;
@@ -428,7 +415,7 @@ fdpp_status fdpp_flat_gemm(const void* x, const void* w, void* y, int M, int N, 
     const int split = choose_split(M, N, K, Mp, nstage, split_k);
     const size_t need = ws_bytes(M, N, split);
     if (workspace_bytes < need)
-        return gfail(FDPP_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+        return fail(FDPP_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
 
     GemmArgs g{};
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -451,7 +438,7 @@ fdpp_status fdpp_flat_gemm(const void* x, const void* w, void* y, int M, int N, 
     if ((st = encode_2d(&tx, x, M, K, g.Mp)) != FDPP_OK) return st;
     const int smem = gemm_smem_bytes(Mp, nstage);
     cudaError_t e = allow_dynamic_smem((const void*)flat_gemm_kernel);
-    if (e != cudaSuccess) return gfail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return fail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     // a programmatic dependent of the kernel before it on the stream (see the producer)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(g.n_tiles * split));
@@ -470,18 +457,18 @@ fdpp_status fdpp_flat_gemm(const void* x, const void* w, void* y, int M, int N, 
     cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, flat_gemm_kernel, tw, tx, g);
     if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) return gfail(FDPP_ERR_CUDA, "flat GEMM launch: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return fail(FDPP_ERR_CUDA, "flat GEMM launch: %s", cudaGetErrorString(e));
     return FDPP_OK;
 }
 
 fdpp_status fdpp_flat_gemm_read_error(const void* workspace, uint32_t* error_bits)
 {
-    if (!workspace || !error_bits) return gfail(FDPP_ERR_INVALID_ARG, "null pointer");
+    if (!workspace || !error_bits) return fail(FDPP_ERR_INVALID_ARG, "null pointer");
     // the copy waits for the legacy stream alone, not for non-blocking streams
     cudaError_t e = cudaDeviceSynchronize();
-    if (e != cudaSuccess) return gfail(FDPP_ERR_CUDA, "cudaDeviceSynchronize: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return fail(FDPP_ERR_CUDA, "cudaDeviceSynchronize: %s", cudaGetErrorString(e));
     if ((e = cudaMemcpy(error_bits, workspace, 4, cudaMemcpyDeviceToHost)) != cudaSuccess)
-        return gfail(FDPP_ERR_CUDA, "cudaMemcpy: %s", cudaGetErrorString(e));
+        return fail(FDPP_ERR_CUDA, "cudaMemcpy: %s", cudaGetErrorString(e));
     return FDPP_OK;
 }
 

@@ -14,7 +14,6 @@
 // kernel behind them is kept, since a stale hint only costs a useless L2 prefetch. Calls issued
 // on one stream follow one another safely; calls that overlap on the GPU (different streams, or
 // other threads, without ordering between them) race on the array and give wrong results.
-#include <cstdio>
 
 #include <cuda_runtime.h>
 
@@ -28,12 +27,6 @@ namespace {
 // cached address would go stale if the caller reset the device's primary context).
 static __device__ __align__(256) unsigned char g_noalloc_scratch[FDPP_NOALLOC_WORKSPACE_BYTES];
 
-fdpp_status setup_failed(fdpp_status s, const char* what)
-{
-    fdpp::set_last_error(what);
-    return s;
-}
-
 // The scratch's device address on the current device, after checking that a problem of `p`
 // fits in it.
 fdpp_status scratch_for(const fdpp_params* p, const char* who, void** scratch)
@@ -41,21 +34,14 @@ fdpp_status scratch_for(const fdpp_params* p, const char* who, void** scratch)
     size_t need = 0;
     fdpp_status st = fdpp_workspace_size(p, &need);
     if (st != FDPP_OK) return st;
-    if (need > (size_t)FDPP_NOALLOC_WORKSPACE_BYTES) {
-        char msg[256];
-        std::snprintf(msg, sizeof msg,
-                      "%s: this problem needs %zu bytes of scratch, the static workspace holds "
-                      "%zu; use fdpp_decode_attn with a workspace",
-                      who, need, (size_t)FDPP_NOALLOC_WORKSPACE_BYTES);
-        return setup_failed(FDPP_ERR_WORKSPACE, msg);
-    }
+    if (need > (size_t)FDPP_NOALLOC_WORKSPACE_BYTES)
+        return fdpp::fail(FDPP_ERR_WORKSPACE,
+                          "%s: this problem needs %zu bytes of scratch, the static workspace holds "
+                          "%zu; use fdpp_decode_attn with a workspace",
+                          who, need, (size_t)FDPP_NOALLOC_WORKSPACE_BYTES);
     void* ptr = nullptr;
     const cudaError_t e = cudaGetSymbolAddress(&ptr, g_noalloc_scratch);
-    if (e != cudaSuccess || !ptr) {
-        char msg[256];
-        std::snprintf(msg, sizeof msg, "%s: cudaGetSymbolAddress: %s", who, cudaGetErrorString(e));
-        return setup_failed(FDPP_ERR_CUDA, msg);
-    }
+    if (e != cudaSuccess || !ptr) return fdpp::fail(FDPP_ERR_CUDA, "%s: cudaGetSymbolAddress: %s", who, cudaGetErrorString(e));
     *scratch = ptr;
     return FDPP_OK;
 }
@@ -73,7 +59,7 @@ extern "C" fdpp_status fdpp_decode_attn_noalloc(const void* q, const void* k_cac
     // header (error bits of this call only), plan and fallback lists; not the start-up hint
     const size_t zero = fdpp::workspace_hint_offset(*p);
     if (cudaMemsetAsync(scratch, 0, zero, (cudaStream_t)stream) != cudaSuccess)
-        return setup_failed(FDPP_ERR_CUDA, "fdpp_decode_attn_noalloc: cudaMemsetAsync failed");
+        return fdpp::fail(FDPP_ERR_CUDA, "fdpp_decode_attn_noalloc: cudaMemsetAsync failed");
     return fdpp_decode_attn(q, k_cache, v_cache, block_table, seq_lens, p, scratch,
                             (size_t)FDPP_NOALLOC_WORKSPACE_BYTES, out, stream);
 }

@@ -13,8 +13,6 @@
 // launch (2.2 us in a graph).
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -231,17 +229,6 @@ __global__ void __launch_bounds__(MOST)
     }
 }
 
-fdpp_status nfail(fdpp_status s, const char* fmt, ...)
-{
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    std::vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    set_last_error(buf);
-    return s;
-}
-
 template <typename T, bool E4M3, bool SMALL>
 cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t s)
 {
@@ -266,17 +253,7 @@ cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t s)
         threads = (unsigned)((vectors + v - 1) / v + 31) / 32 * 32;
         grid = (unsigned)std::min(a.T, std::max(1, NORM_RESIDENT / (int)threads) * sms);
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_pdl(kern, dim3(grid), (int)threads, s, a);
 }
 
 }  // namespace
@@ -287,39 +264,39 @@ using namespace fdpp;
 extern "C" fdpp_status fdpp_rms_norm(const void* x, const void* residual, const void* weight, const fdpp_norm_params* p,
                                      void* out, float* scales, void* sum_out, fdpp_stream stream)
 {
-    if (!p) return nfail(FDPP_ERR_INVALID_ARG, "params is NULL");
-    if (p->num_tokens < 0) return nfail(FDPP_ERR_INVALID_ARG, "num_tokens must be >= 0 (got %d)", p->num_tokens);
-    if (p->dim < 8 || p->dim % 8) return nfail(FDPP_ERR_INVALID_ARG, "dim must be a positive multiple of 8 (got %d)", p->dim);
+    if (!p) return fail(FDPP_ERR_INVALID_ARG, "params is NULL");
+    if (p->num_tokens < 0) return fail(FDPP_ERR_INVALID_ARG, "num_tokens must be >= 0 (got %d)", p->num_tokens);
+    if (p->dim < 8 || p->dim % 8) return fail(FDPP_ERR_INVALID_ARG, "dim must be a positive multiple of 8 (got %d)", p->dim);
     if (p->dim > FDPP_NORM_MAX_DIM)
-        return nfail(FDPP_ERR_UNSUPPORTED, "dim %d > %d", p->dim, FDPP_NORM_MAX_DIM);
+        return fail(FDPP_ERR_UNSUPPORTED, "dim %d > %d", p->dim, FDPP_NORM_MAX_DIM);
     if (p->dtype != FDPP_F32 && p->dtype != FDPP_BF16)
-        return nfail(FDPP_ERR_INVALID_ARG, "dtype must be FDPP_F32 or FDPP_BF16 (got %d)", p->dtype);
+        return fail(FDPP_ERR_INVALID_ARG, "dtype must be FDPP_F32 or FDPP_BF16 (got %d)", p->dtype);
     const bool e4m3 = p->out_dtype == FDPP_E4M3;
     if (!e4m3 && p->out_dtype != p->dtype)
-        return nfail(FDPP_ERR_INVALID_ARG, "out_dtype must be dtype or FDPP_E4M3 (got %d)", p->out_dtype);
-    if (!(p->eps >= 0.f) || !std::isfinite(p->eps)) return nfail(FDPP_ERR_INVALID_ARG, "eps must be finite and >= 0");
-    if (!std::isfinite(p->weight_offset)) return nfail(FDPP_ERR_INVALID_ARG, "weight_offset must be finite");
+        return fail(FDPP_ERR_INVALID_ARG, "out_dtype must be dtype or FDPP_E4M3 (got %d)", p->out_dtype);
+    if (!(p->eps >= 0.f) || !std::isfinite(p->eps)) return fail(FDPP_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (!std::isfinite(p->weight_offset)) return fail(FDPP_ERR_INVALID_ARG, "weight_offset must be finite");
     const long long vec = p->dtype == FDPP_F32 ? 4 : 8, out_vec = e4m3 ? 8 : vec, most = 1ll << 40;
     auto stride_ok = [&](long long stride, long long v) { return stride >= p->dim && stride % v == 0 && stride <= most; };
     if (!stride_ok(p->x_stride, vec) || !stride_ok(p->out_stride, out_vec) ||
         (residual && !stride_ok(p->residual_stride, vec)) || (sum_out && !stride_ok(p->sum_stride, vec)))
-        return nfail(FDPP_ERR_INVALID_ARG, "strides must cover a row and be multiples of 16 bytes (an e4m3 output's: of 8)");
+        return fail(FDPP_ERR_INVALID_ARG, "strides must cover a row and be multiples of 16 bytes (an e4m3 output's: of 8)");
     const bool some = p->num_tokens > 0;     // (an empty tensor's address may be NULL)
-    if (some && (!x || !out)) return nfail(FDPP_ERR_INVALID_ARG, "x and out must be non-NULL");
+    if (some && (!x || !out)) return fail(FDPP_ERR_INVALID_ARG, "x and out must be non-NULL");
     if (((uintptr_t)x | (uintptr_t)residual | (uintptr_t)weight | (uintptr_t)out | (uintptr_t)sum_out) % 16 != 0)
-        return nfail(FDPP_ERR_INVALID_ARG, "x, residual, weight, out and sum_out must be 16-byte aligned");
+        return fail(FDPP_ERR_INVALID_ARG, "x, residual, weight, out and sum_out must be 16-byte aligned");
     if (e4m3) {
         if ((some && !scales) || (uintptr_t)scales % 4 != 0)
-            return nfail(FDPP_ERR_INVALID_ARG, "an e4m3 output needs scales, 4-byte aligned");
+            return fail(FDPP_ERR_INVALID_ARG, "an e4m3 output needs scales, 4-byte aligned");
         if (p->scale_stride < (p->dim + FDPP_SCALE_BLOCK - 1) / FDPP_SCALE_BLOCK || p->scale_stride > most)
-            return nfail(FDPP_ERR_INVALID_ARG, "scale_stride must cover a row's scales");
+            return fail(FDPP_ERR_INVALID_ARG, "scale_stride must cover a row's scales");
     } else if (scales) {
-        return nfail(FDPP_ERR_INVALID_ARG, "scales are of an e4m3 output only");
+        return fail(FDPP_ERR_INVALID_ARG, "scales are of an e4m3 output only");
     }
     if (some &&
         ((out == x && (e4m3 || p->out_stride != p->x_stride)) || (sum_out && sum_out == x && p->sum_stride != p->x_stride) ||
          (sum_out && sum_out == residual && p->sum_stride != p->residual_stride) || out == residual || out == sum_out))
-        return nfail(FDPP_ERR_INVALID_ARG, "out may be x, and sum_out residual or x, where types and strides are the same");
+        return fail(FDPP_ERR_INVALID_ARG, "out may be x, and sum_out residual or x, where types and strides are the same");
     int sms = 0, unused = 0;
     const fdpp_status st = query_device(&sms, &unused, &unused);
     if (st != FDPP_OK) return st;
@@ -348,6 +325,6 @@ extern "C" fdpp_status fdpp_rms_norm(const void* x, const void* residual, const 
         return e4m3 ? launch_norm<T, true, false>(a, sms, s) : launch_norm<T, false, false>(a, sms, s);
     };
     const cudaError_t e = p->dtype == FDPP_F32 ? launch(float{}) : launch(__nv_bfloat16{});
-    if (e != cudaSuccess) return nfail(FDPP_ERR_CUDA, "RMS norm launch: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return fail(FDPP_ERR_CUDA, "RMS norm launch: %s", cudaGetErrorString(e));
     return FDPP_OK;
 }

@@ -2,25 +2,12 @@
 // kernel choice and tensor maps.
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 
 #include "rows_internal.h"
 
 using namespace fdpp;
 
 namespace {
-
-fdpp_status rfail(fdpp_status s, const char* fmt, ...)
-{
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    std::vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    set_last_error(buf);
-    return s;
-}
 
 bool aligned(const void* p, size_t a) { return (uintptr_t)p % a == 0; }
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -45,45 +32,45 @@ int simt_splits(const fdpp_rows_params& p)
 
 fdpp_status check_params(const fdpp_rows_params* p)
 {
-    if (!p) return rfail(FDPP_ERR_INVALID_ARG, "params is NULL");
-    if (p->batch < 1) return rfail(FDPP_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", p->batch);
-    if (p->num_q_heads < 1 || p->num_kv_heads < 1) return rfail(FDPP_ERR_INVALID_ARG, "head counts must be >= 1");
+    if (!p) return fail(FDPP_ERR_INVALID_ARG, "params is NULL");
+    if (p->batch < 1) return fail(FDPP_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", p->batch);
+    if (p->num_q_heads < 1 || p->num_kv_heads < 1) return fail(FDPP_ERR_INVALID_ARG, "head counts must be >= 1");
     if (p->num_q_heads % p->num_kv_heads)
-        return rfail(FDPP_ERR_INVALID_ARG, "num_q_heads (%d) is not a multiple of num_kv_heads (%d)", p->num_q_heads,
+        return fail(FDPP_ERR_INVALID_ARG, "num_q_heads (%d) is not a multiple of num_kv_heads (%d)", p->num_q_heads,
                      p->num_kv_heads);
     if (p->dtype != FDPP_F32 && p->dtype != FDPP_BF16)
-        return rfail(FDPP_ERR_INVALID_ARG, "dtype must be FDPP_F32 or FDPP_BF16 (got %d)", p->dtype);
+        return fail(FDPP_ERR_INVALID_ARG, "dtype must be FDPP_F32 or FDPP_BF16 (got %d)", p->dtype);
     if (p->head_dim != 64 && p->head_dim != 128)
-        return rfail(FDPP_ERR_UNSUPPORTED, "head_dim %d: only 64 and 128 are built", p->head_dim);
+        return fail(FDPP_ERR_UNSUPPORTED, "head_dim %d: only 64 and 128 are built", p->head_dim);
     if (p->num_q_heads / p->num_kv_heads > FDPP_ROWS_MAX_GROUP)
-        return rfail(FDPP_ERR_UNSUPPORTED, "%d query heads per kv head > %d", p->num_q_heads / p->num_kv_heads,
+        return fail(FDPP_ERR_UNSUPPORTED, "%d query heads per kv head > %d", p->num_q_heads / p->num_kv_heads,
                      FDPP_ROWS_MAX_GROUP);
-    if (p->num_tokens < 1) return rfail(FDPP_ERR_INVALID_ARG, "num_tokens must be >= 1");
-    if (p->max_seq_len < 1) return rfail(FDPP_ERR_INVALID_ARG, "max_seq_len must be >= 1");
-    if (p->max_prefix_len < 0) return rfail(FDPP_ERR_INVALID_ARG, "max_prefix_len must be >= 0");
+    if (p->num_tokens < 1) return fail(FDPP_ERR_INVALID_ARG, "num_tokens must be >= 1");
+    if (p->max_seq_len < 1) return fail(FDPP_ERR_INVALID_ARG, "max_seq_len must be >= 1");
+    if (p->max_prefix_len < 0) return fail(FDPP_ERR_INVALID_ARG, "max_prefix_len must be >= 0");
     // (both are turned into units of log2: an infinite factor would make NaN of a score of 0)
     if (!std::isfinite(p->scale * 1.4426950f) || !(p->scale > 0.f))
-        return rfail(FDPP_ERR_INVALID_ARG, "scale must be positive, and scale * log2(e) finite (got %g)", (double)p->scale);
+        return fail(FDPP_ERR_INVALID_ARG, "scale must be positive, and scale * log2(e) finite (got %g)", (double)p->scale);
     if (!std::isfinite(p->softcap * 1.4426950f) || p->softcap < 0.f)
-        return rfail(FDPP_ERR_INVALID_ARG, "softcap must be 0 or positive, and softcap * log2(e) finite (got %g)", (double)p->softcap);
+        return fail(FDPP_ERR_INVALID_ARG, "softcap must be 0 or positive, and softcap * log2(e) finite (got %g)", (double)p->softcap);
     // the tensor kernel's tanh is off by a few 2^-23 softcap: above this limit by more than its weights are
     if (tensor_kernel(*p) && p->softcap > FDPP_ROWS_MAX_SOFTCAP)
-        return rfail(FDPP_ERR_UNSUPPORTED, "softcap %g > %g", (double)p->softcap, (double)FDPP_ROWS_MAX_SOFTCAP);
+        return fail(FDPP_ERR_UNSUPPORTED, "softcap %g > %g", (double)p->softcap, (double)FDPP_ROWS_MAX_SOFTCAP);
     if (p->softcap > 0.f && !std::isfinite(2.f * p->scale * 1.4426950f / p->softcap))
-        return rfail(FDPP_ERR_INVALID_ARG, "scale / softcap overflows");
+        return fail(FDPP_ERR_INVALID_ARG, "scale / softcap overflows");
     if (p->kernel < FDPP_KERNEL_AUTO || p->kernel > FDPP_KERNEL_SIMT)
-        return rfail(FDPP_ERR_INVALID_ARG, "unknown kernel %d", p->kernel);
+        return fail(FDPP_ERR_INVALID_ARG, "unknown kernel %d", p->kernel);
     if (p->kernel == FDPP_KERNEL_TENSOR && p->dtype != FDPP_BF16)
-        return rfail(FDPP_ERR_UNSUPPORTED, "tensor kernel needs bf16");
+        return fail(FDPP_ERR_UNSUPPORTED, "tensor kernel needs bf16");
     if (!aligned(p->slopes, 4) || !aligned(p->key_begin, 4) || !aligned(p->key_end, 4))
-        return rfail(FDPP_ERR_INVALID_ARG, "slopes, key_begin and key_end must be 4-byte aligned");
+        return fail(FDPP_ERR_INVALID_ARG, "slopes, key_begin and key_end must be 4-byte aligned");
     // positions, key tiles and row counts stay within 32 bits
     const long long keys = (long long)p->max_seq_len + p->max_prefix_len;
     const int G = p->num_q_heads / p->num_kv_heads, tpt = ROWS_TILE / G;
     const long long rt = p->batch + 2ll * ((p->num_tokens + 2ll * tpt - 1) / (2 * tpt)) + 1;
     if (keys > (1ll << 30) || rt * p->num_kv_heads > (1ll << 31) / (keys / ROWS_KEYS + 8) ||
         (long long)p->num_tokens * p->num_q_heads >= (1ll << 31) / 2 || simt_units(*p) >= (1ll << 31) - 1)
-        return rfail(FDPP_ERR_INVALID_ARG, "problem too large for one call");
+        return fail(FDPP_ERR_INVALID_ARG, "problem too large for one call");
     return FDPP_OK;
 }
 
@@ -91,8 +78,8 @@ fdpp_status check_tree(const fdpp_rows_params* p)
 {
     const fdpp_status st = check_params(p);
     if (st != FDPP_OK) return st;
-    if (p->slopes) return rfail(FDPP_ERR_UNSUPPORTED, "a tree's keys have no bias on distance: slopes must be NULL");
-    if (p->key_end) return rfail(FDPP_ERR_INVALID_ARG, "the tree says which keys a token sees last: key_end must be NULL");
+    if (p->slopes) return fail(FDPP_ERR_UNSUPPORTED, "a tree's keys have no bias on distance: slopes must be NULL");
+    if (p->key_end) return fail(FDPP_ERR_INVALID_ARG, "the tree says which keys a token sees last: key_end must be NULL");
     return FDPP_OK;
 }
 
@@ -114,11 +101,11 @@ fdpp_rows_params tree_params(const fdpp_rows_params& p)
 fdpp_status check_paged(const fdpp_rows_params* p)
 {
     if (p->block_size < 16 || p->block_size > 256 || (p->block_size & (p->block_size - 1)))
-        return rfail(FDPP_ERR_INVALID_ARG, "block_size must be a power of two in [16, 256] (got %d)", p->block_size);
-    if (p->max_blocks_per_seq < 1) return rfail(FDPP_ERR_INVALID_ARG, "max_blocks_per_seq must be >= 1");
-    if (p->num_kv_blocks < 1) return rfail(FDPP_ERR_INVALID_ARG, "num_kv_blocks must be >= 1");
+        return fail(FDPP_ERR_INVALID_ARG, "block_size must be a power of two in [16, 256] (got %d)", p->block_size);
+    if (p->max_blocks_per_seq < 1) return fail(FDPP_ERR_INVALID_ARG, "max_blocks_per_seq must be >= 1");
+    if (p->num_kv_blocks < 1) return fail(FDPP_ERR_INVALID_ARG, "num_kv_blocks must be >= 1");
     if ((long long)p->max_seq_len > (long long)p->max_blocks_per_seq * p->block_size)
-        return rfail(FDPP_ERR_INVALID_ARG, "max_seq_len exceeds max_blocks_per_seq * block_size");
+        return fail(FDPP_ERR_INVALID_ARG, "max_seq_len exceeds max_blocks_per_seq * block_size");
     return FDPP_OK;
 }
 
@@ -137,7 +124,7 @@ fdpp_status encode_cache(CUtensorMap* map, const void* base, const fdpp_rows_par
     const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return rfail(FDPP_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    if (r != CUDA_SUCCESS) return fail(FDPP_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
     return FDPP_OK;
 }
 
@@ -157,7 +144,7 @@ fdpp_status encode_q(CUtensorMap* map, const void* q, const fdpp_rows_params& p,
     const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return rfail(FDPP_ERR_CUDA, "cuTensorMapEncodeTiled (q) failed (%d)", (int)r);
+    if (r != CUDA_SUCCESS) return fail(FDPP_ERR_CUDA, "cuTensorMapEncodeTiled (q) failed (%d)", (int)r);
     return FDPP_OK;
 }
 
@@ -177,31 +164,31 @@ fdpp_status attend(const void* q, const void* prefix_k, const void* prefix_v, co
     const bool paged = block_table != nullptr;
     if (paged && (st = check_paged(p)) != FDPP_OK) return st;
     if (!q || !k_cache || !v_cache || !seq_lens || !out)
-        return rfail(FDPP_ERR_INVALID_ARG, "q, k_cache, v_cache, seq_lens and out must be non-NULL");
+        return fail(FDPP_ERR_INVALID_ARG, "q, k_cache, v_cache, seq_lens and out must be non-NULL");
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
-        return rfail(FDPP_ERR_INVALID_ARG, "q, k_cache, v_cache and out must be 16-byte aligned");
+        return fail(FDPP_ERR_INVALID_ARG, "q, k_cache, v_cache and out must be 16-byte aligned");
     if (!aligned(seq_lens, 4) || !aligned(block_table, 4) || !aligned(cu_tokens, 4))
-        return rfail(FDPP_ERR_INVALID_ARG, "seq_lens, block_table and cu_tokens must be 4-byte aligned");
+        return fail(FDPP_ERR_INVALID_ARG, "seq_lens, block_table and cu_tokens must be 4-byte aligned");
     if (!cu_tokens && p->num_tokens % p->batch)
-        return rfail(FDPP_ERR_INVALID_ARG, "without cu_tokens num_tokens (%d) must be a multiple of batch (%d)",
+        return fail(FDPP_ERR_INVALID_ARG, "without cu_tokens num_tokens (%d) must be a multiple of batch (%d)",
                      p->num_tokens, p->batch);
     if (prefix) {
-        if (p->max_prefix_len < 1) return rfail(FDPP_ERR_INVALID_ARG, "max_prefix_len must be >= 1");
+        if (p->max_prefix_len < 1) return fail(FDPP_ERR_INVALID_ARG, "max_prefix_len must be >= 1");
         if (!prefix_len || !aligned(prefix_len, 4))
-            return rfail(FDPP_ERR_INVALID_ARG, "prefix_len must be non-NULL and 4-byte aligned");
+            return fail(FDPP_ERR_INVALID_ARG, "prefix_len must be non-NULL and 4-byte aligned");
         if (paged && (!prefix_blocks || prefix_k || prefix_v))
-            return rfail(FDPP_ERR_INVALID_ARG, "paged caches take prefix_blocks, and no prefix_k or prefix_v");
+            return fail(FDPP_ERR_INVALID_ARG, "paged caches take prefix_blocks, and no prefix_k or prefix_v");
         if (!paged && (!prefix_k || !prefix_v || prefix_blocks))
-            return rfail(FDPP_ERR_INVALID_ARG, "contiguous caches take prefix_k and prefix_v, and no prefix_blocks");
+            return fail(FDPP_ERR_INVALID_ARG, "contiguous caches take prefix_k and prefix_v, and no prefix_blocks");
         if (!aligned(prefix_k, 16) || !aligned(prefix_v, 16) || !aligned(prefix_blocks, 4))
-            return rfail(FDPP_ERR_INVALID_ARG, "prefix_k and prefix_v must be 16-byte, prefix_blocks 4-byte aligned");
+            return fail(FDPP_ERR_INVALID_ARG, "prefix_k and prefix_v must be 16-byte, prefix_blocks 4-byte aligned");
     }
-    if (!workspace) return rfail(FDPP_ERR_WORKSPACE, "workspace is NULL");
-    if (!aligned(workspace, 256)) return rfail(FDPP_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (!workspace) return fail(FDPP_ERR_WORKSPACE, "workspace is NULL");
+    if (!aligned(workspace, 256)) return fail(FDPP_ERR_WORKSPACE, "workspace must be 256-byte aligned");
     const RowsLayout w = rows_layout(*p);
     const size_t need = parents ? tree_bytes(*p) : w.total;
     if (workspace_bytes < need)
-        return rfail(FDPP_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+        return fail(FDPP_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
     int sms = 0, smem_sm = 0, smem_blk = 0;
     if ((st = query_device(&sms, &smem_sm, &smem_blk)) != FDPP_OK) return st;
 
@@ -258,12 +245,12 @@ fdpp_status attend(const void* q, const void* prefix_k, const void* prefix_v, co
     if (!tensor_kernel(*p)) {
         a.splits = simt_splits(*p);
         const cudaError_t e = launch_rows_simt(a, p->dtype, s);
-        if (e != cudaSuccess) return rfail(FDPP_ERR_CUDA, "rows kernel launch: %s", cudaGetErrorString(e));
+        if (e != cudaSuccess) return fail(FDPP_ERR_CUDA, "rows kernel launch: %s", cudaGetErrorString(e));
         return FDPP_OK;
     }
     a.parts = std::min(sms, ROWS_MAX_PARTS);
     a.stages = rows_tc_stages(a.D, std::min(smem_blk, smem_sm - 1024));
-    if (a.stages < 4) return rfail(FDPP_ERR_UNSUPPORTED, "too little shared memory for the tensor kernel");
+    if (a.stages < 4) return fail(FDPP_ERR_UNSUPPORTED, "too little shared memory for the tensor kernel");
     const int box = paged ? std::min(p->block_size, ROWS_KEYS) : ROWS_KEYS;
     const long long rows = paged ? p->block_size : p->max_seq_len, outer = paged ? p->num_kv_blocks : p->batch;
     RowsMaps m;
@@ -278,7 +265,7 @@ fdpp_status attend(const void* q, const void* prefix_k, const void* prefix_v, co
         if ((st = encode_cache(&m.pv, prefix_v, *p, p->max_prefix_len, 1, ROWS_KEYS)) != FDPP_OK) return st;
     }
     const cudaError_t e = launch_rows_tc(a, m, s);
-    if (e != cudaSuccess) return rfail(FDPP_ERR_CUDA, "rows kernel launch: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return fail(FDPP_ERR_CUDA, "rows kernel launch: %s", cudaGetErrorString(e));
     return FDPP_OK;
 }
 
@@ -329,7 +316,7 @@ fdpp_status fdpp_rows_workspace_size(const fdpp_rows_params* p, size_t* bytes)
 {
     const fdpp_status st = check_params(p);
     if (st != FDPP_OK) return st;
-    if (!bytes) return rfail(FDPP_ERR_INVALID_ARG, "bytes is NULL");
+    if (!bytes) return fail(FDPP_ERR_INVALID_ARG, "bytes is NULL");
     *bytes = rows_layout(*p).total;
     return FDPP_OK;
 }
@@ -356,7 +343,7 @@ fdpp_status fdpp_tree_workspace_size(const fdpp_rows_params* p, size_t* bytes)
 {
     const fdpp_status st = check_tree(p);
     if (st != FDPP_OK) return st;
-    if (!bytes) return rfail(FDPP_ERR_INVALID_ARG, "bytes is NULL");
+    if (!bytes) return fail(FDPP_ERR_INVALID_ARG, "bytes is NULL");
     *bytes = tree_bytes(tree_params(*p));
     return FDPP_OK;
 }
@@ -368,7 +355,7 @@ fdpp_status fdpp_tree_attn(const void* q, const void* k_cache, const void* v_cac
 {
     const fdpp_status st = check_tree(p);
     if (st != FDPP_OK) return st;
-    if (!parents || !aligned(parents, 4)) return rfail(FDPP_ERR_INVALID_ARG, "parents must be non-NULL and 4-byte aligned");
+    if (!parents || !aligned(parents, 4)) return fail(FDPP_ERR_INVALID_ARG, "parents must be non-NULL and 4-byte aligned");
     const fdpp_rows_params t = tree_params(*p);
     return attend(q, nullptr, nullptr, nullptr, nullptr, false, k_cache, v_cache, block_table, seq_lens, cu_tokens, parents,
                   &t, workspace, workspace_bytes, out, stream);

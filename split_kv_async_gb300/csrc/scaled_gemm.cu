@@ -30,8 +30,6 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <cstdarg>
-#include <cstdio>
 #include <map>
 #include <mutex>
 
@@ -818,36 +816,25 @@ __global__ void __launch_bounds__(TileSmem<BN, PAIR>::THREADS, 1)
 
 // ---- host ---------------------------------------------------------------------------------
 
-fdpp_status sfail(fdpp_status s, const char* fmt, ...)
-{
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    set_last_error(buf);
-    return s;
-}
-
 int blocks_of(int K) { return (K + SB - 1) / SB; }
 
 fdpp_status check_params(const fdpp_scaled_gemm_params* p)
 {
-    if (!p) return sfail(FDPP_ERR_INVALID_ARG, "params is NULL");
+    if (!p) return fail(FDPP_ERR_INVALID_ARG, "params is NULL");
     if (p->M < 0 || p->N < 1 || p->K < 16 || p->K % 16)
-        return sfail(FDPP_ERR_INVALID_ARG, "scaled GEMM shape M=%d N=%d K=%d (M >= 0, N >= 1, K >= 16, K %% 16 == 0)", p->M,
+        return fail(FDPP_ERR_INVALID_ARG, "scaled GEMM shape M=%d N=%d K=%d (M >= 0, N >= 1, K >= 16, K %% 16 == 0)", p->M,
                      p->N, p->K);
-    if (p->N > (1 << 30) || p->K > (1 << 30) || p->M > (1 << 30)) return sfail(FDPP_ERR_INVALID_ARG, "problem too large for one call");
+    if (p->N > (1 << 30) || p->K > (1 << 30) || p->M > (1 << 30)) return fail(FDPP_ERR_INVALID_ARG, "problem too large for one call");
     if (p->out_dtype != FDPP_F32 && p->out_dtype != FDPP_BF16)
-        return sfail(FDPP_ERR_INVALID_ARG, "out_dtype must be FDPP_F32 or FDPP_BF16 (got %d)", p->out_dtype);
+        return fail(FDPP_ERR_INVALID_ARG, "out_dtype must be FDPP_F32 or FDPP_BF16 (got %d)", p->out_dtype);
     const long long most = 1ll << 39;    // of a tensor map's strides
     if (p->x_stride < p->K || p->w_stride < p->K || p->x_stride % 16 || p->w_stride % 16 || p->x_stride > most || p->w_stride > most)
-        return sfail(FDPP_ERR_INVALID_ARG, "x_stride and w_stride must cover a row and be multiples of 16 bytes");
-    if (p->y_stride < p->N || p->y_stride > most) return sfail(FDPP_ERR_INVALID_ARG, "y_stride must cover a row");
+        return fail(FDPP_ERR_INVALID_ARG, "x_stride and w_stride must cover a row and be multiples of 16 bytes");
+    if (p->y_stride < p->N || p->y_stride > most) return fail(FDPP_ERR_INVALID_ARG, "y_stride must cover a row");
     if (p->x_scale_stride < blocks_of(p->K) || p->x_scale_stride > most)
-        return sfail(FDPP_ERR_INVALID_ARG, "x_scale_stride must cover a row's scales");
+        return fail(FDPP_ERR_INVALID_ARG, "x_scale_stride must cover a row's scales");
     if (p->split_k < 0 || p->split_k > std::min(blocks_of(p->K), SG_MAX_SPLIT))
-        return sfail(FDPP_ERR_INVALID_ARG, "split_k %d outside 0 .. %d", p->split_k, std::min(blocks_of(p->K), SG_MAX_SPLIT));
+        return fail(FDPP_ERR_INVALID_ARG, "split_k %d outside 0 .. %d", p->split_k, std::min(blocks_of(p->K), SG_MAX_SPLIT));
     return FDPP_OK;
 }
 
@@ -863,7 +850,7 @@ fdpp_status encode_rows(CUtensorMap* map, const void* base, int rows, int K, lon
     const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return sfail(FDPP_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    if (r != CUDA_SUCCESS) return fail(FDPP_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
     return FDPP_OK;
 }
 
@@ -936,7 +923,7 @@ fdpp_status launch_rows(const fdpp_scaled_gemm_params& p, ScaledArgs& g, const v
     const int nr = g.Mp <= 16 ? 16 : g.Mp <= 32 ? 32 : 64, threads = R_THREADS + 128 * rows_sets(nr);
     const SgKernel kern = p.out_dtype == FDPP_F32 ? rows_kernel<float>(g.Mp) : rows_kernel<__nv_bfloat16>(g.Mp);
     cudaError_t e = allow_dynamic_smem((const void*)kern);
-    if (e != cudaSuccess) return sfail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return fail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     g.split_k = p.split_k ? p.split_k : choose_split(kern, tiles, g.kb, threads, smem, 2, sms);
     CUtensorMap tw, tx;
     fdpp_status st;
@@ -957,7 +944,7 @@ fdpp_status launch_rows(const fdpp_scaled_gemm_params& p, ScaledArgs& g, const v
     cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, kern, tw, tx, g);
     if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) return sfail(FDPP_ERR_CUDA, "scaled GEMM launch: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return fail(FDPP_ERR_CUDA, "scaled GEMM launch: %s", cudaGetErrorString(e));
     return FDPP_OK;
 }
 
@@ -966,10 +953,10 @@ fdpp_status launch_tile(const fdpp_scaled_gemm_params& p, ScaledArgs& g, const v
                         cudaStream_t s)
 {
     constexpr int smem = TileSmem<BN, PAIR>::TOTAL, rows = PAIR ? 2 * SG_ROWS : SG_ROWS, threads = TileSmem<BN, PAIR>::THREADS;
-    if (smem > smem_blk) return sfail(FDPP_ERR_UNSUPPORTED, "too little shared memory for the tile kernel");
+    if (smem > smem_blk) return fail(FDPP_ERR_UNSUPPORTED, "too little shared memory for the tile kernel");
     const long long m_tiles = ((long long)p.M + rows - 1) / rows, n_tiles = ((long long)p.N + BN - 1) / BN;
     if (m_tiles * n_tiles >= (1ll << 31) - sms || T_GROUP * n_tiles >= (1ll << 31))
-        return sfail(FDPP_ERR_INVALID_ARG, "problem too large for one call");
+        return fail(FDPP_ERR_INVALID_ARG, "problem too large for one call");
     g.m_tiles = (int)m_tiles;
     g.n_tiles = (int)n_tiles;
     CUtensorMap tw, tx;
@@ -982,12 +969,12 @@ fdpp_status launch_tile(const fdpp_scaled_gemm_params& p, ScaledArgs& g, const v
     if constexpr (!PAIR) {
         const SgKernel split = scaled_tile_kernel<T, BN, PAIR, true>;
         if ((e = allow_dynamic_smem((const void*)split)) != cudaSuccess)
-            return sfail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+            return fail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         g.split_k = p.split_k ? p.split_k : choose_split(split, m_tiles * n_tiles, g.kb, threads, smem, 1, sms);
         if (g.split_k > 1) kern = split;
     }
     if ((e = allow_dynamic_smem((const void*)kern)) != cudaSuccess)
-        return sfail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        return fail(FDPP_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     const int cluster = PAIR ? 2 : g.split_k;
     const long long tiles = m_tiles * n_tiles;
     cudaLaunchConfig_t cfg = {};
@@ -1005,7 +992,7 @@ fdpp_status launch_tile(const fdpp_scaled_gemm_params& p, ScaledArgs& g, const v
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, kern, tx, tw, g);
     if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) return sfail(FDPP_ERR_CUDA, "scaled GEMM launch: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return fail(FDPP_ERR_CUDA, "scaled GEMM launch: %s", cudaGetErrorString(e));
     return FDPP_OK;
 }
 
@@ -1025,13 +1012,13 @@ try {
     fdpp_status st = check_params(p);
     if (st != FDPP_OK) return st;
     if (!w || !w_scales || (p->M > 0 && (!x || !x_scales || !y)))    // (an empty tensor's address may be NULL)
-        return sfail(FDPP_ERR_INVALID_ARG, "x, w, their scales and y must be non-NULL");
-    if (((uintptr_t)x | (uintptr_t)w) % 16 != 0) return sfail(FDPP_ERR_INVALID_ARG, "x and w must be 16-byte aligned");
-    if (((uintptr_t)x_scales | (uintptr_t)w_scales) % 4 != 0) return sfail(FDPP_ERR_INVALID_ARG, "scales must be 4-byte aligned");
-    if ((uintptr_t)y % (p->out_dtype == FDPP_F32 ? 4 : 2) != 0) return sfail(FDPP_ERR_INVALID_ARG, "y must be aligned to its elements");
-    if (!workspace) return sfail(FDPP_ERR_WORKSPACE, "workspace is NULL");
-    if ((uintptr_t)workspace % 256 != 0) return sfail(FDPP_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-    if (workspace_bytes < 256) return sfail(FDPP_ERR_WORKSPACE, "workspace has %zu bytes, 256 needed", workspace_bytes);
+        return fail(FDPP_ERR_INVALID_ARG, "x, w, their scales and y must be non-NULL");
+    if (((uintptr_t)x | (uintptr_t)w) % 16 != 0) return fail(FDPP_ERR_INVALID_ARG, "x and w must be 16-byte aligned");
+    if (((uintptr_t)x_scales | (uintptr_t)w_scales) % 4 != 0) return fail(FDPP_ERR_INVALID_ARG, "scales must be 4-byte aligned");
+    if ((uintptr_t)y % (p->out_dtype == FDPP_F32 ? 4 : 2) != 0) return fail(FDPP_ERR_INVALID_ARG, "y must be aligned to its elements");
+    if (!workspace) return fail(FDPP_ERR_WORKSPACE, "workspace is NULL");
+    if ((uintptr_t)workspace % 256 != 0) return fail(FDPP_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (workspace_bytes < 256) return fail(FDPP_ERR_WORKSPACE, "workspace has %zu bytes, 256 needed", workspace_bytes);
     int sms = 0, smem_sm = 0, smem_blk = 0;
     if ((st = query_device(&sms, &smem_sm, &smem_blk)) != FDPP_OK) return st;
     if (p->M == 0) return FDPP_OK;
@@ -1071,7 +1058,7 @@ try {
     };
     return p->out_dtype == FDPP_F32 ? launch(float{}) : launch(__nv_bfloat16{});
 } catch (...) {                          // (the cache of cluster counts allocates)
-    return sfail(FDPP_ERR_CUDA, "out of host memory");
+    return fail(FDPP_ERR_CUDA, "out of host memory");
 }
 
 }  // extern "C"

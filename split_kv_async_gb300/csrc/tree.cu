@@ -1,8 +1,6 @@
 // tree.cu -- trees of drafted tokens (fdpp_tree.h): the tokens' lineage, which the rows attention's kernels mask
 // by, and the commit of an accepted path.
 #include <algorithm>
-#include <cstdarg>
-#include <cstdio>
 
 #include "rows_common.cuh"
 
@@ -195,41 +193,14 @@ __global__ void __launch_bounds__(COMMIT_THREADS) tree_commit_kernel(const __gri
     }
 }
 
-template <typename... Args>
-cudaError_t launch_pdl(void (*kern)(Args...), dim3 grid, int threads, cudaStream_t s, Args... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-    return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-fdpp_status tfail(fdpp_status s, const char* fmt, ...)
-{
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    std::vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    set_last_error(buf);
-    return s;
-}
-
 fdpp_status check_params(const fdpp_commit_params* p)
 {
-    if (!p) return tfail(FDPP_ERR_INVALID_ARG, "params is NULL");
-    if (p->batch < 1 || p->batch > 65535) return tfail(FDPP_ERR_INVALID_ARG, "batch must be in [1, 65535] (got %d)", p->batch);
-    if (p->num_tokens < 0) return tfail(FDPP_ERR_INVALID_ARG, "num_tokens must be >= 0 (got %d)", p->num_tokens);
-    if (p->max_seq_len < 1) return tfail(FDPP_ERR_INVALID_ARG, "max_seq_len must be >= 1");
+    if (!p) return fail(FDPP_ERR_INVALID_ARG, "params is NULL");
+    if (p->batch < 1 || p->batch > 65535) return fail(FDPP_ERR_INVALID_ARG, "batch must be in [1, 65535] (got %d)", p->batch);
+    if (p->num_tokens < 0) return fail(FDPP_ERR_INVALID_ARG, "num_tokens must be >= 0 (got %d)", p->num_tokens);
+    if (p->max_seq_len < 1) return fail(FDPP_ERR_INVALID_ARG, "max_seq_len must be >= 1");
     if (p->row_bytes < 16 || p->row_bytes % 16 || p->row_bytes > (1ll << 24))
-        return tfail(FDPP_ERR_INVALID_ARG, "row_bytes must be a positive multiple of 16, at most 2^24 (got %lld)", p->row_bytes);
+        return fail(FDPP_ERR_INVALID_ARG, "row_bytes must be a positive multiple of 16, at most 2^24 (got %lld)", p->row_bytes);
     return FDPP_OK;
 }
 
@@ -268,36 +239,36 @@ fdpp_status fdpp_tree_commit(const int32_t* parents, const int32_t* tokens, cons
     fdpp_status st = check_params(p);
     if (st != FDPP_OK) return st;
     if (!cu_tokens && p->num_tokens % p->batch)
-        return tfail(FDPP_ERR_INVALID_ARG, "without cu_tokens num_tokens (%d) must be a multiple of batch (%d)", p->num_tokens,
+        return fail(FDPP_ERR_INVALID_ARG, "without cu_tokens num_tokens (%d) must be a multiple of batch (%d)", p->num_tokens,
                      p->batch);
     if (block_table) {
         if (p->block_size < 16 || p->block_size > 256 || (p->block_size & (p->block_size - 1)))
-            return tfail(FDPP_ERR_INVALID_ARG, "block_size must be a power of two in [16, 256] (got %d)", p->block_size);
+            return fail(FDPP_ERR_INVALID_ARG, "block_size must be a power of two in [16, 256] (got %d)", p->block_size);
         if (p->max_blocks_per_seq < 1 || p->num_kv_blocks < 1)
-            return tfail(FDPP_ERR_INVALID_ARG, "max_blocks_per_seq and num_kv_blocks must be >= 1");
+            return fail(FDPP_ERR_INVALID_ARG, "max_blocks_per_seq and num_kv_blocks must be >= 1");
         if ((long long)p->max_seq_len > (long long)p->max_blocks_per_seq * p->block_size)
-            return tfail(FDPP_ERR_INVALID_ARG, "max_seq_len exceeds max_blocks_per_seq * block_size");
+            return fail(FDPP_ERR_INVALID_ARG, "max_seq_len exceeds max_blocks_per_seq * block_size");
     }
-    if (!seq_lens || !new_lens || !accepted) return tfail(FDPP_ERR_INVALID_ARG, "seq_lens, new_lens and accepted must be non-NULL");
+    if (!seq_lens || !new_lens || !accepted) return fail(FDPP_ERR_INVALID_ARG, "seq_lens, new_lens and accepted must be non-NULL");
     if (p->num_tokens > 0 && (!parents || !tokens || !choices || !path || !chosen))
-        return tfail(FDPP_ERR_INVALID_ARG, "parents, tokens, choices, path and chosen must be non-NULL");
+        return fail(FDPP_ERR_INVALID_ARG, "parents, tokens, choices, path and chosen must be non-NULL");
     if ((((uintptr_t)parents | (uintptr_t)tokens | (uintptr_t)choices | (uintptr_t)seq_lens | (uintptr_t)cu_tokens |
           (uintptr_t)block_table | (uintptr_t)new_lens | (uintptr_t)accepted | (uintptr_t)path | (uintptr_t)chosen) % 4) != 0)
-        return tfail(FDPP_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+        return fail(FDPP_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
     if (new_lens == seq_lens || accepted == seq_lens || new_lens == accepted)
-        return tfail(FDPP_ERR_INVALID_ARG, "seq_lens, new_lens and accepted must be different arrays");
+        return fail(FDPP_ERR_INVALID_ARG, "seq_lens, new_lens and accepted must be different arrays");
     for (const int32_t* in : {parents, tokens, choices})
-        if (in && (in == path || in == chosen)) return tfail(FDPP_ERR_INVALID_ARG, "path and chosen must not be an input");
-    if (path && path == chosen) return tfail(FDPP_ERR_INVALID_ARG, "path and chosen must be different arrays");
+        if (in && (in == path || in == chosen)) return fail(FDPP_ERR_INVALID_ARG, "path and chosen must not be an input");
+    if (path && path == chosen) return fail(FDPP_ERR_INVALID_ARG, "path and chosen must be different arrays");
     if (num_caches < 0 || num_caches > FDPP_TREE_MAX_CACHES || (num_caches > 0 && !caches))
-        return tfail(FDPP_ERR_INVALID_ARG, "num_caches %d outside 0 .. %d, or caches is NULL", num_caches, FDPP_TREE_MAX_CACHES);
+        return fail(FDPP_ERR_INVALID_ARG, "num_caches %d outside 0 .. %d, or caches is NULL", num_caches, FDPP_TREE_MAX_CACHES);
     for (int i = 0; i < num_caches; ++i)
         if (!caches[i] || (uintptr_t)caches[i] % 16 != 0)
-            return tfail(FDPP_ERR_INVALID_ARG, "cache %d must be non-NULL and 16-byte aligned", i);
-    if (repeated(caches, num_caches)) return tfail(FDPP_ERR_INVALID_ARG, "a cache is given twice");
-    if (!workspace) return tfail(FDPP_ERR_WORKSPACE, "workspace is NULL");
-    if ((uintptr_t)workspace % 256 != 0) return tfail(FDPP_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-    if (workspace_bytes < 256) return tfail(FDPP_ERR_WORKSPACE, "workspace has %zu bytes, 256 needed", workspace_bytes);
+            return fail(FDPP_ERR_INVALID_ARG, "cache %d must be non-NULL and 16-byte aligned", i);
+    if (repeated(caches, num_caches)) return fail(FDPP_ERR_INVALID_ARG, "a cache is given twice");
+    if (!workspace) return fail(FDPP_ERR_WORKSPACE, "workspace is NULL");
+    if ((uintptr_t)workspace % 256 != 0) return fail(FDPP_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (workspace_bytes < 256) return fail(FDPP_ERR_WORKSPACE, "workspace has %zu bytes, 256 needed", workspace_bytes);
     int sms = 0, unused = 0;
     if ((st = query_device(&sms, &unused, &unused)) != FDPP_OK) return st;
 
@@ -332,7 +303,7 @@ fdpp_status fdpp_tree_commit(const int32_t* parents, const int32_t* tokens, cons
     const cudaError_t e = num_caches <= 16   ? launch(CommitArgs<16>{})
                           : num_caches <= 64 ? launch(CommitArgs<64>{})
                                              : launch(CommitArgs<FDPP_TREE_MAX_CACHES>{});
-    if (e != cudaSuccess) return tfail(FDPP_ERR_CUDA, "tree commit launch: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return fail(FDPP_ERR_CUDA, "tree commit launch: %s", cudaGetErrorString(e));
     return FDPP_OK;
 }
 
