@@ -573,6 +573,17 @@ __global__ void __launch_bounds__(TileSmem<BN, PAIR>::THREADS, 1)
     const int kb0 = SPLIT ? (int)((long long)ks * g.kb / g.split_k) : 0;
     const int nkb = (SPLIT ? (int)((long long)(ks + 1) * g.kb / g.split_k) : g.kb) - kb0;
 
+    // Behind it no warp issues anything; whether one gave up, in either CTA of a pair. (Each part of the warps passes it and ends for
+    // itself, in its own registers. Neither CTA's shared or tensor memory goes while the other uses it.)
+    auto meet = [&]() -> bool {
+        __syncthreads();
+        if (PAIR) {
+            if (threadIdx.x == 0 && *abort_) st_dsmem_u32(dsmem_addr(smem_u32((const void*)abort_), rank ^ 1u), 1u);
+            cluster_sync_all();
+        }
+        return *abort_ != 0;
+    };
+
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::HELP_REGS));
         if (warp == 0 && lane == 0) {
@@ -670,6 +681,29 @@ __global__ void __launch_bounds__(TileSmem<BN, PAIR>::THREADS, 1)
             }
         }
         __syncwarp();
+        if (meet()) {                    // copies and MMAs land before the CTAs end (without an abort they have)
+            if (warp == 0 && lane == 0 && rank == 0) {
+                RingBarriers slices{full, (uint32_t)L::STAGE};
+                land_ring(slices, *slices_, PAIR ? ld_dsmem_u32(dsmem_addr(smem_u32((const void*)slices_), 1u)) : *slices_,
+                          (uint32_t)L::STAGES);
+            }
+            if (warp == 1) {             // (of a pair each CTA gets the first one's arrivals)
+                const uint32_t n = PAIR ? ld_dsmem_u32(dsmem_addr(smem_u32((const void*)blocks_), 0u)) : *blocks_;
+                RingBarriers{empty, 0u}.arrived(n, L::STAGES);
+                RingBarriers{accf, 0u}.arrived(n, L::NBUF);
+            }
+            __syncwarp();
+            if (PAIR) cluster_sync_all();
+        }
+        if (SPLIT) {
+            cluster_sync_all();
+            cluster_sync_all();
+        }
+        if (warp == 1) {
+            tc_fence_after();
+            if (PAIR) tmem_dealloc_pair(tmem, 512);
+            else tmem_dealloc(tmem, 512);
+        }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::SUM_REGS));
         constexpr int COLS = L::COLS;
@@ -766,51 +800,28 @@ __global__ void __launch_bounds__(TileSmem<BN, PAIR>::THREADS, 1)
             }
         }
         tc_fence_before();
-    }
-    __syncthreads();
-    if (PAIR) {
-        // neither CTA's shared or tensor memory goes while the other uses it, and if one gave up, so has the other
-        if (threadIdx.x == 0 && *abort_) st_dsmem_u32(dsmem_addr(smem_u32((const void*)abort_), rank ^ 1u), 1u);
-        cluster_sync_all();
-    }
-    if (*abort_) {                       // copies and MMAs land before the CTAs end (without an abort they have)
-        if (warp == 0 && lane == 0 && rank == 0) {
-            RingBarriers slices{full, (uint32_t)L::STAGE};
-            land_ring(slices, *slices_, PAIR ? ld_dsmem_u32(dsmem_addr(smem_u32((const void*)slices_), 1u)) : *slices_,
-                      (uint32_t)L::STAGES);
-        }
-        if (warp == 1) {                 // (of a pair each CTA gets the first one's arrivals)
-            const uint32_t n = PAIR ? ld_dsmem_u32(dsmem_addr(smem_u32((const void*)blocks_), 0u)) : *blocks_;
-            RingBarriers{empty, 0u}.arrived(n, L::STAGES);
-            RingBarriers{accf, 0u}.arrived(n, L::NBUF);
-        }
-        __syncwarp();
-        if (PAIR) cluster_sync_all();
-    }
-    if constexpr (SPLIT) {
-        // every thread of every member passes both cluster barriers, whatever happened before
-        cluster_sync_all();
-        if (!*abort_ && warp >= 4) {                     // (the warps that have the registers for it)
-            int mt, nt;
-            tile_at(g, first, mt, nt);
-            const int r0 = ks * SG_ROWS / g.split_k, r1 = (ks + 1) * SG_ROWS / g.split_k;
-            for (int i = r0 * (BN / 4) + (int)threadIdx.x - 128; i < r1 * (BN / 4); i += L::THREADS - 128) {
-                const int row = i / (BN / 4), piece = i % (BN / 4), m = mt * SG_ROWS + row, n = nt * BN + 4 * piece;
-                if (m >= g.M || n >= g.N) continue;
-                const uint32_t off = sbase + (uint32_t)((row * BN + ((piece ^ (row & 7)) << 2)) * 4);
-                float4 t[SG_MAX_SPLIT];
+        const bool gave_up = meet();
+        if (PAIR && gave_up) cluster_sync_all();
+        if constexpr (SPLIT) {
+            // every thread of every member passes both cluster barriers, whatever happened before
+            cluster_sync_all();
+            if (!gave_up) {
+                int mt, nt;
+                tile_at(g, first, mt, nt);
+                const int r0 = ks * SG_ROWS / g.split_k, r1 = (ks + 1) * SG_ROWS / g.split_k;
+                for (int i = r0 * (BN / 4) + (int)threadIdx.x - 128; i < r1 * (BN / 4); i += L::THREADS - 128) {
+                    const int row = i / (BN / 4), piece = i % (BN / 4), m = mt * SG_ROWS + row, n = nt * BN + 4 * piece;
+                    if (m >= g.M || n >= g.N) continue;
+                    const uint32_t off = sbase + (uint32_t)((row * BN + ((piece ^ (row & 7)) << 2)) * 4);
+                    float4 t[SG_MAX_SPLIT];
 #pragma unroll
-                for (int r = 0; r < SG_MAX_SPLIT; ++r)
-                    if (r < g.split_k) t[r] = ld_dsmem_f4(dsmem_addr(off, (uint32_t)r));
-                store_sum4(g, t, m, n, static_cast<T*>(g.y));
+                    for (int r = 0; r < SG_MAX_SPLIT; ++r)
+                        if (r < g.split_k) t[r] = ld_dsmem_f4(dsmem_addr(off, (uint32_t)r));
+                    store_sum4(g, t, m, n, static_cast<T*>(g.y));
+                }
             }
+            cluster_sync_all();
         }
-        cluster_sync_all();
-    }
-    if (warp == 1) {
-        tc_fence_after();
-        if (PAIR) tmem_dealloc_pair(tmem, 512);
-        else tmem_dealloc(tmem, 512);
     }
 }
 

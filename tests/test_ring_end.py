@@ -134,8 +134,8 @@ def test_every_copy_lands(model, stages, pair):
 def test_kernels_end_by_it():
     """Both kernels of the 8-bit linear land their ring after the barrier behind which no warp issues."""
     source = open(os.path.join(CSRC, "scaled_gemm.cu")).read()
-    for kernel in ("scaled_rows_kernel(", "scaled_tile_kernel("):
+    for kernel, barrier in (("scaled_rows_kernel(", "__syncthreads();"), ("scaled_tile_kernel(", "if (meet())")):
         body = source.split(kernel, 1)[1].split("__global__", 1)[0]
-        end = body.rindex("land_ring(")
-        assert body.rindex("tma_load_2d", 0, end) < body.rindex("__syncthreads()", 0, end) < end
-        assert "ring_used(" in body
+        end = body.index("land_ring(")
+        assert body.rindex("tma_load_2d", 0, end) < body.rindex(barrier, 0, end) < end
+        assert "ring_used(" in body and body.count("land_ring(") == 1
