@@ -17,8 +17,8 @@
 //
 // What bounds it. Few rows: HBM (28672 x 4096 weights: 8 rows 19.9 us, 0.88 of a measured copy, 64 rows 22.3), and for small
 // weights the start and the end of a CTA (4096 x 4096, 8 rows: 5.8 us in a graph, of which the bytes take 2.5). Many rows: 8192 x
-// 28672 x 4096 takes 680 to 700 us in ten calls after a rest, 2.8 PFLOP/s, and 755 one call after the other, when the power
-// limit holds the clock at 1740 MHz: 855 cycles for a block of K, a 32nd of a tile's stores among them. Two buffers of 256
+// 28672 x 4096 takes 680 to 700 us in ten calls after a rest, 2.8 PFLOP/s, and 740 to 770 one call after the other, when the
+// power limit holds the clock at 1650 to 1740 MHz: 823 cycles for a block of K, a 32nd of a tile's stores among them. Two buffers of 256
 // columns are all the tensor memory, so a block's sums have the 512 cycles of the next block's MMAs from the commit to the
 // release. Neither is the bound by itself: the MMAs alone run at 4.6 PFLOP/s on data that lies there, at 3.5 to 3.7 with the
 // loads (128 bytes of shared memory a cycle, written and read), and one CTA's hand-over alone, with its sums, takes 465 cycles
@@ -913,7 +913,7 @@ int max_clusters(SgKernel kern, int split, int threads, int smem)
 // clusters takes a kernel with tensor memory for one CTA per SM; of the rows kernel, whose CTAs share an SM by two, twice
 // as many fit, and as many as there are places for clusters of half the size. (8 rows, us in a graph: 4096 x 4096, 32 tiles, in
 // 2 ranges 8.3, in 4 6.0, in 8 5.8; 6144 x 4096, 48 tiles, in 4 or 5 7.6, in 6, which do not fit, 12.4; 4096 x 14336 in 4 15.3,
-// in 8 12.4. The rule does not look at the rows: 64 of 4096 x 4096 take 7.5 in 4 ranges and 8.6 in the 8 that it gives.)
+// in 8 12.4. The rule does not look at the rows: 64 of 4096 x 4096 take 7.3 in 4 ranges and 8.6 in the 8 that it gives.)
 int choose_split(SgKernel kern, long long tiles, int kb, int threads, int smem, int ctas_per_sm, int sms)
 {
     for (int n = std::min(SG_MAX_SPLIT, kb); n > 1; --n) {
@@ -1052,11 +1052,11 @@ try {
     // Tiles of 128 x 128 (whose sums join soonest where K is split) while each SM has one at most and K is short, then of
     // 128 x 256, for which less is read; pairs of CTAs on 256 x 256 where those would be more than one for an SM too, unless
     // the pairs' larger tiles take more turns. us a call in a graph, 128 x 128, 128 x 256 (four buffers of sums become two) and
-    // pairs: 512 x 4096 x 4096 14.4, 17.3, 16.3; 512 x 4096 x 8192 25.0, 23.3, 27.3; 512 x 4096 x 14336 40.3, 32.7, 43.5;
-    // 640 x 4096 x 14336 77.0, 45.6, 44.6; 1000 x 4096 x 4096 25.8, 17.4, 17.6; 1100 x 4096 x 4096 26.0, 17.6, 30.5;
-    // 256 x 14336 x 4096 25.9, 19.2, 18.3; 128 x 28672 x 4096 28.3, 25.1, 32.6; 256 x 28672 x 4096 37.4, 36.0, 33.6;
-    // 128 x 128256 x 4096 91.4, 94.9, 105.9; 2048 x 14336 x 4096 140, 90.3, 87.8 to 92.2. With one 128 x 256 tile for an SM
-    // at most, pairs take 2 to 5 % less where they are full (640 and 256 rows), and 17 to 33 % more where the single tiles split K.
+    // pairs: 512 x 4096 x 4096 14.2, 16.6, 16.2; 512 x 4096 x 8192 24.7, 22.5, 27.1; 512 x 4096 x 14336 40.0, 31.3, 43.2;
+    // 640 x 4096 x 14336 76.0, 44.9, 43.7; 1000 x 4096 x 4096 25.4, 16.9, 17.0; 1100 x 4096 x 4096 25.4, 17.0, 29.3;
+    // 256 x 14336 x 4096 25.4, 19.0, 17.7; 128 x 28672 x 4096 28.4, 25.4, 32.3; 256 x 28672 x 4096 37.0, 35.8, 33.3;
+    // 128 x 128256 x 4096 92.3, 96.2, 106.2; 2048 x 14336 x 4096 141, 88.1, 85.0. With one 128 x 256 tile for an SM
+    // at most, pairs take 3 to 7 % less where they are full (640 and 256 rows), and 20 to 38 % more where the single tiles split K.
     const long long m_tiles = (p->M + 127ll) / 128, tiles = m_tiles * ((p->N + 127ll) / 128);
     const long long wide_tiles = m_tiles * ((p->N + 255ll) / 256), pair_tiles = (m_tiles + 1) / 2 * ((p->N + 255ll) / 256);
     const bool pairs = wide_tiles > sms && (pair_tiles - 1) / std::max(1, sms / 2) <= (wide_tiles - 1) / sms;
